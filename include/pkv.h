@@ -74,9 +74,19 @@ enum {
                               than its block-table row: the page is skipped */
   PKV_DEVERR_BAD_SLOT = 2, /* a slot outside [0, num_pages * page_size): token not written */
   PKV_DEVERR_TIMEOUT = 4,  /* a bounded wait on a shared-memory barrier gave up */
-  PKV_DEVERR_BAD_GROUP = 8 /* cascade decode: inconsistent groups (a member whose context does
+  PKV_DEVERR_BAD_GROUP = 8, /* cascade decode: inconsistent groups (a member whose context does
                               not extend past the shared prefix, a member index outside the
                               batch, more members or prefix pages than declared) */
+  PKV_DEVERR_BAD_POSITION = 16, /* a position outside the rotation table: the token is left out */
+  PKV_DEVERR_BAD_TREE = 32 /* a draft longer than its request or than the tree width, or a path
+                              that does not increase or leaves the draft: the request is left
+                              out */
+};
+
+/* Limits of the speculative-decoding entry points. */
+enum {
+  PKV_MAX_TREE_NODES = 256, /* drafted nodes of a request */
+  PKV_MAX_TREE_GROUP = 128  /* query heads per KV head in the tree attention */
 };
 
 /* Description of one layer's pair of pools. page_size must be 16; head_dim 64 or 128. */
@@ -457,6 +467,10 @@ int pkv_seq_step(pkv_seq_table* t, const int64_t* free_rids, int32_t n_free,
 int pkv_seq_step_width(const pkv_seq_table* t, const int64_t* new_rids,
                        const int32_t* prompt_counts, int32_t n_new, const int64_t* live_rids,
                        int32_t n_live, int32_t* width_out);
+/* Cuts the listed (distinct) requests back to new_lens[i] tokens, 0 .. their length: pages that
+ * hold none of the kept tokens lose this request's reference and leave its row. PKV_EINVAL
+ * (nothing changed) for an unknown or repeated id or a length outside that range. */
+int pkv_seq_truncate(pkv_seq_table* t, const int64_t* rids, const int64_t* new_lens, int32_t n);
 /* Releases every page of the request whose positions all lie at or past sink_tokens, before
  * the last `window` positions and before the newest token (window 0: none); their row entries
  * become -1. *released (may be NULL) receives the count. */
@@ -654,6 +668,127 @@ int pkv_cascade_set_prefix_chunk_pages(int32_t pages);
  * automatic, 2) or on mma.sync (64 rows per CTA; 1). Same results up to rounding. */
 int pkv_cascade_set_prefix_kernel(int32_t which);
 
+/* ---- speculative decoding: drafted nodes over the cache ------------------------------------- */
+
+/*
+ * A verification step runs the model once over several drafted tokens ("nodes") per request. The
+ * nodes are a request's newest cached rows: with ctx = context_lens[b] and n = tree_lens[b], node i
+ * sits at position ctx - n + i, so pages for them are reserved like any other tokens
+ * (pkv_seq_reserve, which also makes the pages written private). The step appends their rows
+ * (pkv_qk_norm_rope_append, at the rotary positions of their depths), attends for all of them at
+ * once (pkv_tree_decode_attention), and keeps the accepted path (pkv_tree_commit on the device,
+ * pkv_seq_truncate on the host).
+ */
+
+/*
+ * Write phase straight from the projection's output: per-head RMS norm of the queries and keys,
+ * rotary position, and the K and V rows into their cache slots, in one pass. For token n and a
+ * query or key head's row x of D = head_dim values:
+ *   y_i = x_i * rsqrt(mean(x^2) + eps) * weight_i          (weight NULL: y = x)
+ *   for pair i of the first rot_dim dims -- (y_i, y_{i + rot_dim/2}), or (y_{2i}, y_{2i+1}) when
+ *   interleaved -- with c, s the cosine and sine of the token's position:
+ *     (a, b) -> (a c - b s, b c + a s); dims from rot_dim on are unchanged.
+ * The query row goes to q_out, the key row and the unchanged value row to slot_mapping[n] as
+ * pkv_kv_append stores them, but rounded once from fp32 (an FP8/INT8 key code is that of the
+ * fp32 quotient of the unrounded row). Sums and products are fp32: rows whose mean square
+ * overflows fp32 give zeros or NaN.
+ *  q, k, v        device, [num_tokens][heads][head_dim] of dtype (F32, BF16); a token's row is
+ *                 contiguous, tokens are *_stride elements apart (slices of one projection output
+ *                 need no copy). 16-byte aligned, strides too.
+ *  q_weight, k_weight  device [head_dim] of dtype, or NULL (no norm).
+ *  cos_sin        device float [max_positions][rot_dim]: rot_dim / 2 cosines, then the sines.
+ *  positions      device int32 [num_tokens]. A token whose position is outside
+ *                 [0, max_positions) is left out (neither q_out nor the cache is written) and
+ *                 PKV_DEVERR_BAD_POSITION set. cos_sin and positions may be NULL with rot_dim 0.
+ *  rot_dim        0 .. head_dim, a multiple of 16.
+ *  slot_mapping   device int64 [num_tokens], distinct; a negative one skips the cache rows (q_out
+ *                 is still written), one past the pool sets PKV_DEVERR_BAD_SLOT.
+ *  q_out          device, laid out like q with q_out_stride; may be q itself (same stride).
+ * dtype must equal cache_dtype for F32/BF16 caches, as for pkv_kv_append.
+ */
+int pkv_qk_norm_rope_append(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                            const void* v, int64_t v_stride, int32_t dtype, int32_t num_tokens,
+                            int32_t num_q_heads, const void* q_weight, const void* k_weight,
+                            float eps, const float* cos_sin, int32_t max_positions,
+                            int32_t rot_dim, int32_t interleaved, const int32_t* positions,
+                            const int64_t* slot_mapping, void* q_out, int64_t q_out_stride,
+                            void* k_cache, void* v_cache, const pkv_cache_desc* desc,
+                            const float* k_scales, const float* v_scales, void* stream);
+
+/*
+ * Host. Mask rows and depths of draft trees from their parents: parents[t][i] is the index of node
+ * i's parent in tree t, an earlier node, or -1 (a child of the last committed token).
+ *  masks_out   [n_trees][tree_width][ceil(tree_width / 64)]: bit j % 64 of word j / 64 of node i's
+ *              row is set when j is i or above it (the mask pkv_tree_decode_attention takes).
+ *  depths_out  [n_trees][tree_width] or NULL: nodes above node i (its rotary position is the
+ *              position of node 0 plus its depth).
+ */
+int pkv_tree_masks(const int32_t* parents, int64_t n_trees, int32_t tree_width,
+                   uint64_t* masks_out, int32_t* depths_out);
+
+/* Bytes of device workspace pkv_tree_decode_attention needs for these sizes (0 for an empty
+ * call). Its contents do not matter, before or after; one workspace serves one stream at a time
+ * (two captured graphs that may run at the same time need one each). */
+size_t pkv_tree_decode_workspace_size(int32_t dtype_q, int32_t cache_dtype, int32_t batch,
+                                      int32_t tree_width, int32_t num_q_heads,
+                                      int32_t num_kv_heads, int32_t head_dim,
+                                      int32_t max_pages_per_seq);
+
+/*
+ * Attention of drafted nodes over the paged cache. For request b, node t < n = tree_lens[b] and
+ * query head h over KV head j = h / (num_q_heads / num_kv_heads), with base = context_lens[b] - n:
+ *   out[b][t][h] = sum_p softmax(scale <q[b][t][h], K_p>)_p V_p
+ * over the positions p < base and the nodes base + i whose bit i is set in node t's mask row.
+ * A row that sees nothing gives 0. What is not seen takes no part, whatever it holds (NaN and
+ * infinities too). Scores, maxima and sums are fp32; with BF16 queries the weights are rounded
+ * to the cache's matrix type (bf16 for a BF16 cache, f16 for FP8 and INT8) before they meet V.
+ *  q, out       device [batch][tree_width][num_q_heads][head_dim] of dtype_q, 16-byte aligned;
+ *               rows t >= tree_lens[b] of out are left as they were. F32 q takes an F32, FP8 or
+ *               INT8 cache; BF16 q a BF16, FP8 or INT8 cache.
+ *  block_tables, max_pages_per_seq, k_scales, v_scales   as pkv_paged_decode_attention.
+ *  context_lens device int32 [batch], drafted nodes included. A context longer than the table is
+ *               read up to the table's end and flagged with PKV_DEVERR_BAD_PAGE; a page id outside
+ *               the pool is skipped and flagged.
+ *  tree_lens    device int32 [batch], 0 .. min(tree_width, context_lens[b]) (0: nothing to do for
+ *               b), or NULL: tree_width nodes for every request with a context. A request with
+ *               another value is left out and flagged with PKV_DEVERR_BAD_TREE.
+ *  tree_mask    device uint64 rows of ceil(tree_width / 64) words per node, tree_width rows per
+ *               request, requests mask_batch_stride words apart (0: one tree for all); NULL: a
+ *               chain, node t sees nodes 0 .. t. Bits of nodes >= tree_lens[b] are ignored.
+ *  scale        positive and finite.
+ *  workspace    device, >= pkv_tree_decode_workspace_size(...) bytes, 16-byte aligned.
+ * Requires num_q_heads % num_kv_heads == 0, at most PKV_MAX_TREE_GROUP query heads per KV head (any
+ * number, not only powers of two) and tree_width <= PKV_MAX_TREE_NODES. Equal inputs give equal
+ * results; the split over the GPU, and so the rounding, depends on all requests' lengths.
+ */
+int pkv_tree_decode_attention(const void* q, int32_t dtype_q, int32_t batch, int32_t tree_width,
+                              int32_t num_q_heads, const void* k_cache, const void* v_cache,
+                              const pkv_cache_desc* desc, const int32_t* block_tables,
+                              int32_t max_pages_per_seq, const int32_t* context_lens,
+                              const int32_t* tree_lens, const uint64_t* tree_mask,
+                              int64_t mask_batch_stride, float scale, const float* k_scales,
+                              const float* v_scales, void* out, void* workspace,
+                              size_t workspace_bytes, void* stream);
+
+/*
+ * Keeps an accepted path of each draft: for i < path_lens[b] the rows (every KV head, both pools)
+ * of node path[b][i] move to position base + i, base = context_lens[b] - tree_lens[b], and
+ * new_lens[b] = base + path_lens[b]. Rows behind the new length are left as they are.
+ *  path         device int32 [batch][max_path]; row b's first path_lens[b] entries increase strictly
+ *               and lie in [0, tree_lens[b]) (a path from a root down a tree whose parents come
+ *               first always does). Otherwise, or for a length outside [0, min(max_path,
+ *               tree_lens[b])], the request is left as it was, new_lens[b] = context_lens[b], and
+ *               PKV_DEVERR_BAD_TREE is set.
+ *  new_lens     device int32 [batch] or NULL; not one of the input arrays.
+ * The pages from base on must belong to the request alone. A bad page id skips that row and sets
+ * PKV_DEVERR_BAD_PAGE. The request table follows with pkv_seq_truncate.
+ */
+int pkv_tree_commit(void* k_cache, void* v_cache, const pkv_cache_desc* desc,
+                    const int32_t* block_tables, int32_t max_pages_per_seq,
+                    const int32_t* context_lens, const int32_t* tree_lens, const int32_t* path,
+                    const int32_t* path_lens, int32_t batch, int32_t max_path, int32_t* new_lens,
+                    void* stream);
+
 /* ---- prefix cache (host) ----------------------------------------------------------------- */
 
 /*
@@ -697,7 +832,8 @@ int32_t pkv_prefix_size(const pkv_prefix_cache* c);
 /* When on, every kernel the library launches, and each copy of the packed host steps, is
  * bracketed by a pair of CUDA events on its stream. pkv_trace_read() synchronises those events
  * and reports, for the family named ("paged_decode", "decode_combine", "cascade_prefix",
- * "kv_append", "kv_absmax", "copy_pages", and the packed steps' "h2d_copy" and "d2h_copy"),
+ * "kv_append", "kv_absmax", "copy_pages", "qk_norm_rope_append", "tree_attention", "tree_combine",
+ * "tree_commit", and the packed steps' "h2d_copy" and "d2h_copy"),
  * the number of launches and their summed device time in milliseconds since the last reset.
  * pkv_trace_reset() drops all records. */
 int pkv_trace_enable(int on);

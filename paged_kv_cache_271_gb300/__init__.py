@@ -9,7 +9,9 @@ Entry points (same names as the C ABI, without the ``pkv_`` prefix):
 ``kv_append``, ``paged_decode_attention``, ``decode_workspace_size``, ``kv_absmax_scales``,
 ``device_error``, ``pages_needed``, ``slot_mapping``, ``PageAllocator`` (``pkv_alloc``,
 ``pkv_incref``, ``pkv_decref``, ...), ``PrefixCache`` (``pkv_prefix_*``), ``cascade_groups``,
-``cascade_decode_attention``, ``cascade_decode_step``, ``decode_set_chunk_pages``, ``trace_*``.
+``cascade_decode_attention``, ``cascade_decode_step``, ``decode_set_chunk_pages``, ``trace_*``;
+for drafted tokens ``qk_norm_rope_append``, ``tree_masks``, ``tree_decode_attention`` and
+``tree_commit``.
 """
 from __future__ import annotations
 
@@ -25,11 +27,13 @@ __all__ = [
     "decode_set_chunk_pages", "decode_chunk_pages", "pages_needed", "slot_mapping",
     "PageAllocator", "PrefixCache", "CascadeGroups", "cascade_groups", "cascade_decode_attention",
     "cascade_decode_step", "cascade_workspace_size", "HostStep", "trace_enable", "trace_reset",
-    "trace_read",
+    "trace_read", "rope_table", "qk_norm_rope_append", "tree_masks", "tree_decode_workspace_size",
+    "tree_decode_attention", "tree_commit",
 ]
 
 F32, BF16, FP8_E4M3, INT8 = 0, 1, 2, 3
 DEVERR_BAD_PAGE, DEVERR_BAD_SLOT, DEVERR_TIMEOUT, DEVERR_BAD_GROUP = 1, 2, 4, 8
+DEVERR_BAD_POSITION, DEVERR_BAD_TREE = 16, 32
 _HERE = os.path.dirname(os.path.abspath(__file__))
 library_path = os.path.join(_HERE, "libpkv.so")
 _lib = None
@@ -125,6 +129,15 @@ def lib():
         "pkv_seq_add_cached_prefix": (ctypes.c_int, [vp, i64, vp, i64, vp, i64,
                                                      ctypes.POINTER(i64)]),
         "pkv_prefix_insert_request": (ctypes.c_int, [vp, i64, vp, i64, vp, i64]),
+        "pkv_seq_truncate": (ctypes.c_int, [vp, vp, vp, i32]),
+        "pkv_qk_norm_rope_append": (ctypes.c_int, [vp, i64, vp, i64, vp, i64, i32, i32, i32, vp, vp,
+                                                   f32, vp, i32, i32, i32, vp, vp, vp, i64, vp,
+                                                   vp, D, vp, vp, vp]),
+        "pkv_tree_masks": (ctypes.c_int, [vp, i64, i32, vp, vp]),
+        "pkv_tree_decode_workspace_size": (sz, [i32, i32, i32, i32, i32, i32, i32, i32]),
+        "pkv_tree_decode_attention": (ctypes.c_int, [vp, i32, i32, i32, i32, vp, vp, D, vp, i32, vp,
+                                                     vp, vp, i64, f32, vp, vp, vp, vp, sz, vp]),
+        "pkv_tree_commit": (ctypes.c_int, [vp, vp, D, vp, i32, vp, vp, vp, vp, i32, i32, vp, vp]),
         "pkv_seq_release_outside_window": (ctypes.c_int, [vp, i64, i64, i64,
                                                           ctypes.POINTER(i32)]),
         "pkv_seq_len": (i64, [vp, i64]),
@@ -664,6 +677,193 @@ def copy_pages(k_cache, v_cache, src_pages, dst_pages, stream=None):
                                 _dev(dst_pages, "dst_pages"), src_pages.numel(), _stream(stream)))
 
 
+def rope_table(max_positions: int, rot_dim: int, base: float = 10000.0,
+               device="cuda") -> torch.Tensor:
+    """Rotation table [max_positions, rot_dim] fp32 for ``qk_norm_rope_append``: the cosines of
+    pos * base^(-2i/rot_dim), i < rot_dim / 2, then the sines; angles in fp64."""
+    i = torch.arange(0, rot_dim, 2, dtype=torch.float64, device=device)
+    angle = (torch.arange(max_positions, dtype=torch.float64, device=device)[:, None] *
+             float(base) ** (-i / max(rot_dim, 1)))
+    return torch.cat([angle.cos(), angle.sin()], dim=-1).float()
+
+
+def _token_rows(t: torch.Tensor, name: str, heads=None, dim=None):
+    """Address and token stride (elements) of [N, heads, dim] rows, each token contiguous."""
+    if not isinstance(t, torch.Tensor) or t.dim() != 3:
+        raise PkvError(-2, "%s must be [tokens, heads, head_dim]" % name)
+    n, h, d = t.shape
+    if (heads is not None and h != heads) or (dim is not None and d != dim):
+        raise PkvError(-2, "%s must be [tokens, %s, %s], not %s" % (name, heads, dim,
+                                                                    tuple(t.shape)))
+    if n == 0:
+        return None, h * d
+    if (d > 1 and t.stride(2) != 1) or (h > 1 and t.stride(1) != d):
+        raise PkvError(-1, "%s: a token's row must be contiguous" % name)
+    _dev(t[0], name)
+    return ctypes.c_void_p(t.data_ptr()), (t.stride(0) if n > 1 else h * d)
+
+
+def qk_norm_rope_append(q, k, v, positions, slot_mapping, k_cache, v_cache, cos_sin,
+                        q_weight=None, k_weight=None, eps=1e-6, interleaved=False, q_out=None,
+                        k_scales=None, v_scales=None, stream=None):
+    """Write phase from a projection's output: per-head RMS norm of queries and keys (weights None:
+    no norm), rotation by ``cos_sin[positions]`` ([max_positions, rot_dim] fp32, see rope_table;
+    None: no rotation), K and V rows into their slots (pkv_qk_norm_rope_append). q [N, h_q, d],
+    k, v [N, h_kv, d] may be slices of one tensor (tokens any stride apart). Returns the queries
+    (``q_out``, which may be ``q``)."""
+    desc = cache_desc(k_cache)
+    if k_cache.shape != v_cache.shape or k_cache.dtype != v_cache.dtype:
+        raise PkvError(-2, "k_cache and v_cache differ")
+    if k.dtype != q.dtype or v.dtype != q.dtype:
+        raise PkvError(-3, "q, k and v must have one dtype")
+    qp, qs = _token_rows(q, "q", dim=desc.head_dim)
+    kp, ks = _token_rows(k, "k", desc.num_kv_heads, desc.head_dim)
+    vp, vs = _token_rows(v, "v", desc.num_kv_heads, desc.head_dim)
+    n, h_q, _ = q.shape
+    if k.shape[0] != n or v.shape[0] != n or slot_mapping.numel() != n:
+        raise PkvError(-2, "q, k, v and slot_mapping must have one length")
+    if slot_mapping.dtype != torch.int64:
+        raise PkvError(-3, "slot_mapping must be int64")
+    rot, most = 0, 0
+    if cos_sin is not None:
+        if cos_sin.dim() != 2 or cos_sin.dtype != torch.float32:
+            raise PkvError(-2, "cos_sin must be float32 [max_positions, rot_dim]")
+        if positions.dtype != torch.int32 or positions.numel() != n:
+            raise PkvError(-3, "positions must be int32, one per token")
+        most, rot = cos_sin.shape
+    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if w is not None and (w.dtype != q.dtype or w.numel() != desc.head_dim):
+            raise PkvError(-2, "%s must be [head_dim] of q's dtype" % name)
+    _check_scales(desc, k_scales, v_scales)
+    if q_out is None:
+        q_out = torch.empty((n, h_q, desc.head_dim), dtype=q.dtype, device=q.device)
+    elif q_out.dtype != q.dtype or q_out.shape != q.shape:
+        raise PkvError(-2, "q_out must match q in shape and dtype")
+    op, os_ = _token_rows(q_out, "q_out", h_q, desc.head_dim)
+    _check(lib().pkv_qk_norm_rope_append(
+        qp, qs, kp, ks, vp, vs, _dtype_code(q), n, h_q, _opt(q_weight, "q_weight"),
+        _opt(k_weight, "k_weight"), float(eps), _opt(cos_sin, "cos_sin"), most, rot,
+        1 if interleaved else 0, None if cos_sin is None else _dev(positions, "positions"),
+        _dev(slot_mapping, "slot_mapping"), op, os_, _dev(k_cache, "k_cache"),
+        _dev(v_cache, "v_cache"), ctypes.byref(desc), _opt(k_scales, "k_scales"),
+        _opt(v_scales, "v_scales"), _stream(stream)))
+    return q_out
+
+
+def _check_scales(desc, k_scales, v_scales):
+    """An 8-bit cache needs fp32 scales, one per KV head."""
+    if desc.cache_dtype not in (FP8_E4M3, INT8):
+        return
+    for t, name in ((k_scales, "k_scales"), (v_scales, "v_scales")):
+        if t is None:
+            raise PkvError(-1, "an FP8/INT8 cache needs k_scales and v_scales")
+        if t.dtype != torch.float32 or t.numel() != desc.num_kv_heads:
+            raise PkvError(-2, "%s must be float32 [num_kv_heads]" % name)
+
+
+def tree_masks(parents):
+    """Mask rows int64 [n, T, ceil(T/64)] and depths int32 [n, T] (host arrays) of draft trees
+    from ``parents`` [n, T] (or [T]: one tree): each node's parent, an earlier node, or -1
+    (pkv_tree_masks)."""
+    p = np.ascontiguousarray(np.asarray(parents, dtype=np.int32))
+    if p.ndim == 1:
+        p = p[None]
+    if p.ndim != 2:
+        raise PkvError(-2, "parents must be [trees, nodes]")
+    n, t = p.shape
+    masks = np.zeros((n, t, (t + 63) // 64), dtype=np.int64)
+    depths = np.zeros((n, t), dtype=np.int32)
+    _check(lib().pkv_tree_masks(_ptr(p), n, t, _ptr(masks), _ptr(depths)))
+    return masks, depths
+
+
+def tree_decode_workspace_size(dtype_q, cache_dtype, batch, tree_width, num_q_heads, num_kv_heads,
+                               head_dim, max_pages_per_seq) -> int:
+    """Bytes of workspace of a tree_decode_attention call (dtypes as torch dtypes or codes)."""
+    code = lambda d: d if isinstance(d, int) else _dtype_code(torch.empty(0, dtype=d))
+    return int(lib().pkv_tree_decode_workspace_size(code(dtype_q), code(cache_dtype), batch,
+                                                    tree_width, num_q_heads, num_kv_heads,
+                                                    head_dim, max_pages_per_seq))
+
+
+def tree_decode_attention(q, k_cache, v_cache, block_tables, context_lens, scale, tree_mask=None,
+                          tree_lens=None, out=None, k_scales=None, v_scales=None, workspace=None,
+                          stream=None):
+    """Attention of drafted nodes q [B, T, h_q, d] over the paged pools; returns out. A request's
+    nodes are its last ``tree_lens[b]`` cached rows (None: T each); ``tree_mask`` int64
+    [B or 1, T, ceil(T/64)] has bit j of row i set where node i sees node j (None: a chain); every
+    node sees the rows before the draft (pkv_tree_decode_attention). Rows of ``out`` past a
+    request's draft are left as they were (zero in a new ``out``)."""
+    if q.dim() != 4:
+        raise PkvError(-2, "q must be [batch, nodes, num_q_heads, head_dim]")
+    if block_tables.dtype != torch.int32 or context_lens.dtype != torch.int32:
+        raise PkvError(-3, "block_tables and context_lens must be int32")
+    B, T, h_q, d = q.shape
+    if block_tables.dim() != 2 or block_tables.shape[0] != B or context_lens.numel() != B:
+        raise PkvError(-2, "block_tables must be [batch, max_pages], context_lens [batch]")
+    desc = cache_desc(k_cache)
+    if k_cache.shape != v_cache.shape or k_cache.dtype != v_cache.dtype:
+        raise PkvError(-2, "k_cache and v_cache differ")
+    if d != desc.head_dim:
+        raise PkvError(-2, "q head_dim does not match the pool")
+    if tree_lens is not None and (tree_lens.dtype != torch.int32 or tree_lens.numel() != B):
+        raise PkvError(-3, "tree_lens must be int32 [batch]")
+    stride = 0
+    if tree_mask is not None:
+        if (tree_mask.dtype != torch.int64 or tree_mask.dim() != 3 or
+                tree_mask.shape[0] not in (1, B) or
+                tuple(tree_mask.shape[1:]) != (T, (T + 63) // 64)):
+            raise PkvError(-2, "tree_mask must be int64 [batch or 1, nodes, ceil(nodes / 64)]")
+        stride = 0 if tree_mask.shape[0] == 1 else T * tree_mask.shape[2]
+    _check_scales(desc, k_scales, v_scales)
+    if out is None:
+        out = (torch.empty_like if tree_lens is None else torch.zeros_like)(q)
+    elif out.shape != q.shape or out.dtype != q.dtype:
+        raise PkvError(-2, "out must match q in shape and dtype")
+    maxp = block_tables.shape[1]
+    if workspace is None:
+        need = tree_decode_workspace_size(_dtype_code(q), desc.cache_dtype, B, T, h_q,
+                                          desc.num_kv_heads, d, maxp)
+        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    _check(lib().pkv_tree_decode_attention(
+        _dev(q, "q"), _dtype_code(q), B, T, h_q, _dev(k_cache, "k_cache"),
+        _dev(v_cache, "v_cache"), ctypes.byref(desc), _dev(block_tables, "block_tables"), maxp,
+        _dev(context_lens, "context_lens"), _opt(tree_lens, "tree_lens"),
+        _opt(tree_mask, "tree_mask"), stride, float(scale), _opt(k_scales, "k_scales"),
+        _opt(v_scales, "v_scales"), _dev(out, "out"), _dev(workspace, "workspace"),
+        workspace.numel() * workspace.element_size(), _stream(stream)))
+    return out
+
+
+def tree_commit(k_cache, v_cache, block_tables, context_lens, tree_lens, path, path_lens,
+                new_lens=None, stream=None):
+    """Keeps an accepted path of each request's draft: its nodes' rows path[b, :path_lens[b]] move
+    together behind the committed rows (pkv_tree_commit). Returns the requests' new lengths (int32
+    [B] on the device); the request table follows with ``truncate``."""
+    for t, name in ((block_tables, "block_tables"), (context_lens, "context_lens"),
+                    (tree_lens, "tree_lens"), (path, "path"), (path_lens, "path_lens")):
+        if t.dtype != torch.int32:
+            raise PkvError(-3, "%s must be int32" % name)
+    B = context_lens.numel()
+    if (block_tables.dim() != 2 or block_tables.shape[0] != B or path.dim() != 2 or
+            path.shape[0] != B or tree_lens.numel() != B or path_lens.numel() != B):
+        raise PkvError(-2, "block_tables and path must be [batch, n], the lengths [batch]")
+    desc = cache_desc(k_cache)
+    if k_cache.shape != v_cache.shape or k_cache.dtype != v_cache.dtype:
+        raise PkvError(-2, "k_cache and v_cache differ")
+    if new_lens is None:
+        new_lens = torch.empty(B, dtype=torch.int32, device=k_cache.device)
+    elif new_lens.dtype != torch.int32 or new_lens.numel() != B:
+        raise PkvError(-2, "new_lens must be int32 [batch]")
+    _check(lib().pkv_tree_commit(
+        _dev(k_cache, "k_cache"), _dev(v_cache, "v_cache"), ctypes.byref(desc),
+        _dev(block_tables, "block_tables"), block_tables.shape[1],
+        _dev(context_lens, "context_lens"), _dev(tree_lens, "tree_lens"), _dev(path, "path"),
+        _dev(path_lens, "path_lens"), B, path.shape[1], _dev(new_lens, "new_lens"),
+        _stream(stream)))
+    return new_lens
+
+
 def kv_absmax_scales(x, scales_out=None, stream=None, int8=False):
     """Scales per KV head: fp32(max|x[:, h, :]| / 448) for an FP8 cache, / 127 for an INT8
     cache (int8=True); 1 for an all-zero head."""
@@ -961,6 +1161,13 @@ class SeqTable:
                                   ctypes.byref(nc)))
         copies = [(int(src[i]), int(dst[i])) for i in range(nc.value)]
         return (ps, bt, cl, copies) + ((ls,) if live_slots else ())
+
+    def truncate(self, rids, new_lens):
+        """Cuts requests back to ``new_lens`` tokens; pages holding none of them are released."""
+        r, n = _ids(rids), _ids(new_lens)
+        if r.size != n.size:
+            raise PkvError(-1, "rids and new_lens differ in length")
+        _check(lib().pkv_seq_truncate(self._h, _ptr(r), _ptr(n), r.size))
 
     def release_outside_window(self, rid: int, window: int, sink_tokens: int = 0) -> int:
         n = ctypes.c_int32(0)

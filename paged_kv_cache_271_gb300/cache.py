@@ -16,7 +16,8 @@ from collections.abc import Mapping
 import numpy as np
 import torch
 
-from . import PageAllocator, SeqTable, copy_pages, kv_append
+from . import (PageAllocator, SeqTable, copy_pages, kv_append, qk_norm_rope_append, tree_commit,
+               tree_decode_attention)
 
 
 class _RowView(Mapping):
@@ -110,6 +111,11 @@ class PagedKVCache:
         read again). Their table entries become -1. Returns the number of pages released."""
         return self.table.release_outside_window(rid, window, sink_tokens)
 
+    def truncate(self, rids, new_lens):
+        """Cut requests back to ``new_lens`` tokens (rejected drafts, a restarted answer): pages
+        that hold none of the kept tokens go back to the allocator."""
+        self.table.truncate(rids, new_lens)
+
     def reserve(self, rids, counts, copies_out=None) -> np.ndarray:
         """Grow each request by counts[i] tokens (allocating pages on page boundaries) and
         return the int64 slots of the new positions, request by request. Shared, partly filled
@@ -150,6 +156,40 @@ class PagedKVCache:
         if not isinstance(slots, torch.Tensor):
             slots = torch.from_numpy(np.asarray(slots, dtype=np.int64)).to(self.k.device)
         kv_append(k_new, v_new, slots, self.k, self.v, self.k_scales, self.v_scales, stream)
+
+    def write_qkv(self, slots, q, k_new, v_new, positions, cos_sin, q_out=None, stream=None,
+                  **norm):
+        """Norm, rotate and append in one pass (qk_norm_rope_append; ``norm``: q_weight, k_weight,
+        eps, interleaved); returns the rotated queries."""
+        if not isinstance(slots, torch.Tensor):
+            slots = torch.from_numpy(np.asarray(slots, dtype=np.int64)).to(self.k.device)
+        return qk_norm_rope_append(q, k_new, v_new, positions, slots, self.k, self.v, cos_sin,
+                                   q_out=q_out, k_scales=self.k_scales, v_scales=self.v_scales,
+                                   stream=stream, **norm)
+
+    # ---- drafted tokens ----------------------------------------------------------------------
+
+    def attend_tree(self, q, block_tables, context_lens, scale, tree_mask=None, tree_lens=None,
+                    out=None, workspace=None, stream=None):
+        """Attention of drafted nodes q [B, T, h_q, d] (tree_decode_attention over these pools)."""
+        return tree_decode_attention(q, self.k, self.v, block_tables, context_lens, scale,
+                                     tree_mask, tree_lens, out, self.k_scales, self.v_scales,
+                                     workspace, stream)
+
+    def commit_tree(self, rids, block_tables, context_lens, tree_lens, path, path_lens,
+                    stream=None) -> list:
+        """Keep the accepted path of each request's draft: move its rows together (tree_commit),
+        read the new lengths back (this waits for the stream) and truncate the requests to them.
+        Returns the new lengths."""
+        if stream is None:
+            stream = torch.cuda.current_stream(self.k.device)
+        elif not isinstance(stream, torch.cuda.Stream):  # a raw cudaStream_t handle
+            stream = torch.cuda.ExternalStream(int(stream), device=self.k.device)
+        with torch.cuda.stream(stream):
+            new = tree_commit(self.k, self.v, block_tables, context_lens, tree_lens, path,
+                              path_lens, stream=stream).tolist()
+        self.table.truncate(rids, new)
+        return new
 
     # ---- views for the decode ---------------------------------------------------------------
 

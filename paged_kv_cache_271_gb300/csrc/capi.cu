@@ -11,6 +11,7 @@
 #include <string>
 #include <vector>
 
+#include "capi_util.h"
 #include "pkv.h"
 #include "pkv_host.h"
 #include "pkv_internal.h"
@@ -33,7 +34,8 @@ int current_device(int* dev) {
   return PKV_OK;
 }
 
-// Device address of the current device's error word (looked up once per device).
+}  // namespace
+
 int error_word(int** out) {
   int dev = 0;
   int st = current_device(&dev);
@@ -52,30 +54,31 @@ int error_word(int** out) {
 
 // ---- tracing --------------------------------------------------------------------------------
 
+namespace {
+
 struct TraceRec {
   std::string name;
   cudaEvent_t begin, end;
 };
-std::atomic<bool> g_trace_on{false};
 std::mutex g_trace_mu;
 std::vector<TraceRec> g_trace;
 
-template <class F>
-cudaError_t traced(const char* name, cudaStream_t s, F&& launch) {
-  if (!g_trace_on.load(std::memory_order_relaxed)) return launch();
-  TraceRec r{name, nullptr, nullptr};
-  cudaError_t e = cudaEventCreate(&r.begin);
-  if (e == cudaSuccess) e = cudaEventCreate(&r.end);
-  if (e != cudaSuccess) return e;
-  cudaEventRecord(r.begin, s);
-  e = launch();
-  cudaEventRecord(r.end, s);
-  std::lock_guard<std::mutex> lk(g_trace_mu);
-  g_trace.push_back(r);
+}  // namespace
+
+std::atomic<bool> g_trace_on{false};
+
+cudaError_t trace_begin(cudaEvent_t (&ev)[2], cudaStream_t s) {
+  cudaError_t e = cudaEventCreate(&ev[0]);
+  if (e == cudaSuccess) e = cudaEventCreate(&ev[1]);
+  if (e == cudaSuccess) cudaEventRecord(ev[0], s);
   return e;
 }
 
-}  // namespace
+void trace_end(const char* name, const cudaEvent_t (&ev)[2], cudaStream_t s) {
+  cudaEventRecord(ev[1], s);
+  std::lock_guard<std::mutex> lk(g_trace_mu);
+  g_trace.push_back(TraceRec{name, ev[0], ev[1]});
+}
 
 void* current_context() {
   using CtxGetCurrent = CUresult (*)(CUcontext*);
@@ -109,14 +112,12 @@ cudaError_t traced_copy(const char* name, void* dst, const void* src, size_t byt
   return traced(name, s, [&] { return cudaMemcpyAsync(dst, src, bytes, kind, s); });
 }
 
-namespace {
-
 int cuda_status(cudaError_t e, const char* what) {
   if (e == cudaSuccess) return PKV_OK;
   return set_error(PKV_ECUDA, "%s: %s", what, cudaGetErrorString(e));
 }
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+namespace {
 
 std::atomic<int> g_chunk_override{0};
 // Calls whose sequences split into at most this many chunks merge them in the decode kernel
@@ -171,16 +172,10 @@ std::mutex g_map_mu;
 std::vector<MapEntry> g_maps;
 EncodeTiledFn g_encode = nullptr;
 
-// The TMA view of a pool, encoded once per (device, pool, shape). A row of 128 bytes (FP8,
-// INT8 at head_dim 128) is a 2-D tensor [num_pages * h_kv * 16 rows][128 bytes], one
-// (page, KV head) tile per box of 16 rows. A bf16 row of 256 bytes is a 3-D tensor
-// [2 halves][rows][64 elements] (halves 128 bytes apart, rows 256 bytes apart), so that one box
-// of 2 x 16 x 64 moves a whole (page, KV head) tile into shared memory as two 128-byte-swizzled
-// blocks of 16 rows, the first half of every row before the second (the layout the kernels
-// read); *rank receives 2 or 3. force_2d asks for the 2-D view of a bf16 pool too (two boxes
-// of 16 rows x 64 elements per tile).
+}  // namespace
+
 int pool_tensor_map(const void* base, const pkv_cache_desc* d, CUtensorMap* out, int* rank,
-                    bool force_2d = false) {
+                    bool force_2d) {
   int dev = 0;
   cudaError_t ce = cudaGetDevice(&dev);
   if (ce != cudaSuccess) return set_error(PKV_ECUDA, "cudaGetDevice: %s", cudaGetErrorString(ce));
@@ -246,6 +241,8 @@ int pool_tensor_map(const void* base, const pkv_cache_desc* d, CUtensorMap* out,
   return PKV_OK;
 }
 
+namespace {
+
 // Largest chunk (pages per CTA); each sequence is split into the fewest near-equal chunks no
 // larger than this (64 or 32 pages keep the partials near 1 % of the KV bytes); one chunk
 // when every sequence fits in one.
@@ -261,8 +258,6 @@ int chunk_pages_for(int batch, int h_kv, int max_pages) {
   if (max_pages <= chunk) chunk = max_pages < 1 ? 1 : max_pages;
   return chunk;
 }
-
-size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
 // Workspace: acc [batch][h_q][slots][d] and (max, sum) [batch][h_q][slots][2] floats, then one
 // counter per (request, KV head) for the in-place merge; 256-byte aligned regions.
@@ -344,6 +339,8 @@ void cascade_split(int batch, int h_kv, int h_q, int max_pages, const pkv_cascad
   *slots = *chunk_grid + (g->max_prefix_pages + *prefix_chunk_pages - 1) / *prefix_chunk_pages;
 }
 
+}  // namespace
+
 int check_desc(const pkv_cache_desc* d, const char* who) {
   if (!d) return set_error(PKV_EINVAL, "%s: desc is NULL", who);
   if (d->page_size != 16) return set_error(PKV_EINVAL, "%s: page_size must be 16", who);
@@ -359,7 +356,6 @@ int check_desc(const pkv_cache_desc* d, const char* who) {
   return PKV_OK;
 }
 
-}  // namespace
 }  // namespace pkv
 
 using namespace pkv;

@@ -94,7 +94,94 @@ struct AppendArgs {
   int64_t num_slots;  // num_pages * page_size
 };
 
+struct NormRopeArgs {
+  const void* q;        // [num_tokens][h_q][head_dim], tokens q_stride elements apart
+  const void* k;        // [num_tokens][h_kv][head_dim]
+  const void* v;
+  int64_t q_stride, k_stride, v_stride, q_out_stride;
+  void* q_out;
+  const void* q_weight;  // [head_dim] of the input type, or null: no norm
+  const void* k_weight;
+  float eps;
+  const float* cos_sin;  // [max_positions][rot_dim]: rot_dim / 2 cosines, then the sines
+  const int32_t* positions;
+  int max_positions;
+  int rot_dim;
+  int interleaved;
+  const int64_t* slots;
+  void* k_cache;
+  void* v_cache;
+  const float* k_scales;
+  const float* v_scales;
+  int* err;
+  int num_tokens;
+  int h_q;
+  int h_kv;
+  int head_dim;
+  int64_t num_slots;
+};
+
+// Tree attention: `nodes` query positions per request, see tree_plan.cuh for the work split.
+struct TreeArgs {
+  const void* q;  // [batch][nodes][h_q][D]
+  void* out;
+  const void* k_cache;
+  const void* v_cache;
+  const int32_t* block_tables;
+  const int32_t* context_lens;  // drafted nodes included
+  const int32_t* tree_lens;     // [batch] or null: `nodes` each
+  const uint64_t* mask;         // [batch or 1][nodes][mask_words] or null: node i sees 0 .. i
+  int64_t mask_stride;          // words between requests (0: one mask for all)
+  int mask_words;
+  const float* k_scales;
+  const float* v_scales;
+  float* ws_acc;  // [ctas][2][rows of a unit][D] partial weighted values
+  float* ws_ml;   // [ctas][2][rows of a unit][2] partial (max, sum), log2 domain
+  int* err;
+  int batch;
+  int nodes;
+  int h_q;
+  int h_kv;
+  int group;  // h_q / h_kv
+  int num_pages;
+  int max_pages;
+  int tma_rank;
+  float scale_log2;
+  // the work split, the same in the attention and its combine
+  int ctas;
+  int unit_rows;    // query rows of a unit
+  int tile_tokens;  // cached tokens of a tile
+  int min_tiles;    // least tiles a CTA takes
+};
+
+struct CommitArgs {
+  void* k_cache;
+  void* v_cache;
+  const int32_t* block_tables;
+  const int32_t* context_lens;
+  const int32_t* tree_lens;
+  const int32_t* path;
+  const int32_t* path_lens;
+  int32_t* new_lens;  // or null
+  int* err;
+  int batch;
+  int max_path;
+  int max_pages;
+  int num_pages;
+  int h_kv;
+  int row_bytes;
+};
+
 // Each returns the launch status. dtype codes are pkv_dtype values.
+cudaError_t launch_qk_norm_rope_append(const NormRopeArgs& a, int io_dtype, int cache_dtype,
+                                       cudaStream_t s);
+// Tree attention on CUDA cores (every type and head dimension) and the combine of any split.
+constexpr int kTreeSimtRows = 32, kTreeSimtTokens = 32;
+constexpr int kTreeSimtWave = 152 * 4;  // four 55 KB CTAs fit an SM
+cudaError_t launch_tree_simt(const TreeArgs& a, int q_dtype, int kv_dtype, int head_dim,
+                             cudaStream_t s);
+cudaError_t launch_tree_combine(const TreeArgs& a, int q_dtype, int head_dim, cudaStream_t s);
+cudaError_t launch_tree_commit(const CommitArgs& a, cudaStream_t s);
 cudaError_t launch_decode_f32(const DecodeArgs& a, int q_dtype, int head_dim, int group,
                               cudaStream_t s);
 cudaError_t launch_decode_bf16(const DecodeArgs& a, int q_dtype, int head_dim, int group,

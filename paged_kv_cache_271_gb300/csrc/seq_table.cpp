@@ -532,6 +532,41 @@ int pkv_prefix_insert_request(pkv_prefix_cache* c, int64_t tenant, const int32_t
                            (int32_t)full);
 }
 
+int pkv_seq_truncate(pkv_seq_table* t, const int64_t* rids, const int64_t* new_lens, int32_t n) {
+  if (!t || n < 0 || (n > 0 && (!rids || !new_lens)))
+    return pkv::set_error(PKV_EINVAL, "pkv_seq_truncate: bad argument");
+  const uint64_t ep = ++t->epoch;
+  std::vector<Seq*>& listed = t->listed;
+  listed.clear();
+  for (int32_t i = 0; i < n; ++i) {
+    auto it = t->seqs.find(rids[i]);
+    if (it == t->seqs.end() || it->second.mark == ep || new_lens[i] < 0 ||
+        new_lens[i] > it->second.len)
+      return pkv::set_error(PKV_EINVAL, "pkv_seq_truncate: request %lld unknown, listed twice or "
+                            "shorter than %lld tokens", (long long)rids[i],
+                            (long long)new_lens[i]);
+    it->second.mark = ep;
+    listed.push_back(&it->second);
+  }
+  std::vector<int32_t>& gone = t->scratch;
+  for (int32_t i = 0; i < n; ++i) {
+    Seq& s = *listed[i];
+    const size_t keep = (size_t)pages_for(new_lens[i], t->page_size);
+    s.len = new_lens[i];
+    if (keep >= s.pages.size()) continue;
+    gone.clear();
+    for (size_t lp = keep; lp < s.pages.size(); ++lp)
+      if (s.pages[lp] >= 0) gone.push_back(s.pages[lp]);
+    s.pages.resize(keep);
+    s.exp_row = -1;  // an exported row has columns to clear: the next export writes it whole
+    if (!gone.empty()) {
+      const int st = pkv_decref(t->alloc, gone.data(), (int32_t)gone.size());
+      if (st != PKV_OK) return st;  // (pages of a live request are allocated: cannot happen)
+    }
+  }
+  return PKV_OK;
+}
+
 int pkv_seq_release_outside_window(pkv_seq_table* t, int64_t rid, int64_t window,
                                    int64_t sink_tokens, int32_t* released) {
   if (!t || window < 0 || sink_tokens < 0)

@@ -1,0 +1,403 @@
+// Tree attention on CUDA cores, for every cache and query type and both head dimensions, and the
+// combine of a split call.
+//
+// For node t of request b and query head h over KV head j:
+//   s_p = scale <q, K_p> for the positions p that node t sees, out = sum_p softmax(s)_p V_p,
+// the cached positions before the draft all seen, drafted node i seen when bit i of the mask row
+// is set; a row that sees nothing gives 0.
+//
+// A block takes units of 32 rows over tiles of 32 tokens (tree_plan.cuh): K and V of a tile are
+// widened to fp32 in shared memory and used by all 32 rows; a thread computes 4 rows x 2 tokens of
+// scores and 4 rows x D/16 dims of the weighted values, so each 16-byte shared-memory load feeds
+// five to six FMAs. The softmax is online: the running maximum and sum stay in the registers of
+// the 16 threads that share a row. It is bound by the FMA rate and by shared memory; the sums are
+// fp32 throughout, which the fp32 types need.
+#include <math.h>
+
+#include <atomic>
+
+#include "pkv_device.cuh"
+#include "pkv_internal.h"
+#include "tree_plan.cuh"
+
+namespace pkv {
+
+namespace {
+
+constexpr int kThreads = 128;
+constexpr int kRows = kTreeSimtRows, kTok = kTreeSimtTokens;
+
+template <int D>
+struct SimtShape {
+  static constexpr int LD = D + 4;   // row pitch (floats): keeps float4 alignment, spreads banks
+  static constexpr int LP = kTok + 4;
+  static constexpr int SMEM = 4 * (3 * kRows * LD + kRows * LP);
+};
+static_assert(kRows == kTok, "Q, K and V tiles have the same shape");
+
+// Four consecutive elements, widened.
+template <typename T>
+__device__ __forceinline__ float4 load4(const void* base, int64_t i) {
+  float o[4];
+  RowLoad<T, 4>::run(static_cast<const uint8_t*>(base) + i * T::bytes, o);
+  return make_float4(o[0], o[1], o[2], o[3]);
+}
+
+__device__ __forceinline__ void fma4(float4& acc, float p, const float4& v) {
+  acc.x = fmaf(p, v.x, acc.x);
+  acc.y = fmaf(p, v.y, acc.y);
+  acc.z = fmaf(p, v.z, acc.z);
+  acc.w = fmaf(p, v.w, acc.w);
+}
+
+__device__ __forceinline__ void store4(float* p, const float4& v) {
+  *reinterpret_cast<float4*>(p) = v;
+}
+__device__ __forceinline__ void store4(__nv_bfloat16* p, const float4& v) {
+  __nv_bfloat162 w[2] = {__floats2bfloat162_rn(v.x, v.y), __floats2bfloat162_rn(v.z, v.w)};
+  *reinterpret_cast<uint2*>(p) = *reinterpret_cast<uint2*>(w);
+}
+
+template <typename KV, typename Q, int D>
+__global__ void __launch_bounds__(kThreads) tree_simt_kernel(const TreeArgs a) {
+  using S = SimtShape<D>;
+  using TQ = typename Q::storage;
+  constexpr int NQ = D / 64;  // float4 groups of dims a thread accumulates, 64 dims apart
+  constexpr int LD = S::LD, LP = S::LP;
+  extern __shared__ float4 smem4[];
+  float* qs = reinterpret_cast<float*>(smem4);
+  float* ks = qs + kRows * LD;
+  float* vs = ks + kTok * LD;
+  float* ps = vs + kTok * LD;
+  __shared__ long long scratch[33];
+  __shared__ TreeShare share;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  tree_share<kThreads>(a, scratch, &share);
+  TreeWalk walk{share.b, share.off, share.count};
+  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;  // tokens / dims, group of 4 rows
+  TreeRun run;
+  while (walk.next(a, run)) {
+    const int b = run.b, j = run.j;
+    __syncthreads();  // the previous run is done with the shared tiles
+    for (int e = threadIdx.x; e < kRows * (D / 4); e += kThreads) {
+      const int r = e / (D / 4), c = e % (D / 4);
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (r < run.rows) {
+        const int R = run.row0 + r, t = R / a.group, g = R % a.group;
+        v = load4<Q>(a.q, (((int64_t)b * a.nodes + t) * a.h_q + j * a.group + g) * D + 4 * c);
+      }
+      *reinterpret_cast<float4*>(qs + r * LD + 4 * c) = v;
+    }
+    float m[4], l[4];
+    float4 acc[4][NQ];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      m[i] = -INFINITY;
+      l[i] = 0.f;
+#pragma unroll
+      for (int k = 0; k < NQ; ++k) acc[i][k] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    const float sc = a.scale_log2 * (KV::bytes == 1 ? a.k_scales[j] : 1.f);
+    const int32_t* table = a.block_tables + (size_t)b * a.max_pages;
+    for (int tile = run.tile0; tile < run.tile0 + run.n; ++tile) {
+      const int p0 = tile * kTok;
+      const bool tail = p0 + kTok > min(run.req.base, run.req.read);  // not all positions seen
+      uint32_t page_ok = 0;  // one bit per token
+#pragma unroll
+      for (int pg = 0; pg < kTok / kPageSize; ++pg) {
+        const int lp = p0 / kPageSize + pg;
+        const int id = lp * kPageSize < run.req.read ? table[lp] : -1;
+        if (id >= 0 && id < a.num_pages)
+          page_ok |= 0xffffu << (16 * pg);
+        else if (lp * kPageSize < run.req.read && threadIdx.x == 0)
+          atomicOr(a.err, PKV_DEVERR_BAD_PAGE);
+      }
+      __syncthreads();  // the previous tile is used up (and Q is stored)
+      for (int e = threadIdx.x; e < kTok * (D / 4); e += kThreads) {
+        const int r = e / (D / 4), c = e % (D / 4);
+        float4 kv = make_float4(0.f, 0.f, 0.f, 0.f), vv = kv;
+        if (p0 + r < run.req.read && ((page_ok >> r) & 1)) {
+          const int64_t row = ((int64_t)table[(p0 + r) / kPageSize] * a.h_kv + j) * kPageSize +
+                              (p0 + r) % kPageSize;
+          kv = load4<KV>(a.k_cache, row * D + 4 * c);
+          vv = load4<KV>(a.v_cache, row * D + 4 * c);
+        }
+        *reinterpret_cast<float4*>(ks + r * LD + 4 * c) = kv;
+        *reinterpret_cast<float4*>(vs + r * LD + 4 * c) = vv;
+      }
+      __syncthreads();
+      // ---- scores of rows 4 ty + i, tokens tx and tx + 16 ----
+      float s[4][2];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s[i][0] = s[i][1] = 0.f;
+#pragma unroll 4
+      for (int d = 0; d < D; d += 4) {
+        const float4 k0 = *reinterpret_cast<const float4*>(ks + tx * LD + d);
+        const float4 k1 = *reinterpret_cast<const float4*>(ks + (tx + 16) * LD + d);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float4 q = *reinterpret_cast<const float4*>(qs + (4 * ty + i) * LD + d);
+          s[i][0] = fmaf(q.x, k0.x, fmaf(q.y, k0.y, fmaf(q.z, k0.z, fmaf(q.w, k0.w, s[i][0]))));
+          s[i][1] = fmaf(q.x, k1.x, fmaf(q.y, k1.y, fmaf(q.z, k1.z, fmaf(q.w, k1.w, s[i][1]))));
+        }
+      }
+      // ---- online softmax; a row's 16 threads hold the same m and l ----
+      uint32_t seen[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int R = 4 * ty + i;
+        seen[i] = page_ok;
+        if (tail)
+          seen[i] &= R < run.rows
+                         ? (uint32_t)tree_seen(a, run.req, b, (run.row0 + R) / a.group, p0)
+                         : 0u;
+        s[i][0] = (seen[i] >> tx) & 1 ? s[i][0] * sc : -INFINITY;
+        s[i][1] = (seen[i] >> (tx + 16)) & 1 ? s[i][1] * sc : -INFINITY;
+        float mx = fmaxf(s[i][0], s[i][1]);
+#pragma unroll
+        for (int o = 8; o >= 1; o /= 2) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+        const float mn = fmaxf(m[i], mx);
+        const float mu = mn == -INFINITY ? 0.f : mn;
+        const float alpha = exp2f(m[i] - mu);
+        const float e0 = exp2f(s[i][0] - mu), e1 = exp2f(s[i][1] - mu);
+        float sum = e0 + e1;
+#pragma unroll
+        for (int o = 8; o >= 1; o /= 2) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        l[i] = fmaf(l[i], alpha, sum);
+        m[i] = mn;
+#pragma unroll
+        for (int k = 0; k < NQ; ++k) {
+          acc[i][k].x *= alpha;
+          acc[i][k].y *= alpha;
+          acc[i][k].z *= alpha;
+          acc[i][k].w *= alpha;
+        }
+        ps[R * LP + tx] = e0;
+        ps[R * LP + tx + 16] = e1;
+      }
+      __syncwarp();  // a row's P is written and read by the same half warp
+      // ---- weighted values of rows 4 ty + i, dims 4 tx + 64 k .. ----
+      if (!tail && page_ok == 0xffffffffu) {
+#pragma unroll 4
+        for (int t = 0; t < kTok; ++t) {
+          float p[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) p[i] = ps[(4 * ty + i) * LP + t];
+#pragma unroll
+          for (int k = 0; k < NQ; ++k) {
+            const float4 v = *reinterpret_cast<const float4*>(vs + t * LD + 4 * tx + 64 * k);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) fma4(acc[i][k], p[i], v);
+          }
+        }
+      } else {  // an unseen value may be infinite or NaN: it takes no part at all
+        for (int t = 0; t < kTok; ++t) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            if (!((seen[i] >> t) & 1)) continue;
+            const float p = ps[(4 * ty + i) * LP + t];
+#pragma unroll
+            for (int k = 0; k < NQ; ++k)
+              fma4(acc[i][k], p, *reinterpret_cast<const float4*>(vs + t * LD + 4 * tx + 64 * k));
+          }
+        }
+      }
+    }
+    // ---- the run's rows: finished, or a partial ----
+    const float vsc = KV::bytes == 1 ? a.v_scales[j] : 1.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = 4 * ty + i;
+      if (r >= run.rows) continue;
+      if (run.whole) {
+        const int R = run.row0 + r, t = R / a.group, g = R % a.group;
+        TQ* o = static_cast<TQ*>(a.out) +
+                (((int64_t)b * a.nodes + t) * a.h_q + j * a.group + g) * D + 4 * tx;
+#pragma unroll
+        for (int k = 0; k < NQ; ++k) {
+          const float4 v = acc[i][k];
+          const bool any = l[i] != 0.f;  // (a NaN sum stays NaN)
+          store4(o + 64 * k, any ? make_float4(v.x / l[i] * vsc, v.y / l[i] * vsc,
+                                               v.z / l[i] * vsc, v.w / l[i] * vsc)
+                                 : make_float4(0.f, 0.f, 0.f, 0.f));
+        }
+      } else {
+        const size_t part = ((size_t)blockIdx.x * 2 + run.slot) * kRows + r;
+#pragma unroll
+        for (int k = 0; k < NQ; ++k) {
+          const float4 v = acc[i][k];
+          store4(a.ws_acc + part * D + 4 * tx + 64 * k,
+                 make_float4(v.x * vsc, v.y * vsc, v.z * vsc, v.w * vsc));
+        }
+        if (tx == 0) {
+          a.ws_ml[2 * part] = m[i];
+          a.ws_ml[2 * part + 1] = l[i];
+        }
+      }
+    }
+  }
+}
+
+// ---- combine ---------------------------------------------------------------------------------
+
+// Rows of the passes that crossed shares: with partials c = 0 .. n-1 of a row in share order,
+// M = max m_c, out = sum 2^(m_c - M) acc_c / sum 2^(m_c - M) l_c. A warp merges one row at a time;
+// it reads the (m, l) pairs of up to 32 partials at once and the values of eight together. Launched
+// as a programmatic dependent: the split is worked out while the attention still runs.
+constexpr int kCombineThreads = 128;
+constexpr int kCombineRows = 16;  // rows of a block
+
+template <typename TQ, int D>
+__global__ void __launch_bounds__(kCombineThreads) tree_combine_kernel(const TreeArgs a) {
+  constexpr int DL = D / 32;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int j = blockIdx.y, b = blockIdx.z;
+  const int row_block = blockIdx.x * kCombineRows;
+  __shared__ long long scratch[33];
+  const TreeReq req = tree_request(a, b);
+  const TreeSize z = tree_size(a, req);
+  const int rows = req.nodes * a.group;
+  // this grid must not complete before the attention does, also when nothing is left to merge
+  const bool first_block = blockIdx.x == 0 && j == 0 && b == 0;
+  if (row_block >= rows) {
+    if (first_block) asm volatile("griddepcontrol.wait;" ::: "memory");
+    return;
+  }
+  long long before = 0, all = 0;
+  for (int i = threadIdx.x; i < a.batch; i += kCombineThreads) {
+    const long long t = tree_tiles(a, tree_size(a, tree_request(a, i)));
+    all += t;
+    if (i < b) before += t;
+  }
+  long long below, total, pre;
+  block_scan<kCombineThreads>(all, scratch, below, total);
+  block_scan<kCombineThreads>(before, scratch, below, pre);
+  const long long share = tree_share_size(a, total);
+  const int unit = row_block / a.unit_rows;  // (unit_rows is a multiple of kCombineRows)
+  const long long start = pre + ((long long)j * z.units + unit) * z.tiles;
+  const int c0 = (int)(start / share), c1 = (int)((start + z.tiles - 1) / share);
+  if (c0 == c1) {
+    if (first_block) asm volatile("griddepcontrol.wait;" ::: "memory");
+    return;
+  }
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int n = c1 - c0 + 1;
+  for (int rr = warp; rr < kCombineRows; rr += kCombineThreads / 32) {
+    const int R = row_block + rr;
+    if (R >= rows) break;
+    const int r = R - unit * a.unit_rows;
+    auto part = [&](int c) {  // partial c of the pass (it begins in share c0)
+      return ((size_t)(c0 + c) * 2 + (c == 0 ? 1 : 0)) * a.unit_rows + r;
+    };
+    float M = -INFINITY, L = 0.f, A[DL];
+#pragma unroll
+    for (int k = 0; k < DL; ++k) A[k] = 0.f;
+    for (int q0 = 0; q0 < n; q0 += 32) {
+      const int nc = min(32, n - q0);
+      float2 ml = make_float2(-INFINITY, 0.f);
+      if (lane < nc) ml = *reinterpret_cast<const float2*>(a.ws_ml + 2 * part(q0 + lane));
+      float mr = ml.x;
+#pragma unroll
+      for (int o = 16; o >= 1; o /= 2) mr = fmaxf(mr, __shfl_xor_sync(0xffffffffu, mr, o));
+      const float Mn = fmaxf(M, mr);
+      const float Mu = Mn == -INFINITY ? 0.f : Mn;
+      const float rescale = exp2f(M - Mu);
+      // a partial that saw nothing weighs 0; a NaN sum stays one whatever its weight
+      const float w = ml.x == -INFINITY ? 0.f : exp2f(ml.x - Mu);
+      float lw = w != 0.f || ml.y != ml.y ? w * ml.y : 0.f;
+#pragma unroll
+      for (int o = 16; o >= 1; o /= 2) lw += __shfl_xor_sync(0xffffffffu, lw, o);
+      L = fmaf(L, rescale, lw);
+#pragma unroll
+      for (int k = 0; k < DL; ++k) A[k] *= rescale;
+      M = Mn;
+      for (int q = 0; q < nc; q += 8) {
+        float v[8][DL];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          const float* src = a.ws_acc + part(q0 + min(q + u, nc - 1)) * D + lane * DL;
+          if constexpr (DL == 4) {
+            const float4 x = *reinterpret_cast<const float4*>(src);
+            v[u][0] = x.x; v[u][1] = x.y; v[u][2] = x.z; v[u][3] = x.w;
+          } else {
+            const float2 x = *reinterpret_cast<const float2*>(src);
+            v[u][0] = x.x; v[u][1] = x.y;
+          }
+        }
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          const float wu = __shfl_sync(0xffffffffu, w, (q + u) & 31);
+          if (q + u < nc && wu != 0.f) {
+#pragma unroll
+            for (int k = 0; k < DL; ++k) A[k] = fmaf(wu, v[u][k], A[k]);
+          }
+        }
+      }
+    }
+    const int t = R / a.group, g = R % a.group;
+    TQ* o = static_cast<TQ*>(a.out) + (((int64_t)b * a.nodes + t) * a.h_q + j * a.group + g) * D +
+            lane * DL;
+#pragma unroll
+    for (int k = 0; k < DL; ++k) store_from_float(o, k, L != 0.f ? A[k] / L : 0.f);
+  }
+}
+
+template <typename KV, typename Q, int D>
+cudaError_t simt_go(const TreeArgs& a, cudaStream_t s) {
+  static std::atomic<unsigned long long> attr_done{0};  // one bit per device
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= 64 || !((attr_done.load() >> dev) & 1ull)) {
+    e = cudaFuncSetAttribute(tree_simt_kernel<KV, Q, D>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, SimtShape<D>::SMEM);
+    if (e != cudaSuccess) return e;
+    if (dev < 64) attr_done.fetch_or(1ull << dev);
+  }
+  tree_simt_kernel<KV, Q, D><<<a.ctas, kThreads, SimtShape<D>::SMEM, s>>>(a);
+  return cudaGetLastError();
+}
+
+template <int D>
+cudaError_t simt_types(const TreeArgs& a, int q_dtype, int kv_dtype, cudaStream_t s) {
+  if (q_dtype == PKV_F32) {
+    if (kv_dtype == PKV_F32) return simt_go<F32, F32, D>(a, s);
+    if (kv_dtype == PKV_FP8_E4M3) return simt_go<FP8, F32, D>(a, s);
+    return simt_go<INT8, F32, D>(a, s);
+  }
+  if (kv_dtype == PKV_BF16) return simt_go<BF16, BF16, D>(a, s);
+  if (kv_dtype == PKV_FP8_E4M3) return simt_go<FP8, BF16, D>(a, s);
+  return simt_go<INT8, BF16, D>(a, s);
+}
+
+template <typename TQ, int D>
+cudaError_t launch_combine(const TreeArgs& a, cudaStream_t s) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((a.nodes * a.group + kCombineRows - 1) / kCombineRows, a.h_kv, a.batch);
+  cfg.blockDim = dim3(kCombineThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, tree_combine_kernel<TQ, D>, a);
+}
+
+}  // namespace
+
+cudaError_t launch_tree_simt(const TreeArgs& a, int q_dtype, int kv_dtype, int head_dim,
+                             cudaStream_t s) {
+  return head_dim == 64 ? simt_types<64>(a, q_dtype, kv_dtype, s)
+                        : simt_types<128>(a, q_dtype, kv_dtype, s);
+}
+
+cudaError_t launch_tree_combine(const TreeArgs& a, int q_dtype, int head_dim, cudaStream_t s) {
+  static_assert(kTreeSimtRows % kCombineRows == 0, "a combine block lies in one unit");
+  if (q_dtype == PKV_BF16)
+    return head_dim == 64 ? launch_combine<__nv_bfloat16, 64>(a, s)
+                          : launch_combine<__nv_bfloat16, 128>(a, s);
+  return head_dim == 64 ? launch_combine<float, 64>(a, s) : launch_combine<float, 128>(a, s);
+}
+
+}  // namespace pkv
