@@ -3,6 +3,8 @@
 #include <algorithm>
 #include <cmath>
 
+#include <cuda.h>
+
 #include "capi_util.h"
 #include "pkv.h"
 #include "pkv_internal.h"
@@ -15,10 +17,13 @@ namespace {
 // kernel that a call uses.
 struct TreeSplit {
   int rows, tokens, min_tiles, wave;
+  bool tc;
 };
 
-TreeSplit tree_split() {
-  return TreeSplit{kTreeSimtRows, kTreeSimtTokens, 4, kTreeSimtWave};
+// bf16 queries run on the tensor cores, fp32 queries (whose weights keep 24 bits) on CUDA cores.
+TreeSplit tree_split(int dtype_q) {
+  if (dtype_q == PKV_BF16) return TreeSplit{kTreeTcRows, kTreeTcTokens, 2, kTreeTcWave, true};
+  return TreeSplit{kTreeSimtRows, kTreeSimtTokens, 4, kTreeSimtWave, false};
 }
 
 // CTAs of a call: one wave, or fewer when the table cannot hold that many shares.
@@ -54,8 +59,8 @@ int check_tree_sizes(const char* who, int batch, int nodes, int h_q, int h_kv, i
                      PKV_MAX_TREE_NODES, PKV_MAX_TREE_GROUP);
   if (h_kv > 65535 || batch > 65535)
     return set_error(PKV_ESHAPE, "%s: batch and kv heads must be <= 65535", who);
-  if (max_pages > (1 << 27) - 1)
-    return set_error(PKV_ESHAPE, "%s: a table row holds more than 2^31 positions", who);
+  if (max_pages > (1 << 27) - 16)  // (positions and tile ends stay below 2^31)
+    return set_error(PKV_ESHAPE, "%s: a table row holds 2^31 positions or more", who);
   return PKV_OK;
 }
 
@@ -148,7 +153,7 @@ size_t pkv_tree_decode_workspace_size(int32_t dtype_q, int32_t cache_dtype, int3
   if (batch <= 0 || tree_width <= 0 || num_q_heads <= 0 || num_kv_heads <= 0 || head_dim <= 0 ||
       max_pages_per_seq <= 0)
     return 0;
-  const TreeSplit t = tree_split();
+  const TreeSplit t = tree_split(dtype_q);
   const int ctas = tree_ctas(t, batch, tree_width, num_q_heads, num_kv_heads, max_pages_per_seq);
   return tree_acc_bytes(t, ctas, head_dim) + tree_ml_bytes(t, ctas);
 }
@@ -185,7 +190,10 @@ int pkv_tree_decode_attention(const void* q, int32_t dtype_q, int32_t batch, int
       (reinterpret_cast<uintptr_t>(tree_mask) & 7u))
     return set_error(PKV_EALIGN, "%s: q, out and pools must be 16-byte, the mask 8-byte aligned",
                      who);
-  const TreeSplit t = tree_split();
+  if (dtype_q == PKV_BF16 && kv == PKV_BF16 &&
+      (long long)desc->num_pages * h_kv * desc->page_size >= (1ll << 31))
+    return set_error(PKV_ESHAPE, "%s: a bf16 pool must have fewer than 2^31 rows", who);
+  const TreeSplit t = tree_split(dtype_q);
   TreeArgs a{};
   a.ctas = tree_ctas(t, batch, tree_width, num_q_heads, h_kv, max_pages_per_seq);
   const size_t acc = tree_acc_bytes(t, a.ctas, D), need = acc + tree_ml_bytes(t, a.ctas);
@@ -221,8 +229,16 @@ int pkv_tree_decode_attention(const void* q, int32_t dtype_q, int32_t batch, int
   st = error_word(&a.err);
   if (st != PKV_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  cudaError_t e =
-      traced("tree_attention", s, [&] { return launch_tree_simt(a, dtype_q, kv, D, s); });
+  CUtensorMap tk{}, tv{};
+  if (t.tc && kv == PKV_BF16) {
+    int rank = 2;
+    st = pool_tensor_map(k_cache, desc, &tk, &rank, true);
+    if (st == PKV_OK) st = pool_tensor_map(v_cache, desc, &tv, &a.tma_rank);
+    if (st != PKV_OK) return st;
+  }
+  cudaError_t e = traced("tree_attention", s, [&] {
+    return t.tc ? launch_tree_tc(a, kv, D, &tk, &tv, s) : launch_tree_simt(a, kv, D, s);
+  });
   st = cuda_status(e, "tree_attention launch");
   if (st != PKV_OK || a.ctas == 1) return st;  // (one CTA finishes every pass)
   e = traced("tree_combine", s, [&] { return launch_tree_combine(a, dtype_q, D, s); });

@@ -175,11 +175,16 @@ struct CommitArgs {
 // Each returns the launch status. dtype codes are pkv_dtype values.
 cudaError_t launch_qk_norm_rope_append(const NormRopeArgs& a, int io_dtype, int cache_dtype,
                                        cudaStream_t s);
-// Tree attention on CUDA cores (every type and head dimension) and the combine of any split.
+// Tree attention on CUDA cores (fp32 queries) and the combine of any split.
 constexpr int kTreeSimtRows = 32, kTreeSimtTokens = 32;
 constexpr int kTreeSimtWave = 152 * 4;  // four 55 KB CTAs fit an SM
-cudaError_t launch_tree_simt(const TreeArgs& a, int q_dtype, int kv_dtype, int head_dim,
-                             cudaStream_t s);
+cudaError_t launch_tree_simt(const TreeArgs& a, int kv_dtype, int head_dim, cudaStream_t s);
+// The same on tcgen05: bf16 queries; tk/tv: the 2-D K map and the V map of a bf16 pool (unused for
+// 8-bit caches).
+constexpr int kTreeTcRows = 256, kTreeTcTokens = 64;
+constexpr int kTreeTcWave = 152;  // one CTA per SM
+cudaError_t launch_tree_tc(const TreeArgs& a, int kv_dtype, int head_dim, const void* tk,
+                           const void* tv, cudaStream_t s);
 cudaError_t launch_tree_combine(const TreeArgs& a, int q_dtype, int head_dim, cudaStream_t s);
 cudaError_t launch_tree_commit(const CommitArgs& a, cudaStream_t s);
 cudaError_t launch_decode_f32(const DecodeArgs& a, int q_dtype, int head_dim, int group,

@@ -359,15 +359,10 @@ cudaError_t simt_go(const TreeArgs& a, cudaStream_t s) {
 }
 
 template <int D>
-cudaError_t simt_types(const TreeArgs& a, int q_dtype, int kv_dtype, cudaStream_t s) {
-  if (q_dtype == PKV_F32) {
-    if (kv_dtype == PKV_F32) return simt_go<F32, F32, D>(a, s);
-    if (kv_dtype == PKV_FP8_E4M3) return simt_go<FP8, F32, D>(a, s);
-    return simt_go<INT8, F32, D>(a, s);
-  }
-  if (kv_dtype == PKV_BF16) return simt_go<BF16, BF16, D>(a, s);
-  if (kv_dtype == PKV_FP8_E4M3) return simt_go<FP8, BF16, D>(a, s);
-  return simt_go<INT8, BF16, D>(a, s);
+cudaError_t simt_types(const TreeArgs& a, int kv_dtype, cudaStream_t s) {
+  if (kv_dtype == PKV_F32) return simt_go<F32, F32, D>(a, s);
+  if (kv_dtype == PKV_FP8_E4M3) return simt_go<FP8, F32, D>(a, s);
+  return simt_go<INT8, F32, D>(a, s);
 }
 
 template <typename TQ, int D>
@@ -386,10 +381,8 @@ cudaError_t launch_combine(const TreeArgs& a, cudaStream_t s) {
 
 }  // namespace
 
-cudaError_t launch_tree_simt(const TreeArgs& a, int q_dtype, int kv_dtype, int head_dim,
-                             cudaStream_t s) {
-  return head_dim == 64 ? simt_types<64>(a, q_dtype, kv_dtype, s)
-                        : simt_types<128>(a, q_dtype, kv_dtype, s);
+cudaError_t launch_tree_simt(const TreeArgs& a, int kv_dtype, int head_dim, cudaStream_t s) {
+  return head_dim == 64 ? simt_types<64>(a, kv_dtype, s) : simt_types<128>(a, kv_dtype, s);
 }
 
 cudaError_t launch_tree_combine(const TreeArgs& a, int q_dtype, int head_dim, cudaStream_t s) {
