@@ -26,14 +26,6 @@ TreeSplit tree_split(int dtype_q) {
   return TreeSplit{kTreeSimtRows, kTreeSimtTokens, 4, kTreeSimtWave, false};
 }
 
-// CTAs of a call: one wave, or fewer when the table cannot hold that many shares.
-int tree_ctas(const TreeSplit& t, int batch, int nodes, int h_q, int h_kv, int max_pages) {
-  const long long units = ((long long)nodes * (h_q / h_kv) + t.rows - 1) / t.rows;
-  const long long tiles = ((long long)max_pages * 16 + t.tokens - 1) / t.tokens;
-  const long long most = ((long long)batch * h_kv * units * tiles + t.min_tiles - 1) / t.min_tiles;
-  return (int)std::max(1ll, std::min<long long>(t.wave, most));
-}
-
 size_t tree_acc_bytes(const TreeSplit& t, int ctas, int head_dim) {
   return align256((size_t)ctas * 2 * t.rows * head_dim * sizeof(float));
 }
@@ -47,6 +39,20 @@ int check_tree_types(const char* who, int dtype_q, int kv) {
   if (!is_coded(kv) && kv != dtype_q)
     return set_error(PKV_EDTYPE, "%s: q dtype must match an F32/BF16 cache", who);
   return PKV_OK;
+}
+
+// Tiles that the call's table could hold at most.
+long long tree_most_tiles(const TreeSplit& t, int batch, int nodes, int h_q, int h_kv,
+                          int max_pages) {
+  const long long units = ((long long)nodes * (h_q / h_kv) + t.rows - 1) / t.rows;
+  const long long tiles = ((long long)max_pages * 16 + t.tokens - 1) / t.tokens;
+  return (long long)batch * h_kv * units * tiles;
+}
+
+// CTAs of a call: one wave, or fewer when the table cannot hold that many shares.
+int tree_ctas(const TreeSplit& t, int batch, int nodes, int h_q, int h_kv, int max_pages) {
+  const long long tiles = tree_most_tiles(t, batch, nodes, h_q, h_kv, max_pages);
+  return (int)std::max(1ll, std::min<long long>(t.wave, (tiles + t.min_tiles - 1) / t.min_tiles));
 }
 
 int check_tree_sizes(const char* who, int batch, int nodes, int h_q, int h_kv, int max_pages) {
@@ -194,6 +200,8 @@ int pkv_tree_decode_attention(const void* q, int32_t dtype_q, int32_t batch, int
       (long long)desc->num_pages * h_kv * desc->page_size >= (1ll << 31))
     return set_error(PKV_ESHAPE, "%s: a bf16 pool must have fewer than 2^31 rows", who);
   const TreeSplit t = tree_split(dtype_q);
+  if (tree_most_tiles(t, batch, tree_width, num_q_heads, h_kv, max_pages_per_seq) >= (1ll << 31))
+    return set_error(PKV_ESHAPE, "%s: the table can hold 2^31 tiles of work or more", who);
   TreeArgs a{};
   a.ctas = tree_ctas(t, batch, tree_width, num_q_heads, h_kv, max_pages_per_seq);
   const size_t acc = tree_acc_bytes(t, a.ctas, D), need = acc + tree_ml_bytes(t, a.ctas);

@@ -53,10 +53,6 @@ __device__ __forceinline__ void fma4(float4& acc, float p, const float4& v) {
 __device__ __forceinline__ void store4(float* p, const float4& v) {
   *reinterpret_cast<float4*>(p) = v;
 }
-__device__ __forceinline__ void store4(__nv_bfloat16* p, const float4& v) {
-  __nv_bfloat162 w[2] = {__floats2bfloat162_rn(v.x, v.y), __floats2bfloat162_rn(v.z, v.w)};
-  *reinterpret_cast<uint2*>(p) = *reinterpret_cast<uint2*>(w);
-}
 
 template <typename KV, typename Q, int D>
 __global__ void __launch_bounds__(kThreads) tree_simt_kernel(const TreeArgs a) {
@@ -69,7 +65,7 @@ __global__ void __launch_bounds__(kThreads) tree_simt_kernel(const TreeArgs a) {
   float* ks = qs + kRows * LD;
   float* vs = ks + kTok * LD;
   float* ps = vs + kTok * LD;
-  __shared__ long long scratch[33];
+  __shared__ int scratch[32];
   __shared__ TreeShare share;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   tree_share<kThreads>(a, scratch, &share);
@@ -253,7 +249,7 @@ __global__ void __launch_bounds__(kCombineThreads) tree_combine_kernel(const Tre
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int j = blockIdx.y, b = blockIdx.z;
   const int row_block = blockIdx.x * kCombineRows;
-  __shared__ long long scratch[33];
+  __shared__ int scratch[2][32];
   const TreeReq req = tree_request(a, b);
   const TreeSize z = tree_size(a, req);
   const int rows = req.nodes * a.group;
@@ -263,19 +259,19 @@ __global__ void __launch_bounds__(kCombineThreads) tree_combine_kernel(const Tre
     if (first_block) asm volatile("griddepcontrol.wait;" ::: "memory");
     return;
   }
-  long long before = 0, all = 0;
+  int before = 0, all = 0;
   for (int i = threadIdx.x; i < a.batch; i += kCombineThreads) {
-    const long long t = tree_tiles(a, tree_size(a, tree_request(a, i)));
+    const int t = tree_tiles(a, tree_size(a, tree_request(a, i)));
     all += t;
     if (i < b) before += t;
   }
-  long long below, total, pre;
-  block_scan<kCombineThreads>(all, scratch, below, total);
-  block_scan<kCombineThreads>(before, scratch, below, pre);
-  const long long share = tree_share_size(a, total);
+  int below, total, pre;
+  block_scan<kCombineThreads>(all, scratch[0], below, total);
+  block_scan<kCombineThreads>(before, scratch[1], below, pre);
+  const int share = tree_share_size(a, total);
   const int unit = row_block / a.unit_rows;  // (unit_rows is a multiple of kCombineRows)
-  const long long start = pre + ((long long)j * z.units + unit) * z.tiles;
-  const int c0 = (int)(start / share), c1 = (int)((start + z.tiles - 1) / share);
+  const int start = pre + (j * z.units + unit) * z.tiles;
+  const int c0 = start / share, c1 = (start + z.tiles - 1) / share;
   if (c0 == c1) {
     if (first_block) asm volatile("griddepcontrol.wait;" ::: "memory");
     return;

@@ -51,8 +51,8 @@ constexpr int kPages = kTok / kPageSize;   // pages of a tile
 constexpr int kGroupThreads = 128;         // a softmax group: one row per thread
 constexpr int kSoftThreads = 2 * kGroupThreads;
 constexpr int kMmaWarp = kSoftThreads / 32;
-constexpr int kCopyWarp = kMmaWarp + 1;
-constexpr int kConvWarp = kCopyWarp + 1;   // first of four (8-bit caches)
+constexpr int kCopyWarp = kMmaWarp + 1;    // (its warpgroup's last two warps are idle)
+constexpr int kConvWarp = kMmaWarp + 4;    // first of four (8-bit caches)
 constexpr int kConvThreads = 128;
 constexpr int kSBufs = 3;
 // tensor memory columns: O of group 0 and 1, Q of the rows 0 .. 127 and 128 .. 255, S (then P)
@@ -66,6 +66,8 @@ template <typename KV, int D>
 struct TcShape {
   static constexpr bool W8 = KV::bytes == 1;
   static constexpr int THREADS = 32 * (W8 ? kConvWarp + kConvThreads / 32 : kConvWarp);
+  // registers of the softmax warps and of the others, out of what the launch gives every warp
+  static constexpr int SOFT_REGS = W8 ? 176 : 208, REGS = W8 ? 72 : 80;
   static constexpr int TILE = kTok * D * 2;       // K (or V) of a tile in MMA form
   static constexpr int STAGE = 2 * TILE;
   static constexpr int RAW_TILE = kTok * D;       // 8-bit codes
@@ -88,31 +90,59 @@ __device__ __forceinline__ uint32_t s_col(int buf) {
   return buf == 2 ? kColS2 : kColS + 64 * buf;
 }
 
-// Steps of a unit in order: with up to 128 rows step u is tile u, otherwise tile u / 2 for rows
-// 128 (u % 2) ... Group u % 2 takes it; it uses S buffer u % bufs.
-struct Steps {
-  int n, bufs;
-  bool wide;
-  __device__ __forceinline__ explicit Steps(const TreeRun& r)
-      : n(r.rows > kGroupThreads ? 2 * r.n : r.n),
-        bufs(r.rows > kGroupThreads ? 2 : kSBufs),
-        wide(r.rows > kGroupThreads) {}
-  __device__ __forceinline__ int tile(int u) const { return wide ? u >> 1 : u; }
-  __device__ __forceinline__ int buf(int u) const { return wide ? u & 1 : u % 3; }
-  // parity of the buffer's barriers in step u; `ph` holds each buffer's parity at the unit's start
-  __device__ __forceinline__ uint32_t parity(uint32_t ph, int u) const {
-    return ((ph >> buf(u)) ^ (wide ? u >> 1 : u / 3)) & 1u;
-  }
-  __device__ __forceinline__ uint32_t after(uint32_t ph) const {
-#pragma unroll
-    for (int b = 0; b < kSBufs; ++b) {
-      if (b >= bufs) break;
-      const int uses = wide ? n / 2 : (n + 2 - b) / 3;
-      ph ^= (uint32_t)(uses & 1) << b;
+// A unit's steps in order: with up to 128 rows step u is tile u, otherwise ("wide") tile u / 2 for
+// rows 128 (u % 2) ... Group u % 2 takes it. S buffers go round, 3 or 2 of them; every buffer's
+// three barriers complete once per step that uses it.
+struct Buf {
+  int i;       // buffer
+  uint32_t q;  // parity of its uses in this unit before this step
+  __device__ __forceinline__ void advance(bool wide, int steps) {  // by 1 or 2 steps
+    const int bufs = wide ? 2 : kSBufs;
+    i += steps;
+    if (i >= bufs) {
+      i -= bufs;
+      q ^= 1u;
     }
-    return ph;
+  }
+  // parity of the barriers in this step; ph holds each buffer's at the unit's start
+  __device__ __forceinline__ uint32_t parity(uint32_t ph) const { return ((ph >> i) ^ q) & 1u; }
+};
+
+// The buffers' parities after a unit of n steps.
+__device__ __forceinline__ uint32_t after_steps(uint32_t ph, bool wide, int n) {
+  if (wide) return ph ^ ((n >> 1) & 1 ? 3u : 0u);
+  const uint32_t t = (uint32_t)n / 3u, m = (uint32_t)n - 3u * t;
+  if (t & 1) ph ^= 7u;
+  return ph ^ ((1u << m) - 1u);
+}
+
+// A place in a ring of N stages and the parity of its current use.
+template <int N>
+struct Place {
+  int st = 0;
+  uint32_t par = 0;
+  __device__ __forceinline__ void advance(int k) {  // k <= N
+    st += k;
+    if (st >= N) {
+      st -= N;
+      par ^= 1u;
+    }
+  }
+  __device__ __forceinline__ void skip(int k) {  // any k
+    const int t = st + k, w = t / N;
+    st = t - w * N;
+    par ^= (uint32_t)w & 1u;
   }
 };
+
+template <int N>
+__device__ __forceinline__ void regs_up() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_down() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
 
 template <bool F16>
 __device__ __forceinline__ uint32_t pack_p(float a, float b) {
@@ -156,24 +186,24 @@ __global__ void __launch_bounds__(TcShape<KV, D>::THREADS, 1) tree_tc_kernel(
   uint32_t* s_taddr = bad_nodes + 16;
   float2* ml = reinterpret_cast<float2*>(smem + S::OFF_ML);          // [2][128]
 
-  __shared__ long long scratch[33];
+  __shared__ int scratch[32];
   __shared__ TreeShare share;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (threadIdx.x == kCopyWarp * 32) {
     for (int s = 0; s < NS; ++s) {
-      mbar_init(&full[s], W8 ? kConvThreads : 1);
+      mbar_init(&full[s], W8 ? kConvThreads / 32 : 1);
       mbar_init(&freed[s], 1);
     }
     for (int s = 0; s < NR; ++s) {
       mbar_init(&raw_full[s], 1);
-      mbar_init(&raw_freed[s], kConvThreads);
+      mbar_init(&raw_freed[s], kConvThreads / 32);
     }
     for (int s = 0; s < kSBufs; ++s) {
       mbar_init(&s_done[s], 1);
-      mbar_init(&p_ready[s], kGroupThreads);
+      mbar_init(&p_ready[s], kGroupThreads / 32);
       mbar_init(&pv_done[s], 1);
     }
-    mbar_init(q_ready, kSoftThreads);
+    mbar_init(q_ready, kSoftThreads / 32);
     mbar_init(mma_idle, 1);
     mbar_fence_init();
     if constexpr (!W8) {
@@ -198,182 +228,206 @@ __global__ void __launch_bounds__(TcShape<KV, D>::THREADS, 1) tree_tc_kernel(
   TreeWalk walk{share.b, share.off, share.count};
   TreeRun run;
 
-  if (warp == kCopyWarp) {
-    // ===================== copies: the share's tiles, in order =====================
-    constexpr int N = W8 ? NR : NS;
-    uint64_t* const arrive = W8 ? raw_full : full;
-    uint64_t* const leave = W8 ? raw_freed : freed;
-    int* const masks = W8 ? raw_mask : page_mask;
-    // the row units of more than 256 rows read the same tiles again
-    const uint64_t pol =
-        a.nodes * a.group > kTreeTcRows ? l2_evict_last_policy() : l2_evict_first_policy();
-    uint32_t gt = 0;
-    bool ok = true;
-    while (ok && walk.next(a, run)) {
-      const int pages = (run.req.read + kPageSize - 1) / kPageSize;
-      const int32_t* table = a.block_tables + (size_t)run.b * a.max_pages;
-      const int first = run.tile0 * kPages;
-      int ids = -1;  // lane L: the id of page 32 m + L of the run (8 tiles a batch)
-      for (int i = 0; i < run.n; ++i, ++gt) {
-        if ((i & 7) == 0) {
-          const int lp = first + kPages * i + lane;
-          ids = lp < pages ? table[lp] : -1;
-        }
-        int pid[kPages];
-#pragma unroll
-        for (int p = 0; p < kPages; ++p)
-          pid[p] = __shfl_sync(0xffffffffu, ids, (kPages * i + p) & 31);
-        const uint32_t st = gt % N;
-        if (gt >= N) {
-          ok = mbar_wait(&leave[st], (gt / N - 1) & 1u, a.err);
-          ok = __all_sync(0xffffffffu, ok);
-          if (!ok) break;
-        }
-        if (lane != 0) continue;
-        int mask = 0;
-#pragma unroll
-        for (int p = 0; p < kPages; ++p) {
-          if (first + kPages * i + p >= pages) continue;
-          if (pid[p] < 0 || pid[p] >= a.num_pages)
-            atomicOr(a.err, PKV_DEVERR_BAD_PAGE);
-          else
-            mask |= 1 << p;
-        }
-        masks[st] = mask;
-        if constexpr (W8) fence_proxy_async_smem();
-        mbar_arrive_expect_tx(&arrive[st],
-                              __popc(mask) * 2 * (W8 ? PAGE_RAW : PAGE_MMA));
-#pragma unroll
-        for (int p = 0; p < kPages; ++p) {
-          if (!((mask >> p) & 1)) continue;
-          if constexpr (W8) {
-            const int64_t src = ((int64_t)pid[p] * a.h_kv + run.j) * PAGE_RAW;
-            uint8_t* dst = smem + S::OFF_RAW + st * S::RAW_STAGE + p * PAGE_RAW;
-            bulk_g2s(dst, static_cast<const uint8_t*>(a.k_cache) + src, PAGE_RAW, &arrive[st], pol);
-            bulk_g2s(dst + S::RAW_TILE, static_cast<const uint8_t*>(a.v_cache) + src, PAGE_RAW,
-                     &arrive[st], pol);
-          } else {
-            const int row = (pid[p] * a.h_kv + run.j) * kPageSize;
-            const uint32_t dst = ring + st * S::STAGE;
-            // K: 64-dim blocks of all 64 rows (one N = 64 operand); V: one block per page (K = 16)
-#pragma unroll
-            for (int bx = 0; bx < D / 64; ++bx)
-              tma_load_2d(dst + bx * (kTok * 128) + p * 2048, &tm_k, bx * 64, row, &arrive[st], pol);
-            tma_tile<D / 64, 64>(dst + S::TILE + p * PAGE_MMA, &tm_v, a.tma_rank, row, &arrive[st],
-                                 pol);
+  if (warp >= kMmaWarp && warp < kConvWarp) {
+    regs_down<S::REGS>();
+    if (warp == kCopyWarp) {
+      // ===================== copies: the share's tiles, in order =====================
+      constexpr int N = W8 ? NR : NS;
+      uint64_t* const arrive = W8 ? raw_full : full;
+      uint64_t* const leave = W8 ? raw_freed : freed;
+      int* const masks = W8 ? raw_mask : page_mask;
+      // the row units of more than 256 rows read the same tiles again
+      const uint64_t pol =
+          a.nodes * a.group > kTreeTcRows ? l2_evict_last_policy() : l2_evict_first_policy();
+      Place<N> at;
+      int issued = 0;
+      bool ok = true;
+      while (ok && walk.next(a, run)) {
+        const int pages = (run.req.read + kPageSize - 1) / kPageSize;
+        const int32_t* table = a.block_tables + (size_t)run.b * a.max_pages;
+        int lp = run.tile0 * kPages + lane;  // lane p: page p of the tile (p < 4)
+        int ids = -1;                        // lane L: the id of page 32 m + L of the run
+        for (int i = 0; i < run.n; ++i, lp += kPages) {
+          if ((i & 7) == 0) ids = lp < pages ? table[lp] : -1;
+          const int id = __shfl_sync(0xffffffffu, ids, (kPages * i + lane) & 31);
+          const bool there = lane < kPages && lp < pages;
+          const bool good = there && id >= 0 && id < a.num_pages;
+          if (there && !good) atomicOr(a.err, PKV_DEVERR_BAD_PAGE);
+          const uint32_t mask = __ballot_sync(0xffffffffu, good);
+          if (issued >= N) {
+            ok = mbar_wait(&leave[at.st], at.par ^ 1u, a.err);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
           }
+          if (lane == 0) {
+            masks[at.st] = (int)mask;
+            if constexpr (W8) fence_proxy_async_smem();
+            mbar_arrive_expect_tx(&arrive[at.st], __popc(mask) * 2 * (W8 ? PAGE_RAW : PAGE_MMA));
+          }
+          __syncwarp();
+          if (good) {  // lane p copies page p
+            if constexpr (W8) {
+              const int64_t src = ((int64_t)id * a.h_kv + run.j) * PAGE_RAW;
+              uint8_t* dst = smem + S::OFF_RAW + at.st * S::RAW_STAGE + lane * PAGE_RAW;
+              bulk_g2s(dst, static_cast<const uint8_t*>(a.k_cache) + src, PAGE_RAW,
+                       &arrive[at.st], pol);
+              bulk_g2s(dst + S::RAW_TILE, static_cast<const uint8_t*>(a.v_cache) + src, PAGE_RAW,
+                       &arrive[at.st], pol);
+            } else {
+              const int row = (id * a.h_kv + run.j) * kPageSize;
+              const uint32_t dst = ring + at.st * S::STAGE;
+              // K: 64-dim blocks of all 64 rows (one N = 64 operand); V: a block per page (K = 16)
+#pragma unroll
+              for (int bx = 0; bx < D / 64; ++bx)
+                tma_load_2d(dst + bx * (kTok * 128) + lane * 2048, &tm_k, bx * 64, row,
+                            &arrive[at.st], pol);
+              tma_tile<D / 64, 64>(dst + S::TILE + lane * PAGE_MMA, &tm_v, a.tma_rank, row,
+                                   &arrive[at.st], pol);
+            }
+          }
+          __syncwarp();
+          at.advance(1);
+          ++issued;
         }
       }
-    }
-    if (lane == 0)  // before leaving, every copy issued has landed
-      for (uint32_t t = gt > N ? gt - N : 0; t < gt; ++t)
-        mbar_wait(&arrive[t % N], (t / N) & 1u, a.err);
-  } else if (warp == kMmaWarp) {
-    // ===================== MMAs (lane 0) =====================
-    if (lane == 0) {
+      if (lane == 0) {  // before leaving, every copy issued has landed
+        for (int k = min(issued, N); k > 0; --k) {
+          const int back = issued - k;
+          mbar_wait(&arrive[back % N], (uint32_t)(back / N) & 1u, a.err);
+        }
+      }
+    } else if (warp == kMmaWarp && lane == 0) {
+      // ===================== MMAs (one lane) =====================
+      const uint64_t k_desc = tc_desc(ring, 16, 1024), v_desc = tc_desc(ring + S::TILE, 2048, 1024);
       bool ok = true;
       uint32_t ph = 0, unit = 0;
-      uint32_t gt = 0;  // tiles of earlier runs
-      for (; ok && walk.next(a, run); ++unit) {
-        const Steps st(run);
+      Place<NS> ks, vs;  // tiles of the next S and of the next P V
+      while (ok && walk.next(a, run)) {
+        const bool wide = run.rows > kGroupThreads;
+        const int n = wide ? 2 * run.n : run.n;
         ok = mbar_wait(q_ready, unit & 1, a.err);
+        ++unit;
         tc_fence_after();
-        auto s_mma = [&](int u) {
-          const uint32_t t = gt + st.tile(u), stage = t % NS;
-          if (!mbar_wait(&full[stage], (t / NS) & 1u, a.err)) return false;
+        bool odd = false;  // the next S's step
+        auto s_mma = [&](int buf) {
+          if (!mbar_wait(&full[ks.st], ks.par, a.err)) return false;
           tc_fence_after();
-          const uint32_t kb = ring + stage * S::STAGE;
-          const uint32_t q = tmem + kColQ + (st.wide && (u & 1) ? 64 : 0);
+          const uint64_t kd = k_desc + (uint32_t)(ks.st * (S::STAGE >> 4));
+          const uint32_t q = tmem + kColQ + (wide && odd ? 64 : 0), d = tmem + s_col(buf);
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk)
-            tc_mma_ta(tmem + s_col(st.buf(u)), q + 8 * kk,
-                      tc_desc(kb + (kk >> 2) * (kTok * 128) + (kk & 3) * 32, 16, 1024), S::IDESC_S,
-                      kk > 0 ? 1u : 0u);
-          tc_commit(&s_done[st.buf(u)]);
+            tc_mma_ta(d, q + 8 * kk, kd + (((kk >> 2) * (kTok * 128) + (kk & 3) * 32) >> 4),
+                      S::IDESC_S, kk > 0 ? 1u : 0u);
+          tc_commit(&s_done[buf]);
+          if (!wide || odd) ks.advance(1);
+          odd = !odd;
           return true;
         };
-        for (int u = 0; ok && u < st.bufs && u < st.n; ++u) ok = s_mma(u);
-        for (int u = 0; ok && u < st.n; ++u) {
-          const int b = st.buf(u);
-          ok = mbar_wait(&p_ready[b], st.parity(ph, u), a.err);
+        const int bufs = wide ? 2 : kSBufs;
+        for (int u = 0; ok && u < bufs && u < n; ++u) ok = s_mma(u);
+        Buf b{0, 0};
+        for (int u = 0; ok && u < n; ++u, b.advance(wide, 1)) {
+          const uint32_t par = b.parity(ph);
+          ok = mbar_wait(&p_ready[b.i], par, a.err);
           if (!ok) break;
           tc_fence_after();
-          const uint32_t stage = (gt + st.tile(u)) % NS;
-          const uint32_t vb = ring + stage * S::STAGE + S::TILE;
+          const uint64_t vd = v_desc + (uint32_t)(vs.st * (S::STAGE >> 4));
+          const uint32_t o = tmem + kColO + ((u & 1) << 7), pc = tmem + s_col(b.i);
 #pragma unroll
           for (int kk = 0; kk < kPages; ++kk)
-            tc_mma_ta(tmem + kColO + 128 * (u & 1), tmem + s_col(b) + 8 * kk,
-                      tc_desc(vb + kk * PAGE_MMA, 2048, 1024), S::IDESC_PV, u < 2 && kk == 0 ? 0u : 1u);
-          tc_commit(&pv_done[b]);
-          if (!st.wide || (u & 1)) tc_commit(&freed[stage]);
-          if (u + st.bufs < st.n) {  // its S overwrites the buffer that this P lives in
-            ok = mbar_wait(&pv_done[b], st.parity(ph, u), a.err);
-            if (ok) ok = s_mma(u + st.bufs);
+            tc_mma_ta(o, pc + 8 * kk, vd + ((kk * PAGE_MMA) >> 4), S::IDESC_PV,
+                      u < 2 && kk == 0 ? 0u : 1u);
+          tc_commit(&pv_done[b.i]);
+          if (!wide || (u & 1)) {
+            tc_commit(&freed[vs.st]);
+            vs.advance(1);
+          }
+          if (u + bufs < n) {  // its S overwrites the buffer that this P lives in
+            ok = mbar_wait(&pv_done[b.i], par, a.err);
+            if (ok) ok = s_mma(b.i);
           }
         }
-        ph = st.after(ph);
-        gt += run.n;
+        ph = after_steps(ph, wide, n);
       }
       tc_commit(mma_idle);  // before leaving, every MMA issued is complete
       mbar_wait(mma_idle, 0, a.err);
     }
-  } else if (W8 && warp >= kConvWarp) {
+  } else if (warp >= kConvWarp) {
     // ===================== 8-bit codes to f16 in MMA form =====================
     if constexpr (W8) {
+      regs_down<S::REGS>();
+      constexpr int CPR = D / 16;                               // 16-code chunks of a row
+      constexpr int PER = 2 * kTok * CPR / kConvThreads;        // chunks of a thread, half K half V
       const int i0 = threadIdx.x - kConvWarp * 32;
+      // a thread's chunks are PER / 2 rows of K and the same of V, ROWS rows apart. Eight threads
+      // read and write distinct banks: four chunks each of two rows.
+      constexpr int ROWS = kConvThreads / CPR;
+      int row0, c;
+      if constexpr (CPR == 8) {
+        row0 = 2 * (i0 >> 4) + ((i0 >> 2) & 1);
+        c = (i0 & 3) + 4 * (((i0 >> 2) ^ (i0 >> 3)) & 1);
+      } else {
+        row0 = i0 >> 2;
+        c = i0 & 3;
+      }
+      const int ch = 2 * c;  // 16-byte chunks ch and ch + 1 of the row's f16
+      const uint32_t x0 = ((ch & 7) ^ (row0 & 7)) << 4, x1 = (((ch & 7) + 1) ^ (row0 & 7)) << 4;
+      static_assert(ROWS % 8 == 0, "a thread's rows share their swizzle");
+      const uint32_t src0 = ring + S::OFF_RAW + row0 * D + c * 16;
+      const uint32_t k0 = ring + (ch >> 3) * (kTok * 128) + row0 * 128;
+      const uint32_t v0 = ring + S::TILE + (ch >> 3) * 2048;
+      Place<NR> raw;
+      Place<NS> out;
       bool ok = true;
-      const uint32_t count = (uint32_t)share.count;
-      for (uint32_t gt = 0; ok && gt < count; ++gt) {
-        const uint32_t rs = gt % NR, cs = gt % NS;
-        ok = mbar_wait(&raw_full[rs], (gt / NR) & 1u, a.err);
-        if (ok && gt >= NS) ok = mbar_wait(&freed[cs], (gt / NS - 1) & 1u, a.err);
+      const int count = share.count;
+      for (int t = 0; t < count; ++t, raw.advance(1), out.advance(1)) {
+        ok = mbar_wait(&raw_full[raw.st], raw.par, a.err);
+        if (ok && t >= NS) ok = mbar_wait(&freed[out.st], out.par ^ 1u, a.err);
         if (!ok) break;
-        const uint32_t src = ring + S::OFF_RAW + rs * S::RAW_STAGE;
-        const uint32_t dst = ring + cs * S::STAGE;
-        constexpr int CPR = D / 16;  // 16-code chunks of a row
-#pragma unroll 2
-        for (int i = i0; i < 2 * kTok * CPR; i += kConvThreads) {
-          const bool v = i >= kTok * CPR;
-          const int e = v ? i - kTok * CPR : i;
-          // eight threads read and write distinct banks: four chunks each of two rows
-          int row, c;
-          if constexpr (CPR == 8) {
-            row = 2 * (e >> 4) + ((e >> 2) & 1);
-            c = (e & 3) + 4 * (((e >> 2) ^ (e >> 3)) & 1);
-          } else {
-            row = e >> 2;
-            c = e & 3;
-          }
-          const uint4 w = lds128(src + (v ? S::RAW_TILE : 0) + row * D + c * 16);
-          uint4 lo, hi;
-          widen4<KV>(w.x, lo.x, lo.y);
-          widen4<KV>(w.y, lo.z, lo.w);
-          widen4<KV>(w.z, hi.x, hi.y);
-          widen4<KV>(w.w, hi.z, hi.w);
-          const int ch = 2 * c, x = row & 7;  // 16-byte chunks ch and ch + 1 of the row's f16
-          const uint32_t at =
-              v ? dst + S::TILE + (row >> 4) * PAGE_MMA + (ch >> 3) * 2048 + (row & 15) * 128
-                : dst + (ch >> 3) * (kTok * 128) + row * 128;
-          sts128(at + (((ch & 7) ^ x) << 4), lo);
-          sts128(at + ((((ch & 7) + 1) ^ x) << 4), hi);
+        const uint32_t src = src0 + raw.st * S::RAW_STAGE, dst = out.st * S::STAGE;
+        uint4 w[PER];
+#pragma unroll
+        for (int i = 0; i < PER / 2; ++i) {
+          w[i] = lds128(src + i * ROWS * D);
+          w[PER / 2 + i] = lds128(src + S::RAW_TILE + i * ROWS * D);
         }
-        if (i0 == 0) page_mask[cs] = raw_mask[rs];
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+          uint4 lo, hi;
+          widen4<KV>(w[i].x, lo.x, lo.y);
+          widen4<KV>(w[i].y, lo.z, lo.w);
+          widen4<KV>(w[i].z, hi.x, hi.y);
+          widen4<KV>(w[i].w, hi.z, hi.w);
+          const int r = row0 + (i % (PER / 2)) * ROWS;
+          const uint32_t at = dst + (i < PER / 2
+                                         ? k0 + i * ROWS * 128
+                                         : v0 + (r >> 4) * PAGE_MMA + (r & 15) * 128);
+          sts128(at + x0, lo);
+          sts128(at + x1, hi);
+        }
+        if (i0 == 0) page_mask[out.st] = raw_mask[raw.st];
         fence_proxy_async_smem();
-        mbar_arrive(&full[cs]);
-        mbar_arrive(&raw_freed[rs]);
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&full[out.st]);
+          mbar_arrive(&raw_freed[raw.st]);
+        }
       }
     }
-  } else if (warp < kMmaWarp) {
+  } else {
     // ===================== softmax =====================
+    regs_up<S::SOFT_REGS>();
     const int wg = warp >> 2;             // group
     const int r = threadIdx.x & 127;      // row of the group
     const uint32_t lane_t = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     bool ok = true;
-    uint32_t ph = 0, unit = 0, gt = 0;
+    uint32_t ph = 0, unit = 0;
+    Place<NS> base;  // the run's first tile
     for (; walk.next(a, run); ++unit) {
-      const Steps st(run);
+      const bool wide = run.rows > kGroupThreads;
+      const int n = wide ? 2 * run.n : run.n;  // steps; this group's: wg, wg + 2, ...
       const int b = run.b, j = run.j;
-      const int R = run.row0 + (st.wide ? wg * kGroupThreads : 0) + r;
+      const int R = run.row0 + (wide ? wg * kGroupThreads : 0) + r;
       const bool live = R < run.row0 + run.rows;
       const int t = live ? R / a.group : 0, head = j * a.group + (live ? R % a.group : 0);
       uint32_t* const bad = bad_nodes + 8 * (unit & 1);
@@ -402,8 +456,8 @@ __global__ void __launch_bounds__(TcShape<KV, D>::THREADS, 1) tree_tc_kernel(
           // (at least the smallest normal number: an unseen score of -inf must stay one)
           sc = fmaxf(sc * __int_as_float((127 - e) << 23), 0x1p-126f);
         }
-        if (ok && (st.wide || wg == 0)) {
-          const uint32_t q_col = kColQ + (st.wide ? 64 * wg : 0);
+        if (ok && (wide || wg == 0)) {
+          const uint32_t q_col = kColQ + (wide ? 64 * wg : 0);
 #pragma unroll
           for (int h = 0; h < D / 64; ++h) {
             uint32_t w[32];
@@ -420,25 +474,30 @@ __global__ void __launch_bounds__(TcShape<KV, D>::THREADS, 1) tree_tc_kernel(
           tmem_wait_st();
         }
         tc_fence_before();
-        mbar_arrive(q_ready);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(q_ready);
       }
       float m_used = -INFINITY, l = 0.f;
-      for (int u = wg; ok && u < st.n; u += 2) {
-        const uint32_t tl = gt + st.tile(u), stage = tl % NS;
-        const int buf = st.buf(u);
-        ok = mbar_wait(&full[stage], (tl / NS) & 1u, a.err) &&
-             mbar_wait(&s_done[buf], st.parity(ph, u), a.err);
+      Place<NS> at = base;
+      if (!wide) at.advance(wg);
+      Buf bf{wg, 0};
+      int prev_buf = 0;         // this group's last step
+      uint32_t prev_par = 0;
+      int p0 = (run.tile0 + (wide ? 0 : wg)) * kTok;
+      const int seen_by_all = min(run.req.base, run.req.read) - kTok;
+      for (int u = wg; ok && u < n; u += 2) {
+        const uint32_t par = bf.parity(ph);
+        ok = mbar_wait(&full[at.st], at.par, a.err) && mbar_wait(&s_done[bf.i], par, a.err);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
-        const int mask = page_mask[stage];
-        const int p0 = (run.tile0 + st.tile(u)) * kTok;
+        const int mask = page_mask[at.st];
         tc_fence_after();
         uint32_t sr[64];
-        const uint32_t scol = s_col(buf);
+        const uint32_t scol = s_col(bf.i);
         tmem_ld32(lane_t + scol, *reinterpret_cast<uint32_t(*)[32]>(&sr[0]));
         tmem_ld32(lane_t + scol + 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[32]));
         tmem_wait_ld();
-        const bool masked = mask != (1 << kPages) - 1 || p0 + kTok > min(run.req.base, run.req.read);
+        const bool masked = mask != (1 << kPages) - 1 || p0 > seen_by_all;
         if (masked) {
           uint64_t seen = live ? tree_seen(a, run.req, b, t, p0) : 0ull;
 #pragma unroll
@@ -447,10 +506,10 @@ __global__ void __launch_bounds__(TcShape<KV, D>::THREADS, 1) tree_tc_kernel(
 #pragma unroll
           for (int k = 0; k < 64; ++k)
             if (!((seen >> k) & 1)) sr[k] = __float_as_uint(-INFINITY);
-          if (!st.wide || wg == 0) {  // mend V: two threads to a row
+          if (!wide || wg == 0) {  // mend V: two threads to a row
             const int vr = r >> 1, pos = p0 + vr;
             constexpr int CH = D / 16;  // 16-byte chunks of half a row
-            const uint32_t vrow = ring + stage * S::STAGE + S::TILE + (vr >> 4) * PAGE_MMA +
+            const uint32_t vrow = ring + at.st * S::STAGE + S::TILE + (vr >> 4) * PAGE_MMA +
                                   (vr & 15) * 128 + (D == 128 ? (r & 1) * 2048 : 0);
             const int c0 = D == 128 ? 0 : (r & 1) * CH;
             if (pos >= run.req.read || !((mask >> (vr >> 4)) & 1)) {
@@ -461,8 +520,8 @@ __global__ void __launch_bounds__(TcShape<KV, D>::THREADS, 1) tree_tc_kernel(
               bool hot = false;
 #pragma unroll
               for (int c = 0; c < CH; ++c) {
-                const uint32_t at = vrow + (((c0 + c) ^ (vr & 7)) << 4);
-                uint4 x = lds128(at);
+                const uint32_t xa = vrow + (((c0 + c) ^ (vr & 7)) << 4);
+                uint4 x = lds128(xa);
                 uint32_t* w = &x.x;
                 bool here = false;
 #pragma unroll
@@ -476,7 +535,7 @@ __global__ void __launch_bounds__(TcShape<KV, D>::THREADS, 1) tree_tc_kernel(
                     here = true;
                   }
                 }
-                if (here) sts128(at, x);
+                if (here) sts128(xa, x);
                 hot |= here;
               }
               if (hot) {
@@ -499,7 +558,7 @@ __global__ void __launch_bounds__(TcShape<KV, D>::THREADS, 1) tree_tc_kernel(
         } else {
           const bool need = mx > m_used + kLazyLog2;
           if (__any_sync(0xffffffffu, need)) {  // rescale this warp's rows of O (in TMEM)
-            ok = mbar_wait(&pv_done[st.buf(u - 2)], st.parity(ph, u - 2), a.err);
+            ok = mbar_wait(&pv_done[prev_buf], prev_par, a.err);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             tc_fence_after();
@@ -538,14 +597,19 @@ __global__ void __launch_bounds__(TcShape<KV, D>::THREADS, 1) tree_tc_kernel(
              ((sum8[4] + sum8[5]) + (sum8[6] + sum8[7]));
         tmem_wait_st();
         tc_fence_before();
-        mbar_arrive(&p_ready[buf]);
+        __syncwarp();  // (one arrival per warp: arrivals on one barrier go one by one)
+        if (lane == 0) mbar_arrive(&p_ready[bf.i]);
+        prev_buf = bf.i;
+        prev_par = par;
+        bf.advance(wide, 2);
+        at.advance(wide ? 1 : 2);
+        p0 += wide ? kTok : 2 * kTok;
       }
       // ---- the unit's rows ----
-      const int last = wg < st.n ? ((st.n - 1 - wg) & ~1) + wg : -1;  // this group's last step
-      if (ok && last >= 0) ok = mbar_wait(&pv_done[st.buf(last)], st.parity(ph, last), a.err);
+      if (ok && wg < n) ok = mbar_wait(&pv_done[prev_buf], prev_par, a.err);
       ok = __all_sync(0xffffffffu, ok);
       tc_fence_after();
-      if (!st.wide) ml[wg * kGroupThreads + r] = make_float2(m_used, l);
+      if (!wide) ml[wg * kGroupThreads + r] = make_float2(m_used, l);
       tc_fence_before();
       // both groups are here whatever became of their waits
       asm volatile("bar.sync 1, 256;" ::: "memory");
@@ -555,8 +619,8 @@ __global__ void __launch_bounds__(TcShape<KV, D>::THREADS, 1) tree_tc_kernel(
         // wide: the group's own rows, all dims; else group wg takes dims wg D/2 .. of every row and
         // merges the two groups' O
         float M = m_used, L = l, w0 = 1.f, w1 = 0.f;
-        const bool two = !st.wide && st.n > 1;
-        if (!st.wide) {
+        const bool two = !wide && n > 1;
+        if (!wide) {
           const float2 x = ml[r], y = ml[kGroupThreads + r];
           M = fmaxf(x.x, y.x);
           const float Mu = M == -INFINITY ? 0.f : M;
@@ -572,10 +636,10 @@ __global__ void __launch_bounds__(TcShape<KV, D>::THREADS, 1) tree_tc_kernel(
         uint32_t any_bad = 0;
 #pragma unroll
         for (int k = 0; k < 8; ++k) any_bad |= bad[k];
-        const int c_lo = st.wide ? 0 : wg * (D / 2), c_hi = st.wide ? D : c_lo + D / 2;
+        const int c_lo = wide ? 0 : wg * (D / 2), c_hi = wide ? D : c_lo + D / 2;
         for (int c = c_lo; c < c_hi; c += 32) {
           uint32_t o[32];
-          tmem_ld32(lane_t + kColO + (st.wide ? 128 * wg : 0) + c, o);
+          tmem_ld32(lane_t + kColO + (wide ? 128 * wg : 0) + c, o);
           if (two) {
             uint32_t o1[32];
             tmem_ld32(lane_t + kColO + 128 + c, o1);
@@ -585,7 +649,7 @@ __global__ void __launch_bounds__(TcShape<KV, D>::THREADS, 1) tree_tc_kernel(
               o[k] = __float_as_uint(w0 * __uint_as_float(o[k]) + w1 * __uint_as_float(o1[k]));
           } else {
             tmem_wait_ld();
-            if (!st.wide)
+            if (!wide)
 #pragma unroll
               for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(w0 * __uint_as_float(o[k]));
           }
@@ -634,8 +698,8 @@ __global__ void __launch_bounds__(TcShape<KV, D>::THREADS, 1) tree_tc_kernel(
           }
         }
       }
-      ph = st.after(ph);
-      gt += run.n;
+      ph = after_steps(ph, wide, n);
+      base.skip(run.n);
     }
   }
 
@@ -662,6 +726,13 @@ cudaError_t launch_t(const TreeArgs& a, const CUtensorMap& tk, const CUtensorMap
     e = cudaFuncSetAttribute(tree_tc_kernel<KV, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              S::SMEM);
     if (e != cudaSuccess) return e;
+    // the softmax warps may take no more registers than the launch brings and the others give up
+    cudaFuncAttributes fa{};
+    e = cudaFuncGetAttributes(&fa, tree_tc_kernel<KV, D>);
+    if (e != cudaSuccess) return e;
+    if (kSoftThreads * S::SOFT_REGS + (S::THREADS - kSoftThreads) * S::REGS >
+        S::THREADS * fa.numRegs)
+      return cudaErrorLaunchOutOfResources;
     if (dev < 64) attr_done.fetch_or(1ull << dev);
   }
   tree_tc_kernel<KV, D><<<a.ctas, S::THREADS, S::SMEM, s>>>(a, tk, tv);

@@ -56,21 +56,21 @@ __device__ __forceinline__ TreeSize tree_size(const TreeArgs& a, const TreeReq& 
                   (r.nodes * a.group + a.unit_rows - 1) / a.unit_rows};
 }
 
-__device__ __forceinline__ long long tree_tiles(const TreeArgs& a, const TreeSize& z) {
-  return (long long)z.tiles * z.units * a.h_kv;
+// (The host refuses a call whose table could hold 2^31 tiles: the stream's positions are ints.)
+__device__ __forceinline__ int tree_tiles(const TreeArgs& a, const TreeSize& z) {
+  return z.tiles * z.units * a.h_kv;
 }
 
 // Sums over a block: `below` of the values of threads before this one, `total` of all. Shared
-// scratch of 33 words; every thread of the block calls it.
+// scratch of 32 words; every thread of the block calls it.
 template <int THREADS>
-__device__ __forceinline__ void block_scan(long long v, long long* scratch, long long& below,
-                                           long long& total) {
+__device__ __forceinline__ void block_scan(int v, int* scratch, int& below, int& total) {
   constexpr int W = (THREADS + 31) / 32;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  long long x = v;
+  int x = v;
 #pragma unroll
   for (int o = 1; o < 32; o *= 2) {
-    const long long y = __shfl_up_sync(0xffffffffu, x, o);
+    const int y = __shfl_up_sync(0xffffffffu, x, o);
     if (lane >= o) x += y;
   }
   if (lane == 31) scratch[warp] = x;
@@ -82,30 +82,25 @@ __device__ __forceinline__ void block_scan(long long v, long long* scratch, long
     if (w < warp) below += scratch[w];
     total += scratch[w];
   }
-  __syncthreads();
 }
 
 // Where a CTA's share begins: in request b at tile `off` of that request's part of the stream,
 // `count` tiles long (0: nothing to do).
 struct TreeShare {
-  int b;
-  long long off;
-  long long count;
+  int b, off, count;
 };
 
-__device__ __forceinline__ long long tree_share_size(const TreeArgs& a, long long total) {
-  const long long s = (total + a.ctas - 1) / a.ctas;
-  return s < a.min_tiles ? a.min_tiles : s;
+__device__ __forceinline__ int tree_share_size(const TreeArgs& a, int total) {
+  return max(a.min_tiles, (int)(((unsigned)total + a.ctas - 1) / (unsigned)a.ctas));
 }
 
 // Every thread of a block of THREADS takes part; `out` and `scratch` are shared memory. Argument
-// errors are reported by block 0.
+// errors are reported by block 0. Ends with a block barrier.
 template <int THREADS>
-__device__ __forceinline__ void tree_share(const TreeArgs& a, long long* scratch, TreeShare* out) {
+__device__ __forceinline__ void tree_share(const TreeArgs& a, int* scratch, TreeShare* out) {
   const int per = (a.batch + THREADS - 1) / THREADS;
   const int b0 = min(a.batch, (int)threadIdx.x * per), b1 = min(a.batch, b0 + per);
-  long long mine = 0;
-  int err = 0;
+  int mine = 0, err = 0;
   for (int b = b0; b < b1; ++b) {
     const TreeReq r = tree_request(a, b);
     err |= r.err;
@@ -113,22 +108,20 @@ __device__ __forceinline__ void tree_share(const TreeArgs& a, long long* scratch
   }
   if (err && blockIdx.x == 0) atomicOr(a.err, err);
   if (threadIdx.x == 0) out->count = 0;
-  long long below, total;
+  int below, total;
   block_scan<THREADS>(mine, scratch, below, total);
-  const long long share = tree_share_size(a, total);
+  const int share = tree_share_size(a, total);
   const long long start = (long long)blockIdx.x * share;
   if (start >= below && start < below + mine) {
-    long long at = below;
-    for (int b = b0; b < b1; ++b) {
-      const long long t = tree_tiles(a, tree_size(a, tree_request(a, b)));
-      if (start < at + t) {
-        out->b = b;
-        out->off = start - at;
-        out->count = min(share, total - start);
-        break;
-      }
+    int at = below, b = b0;
+    for (; b < b1 - 1; ++b) {  // (one request per thread up to THREADS requests)
+      const int t = tree_tiles(a, tree_size(a, tree_request(a, b)));
+      if (start < at + t) break;
       at += t;
     }
+    out->b = b;
+    out->off = (int)start - at;
+    out->count = min(share, total - (int)start);
   }
   __syncthreads();
 }
@@ -136,39 +129,37 @@ __device__ __forceinline__ void tree_share(const TreeArgs& a, long long* scratch
 // A run of tiles of one pass.
 struct TreeRun {
   TreeReq req;
-  int b, j;           // request, KV head
-  int row0, rows;     // first row of the unit and its rows: row r is node r / group, head r % group
-  int tile0, n;       // tiles tile0 .. tile0 + n - 1
-  bool whole;         // the pass lies in this share
-  int slot;           // partial slot otherwise
+  int b, j;        // request, KV head
+  int row0, rows;  // first row of the unit and its rows: row r is node r / group, head r % group
+  int tile0, n;    // tiles tile0 .. tile0 + n - 1
+  bool whole;      // the pass lies in this share
+  int slot;        // partial slot otherwise
 };
 
 // Walks a share run by run. Uniform over its callers (it reads the lengths itself).
 struct TreeWalk {
-  int b;
-  long long off, left;
+  int b, off, left;
   __device__ __forceinline__ bool next(const TreeArgs& a, TreeRun& r) {
     while (left > 0 && b < a.batch) {
       const TreeReq q = tree_request(a, b);
       const TreeSize z = tree_size(a, q);
-      const long long t = tree_tiles(a, z);
+      const int t = tree_tiles(a, z);
       if (off >= t) {
         off -= t;
         ++b;
         continue;
       }
-      const int pass = (int)(off / z.tiles);
-      const int tile0 = (int)(off % z.tiles);
-      const int unit = pass % z.units;
+      const int pass = (int)((unsigned)off / (unsigned)z.tiles);
+      const int unit = (int)((unsigned)pass % (unsigned)z.units);
       r.req = q;
       r.b = b;
-      r.j = pass / z.units;
+      r.j = (int)((unsigned)pass / (unsigned)z.units);
       r.row0 = unit * a.unit_rows;
       r.rows = min(a.unit_rows, q.nodes * a.group - r.row0);
-      r.tile0 = tile0;
-      r.n = (int)min((long long)(z.tiles - tile0), left);
-      r.whole = tile0 == 0 && r.n == z.tiles;
-      r.slot = tile0 > 0 ? 0 : 1;
+      r.tile0 = off - pass * z.tiles;
+      r.n = min(z.tiles - r.tile0, left);
+      r.whole = r.n == z.tiles;
+      r.slot = r.tile0 > 0 ? 0 : 1;
       off += r.n;
       left -= r.n;
       return true;
