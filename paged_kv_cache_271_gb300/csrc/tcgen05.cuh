@@ -23,6 +23,19 @@ __device__ __forceinline__ uint64_t tc_desc(uint32_t saddr, uint32_t lbo, uint32
          ((uint64_t)((sbo >> 4) & 0x3FFFu) << 32) | (1ull << 46) | (2ull << 61);
 }
 
+// True in one lane of a converged warp. The tensor-core and TMA instructions take their operands
+// from uniform registers: code that the whole warp runs with warp-uniform values, in which one
+// elected lane issues, keeps them there; under a lane-index test every operand is moved across
+// before every instruction (about 50 cycles per MMA issued).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n.reg .pred q;\nelect.sync _|q, 0xffffffff;\nselp.u32 %0, 1, 0, q;\n}" : "=r"(p));
+  return p != 0;
+}
+
+// v, the same in every lane, as a warp-uniform value.
+__device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xffffffffu, v, 0); }
+
 // D (+)= A B with the A operand in tensor memory (its 128 lanes are A's rows; its 32-bit columns
 // hold bf16 pairs along K, the lower index in the low half) and B described in shared memory.
 __device__ __forceinline__ void tc_mma_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t b,

@@ -165,7 +165,7 @@ __global__ void __launch_bounds__(TcShape<KV, D>::THREADS, 1) tree_tc_kernel(
   constexpr int NS = S::NS, NR = S::NR;
   constexpr int PAGE_MMA = kPageSize * D * 2;  // V bytes of a page in MMA form
   constexpr int PAGE_RAW = kPageSize * D;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
 
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
@@ -224,7 +224,7 @@ __global__ void __launch_bounds__(TcShape<KV, D>::THREADS, 1) tree_tc_kernel(
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *s_taddr;
+  const uint32_t tmem = (uint32_t)uniform((int)*s_taddr);
   TreeWalk walk{share.b, share.off, share.count};
   TreeRun run;
 
@@ -243,46 +243,53 @@ __global__ void __launch_bounds__(TcShape<KV, D>::THREADS, 1) tree_tc_kernel(
       int issued = 0;
       bool ok = true;
       while (ok && walk.next(a, run)) {
-        const int pages = (run.req.read + kPageSize - 1) / kPageSize;
+        const int pages = uniform((run.req.read + kPageSize - 1) / kPageSize);
+        const int n = uniform(run.n), j = uniform(run.j);
         const int32_t* table = a.block_tables + (size_t)run.b * a.max_pages;
-        int lp = run.tile0 * kPages + lane;  // lane p: page p of the tile (p < 4)
-        int ids = -1;                        // lane L: the id of page 32 m + L of the run
-        for (int i = 0; i < run.n; ++i, lp += kPages) {
-          if ((i & 7) == 0) ids = lp < pages ? table[lp] : -1;
-          const int id = __shfl_sync(0xffffffffu, ids, (kPages * i + lane) & 31);
-          const bool there = lane < kPages && lp < pages;
-          const bool good = there && id >= 0 && id < a.num_pages;
-          if (there && !good) atomicOr(a.err, PKV_DEVERR_BAD_PAGE);
-          const uint32_t mask = __ballot_sync(0xffffffffu, good);
+        int lp = uniform(run.tile0 * kPages);  // first page of the tile
+        int ids = -1;                          // lane L: the id of page 32 m + L of the run
+        for (int i = 0; i < n; ++i, lp += kPages) {
+          if ((i & 7) == 0) ids = lp + lane < pages ? table[lp + lane] : -1;
+          int id[kPages];
+          uint32_t mask = 0;
+#pragma unroll
+          for (int p = 0; p < kPages; ++p) {
+            id[p] = __shfl_sync(0xffffffffu, ids, (kPages * i + p) & 31);
+            if (lp + p < pages && id[p] >= 0 && id[p] < a.num_pages) mask |= 1u << p;
+          }
           if (issued >= N) {
             ok = mbar_wait(&leave[at.st], at.par ^ 1u, a.err);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
           }
-          if (lane == 0) {
+          if (mask != (1u << min(kPages, pages - lp)) - 1 && lane == 0)
+            atomicOr(a.err, PKV_DEVERR_BAD_PAGE);
+          __syncwarp();
+          if (elect_one()) {
             masks[at.st] = (int)mask;
             if constexpr (W8) fence_proxy_async_smem();
             mbar_arrive_expect_tx(&arrive[at.st], __popc(mask) * 2 * (W8 ? PAGE_RAW : PAGE_MMA));
-          }
-          __syncwarp();
-          if (good) {  // lane p copies page p
-            if constexpr (W8) {
-              const int64_t src = ((int64_t)id * a.h_kv + run.j) * PAGE_RAW;
-              uint8_t* dst = smem + S::OFF_RAW + at.st * S::RAW_STAGE + lane * PAGE_RAW;
-              bulk_g2s(dst, static_cast<const uint8_t*>(a.k_cache) + src, PAGE_RAW,
-                       &arrive[at.st], pol);
-              bulk_g2s(dst + S::RAW_TILE, static_cast<const uint8_t*>(a.v_cache) + src, PAGE_RAW,
-                       &arrive[at.st], pol);
-            } else {
-              const int row = (id * a.h_kv + run.j) * kPageSize;
-              const uint32_t dst = ring + at.st * S::STAGE;
-              // K: 64-dim blocks of all 64 rows (one N = 64 operand); V: a block per page (K = 16)
 #pragma unroll
-              for (int bx = 0; bx < D / 64; ++bx)
-                tma_load_2d(dst + bx * (kTok * 128) + lane * 2048, &tm_k, bx * 64, row,
-                            &arrive[at.st], pol);
-              tma_tile<D / 64, 64>(dst + S::TILE + lane * PAGE_MMA, &tm_v, a.tma_rank, row,
-                                   &arrive[at.st], pol);
+            for (int p = 0; p < kPages; ++p) {
+              if (!((mask >> p) & 1)) continue;
+              if constexpr (W8) {
+                const int64_t src = ((int64_t)id[p] * a.h_kv + j) * PAGE_RAW;
+                uint8_t* dst = smem + S::OFF_RAW + at.st * S::RAW_STAGE + p * PAGE_RAW;
+                bulk_g2s(dst, static_cast<const uint8_t*>(a.k_cache) + src, PAGE_RAW,
+                         &arrive[at.st], pol);
+                bulk_g2s(dst + S::RAW_TILE, static_cast<const uint8_t*>(a.v_cache) + src, PAGE_RAW,
+                         &arrive[at.st], pol);
+              } else {
+                const int row = (id[p] * a.h_kv + j) * kPageSize;
+                const uint32_t dst = ring + at.st * S::STAGE;
+                // K: 64-dim blocks of all 64 rows (one N = 64 operand); V: a block per page (K = 16)
+#pragma unroll
+                for (int bx = 0; bx < D / 64; ++bx)
+                  tma_load_2d(dst + bx * (kTok * 128) + p * 2048, &tm_k, bx * 64, row,
+                              &arrive[at.st], pol);
+                tma_tile<D / 64, 64>(dst + S::TILE + p * PAGE_MMA, &tm_v, a.tma_rank, row,
+                                     &arrive[at.st], pol);
+              }
             }
           }
           __syncwarp();
@@ -296,29 +303,35 @@ __global__ void __launch_bounds__(TcShape<KV, D>::THREADS, 1) tree_tc_kernel(
           mbar_wait(&arrive[back % N], (uint32_t)(back / N) & 1u, a.err);
         }
       }
-    } else if (warp == kMmaWarp && lane == 0) {
-      // ===================== MMAs (one lane) =====================
+    } else if (warp == kMmaWarp) {
+      // ===================== MMAs (one elected lane issues) =====================
       const uint64_t k_desc = tc_desc(ring, 16, 1024), v_desc = tc_desc(ring + S::TILE, 2048, 1024);
       bool ok = true;
       uint32_t ph = 0, unit = 0;
       Place<NS> ks, vs;  // tiles of the next S and of the next P V
-      while (ok && walk.next(a, run)) {
-        const bool wide = run.rows > kGroupThreads;
-        const int n = wide ? 2 * run.n : run.n;
-        ok = mbar_wait(q_ready, unit & 1, a.err);
-        ++unit;
+      auto wait = [&](uint64_t* bar, uint32_t par) {
+        const bool got = __all_sync(0xffffffffu, mbar_wait(bar, par, a.err));
         tc_fence_after();
+        return got;
+      };
+      while (ok && walk.next(a, run)) {
+        const bool wide = uniform(run.rows) > kGroupThreads;
+        const int n = uniform(wide ? 2 * run.n : run.n);
+        ok = wait(q_ready, unit & 1);
+        ++unit;
         bool odd = false;  // the next S's step
         auto s_mma = [&](int buf) {
-          if (!mbar_wait(&full[ks.st], ks.par, a.err)) return false;
-          tc_fence_after();
+          if (!wait(&full[ks.st], ks.par)) return false;
           const uint64_t kd = k_desc + (uint32_t)(ks.st * (S::STAGE >> 4));
           const uint32_t q = tmem + kColQ + (wide && odd ? 64 : 0), d = tmem + s_col(buf);
+          if (elect_one()) {
 #pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk)
-            tc_mma_ta(d, q + 8 * kk, kd + (((kk >> 2) * (kTok * 128) + (kk & 3) * 32) >> 4),
-                      S::IDESC_S, kk > 0 ? 1u : 0u);
-          tc_commit(&s_done[buf]);
+            for (int kk = 0; kk < D / 16; ++kk)
+              tc_mma_ta(d, q + 8 * kk, kd + (((kk >> 2) * (kTok * 128) + (kk & 3) * 32) >> 4),
+                        S::IDESC_S, kk > 0 ? 1u : 0u);
+            tc_commit(&s_done[buf]);
+          }
+          __syncwarp();
           if (!wide || odd) ks.advance(1);
           odd = !odd;
           return true;
@@ -328,29 +341,31 @@ __global__ void __launch_bounds__(TcShape<KV, D>::THREADS, 1) tree_tc_kernel(
         Buf b{0, 0};
         for (int u = 0; ok && u < n; ++u, b.advance(wide, 1)) {
           const uint32_t par = b.parity(ph);
-          ok = mbar_wait(&p_ready[b.i], par, a.err);
+          ok = wait(&p_ready[b.i], par);
           if (!ok) break;
-          tc_fence_after();
           const uint64_t vd = v_desc + (uint32_t)(vs.st * (S::STAGE >> 4));
           const uint32_t o = tmem + kColO + ((u & 1) << 7), pc = tmem + s_col(b.i);
+          const bool tile_done = !wide || (u & 1);
+          if (elect_one()) {
 #pragma unroll
-          for (int kk = 0; kk < kPages; ++kk)
-            tc_mma_ta(o, pc + 8 * kk, vd + ((kk * PAGE_MMA) >> 4), S::IDESC_PV,
-                      u < 2 && kk == 0 ? 0u : 1u);
-          tc_commit(&pv_done[b.i]);
-          if (!wide || (u & 1)) {
-            tc_commit(&freed[vs.st]);
-            vs.advance(1);
+            for (int kk = 0; kk < kPages; ++kk)
+              tc_mma_ta(o, pc + 8 * kk, vd + ((kk * PAGE_MMA) >> 4), S::IDESC_PV,
+                        u < 2 && kk == 0 ? 0u : 1u);
+            tc_commit(&pv_done[b.i]);
+            if (tile_done) tc_commit(&freed[vs.st]);
           }
+          __syncwarp();
+          if (tile_done) vs.advance(1);
           if (u + bufs < n) {  // its S overwrites the buffer that this P lives in
-            ok = mbar_wait(&pv_done[b.i], par, a.err);
+            ok = wait(&pv_done[b.i], par);
             if (ok) ok = s_mma(b.i);
           }
         }
         ph = after_steps(ph, wide, n);
       }
-      tc_commit(mma_idle);  // before leaving, every MMA issued is complete
-      mbar_wait(mma_idle, 0, a.err);
+      if (elect_one()) tc_commit(mma_idle);  // before leaving, every MMA issued is complete
+      __syncwarp();
+      wait(mma_idle, 0);
     }
   } else if (warp >= kConvWarp) {
     // ===================== 8-bit codes to f16 in MMA form =====================
