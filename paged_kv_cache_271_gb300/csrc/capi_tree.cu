@@ -13,17 +13,17 @@ using namespace pkv;
 
 namespace {
 
-// Query rows of a unit, tokens of a tile, least tiles of a CTA and the CTAs of one wave of the
-// kernel that a call uses.
+// Query rows of a unit, tokens of a tile, least tiles of a CTA, cost of a pass in tiles and the
+// CTAs of one wave of the kernel that a call uses.
 struct TreeSplit {
-  int rows, tokens, min_tiles, wave;
+  int rows, tokens, min_tiles, pass_cost, wave;
   bool tc;
 };
 
 // bf16 queries run on the tensor cores, fp32 queries (whose weights keep 24 bits) on CUDA cores.
 TreeSplit tree_split(int dtype_q) {
-  if (dtype_q == PKV_BF16) return TreeSplit{kTreeTcRows, kTreeTcTokens, 2, kTreeTcWave, true};
-  return TreeSplit{kTreeSimtRows, kTreeSimtTokens, 4, kTreeSimtWave, false};
+  if (dtype_q == PKV_BF16) return TreeSplit{kTreeTcRows, kTreeTcTokens, 2, 4, kTreeTcWave, true};
+  return TreeSplit{kTreeSimtRows, kTreeSimtTokens, 4, 1, kTreeSimtWave, false};
 }
 
 size_t tree_acc_bytes(const TreeSplit& t, int ctas, int head_dim) {
@@ -46,7 +46,7 @@ long long tree_most_tiles(const TreeSplit& t, int batch, int nodes, int h_q, int
                           int max_pages) {
   const long long units = ((long long)nodes * (h_q / h_kv) + t.rows - 1) / t.rows;
   const long long tiles = ((long long)max_pages * 16 + t.tokens - 1) / t.tokens;
-  return (long long)batch * h_kv * units * tiles;
+  return (long long)batch * h_kv * units * (tiles + t.pass_cost);
 }
 
 // CTAs of a call: one wave, or fewer when the table cannot hold that many shares.
@@ -200,8 +200,8 @@ int pkv_tree_decode_attention(const void* q, int32_t dtype_q, int32_t batch, int
       (long long)desc->num_pages * h_kv * desc->page_size >= (1ll << 31))
     return set_error(PKV_ESHAPE, "%s: a bf16 pool must have fewer than 2^31 rows", who);
   const TreeSplit t = tree_split(dtype_q);
-  if (tree_most_tiles(t, batch, tree_width, num_q_heads, h_kv, max_pages_per_seq) >= (1ll << 31))
-    return set_error(PKV_ESHAPE, "%s: the table can hold 2^31 tiles of work or more", who);
+  if (tree_most_tiles(t, batch, tree_width, num_q_heads, h_kv, max_pages_per_seq) >= (1ll << 30))
+    return set_error(PKV_ESHAPE, "%s: the table can hold 2^30 tiles of work or more", who);
   TreeArgs a{};
   a.ctas = tree_ctas(t, batch, tree_width, num_q_heads, h_kv, max_pages_per_seq);
   const size_t acc = tree_acc_bytes(t, a.ctas, D), need = acc + tree_ml_bytes(t, a.ctas);
@@ -234,6 +234,7 @@ int pkv_tree_decode_attention(const void* q, int32_t dtype_q, int32_t batch, int
   a.unit_rows = t.rows;
   a.tile_tokens = t.tokens;
   a.min_tiles = t.min_tiles;
+  a.pass_cost = t.pass_cost;
   st = error_word(&a.err);
   if (st != PKV_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);

@@ -152,6 +152,7 @@ struct TreeArgs {
   int unit_rows;    // query rows of a unit
   int tile_tokens;  // cached tokens of a tile
   int min_tiles;    // least tiles a CTA takes
+  int pass_cost;    // what beginning a pass costs a CTA, in tiles
 };
 
 struct CommitArgs {

@@ -65,11 +65,11 @@ __global__ void __launch_bounds__(kThreads) tree_simt_kernel(const TreeArgs a) {
   float* ks = qs + kRows * LD;
   float* vs = ks + kTok * LD;
   float* ps = vs + kTok * LD;
-  __shared__ int scratch[32];
+  __shared__ int scratch[64];
   __shared__ TreeShare share;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   tree_share<kThreads>(a, scratch, &share);
-  TreeWalk walk{share.b, share.off, share.count};
+  TreeWalk walk(share);
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;  // tokens / dims, group of 4 rows
   TreeRun run;
   while (walk.next(a, run)) {
@@ -249,7 +249,7 @@ __global__ void __launch_bounds__(kCombineThreads) tree_combine_kernel(const Tre
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int j = blockIdx.y, b = blockIdx.z;
   const int row_block = blockIdx.x * kCombineRows;
-  __shared__ int scratch[2][32];
+  __shared__ int scratch[4][32];
   const TreeReq req = tree_request(a, b);
   const TreeSize z = tree_size(a, req);
   const int rows = req.nodes * a.group;
@@ -259,19 +259,28 @@ __global__ void __launch_bounds__(kCombineThreads) tree_combine_kernel(const Tre
     if (first_block) asm volatile("griddepcontrol.wait;" ::: "memory");
     return;
   }
-  int before = 0, all = 0;
+  int tiles = 0, passes = 0, tiles_before = 0, passes_before = 0;
   for (int i = threadIdx.x; i < a.batch; i += kCombineThreads) {
-    const int t = tree_tiles(a, tree_size(a, tree_request(a, i)));
-    all += t;
-    if (i < b) before += t;
+    const TreeSize y = tree_size(a, tree_request(a, i));
+    const int p = y.units * a.h_kv;
+    tiles += y.tiles * p;
+    passes += p;
+    if (i < b) {
+      tiles_before += y.tiles * p;
+      passes_before += p;
+    }
   }
-  int below, total, pre;
-  block_scan<kCombineThreads>(all, scratch[0], below, total);
-  block_scan<kCombineThreads>(before, scratch[1], below, pre);
-  const int share = tree_share_size(a, total);
+  int below, tiles_all, passes_all, tiles_pre, passes_pre;
+  block_scan<kCombineThreads>(tiles, scratch[0], below, tiles_all);
+  block_scan<kCombineThreads>(passes, scratch[1], below, passes_all);
+  block_scan<kCombineThreads>(tiles_before, scratch[2], below, tiles_pre);
+  block_scan<kCombineThreads>(passes_before, scratch[3], below, passes_pre);
+  const TreeStream st = tree_stream(a, tiles_all, passes_all);
   const int unit = row_block / a.unit_rows;  // (unit_rows is a multiple of kCombineRows)
-  const int start = pre + (j * z.units + unit) * z.tiles;
-  const int c0 = start / share, c1 = (start + z.tiles - 1) / share;
+  // the pass's first tile in the stream, and the shares that hold its tiles
+  const int start = tiles_pre + st.pass_cost * passes_pre +
+                    (j * z.units + unit) * (z.tiles + st.pass_cost) + st.pass_cost;
+  const int c0 = start / st.share, c1 = (start + z.tiles - 1) / st.share;
   if (c0 == c1) {
     if (first_block) asm volatile("griddepcontrol.wait;" ::: "memory");
     return;

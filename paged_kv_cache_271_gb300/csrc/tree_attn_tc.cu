@@ -78,7 +78,7 @@ struct TcShape {
   static constexpr int OFF_RAW = NS * STAGE;
   static constexpr int OFF_ML = OFF_RAW + NR * RAW_STAGE;   // [2][128] (max, sum)
   static constexpr int OFF_BAR = OFF_ML + 2 * kGroupThreads * 8;
-  static constexpr int BARS = 2 * NS + 2 * NR + 3 * kSBufs + 2;
+  static constexpr int BARS = 2 * NS + 2 * NR + 3 * kSBufs + 3;
   static constexpr int OFF_MISC = OFF_BAR + 8 * BARS;       // masks, bad nodes, TMEM address
   static constexpr uint32_t IDESC_S = tc_idesc(128, kTok, false, W8);
   static constexpr uint32_t IDESC_PV = tc_idesc(128, D, true, W8);
@@ -178,15 +178,16 @@ __global__ void __launch_bounds__(TcShape<KV, D>::THREADS, 1) tree_tc_kernel(
   uint64_t* s_done = raw_freed + NR;                                 // [3] S in its buffer
   uint64_t* p_ready = s_done + kSBufs;                               // [3] P in its buffer
   uint64_t* pv_done = p_ready + kSBufs;                              // [3] that P V complete
-  uint64_t* q_ready = pv_done + kSBufs;  // Q of a unit stored, the last unit's O read
-  uint64_t* mma_idle = q_ready + 1;
+  uint64_t* q_ready = pv_done + kSBufs;                              // Q of a unit stored
+  uint64_t* o_read = q_ready + 1;                                    // O of a unit read
+  uint64_t* mma_idle = o_read + 1;
   int* page_mask = reinterpret_cast<int*>(smem + S::OFF_MISC);       // [NS] good pages of the tile
   int* raw_mask = page_mask + NS;                                    // [NR]
   uint32_t* bad_nodes = reinterpret_cast<uint32_t*>(raw_mask + NR);  // [2][8] V row not finite
   uint32_t* s_taddr = bad_nodes + 16;
   float2* ml = reinterpret_cast<float2*>(smem + S::OFF_ML);          // [2][128]
 
-  __shared__ int scratch[32];
+  __shared__ int scratch[64];
   __shared__ TreeShare share;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (threadIdx.x == kCopyWarp * 32) {
@@ -204,6 +205,7 @@ __global__ void __launch_bounds__(TcShape<KV, D>::THREADS, 1) tree_tc_kernel(
       mbar_init(&pv_done[s], 1);
     }
     mbar_init(q_ready, kSoftThreads / 32);
+    mbar_init(o_read, kSoftThreads / 32);
     mbar_init(mma_idle, 1);
     mbar_fence_init();
     if constexpr (!W8) {
@@ -225,7 +227,7 @@ __global__ void __launch_bounds__(TcShape<KV, D>::THREADS, 1) tree_tc_kernel(
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = (uint32_t)uniform((int)*s_taddr);
-  TreeWalk walk{share.b, share.off, share.count};
+  TreeWalk walk(share);
   TreeRun run;
 
   if (warp >= kMmaWarp && warp < kConvWarp) {
@@ -342,6 +344,7 @@ __global__ void __launch_bounds__(TcShape<KV, D>::THREADS, 1) tree_tc_kernel(
         for (int u = 0; ok && u < n; ++u, b.advance(wide, 1)) {
           const uint32_t par = b.parity(ph);
           ok = wait(&p_ready[b.i], par);
+          if (ok && u == 0 && unit > 1) ok = wait(o_read, unit & 1);  // (of the last unit)
           if (!ok) break;
           const uint64_t vd = v_desc + (uint32_t)(vs.st * (S::STAGE >> 4));
           const uint32_t o = tmem + kColO + ((u & 1) << 7), pc = tmem + s_col(b.i);
@@ -394,8 +397,12 @@ __global__ void __launch_bounds__(TcShape<KV, D>::THREADS, 1) tree_tc_kernel(
       Place<NR> raw;
       Place<NS> out;
       bool ok = true;
-      const int count = share.count;
-      for (int t = 0; t < count; ++t, raw.advance(1), out.advance(1)) {
+      int t = 0, end = 0;  // tiles done, tiles of the runs so far
+      for (;; ++t, raw.advance(1), out.advance(1)) {
+        if (t == end) {
+          if (!walk.next(a, run)) break;
+          end += run.n;
+        }
         ok = mbar_wait(&raw_full[raw.st], raw.par, a.err);
         if (ok && t >= NS) ok = mbar_wait(&freed[out.st], out.par ^ 1u, a.err);
         if (!ok) break;
@@ -438,60 +445,95 @@ __global__ void __launch_bounds__(TcShape<KV, D>::THREADS, 1) tree_tc_kernel(
     bool ok = true;
     uint32_t ph = 0, unit = 0;
     Place<NS> base;  // the run's first tile
-    for (; walk.next(a, run); ++unit) {
+    // The row of this thread in a run (row `row` of its unit, node t, query head `head`) and its
+    // score factor.
+    struct Row {
+      int row, t, head;
+      bool live;
+      float sc;
+    };
+    auto find_row = [&](const TreeRun& run) {
+      Row x;
+      x.row = (run.rows > kGroupThreads ? wg * kGroupThreads : 0) + r;
+      x.live = x.row < run.rows;
+      const unsigned R = x.live ? run.row0 + x.row : 0;
+      x.t = (int)(R / (unsigned)a.group);
+      x.head = run.j * a.group + (int)(R - x.t * (unsigned)a.group);
+      x.sc = 0.f;
+      return x;
+    };
+    auto row_at = [&](const TreeRun& run, const Row& x) {  // its offset in q and out
+      return (((size_t)run.b * a.nodes + x.t) * a.h_q + x.head) * D;
+    };
+    // The row's query into tensor memory, once the S of the last unit are done.
+    auto store_query = [&](const TreeRun& run, Row& x) {
       const bool wide = run.rows > kGroupThreads;
-      const int n = wide ? 2 * run.n : run.n;  // steps; this group's: wg, wg + 2, ...
-      const int b = run.b, j = run.j;
-      const int R = run.row0 + (wide ? wg * kGroupThreads : 0) + r;
-      const bool live = R < run.row0 + run.rows;
-      const int t = live ? R / a.group : 0, head = j * a.group + (live ? R % a.group : 0);
-      uint32_t* const bad = bad_nodes + 8 * (unit & 1);
-      float sc = a.scale_log2 * (W8 ? a.k_scales[j] : 1.f);
-      // ---- the row's query into tensor memory (both groups' reads of the last unit's O are done) ----
-      {
-        const uint4* qrow = reinterpret_cast<const uint4*>(
-            static_cast<const __nv_bfloat16*>(a.q) +
-            (((size_t)b * a.nodes + t) * a.h_q + head) * D);
-        uint4 qv[D / 8];
-#pragma unroll
-        for (int c = 0; c < D / 8; ++c) qv[c] = live ? qrow[c] : make_uint4(0, 0, 0, 0);
-        float up = 1.f;
-        if constexpr (W8) {
-          uint32_t mx = 0;  // largest |q| as bits (bf16 magnitudes order like integers)
+      const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) +
+                                                        row_at(run, x));
+      float up = 1.f;
+      x.sc = a.scale_log2;
+      if constexpr (W8) {
+        uint32_t mx = 0;  // largest |q| as bits (bf16 magnitudes order like integers)
+        if (x.live) {
 #pragma unroll
           for (int c = 0; c < D / 8; ++c) {
-            const uint32_t w[4] = {qv[c].x, qv[c].y, qv[c].z, qv[c].w};
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              mx = max(mx, max(w[k] & 0x7fffu, (w[k] >> 16) & 0x7fffu));
+            const uint4 v = src[c];
+            const uint32_t m = max(max(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu) & 0x7fff0000u,
+                                   max(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu) & 0x7fff0000u) >> 16;
+            mx = max(mx, max(m, max(max(v.x & 0x7fffu, v.y & 0x7fffu),
+                                    max(v.z & 0x7fffu, v.w & 0x7fffu))));
           }
-          const int ex = mx >> 7;  // biased exponent: mx * 2^e in [2^14, 2^15), none for 0, inf, NaN
-          const int e = mx != 0 && ex < 255 ? min(126, max(-126, 141 - ex)) : 0;
-          up = __int_as_float((127 + e) << 23);
-          // (at least the smallest normal number: an unseen score of -inf must stay one)
-          sc = fmaxf(sc * __int_as_float((127 - e) << 23), 0x1p-126f);
         }
-        if (ok && (wide || wg == 0)) {
-          const uint32_t q_col = kColQ + (wide ? 64 * wg : 0);
-#pragma unroll
-          for (int h = 0; h < D / 64; ++h) {
-            uint32_t w[32];
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              const uint32_t x[4] = {qv[8 * h + k].x, qv[8 * h + k].y, qv[8 * h + k].z,
-                                     qv[8 * h + k].w};
-#pragma unroll
-              for (int m = 0; m < 4; ++m)
-                w[4 * k + m] = W8 ? pack_f16(bf16lo(x[m]) * up, bf16hi(x[m]) * up) : x[m];
-            }
-            tmem_st32(lane_t + q_col + 32 * h, w);
-          }
-          tmem_wait_st();
-        }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(q_ready);
+        const int ex = mx >> 7;  // biased exponent: mx * 2^e in [2^14, 2^15), none for 0, inf, NaN
+        const int e = mx != 0 && ex < 255 ? min(126, max(-126, 141 - ex)) : 0;
+        up = __int_as_float((127 + e) << 23);
+        // (at least the smallest normal number: an unseen score of -inf must stay one)
+        x.sc = fmaxf(x.sc * a.k_scales[run.j] * __int_as_float((127 - e) << 23), 0x1p-126f);
       }
+      if (ok && (wide || wg == 0)) {
+        const uint32_t q_col = kColQ + (wide ? 64 * wg : 0);
+#pragma unroll
+        for (int h = 0; h < D / 64; ++h) {
+          uint32_t w[32];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const uint4 v = x.live ? src[8 * h + k] : make_uint4(0, 0, 0, 0);
+            const uint32_t y[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int m = 0; m < 4; ++m)
+              w[4 * k + m] = W8 ? pack_f16(bf16lo(y[m]) * up, bf16hi(y[m]) * up) : y[m];
+          }
+          tmem_st32(lane_t + q_col + 32 * h, w);
+        }
+        tmem_wait_st();
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(q_ready);
+    };
+    Row me{}, then{};
+    TreeRun next_run;
+    bool more = walk.next(a, run);
+    if (more) {
+      me = find_row(run);
+      store_query(run, me);
+    }
+    for (; more; ++unit, run = next_run, me = then) {
+      // the next unit is worked out, and its query brought near, while this one's first scores run
+      more = walk.next(a, next_run);
+      if (more) {
+        then = find_row(next_run);
+        if (then.live) {
+          const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(a.q) + row_at(next_run, then);
+          asm volatile("prefetch.global.L2 [%0];" ::"l"(src));
+          if (D == 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(src + 64));
+        }
+      }
+      const bool wide = run.rows > kGroupThreads, live = me.live;
+      const int n = wide ? 2 * run.n : run.n;  // steps; this group's: wg, wg + 2, ...
+      const int b = run.b, j = run.j, t = me.t;
+      const float sc = me.sc;
+      uint32_t* const bad = bad_nodes + 8 * (unit & 1);
       float m_used = -INFINITY, l = 0.f;
       Place<NS> at = base;
       if (!wide) at.advance(wg);
@@ -630,27 +672,73 @@ __global__ void __launch_bounds__(TcShape<KV, D>::THREADS, 1) tree_tc_kernel(
       asm volatile("bar.sync 1, 256;" ::: "memory");
       tc_fence_after();
       if (threadIdx.x < 8) bad_nodes[8 * ((unit + 1) & 1) + threadIdx.x] = 0;
-      if (ok) {
-        // wide: the group's own rows, all dims; else group wg takes dims wg D/2 .. of every row and
-        // merges the two groups' O
-        float M = m_used, L = l, w0 = 1.f, w1 = 0.f;
-        const bool two = !wide && n > 1;
-        if (!wide) {
-          const float2 x = ml[r], y = ml[kGroupThreads + r];
-          M = fmaxf(x.x, y.x);
-          const float Mu = M == -INFINITY ? 0.f : M;
-          w0 = exp2f(x.x - Mu);
-          w1 = two ? exp2f(y.x - Mu) : 0.f;
-          L = w0 * x.y + (two ? w1 * y.y : 0.f);
-        }
-        const float vs = W8 ? a.v_scales[j] : 1.f;
-        const float f = run.whole ? (L != 0.f ? vs / L : 0.f) : vs;
-        const size_t part = ((size_t)blockIdx.x * 2 + run.slot) * kTreeTcRows + (R - run.row0);
-        __nv_bfloat16* orow = static_cast<__nv_bfloat16*>(a.out) +
-                              (((size_t)b * a.nodes + t) * a.h_q + head) * D;
-        uint32_t any_bad = 0;
+      // wide: the group's own rows, all dims; else group wg takes dims wg D/2 .. of every row and
+      // merges the two groups' O
+      float M = m_used, L = l, w0 = 1.f, w1 = 0.f;
+      const bool two = !wide && n > 1;
+      if (!wide) {
+        const float2 x = ml[r], y = ml[kGroupThreads + r];
+        M = fmaxf(x.x, y.x);
+        const float Mu = M == -INFINITY ? 0.f : M;
+        w0 = exp2f(x.x - Mu);
+        w1 = two ? exp2f(y.x - Mu) : 0.f;
+        L = w0 * x.y + (two ? w1 * y.y : 0.f);
+      }
+      const float vs = W8 ? a.v_scales[j] : 1.f;
+      const float f = run.whole ? (L != 0.f ? vs / L : 0.f) : vs;
+      uint32_t any_bad = 0;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) any_bad |= bad[k];
+      for (int k = 0; k < 8; ++k) any_bad |= bad[k];
+      // 32 dims from c on of this thread's row: finished, or a partial
+      auto emit = [&](int c, uint32_t (&o)[32]) {
+        if (!live) return;
+        if (any_bad) {  // the infinite and NaN values of the nodes this row sees
+          for (int nd = 0; nd < run.req.nodes; ++nd) {
+            if (!((bad[nd >> 5] >> (nd & 31)) & 1)) continue;
+            const int pos = run.req.base + nd;
+            if (!(tree_seen(a, run.req, b, t, pos) & 1)) continue;
+            const int id = a.block_tables[(size_t)b * a.max_pages + pos / kPageSize];
+            const int64_t at =
+                ((((int64_t)id * a.h_kv + j) * kPageSize + pos % kPageSize) * D + c) * KV::bytes;
+            const uint8_t* v = static_cast<const uint8_t*>(a.v_cache) + at;
+#pragma unroll
+            for (int k = 0; k < 32; k += 4) {
+              float x[4];
+              RowLoad<KV, 4>::run(v + k * KV::bytes, x);
+#pragma unroll
+              for (int m = 0; m < 4; ++m)
+                if (!(fabsf(x[m]) < INFINITY))
+                  o[k + m] = __float_as_uint(__uint_as_float(o[k + m]) + x[m]);
+            }
+          }
+        }
+        if (run.whole) {
+          __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.out) + row_at(run, me) + c;
+#pragma unroll
+          for (int k = 0; k < 32; k += 8) {
+            uint4 v;
+            uint32_t* w = &v.x;
+#pragma unroll
+            for (int m = 0; m < 4; ++m)
+              w[m] = L != 0.f ? pack_bf16(__uint_as_float(o[k + 2 * m]) * f,
+                                          __uint_as_float(o[k + 2 * m + 1]) * f)
+                              : 0u;
+            *reinterpret_cast<uint4*>(dst + k) = v;
+          }
+        } else {
+          const size_t part = ((size_t)blockIdx.x * 2 + run.slot) * kTreeTcRows + me.row;
+          float* dst = a.ws_acc + part * D + c;
+#pragma unroll
+          for (int k = 0; k < 32; k += 4)
+            *reinterpret_cast<float4*>(dst + k) =
+                make_float4(__uint_as_float(o[k]) * f, __uint_as_float(o[k + 1]) * f,
+                            __uint_as_float(o[k + 2]) * f, __uint_as_float(o[k + 3]) * f);
+          if (c == 0) *reinterpret_cast<float2*>(a.ws_ml + 2 * part) = make_float2(M, L);
+        }
+      };
+      // the next query first, so that the next unit's scores run while this one's rows are written
+      if (more) store_query(next_run, then);
+      if (ok) {
         const int c_lo = wide ? 0 : wg * (D / 2), c_hi = wide ? D : c_lo + D / 2;
         for (int c = c_lo; c < c_hi; c += 32) {
           uint32_t o[32];
@@ -664,55 +752,17 @@ __global__ void __launch_bounds__(TcShape<KV, D>::THREADS, 1) tree_tc_kernel(
               o[k] = __float_as_uint(w0 * __uint_as_float(o[k]) + w1 * __uint_as_float(o1[k]));
           } else {
             tmem_wait_ld();
-            if (!wide)
+            if (!wide) {
 #pragma unroll
               for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(w0 * __uint_as_float(o[k]));
-          }
-          if (any_bad && live) {  // the infinite and NaN values of the nodes this row sees
-            for (int n = 0; n < run.req.nodes; ++n) {
-              if (!((bad[n >> 5] >> (n & 31)) & 1)) continue;
-              const int pos = run.req.base + n;
-              if (!(tree_seen(a, run.req, b, t, pos) & 1)) continue;
-              const int id = a.block_tables[(size_t)b * a.max_pages + pos / kPageSize];
-              const int64_t at =
-                  ((((int64_t)id * a.h_kv + j) * kPageSize + pos % kPageSize) * D + c) * KV::bytes;
-              const uint8_t* v = static_cast<const uint8_t*>(a.v_cache) + at;
-#pragma unroll
-              for (int k = 0; k < 32; k += 4) {
-                float x[4];
-                RowLoad<KV, 4>::run(v + k * KV::bytes, x);
-#pragma unroll
-                for (int m = 0; m < 4; ++m)
-                  if (!(fabsf(x[m]) < INFINITY))
-                    o[k + m] = __float_as_uint(__uint_as_float(o[k + m]) + x[m]);
-              }
             }
           }
-          if (live) {
-            if (run.whole) {
-#pragma unroll
-              for (int k = 0; k < 32; k += 8) {
-                uint4 v;
-                uint32_t* w = &v.x;
-#pragma unroll
-                for (int m = 0; m < 4; ++m)
-                  w[m] = L != 0.f ? pack_bf16(__uint_as_float(o[k + 2 * m]) * f,
-                                              __uint_as_float(o[k + 2 * m + 1]) * f)
-                                  : 0u;
-                *reinterpret_cast<uint4*>(orow + c + k) = v;
-              }
-            } else {
-              float* dst = a.ws_acc + part * D + c;
-#pragma unroll
-              for (int k = 0; k < 32; k += 4)
-                *reinterpret_cast<float4*>(dst + k) =
-                    make_float4(__uint_as_float(o[k]) * f, __uint_as_float(o[k + 1]) * f,
-                                __uint_as_float(o[k + 2]) * f, __uint_as_float(o[k + 3]) * f);
-              if (c == 0) *reinterpret_cast<float2*>(a.ws_ml + 2 * part) = make_float2(M, L);
-            }
-          }
+          emit(c, o);
         }
       }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(o_read);
       ph = after_steps(ph, wide, n);
       base.skip(run.n);
     }

@@ -5,7 +5,10 @@
 // KV head are cut into units of unit_rows. A (KV head, unit) of b is one pass over b's tiles, and
 // the tiles of all passes of all requests, in order, form one stream. Each CTA takes an equal
 // contiguous share of it, whatever the lengths: no CTA idles beside a long request, and few rows
-// over a long context still fill the GPU. A pass that lies in one share is finished by its CTA; one
+// over a long context still fill the GPU. Beginning a pass (its queries, its output) costs a CTA
+// about as much as pass_cost tiles, so in calls of many tiles per CTA every pass counts that much
+// more, before its first tile: shares with many short passes get fewer tiles. A pass that lies in one
+// share is finished by its CTA; one
 // that crosses shares leaves a partial (running maximum, sum, weighted values) in each, at most
 // two per CTA (slot 0: the pass began in an earlier share; slot 1: it began here and goes on),
 // which the combine merges in share order. The split depends on the lengths and the grid alone, so
@@ -56,11 +59,6 @@ __device__ __forceinline__ TreeSize tree_size(const TreeArgs& a, const TreeReq& 
                   (r.nodes * a.group + a.unit_rows - 1) / a.unit_rows};
 }
 
-// (The host refuses a call whose table could hold 2^31 tiles: the stream's positions are ints.)
-__device__ __forceinline__ int tree_tiles(const TreeArgs& a, const TreeSize& z) {
-  return z.tiles * z.units * a.h_kv;
-}
-
 // Sums over a block: `below` of the values of threads before this one, `total` of all. Shared
 // scratch of 32 words; every thread of the block calls it.
 template <int THREADS>
@@ -84,44 +82,63 @@ __device__ __forceinline__ void block_scan(int v, int* scratch, int& below, int&
   }
 }
 
-// Where a CTA's share begins: in request b at tile `off` of that request's part of the stream,
-// `count` tiles long (0: nothing to do).
-struct TreeShare {
-  int b, off, count;
+// The stream of a call: its length, what a pass costs beyond its tiles, and a share's length, in
+// tiles. (The host refuses a call whose table could hold 2^30 of them: positions are ints.)
+struct TreeStream {
+  int total, pass_cost, share;
 };
 
-__device__ __forceinline__ int tree_share_size(const TreeArgs& a, int total) {
-  return max(a.min_tiles, (int)(((unsigned)total + a.ctas - 1) / (unsigned)a.ctas));
+__device__ __forceinline__ TreeStream tree_stream(const TreeArgs& a, int tiles, int passes) {
+  TreeStream s;
+  s.pass_cost = tiles >= 16 * a.ctas ? a.pass_cost : 0;
+  s.total = tiles + s.pass_cost * passes;
+  s.share = max(a.min_tiles, (int)(((unsigned)s.total + a.ctas - 1) / (unsigned)a.ctas));
+  return s;
 }
 
-// Every thread of a block of THREADS takes part; `out` and `scratch` are shared memory. Argument
-// errors are reported by block 0. Ends with a block barrier.
+// A request's part of the stream.
+__device__ __forceinline__ int tree_length(const TreeArgs& a, const TreeSize& z, int pass_cost) {
+  return (z.tiles + pass_cost) * z.units * a.h_kv;
+}
+
+// A CTA's share: from request b on, `off` into that request's part of the stream, `count` long.
+struct TreeShare {
+  int b, off, count, pass_cost;
+};
+
+// Every thread of a block of THREADS takes part; `out` and `scratch` (64 words) are shared memory.
+// Argument errors are reported by block 0. Ends with a block barrier.
 template <int THREADS>
 __device__ __forceinline__ void tree_share(const TreeArgs& a, int* scratch, TreeShare* out) {
   const int per = (a.batch + THREADS - 1) / THREADS;
   const int b0 = min(a.batch, (int)threadIdx.x * per), b1 = min(a.batch, b0 + per);
-  int mine = 0, err = 0;
+  int tiles = 0, passes = 0, err = 0;
   for (int b = b0; b < b1; ++b) {
     const TreeReq r = tree_request(a, b);
+    const TreeSize z = tree_size(a, r);
     err |= r.err;
-    mine += tree_tiles(a, tree_size(a, r));
+    tiles += z.tiles * z.units * a.h_kv;
+    passes += z.units * a.h_kv;
   }
   if (err && blockIdx.x == 0) atomicOr(a.err, err);
   if (threadIdx.x == 0) out->count = 0;
-  int below, total;
-  block_scan<THREADS>(mine, scratch, below, total);
-  const int share = tree_share_size(a, total);
-  const long long start = (long long)blockIdx.x * share;
-  if (start >= below && start < below + mine) {
+  int tiles_below, tiles_all, passes_below, passes_all;
+  block_scan<THREADS>(tiles, scratch, tiles_below, tiles_all);
+  block_scan<THREADS>(passes, scratch + 32, passes_below, passes_all);
+  const TreeStream s = tree_stream(a, tiles_all, passes_all);
+  const int mine = tiles + s.pass_cost * passes, below = tiles_below + s.pass_cost * passes_below;
+  const long long start = (long long)blockIdx.x * s.share;
+  if (start >= below && start < (long long)below + mine) {
     int at = below, b = b0;
     for (; b < b1 - 1; ++b) {  // (one request per thread up to THREADS requests)
-      const int t = tree_tiles(a, tree_size(a, tree_request(a, b)));
+      const int t = tree_length(a, tree_size(a, tree_request(a, b)), s.pass_cost);
       if (start < at + t) break;
       at += t;
     }
     out->b = b;
     out->off = (int)start - at;
-    out->count = min(share, total - (int)start);
+    out->count = min(s.share, s.total - (int)start);
+    out->pass_cost = s.pass_cost;
   }
   __syncthreads();
 }
@@ -138,30 +155,34 @@ struct TreeRun {
 
 // Walks a share run by run. Uniform over its callers (it reads the lengths itself).
 struct TreeWalk {
-  int b, off, left;
+  int b, off, left, pass_cost;
+  __device__ __forceinline__ explicit TreeWalk(const TreeShare& s)
+      : b(s.b), off(s.off), left(s.count), pass_cost(s.pass_cost) {}
   __device__ __forceinline__ bool next(const TreeArgs& a, TreeRun& r) {
     while (left > 0 && b < a.batch) {
       const TreeReq q = tree_request(a, b);
       const TreeSize z = tree_size(a, q);
-      const int t = tree_tiles(a, z);
-      if (off >= t) {
-        off -= t;
+      if (off >= tree_length(a, z, pass_cost)) {
+        off -= tree_length(a, z, pass_cost);
         ++b;
         continue;
       }
-      const int pass = (int)((unsigned)off / (unsigned)z.tiles);
-      const int unit = (int)((unsigned)pass % (unsigned)z.units);
+      const int len = z.tiles + pass_cost;  // of a pass, its cost first
+      const int pass = (int)((unsigned)off / (unsigned)len);
+      const int x0 = off - pass * len, x1 = min(len, x0 + left);
+      off += x1 - x0;
+      left -= x1 - x0;
+      if (x1 <= pass_cost) continue;  // (none of its tiles)
+      const int j = (int)((unsigned)pass / (unsigned)z.units);
       r.req = q;
       r.b = b;
-      r.j = (int)((unsigned)pass / (unsigned)z.units);
-      r.row0 = unit * a.unit_rows;
+      r.j = j;
+      r.row0 = (pass - j * z.units) * a.unit_rows;
       r.rows = min(a.unit_rows, q.nodes * a.group - r.row0);
-      r.tile0 = off - pass * z.tiles;
-      r.n = min(z.tiles - r.tile0, left);
+      r.tile0 = max(0, x0 - pass_cost);
+      r.n = x1 - pass_cost - r.tile0;
       r.whole = r.n == z.tiles;
       r.slot = r.tile0 > 0 ? 0 : 1;
-      off += r.n;
-      left -= r.n;
       return true;
     }
     return false;
