@@ -51,7 +51,7 @@ constexpr int kPages = kTok / kPageSize;   // pages of a tile
 constexpr int kGroupThreads = 128;         // a softmax group: one row per thread
 constexpr int kSoftThreads = 2 * kGroupThreads;
 constexpr int kMmaWarp = kSoftThreads / 32;
-constexpr int kCopyWarp = kMmaWarp + 1;    // (its warpgroup's last two warps are idle)
+constexpr int kCopyWarp = kMmaWarp + 1;    // copies K; the warp after it V
 constexpr int kConvWarp = kMmaWarp + 4;    // first of four (8-bit caches)
 constexpr int kConvThreads = 128;
 constexpr int kSBufs = 3;
@@ -69,20 +69,21 @@ struct TcShape {
   // registers of the softmax warps and of the others, out of what the launch gives every warp
   static constexpr int SOFT_REGS = W8 ? 176 : 208, REGS = W8 ? 72 : 80;
   static constexpr int TILE = kTok * D * 2;       // K (or V) of a tile in MMA form
-  static constexpr int STAGE = 2 * TILE;
   static constexpr int RAW_TILE = kTok * D;       // 8-bit codes
   static constexpr int RAW_STAGE = 2 * RAW_TILE;
-  // a ring of 192 KB; 8-bit caches: half of it raw codes, half MMA form
-  static constexpr int NS = (W8 ? 96 : 192) * 1024 / STAGE;
+  // 208 KB of rings: K tiles, needed until their S is done, and V tiles, needed until their P V
+  // is done, go round separately; 8-bit caches have 96 KB of raw codes before them
+  static constexpr int NK = (W8 ? 48 : 96) * 1024 / TILE, NV = (W8 ? 64 : 112) * 1024 / TILE;
   static constexpr int NR = W8 ? 96 * 1024 / RAW_STAGE : 0;
-  static constexpr int OFF_RAW = NS * STAGE;
+  static constexpr int OFF_V = NK * TILE;
+  static constexpr int OFF_RAW = OFF_V + NV * TILE;
   static constexpr int OFF_ML = OFF_RAW + NR * RAW_STAGE;   // [2][128] (max, sum)
   static constexpr int OFF_BAR = OFF_ML + 2 * kGroupThreads * 8;
-  static constexpr int BARS = 2 * NS + 2 * NR + 3 * kSBufs + 3;
+  static constexpr int BARS = 2 * NK + 2 * NV + 2 * NR + 3 * kSBufs + 3;
   static constexpr int OFF_MISC = OFF_BAR + 8 * BARS;       // masks, bad nodes, TMEM address
   static constexpr uint32_t IDESC_S = tc_idesc(128, kTok, false, W8);
   static constexpr uint32_t IDESC_PV = tc_idesc(128, D, true, W8);
-  static constexpr int SMEM = 1024 + OFF_MISC + 4 * (NS + NR + 2 * 8 + 1) + 16;
+  static constexpr int SMEM = 1024 + OFF_MISC + 4 * (NV + NR + 2 * 8 + 1) + 16;
   static_assert(SMEM <= 227 * 1024 && SMEM > 114 * 1024, "one CTA per SM");
 };
 
@@ -162,7 +163,7 @@ __global__ void __launch_bounds__(TcShape<KV, D>::THREADS, 1) tree_tc_kernel(
     const __grid_constant__ CUtensorMap tm_v) {
   using S = TcShape<KV, D>;
   constexpr bool W8 = S::W8;
-  constexpr int NS = S::NS, NR = S::NR;
+  constexpr int NK = S::NK, NV = S::NV, NR = S::NR;
   constexpr int PAGE_MMA = kPageSize * D * 2;  // V bytes of a page in MMA form
   constexpr int PAGE_RAW = kPageSize * D;
   const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
@@ -171,9 +172,11 @@ __global__ void __launch_bounds__(TcShape<KV, D>::THREADS, 1) tree_tc_kernel(
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t ring = smem_u32(smem);
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + S::OFF_BAR);  // [NS] tile in MMA form
-  uint64_t* freed = full + NS;                                       // [NS] its P V done
-  uint64_t* raw_full = freed + NS;                                   // [NR] codes arrived
+  uint64_t* full_k = reinterpret_cast<uint64_t*>(smem + S::OFF_BAR);  // [NK] K of a tile is there
+  uint64_t* free_k = full_k + NK;                                    // [NK] its S done
+  uint64_t* full_v = free_k + NK;                                    // [NV] V of a tile is there
+  uint64_t* free_v = full_v + NV;                                    // [NV] its P V done
+  uint64_t* raw_full = free_v + NV;                                  // [NR] codes arrived
   uint64_t* raw_freed = raw_full + NR;                               // [NR] codes widened
   uint64_t* s_done = raw_freed + NR;                                 // [3] S in its buffer
   uint64_t* p_ready = s_done + kSBufs;                               // [3] P in its buffer
@@ -181,8 +184,8 @@ __global__ void __launch_bounds__(TcShape<KV, D>::THREADS, 1) tree_tc_kernel(
   uint64_t* q_ready = pv_done + kSBufs;                              // Q of a unit stored
   uint64_t* o_read = q_ready + 1;                                    // O of a unit read
   uint64_t* mma_idle = o_read + 1;
-  int* page_mask = reinterpret_cast<int*>(smem + S::OFF_MISC);       // [NS] good pages of the tile
-  int* raw_mask = page_mask + NS;                                    // [NR]
+  int* page_mask = reinterpret_cast<int*>(smem + S::OFF_MISC);       // [NV] good pages of the tile
+  int* raw_mask = page_mask + NV;                                    // [NR]
   uint32_t* bad_nodes = reinterpret_cast<uint32_t*>(raw_mask + NR);  // [2][8] V row not finite
   uint32_t* s_taddr = bad_nodes + 16;
   float2* ml = reinterpret_cast<float2*>(smem + S::OFF_ML);          // [2][128]
@@ -191,12 +194,16 @@ __global__ void __launch_bounds__(TcShape<KV, D>::THREADS, 1) tree_tc_kernel(
   __shared__ TreeShare share;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (threadIdx.x == kCopyWarp * 32) {
-    for (int s = 0; s < NS; ++s) {
-      mbar_init(&full[s], W8 ? kConvThreads / 32 : 1);
-      mbar_init(&freed[s], 1);
+    for (int s = 0; s < NK; ++s) {
+      mbar_init(&full_k[s], W8 ? kConvThreads / 32 : 1);
+      mbar_init(&free_k[s], 1);
+    }
+    for (int s = 0; s < NV; ++s) {
+      mbar_init(&full_v[s], W8 ? kConvThreads / 32 : 1);
+      mbar_init(&free_v[s], 1);
     }
     for (int s = 0; s < NR; ++s) {
-      mbar_init(&raw_full[s], 1);
+      mbar_init(&raw_full[s], 2);
       mbar_init(&raw_freed[s], kConvThreads / 32);
     }
     for (int s = 0; s < kSBufs; ++s) {
@@ -232,17 +239,23 @@ __global__ void __launch_bounds__(TcShape<KV, D>::THREADS, 1) tree_tc_kernel(
 
   if (warp >= kMmaWarp && warp < kConvWarp) {
     regs_down<S::REGS>();
-    if (warp == kCopyWarp) {
+    if (warp == kCopyWarp || warp == kCopyWarp + 1) {
       // ===================== copies: the share's tiles, in order =====================
-      constexpr int N = W8 ? NR : NS;
-      uint64_t* const arrive = W8 ? raw_full : full;
-      uint64_t* const leave = W8 ? raw_freed : freed;
-      int* const masks = W8 ? raw_mask : page_mask;
+      // One warp copies K, one V, each through its own ring (8-bit caches: both into the same
+      // stages): a copy's issue takes a while, and a tile of 64 tokens is 8 to 12 of them.
+      const bool is_k = warp == kCopyWarp;
       // the row units of more than 256 rows read the same tiles again
       const uint64_t pol =
           a.nodes * a.group > kTreeTcRows ? l2_evict_last_policy() : l2_evict_first_policy();
-      Place<N> at;
-      int issued = 0;
+      const int stages = W8 ? NR : is_k ? NK : NV;
+      uint64_t* const there = W8 ? raw_full : is_k ? full_k : full_v;
+      uint64_t* const gone = W8 ? raw_freed : is_k ? free_k : free_v;
+      int* const masks = W8 ? raw_mask : page_mask;  // (written by the V warp)
+      const uint32_t ring0 = ring + (is_k ? 0 : S::OFF_V);
+      uint8_t* const raw0 = smem + S::OFF_RAW + (is_k ? 0 : S::RAW_TILE);
+      const uint8_t* const pool = static_cast<const uint8_t*>(is_k ? a.k_cache : a.v_cache);
+      int st = 0, issued = 0;
+      uint32_t par = 0;
       bool ok = true;
       while (ok && walk.next(a, run)) {
         const int pages = uniform((run.req.read + kPageSize - 1) / kPageSize);
@@ -259,58 +272,54 @@ __global__ void __launch_bounds__(TcShape<KV, D>::THREADS, 1) tree_tc_kernel(
             id[p] = __shfl_sync(0xffffffffu, ids, (kPages * i + p) & 31);
             if (lp + p < pages && id[p] >= 0 && id[p] < a.num_pages) mask |= 1u << p;
           }
-          if (issued >= N) {
-            ok = mbar_wait(&leave[at.st], at.par ^ 1u, a.err);
-            ok = __all_sync(0xffffffffu, ok);
+          if (is_k && mask != (1u << min(kPages, pages - lp)) - 1 && lane == 0)
+            atomicOr(a.err, PKV_DEVERR_BAD_PAGE);
+          if (issued >= stages) {
+            ok = __all_sync(0xffffffffu, mbar_wait(&gone[st], par ^ 1u, a.err));
             if (!ok) break;
           }
-          if (mask != (1u << min(kPages, pages - lp)) - 1 && lane == 0)
-            atomicOr(a.err, PKV_DEVERR_BAD_PAGE);
-          __syncwarp();
           if (elect_one()) {
-            masks[at.st] = (int)mask;
+            if (!is_k) masks[st] = (int)mask;
             if constexpr (W8) fence_proxy_async_smem();
-            mbar_arrive_expect_tx(&arrive[at.st], __popc(mask) * 2 * (W8 ? PAGE_RAW : PAGE_MMA));
+            mbar_arrive_expect_tx(&there[st], __popc(mask) * (W8 ? PAGE_RAW : PAGE_MMA));
 #pragma unroll
             for (int p = 0; p < kPages; ++p) {
               if (!((mask >> p) & 1)) continue;
               if constexpr (W8) {
-                const int64_t src = ((int64_t)id[p] * a.h_kv + j) * PAGE_RAW;
-                uint8_t* dst = smem + S::OFF_RAW + at.st * S::RAW_STAGE + p * PAGE_RAW;
-                bulk_g2s(dst, static_cast<const uint8_t*>(a.k_cache) + src, PAGE_RAW,
-                         &arrive[at.st], pol);
-                bulk_g2s(dst + S::RAW_TILE, static_cast<const uint8_t*>(a.v_cache) + src, PAGE_RAW,
-                         &arrive[at.st], pol);
+                bulk_g2s(raw0 + st * S::RAW_STAGE + p * PAGE_RAW,
+                         pool + ((int64_t)id[p] * a.h_kv + j) * PAGE_RAW, PAGE_RAW, &there[st], pol);
               } else {
                 const int row = (id[p] * a.h_kv + j) * kPageSize;
-                const uint32_t dst = ring + at.st * S::STAGE;
-                // K: 64-dim blocks of all 64 rows (one N = 64 operand); V: a block per page (K = 16)
+                const uint32_t dst = ring0 + st * S::TILE;
+                if (is_k) {  // 64-dim blocks of all 64 rows (one N = 64 operand)
 #pragma unroll
-                for (int bx = 0; bx < D / 64; ++bx)
-                  tma_load_2d(dst + bx * (kTok * 128) + p * 2048, &tm_k, bx * 64, row,
-                              &arrive[at.st], pol);
-                tma_tile<D / 64, 64>(dst + S::TILE + p * PAGE_MMA, &tm_v, a.tma_rank, row,
-                                     &arrive[at.st], pol);
+                  for (int bx = 0; bx < D / 64; ++bx)
+                    tma_load_2d(dst + bx * (kTok * 128) + p * 2048, &tm_k, bx * 64, row, &there[st],
+                                pol);
+                } else {  // a block per page (K = 16)
+                  tma_tile<D / 64, 64>(dst + p * PAGE_MMA, &tm_v, a.tma_rank, row, &there[st], pol);
+                }
               }
             }
           }
           __syncwarp();
-          at.advance(1);
+          if (++st == stages) {
+            st = 0;
+            par ^= 1u;
+          }
           ++issued;
         }
       }
-      if (lane == 0) {  // before leaving, every copy issued has landed
-        for (int k = min(issued, N); k > 0; --k) {
-          const int back = issued - k;
-          mbar_wait(&arrive[back % N], (uint32_t)(back / N) & 1u, a.err);
-        }
-      }
+      if (lane == 0)  // before leaving, every copy issued has landed
+        for (int t = max(0, issued - stages); t < issued; ++t)
+          mbar_wait(&there[t % stages], (uint32_t)(t / stages) & 1u, a.err);
     } else if (warp == kMmaWarp) {
       // ===================== MMAs (one elected lane issues) =====================
-      const uint64_t k_desc = tc_desc(ring, 16, 1024), v_desc = tc_desc(ring + S::TILE, 2048, 1024);
+      const uint64_t k_desc = tc_desc(ring, 16, 1024), v_desc = tc_desc(ring + S::OFF_V, 2048, 1024);
       bool ok = true;
       uint32_t ph = 0, unit = 0;
-      Place<NS> ks, vs;  // tiles of the next S and of the next P V
+      Place<NK> ks;  // tile of the next S
+      Place<NV> vs;  // tile of the next P V
       auto wait = [&](uint64_t* bar, uint32_t par) {
         const bool got = __all_sync(0xffffffffu, mbar_wait(bar, par, a.err));
         tc_fence_after();
@@ -323,30 +332,35 @@ __global__ void __launch_bounds__(TcShape<KV, D>::THREADS, 1) tree_tc_kernel(
         ++unit;
         bool odd = false;  // the next S's step
         auto s_mma = [&](int buf) {
-          if (!wait(&full[ks.st], ks.par)) return false;
-          const uint64_t kd = k_desc + (uint32_t)(ks.st * (S::STAGE >> 4));
+          if (!(wide && odd) && !wait(&full_k[ks.st], ks.par)) return false;
+          const uint64_t kd = k_desc + (uint32_t)(ks.st * (S::TILE >> 4));
           const uint32_t q = tmem + kColQ + (wide && odd ? 64 : 0), d = tmem + s_col(buf);
+          const bool tile_done = !wide || odd;
           if (elect_one()) {
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk)
               tc_mma_ta(d, q + 8 * kk, kd + (((kk >> 2) * (kTok * 128) + (kk & 3) * 32) >> 4),
                         S::IDESC_S, kk > 0 ? 1u : 0u);
             tc_commit(&s_done[buf]);
+            if (tile_done) tc_commit(&free_k[ks.st]);
           }
           __syncwarp();
-          if (!wide || odd) ks.advance(1);
+          if (tile_done) ks.advance(1);
           odd = !odd;
           return true;
         };
-        const int bufs = wide ? 2 : kSBufs;
-        for (int u = 0; ok && u < bufs && u < n; ++u) ok = s_mma(u);
-        Buf b{0, 0};
-        for (int u = 0; ok && u < n; ++u, b.advance(wide, 1)) {
+        // S runs two steps ahead of P V. Its buffer held P of an earlier step, whose P V must be
+        // complete: with three buffers that of the step before this one, which is (the wait costs
+        // nothing); with two that of this step.
+        for (int u = 0; ok && u < 2 && u < n; ++u) ok = s_mma(u);
+        Buf b{0, 0}, before{0, 0}, ahead{2, 0};
+        if (wide) ahead.i = 0;
+        for (int u = 0; ok && u < n; ++u) {
           const uint32_t par = b.parity(ph);
           ok = wait(&p_ready[b.i], par);
           if (ok && u == 0 && unit > 1) ok = wait(o_read, unit & 1);  // (of the last unit)
           if (!ok) break;
-          const uint64_t vd = v_desc + (uint32_t)(vs.st * (S::STAGE >> 4));
+          const uint64_t vd = v_desc + (uint32_t)(vs.st * (S::TILE >> 4));
           const uint32_t o = tmem + kColO + ((u & 1) << 7), pc = tmem + s_col(b.i);
           const bool tile_done = !wide || (u & 1);
           if (elect_one()) {
@@ -355,14 +369,20 @@ __global__ void __launch_bounds__(TcShape<KV, D>::THREADS, 1) tree_tc_kernel(
               tc_mma_ta(o, pc + 8 * kk, vd + ((kk * PAGE_MMA) >> 4), S::IDESC_PV,
                         u < 2 && kk == 0 ? 0u : 1u);
             tc_commit(&pv_done[b.i]);
-            if (tile_done) tc_commit(&freed[vs.st]);
+            if (tile_done) tc_commit(&free_v[vs.st]);
           }
           __syncwarp();
           if (tile_done) vs.advance(1);
-          if (u + bufs < n) {  // its S overwrites the buffer that this P lives in
-            ok = wait(&pv_done[b.i], par);
-            if (ok) ok = s_mma(b.i);
+          if (u + 2 < n) {
+            if (wide)
+              ok = wait(&pv_done[b.i], par);
+            else if (u > 0)
+              ok = wait(&pv_done[before.i], before.parity(ph));
+            if (ok) ok = s_mma(ahead.i);
           }
+          before = b;
+          b.advance(wide, 1);
+          ahead.advance(wide, 1);
         }
         ph = after_steps(ph, wide, n);
       }
@@ -393,47 +413,58 @@ __global__ void __launch_bounds__(TcShape<KV, D>::THREADS, 1) tree_tc_kernel(
       static_assert(ROWS % 8 == 0, "a thread's rows share their swizzle");
       const uint32_t src0 = ring + S::OFF_RAW + row0 * D + c * 16;
       const uint32_t k0 = ring + (ch >> 3) * (kTok * 128) + row0 * 128;
-      const uint32_t v0 = ring + S::TILE + (ch >> 3) * 2048;
-      Place<NR> raw;
-      Place<NS> out;
+      const uint32_t v0 = ring + S::OFF_V + (ch >> 3) * 2048;
+      Place<W8 ? NR : 1> raw;
+      Place<NK> pk;
+      Place<NV> pv;
       bool ok = true;
       int t = 0, end = 0;  // tiles done, tiles of the runs so far
-      for (;; ++t, raw.advance(1), out.advance(1)) {
+      for (;; ++t, raw.advance(1), pk.advance(1), pv.advance(1)) {
         if (t == end) {
           if (!walk.next(a, run)) break;
           end += run.n;
         }
         ok = mbar_wait(&raw_full[raw.st], raw.par, a.err);
-        if (ok && t >= NS) ok = mbar_wait(&freed[out.st], out.par ^ 1u, a.err);
         if (!ok) break;
-        const uint32_t src = src0 + raw.st * S::RAW_STAGE, dst = out.st * S::STAGE;
-        uint4 w[PER];
+        const uint32_t src = src0 + raw.st * S::RAW_STAGE;
+        const int mask = raw_mask[raw.st];
+        uint4 w[PER];  // K, then V
 #pragma unroll
         for (int i = 0; i < PER / 2; ++i) {
           w[i] = lds128(src + i * ROWS * D);
           w[PER / 2 + i] = lds128(src + S::RAW_TILE + i * ROWS * D);
         }
-#pragma unroll
-        for (int i = 0; i < PER; ++i) {
+        auto widen_to = [&](const uint4& v, uint32_t at) {
           uint4 lo, hi;
-          widen4<KV>(w[i].x, lo.x, lo.y);
-          widen4<KV>(w[i].y, lo.z, lo.w);
-          widen4<KV>(w[i].z, hi.x, hi.y);
-          widen4<KV>(w[i].w, hi.z, hi.w);
-          const int r = row0 + (i % (PER / 2)) * ROWS;
-          const uint32_t at = dst + (i < PER / 2
-                                         ? k0 + i * ROWS * 128
-                                         : v0 + (r >> 4) * PAGE_MMA + (r & 15) * 128);
+          widen4<KV>(v.x, lo.x, lo.y);
+          widen4<KV>(v.y, lo.z, lo.w);
+          widen4<KV>(v.z, hi.x, hi.y);
+          widen4<KV>(v.w, hi.z, hi.w);
           sts128(at + x0, lo);
           sts128(at + x1, hi);
-        }
-        if (i0 == 0) page_mask[out.st] = raw_mask[raw.st];
+        };
+        if (t >= NK) ok = mbar_wait(&free_k[pk.st], pk.par ^ 1u, a.err);
+        if (!ok) break;
+#pragma unroll
+        for (int i = 0; i < PER / 2; ++i) widen_to(w[i], k0 + pk.st * S::TILE + i * ROWS * 128);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
-          mbar_arrive(&full[out.st]);
-          mbar_arrive(&raw_freed[raw.st]);
+          mbar_arrive(&full_k[pk.st]);
+          mbar_arrive(&raw_freed[raw.st]);  // (K and V codes are in registers)
         }
+        if (t >= NV) ok = mbar_wait(&free_v[pv.st], pv.par ^ 1u, a.err);
+        if (!ok) break;
+#pragma unroll
+        for (int i = 0; i < PER / 2; ++i) {
+          const int r = row0 + i * ROWS;
+          widen_to(w[PER / 2 + i],
+                   v0 + pv.st * S::TILE + (r >> 4) * PAGE_MMA + (r & 15) * 128);
+        }
+        if (i0 == 0) page_mask[pv.st] = mask;
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&full_v[pv.st]);
       }
     }
   } else {
@@ -444,7 +475,7 @@ __global__ void __launch_bounds__(TcShape<KV, D>::THREADS, 1) tree_tc_kernel(
     const uint32_t lane_t = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     bool ok = true;
     uint32_t ph = 0, unit = 0;
-    Place<NS> base;  // the run's first tile
+    Place<NV> base;  // V of the run's first tile
     // The row of this thread in a run (row `row` of its unit, node t, query head `head`) and its
     // score factor.
     struct Row {
@@ -535,7 +566,7 @@ __global__ void __launch_bounds__(TcShape<KV, D>::THREADS, 1) tree_tc_kernel(
       const float sc = me.sc;
       uint32_t* const bad = bad_nodes + 8 * (unit & 1);
       float m_used = -INFINITY, l = 0.f;
-      Place<NS> at = base;
+      Place<NV> at = base;
       if (!wide) at.advance(wg);
       Buf bf{wg, 0};
       int prev_buf = 0;         // this group's last step
@@ -544,7 +575,8 @@ __global__ void __launch_bounds__(TcShape<KV, D>::THREADS, 1) tree_tc_kernel(
       const int seen_by_all = min(run.req.base, run.req.read) - kTok;
       for (int u = wg; ok && u < n; u += 2) {
         const uint32_t par = bf.parity(ph);
-        ok = mbar_wait(&full[at.st], at.par, a.err) && mbar_wait(&s_done[bf.i], par, a.err);
+        // (V of the tile too: the MMA warp takes a P as the word that it is there)
+        ok = mbar_wait(&full_v[at.st], at.par, a.err) && mbar_wait(&s_done[bf.i], par, a.err);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         const int mask = page_mask[at.st];
@@ -566,7 +598,7 @@ __global__ void __launch_bounds__(TcShape<KV, D>::THREADS, 1) tree_tc_kernel(
           if (!wide || wg == 0) {  // mend V: two threads to a row
             const int vr = r >> 1, pos = p0 + vr;
             constexpr int CH = D / 16;  // 16-byte chunks of half a row
-            const uint32_t vrow = ring + at.st * S::STAGE + S::TILE + (vr >> 4) * PAGE_MMA +
+            const uint32_t vrow = ring + S::OFF_V + at.st * S::TILE + (vr >> 4) * PAGE_MMA +
                                   (vr & 15) * 128 + (D == 128 ? (r & 1) * 2048 : 0);
             const int c0 = D == 128 ? 0 : (r & 1) * CH;
             if (pos >= run.req.read || !((mask >> (vr >> 4)) & 1)) {
