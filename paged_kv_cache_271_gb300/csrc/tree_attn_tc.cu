@@ -50,9 +50,9 @@ constexpr int kTok = kTreeTcTokens;        // tokens of a tile
 constexpr int kPages = kTok / kPageSize;   // pages of a tile
 constexpr int kGroupThreads = 128;         // a softmax group: one row per thread
 constexpr int kSoftThreads = 2 * kGroupThreads;
-constexpr int kMmaWarp = kSoftThreads / 32;
-constexpr int kCopyWarp = kMmaWarp + 1;    // copies K; the warp after it V
-constexpr int kConvWarp = kMmaWarp + 4;    // first of four (8-bit caches)
+constexpr int kMmaWarp = kSoftThreads / 32;  // two: MMAs of group 0's and of group 1's steps
+constexpr int kCopyWarp = kMmaWarp + 2;      // two: copies of K and of V
+constexpr int kConvWarp = kMmaWarp + 4;      // first of four (8-bit caches)
 constexpr int kConvThreads = 128;
 constexpr int kSBufs = 3;
 // tensor memory columns: O of group 0 and 1, Q of the rows 0 .. 127 and 128 .. 255, S (then P)
@@ -181,7 +181,9 @@ __global__ void __launch_bounds__(TcShape<KV, D>::THREADS, 1) tree_tc_kernel(
   uint64_t* s_done = raw_freed + NR;                                 // [3] S in its buffer
   uint64_t* p_ready = s_done + kSBufs;                               // [3] P in its buffer
   uint64_t* pv_done = p_ready + kSBufs;                              // [3] that P V complete
-  uint64_t* q_ready = pv_done + kSBufs;                              // Q of a unit stored
+  // Q of a unit stored; the MMA warps arrive too, for the unit after the one they have seen, so
+  // that no phase completes before both have seen the last (one may have no step in a unit)
+  uint64_t* q_ready = pv_done + kSBufs;
   uint64_t* o_read = q_ready + 1;                                    // O of a unit read
   uint64_t* mma_idle = o_read + 1;
   int* page_mask = reinterpret_cast<int*>(smem + S::OFF_MISC);       // [NV] good pages of the tile
@@ -196,11 +198,11 @@ __global__ void __launch_bounds__(TcShape<KV, D>::THREADS, 1) tree_tc_kernel(
   if (threadIdx.x == kCopyWarp * 32) {
     for (int s = 0; s < NK; ++s) {
       mbar_init(&full_k[s], W8 ? kConvThreads / 32 : 1);
-      mbar_init(&free_k[s], 1);
+      mbar_init(&free_k[s], 2);
     }
     for (int s = 0; s < NV; ++s) {
       mbar_init(&full_v[s], W8 ? kConvThreads / 32 : 1);
-      mbar_init(&free_v[s], 1);
+      mbar_init(&free_v[s], 2);
     }
     for (int s = 0; s < NR; ++s) {
       mbar_init(&raw_full[s], 2);
@@ -211,9 +213,9 @@ __global__ void __launch_bounds__(TcShape<KV, D>::THREADS, 1) tree_tc_kernel(
       mbar_init(&p_ready[s], kGroupThreads / 32);
       mbar_init(&pv_done[s], 1);
     }
-    mbar_init(q_ready, kSoftThreads / 32);
+    mbar_init(q_ready, kSoftThreads / 32 + 2);
     mbar_init(o_read, kSoftThreads / 32);
-    mbar_init(mma_idle, 1);
+    mbar_init(mma_idle, 2);
     mbar_fence_init();
     if constexpr (!W8) {
       asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm_k)) : "memory");
@@ -313,78 +315,88 @@ __global__ void __launch_bounds__(TcShape<KV, D>::THREADS, 1) tree_tc_kernel(
       if (lane == 0)  // before leaving, every copy issued has landed
         for (int t = max(0, issued - stages); t < issued; ++t)
           mbar_wait(&there[t % stages], (uint32_t)(t / stages) & 1u, a.err);
-    } else if (warp == kMmaWarp) {
+    } else {
       // ===================== MMAs (one elected lane issues) =====================
+      // Two warps, one for each softmax group's steps: issuing a step's MMAs and waiting for its
+      // P V takes about as long as they run, so one warp's waits overlap the other's MMAs.
+      const int w = warp - kMmaWarp;
       const uint64_t k_desc = tc_desc(ring, 16, 1024), v_desc = tc_desc(ring + S::OFF_V, 2048, 1024);
+      const uint32_t o = tmem + kColO + 128 * w;
       bool ok = true;
       uint32_t ph = 0, unit = 0;
-      Place<NK> ks;  // tile of the next S
-      Place<NV> vs;  // tile of the next P V
+      Place<NK> k_base;  // the run's first tile
+      Place<NV> v_base;
       auto wait = [&](uint64_t* bar, uint32_t par) {
         const bool got = __all_sync(0xffffffffu, mbar_wait(bar, par, a.err));
         tc_fence_after();
         return got;
       };
-      while (ok && walk.next(a, run)) {
+      if (elect_one()) mbar_arrive(q_ready);
+      __syncwarp();
+      for (; ok && walk.next(a, run); ++unit) {
+        const int tiles = uniform(run.n);
         const bool wide = uniform(run.rows) > kGroupThreads;
-        const int n = uniform(wide ? 2 * run.n : run.n);
+        const int n = wide ? 2 * tiles : tiles, stride = wide ? 1 : 2;  // tiles between steps
+        Place<NK> ks = k_base;  // K of the next S
+        Place<NV> vs = v_base;  // V of the next P V
+        if (!wide) {
+          ks.advance(w);
+          vs.advance(w);
+        }
+        const uint32_t q = tmem + kColQ + (wide ? 64 * w : 0);
         ok = wait(q_ready, unit & 1);
-        ++unit;
-        bool odd = false;  // the next S's step
+        if (elect_one()) mbar_arrive(q_ready);  // (the next unit's: this phase has been seen)
+        __syncwarp();
         auto s_mma = [&](int buf) {
-          if (!(wide && odd) && !wait(&full_k[ks.st], ks.par)) return false;
+          if (!wait(&full_k[ks.st], ks.par)) return false;
           const uint64_t kd = k_desc + (uint32_t)(ks.st * (S::TILE >> 4));
-          const uint32_t q = tmem + kColQ + (wide && odd ? 64 : 0), d = tmem + s_col(buf);
-          const bool tile_done = !wide || odd;
+          const uint32_t d = tmem + s_col(buf);
           if (elect_one()) {
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk)
               tc_mma_ta(d, q + 8 * kk, kd + (((kk >> 2) * (kTok * 128) + (kk & 3) * 32) >> 4),
                         S::IDESC_S, kk > 0 ? 1u : 0u);
             tc_commit(&s_done[buf]);
-            if (tile_done) tc_commit(&free_k[ks.st]);
           }
           __syncwarp();
-          if (tile_done) ks.advance(1);
-          odd = !odd;
+          ks.advance(stride);
           return true;
         };
-        // S runs two steps ahead of P V. Its buffer held P of an earlier step, whose P V must be
-        // complete: with three buffers that of the step before this one, which is (the wait costs
-        // nothing); with two that of this step.
-        for (int u = 0; ok && u < 2 && u < n; ++u) ok = s_mma(u);
-        Buf b{0, 0}, before{0, 0}, ahead{2, 0};
-        if (wide) ahead.i = 0;
-        for (int u = 0; ok && u < n; ++u) {
+        Buf b{w, 0}, before{w - 1, 0}, ahead{w, 0};
+        if (ok && w < n) ok = s_mma(w);
+        ahead.advance(wide, 2);
+        for (int u = w; ok && u < n; u += 2) {
           const uint32_t par = b.parity(ph);
           ok = wait(&p_ready[b.i], par);
-          if (ok && u == 0 && unit > 1) ok = wait(o_read, unit & 1);  // (of the last unit)
+          if (ok && u < 2 && unit > 0) ok = wait(o_read, (unit - 1) & 1);  // (of the last unit)
           if (!ok) break;
           const uint64_t vd = v_desc + (uint32_t)(vs.st * (S::TILE >> 4));
-          const uint32_t o = tmem + kColO + ((u & 1) << 7), pc = tmem + s_col(b.i);
-          const bool tile_done = !wide || (u & 1);
+          const uint32_t pc = tmem + s_col(b.i);
           if (elect_one()) {
 #pragma unroll
             for (int kk = 0; kk < kPages; ++kk)
               tc_mma_ta(o, pc + 8 * kk, vd + ((kk * PAGE_MMA) >> 4), S::IDESC_PV,
                         u < 2 && kk == 0 ? 0u : 1u);
             tc_commit(&pv_done[b.i]);
-            if (tile_done) tc_commit(&free_v[vs.st]);
           }
           __syncwarp();
-          if (tile_done) vs.advance(1);
+          vs.advance(stride);
           if (u + 2 < n) {
+            // the next S overwrites the buffer of an earlier P, whose P V must be complete: of this
+            // step with two buffers, of the step before it with three
             if (wide)
               ok = wait(&pv_done[b.i], par);
             else if (u > 0)
               ok = wait(&pv_done[before.i], before.parity(ph));
             if (ok) ok = s_mma(ahead.i);
           }
-          before = b;
-          b.advance(wide, 1);
-          ahead.advance(wide, 1);
+          b.advance(wide, 2);
+          ahead.advance(wide, 2);
+          before.advance(wide, 2);
         }
         ph = after_steps(ph, wide, n);
+        k_base.skip(tiles);
+        v_base.skip(tiles);
       }
       if (elect_one()) tc_commit(mma_idle);  // before leaving, every MMA issued is complete
       __syncwarp();
@@ -475,7 +487,8 @@ __global__ void __launch_bounds__(TcShape<KV, D>::THREADS, 1) tree_tc_kernel(
     const uint32_t lane_t = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     bool ok = true;
     uint32_t ph = 0, unit = 0;
-    Place<NV> base;  // V of the run's first tile
+    Place<NV> base;  // V and K of the run's first tile
+    Place<NK> k_base;
     // The row of this thread in a run (row `row` of its unit, node t, query head `head`) and its
     // score factor.
     struct Row {
@@ -567,18 +580,35 @@ __global__ void __launch_bounds__(TcShape<KV, D>::THREADS, 1) tree_tc_kernel(
       uint32_t* const bad = bad_nodes + 8 * (unit & 1);
       float m_used = -INFINITY, l = 0.f;
       Place<NV> at = base;
-      if (!wide) at.advance(wg);
-      Buf bf{wg, 0};
+      Place<NK> k_at = k_base;
+      if (!wide) {
+        at.advance(wg);
+        k_at.advance(wg);
+      }
+      int v_prev = 0;
+      Buf bf{wg, 0}, other{wg - 1, 0};  // S buffers of this step and of the step before it
       int prev_buf = 0;         // this group's last step
       uint32_t prev_par = 0;
       int p0 = (run.tile0 + (wide ? 0 : wg)) * kTok;
       const int seen_by_all = min(run.req.base, run.req.read) - kTok;
       for (int u = wg; ok && u < n; u += 2) {
         const uint32_t par = bf.parity(ph);
-        // (V of the tile too: the MMA warp takes a P as the word that it is there)
-        ok = mbar_wait(&full_v[at.st], at.par, a.err) && mbar_wait(&s_done[bf.i], par, a.err);
+        // V of the tile too: the MMA warp takes a P as the word that it is there. A narrow unit's
+        // buffers go round between the groups: a group waits for every S in order, the other's too,
+        // so that the phase it waits for is never the one after the next.
+        ok = mbar_wait(&full_v[at.st], at.par, a.err) &&
+             (wide || u == 0 || mbar_wait(&s_done[other.i], other.parity(ph), a.err)) &&
+             mbar_wait(&s_done[bf.i], par, a.err);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
+        if ((warp & 3) == 0 && lane == 0) {
+          // this tile's K is used up (a wide unit's once both groups say so), and the V of the
+          // group's tile before it too: its P V came before this S
+          mbar_arrive_n(&free_k[k_at.st], wide ? 1 : 2);
+          if (u > 1) mbar_arrive_n(&free_v[v_prev], wide ? 1 : 2);
+        }
+        v_prev = at.st;
+        k_at.advance(wide ? 1 : 2);
         const int mask = page_mask[at.st];
         tc_fence_after();
         uint32_t sr[64];
@@ -595,7 +625,9 @@ __global__ void __launch_bounds__(TcShape<KV, D>::THREADS, 1) tree_tc_kernel(
 #pragma unroll
           for (int k = 0; k < 64; ++k)
             if (!((seen >> k) & 1)) sr[k] = __float_as_uint(-INFINITY);
-          if (!wide || wg == 0) {  // mend V: two threads to a row
+          {
+            // Mend V: two threads to a row. In a wide unit both groups do (and write every row they
+            // look at): each group's P V waits for its own group only.
             const int vr = r >> 1, pos = p0 + vr;
             constexpr int CH = D / 16;  // 16-byte chunks of half a row
             const uint32_t vrow = ring + S::OFF_V + at.st * S::TILE + (vr >> 4) * PAGE_MMA +
@@ -624,7 +656,7 @@ __global__ void __launch_bounds__(TcShape<KV, D>::THREADS, 1) tree_tc_kernel(
                     here = true;
                   }
                 }
-                if (here) sts128(xa, x);
+                if (here || wide) sts128(xa, x);
                 hot |= here;
               }
               if (hot) {
@@ -646,11 +678,8 @@ __global__ void __launch_bounds__(TcShape<KV, D>::THREADS, 1) tree_tc_kernel(
           m_used = mx;
         } else {
           const bool need = mx > m_used + kLazyLog2;
-          if (__any_sync(0xffffffffu, need)) {  // rescale this warp's rows of O (in TMEM)
-            ok = mbar_wait(&pv_done[prev_buf], prev_par, a.err);
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok) break;
-            tc_fence_after();
+          // rescale this warp's rows of O (in TMEM): the group's last P V came before this S
+          if (__any_sync(0xffffffffu, need)) {
             const float m_new = need ? mx : m_used;
             const float alpha = m_new == -INFINITY ? 1.f : exp2f(m_used - m_new);
 #pragma unroll
@@ -691,12 +720,15 @@ __global__ void __launch_bounds__(TcShape<KV, D>::THREADS, 1) tree_tc_kernel(
         prev_buf = bf.i;
         prev_par = par;
         bf.advance(wide, 2);
+        other.advance(wide, 2);
         at.advance(wide ? 1 : 2);
         p0 += wide ? kTok : 2 * kTok;
       }
       // ---- the unit's rows ----
       if (ok && wg < n) ok = mbar_wait(&pv_done[prev_buf], prev_par, a.err);
       ok = __all_sync(0xffffffffu, ok);
+      if (ok && wg < n && (warp & 3) == 0 && lane == 0)
+        mbar_arrive_n(&free_v[v_prev], wide ? 1 : 2);
       tc_fence_after();
       if (!wide) ml[wg * kGroupThreads + r] = make_float2(m_used, l);
       tc_fence_before();
@@ -797,6 +829,7 @@ __global__ void __launch_bounds__(TcShape<KV, D>::THREADS, 1) tree_tc_kernel(
       if (lane == 0) mbar_arrive(o_read);
       ph = after_steps(ph, wide, n);
       base.skip(run.n);
+      k_base.skip(run.n);
     }
   }
 
