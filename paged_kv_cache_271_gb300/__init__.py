@@ -16,6 +16,7 @@ for drafted tokens ``qk_norm_rope_append``, ``tree_masks``, ``tree_decode_attent
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import numpy as np
@@ -687,20 +688,57 @@ def rope_table(max_positions: int, rot_dim: int, base: float = 10000.0,
     return torch.cat([angle.cos(), angle.sin()], dim=-1).float()
 
 
-def _token_rows(t: torch.Tensor, name: str, heads=None, dim=None):
+# The calls below run once per layer and step, where a small call's time is this file's: they read
+# the current device once and take addresses as integers. _dev says what is wrong with a tensor.
+
+def _addr(t, name, dev: int) -> int:
+    """Address of a contiguous tensor on device ``dev`` (the current one)."""
+    if isinstance(t, torch.Tensor) and t.get_device() == dev and t.is_contiguous():
+        return t.data_ptr()
+    return _dev(t, name).value
+
+
+def _opt_addr(t, name, dev: int):
+    return None if t is None else _addr(t, name, dev)
+
+
+def _raw_stream(stream, dev: int) -> int:
+    if stream is None:
+        return torch.cuda.current_stream(dev).cuda_stream
+    return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
+
+
+@functools.lru_cache(maxsize=256)
+def _pool_desc(shape, dtype) -> _Desc:
+    """cache_desc of pools of this shape and type (never changed: shared between calls)."""
+    if len(shape) != 4:
+        raise PkvError(-2, "pool must be [num_pages, num_kv_heads, page_size, head_dim]")
+    n, h, p, d = shape
+    return _Desc(n, p, h, d, _dtype_code(torch.empty(0, dtype=dtype)))
+
+
+def _pools(k_cache, v_cache) -> _Desc:
+    if k_cache.shape != v_cache.shape or k_cache.dtype != v_cache.dtype:
+        raise PkvError(-2, "k_cache and v_cache differ")
+    return _pool_desc(k_cache.shape, k_cache.dtype)
+
+
+def _token_rows(t: torch.Tensor, name: str, dev: int, heads, dim: int):
     """Address and token stride (elements) of [N, heads, dim] rows, each token contiguous."""
     if not isinstance(t, torch.Tensor) or t.dim() != 3:
         raise PkvError(-2, "%s must be [tokens, heads, head_dim]" % name)
     n, h, d = t.shape
-    if (heads is not None and h != heads) or (dim is not None and d != dim):
+    if (heads is not None and h != heads) or d != dim:
         raise PkvError(-2, "%s must be [tokens, %s, %s], not %s" % (name, heads, dim,
                                                                     tuple(t.shape)))
     if n == 0:
         return None, h * d
-    if (d > 1 and t.stride(2) != 1) or (h > 1 and t.stride(1) != d):
+    s0, s1, s2 = t.stride()
+    if s2 != 1 or (h > 1 and s1 != d):
         raise PkvError(-1, "%s: a token's row must be contiguous" % name)
-    _dev(t[0], name)
-    return ctypes.c_void_p(t.data_ptr()), (t.stride(0) if n > 1 else h * d)
+    if t.get_device() != dev:
+        _dev(t[0], name)
+    return t.data_ptr(), (s0 if n > 1 else h * d)
 
 
 def qk_norm_rope_append(q, k, v, positions, slot_mapping, k_cache, v_cache, cos_sin,
@@ -711,42 +749,45 @@ def qk_norm_rope_append(q, k, v, positions, slot_mapping, k_cache, v_cache, cos_
     None: no rotation), K and V rows into their slots (pkv_qk_norm_rope_append). q [N, h_q, d],
     k, v [N, h_kv, d] may be slices of one tensor (tokens any stride apart). Returns the queries
     (``q_out``, which may be ``q``)."""
-    desc = cache_desc(k_cache)
-    if k_cache.shape != v_cache.shape or k_cache.dtype != v_cache.dtype:
-        raise PkvError(-2, "k_cache and v_cache differ")
-    if k.dtype != q.dtype or v.dtype != q.dtype:
+    desc = _pools(k_cache, v_cache)
+    dtype, d = q.dtype, desc.head_dim
+    if k.dtype != dtype or v.dtype != dtype:
         raise PkvError(-3, "q, k and v must have one dtype")
-    qp, qs = _token_rows(q, "q", dim=desc.head_dim)
-    kp, ks = _token_rows(k, "k", desc.num_kv_heads, desc.head_dim)
-    vp, vs = _token_rows(v, "v", desc.num_kv_heads, desc.head_dim)
+    dev = torch.cuda.current_device()
+    qp, qs = _token_rows(q, "q", dev, None, d)
+    kp, ks = _token_rows(k, "k", dev, desc.num_kv_heads, d)
+    vp, vs = _token_rows(v, "v", dev, desc.num_kv_heads, d)
     n, h_q, _ = q.shape
     if k.shape[0] != n or v.shape[0] != n or slot_mapping.numel() != n:
         raise PkvError(-2, "q, k, v and slot_mapping must have one length")
     if slot_mapping.dtype != torch.int64:
         raise PkvError(-3, "slot_mapping must be int64")
-    rot, most = 0, 0
+    rot = most = 0
+    table = pos = None
     if cos_sin is not None:
         if cos_sin.dim() != 2 or cos_sin.dtype != torch.float32:
             raise PkvError(-2, "cos_sin must be float32 [max_positions, rot_dim]")
         if positions.dtype != torch.int32 or positions.numel() != n:
             raise PkvError(-3, "positions must be int32, one per token")
         most, rot = cos_sin.shape
+        table, pos = _addr(cos_sin, "cos_sin", dev), _addr(positions, "positions", dev)
     for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-        if w is not None and (w.dtype != q.dtype or w.numel() != desc.head_dim):
+        if w is not None and (w.dtype != dtype or w.numel() != d):
             raise PkvError(-2, "%s must be [head_dim] of q's dtype" % name)
     _check_scales(desc, k_scales, v_scales)
     if q_out is None:
-        q_out = torch.empty((n, h_q, desc.head_dim), dtype=q.dtype, device=q.device)
-    elif q_out.dtype != q.dtype or q_out.shape != q.shape:
-        raise PkvError(-2, "q_out must match q in shape and dtype")
-    op, os_ = _token_rows(q_out, "q_out", h_q, desc.head_dim)
+        q_out = torch.empty((n, h_q, d), dtype=dtype, device=q.device)
+        op, os_ = q_out.data_ptr(), h_q * d
+    else:
+        if q_out.dtype != dtype or q_out.shape != q.shape:
+            raise PkvError(-2, "q_out must match q in shape and dtype")
+        op, os_ = _token_rows(q_out, "q_out", dev, h_q, d)
     _check(lib().pkv_qk_norm_rope_append(
-        qp, qs, kp, ks, vp, vs, _dtype_code(q), n, h_q, _opt(q_weight, "q_weight"),
-        _opt(k_weight, "k_weight"), float(eps), _opt(cos_sin, "cos_sin"), most, rot,
-        1 if interleaved else 0, None if cos_sin is None else _dev(positions, "positions"),
-        _dev(slot_mapping, "slot_mapping"), op, os_, _dev(k_cache, "k_cache"),
-        _dev(v_cache, "v_cache"), ctypes.byref(desc), _opt(k_scales, "k_scales"),
-        _opt(v_scales, "v_scales"), _stream(stream)))
+        qp, qs, kp, ks, vp, vs, _dtype_code(q), n, h_q, _opt_addr(q_weight, "q_weight", dev),
+        _opt_addr(k_weight, "k_weight", dev), eps, table, most, rot, 1 if interleaved else 0, pos,
+        _addr(slot_mapping, "slot_mapping", dev), op, os_, _addr(k_cache, "k_cache", dev),
+        _addr(v_cache, "v_cache", dev), desc, _opt_addr(k_scales, "k_scales", dev),
+        _opt_addr(v_scales, "v_scales", dev), _raw_stream(stream, dev)))
     return q_out
 
 
@@ -777,6 +818,7 @@ def tree_masks(parents):
     return masks, depths
 
 
+@functools.lru_cache(maxsize=256)
 def tree_decode_workspace_size(dtype_q, cache_dtype, batch, tree_width, num_q_heads, num_kv_heads,
                                head_dim, max_pages_per_seq) -> int:
     """Bytes of workspace of a tree_decode_attention call (dtypes as torch dtypes or codes)."""
@@ -801,37 +843,37 @@ def tree_decode_attention(q, k_cache, v_cache, block_tables, context_lens, scale
     B, T, h_q, d = q.shape
     if block_tables.dim() != 2 or block_tables.shape[0] != B or context_lens.numel() != B:
         raise PkvError(-2, "block_tables must be [batch, max_pages], context_lens [batch]")
-    desc = cache_desc(k_cache)
-    if k_cache.shape != v_cache.shape or k_cache.dtype != v_cache.dtype:
-        raise PkvError(-2, "k_cache and v_cache differ")
+    desc = _pools(k_cache, v_cache)
     if d != desc.head_dim:
         raise PkvError(-2, "q head_dim does not match the pool")
     if tree_lens is not None and (tree_lens.dtype != torch.int32 or tree_lens.numel() != B):
         raise PkvError(-3, "tree_lens must be int32 [batch]")
     stride = 0
     if tree_mask is not None:
-        if (tree_mask.dtype != torch.int64 or tree_mask.dim() != 3 or
-                tree_mask.shape[0] not in (1, B) or
-                tuple(tree_mask.shape[1:]) != (T, (T + 63) // 64)):
+        words = (T + 63) // 64
+        if (tree_mask.dtype != torch.int64 or
+                tree_mask.shape not in ((B, T, words), (1, T, words))):
             raise PkvError(-2, "tree_mask must be int64 [batch or 1, nodes, ceil(nodes / 64)]")
-        stride = 0 if tree_mask.shape[0] == 1 else T * tree_mask.shape[2]
+        stride = 0 if tree_mask.shape[0] == 1 else T * words
     _check_scales(desc, k_scales, v_scales)
     if out is None:
         out = (torch.empty_like if tree_lens is None else torch.zeros_like)(q)
     elif out.shape != q.shape or out.dtype != q.dtype:
         raise PkvError(-2, "out must match q in shape and dtype")
-    maxp = block_tables.shape[1]
+    dev = torch.cuda.current_device()
+    code, maxp = _dtype_code(q), block_tables.shape[1]
     if workspace is None:
-        need = tree_decode_workspace_size(_dtype_code(q), desc.cache_dtype, B, T, h_q,
-                                          desc.num_kv_heads, d, maxp)
+        need = tree_decode_workspace_size(code, desc.cache_dtype, B, T, h_q, desc.num_kv_heads, d,
+                                          maxp)
         workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
     _check(lib().pkv_tree_decode_attention(
-        _dev(q, "q"), _dtype_code(q), B, T, h_q, _dev(k_cache, "k_cache"),
-        _dev(v_cache, "v_cache"), ctypes.byref(desc), _dev(block_tables, "block_tables"), maxp,
-        _dev(context_lens, "context_lens"), _opt(tree_lens, "tree_lens"),
-        _opt(tree_mask, "tree_mask"), stride, float(scale), _opt(k_scales, "k_scales"),
-        _opt(v_scales, "v_scales"), _dev(out, "out"), _dev(workspace, "workspace"),
-        workspace.numel() * workspace.element_size(), _stream(stream)))
+        _addr(q, "q", dev), code, B, T, h_q, _addr(k_cache, "k_cache", dev),
+        _addr(v_cache, "v_cache", dev), desc, _addr(block_tables, "block_tables", dev), maxp,
+        _addr(context_lens, "context_lens", dev), _opt_addr(tree_lens, "tree_lens", dev),
+        _opt_addr(tree_mask, "tree_mask", dev), stride, scale,
+        _opt_addr(k_scales, "k_scales", dev), _opt_addr(v_scales, "v_scales", dev),
+        _addr(out, "out", dev), _addr(workspace, "workspace", dev),
+        workspace.numel() * workspace.element_size(), _raw_stream(stream, dev)))
     return out
 
 
@@ -840,27 +882,26 @@ def tree_commit(k_cache, v_cache, block_tables, context_lens, tree_lens, path, p
     """Keeps an accepted path of each request's draft: its nodes' rows path[b, :path_lens[b]] move
     together behind the committed rows (pkv_tree_commit). Returns the requests' new lengths (int32
     [B] on the device); the request table follows with ``truncate``."""
-    for t, name in ((block_tables, "block_tables"), (context_lens, "context_lens"),
-                    (tree_lens, "tree_lens"), (path, "path"), (path_lens, "path_lens")):
+    ints = ((block_tables, "block_tables"), (context_lens, "context_lens"),
+            (tree_lens, "tree_lens"), (path, "path"), (path_lens, "path_lens"))
+    for t, name in ints:
         if t.dtype != torch.int32:
             raise PkvError(-3, "%s must be int32" % name)
     B = context_lens.numel()
     if (block_tables.dim() != 2 or block_tables.shape[0] != B or path.dim() != 2 or
             path.shape[0] != B or tree_lens.numel() != B or path_lens.numel() != B):
         raise PkvError(-2, "block_tables and path must be [batch, n], the lengths [batch]")
-    desc = cache_desc(k_cache)
-    if k_cache.shape != v_cache.shape or k_cache.dtype != v_cache.dtype:
-        raise PkvError(-2, "k_cache and v_cache differ")
+    desc = _pools(k_cache, v_cache)
     if new_lens is None:
         new_lens = torch.empty(B, dtype=torch.int32, device=k_cache.device)
     elif new_lens.dtype != torch.int32 or new_lens.numel() != B:
         raise PkvError(-2, "new_lens must be int32 [batch]")
+    dev = torch.cuda.current_device()
+    bt, cl, tl, pa, pl = (_addr(t, name, dev) for t, name in ints)
     _check(lib().pkv_tree_commit(
-        _dev(k_cache, "k_cache"), _dev(v_cache, "v_cache"), ctypes.byref(desc),
-        _dev(block_tables, "block_tables"), block_tables.shape[1],
-        _dev(context_lens, "context_lens"), _dev(tree_lens, "tree_lens"), _dev(path, "path"),
-        _dev(path_lens, "path_lens"), B, path.shape[1], _dev(new_lens, "new_lens"),
-        _stream(stream)))
+        _addr(k_cache, "k_cache", dev), _addr(v_cache, "v_cache", dev), desc, bt,
+        block_tables.shape[1], cl, tl, pa, pl, B, path.shape[1],
+        _addr(new_lens, "new_lens", dev), _raw_stream(stream, dev)))
     return new_lens
 
 
