@@ -9,10 +9,12 @@
 // The query row goes to q_out; the key row, and the value row unchanged, to the token's cache
 // slot, rounded once from fp32 (FP8 / INT8: the code of the fp32 quotient by the head's scale).
 //
-// The pass is bound by memory: every row is read once and written once, about ten operations a
-// value. A row is held by LPR lanes of a warp, 16 bytes each, so its sum of squares is a shuffle
-// reduction inside the row's lanes and the rotation's partner values come by one shuffle (R/2
-// dims is a whole number of lanes) or sit in the same lane (interleaved).
+// The pass is bound by memory -- every row is read once and written once -- as long as the dozen
+// operations a value are not many more instructions. A row is held by D / VEC lanes of a warp, and
+// each lane holds both values of its pairs: for halves i and i + R/2 two 8-byte chunks R/2 apart
+// (past the rotated dims, two neighbouring ones), so that the rotation needs no shuffle and the sum
+// of squares is the only reduction. What does not change from token to token (a row's kind, its
+// addresses, its head's scale, the weights) is worked out once per block.
 #include <algorithm>
 #include <math.h>
 
@@ -25,175 +27,263 @@ namespace pkv {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kWave = 152 * 3;  // blocks resident at once (three on each SM)
 
 template <typename TIN, int D>
 struct RowShape {
-  static constexpr int VEC = Vec16<TIN>::N;
+  static constexpr int VEC = Vec16<TIN>::N;     // values of a lane
+  static constexpr int CH = VEC / 2;            // values of a chunk (8 bytes)
   static constexpr int LPR = D / VEC;           // lanes of a row
   static constexpr int ROWS = kThreads / LPR;   // rows a block takes at a time
 };
 
-__device__ __forceinline__ uint4 pack_vec(const float (&y)[8]) {
-  uint4 v;
-  uint32_t* w = &v.x;
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const __nv_bfloat162 p = __floats2bfloat162_rn(y[2 * k], y[2 * k + 1]);
-    w[k] = *reinterpret_cast<const uint32_t*>(&p);
-  }
-  return v;
+__device__ __forceinline__ void widen(const uint2& v, float (&o)[4]) {
+  o[0] = bf16lo(v.x);
+  o[1] = bf16hi(v.x);
+  o[2] = bf16lo(v.y);
+  o[3] = bf16hi(v.y);
 }
-__device__ __forceinline__ uint4 pack_vec(const float (&y)[4]) {
-  return make_uint4(__float_as_uint(y[0]), __float_as_uint(y[1]), __float_as_uint(y[2]),
-                    __float_as_uint(y[3]));
+__device__ __forceinline__ void widen(const uint2& v, float (&o)[2]) {
+  o[0] = __uint_as_float(v.x);
+  o[1] = __uint_as_float(v.y);
+}
+__device__ __forceinline__ uint2 narrow(const float (&y)[4]) {
+  const __nv_bfloat162 a = __floats2bfloat162_rn(y[0], y[1]), b = __floats2bfloat162_rn(y[2], y[3]);
+  return make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+}
+__device__ __forceinline__ uint2 narrow(const float (&y)[2]) {
+  return make_uint2(__float_as_uint(y[0]), __float_as_uint(y[1]));
 }
 
-// One 16-byte vector (column cl of a row) of a K or V row into its pool row. Rows that were
-// computed in fp32 are divided as such (float: always the IEEE division); unchanged rows of bf16
-// input as the quantising append divides them.
-template <typename TDIV, int CACHE, int VEC>
-__device__ __forceinline__ void store_cache(void* pool, int64_t row, int D, int cl, float scale,
-                                            const float (&y)[VEC]) {
-  const int64_t at = row * D + cl * VEC;
+// The codes of N values. Rows that were computed in fp32 are divided as such (TDIV float: always
+// the IEEE division), unchanged rows of bf16 input as the quantising append divides them.
+template <typename TDIV, int CACHE, int N>
+__device__ __forceinline__ uint32_t codes_of(const float (&y)[N], const KnownDivisor& d) {
+  float q[N];
+  const bool slow = divide_vec<TDIV, N>(y, d, q);
+  uint32_t w = 0;
   if constexpr (CACHE == PKV_FP8_E4M3) {
-    quantize_store<TDIV, VEC>(y, known_divisor(scale), static_cast<uint8_t*>(pool) + at);
-  } else if constexpr (CACHE == PKV_INT8) {
-    quantize_store_int8<TDIV, VEC>(y, known_divisor(scale), static_cast<uint8_t*>(pool) + at);
+#pragma unroll
+    for (int k = 0; k < N / 2; ++k)
+      w |= (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(q[2 * k], q[2 * k + 1]), __NV_SATFINITE,
+                                              __NV_E4M3)
+           << (16 * k);
   } else {
-    constexpr int EB = CACHE == PKV_F32 ? 4 : 2;
-    *reinterpret_cast<uint4*>(static_cast<uint8_t*>(pool) + at * EB) = pack_vec(y);
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      if (slow) q[k] = q[k] == q[k] ? q[k] : 0.f;
+      w |= (int8_code_bits(q[k]) & 0xffu) << (8 * k);
+    }
+  }
+  return w;
+}
+
+// A chunk of a K or V row into its pool row at element `at`.
+template <typename TDIV, int CACHE, int N>
+__device__ __forceinline__ void store_chunk(void* pool, int64_t at, const KnownDivisor& d,
+                                            const float (&y)[N]) {
+  if constexpr (CACHE == PKV_F32 || CACHE == PKV_BF16) {
+    *reinterpret_cast<uint2*>(static_cast<uint8_t*>(pool) + at * (8 / N)) = narrow(y);
+  } else {
+    const uint32_t w = codes_of<TDIV, CACHE, N>(y, d);
+    uint8_t* p = static_cast<uint8_t*>(pool) + at;
+    if constexpr (N == 4)
+      *reinterpret_cast<uint32_t*>(p) = w;
+    else
+      *reinterpret_cast<uint16_t*>(p) = (uint16_t)w;
   }
 }
 
-// A block takes one token and the row groups blockIdx.y, blockIdx.y + gridDim.y, ... of its
-// h_q + 2 h_kv rows (queries, keys, values), ROWS rows at a time. A lane keeps its columns, so
-// the token's cos and sin of those columns are read once.
-template <typename TIN, int CACHE, int D>
-__global__ void __launch_bounds__(kThreads) qk_norm_rope_append_kernel(const NormRopeArgs a) {
+// Row groups of a token a block takes at most; a token of more is shared by `parts` blocks (block
+// b always takes part b % parts). The next token's rows, position and slot are on their way while
+// this one's are worked on, its cos and sin right after.
+constexpr int kGroups = 3;
+
+template <typename TIN, int CACHE, int D, bool INTER>
+__global__ void __launch_bounds__(kThreads, 3) qk_norm_rope_append_kernel(const NormRopeArgs a,
+                                                                          int parts, int groups) {
   using S = RowShape<TIN, D>;
-  constexpr int VEC = S::VEC, LPR = S::LPR, ROWS = S::ROWS;
-  const int64_t n = blockIdx.x;
-  const int lane = threadIdx.x & 31, cl = threadIdx.x % LPR, rl = threadIdx.x / LPR;
-  const int col = cl * VEC;
-  const int pos = a.rot_dim > 0 ? a.positions[n] : 0;
-  if (a.rot_dim > 0 && (pos < 0 || pos >= a.max_positions)) {  // the whole token is left out
-    if (threadIdx.x == 0 && blockIdx.y == 0) atomicOr(a.err, PKV_DEVERR_BAD_POSITION);
-    return;
-  }
-  int64_t slot = a.slots[n];
-  if (slot >= a.num_slots) {
-    if (threadIdx.x == 0 && blockIdx.y == 0) atomicOr(a.err, PKV_DEVERR_BAD_SLOT);
-    slot = -1;
-  }
-  const int64_t crow0 = (slot / kPageSize) * a.h_kv * kPageSize + slot % kPageSize;
-
-  // cos and sin of this lane's values; a value's partner is `far` lanes away (0: in this lane)
-  float cs[VEC], sn[VEC];
-  const int half = a.rot_dim / 2;
-  const bool turns = col < a.rot_dim;
-  int partner = lane;
-  if (turns) {
-    const float* row = a.cos_sin + (int64_t)pos * a.rot_dim;
-    if (a.interleaved) {
-#pragma unroll
-      for (int k = 0; k < VEC; ++k) {
-        cs[k] = row[(col + k) / 2];
-        sn[k] = row[half + (col + k) / 2];
-        if ((k & 1) == 0) sn[k] = -sn[k];
-      }
-    } else {
-      const bool upper = col >= half;
-      const int c0 = upper ? col - half : col;
-      partner = upper ? lane - half / VEC : lane + half / VEC;
-#pragma unroll
-      for (int k = 0; k < VEC; k += 4) {
-        const float4 c4 = *reinterpret_cast<const float4*>(row + c0 + k);
-        const float4 s4 = *reinterpret_cast<const float4*>(row + half + c0 + k);
-        cs[k] = c4.x; cs[k + 1] = c4.y; cs[k + 2] = c4.z; cs[k + 3] = c4.w;
-        sn[k] = upper ? s4.x : -s4.x;
-        sn[k + 1] = upper ? s4.y : -s4.y;
-        sn[k + 2] = upper ? s4.z : -s4.z;
-        sn[k + 3] = upper ? s4.w : -s4.w;
-      }
-    }
-  } else {
-#pragma unroll
-    for (int k = 0; k < VEC; ++k) {
-      cs[k] = 1.f;
-      sn[k] = 0.f;
-    }
-  }
-
+  constexpr int CH = S::CH, LPR = S::LPR, ROWS = S::ROWS, VEC = S::VEC;
+  const int cl = threadIdx.x % LPR, rl = threadIdx.x / LPR;
   const int h_q = a.h_q, h_kv = a.h_kv, rows = h_q + 2 * h_kv;
-  for (int r0 = blockIdx.y * ROWS; r0 < rows; r0 += gridDim.y * ROWS) {
-    const int r = r0 + rl;
-    // 0 query, 1 key, 2 value, 3 nothing to do
-    const int kind = r >= rows ? 3 : r >= h_q + h_kv ? 2 : r >= h_q ? 1 : 0;
-    const bool live = kind == 0 || (kind < 3 && slot >= 0);
-    const int h = kind == 0 ? r : kind == 1 ? r - h_q : r - h_q - h_kv;
-    const TIN* src = kind == 0 ? static_cast<const TIN*>(a.q) + n * a.q_stride
-                   : kind == 1 ? static_cast<const TIN*>(a.k) + n * a.k_stride
-                               : static_cast<const TIN*>(a.v) + n * a.v_stride;
-    uint4 raw = make_uint4(0, 0, 0, 0);
-    if (live) raw = __ldcs(reinterpret_cast<const uint4*>(src + (int64_t)h * D + col));
-    float x[VEC];
-    Vec16<TIN>::load(&raw, x);
-    if (kind == 2) {
-      if (live)
-        store_cache<TIN, CACHE, VEC>(a.v_cache, crow0 + (int64_t)h * kPageSize, D, cl,
-                                     a.v_scales ? a.v_scales[h] : 1.f, x);
+  const int half = a.rot_dim / 2;
+  // this lane's two chunks of a row, and the first of its columns in the table's halves
+  const bool turns = cl * VEC < a.rot_dim;
+  const int ca = turns ? cl * CH : a.rot_dim + (cl * VEC - a.rot_dim);
+  const int cb = turns ? ca + half : ca + CH;
+  __shared__ float weights[3][D];  // of queries, of keys, ones
+  for (int i = threadIdx.x; i < D; i += kThreads) {
+    weights[0][i] = a.q_weight ? load_as_float(static_cast<const TIN*>(a.q_weight), i) : 1.f;
+    weights[1][i] = a.k_weight ? load_as_float(static_cast<const TIN*>(a.k_weight), i) : 1.f;
+    weights[2][i] = 1.f;
+  }
+  __syncthreads();
+
+  // this thread's rows: kind 0 query, 1 key, 2 value, 3 none
+  const int part = blockIdx.x % parts, row0 = part * groups * ROWS + rl;
+  int kind[kGroups], head[kGroups];
+  const TIN* src[kGroups];
+  KnownDivisor scale[kGroups];
+  bool norm[kGroups];
+#pragma unroll
+  for (int g = 0; g < kGroups; ++g) {
+    const int r = row0 + g * ROWS;
+    kind[g] = g >= groups || r >= rows ? 3 : r >= h_q + h_kv ? 2 : r >= h_q ? 1 : 0;
+    head[g] = kind[g] == 0 ? r : kind[g] == 1 ? r - h_q : kind[g] == 2 ? r - h_q - h_kv : 0;
+    src[g] = static_cast<const TIN*>(kind[g] == 0 ? a.q : kind[g] == 1 ? a.k : a.v) + head[g] * D;
+    norm[g] = kind[g] == 0 ? a.q_weight != nullptr : kind[g] == 1 && a.k_weight != nullptr;
+    if constexpr (CACHE == PKV_FP8_E4M3 || CACHE == PKV_INT8)
+      scale[g] = known_divisor(kind[g] == 1   ? a.k_scales[head[g]]
+                               : kind[g] == 2 ? a.v_scales[head[g]]
+                                              : 1.f);
+  }
+
+  struct Token {
+    int pos;
+    int64_t slot;
+    uint2 xa[kGroups], xb[kGroups];
+    float cs[CH], sn[CH];
+  };
+  auto load_rows = [&](int64_t n, Token& t) {
+#pragma unroll
+    for (int g = 0; g < kGroups; ++g) {
+      t.xa[g] = t.xb[g] = make_uint2(0, 0);
+      if (kind[g] == 3) continue;
+      const int64_t stride = kind[g] == 0 ? a.q_stride : kind[g] == 1 ? a.k_stride : a.v_stride;
+      const TIN* p = src[g] + n * stride;
+      t.xa[g] = __ldcs(reinterpret_cast<const uint2*>(p + ca));
+      t.xb[g] = __ldcs(reinterpret_cast<const uint2*>(p + cb));
     }
-    const TIN* w = static_cast<const TIN*>(kind == 0 ? a.q_weight : kind == 1 ? a.k_weight : nullptr);
-    float ss = 0.f;
+    t.pos = a.rot_dim > 0 ? a.positions[n] : 0;
+    t.slot = a.slots[n];
+  };
+  auto load_turn = [&](Token& t) {
 #pragma unroll
-    for (int k = 0; k < VEC; ++k) ss = fmaf(x[k], x[k], ss);
-#pragma unroll
-    for (int o = LPR / 2; o >= 1; o /= 2) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-    if (w) {
-      const float rstd = rsqrtf(fmaf(ss, 1.f / D, a.eps));
-      float wv[VEC];
-      Vec16<TIN>::load(w + col, wv);
-#pragma unroll
-      for (int k = 0; k < VEC; ++k) x[k] = x[k] * rstd * wv[k];
+    for (int e = 0; e < CH; ++e) {
+      t.cs[e] = 1.f;
+      t.sn[e] = 0.f;
     }
-    float y[VEC];
-    if (a.interleaved) {
+    if (!turns || t.pos < 0 || t.pos >= a.max_positions) return;
+    const float* row = a.cos_sin + (int64_t)t.pos * a.rot_dim;
+    if constexpr (INTER) {  // the pairs of chunk a, then of chunk b
 #pragma unroll
-      for (int k = 0; k < VEC; ++k) y[k] = fmaf(x[k], cs[k], x[k ^ 1] * sn[k]);
+      for (int e = 0; e < CH / 2; ++e) {
+        t.cs[e] = row[ca / 2 + e];
+        t.sn[e] = row[half + ca / 2 + e];
+        t.cs[CH / 2 + e] = row[cb / 2 + e];
+        t.sn[CH / 2 + e] = row[half + cb / 2 + e];
+      }
     } else {
 #pragma unroll
-      for (int k = 0; k < VEC; ++k) {
-        const float o = __shfl_sync(0xffffffffu, x[k], partner);
-        y[k] = fmaf(x[k], cs[k], o * sn[k]);
+      for (int e = 0; e < CH; e += 2) {
+        const float2 c = *reinterpret_cast<const float2*>(row + ca + e);
+        const float2 s = *reinterpret_cast<const float2*>(row + half + ca + e);
+        t.cs[e] = c.x;
+        t.cs[e + 1] = c.y;
+        t.sn[e] = s.x;
+        t.sn[e + 1] = s.y;
       }
     }
-    if (!turns) {  // (not x * 1 + o * 0: o may be infinite)
-#pragma unroll
-      for (int k = 0; k < VEC; ++k) y[k] = x[k];
+  };
+
+  const int64_t step = gridDim.x / parts;
+  int64_t n = blockIdx.x / parts;
+  Token cur, nxt;
+  load_rows(n, cur);
+  load_turn(cur);
+  for (; n < a.num_tokens; n += step) {
+    const bool more = n + step < a.num_tokens;
+    if (more) load_rows(n + step, nxt);
+    const bool left_out = a.rot_dim > 0 && (cur.pos < 0 || cur.pos >= a.max_positions);
+    int64_t slot = cur.slot;
+    if (left_out) {  // the whole token
+      if (threadIdx.x == 0 && part == 0) atomicOr(a.err, PKV_DEVERR_BAD_POSITION);
+    } else if (slot >= a.num_slots) {
+      if (threadIdx.x == 0 && part == 0) atomicOr(a.err, PKV_DEVERR_BAD_SLOT);
+      slot = -1;
     }
-    if (kind == 0)
-      *reinterpret_cast<uint4*>(static_cast<TIN*>(a.q_out) + n * a.q_out_stride + (int64_t)h * D +
-                                col) = pack_vec(y);
-    else if (kind == 1 && live)
-      store_cache<float, CACHE, VEC>(a.k_cache, crow0 + (int64_t)h * kPageSize, D, cl,
-                                     a.k_scales ? a.k_scales[h] : 1.f, y);
+    const int64_t crow0 = (slot / kPageSize) * h_kv * kPageSize + slot % kPageSize;
+#pragma unroll
+    for (int g = 0; g < kGroups; ++g) {
+      if (left_out || g >= groups) break;  // (uniform over the block)
+      float xa[CH], xb[CH];
+      widen(cur.xa[g], xa);
+      widen(cur.xb[g], xb);
+      const int64_t at = (crow0 + (int64_t)head[g] * kPageSize) * D;
+      if (kind[g] == 2 && slot >= 0) {
+        store_chunk<TIN, CACHE, CH>(a.v_cache, at + ca, scale[g], xa);
+        store_chunk<TIN, CACHE, CH>(a.v_cache, at + cb, scale[g], xb);
+      }
+      if (__all_sync(0xffffffffu, kind[g] >= 2)) continue;
+      float ss = 0.f;
+#pragma unroll
+      for (int e = 0; e < CH; ++e) ss = fmaf(xa[e], xa[e], fmaf(xb[e], xb[e], ss));
+#pragma unroll
+      for (int o = LPR / 2; o >= 1; o /= 2) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+      const float rstd = norm[g] ? rsqrtf(fmaf(ss, 1.f / D, a.eps)) : 1.f;
+      const float* w = weights[kind[g] < 2 ? kind[g] : 2];
+#pragma unroll
+      for (int e = 0; e < CH; ++e) {
+        xa[e] *= rstd * w[ca + e];
+        xb[e] *= rstd * w[cb + e];
+      }
+      if (turns) {
+        if constexpr (INTER) {
+#pragma unroll
+          for (int e = 0; e < CH; e += 2) {
+            const float a0 = xa[e], a1 = xa[e + 1], b0 = xb[e], b1 = xb[e + 1];
+            const float ac = cur.cs[e / 2], as = cur.sn[e / 2];
+            const float bc = cur.cs[CH / 2 + e / 2], bs = cur.sn[CH / 2 + e / 2];
+            xa[e] = fmaf(a0, ac, -(a1 * as));
+            xa[e + 1] = fmaf(a1, ac, a0 * as);
+            xb[e] = fmaf(b0, bc, -(b1 * bs));
+            xb[e + 1] = fmaf(b1, bc, b0 * bs);
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < CH; ++e) {
+            const float f = xa[e], s = xb[e];
+            xa[e] = fmaf(f, cur.cs[e], -(s * cur.sn[e]));
+            xb[e] = fmaf(s, cur.cs[e], f * cur.sn[e]);
+          }
+        }
+      }
+      if (kind[g] == 0) {
+        TIN* out = static_cast<TIN*>(a.q_out) + n * a.q_out_stride + head[g] * D;
+        *reinterpret_cast<uint2*>(out + ca) = narrow(xa);
+        *reinterpret_cast<uint2*>(out + cb) = narrow(xb);
+      } else if (kind[g] == 1 && slot >= 0) {
+        store_chunk<float, CACHE, CH>(a.k_cache, at + ca, scale[g], xa);
+        store_chunk<float, CACHE, CH>(a.k_cache, at + cb, scale[g], xb);
+      }
+    }
+    if (more) {
+      load_turn(nxt);
+      cur = nxt;
+    }
   }
+}
+
+template <typename TIN, int CACHE, int D>
+cudaError_t launch_d(const NormRopeArgs& a, cudaStream_t s) {
+  constexpr int R = RowShape<TIN, D>::ROWS;
+  const int all = (a.h_q + 2 * a.h_kv + R - 1) / R;  // row groups of a token
+  // few tokens: a block for every group; otherwise the fewest near-equal parts of <= kGroups
+  int parts = (int64_t)a.num_tokens * all <= kWave ? all : (all + kGroups - 1) / kGroups;
+  const int groups = (all + parts - 1) / parts;
+  parts = (all + groups - 1) / groups;
+  const int64_t tokens = std::min<int64_t>(a.num_tokens, std::max(1, kWave / parts));
+  const int grid = (int)(tokens * parts);
+  if (a.interleaved)
+    qk_norm_rope_append_kernel<TIN, CACHE, D, true><<<grid, kThreads, 0, s>>>(a, parts, groups);
+  else
+    qk_norm_rope_append_kernel<TIN, CACHE, D, false><<<grid, kThreads, 0, s>>>(a, parts, groups);
+  return cudaGetLastError();
 }
 
 template <typename TIN, int CACHE>
 cudaError_t launch_t(const NormRopeArgs& a, cudaStream_t s) {
-  const int rows = a.h_q + 2 * a.h_kv;
-  auto go = [&](auto kern, int rows_per_pass) {
-    const int passes = (rows + rows_per_pass - 1) / rows_per_pass;
-    // few tokens: a block for every pass of a token; many: a block for every token
-    const int split = std::min<int64_t>(passes, std::max<int64_t>(1, 152 * 8 / a.num_tokens));
-    kern<<<dim3(a.num_tokens, split), kThreads, 0, s>>>(a);
-  };
-  if (a.head_dim == 64)
-    go(qk_norm_rope_append_kernel<TIN, CACHE, 64>, RowShape<TIN, 64>::ROWS);
-  else
-    go(qk_norm_rope_append_kernel<TIN, CACHE, 128>, RowShape<TIN, 128>::ROWS);
-  return cudaGetLastError();
+  return a.head_dim == 64 ? launch_d<TIN, CACHE, 64>(a, s) : launch_d<TIN, CACHE, 128>(a, s);
 }
 
 }  // namespace
