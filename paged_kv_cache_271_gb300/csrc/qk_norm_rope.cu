@@ -47,6 +47,18 @@ __device__ __forceinline__ void widen(const uint2& v, float (&o)[2]) {
   o[0] = __uint_as_float(v.x);
   o[1] = __uint_as_float(v.y);
 }
+__device__ __forceinline__ void vec_load(const float* p, float (&o)[4]) {  // (16-byte aligned)
+  const float4 v = *reinterpret_cast<const float4*>(p);
+  o[0] = v.x;
+  o[1] = v.y;
+  o[2] = v.z;
+  o[3] = v.w;
+}
+__device__ __forceinline__ void vec_load(const float* p, float (&o)[2]) {
+  const float2 v = *reinterpret_cast<const float2*>(p);
+  o[0] = v.x;
+  o[1] = v.y;
+}
 __device__ __forceinline__ uint2 narrow(const float (&y)[4]) {
   const __nv_bfloat162 a = __floats2bfloat162_rn(y[0], y[1]), b = __floats2bfloat162_rn(y[2], y[3]);
   return make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
@@ -111,7 +123,7 @@ __global__ void __launch_bounds__(kThreads, 3) qk_norm_rope_append_kernel(const 
   const bool turns = cl * VEC < a.rot_dim;
   const int ca = turns ? cl * CH : a.rot_dim + (cl * VEC - a.rot_dim);
   const int cb = turns ? ca + half : ca + CH;
-  __shared__ float weights[3][D];  // of queries, of keys, ones
+  __shared__ alignas(16) float weights[3][D];  // of queries, of keys, ones
   for (int i = threadIdx.x; i < D; i += kThreads) {
     weights[0][i] = a.q_weight ? load_as_float(static_cast<const TIN*>(a.q_weight), i) : 1.f;
     weights[1][i] = a.k_weight ? load_as_float(static_cast<const TIN*>(a.k_weight), i) : 1.f;
@@ -119,24 +131,37 @@ __global__ void __launch_bounds__(kThreads, 3) qk_norm_rope_append_kernel(const 
   }
   __syncthreads();
 
-  // this thread's rows: kind 0 query, 1 key, 2 value, 3 none
+  // This thread's rows: kind 0 query, 1 key, 2 value, 3 none. Addresses are of chunk a; chunk b lies
+  // `over` elements behind it.
   const int part = blockIdx.x % parts, row0 = part * groups * ROWS + rl;
-  int kind[kGroups], head[kGroups];
+  const int over = cb - ca;
+  const int64_t step = gridDim.x / parts, n0 = blockIdx.x / parts;
+  int kind[kGroups];
   const TIN* src[kGroups];
+  int64_t src_step[kGroups];
+  TIN* q_out[kGroups];
+  int in_slot[kGroups];  // elements from the token's first cache row to this row's chunk a
   KnownDivisor scale[kGroups];
-  bool norm[kGroups];
+  bool norm[kGroups], rows_to_turn[kGroups];  // (the latter uniform over a warp)
 #pragma unroll
   for (int g = 0; g < kGroups; ++g) {
     const int r = row0 + g * ROWS;
     kind[g] = g >= groups || r >= rows ? 3 : r >= h_q + h_kv ? 2 : r >= h_q ? 1 : 0;
-    head[g] = kind[g] == 0 ? r : kind[g] == 1 ? r - h_q : kind[g] == 2 ? r - h_q - h_kv : 0;
-    src[g] = static_cast<const TIN*>(kind[g] == 0 ? a.q : kind[g] == 1 ? a.k : a.v) + head[g] * D;
+    const int head = kind[g] == 0 ? r : kind[g] == 1 ? r - h_q : kind[g] == 2 ? r - h_q - h_kv : 0;
+    const int64_t stride = kind[g] == 0 ? a.q_stride : kind[g] == 1 ? a.k_stride : a.v_stride;
+    src[g] = static_cast<const TIN*>(kind[g] == 0 ? a.q : kind[g] == 1 ? a.k : a.v) + n0 * stride +
+             head * D + ca;
+    src_step[g] = step * stride;
+    q_out[g] = static_cast<TIN*>(a.q_out) + n0 * a.q_out_stride + head * D + ca;
+    in_slot[g] = head * kPageSize * D + ca;
     norm[g] = kind[g] == 0 ? a.q_weight != nullptr : kind[g] == 1 && a.k_weight != nullptr;
+    rows_to_turn[g] = __any_sync(0xffffffffu, kind[g] < 2);
     if constexpr (CACHE == PKV_FP8_E4M3 || CACHE == PKV_INT8)
-      scale[g] = known_divisor(kind[g] == 1   ? a.k_scales[head[g]]
-                               : kind[g] == 2 ? a.v_scales[head[g]]
+      scale[g] = known_divisor(kind[g] == 1   ? a.k_scales[head]
+                               : kind[g] == 2 ? a.v_scales[head]
                                               : 1.f);
   }
+  const int64_t out_step = step * a.q_out_stride;
 
   struct Token {
     int pos;
@@ -144,26 +169,20 @@ __global__ void __launch_bounds__(kThreads, 3) qk_norm_rope_append_kernel(const 
     uint2 xa[kGroups], xb[kGroups];
     float cs[CH], sn[CH];
   };
-  auto load_rows = [&](int64_t n, Token& t) {
+  auto load_rows = [&](int64_t n, Token& t) {  // (called for n0, n0 + step, ... in turn)
 #pragma unroll
     for (int g = 0; g < kGroups; ++g) {
-      t.xa[g] = t.xb[g] = make_uint2(0, 0);
-      if (kind[g] == 3) continue;
-      const int64_t stride = kind[g] == 0 ? a.q_stride : kind[g] == 1 ? a.k_stride : a.v_stride;
-      const TIN* p = src[g] + n * stride;
-      t.xa[g] = __ldcs(reinterpret_cast<const uint2*>(p + ca));
-      t.xb[g] = __ldcs(reinterpret_cast<const uint2*>(p + cb));
+      if (kind[g] != 3) {
+        t.xa[g] = __ldcs(reinterpret_cast<const uint2*>(src[g]));
+        t.xb[g] = __ldcs(reinterpret_cast<const uint2*>(src[g] + over));
+      }
+      src[g] += src_step[g];
     }
     t.pos = a.rot_dim > 0 ? a.positions[n] : 0;
     t.slot = a.slots[n];
   };
   auto load_turn = [&](Token& t) {
-#pragma unroll
-    for (int e = 0; e < CH; ++e) {
-      t.cs[e] = 1.f;
-      t.sn[e] = 0.f;
-    }
-    if (!turns || t.pos < 0 || t.pos >= a.max_positions) return;
+    if (!turns || (unsigned)t.pos >= (unsigned)a.max_positions) return;
     const float* row = a.cos_sin + (int64_t)t.pos * a.rot_dim;
     if constexpr (INTER) {  // the pairs of chunk a, then of chunk b
 #pragma unroll
@@ -174,47 +193,34 @@ __global__ void __launch_bounds__(kThreads, 3) qk_norm_rope_append_kernel(const 
         t.sn[CH / 2 + e] = row[half + cb / 2 + e];
       }
     } else {
-#pragma unroll
-      for (int e = 0; e < CH; e += 2) {
-        const float2 c = *reinterpret_cast<const float2*>(row + ca + e);
-        const float2 s = *reinterpret_cast<const float2*>(row + half + ca + e);
-        t.cs[e] = c.x;
-        t.cs[e + 1] = c.y;
-        t.sn[e] = s.x;
-        t.sn[e + 1] = s.y;
-      }
+      vec_load(row + ca, t.cs);
+      vec_load(row + half + ca, t.sn);
     }
   };
-
-  const int64_t step = gridDim.x / parts;
-  int64_t n = blockIdx.x / parts;
-  Token cur, nxt;
-  load_rows(n, cur);
-  load_turn(cur);
-  for (; n < a.num_tokens; n += step) {
-    const bool more = n + step < a.num_tokens;
-    if (more) load_rows(n + step, nxt);
-    const bool left_out = a.rot_dim > 0 && (cur.pos < 0 || cur.pos >= a.max_positions);
-    int64_t slot = cur.slot;
+  auto work = [&](Token& t) {  // (likewise)
+    const bool left_out = a.rot_dim > 0 && (unsigned)t.pos >= (unsigned)a.max_positions;
+    bool stored = t.slot >= 0;
     if (left_out) {  // the whole token
       if (threadIdx.x == 0 && part == 0) atomicOr(a.err, PKV_DEVERR_BAD_POSITION);
-    } else if (slot >= a.num_slots) {
+    } else if (t.slot >= a.num_slots) {
       if (threadIdx.x == 0 && part == 0) atomicOr(a.err, PKV_DEVERR_BAD_SLOT);
-      slot = -1;
+      stored = false;
     }
-    const int64_t crow0 = (slot / kPageSize) * h_kv * kPageSize + slot % kPageSize;
+    const uint64_t slot = (uint64_t)t.slot;
+    const int64_t row0 = (int64_t)(((slot >> 4) * h_kv * kPageSize + (slot & 15)) * D);
+    static_assert(kPageSize == 16, "slot arithmetic");
 #pragma unroll
     for (int g = 0; g < kGroups; ++g) {
       if (left_out || g >= groups) break;  // (uniform over the block)
       float xa[CH], xb[CH];
-      widen(cur.xa[g], xa);
-      widen(cur.xb[g], xb);
-      const int64_t at = (crow0 + (int64_t)head[g] * kPageSize) * D;
-      if (kind[g] == 2 && slot >= 0) {
-        store_chunk<TIN, CACHE, CH>(a.v_cache, at + ca, scale[g], xa);
-        store_chunk<TIN, CACHE, CH>(a.v_cache, at + cb, scale[g], xb);
+      widen(t.xa[g], xa);
+      widen(t.xb[g], xb);
+      const int64_t at = row0 + in_slot[g];
+      if (kind[g] == 2 && stored) {
+        store_chunk<TIN, CACHE, CH>(a.v_cache, at, scale[g], xa);
+        store_chunk<TIN, CACHE, CH>(a.v_cache, at + over, scale[g], xb);
       }
-      if (__all_sync(0xffffffffu, kind[g] >= 2)) continue;
+      if (!rows_to_turn[g]) continue;
       float ss = 0.f;
 #pragma unroll
       for (int e = 0; e < CH; ++e) ss = fmaf(xa[e], xa[e], fmaf(xb[e], xb[e], ss));
@@ -222,18 +228,21 @@ __global__ void __launch_bounds__(kThreads, 3) qk_norm_rope_append_kernel(const 
       for (int o = LPR / 2; o >= 1; o /= 2) ss += __shfl_xor_sync(0xffffffffu, ss, o);
       const float rstd = norm[g] ? rsqrtf(fmaf(ss, 1.f / D, a.eps)) : 1.f;
       const float* w = weights[kind[g] < 2 ? kind[g] : 2];
+      float wa[CH], wb[CH];
+      vec_load(w + ca, wa);
+      vec_load(w + cb, wb);
 #pragma unroll
       for (int e = 0; e < CH; ++e) {
-        xa[e] *= rstd * w[ca + e];
-        xb[e] *= rstd * w[cb + e];
+        xa[e] *= rstd * wa[e];
+        xb[e] *= rstd * wb[e];
       }
       if (turns) {
         if constexpr (INTER) {
 #pragma unroll
           for (int e = 0; e < CH; e += 2) {
             const float a0 = xa[e], a1 = xa[e + 1], b0 = xb[e], b1 = xb[e + 1];
-            const float ac = cur.cs[e / 2], as = cur.sn[e / 2];
-            const float bc = cur.cs[CH / 2 + e / 2], bs = cur.sn[CH / 2 + e / 2];
+            const float ac = t.cs[e / 2], as = t.sn[e / 2];
+            const float bc = t.cs[CH / 2 + e / 2], bs = t.sn[CH / 2 + e / 2];
             xa[e] = fmaf(a0, ac, -(a1 * as));
             xa[e + 1] = fmaf(a1, ac, a0 * as);
             xb[e] = fmaf(b0, bc, -(b1 * bs));
@@ -243,24 +252,35 @@ __global__ void __launch_bounds__(kThreads, 3) qk_norm_rope_append_kernel(const 
 #pragma unroll
           for (int e = 0; e < CH; ++e) {
             const float f = xa[e], s = xb[e];
-            xa[e] = fmaf(f, cur.cs[e], -(s * cur.sn[e]));
-            xb[e] = fmaf(s, cur.cs[e], f * cur.sn[e]);
+            xa[e] = fmaf(f, t.cs[e], -(s * t.sn[e]));
+            xb[e] = fmaf(s, t.cs[e], f * t.sn[e]);
           }
         }
       }
       if (kind[g] == 0) {
-        TIN* out = static_cast<TIN*>(a.q_out) + n * a.q_out_stride + head[g] * D;
-        *reinterpret_cast<uint2*>(out + ca) = narrow(xa);
-        *reinterpret_cast<uint2*>(out + cb) = narrow(xb);
-      } else if (kind[g] == 1 && slot >= 0) {
-        store_chunk<float, CACHE, CH>(a.k_cache, at + ca, scale[g], xa);
-        store_chunk<float, CACHE, CH>(a.k_cache, at + cb, scale[g], xb);
+        *reinterpret_cast<uint2*>(q_out[g]) = narrow(xa);
+        *reinterpret_cast<uint2*>(q_out[g] + over) = narrow(xb);
+      } else if (kind[g] == 1 && stored) {
+        store_chunk<float, CACHE, CH>(a.k_cache, at, scale[g], xa);
+        store_chunk<float, CACHE, CH>(a.k_cache, at + over, scale[g], xb);
       }
     }
-    if (more) {
-      load_turn(nxt);
-      cur = nxt;
-    }
+#pragma unroll
+    for (int g = 0; g < kGroups; ++g) q_out[g] += out_step;
+  };
+
+  Token even{}, odd{};
+  load_rows(n0, even);
+  load_turn(even);
+  for (int64_t n = n0; n < a.num_tokens; n += 2 * step) {
+    const bool second = n + step < a.num_tokens, third = n + 2 * step < a.num_tokens;
+    if (second) load_rows(n + step, odd);
+    work(even);
+    if (!second) break;
+    load_turn(odd);
+    if (third) load_rows(n + 2 * step, even);
+    work(odd);
+    if (third) load_turn(even);
   }
 }
 
