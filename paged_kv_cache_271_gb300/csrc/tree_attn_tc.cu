@@ -71,13 +71,14 @@ struct TcShape {
   static constexpr int TILE = kTok * D * 2;       // K (or V) of a tile in MMA form
   static constexpr int RAW_TILE = kTok * D;       // 8-bit codes
   static constexpr int RAW_STAGE = 2 * RAW_TILE;
-  // 208 KB of rings: K tiles, needed until their S is done, and V tiles, needed until their P V
-  // is done, go round separately; 8-bit caches have 96 KB of raw codes before them
-  static constexpr int NK = (W8 ? 48 : 96) * 1024 / TILE, NV = (W8 ? 64 : 112) * 1024 / TILE;
-  static constexpr int NR = W8 ? 96 * 1024 / RAW_STAGE : 0;
+  // 192 KB of rings: K tiles, needed until their S is done, and V tiles, needed until their P V
+  // is done, go round separately; 8-bit caches have 80 KB of raw codes before them
+  static constexpr int NK = (W8 ? 48 : 96) * 1024 / TILE, NV = (W8 ? 64 : 96) * 1024 / TILE;
+  static constexpr int NR = W8 ? 80 * 1024 / RAW_STAGE : 0;
   static constexpr int OFF_V = NK * TILE;
   static constexpr int OFF_RAW = OFF_V + NV * TILE;
-  static constexpr int OFF_ML = OFF_RAW + NR * RAW_STAGE;   // [2][128] (max, sum)
+  static constexpr int OFF_Q = OFF_RAW + NR * RAW_STAGE;    // 2 KB per softmax warp
+  static constexpr int OFF_ML = OFF_Q + kSoftThreads / 32 * 2048;  // [2][128] (max, sum)
   static constexpr int OFF_BAR = OFF_ML + 2 * kGroupThreads * 8;
   static constexpr int BARS = 2 * NK + 2 * NV + 2 * NR + 3 * kSBufs + 3;
   static constexpr int OFF_MISC = OFF_BAR + 8 * BARS;       // masks, bad nodes, TMEM address
@@ -348,7 +349,6 @@ __global__ void __launch_bounds__(TcShape<KV, D>::THREADS, 1) tree_tc_kernel(
         if (elect_one()) mbar_arrive(q_ready);  // (the next unit's: this phase has been seen)
         __syncwarp();
         auto s_mma = [&](int buf) {
-          if (!wait(&full_k[ks.st], ks.par)) return false;
           const uint64_t kd = k_desc + (uint32_t)(ks.st * (S::TILE >> 4));
           const uint32_t d = tmem + s_col(buf);
           if (elect_one()) {
@@ -360,14 +360,17 @@ __global__ void __launch_bounds__(TcShape<KV, D>::THREADS, 1) tree_tc_kernel(
           }
           __syncwarp();
           ks.advance(stride);
-          return true;
         };
         Buf b{w, 0}, before{w - 1, 0}, ahead{w, 0};
-        if (ok && w < n) ok = s_mma(w);
+        if (ok && w < n) {
+          ok = wait(&full_k[ks.st], ks.par);
+          if (ok) s_mma(w);
+        }
         ahead.advance(wide, 2);
         for (int u = w; ok && u < n; u += 2) {
           const uint32_t par = b.parity(ph);
-          ok = wait(&p_ready[b.i], par);
+          if (u + 2 < n) ok = wait(&full_k[ks.st], ks.par);  // K of the next S, before P is there
+          if (ok) ok = wait(&p_ready[b.i], par);
           if (ok && u < 2 && unit > 0) ok = wait(o_read, (unit - 1) & 1);  // (of the last unit)
           if (!ok) break;
           const uint64_t vd = v_desc + (uint32_t)(vs.st * (S::TILE >> 4));
@@ -388,7 +391,7 @@ __global__ void __launch_bounds__(TcShape<KV, D>::THREADS, 1) tree_tc_kernel(
               ok = wait(&pv_done[b.i], par);
             else if (u > 0)
               ok = wait(&pv_done[before.i], before.parity(ph));
-            if (ok) ok = s_mma(ahead.i);
+            if (ok) s_mma(ahead.i);
           }
           b.advance(wide, 2);
           ahead.advance(wide, 2);
@@ -512,44 +515,68 @@ __global__ void __launch_bounds__(TcShape<KV, D>::THREADS, 1) tree_tc_kernel(
     // The row's query into tensor memory, once the S of the last unit are done.
     auto store_query = [&](const TreeRun& run, Row& x) {
       const bool wide = run.rows > kGroupThreads;
-      const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) +
-                                                        row_at(run, x));
-      float up = 1.f;
       x.sc = a.scale_log2;
-      if constexpr (W8) {
-        uint32_t mx = 0;  // largest |q| as bits (bf16 magnitudes order like integers)
-        if (x.live) {
+      const bool mine = wide || wg == 0;  // (8-bit caches: both groups need the row's scale)
+      if (ok && (mine || W8)) {
+        // Four lanes read 64 consecutive bytes of a row, eight rows an instruction (a lane reading
+        // its own row would touch 32 lines an instruction); 32 rows x 64 bytes at a time change
+        // hands through shared memory.
+        constexpr int RND = D / 32;  // rounds of 64 bytes
+        const size_t off = row_at(run, x);
+        uint4 in[RND][4];
 #pragma unroll
-          for (int c = 0; c < D / 8; ++c) {
-            const uint4 v = src[c];
-            const uint32_t m = max(max(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu) & 0x7fff0000u,
-                                   max(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu) & 0x7fff0000u) >> 16;
-            mx = max(mx, max(m, max(max(v.x & 0x7fffu, v.y & 0x7fffu),
-                                    max(v.z & 0x7fffu, v.w & 0x7fffu))));
+        for (int g = 0; g < 4; ++g) {
+          const int from = 8 * g + (lane >> 2);
+          const size_t at = __shfl_sync(0xffffffffu, (unsigned long long)off, from);
+          const bool there = __shfl_sync(0xffffffffu, (int)x.live, from) != 0;
+          const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) +
+                                                            at) + (lane & 3);
+#pragma unroll
+          for (int d = 0; d < RND; ++d) in[d][g] = there ? src[4 * d] : make_uint4(0, 0, 0, 0);
+        }
+        const uint32_t stage = ring + S::OFF_Q + warp * 2048;
+        uint32_t w[D / 2];  // this lane's row, bf16 pairs
+#pragma unroll
+        for (int d = 0; d < RND; ++d) {
+          __syncwarp();
+#pragma unroll
+          for (int g = 0; g < 4; ++g) {
+            const int row = 8 * g + (lane >> 2);
+            sts128(stage + row * 64 + (((lane & 3) ^ ((row >> 1) & 3)) << 4), in[d][g]);
+          }
+          __syncwarp();
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const uint4 v = lds128(stage + lane * 64 + ((c ^ ((lane >> 1) & 3)) << 4));
+            w[16 * d + 4 * c] = v.x;
+            w[16 * d + 4 * c + 1] = v.y;
+            w[16 * d + 4 * c + 2] = v.z;
+            w[16 * d + 4 * c + 3] = v.w;
           }
         }
-        const int ex = mx >> 7;  // biased exponent: mx * 2^e in [2^14, 2^15), none for 0, inf, NaN
-        const int e = mx != 0 && ex < 255 ? min(126, max(-126, 141 - ex)) : 0;
-        up = __int_as_float((127 + e) << 23);
-        // (at least the smallest normal number: an unseen score of -inf must stay one)
-        x.sc = fmaxf(x.sc * a.k_scales[run.j] * __int_as_float((127 - e) << 23), 0x1p-126f);
-      }
-      if (ok && (wide || wg == 0)) {
-        const uint32_t q_col = kColQ + (wide ? 64 * wg : 0);
+        if constexpr (W8) {
+          uint32_t lo = 0, hi = 0;  // largest |q| as bits (bf16 magnitudes order like integers)
 #pragma unroll
-        for (int h = 0; h < D / 64; ++h) {
-          uint32_t w[32];
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const uint4 v = x.live ? src[8 * h + k] : make_uint4(0, 0, 0, 0);
-            const uint32_t y[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-            for (int m = 0; m < 4; ++m)
-              w[4 * k + m] = W8 ? pack_f16(bf16lo(y[m]) * up, bf16hi(y[m]) * up) : y[m];
+          for (int k = 0; k < D / 2; ++k) {
+            lo = max(lo, w[k] & 0x7fffu);
+            hi = max(hi, w[k] & 0x7fff0000u);
           }
-          tmem_st32(lane_t + q_col + 32 * h, w);
+          const uint32_t mx = max(lo, hi >> 16);
+          const int ex = mx >> 7;  // biased exponent: mx * 2^e in [2^14, 2^15), none for 0, inf, NaN
+          const int e = mx != 0 && ex < 255 ? min(126, max(-126, 141 - ex)) : 0;
+          const float up = __int_as_float((127 + e) << 23);
+          // (at least the smallest normal number: an unseen score of -inf must stay one)
+          x.sc = fmaxf(x.sc * a.k_scales[run.j] * __int_as_float((127 - e) << 23), 0x1p-126f);
+#pragma unroll
+          for (int k = 0; k < D / 2; ++k) w[k] = pack_f16(bf16lo(w[k]) * up, bf16hi(w[k]) * up);
         }
-        tmem_wait_st();
+        if (mine) {
+          const uint32_t q_col = kColQ + (wide ? 64 * wg : 0);
+#pragma unroll
+          for (int h = 0; h < D / 64; ++h)
+            tmem_st32(lane_t + q_col + 32 * h, *reinterpret_cast<const uint32_t(*)[32]>(&w[32 * h]));
+          tmem_wait_st();
+        }
       }
       tc_fence_before();
       __syncwarp();
@@ -667,13 +694,18 @@ __global__ void __launch_bounds__(TcShape<KV, D>::THREADS, 1) tree_tc_kernel(
             fence_proxy_async_smem();
           }
         }
-        float mx8[8];
+        float mx4[4];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) mx8[k] = -INFINITY;
+        for (int k = 0; k < 4; ++k) mx4[k] = __uint_as_float(sr[k]);
 #pragma unroll
-        for (int k = 0; k < 64; ++k) mx8[k & 7] = fmaxf(mx8[k & 7], __uint_as_float(sr[k]));
-        const float mx = sc * fmaxf(fmaxf(fmaxf(mx8[0], mx8[1]), fmaxf(mx8[2], mx8[3])),
-                                    fmaxf(fmaxf(mx8[4], mx8[5]), fmaxf(mx8[6], mx8[7])));
+        for (int k = 4; k < 60; k += 8) {
+#pragma unroll
+          for (int m = 0; m < 4; ++m)
+            mx4[m] = max3(mx4[m], __uint_as_float(sr[k + 2 * m]), __uint_as_float(sr[k + 2 * m + 1]));
+        }
+        const float mx = sc * max3(max3(mx4[0], mx4[1], mx4[2]),
+                                   max3(mx4[3], __uint_as_float(sr[60]), __uint_as_float(sr[61])),
+                                   fmaxf(__uint_as_float(sr[62]), __uint_as_float(sr[63])));
         if (u == wg) {
           m_used = mx;
         } else {
@@ -699,20 +731,22 @@ __global__ void __launch_bounds__(TcShape<KV, D>::THREADS, 1) tree_tc_kernel(
         // P = 2^(s - m) over the first 32 columns of the tile's S buffer
         const float m_use = m_used == -INFINITY ? 0.f : m_used;
         uint32_t pw[32];
-        float sum8[8];
-#pragma unroll
-        for (int k = 0; k < 8; ++k) sum8[k] = 0.f;
+        uint64_t sum[4] = {0, 0, 0, 0};  // (pairs of zeros)
+        const uint64_t sc2 = pack2(sc, sc), m2 = pack2(-m_use, -m_use);
 #pragma unroll
         for (int k = 0; k < 32; ++k) {
-          const float e0 = ex2_approx(fmaf(__uint_as_float(sr[2 * k]), sc, -m_use));
-          const float e1 = ex2_approx(fmaf(__uint_as_float(sr[2 * k + 1]), sc, -m_use));
-          sum8[(2 * k) & 7] += e0;
-          sum8[(2 * k + 1) & 7] += e1;
+          float e0, e1;
+          unpack2(fma2(pack2(__uint_as_float(sr[2 * k]), __uint_as_float(sr[2 * k + 1])), sc2, m2),
+                  e0, e1);
+          e0 = ex2_approx(e0);
+          e1 = ex2_approx(e1);
+          sum[k & 3] = add2(sum[k & 3], pack2(e0, e1));
           pw[k] = pack_p<W8>(e0, e1);
         }
         tmem_st32(lane_t + scol, pw);
-        l += ((sum8[0] + sum8[1]) + (sum8[2] + sum8[3])) +
-             ((sum8[4] + sum8[5]) + (sum8[6] + sum8[7]));
+        float s0, s1;
+        unpack2(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), s0, s1);
+        l += s0 + s1;
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();  // (one arrival per warp: arrivals on one barrier go one by one)
