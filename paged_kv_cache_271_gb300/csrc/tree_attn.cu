@@ -69,7 +69,7 @@ __global__ void __launch_bounds__(kThreads) tree_simt_kernel(const TreeArgs a) {
   __shared__ TreeShare share;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   tree_share<kThreads>(a, scratch, &share);
-  TreeWalk walk(share);
+  TreeWalk walk(a, share);
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;  // tokens / dims, group of 4 rows
   TreeRun run;
   while (walk.next(a, run)) {

@@ -55,6 +55,10 @@ constexpr int kCopyWarp = kMmaWarp + 2;      // two: copies of K and of V
 constexpr int kConvWarp = kMmaWarp + 4;      // first of four (8-bit caches)
 constexpr int kConvThreads = 128;
 constexpr int kSBufs = 3;
+// Runs on their way from the K copy warp, which walks the share, to the other warps. It is ahead by
+// the tiles of the rings at most, each a run of its own at worst, besides the run whose rows are
+// being written and the one it is about to copy.
+constexpr int kRuns = 32;
 // tensor memory columns: O of group 0 and 1, Q of the rows 0 .. 127 and 128 .. 255, S (then P)
 // buffers; the third S buffer shares the second Q's columns (units of up to 128 rows have one Q)
 constexpr uint32_t kColO = 0, kColQ = 256, kColS = 384, kColS2 = 320;
@@ -80,7 +84,8 @@ struct TcShape {
   static constexpr int OFF_Q = OFF_RAW + NR * RAW_STAGE;    // 2 KB per softmax warp
   static constexpr int OFF_ML = OFF_Q + kSoftThreads / 32 * 2048;  // [2][128] (max, sum)
   static constexpr int OFF_BAR = OFF_ML + 2 * kGroupThreads * 8;
-  static constexpr int BARS = 2 * NK + 2 * NV + 2 * NR + 3 * kSBufs + 3;
+  static constexpr int BARS = 2 * NK + 2 * NV + 2 * NR + 3 * kSBufs + 4 + kRuns;
+  static_assert(NK + NR + 3 <= kRuns, "runs in flight");
   static constexpr int OFF_MISC = OFF_BAR + 8 * BARS;       // masks, bad nodes, TMEM address
   static constexpr uint32_t IDESC_S = tc_idesc(128, kTok, false, W8);
   static constexpr uint32_t IDESC_PV = tc_idesc(128, D, true, W8);
@@ -186,7 +191,9 @@ __global__ void __launch_bounds__(TcShape<KV, D>::THREADS, 1) tree_tc_kernel(
   // that no phase completes before both have seen the last (one may have no step in a unit)
   uint64_t* q_ready = pv_done + kSBufs;
   uint64_t* o_read = q_ready + 1;                                    // O of a unit read
-  uint64_t* mma_idle = o_read + 1;
+  uint64_t* met = o_read + 1;                                        // both groups ended a unit
+  uint64_t* mma_idle = met + 1;
+  uint64_t* run_there = mma_idle + 1;                                // [kRuns]
   int* page_mask = reinterpret_cast<int*>(smem + S::OFF_MISC);       // [NV] good pages of the tile
   int* raw_mask = page_mask + NV;                                    // [NR]
   uint32_t* bad_nodes = reinterpret_cast<uint32_t*>(raw_mask + NR);  // [2][8] V row not finite
@@ -195,6 +202,7 @@ __global__ void __launch_bounds__(TcShape<KV, D>::THREADS, 1) tree_tc_kernel(
 
   __shared__ int scratch[64];
   __shared__ TreeShare share;
+  __shared__ TreeRun runs[kRuns];  // (n = 0: the share's end)
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (threadIdx.x == kCopyWarp * 32) {
     for (int s = 0; s < NK; ++s) {
@@ -216,7 +224,9 @@ __global__ void __launch_bounds__(TcShape<KV, D>::THREADS, 1) tree_tc_kernel(
     }
     mbar_init(q_ready, kSoftThreads / 32 + 2);
     mbar_init(o_read, kSoftThreads / 32);
+    mbar_init(met, kSoftThreads / 32);
     mbar_init(mma_idle, 2);
+    for (int i = 0; i < kRuns; ++i) mbar_init(&run_there[i], 1);
     mbar_fence_init();
     if constexpr (!W8) {
       asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm_k)) : "memory");
@@ -237,8 +247,12 @@ __global__ void __launch_bounds__(TcShape<KV, D>::THREADS, 1) tree_tc_kernel(
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = (uint32_t)uniform((int)*s_taddr);
-  TreeWalk walk(share);
-  TreeRun run;
+  // run i of the share, or nullptr after the last (or a wait that gave up)
+  auto get_run = [&](uint32_t i) -> const TreeRun* {
+    const bool got = mbar_wait(&run_there[i % kRuns], (i / kRuns) & 1u, a.err);
+    const TreeRun* r = &runs[i % kRuns];
+    return __all_sync(0xffffffffu, got && r->n > 0) ? r : nullptr;
+  };
 
   if (warp >= kMmaWarp && warp < kConvWarp) {
     regs_down<S::REGS>();
@@ -260,11 +274,25 @@ __global__ void __launch_bounds__(TcShape<KV, D>::THREADS, 1) tree_tc_kernel(
       int st = 0, issued = 0;
       uint32_t par = 0;
       bool ok = true;
-      while (ok && walk.next(a, run)) {
-        const int pages = uniform((run.req.read + kPageSize - 1) / kPageSize);
-        const int n = uniform(run.n), j = uniform(run.j);
-        const int32_t* table = a.block_tables + (size_t)run.b * a.max_pages;
-        int lp = uniform(run.tile0 * kPages);  // first page of the tile
+      TreeWalk walk(a, share);
+      for (uint32_t unit = 0;; ++unit) {
+        const TreeRun* run = nullptr;
+        if (is_k) {  // (a wait that gave up ends the share for every warp)
+          TreeRun* r = &runs[unit % kRuns];
+          if (lane == 0) {
+            if (!ok || !walk.next(a, *r)) r->n = 0;
+            mbar_arrive(&run_there[unit % kRuns]);
+          }
+          __syncwarp();
+          if (r->n > 0) run = r;
+        } else if (ok) {
+          run = get_run(unit);
+        }
+        if (!run) break;
+        const int pages = uniform((run->req.read + kPageSize - 1) / kPageSize);
+        const int n = uniform(run->n), j = uniform(run->j);
+        const int32_t* table = a.block_tables + (size_t)run->b * a.max_pages;
+        int lp = uniform(run->tile0 * kPages);  // first page of the tile
         int ids = -1;                          // lane L: the id of page 32 m + L of the run
         for (int i = 0; i < n; ++i, lp += kPages) {
           if ((i & 7) == 0) ids = lp + lane < pages ? table[lp + lane] : -1;
@@ -334,9 +362,11 @@ __global__ void __launch_bounds__(TcShape<KV, D>::THREADS, 1) tree_tc_kernel(
       };
       if (elect_one()) mbar_arrive(q_ready);
       __syncwarp();
-      for (; ok && walk.next(a, run); ++unit) {
-        const int tiles = uniform(run.n);
-        const bool wide = uniform(run.rows) > kGroupThreads;
+      for (; ok; ++unit) {
+        const TreeRun* run = get_run(unit);
+        if (!run) break;
+        const int tiles = uniform(run->n);
+        const bool wide = uniform(run->rows) > kGroupThreads;
         const int n = wide ? 2 * tiles : tiles, stride = wide ? 1 : 2;  // tiles between steps
         Place<NK> ks = k_base;  // K of the next S
         Place<NV> vs = v_base;  // V of the next P V
@@ -434,10 +464,12 @@ __global__ void __launch_bounds__(TcShape<KV, D>::THREADS, 1) tree_tc_kernel(
       Place<NV> pv;
       bool ok = true;
       int t = 0, end = 0;  // tiles done, tiles of the runs so far
+      uint32_t unit = 0;
       for (;; ++t, raw.advance(1), pk.advance(1), pv.advance(1)) {
         if (t == end) {
-          if (!walk.next(a, run)) break;
-          end += run.n;
+          const TreeRun* run = get_run(unit++);
+          if (!run) break;
+          end += run->n;
         }
         ok = mbar_wait(&raw_full[raw.st], raw.par, a.err);
         if (!ok) break;
@@ -512,28 +544,32 @@ __global__ void __launch_bounds__(TcShape<KV, D>::THREADS, 1) tree_tc_kernel(
     auto row_at = [&](const TreeRun& run, const Row& x) {  // its offset in q and out
       return (((size_t)run.b * a.nodes + x.t) * a.h_q + x.head) * D;
     };
-    // The row's query into tensor memory, once the S of the last unit are done.
-    auto store_query = [&](const TreeRun& run, Row& x) {
+    // A unit's queries come in two steps. load_query: four lanes read 64 consecutive bytes of a row,
+    // eight rows an instruction (a lane reading its own row would touch 32 lines an instruction).
+    // store_query, once the S of the last unit are done: 32 rows x 64 bytes at a time change hands
+    // through shared memory, and each lane puts its row into tensor memory.
+    constexpr int RND = D / 32;  // rounds of 64 bytes
+    auto needs_query = [&](const TreeRun& run) {  // (8-bit caches: both groups need a row's scale)
+      return ok && (W8 || run.rows > kGroupThreads || wg == 0);
+    };
+    auto load_query = [&](const TreeRun& run, const Row& x, uint4 (&in)[RND][4]) {
+      if (!needs_query(run)) return;
+      const size_t off = row_at(run, x);
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const int from = 8 * g + (lane >> 2);
+        const size_t at = __shfl_sync(0xffffffffu, (unsigned long long)off, from);
+        const bool there = __shfl_sync(0xffffffffu, (int)x.live, from) != 0;
+        const uint4* src =
+            reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + at) + (lane & 3);
+#pragma unroll
+        for (int d = 0; d < RND; ++d) in[d][g] = there ? src[4 * d] : make_uint4(0, 0, 0, 0);
+      }
+    };
+    auto store_query = [&](const TreeRun& run, Row& x, const uint4 (&in)[RND][4]) {
       const bool wide = run.rows > kGroupThreads;
       x.sc = a.scale_log2;
-      const bool mine = wide || wg == 0;  // (8-bit caches: both groups need the row's scale)
-      if (ok && (mine || W8)) {
-        // Four lanes read 64 consecutive bytes of a row, eight rows an instruction (a lane reading
-        // its own row would touch 32 lines an instruction); 32 rows x 64 bytes at a time change
-        // hands through shared memory.
-        constexpr int RND = D / 32;  // rounds of 64 bytes
-        const size_t off = row_at(run, x);
-        uint4 in[RND][4];
-#pragma unroll
-        for (int g = 0; g < 4; ++g) {
-          const int from = 8 * g + (lane >> 2);
-          const size_t at = __shfl_sync(0xffffffffu, (unsigned long long)off, from);
-          const bool there = __shfl_sync(0xffffffffu, (int)x.live, from) != 0;
-          const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) +
-                                                            at) + (lane & 3);
-#pragma unroll
-          for (int d = 0; d < RND; ++d) in[d][g] = there ? src[4 * d] : make_uint4(0, 0, 0, 0);
-        }
+      if (needs_query(run)) {
         const uint32_t stage = ring + S::OFF_Q + warp * 2048;
         uint32_t w[D / 2];  // this lane's row, bf16 pairs
 #pragma unroll
@@ -570,7 +606,7 @@ __global__ void __launch_bounds__(TcShape<KV, D>::THREADS, 1) tree_tc_kernel(
 #pragma unroll
           for (int k = 0; k < D / 2; ++k) w[k] = pack_f16(bf16lo(w[k]) * up, bf16hi(w[k]) * up);
         }
-        if (mine) {
+        if (wide || wg == 0) {
           const uint32_t q_col = kColQ + (wide ? 64 * wg : 0);
 #pragma unroll
           for (int h = 0; h < D / 64; ++h)
@@ -582,24 +618,16 @@ __global__ void __launch_bounds__(TcShape<KV, D>::THREADS, 1) tree_tc_kernel(
       __syncwarp();
       if (lane == 0) mbar_arrive(q_ready);
     };
-    Row me{}, then{};
-    TreeRun next_run;
-    bool more = walk.next(a, run);
-    if (more) {
-      me = find_row(run);
-      store_query(run, me);
+    Row me{};
+    const TreeRun* next = get_run(0);
+    if (next) {
+      uint4 in[RND][4];
+      me = find_row(*next);
+      load_query(*next, me, in);
+      store_query(*next, me, in);
     }
-    for (; more; ++unit, run = next_run, me = then) {
-      // the next unit is worked out, and its query brought near, while this one's first scores run
-      more = walk.next(a, next_run);
-      if (more) {
-        then = find_row(next_run);
-        if (then.live) {
-          const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(a.q) + row_at(next_run, then);
-          asm volatile("prefetch.global.L2 [%0];" ::"l"(src));
-          if (D == 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(src + 64));
-        }
-      }
+    for (; next; ++unit) {
+      const TreeRun& run = *next;
       const bool wide = run.rows > kGroupThreads, live = me.live;
       const int n = wide ? 2 * run.n : run.n;  // steps; this group's: wg, wg + 2, ...
       const int b = run.b, j = run.j, t = me.t;
@@ -759,6 +787,13 @@ __global__ void __launch_bounds__(TcShape<KV, D>::THREADS, 1) tree_tc_kernel(
         p0 += wide ? kTok : 2 * kTok;
       }
       // ---- the unit's rows ----
+      uint4 in[RND][4];  // the next unit's queries, on their way during the waits
+      next = get_run(unit + 1);
+      Row then{};
+      if (next) {
+        then = find_row(*next);
+        load_query(*next, then, in);
+      }
       if (ok && wg < n) ok = mbar_wait(&pv_done[prev_buf], prev_par, a.err);
       ok = __all_sync(0xffffffffu, ok);
       if (ok && wg < n && (warp & 3) == 0 && lane == 0)
@@ -766,8 +801,10 @@ __global__ void __launch_bounds__(TcShape<KV, D>::THREADS, 1) tree_tc_kernel(
       tc_fence_after();
       if (!wide) ml[wg * kGroupThreads + r] = make_float2(m_used, l);
       tc_fence_before();
-      // both groups are here whatever became of their waits
-      asm volatile("bar.sync 1, 256;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) mbar_arrive(met);
+      ok = mbar_wait(met, unit & 1, a.err) && ok;
+      ok = __all_sync(0xffffffffu, ok);
       tc_fence_after();
       if (threadIdx.x < 8) bad_nodes[8 * ((unit + 1) & 1) + threadIdx.x] = 0;
       // wide: the group's own rows, all dims; else group wg takes dims wg D/2 .. of every row and
@@ -835,7 +872,7 @@ __global__ void __launch_bounds__(TcShape<KV, D>::THREADS, 1) tree_tc_kernel(
         }
       };
       // the next query first, so that the next unit's scores run while this one's rows are written
-      if (more) store_query(next_run, then);
+      if (next) store_query(*next, then, in);
       if (ok) {
         const int c_lo = wide ? 0 : wg * (D / 2), c_hi = wide ? D : c_lo + D / 2;
         for (int c = c_lo; c < c_hi; c += 32) {
@@ -864,6 +901,7 @@ __global__ void __launch_bounds__(TcShape<KV, D>::THREADS, 1) tree_tc_kernel(
       ph = after_steps(ph, wide, n);
       base.skip(run.n);
       k_base.skip(run.n);
+      me = then;
     }
   }
 

@@ -153,37 +153,55 @@ struct TreeRun {
   int slot;        // partial slot otherwise
 };
 
-// Walks a share run by run. Uniform over its callers (it reads the lengths itself).
+// Walks a share run by run. Uniform over its callers (it reads the lengths itself, a request's when
+// the walk comes to it).
 struct TreeWalk {
-  int b, off, left, pass_cost;
-  __device__ __forceinline__ explicit TreeWalk(const TreeShare& s)
-      : b(s.b), off(s.off), left(s.count), pass_cost(s.pass_cost) {}
+  int b, left, pass_cost;
+  TreeReq req;  // of request b
+  TreeSize z;
+  int j, unit, x;  // KV head, unit and offset in its pass of the next run
+  __device__ __forceinline__ TreeWalk(const TreeArgs& a, const TreeShare& s)
+      : b(s.b), left(s.count), pass_cost(s.pass_cost) {
+    if (left <= 0) return;
+    load(a);
+    const unsigned len = z.tiles + pass_cost, pass = (unsigned)s.off / len;
+    x = s.off - pass * len;
+    j = pass / (unsigned)z.units;
+    unit = pass - j * z.units;
+  }
+  __device__ __forceinline__ void load(const TreeArgs& a) {
+    req = tree_request(a, b);
+    z = tree_size(a, req);
+    j = unit = x = 0;
+  }
   __device__ __forceinline__ bool next(const TreeArgs& a, TreeRun& r) {
-    while (left > 0 && b < a.batch) {
-      const TreeReq q = tree_request(a, b);
-      const TreeSize z = tree_size(a, q);
-      if (off >= tree_length(a, z, pass_cost)) {
-        off -= tree_length(a, z, pass_cost);
-        ++b;
+    while (left > 0) {
+      if (j >= a.h_kv || z.units == 0) {
+        if (++b >= a.batch) return false;
+        load(a);
         continue;
       }
       const int len = z.tiles + pass_cost;  // of a pass, its cost first
-      const int pass = (int)((unsigned)off / (unsigned)len);
-      const int x0 = off - pass * len, x1 = min(len, x0 + left);
-      off += x1 - x0;
-      left -= x1 - x0;
-      if (x1 <= pass_cost) continue;  // (none of its tiles)
-      const int j = (int)((unsigned)pass / (unsigned)z.units);
-      r.req = q;
+      const int x0 = x, x1 = min(len, x0 + left);
+      r.req = req;
       r.b = b;
       r.j = j;
-      r.row0 = (pass - j * z.units) * a.unit_rows;
-      r.rows = min(a.unit_rows, q.nodes * a.group - r.row0);
+      r.row0 = unit * a.unit_rows;
+      r.rows = min(a.unit_rows, req.nodes * a.group - r.row0);
       r.tile0 = max(0, x0 - pass_cost);
       r.n = x1 - pass_cost - r.tile0;
       r.whole = r.n == z.tiles;
       r.slot = r.tile0 > 0 ? 0 : 1;
-      return true;
+      left -= x1 - x0;
+      x = x1;
+      if (x == len) {
+        x = 0;
+        if (++unit == z.units) {
+          unit = 0;
+          ++j;
+        }
+      }
+      if (x1 > pass_cost) return true;  // (it has some of the pass's tiles)
     }
     return false;
   }
