@@ -13,17 +13,19 @@ using namespace pkv;
 
 namespace {
 
-// Query rows of a unit, tokens of a tile, least tiles of a CTA, cost of a pass in tiles and the
-// CTAs of one wave of the kernel that a call uses.
+// Query rows of a unit, tokens of a tile, least tiles of a CTA, cost of a pass in tiles, the weights
+// of narrow and wide passes (tree_plan.cuh) and the CTAs of one wave of the kernel that a call uses.
 struct TreeSplit {
-  int rows, tokens, min_tiles, pass_cost, wave;
+  int rows, tokens, min_tiles, pass_cost, narrow_rows, wide_tile, wave;
   bool tc;
 };
 
 // bf16 queries run on the tensor cores, fp32 queries (whose weights keep 24 bits) on CUDA cores.
-TreeSplit tree_split(int dtype_q) {
-  if (dtype_q == PKV_BF16) return TreeSplit{kTreeTcRows, kTreeTcTokens, 2, 4, kTreeTcWave, true};
-  return TreeSplit{kTreeSimtRows, kTreeSimtTokens, 4, 1, kTreeSimtWave, false};
+TreeSplit tree_split(int dtype_q, int kv) {
+  if (dtype_q == PKV_BF16)
+    return TreeSplit{kTreeTcRows,     kTreeTcTokens, 2, 8, kTreeTcRows / 2,
+                     is_coded(kv) ? 4 : 3, kTreeTcWave,   true};
+  return TreeSplit{kTreeSimtRows, kTreeSimtTokens, 4, 1, kTreeSimtRows, 2, kTreeSimtWave, false};
 }
 
 size_t tree_acc_bytes(const TreeSplit& t, int ctas, int head_dim) {
@@ -41,18 +43,18 @@ int check_tree_types(const char* who, int dtype_q, int kv) {
   return PKV_OK;
 }
 
-// Tiles that the call's table could hold at most.
-long long tree_most_tiles(const TreeSplit& t, int batch, int nodes, int h_q, int h_kv,
-                          int max_pages) {
+// Half tiles of work (tree_plan.cuh) that the call's table could hold at most.
+long long tree_most_work(const TreeSplit& t, int batch, int nodes, int h_q, int h_kv,
+                         int max_pages) {
   const long long units = ((long long)nodes * (h_q / h_kv) + t.rows - 1) / t.rows;
   const long long tiles = ((long long)max_pages * 16 + t.tokens - 1) / t.tokens;
-  return (long long)batch * h_kv * units * (tiles + t.pass_cost);
+  return (long long)batch * h_kv * units * (tiles * t.wide_tile + 2 * t.pass_cost);
 }
 
 // CTAs of a call: one wave, or fewer when the table cannot hold that many shares.
 int tree_ctas(const TreeSplit& t, int batch, int nodes, int h_q, int h_kv, int max_pages) {
-  const long long tiles = tree_most_tiles(t, batch, nodes, h_q, h_kv, max_pages);
-  return (int)std::max(1ll, std::min<long long>(t.wave, (tiles + t.min_tiles - 1) / t.min_tiles));
+  const long long work = tree_most_work(t, batch, nodes, h_q, h_kv, max_pages);
+  return (int)std::max(1ll, std::min<long long>(t.wave, work / (2 * t.min_tiles) + 1));
 }
 
 int check_tree_sizes(const char* who, int batch, int nodes, int h_q, int h_kv, int max_pages) {
@@ -159,7 +161,7 @@ size_t pkv_tree_decode_workspace_size(int32_t dtype_q, int32_t cache_dtype, int3
   if (batch <= 0 || tree_width <= 0 || num_q_heads <= 0 || num_kv_heads <= 0 || head_dim <= 0 ||
       max_pages_per_seq <= 0)
     return 0;
-  const TreeSplit t = tree_split(dtype_q);
+  const TreeSplit t = tree_split(dtype_q, cache_dtype);
   const int ctas = tree_ctas(t, batch, tree_width, num_q_heads, num_kv_heads, max_pages_per_seq);
   return tree_acc_bytes(t, ctas, head_dim) + tree_ml_bytes(t, ctas);
 }
@@ -199,9 +201,9 @@ int pkv_tree_decode_attention(const void* q, int32_t dtype_q, int32_t batch, int
   if (dtype_q == PKV_BF16 && kv == PKV_BF16 &&
       (long long)desc->num_pages * h_kv * desc->page_size >= (1ll << 31))
     return set_error(PKV_ESHAPE, "%s: a bf16 pool must have fewer than 2^31 rows", who);
-  const TreeSplit t = tree_split(dtype_q);
-  if (tree_most_tiles(t, batch, tree_width, num_q_heads, h_kv, max_pages_per_seq) >= (1ll << 30))
-    return set_error(PKV_ESHAPE, "%s: the table can hold 2^30 tiles of work or more", who);
+  const TreeSplit t = tree_split(dtype_q, kv);
+  if (tree_most_work(t, batch, tree_width, num_q_heads, h_kv, max_pages_per_seq) >= (1ll << 30))
+    return set_error(PKV_ESHAPE, "%s: the table can hold 2^30 half tiles of work or more", who);
   TreeArgs a{};
   a.ctas = tree_ctas(t, batch, tree_width, num_q_heads, h_kv, max_pages_per_seq);
   const size_t acc = tree_acc_bytes(t, a.ctas, D), need = acc + tree_ml_bytes(t, a.ctas);
@@ -235,6 +237,8 @@ int pkv_tree_decode_attention(const void* q, int32_t dtype_q, int32_t batch, int
   a.tile_tokens = t.tokens;
   a.min_tiles = t.min_tiles;
   a.pass_cost = t.pass_cost;
+  a.narrow_rows = t.narrow_rows;
+  a.wide_tile = t.wide_tile;
   st = error_word(&a.err);
   if (st != PKV_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);

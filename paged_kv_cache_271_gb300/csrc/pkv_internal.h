@@ -153,6 +153,8 @@ struct TreeArgs {
   int tile_tokens;  // cached tokens of a tile
   int min_tiles;    // least tiles a CTA takes
   int pass_cost;    // what beginning a pass costs a CTA, in tiles
+  int narrow_rows;  // a tile of a pass of up to this many rows counts 2 half tiles,
+  int wide_tile;    // of a wider one this many
 };
 
 struct CommitArgs {

@@ -259,28 +259,30 @@ __global__ void __launch_bounds__(kCombineThreads) tree_combine_kernel(const Tre
     if (first_block) asm volatile("griddepcontrol.wait;" ::: "memory");
     return;
   }
-  int tiles = 0, passes = 0, tiles_before = 0, passes_before = 0;
+  int work = 0, passes = 0, work_before = 0, passes_before = 0;
   for (int i = threadIdx.x; i < a.batch; i += kCombineThreads) {
     const TreeSize y = tree_size(a, tree_request(a, i));
-    const int p = y.units * a.h_kv;
-    tiles += y.tiles * p;
+    const int w = tree_work(a, y) * a.h_kv, p = y.units * a.h_kv;
+    work += w;
     passes += p;
     if (i < b) {
-      tiles_before += y.tiles * p;
+      work_before += w;
       passes_before += p;
     }
   }
-  int below, tiles_all, passes_all, tiles_pre, passes_pre;
-  block_scan<kCombineThreads>(tiles, scratch[0], below, tiles_all);
+  int below, work_all, passes_all, work_pre, passes_pre;
+  block_scan<kCombineThreads>(work, scratch[0], below, work_all);
   block_scan<kCombineThreads>(passes, scratch[1], below, passes_all);
-  block_scan<kCombineThreads>(tiles_before, scratch[2], below, tiles_pre);
+  block_scan<kCombineThreads>(work_before, scratch[2], below, work_pre);
   block_scan<kCombineThreads>(passes_before, scratch[3], below, passes_pre);
-  const TreeStream st = tree_stream(a, tiles_all, passes_all);
+  const TreeStream st = tree_stream(a, work_all, passes_all);
   const int unit = row_block / a.unit_rows;  // (unit_rows is a multiple of kCombineRows)
-  // the pass's first tile in the stream, and the shares that hold its tiles
-  const int start = tiles_pre + st.pass_cost * passes_pre +
-                    (j * z.units + unit) * (z.tiles + st.pass_cost) + st.pass_cost;
-  const int c0 = start / st.share, c1 = (start + z.tiles - 1) / st.share;
+  // the pass's tiles in the stream, and the shares that hold the ends of its first and last
+  const int tile = unit == z.units - 1 ? z.last_tile : a.wide_tile;
+  const int start = work_pre + st.pass_cost * passes_pre +
+                    j * (tree_work(a, z) + z.units * st.pass_cost) +
+                    unit * (z.tiles * a.wide_tile + st.pass_cost) + st.pass_cost;
+  const int c0 = (start + tile - 1) / st.share, c1 = (start + z.tiles * tile - 1) / st.share;
   if (c0 == c1) {
     if (first_block) asm volatile("griddepcontrol.wait;" ::: "memory");
     return;

@@ -824,10 +824,29 @@ __global__ void __launch_bounds__(TcShape<KV, D>::THREADS, 1) tree_tc_kernel(
       uint32_t any_bad = 0;
 #pragma unroll
       for (int k = 0; k < 8; ++k) any_bad |= bad[k];
-      // 32 dims from c on of this thread's row: finished, or a partial
+      // 32 dims from c on of this thread's row: finished, or a partial. Rows leave as they came: 64
+      // bytes of each at a time through shared memory, four lanes writing a row's.
+      const uint32_t stage = ring + S::OFF_Q + warp * 2048;
+      const size_t out_off = row_at(run, me);
+      const int part0 = ((int)blockIdx.x * 2 + run.slot) * kTreeTcRows + me.row - lane;
+      auto leave = [&](const uint32_t (&v)[16], auto&& address) {
+        __syncwarp();
+#pragma unroll
+        for (int c4 = 0; c4 < 4; ++c4)
+          sts128(stage + lane * 64 + ((c4 ^ ((lane >> 1) & 3)) << 4),
+                 make_uint4(v[4 * c4], v[4 * c4 + 1], v[4 * c4 + 2], v[4 * c4 + 3]));
+        __syncwarp();
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          const int row = 8 * g + (lane >> 2);
+          const uint4 x = lds128(stage + row * 64 + (((lane & 3) ^ ((row >> 1) & 3)) << 4));
+          const size_t at = __shfl_sync(0xffffffffu, (unsigned long long)out_off, row);
+          if (__shfl_sync(0xffffffffu, (int)live, row))
+            *reinterpret_cast<uint4*>(address(row, at) + 16 * (lane & 3)) = x;
+        }
+      };
       auto emit = [&](int c, uint32_t (&o)[32]) {
-        if (!live) return;
-        if (any_bad) {  // the infinite and NaN values of the nodes this row sees
+        if (any_bad && live) {  // the infinite and NaN values of the nodes this row sees
           for (int nd = 0; nd < run.req.nodes; ++nd) {
             if (!((bad[nd >> 5] >> (nd & 31)) & 1)) continue;
             const int pos = run.req.base + nd;
@@ -847,28 +866,25 @@ __global__ void __launch_bounds__(TcShape<KV, D>::THREADS, 1) tree_tc_kernel(
             }
           }
         }
+        uint32_t v[16];
         if (run.whole) {
-          __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.out) + row_at(run, me) + c;
 #pragma unroll
-          for (int k = 0; k < 32; k += 8) {
-            uint4 v;
-            uint32_t* w = &v.x;
-#pragma unroll
-            for (int m = 0; m < 4; ++m)
-              w[m] = L != 0.f ? pack_bf16(__uint_as_float(o[k + 2 * m]) * f,
-                                          __uint_as_float(o[k + 2 * m + 1]) * f)
-                              : 0u;
-            *reinterpret_cast<uint4*>(dst + k) = v;
-          }
+          for (int k = 0; k < 16; ++k)
+            v[k] = L != 0.f ? pack_bf16(__uint_as_float(o[2 * k]) * f, __uint_as_float(o[2 * k + 1]) * f)
+                            : 0u;
+          leave(v, [&](int, size_t at) { return static_cast<uint8_t*>(a.out) + 2 * (at + c); });
         } else {
-          const size_t part = ((size_t)blockIdx.x * 2 + run.slot) * kTreeTcRows + me.row;
-          float* dst = a.ws_acc + part * D + c;
 #pragma unroll
-          for (int k = 0; k < 32; k += 4)
-            *reinterpret_cast<float4*>(dst + k) =
-                make_float4(__uint_as_float(o[k]) * f, __uint_as_float(o[k + 1]) * f,
-                            __uint_as_float(o[k + 2]) * f, __uint_as_float(o[k + 3]) * f);
-          if (c == 0) *reinterpret_cast<float2*>(a.ws_ml + 2 * part) = make_float2(M, L);
+          for (int h = 0; h < 2; ++h) {
+#pragma unroll
+            for (int k = 0; k < 16; ++k)
+              v[k] = __float_as_uint(__uint_as_float(o[16 * h + k]) * f);
+            leave(v, [&](int row, size_t) {
+              return reinterpret_cast<uint8_t*>(a.ws_acc + (size_t)(part0 + row) * D + c + 16 * h);
+            });
+          }
+          if (c == 0 && live)
+            *reinterpret_cast<float2*>(a.ws_ml + 2 * (size_t)(part0 + lane)) = make_float2(M, L);
         }
       };
       // the next query first, so that the next unit's scores run while this one's rows are written

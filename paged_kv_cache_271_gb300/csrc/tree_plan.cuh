@@ -3,16 +3,17 @@
 //
 // Request b reads its cached positions in tiles of tile_tokens; its (node, query head) rows of one
 // KV head are cut into units of unit_rows. A (KV head, unit) of b is one pass over b's tiles, and
-// the tiles of all passes of all requests, in order, form one stream. Each CTA takes an equal
-// contiguous share of it, whatever the lengths: no CTA idles beside a long request, and few rows
-// over a long context still fill the GPU. Beginning a pass (its queries, its output) costs a CTA
-// about as much as pass_cost tiles, so in calls of many tiles per CTA every pass counts that much
-// more, before its first tile: shares with many short passes get fewer tiles. A pass that lies in one
-// share is finished by its CTA; one
-// that crosses shares leaves a partial (running maximum, sum, weighted values) in each, at most
-// two per CTA (slot 0: the pass began in an earlier share; slot 1: it began here and goes on),
-// which the combine merges in share order. The split depends on the lengths and the grid alone, so
-// equal inputs give equal results.
+// the passes of all requests, in order, form one stream. Each CTA takes an equal contiguous share of
+// it, whatever the lengths: no CTA idles beside a long request, and few rows over a long context
+// still fill the GPU. The stream is measured in half tiles of work: a tile of a pass of up to
+// narrow_rows rows counts 2, of a wider one wide_tile; and beginning a pass (its queries, its
+// output) costs a CTA as much as pass_cost, so in calls of many tiles per CTA every pass is that
+// much longer, at its beginning: shares with many short passes get fewer tiles. A tile belongs to
+// the share that holds its end. A pass whose tiles lie in one share is finished by its CTA; one that
+// crosses shares leaves a partial (running maximum, sum, weighted values) in each, at most two per
+// CTA (slot 0: the pass began in an earlier share; slot 1: it began here and goes on), which the
+// combine merges in share order. The split depends on the lengths and the grid alone, so equal
+// inputs give equal results.
 #pragma once
 
 #include <stdint.h>
@@ -49,14 +50,21 @@ __device__ __forceinline__ TreeReq tree_request(const TreeArgs& a, int b) {
 }
 
 struct TreeSize {
-  int tiles;  // of one pass
-  int units;  // row units of one KV head
+  int tiles;      // of one pass
+  int units;      // row units of one KV head
+  int last_tile;  // half tiles a tile of the last unit counts (of the others: wide_tile)
 };
 
 __device__ __forceinline__ TreeSize tree_size(const TreeArgs& a, const TreeReq& r) {
-  if (r.nodes == 0) return TreeSize{0, 0};
-  return TreeSize{(r.read + a.tile_tokens - 1) / a.tile_tokens,
-                  (r.nodes * a.group + a.unit_rows - 1) / a.unit_rows};
+  if (r.nodes == 0) return TreeSize{0, 0, 2};
+  const int rows = r.nodes * a.group, units = (rows + a.unit_rows - 1) / a.unit_rows;
+  return TreeSize{(r.read + a.tile_tokens - 1) / a.tile_tokens, units,
+                  rows - (units - 1) * a.unit_rows > a.narrow_rows ? a.wide_tile : 2};
+}
+
+// Half tiles of one KV head's passes, without what the passes cost besides.
+__device__ __forceinline__ int tree_work(const TreeArgs& a, const TreeSize& z) {
+  return z.units == 0 ? 0 : z.tiles * ((z.units - 1) * a.wide_tile + z.last_tile);
 }
 
 // Sums over a block: `below` of the values of threads before this one, `total` of all. Shared
@@ -83,22 +91,22 @@ __device__ __forceinline__ void block_scan(int v, int* scratch, int& below, int&
 }
 
 // The stream of a call: its length, what a pass costs beyond its tiles, and a share's length, in
-// tiles. (The host refuses a call whose table could hold 2^30 of them: positions are ints.)
+// half tiles. (The host refuses a call whose table could hold 2^30 of them: positions are ints.)
 struct TreeStream {
   int total, pass_cost, share;
 };
 
-__device__ __forceinline__ TreeStream tree_stream(const TreeArgs& a, int tiles, int passes) {
+__device__ __forceinline__ TreeStream tree_stream(const TreeArgs& a, int work, int passes) {
   TreeStream s;
-  s.pass_cost = tiles >= 16 * a.ctas ? a.pass_cost : 0;
-  s.total = tiles + s.pass_cost * passes;
-  s.share = max(a.min_tiles, (int)(((unsigned)s.total + a.ctas - 1) / (unsigned)a.ctas));
+  s.pass_cost = work >= 32 * a.ctas ? 2 * a.pass_cost : 0;
+  s.total = work + s.pass_cost * passes;
+  s.share = max(2 * a.min_tiles, (int)(((unsigned)s.total + a.ctas - 1) / (unsigned)a.ctas));
   return s;
 }
 
 // A request's part of the stream.
 __device__ __forceinline__ int tree_length(const TreeArgs& a, const TreeSize& z, int pass_cost) {
-  return (z.tiles + pass_cost) * z.units * a.h_kv;
+  return (tree_work(a, z) + z.units * pass_cost) * a.h_kv;
 }
 
 // A CTA's share: from request b on, `off` into that request's part of the stream, `count` long.
@@ -112,21 +120,21 @@ template <int THREADS>
 __device__ __forceinline__ void tree_share(const TreeArgs& a, int* scratch, TreeShare* out) {
   const int per = (a.batch + THREADS - 1) / THREADS;
   const int b0 = min(a.batch, (int)threadIdx.x * per), b1 = min(a.batch, b0 + per);
-  int tiles = 0, passes = 0, err = 0;
+  int work = 0, passes = 0, err = 0;
   for (int b = b0; b < b1; ++b) {
     const TreeReq r = tree_request(a, b);
     const TreeSize z = tree_size(a, r);
     err |= r.err;
-    tiles += z.tiles * z.units * a.h_kv;
+    work += tree_work(a, z) * a.h_kv;
     passes += z.units * a.h_kv;
   }
   if (err && blockIdx.x == 0) atomicOr(a.err, err);
   if (threadIdx.x == 0) out->count = 0;
-  int tiles_below, tiles_all, passes_below, passes_all;
-  block_scan<THREADS>(tiles, scratch, tiles_below, tiles_all);
+  int work_below, work_all, passes_below, passes_all;
+  block_scan<THREADS>(work, scratch, work_below, work_all);
   block_scan<THREADS>(passes, scratch + 32, passes_below, passes_all);
-  const TreeStream s = tree_stream(a, tiles_all, passes_all);
-  const int mine = tiles + s.pass_cost * passes, below = tiles_below + s.pass_cost * passes_below;
+  const TreeStream s = tree_stream(a, work_all, passes_all);
+  const int mine = work + s.pass_cost * passes, below = work_below + s.pass_cost * passes_below;
   const long long start = (long long)blockIdx.x * s.share;
   if (start >= below && start < (long long)below + mine) {
     int at = below, b = b0;
@@ -160,20 +168,29 @@ struct TreeWalk {
   TreeReq req;  // of request b
   TreeSize z;
   int j, unit, x;  // KV head, unit and offset in its pass of the next run
+  int wide_tile;
   __device__ __forceinline__ TreeWalk(const TreeArgs& a, const TreeShare& s)
       : b(s.b), left(s.count), pass_cost(s.pass_cost) {
     if (left <= 0) return;
     load(a);
-    const unsigned len = z.tiles + pass_cost, pass = (unsigned)s.off / len;
-    x = s.off - pass * len;
-    j = pass / (unsigned)z.units;
-    unit = pass - j * z.units;
+    const int head = tree_work(a, z) + z.units * pass_cost;  // of one KV head
+    j = (int)((unsigned)s.off / (unsigned)head);
+    x = s.off - j * head;
+    while (unit < z.units - 1 && x >= length()) {
+      x -= length();
+      ++unit;
+    }
   }
   __device__ __forceinline__ void load(const TreeArgs& a) {
     req = tree_request(a, b);
     z = tree_size(a, req);
+    wide_tile = a.wide_tile;
     j = unit = x = 0;
   }
+  __device__ __forceinline__ int tile() const {
+    return unit == z.units - 1 ? z.last_tile : wide_tile;
+  }
+  __device__ __forceinline__ int length() const { return z.tiles * tile() + pass_cost; }
   __device__ __forceinline__ bool next(const TreeArgs& a, TreeRun& r) {
     while (left > 0) {
       if (j >= a.h_kv || z.units == 0) {
@@ -181,17 +198,19 @@ struct TreeWalk {
         load(a);
         continue;
       }
-      const int len = z.tiles + pass_cost;  // of a pass, its cost first
+      const int len = length(), per = tile();
       const int x0 = x, x1 = min(len, x0 + left);
+      const int tile0 = (int)((unsigned)max(0, x0 - pass_cost) / (unsigned)per);
+      const int tile1 = (int)((unsigned)max(0, x1 - pass_cost) / (unsigned)per);
       r.req = req;
       r.b = b;
       r.j = j;
       r.row0 = unit * a.unit_rows;
       r.rows = min(a.unit_rows, req.nodes * a.group - r.row0);
-      r.tile0 = max(0, x0 - pass_cost);
-      r.n = x1 - pass_cost - r.tile0;
+      r.tile0 = tile0;
+      r.n = tile1 - tile0;
       r.whole = r.n == z.tiles;
-      r.slot = r.tile0 > 0 ? 0 : 1;
+      r.slot = tile0 > 0 ? 0 : 1;
       left -= x1 - x0;
       x = x1;
       if (x == len) {
@@ -201,7 +220,7 @@ struct TreeWalk {
           ++j;
         }
       }
-      if (x1 > pass_cost) return true;  // (it has some of the pass's tiles)
+      if (tile1 > tile0) return true;
     }
     return false;
   }
