@@ -27,11 +27,14 @@ namespace {
 constexpr int kThreads = 128;
 constexpr int kRows = kTreeSimtRows, kTok = kTreeSimtTokens;
 
-template <int D>
+template <typename KV, int D>
 struct SimtShape {
   static constexpr int LD = D + 4;   // row pitch (floats): keeps float4 alignment, spreads banks
   static constexpr int LP = kTok + 4;
-  static constexpr int SMEM = 4 * (3 * kRows * LD + kRows * LP);
+  // an fp32 cache's next tile is copied (cp.async) while this one is worked on: two K and V tiles
+  static constexpr bool AHEAD = KV::bytes == 4;
+  static constexpr int TILES = AHEAD ? 2 : 1;
+  static constexpr int SMEM = 4 * ((1 + 2 * TILES) * kRows * LD + kRows * LP);
 };
 static_assert(kRows == kTok, "Q, K and V tiles have the same shape");
 
@@ -54,17 +57,23 @@ __device__ __forceinline__ void store4(float* p, const float4& v) {
   *reinterpret_cast<float4*>(p) = v;
 }
 
+// 16 bytes from global to shared memory, asynchronously; zeros when the source is not there.
+__device__ __forceinline__ void copy16(float* dst, const void* src, bool there) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src),
+               "r"(there ? 16 : 0)
+               : "memory");
+}
+
 template <typename KV, typename Q, int D>
 __global__ void __launch_bounds__(kThreads) tree_simt_kernel(const TreeArgs a) {
-  using S = SimtShape<D>;
+  using S = SimtShape<KV, D>;
   using TQ = typename Q::storage;
   constexpr int NQ = D / 64;  // float4 groups of dims a thread accumulates, 64 dims apart
   constexpr int LD = S::LD, LP = S::LP;
   extern __shared__ float4 smem4[];
   float* qs = reinterpret_cast<float*>(smem4);
-  float* ks = qs + kRows * LD;
-  float* vs = ks + kTok * LD;
-  float* ps = vs + kTok * LD;
+  float* tiles = qs + kRows * LD;  // K and V of a tile, of the next one behind them
+  float* ps = tiles + 2 * S::TILES * kTok * LD;
   __shared__ int scratch[64];
   __shared__ TreeShare share;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -95,8 +104,30 @@ __global__ void __launch_bounds__(kThreads) tree_simt_kernel(const TreeArgs a) {
     }
     const float sc = a.scale_log2 * (KV::bytes == 1 ? a.k_scales[j] : 1.f);
     const int32_t* table = a.block_tables + (size_t)b * a.max_pages;
-    for (int tile = run.tile0; tile < run.tile0 + run.n; ++tile) {
-      const int p0 = tile * kTok;
+    // a tile's K and V, widened, into buffer `at`; rows past the context or on a bad page are zero
+    auto fetch = [&](int tile, float* at) {
+      for (int e = threadIdx.x; e < kTok * (D / 4); e += kThreads) {
+        const int r = e / (D / 4), c = e % (D / 4), pos = tile * kTok + r;
+        const int id = pos < run.req.read ? table[pos / kPageSize] : -1;
+        const bool there = id >= 0 && id < a.num_pages;
+        const int64_t from =
+            there ? (((int64_t)id * a.h_kv + j) * kPageSize + pos % kPageSize) * D + 4 * c : 0;
+        float* k = at + r * LD + 4 * c;
+        float* v = k + kTok * LD;
+        if constexpr (S::AHEAD) {
+          copy16(k, static_cast<const float*>(a.k_cache) + from, there);
+          copy16(v, static_cast<const float*>(a.v_cache) + from, there);
+        } else {
+          const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
+          *reinterpret_cast<float4*>(k) = there ? load4<KV>(a.k_cache, from) : zero;
+          *reinterpret_cast<float4*>(v) = there ? load4<KV>(a.v_cache, from) : zero;
+        }
+      }
+      if constexpr (S::AHEAD) asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    if constexpr (S::AHEAD) fetch(run.tile0, tiles);
+    for (int i0 = 0; i0 < run.n; ++i0) {
+      const int tile = run.tile0 + i0, p0 = tile * kTok;
       const bool tail = p0 + kTok > min(run.req.base, run.req.read);  // not all positions seen
       uint32_t page_ok = 0;  // one bit per token
 #pragma unroll
@@ -108,19 +139,20 @@ __global__ void __launch_bounds__(kThreads) tree_simt_kernel(const TreeArgs a) {
         else if (lp * kPageSize < run.req.read && threadIdx.x == 0)
           atomicOr(a.err, PKV_DEVERR_BAD_PAGE);
       }
-      __syncthreads();  // the previous tile is used up (and Q is stored)
-      for (int e = threadIdx.x; e < kTok * (D / 4); e += kThreads) {
-        const int r = e / (D / 4), c = e % (D / 4);
-        float4 kv = make_float4(0.f, 0.f, 0.f, 0.f), vv = kv;
-        if (p0 + r < run.req.read && ((page_ok >> r) & 1)) {
-          const int64_t row = ((int64_t)table[(p0 + r) / kPageSize] * a.h_kv + j) * kPageSize +
-                              (p0 + r) % kPageSize;
-          kv = load4<KV>(a.k_cache, row * D + 4 * c);
-          vv = load4<KV>(a.v_cache, row * D + 4 * c);
+      float* ks = tiles;
+      if constexpr (S::AHEAD) {
+        ks = tiles + (i0 & 1) * 2 * kTok * LD;
+        if (i0 + 1 < run.n) {
+          fetch(tile + 1, tiles + (~i0 & 1) * 2 * kTok * LD);
+          asm volatile("cp.async.wait_group 1;" ::: "memory");
+        } else {
+          asm volatile("cp.async.wait_group 0;" ::: "memory");
         }
-        *reinterpret_cast<float4*>(ks + r * LD + 4 * c) = kv;
-        *reinterpret_cast<float4*>(vs + r * LD + 4 * c) = vv;
+      } else {
+        __syncthreads();  // the previous tile is used up
+        fetch(tile, tiles);
       }
+      const float* vs = ks + kTok * LD;
       __syncthreads();
       // ---- scores of rows 4 ty + i, tokens tx and tx + 16 ----
       float s[4][2];
@@ -139,6 +171,7 @@ __global__ void __launch_bounds__(kThreads) tree_simt_kernel(const TreeArgs a) {
       }
       // ---- online softmax; a row's 16 threads hold the same m and l ----
       uint32_t seen[4];
+      float scale[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int R = 4 * ty + i;
@@ -161,18 +194,18 @@ __global__ void __launch_bounds__(kThreads) tree_simt_kernel(const TreeArgs a) {
         for (int o = 8; o >= 1; o /= 2) sum += __shfl_xor_sync(0xffffffffu, sum, o);
         l[i] = fmaf(l[i], alpha, sum);
         m[i] = mn;
-#pragma unroll
-        for (int k = 0; k < NQ; ++k) {
-          acc[i][k].x *= alpha;
-          acc[i][k].y *= alpha;
-          acc[i][k].z *= alpha;
-          acc[i][k].w *= alpha;
-        }
+        scale[i] = alpha;
         ps[R * LP + tx] = e0;
         ps[R * LP + tx + 16] = e1;
       }
       __syncwarp();  // a row's P is written and read by the same half warp
-      // ---- weighted values of rows 4 ty + i, dims 4 tx + 64 k .. ----
+      // ---- weighted values of rows 4 ty + i, dims 4 tx + 64 k ..: the tile's own sums first, so that
+      // a long context's sums do not round once per token against the whole ----
+      float4 own[4][NQ];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int k = 0; k < NQ; ++k) own[i][k] = make_float4(0.f, 0.f, 0.f, 0.f);
       if (!tail && page_ok == 0xffffffffu) {
 #pragma unroll 4
         for (int t = 0; t < kTok; ++t) {
@@ -183,7 +216,7 @@ __global__ void __launch_bounds__(kThreads) tree_simt_kernel(const TreeArgs a) {
           for (int k = 0; k < NQ; ++k) {
             const float4 v = *reinterpret_cast<const float4*>(vs + t * LD + 4 * tx + 64 * k);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) fma4(acc[i][k], p[i], v);
+            for (int i = 0; i < 4; ++i) fma4(own[i][k], p[i], v);
           }
         }
       } else {  // an unseen value may be infinite or NaN: it takes no part at all
@@ -194,10 +227,20 @@ __global__ void __launch_bounds__(kThreads) tree_simt_kernel(const TreeArgs a) {
             const float p = ps[(4 * ty + i) * LP + t];
 #pragma unroll
             for (int k = 0; k < NQ; ++k)
-              fma4(acc[i][k], p, *reinterpret_cast<const float4*>(vs + t * LD + 4 * tx + 64 * k));
+              fma4(own[i][k], p, *reinterpret_cast<const float4*>(vs + t * LD + 4 * tx + 64 * k));
           }
         }
       }
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int k = 0; k < NQ; ++k) {
+          acc[i][k].x = fmaf(acc[i][k].x, scale[i], own[i][k].x);
+          acc[i][k].y = fmaf(acc[i][k].y, scale[i], own[i][k].y);
+          acc[i][k].z = fmaf(acc[i][k].z, scale[i], own[i][k].z);
+          acc[i][k].w = fmaf(acc[i][k].w, scale[i], own[i][k].w);
+        }
+      if constexpr (S::AHEAD) __syncthreads();  // the tile after the next may overwrite this one
     }
     // ---- the run's rows: finished, or a partial ----
     const float vsc = KV::bytes == 1 ? a.v_scales[j] : 1.f;
@@ -237,18 +280,21 @@ __global__ void __launch_bounds__(kThreads) tree_simt_kernel(const TreeArgs a) {
 // ---- combine ---------------------------------------------------------------------------------
 
 // Rows of the passes that crossed shares: with partials c = 0 .. n-1 of a row in share order,
-// M = max m_c, out = sum 2^(m_c - M) acc_c / sum 2^(m_c - M) l_c. A warp merges one row at a time;
-// it reads the (m, l) pairs of up to 32 partials at once and the values of eight together. Launched
-// as a programmatic dependent: the split is worked out while the attention still runs.
+// M = max m_c, out = sum 2^(m_c - M) acc_c / sum 2^(m_c - M) l_c. A warp merges RW rows, reading
+// the (m, l) pairs of up to 32 partials of each at once and the values of CB partials of each
+// together: a row is two reads that wait on one another, so what counts is how many are under way.
+// Few rows in all: one row per warp; many: four, in fewer blocks, each of which has to find its place
+// in the split first. Launched as a programmatic dependent: blocks that start early find it while
+// the attention still runs.
 constexpr int kCombineThreads = 128;
-constexpr int kCombineRows = 16;  // rows of a block
+constexpr int kCombineWarps = kCombineThreads / 32;
 
-template <typename TQ, int D>
+template <typename TQ, int D, int RW, int CB>
 __global__ void __launch_bounds__(kCombineThreads) tree_combine_kernel(const TreeArgs a) {
   constexpr int DL = D / 32;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int j = blockIdx.y, b = blockIdx.z;
-  const int row_block = blockIdx.x * kCombineRows;
+  const int row_block = blockIdx.x * (kCombineWarps * RW);
   __shared__ int scratch[4][32];
   const TreeReq req = tree_request(a, b);
   const TreeSize z = tree_size(a, req);
@@ -276,7 +322,7 @@ __global__ void __launch_bounds__(kCombineThreads) tree_combine_kernel(const Tre
   block_scan<kCombineThreads>(work_before, scratch[2], below, work_pre);
   block_scan<kCombineThreads>(passes_before, scratch[3], below, passes_pre);
   const TreeStream st = tree_stream(a, work_all, passes_all);
-  const int unit = row_block / a.unit_rows;  // (unit_rows is a multiple of kCombineRows)
+  const int unit = row_block / a.unit_rows;  // (a block's rows lie in one unit)
   // the pass's tiles in the stream, and the shares that hold the ends of its first and last
   const int tile = unit == z.units - 1 ? z.last_tile : a.wide_tile;
   const int start = work_pre + st.pass_cost * passes_pre +
@@ -289,63 +335,83 @@ __global__ void __launch_bounds__(kCombineThreads) tree_combine_kernel(const Tre
   }
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int n = c1 - c0 + 1;
-  for (int rr = warp; rr < kCombineRows; rr += kCombineThreads / 32) {
-    const int R = row_block + rr;
-    if (R >= rows) break;
-    const int r = R - unit * a.unit_rows;
-    auto part = [&](int c) {  // partial c of the pass (it begins in share c0)
-      return ((size_t)(c0 + c) * 2 + (c == 0 ? 1 : 0)) * a.unit_rows + r;
-    };
-    float M = -INFINITY, L = 0.f, A[DL];
+  const int first = row_block + warp * RW;  // this warp's rows
+  const int live = min(RW, rows - first);
+  if (live <= 0) return;
+  auto part = [&](int i, int c) {  // partial c of row first + i (the pass begins in share c0)
+    return ((size_t)(c0 + c) * 2 + (c == 0 ? 1 : 0)) * a.unit_rows + first + min(i, live - 1) -
+           unit * a.unit_rows;
+  };
+  float M[RW], L[RW], A[RW][DL];
 #pragma unroll
-    for (int k = 0; k < DL; ++k) A[k] = 0.f;
-    for (int q0 = 0; q0 < n; q0 += 32) {
-      const int nc = min(32, n - q0);
-      float2 ml = make_float2(-INFINITY, 0.f);
-      if (lane < nc) ml = *reinterpret_cast<const float2*>(a.ws_ml + 2 * part(q0 + lane));
-      float mr = ml.x;
+  for (int i = 0; i < RW; ++i) {
+    M[i] = -INFINITY;
+    L[i] = 0.f;
+#pragma unroll
+    for (int k = 0; k < DL; ++k) A[i][k] = 0.f;
+  }
+  for (int q0 = 0; q0 < n; q0 += 32) {
+    const int nc = min(32, n - q0);
+    float2 ml[RW];
+#pragma unroll
+    for (int i = 0; i < RW; ++i) {
+      ml[i] = make_float2(-INFINITY, 0.f);
+      if (lane < nc) ml[i] = *reinterpret_cast<const float2*>(a.ws_ml + 2 * part(i, q0 + lane));
+    }
+    float w[RW];
+#pragma unroll
+    for (int i = 0; i < RW; ++i) {
+      float mr = ml[i].x;
 #pragma unroll
       for (int o = 16; o >= 1; o /= 2) mr = fmaxf(mr, __shfl_xor_sync(0xffffffffu, mr, o));
-      const float Mn = fmaxf(M, mr);
+      const float Mn = fmaxf(M[i], mr);
       const float Mu = Mn == -INFINITY ? 0.f : Mn;
-      const float rescale = exp2f(M - Mu);
+      const float rescale = exp2f(M[i] - Mu);
       // a partial that saw nothing weighs 0; a NaN sum stays one whatever its weight
-      const float w = ml.x == -INFINITY ? 0.f : exp2f(ml.x - Mu);
-      float lw = w != 0.f || ml.y != ml.y ? w * ml.y : 0.f;
+      w[i] = ml[i].x == -INFINITY ? 0.f : exp2f(ml[i].x - Mu);
+      float lw = w[i] != 0.f || ml[i].y != ml[i].y ? w[i] * ml[i].y : 0.f;
 #pragma unroll
       for (int o = 16; o >= 1; o /= 2) lw += __shfl_xor_sync(0xffffffffu, lw, o);
-      L = fmaf(L, rescale, lw);
+      L[i] = fmaf(L[i], rescale, lw);
 #pragma unroll
-      for (int k = 0; k < DL; ++k) A[k] *= rescale;
-      M = Mn;
-      for (int q = 0; q < nc; q += 8) {
-        float v[8][DL];
+      for (int k = 0; k < DL; ++k) A[i][k] *= rescale;
+      M[i] = Mn;
+    }
+    for (int q = 0; q < nc; q += CB) {
+      float v[RW][CB][DL];
 #pragma unroll
-        for (int u = 0; u < 8; ++u) {
-          const float* src = a.ws_acc + part(q0 + min(q + u, nc - 1)) * D + lane * DL;
+      for (int i = 0; i < RW; ++i)
+#pragma unroll
+        for (int u = 0; u < CB; ++u) {
+          const float* src = a.ws_acc + part(i, q0 + min(q + u, nc - 1)) * D + lane * DL;
           if constexpr (DL == 4) {
             const float4 x = *reinterpret_cast<const float4*>(src);
-            v[u][0] = x.x; v[u][1] = x.y; v[u][2] = x.z; v[u][3] = x.w;
+            v[i][u][0] = x.x; v[i][u][1] = x.y; v[i][u][2] = x.z; v[i][u][3] = x.w;
           } else {
             const float2 x = *reinterpret_cast<const float2*>(src);
-            v[u][0] = x.x; v[u][1] = x.y;
+            v[i][u][0] = x.x; v[i][u][1] = x.y;
           }
         }
 #pragma unroll
-        for (int u = 0; u < 8; ++u) {
-          const float wu = __shfl_sync(0xffffffffu, w, (q + u) & 31);
+      for (int i = 0; i < RW; ++i)
+#pragma unroll
+        for (int u = 0; u < CB; ++u) {
+          const float wu = __shfl_sync(0xffffffffu, w[i], (q + u) & 31);
           if (q + u < nc && wu != 0.f) {
 #pragma unroll
-            for (int k = 0; k < DL; ++k) A[k] = fmaf(wu, v[u][k], A[k]);
+            for (int k = 0; k < DL; ++k) A[i][k] = fmaf(wu, v[i][u][k], A[i][k]);
           }
         }
-      }
     }
-    const int t = R / a.group, g = R % a.group;
+  }
+#pragma unroll
+  for (int i = 0; i < RW; ++i) {
+    if (i >= live) break;
+    const int R = first + i, t = R / a.group, g = R % a.group;
     TQ* o = static_cast<TQ*>(a.out) + (((int64_t)b * a.nodes + t) * a.h_q + j * a.group + g) * D +
             lane * DL;
 #pragma unroll
-    for (int k = 0; k < DL; ++k) store_from_float(o, k, L != 0.f ? A[k] / L : 0.f);
+    for (int k = 0; k < DL; ++k) store_from_float(o, k, L[i] != 0.f ? A[i][k] / L[i] : 0.f);
   }
 }
 
@@ -357,11 +423,11 @@ cudaError_t simt_go(const TreeArgs& a, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   if (dev >= 64 || !((attr_done.load() >> dev) & 1ull)) {
     e = cudaFuncSetAttribute(tree_simt_kernel<KV, Q, D>,
-                             cudaFuncAttributeMaxDynamicSharedMemorySize, SimtShape<D>::SMEM);
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, SimtShape<KV, D>::SMEM);
     if (e != cudaSuccess) return e;
     if (dev < 64) attr_done.fetch_or(1ull << dev);
   }
-  tree_simt_kernel<KV, Q, D><<<a.ctas, kThreads, SimtShape<D>::SMEM, s>>>(a);
+  tree_simt_kernel<KV, Q, D><<<a.ctas, kThreads, SimtShape<KV, D>::SMEM, s>>>(a);
   return cudaGetLastError();
 }
 
@@ -372,10 +438,12 @@ cudaError_t simt_types(const TreeArgs& a, int kv_dtype, cudaStream_t s) {
   return simt_go<INT8, F32, D>(a, s);
 }
 
-template <typename TQ, int D>
-cudaError_t launch_combine(const TreeArgs& a, cudaStream_t s) {
+template <typename TQ, int D, int RW, int CB>
+cudaError_t launch_combine_rows(const TreeArgs& a, cudaStream_t s) {
+  constexpr int R = kCombineWarps * RW;
+  static_assert(kTreeSimtRows % R == 0 && kTreeTcRows % R == 0, "a block's rows lie in one unit");
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((a.nodes * a.group + kCombineRows - 1) / kCombineRows, a.h_kv, a.batch);
+  cfg.gridDim = dim3((a.nodes * a.group + R - 1) / R, a.h_kv, a.batch);
   cfg.blockDim = dim3(kCombineThreads);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
@@ -383,7 +451,15 @@ cudaError_t launch_combine(const TreeArgs& a, cudaStream_t s) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, tree_combine_kernel<TQ, D>, a);
+  return cudaLaunchKernelEx(&cfg, tree_combine_kernel<TQ, D, RW, CB>, a);
+}
+
+template <typename TQ, int D>
+cudaError_t launch_combine(const TreeArgs& a, cudaStream_t s) {
+  // one row per warp while its blocks are resident at once
+  const long long rows = (long long)a.nodes * a.group * a.h_kv * a.batch;
+  return rows <= 152 * 7 * kCombineWarps ? launch_combine_rows<TQ, D, 1, 16>(a, s)
+                                         : launch_combine_rows<TQ, D, 4, 4>(a, s);
 }
 
 }  // namespace
@@ -393,7 +469,6 @@ cudaError_t launch_tree_simt(const TreeArgs& a, int kv_dtype, int head_dim, cuda
 }
 
 cudaError_t launch_tree_combine(const TreeArgs& a, int q_dtype, int head_dim, cudaStream_t s) {
-  static_assert(kTreeSimtRows % kCombineRows == 0, "a combine block lies in one unit");
   if (q_dtype == PKV_BF16)
     return head_dim == 64 ? launch_combine<__nv_bfloat16, 64>(a, s)
                           : launch_combine<__nv_bfloat16, 128>(a, s);
