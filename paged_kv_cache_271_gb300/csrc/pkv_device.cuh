@@ -128,6 +128,15 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, int* e
   }
 }
 
+// Waits for a phase of each of two barriers; both are asked before the first answer is needed.
+__device__ __forceinline__ bool mbar_wait_both(uint64_t* bar0, uint32_t parity0, uint64_t* bar1,
+                                               uint32_t parity1, int* err) {
+  const bool got0 = mbar_try_wait(smem_u32(bar0), parity0);
+  const bool got1 = mbar_try_wait(smem_u32(bar1), parity1);
+  if (got0 && got1) return true;
+  return mbar_wait(bar0, parity0, err) && mbar_wait(bar1, parity1, err);
+}
+
 // ---- bulk copies (TMA, untiled) -----------------------------------------------------------
 
 // Orders this thread's earlier generic-proxy shared-memory accesses before later async-proxy
@@ -157,6 +166,11 @@ __device__ __forceinline__ void bulk_g2s(void* smem_dst, const void* gsrc, uint3
       " [%0], [%1], %2, [%3], %4;" ::"r"(smem_u32(smem_dst)),
       "l"(gsrc), "r"(bytes), "r"(smem_u32(bar)), "l"(policy)
       : "memory");
+}
+
+// Asks for `bytes` (multiple of 16, 16-byte aligned address) to be brought into L2.
+__device__ __forceinline__ void bulk_prefetch_l2(const void* gsrc, uint32_t bytes) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(gsrc), "r"(bytes) : "memory");
 }
 
 // ---- element conversions (all exact) -------------------------------------------------------

@@ -54,14 +54,15 @@ constexpr int kMmaWarp = kSoftThreads / 32;  // two: MMAs of group 0's and of gr
 constexpr int kCopyWarp = kMmaWarp + 2;      // two: copies of K and of V
 constexpr int kConvWarp = kMmaWarp + 4;      // first of four (8-bit caches)
 constexpr int kConvThreads = 128;
-constexpr int kSBufs = 3;
+constexpr int kSBufs = 4;
 // Runs on their way from the K copy warp, which walks the share, to the other warps. It is ahead by
 // the tiles of the rings at most, each a run of its own at worst, besides the run whose rows are
 // being written and the one it is about to copy.
 constexpr int kRuns = 32;
-// tensor memory columns: O of group 0 and 1, Q of the rows 0 .. 127 and 128 .. 255, S (then P)
-// buffers; the third S buffer shares the second Q's columns (units of up to 128 rows have one Q)
-constexpr uint32_t kColO = 0, kColQ = 256, kColS = 384, kColS2 = 320;
+// tensor memory columns: O, Q and S (then P) buffers. Units of up to 128 rows: one O, one Q and four
+// S buffers, two of them in the columns that larger units use for the second O; larger units: an O,
+// a Q and an S buffer for each group.
+constexpr uint32_t kColO = 0, kColQ = 256, kColS = 384;
 constexpr uint32_t kTmemCols = 512;
 constexpr float kLazyLog2 = 8.f;
 static_assert(2 * kGroupThreads == kTreeTcRows, "a unit is two groups' rows");
@@ -83,8 +84,9 @@ struct TcShape {
   static constexpr int OFF_RAW = OFF_V + NV * TILE;
   static constexpr int OFF_Q = OFF_RAW + NR * RAW_STAGE;    // 2 KB per softmax warp
   static constexpr int OFF_ML = OFF_Q + kSoftThreads / 32 * 2048;  // [2][128] (max, sum)
-  static constexpr int OFF_BAR = OFF_ML + 2 * kGroupThreads * 8;
-  static constexpr int BARS = 2 * NK + 2 * NV + 2 * NR + 3 * kSBufs + 4 + kRuns;
+  static constexpr int OFF_REF = OFF_ML + 2 * kGroupThreads * 8;   // [128] reference maxima
+  static constexpr int OFF_BAR = OFF_REF + kGroupThreads * 4;
+  static constexpr int BARS = 2 * NK + 2 * NV + 2 * NR + 3 * kSBufs + 6 + kRuns;
   static_assert(NK + NR + 3 <= kRuns, "runs in flight");
   static constexpr int OFF_MISC = OFF_BAR + 8 * BARS;       // masks, bad nodes, TMEM address
   static constexpr uint32_t IDESC_S = tc_idesc(128, kTok, false, W8);
@@ -94,33 +96,22 @@ struct TcShape {
 };
 
 __device__ __forceinline__ uint32_t s_col(int buf) {
-  return buf == 2 ? kColS2 : kColS + 64 * buf;
+  return buf < 2 ? kColS + 64 * buf : kColO + 64 * buf;
 }
 
 // A unit's steps in order: with up to 128 rows step u is tile u, otherwise ("wide") tile u / 2 for
-// rows 128 (u % 2) ... Group u % 2 takes it. S buffers go round, 3 or 2 of them; every buffer's
-// three barriers complete once per step that uses it.
-struct Buf {
-  int i;       // buffer
-  uint32_t q;  // parity of its uses in this unit before this step
-  __device__ __forceinline__ void advance(bool wide, int steps) {  // by 1 or 2 steps
-    const int bufs = wide ? 2 : kSBufs;
-    i += steps;
-    if (i >= bufs) {
-      i -= bufs;
-      q ^= 1u;
-    }
-  }
-  // parity of the barriers in this step; ph holds each buffer's at the unit's start
-  __device__ __forceinline__ uint32_t parity(uint32_t ph) const { return ((ph >> i) ^ q) & 1u; }
-};
-
-// The buffers' parities after a unit of n steps.
+// rows 128 (u % 2) ... Group u % 2 takes it, in S buffer u % 4 (wide: u % 2). Every buffer's three
+// barriers complete once per step that uses it.
+__device__ __forceinline__ int buf_of(bool wide, int u) { return wide ? u & 1 : u & 3; }
+// parity of the buffer's barriers in step u; ph holds each buffer's at the unit's start
+__device__ __forceinline__ uint32_t parity_of(uint32_t ph, bool wide, int u) {
+  return ((ph >> buf_of(wide, u)) ^ (uint32_t)(u >> (wide ? 1 : 2))) & 1u;
+}
+// the buffers' parities after a unit of n steps
 __device__ __forceinline__ uint32_t after_steps(uint32_t ph, bool wide, int n) {
   if (wide) return ph ^ ((n >> 1) & 1 ? 3u : 0u);
-  const uint32_t t = (uint32_t)n / 3u, m = (uint32_t)n - 3u * t;
-  if (t & 1) ph ^= 7u;
-  return ph ^ ((1u << m) - 1u);
+  if ((n >> 2) & 1) ph ^= 15u;
+  return ph ^ ((1u << (n & 3)) - 1u);
 }
 
 // A place in a ring of N stages and the parity of its current use.
@@ -140,6 +131,11 @@ struct Place {
     st = t - w * N;
     par ^= (uint32_t)w & 1u;
   }
+};
+
+template <bool B>
+struct BoolConst {
+  static constexpr bool value = B;
 };
 
 template <int N>
@@ -184,21 +180,23 @@ __global__ void __launch_bounds__(TcShape<KV, D>::THREADS, 1) tree_tc_kernel(
   uint64_t* free_v = full_v + NV;                                    // [NV] its P V done
   uint64_t* raw_full = free_v + NV;                                  // [NR] codes arrived
   uint64_t* raw_freed = raw_full + NR;                               // [NR] codes widened
-  uint64_t* s_done = raw_freed + NR;                                 // [3] S in its buffer
-  uint64_t* p_ready = s_done + kSBufs;                               // [3] P in its buffer
-  uint64_t* pv_done = p_ready + kSBufs;                              // [3] that P V complete
+  uint64_t* s_done = raw_freed + NR;                                 // [4] S in its buffer
+  uint64_t* p_ready = s_done + kSBufs;                               // [4] P in its buffer
+  uint64_t* pv_done = p_ready + kSBufs;                              // [4] that P V complete
   // Q of a unit stored; the MMA warps arrive too, for the unit after the one they have seen, so
   // that no phase completes before both have seen the last (one may have no step in a unit)
   uint64_t* q_ready = pv_done + kSBufs;
   uint64_t* o_read = q_ready + 1;                                    // O of a unit read
   uint64_t* met = o_read + 1;                                        // both groups ended a unit
   uint64_t* mma_idle = met + 1;
-  uint64_t* run_there = mma_idle + 1;                                // [kRuns]
+  uint64_t* ref_set = mma_idle + 1;                                  // [2] a group's step set it
+  uint64_t* run_there = ref_set + 2;                                 // [kRuns]
   int* page_mask = reinterpret_cast<int*>(smem + S::OFF_MISC);       // [NV] good pages of the tile
   int* raw_mask = page_mask + NV;                                    // [NR]
   uint32_t* bad_nodes = reinterpret_cast<uint32_t*>(raw_mask + NR);  // [2][8] V row not finite
   uint32_t* s_taddr = bad_nodes + 16;
   float2* ml = reinterpret_cast<float2*>(smem + S::OFF_ML);          // [2][128]
+  float* ref = reinterpret_cast<float*>(smem + S::OFF_REF);          // [128]
 
   __shared__ int scratch[64];
   __shared__ TreeShare share;
@@ -226,6 +224,7 @@ __global__ void __launch_bounds__(TcShape<KV, D>::THREADS, 1) tree_tc_kernel(
     mbar_init(o_read, kSoftThreads / 32);
     mbar_init(met, kSoftThreads / 32);
     mbar_init(mma_idle, 2);
+    for (int g = 0; g < 2; ++g) mbar_init(&ref_set[g], kGroupThreads / 32);
     for (int i = 0; i < kRuns; ++i) mbar_init(&run_there[i], 1);
     mbar_fence_init();
     if constexpr (!W8) {
@@ -292,6 +291,14 @@ __global__ void __launch_bounds__(TcShape<KV, D>::THREADS, 1) tree_tc_kernel(
         const int pages = uniform((run->req.read + kPageSize - 1) / kPageSize);
         const int n = uniform(run->n), j = uniform(run->j);
         const int32_t* table = a.block_tables + (size_t)run->b * a.max_pages;
+        if (is_k) {  // the run's queries into L2, some tiles before their rows are read
+          const int t0 = uniform(run->row0) / a.group;
+          const int t1 = (uniform(run->row0 + run->rows) - 1) / a.group;
+          const uint8_t* q = static_cast<const uint8_t*>(a.q) +
+                             2 * (((size_t)run->b * a.nodes * a.h_q) + (size_t)j * a.group) * D;
+          for (int t = t0 + lane; t <= t1; t += 32)
+            bulk_prefetch_l2(q + 2 * (size_t)t * a.h_q * D, 2 * a.group * D);
+        }
         int lp = uniform(run->tile0 * kPages);  // first page of the tile
         int ids = -1;                          // lane L: the id of page 32 m + L of the run
         for (int i = 0; i < n; ++i, lp += kPages) {
@@ -346,11 +353,11 @@ __global__ void __launch_bounds__(TcShape<KV, D>::THREADS, 1) tree_tc_kernel(
           mbar_wait(&there[t % stages], (uint32_t)(t / stages) & 1u, a.err);
     } else {
       // ===================== MMAs (one elected lane issues) =====================
-      // Two warps, one for each softmax group's steps: issuing a step's MMAs and waiting for its
-      // P V takes about as long as they run, so one warp's waits overlap the other's MMAs.
+      // Two warps, since issuing a step's MMAs takes about as long as they run. Units of up to 128
+      // rows: one issues the S, up to four tiles ahead, the other the P V, all into one O. Larger
+      // ones: each issues the steps of one group, the next S as soon as the P V of its buffer is done.
       const int w = warp - kMmaWarp;
       const uint64_t k_desc = tc_desc(ring, 16, 1024), v_desc = tc_desc(ring + S::OFF_V, 2048, 1024);
-      const uint32_t o = tmem + kColO + 128 * w;
       bool ok = true;
       uint32_t ph = 0, unit = 0;
       Place<NK> k_base;  // the run's first tile
@@ -360,6 +367,31 @@ __global__ void __launch_bounds__(TcShape<KV, D>::THREADS, 1) tree_tc_kernel(
         tc_fence_after();
         return got;
       };
+      auto s_mma = [&](const Place<NK>& k, uint32_t q, int buf) {
+        const uint64_t kd = k_desc + (uint32_t)(k.st * (S::TILE >> 4));
+        const uint32_t d = tmem + s_col(buf);
+        if (elect_one()) {
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk)
+            tc_mma_ta(d, q + 8 * kk, kd + (((kk >> 2) * (kTok * 128) + (kk & 3) * 32) >> 4),
+                      S::IDESC_S, kk > 0 ? 1u : 0u);
+          tc_commit(&s_done[buf]);
+        }
+        __syncwarp();
+      };
+      auto pv_mma = [&](const Place<NV>& v, uint32_t o, int buf, bool first, bool free) {
+        const uint64_t vd = v_desc + (uint32_t)(v.st * (S::TILE >> 4));
+        const uint32_t pc = tmem + s_col(buf);
+        if (elect_one()) {
+#pragma unroll
+          for (int kk = 0; kk < kPages; ++kk)
+            tc_mma_ta(o, pc + 8 * kk, vd + ((kk * PAGE_MMA) >> 4), S::IDESC_PV,
+                      first && kk == 0 ? 0u : 1u);
+          tc_commit(&pv_done[buf]);
+          if (free) tc_commit(&free_v[v.st]);
+        }
+        __syncwarp();
+      };
       if (elect_one()) mbar_arrive(q_ready);
       __syncwarp();
       for (; ok; ++unit) {
@@ -367,65 +399,46 @@ __global__ void __launch_bounds__(TcShape<KV, D>::THREADS, 1) tree_tc_kernel(
         if (!run) break;
         const int tiles = uniform(run->n);
         const bool wide = uniform(run->rows) > kGroupThreads;
-        const int n = wide ? 2 * tiles : tiles, stride = wide ? 1 : 2;  // tiles between steps
+        const int n = wide ? 2 * tiles : tiles;
         Place<NK> ks = k_base;  // K of the next S
         Place<NV> vs = v_base;  // V of the next P V
-        if (!wide) {
-          ks.advance(w);
-          vs.advance(w);
-        }
-        const uint32_t q = tmem + kColQ + (wide ? 64 * w : 0);
+        const uint32_t o_par = (unit - 1) & 1;  // the last unit's O is read (unit > 0)
         ok = wait(q_ready, unit & 1);
         if (elect_one()) mbar_arrive(q_ready);  // (the next unit's: this phase has been seen)
         __syncwarp();
-        auto s_mma = [&](int buf) {
-          const uint64_t kd = k_desc + (uint32_t)(ks.st * (S::TILE >> 4));
-          const uint32_t d = tmem + s_col(buf);
-          if (elect_one()) {
-#pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk)
-              tc_mma_ta(d, q + 8 * kk, kd + (((kk >> 2) * (kTok * 128) + (kk & 3) * 32) >> 4),
-                        S::IDESC_S, kk > 0 ? 1u : 0u);
-            tc_commit(&s_done[buf]);
+        if (wide) {
+          const uint32_t q = tmem + kColQ + 64 * w, o = tmem + kColO + 128 * w;
+          if (ok) ok = wait(&full_k[ks.st], ks.par);
+          if (ok) s_mma(ks, q, w);
+          ks.advance(1);
+          for (int u = w; ok && u < n; u += 2) {
+            const uint32_t par = parity_of(ph, true, u);
+            if (u + 2 < n) ok = wait(&full_k[ks.st], ks.par);  // K of the next S, before P is there
+            if (ok) ok = wait(&p_ready[w], par);
+            if (ok && u < 2 && unit > 0) ok = wait(o_read, o_par);
+            if (!ok) break;
+            pv_mma(vs, o, w, u < 2, false);
+            vs.advance(1);
+            if (u + 2 < n) {  // the next S overwrites the buffer of this P
+              ok = wait(&pv_done[w], par);
+              if (ok) s_mma(ks, q, w);
+              ks.advance(1);
+            }
           }
-          __syncwarp();
-          ks.advance(stride);
-        };
-        Buf b{w, 0}, before{w - 1, 0}, ahead{w, 0};
-        if (ok && w < n) {
-          ok = wait(&full_k[ks.st], ks.par);
-          if (ok) s_mma(w);
-        }
-        ahead.advance(wide, 2);
-        for (int u = w; ok && u < n; u += 2) {
-          const uint32_t par = b.parity(ph);
-          if (u + 2 < n) ok = wait(&full_k[ks.st], ks.par);  // K of the next S, before P is there
-          if (ok) ok = wait(&p_ready[b.i], par);
-          if (ok && u < 2 && unit > 0) ok = wait(o_read, (unit - 1) & 1);  // (of the last unit)
-          if (!ok) break;
-          const uint64_t vd = v_desc + (uint32_t)(vs.st * (S::TILE >> 4));
-          const uint32_t pc = tmem + s_col(b.i);
-          if (elect_one()) {
-#pragma unroll
-            for (int kk = 0; kk < kPages; ++kk)
-              tc_mma_ta(o, pc + 8 * kk, vd + ((kk * PAGE_MMA) >> 4), S::IDESC_PV,
-                        u < 2 && kk == 0 ? 0u : 1u);
-            tc_commit(&pv_done[b.i]);
+        } else if (w == 0) {
+          for (int u = 0; ok && u < n; ++u, ks.advance(1)) {
+            ok = wait(&full_k[ks.st], ks.par);
+            // the buffer's last P is used up; the first steps' buffers 2 and 3 may hold an O
+            if (ok && u >= 4) ok = wait(&pv_done[u & 3], parity_of(ph, false, u - 4));
+            if (ok && u == 2 && unit > 0) ok = wait(o_read, o_par);
+            if (ok) s_mma(ks, tmem + kColQ, u & 3);
           }
-          __syncwarp();
-          vs.advance(stride);
-          if (u + 2 < n) {
-            // the next S overwrites the buffer of an earlier P, whose P V must be complete: of this
-            // step with two buffers, of the step before it with three
-            if (wide)
-              ok = wait(&pv_done[b.i], par);
-            else if (u > 0)
-              ok = wait(&pv_done[before.i], before.parity(ph));
-            if (ok) s_mma(ahead.i);
+        } else {
+          for (int u = 0; ok && u < n; ++u, vs.advance(1)) {
+            ok = wait(&p_ready[u & 3], parity_of(ph, false, u));
+            if (ok && u == 0 && unit > 0) ok = wait(o_read, o_par);
+            if (ok) pv_mma(vs, tmem + kColO, u & 3, u == 0, true);
           }
-          b.advance(wide, 2);
-          ahead.advance(wide, 2);
-          before.advance(wide, 2);
         }
         ph = after_steps(ph, wide, n);
         k_base.skip(tiles);
@@ -521,15 +534,16 @@ __global__ void __launch_bounds__(TcShape<KV, D>::THREADS, 1) tree_tc_kernel(
     const int r = threadIdx.x & 127;      // row of the group
     const uint32_t lane_t = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     bool ok = true;
-    uint32_t ph = 0, unit = 0;
+    uint32_t ph = 0, ph_ref = 0, unit = 0;  // ph_ref: parities of ref_set at the unit's start
     Place<NV> base;  // V and K of the run's first tile
     Place<NK> k_base;
-    // The row of this thread in a run (row `row` of its unit, node t, query head `head`) and its
-    // score factor.
+    // The row of this thread in a run (row `row` of its unit, node t, query head `head`), its score
+    // factor, the factor of V, and the first 64 nodes it sees (loaded a unit ahead of their use).
     struct Row {
       int row, t, head;
       bool live;
-      float sc;
+      float sc, vs;
+      uint64_t seen0;
     };
     auto find_row = [&](const TreeRun& run) {
       Row x;
@@ -538,7 +552,9 @@ __global__ void __launch_bounds__(TcShape<KV, D>::THREADS, 1) tree_tc_kernel(
       const unsigned R = x.live ? run.row0 + x.row : 0;
       x.t = (int)(R / (unsigned)a.group);
       x.head = run.j * a.group + (int)(R - x.t * (unsigned)a.group);
-      x.sc = 0.f;
+      x.sc = W8 ? a.scale_log2 * a.k_scales[run.j] : a.scale_log2;
+      x.vs = W8 ? a.v_scales[run.j] : 1.f;
+      x.seen0 = x.live && a.mask ? *tree_row(a, run.b, x.t) : 0ull;
       return x;
     };
     auto row_at = [&](const TreeRun& run, const Row& x) {  // its offset in q and out
@@ -566,51 +582,69 @@ __global__ void __launch_bounds__(TcShape<KV, D>::THREADS, 1) tree_tc_kernel(
         for (int d = 0; d < RND; ++d) in[d][g] = there ? src[4 * d] : make_uint4(0, 0, 0, 0);
       }
     };
-    auto store_query = [&](const TreeRun& run, Row& x, const uint4 (&in)[RND][4]) {
+    auto store_query = [&](const TreeRun& run, Row& x, uint4 (&in)[RND][4]) {
       const bool wide = run.rows > kGroupThreads;
-      x.sc = a.scale_log2;
       if (needs_query(run)) {
-        const uint32_t stage = ring + S::OFF_Q + warp * 2048;
-        uint32_t w[D / 2];  // this lane's row, bf16 pairs
-#pragma unroll
-        for (int d = 0; d < RND; ++d) {
-          __syncwarp();
+        if constexpr (W8) {  // f16, scaled by a row's 2^e (the four lanes that hold a row agree)
+          const float sc = x.sc;
 #pragma unroll
           for (int g = 0; g < 4; ++g) {
-            const int row = 8 * g + (lane >> 2);
-            sts128(stage + row * 64 + (((lane & 3) ^ ((row >> 1) & 3)) << 4), in[d][g]);
-          }
-          __syncwarp();
+            uint32_t lo = 0, hi = 0;  // largest |q| as bits (bf16 magnitudes order like integers)
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const uint4 v = lds128(stage + lane * 64 + ((c ^ ((lane >> 1) & 3)) << 4));
-            w[16 * d + 4 * c] = v.x;
-            w[16 * d + 4 * c + 1] = v.y;
-            w[16 * d + 4 * c + 2] = v.z;
-            w[16 * d + 4 * c + 3] = v.w;
-          }
-        }
-        if constexpr (W8) {
-          uint32_t lo = 0, hi = 0;  // largest |q| as bits (bf16 magnitudes order like integers)
+            for (int d = 0; d < RND; ++d) {
+              const uint32_t* w = &in[d][g].x;
 #pragma unroll
-          for (int k = 0; k < D / 2; ++k) {
-            lo = max(lo, w[k] & 0x7fffu);
-            hi = max(hi, w[k] & 0x7fff0000u);
-          }
-          const uint32_t mx = max(lo, hi >> 16);
-          const int ex = mx >> 7;  // biased exponent: mx * 2^e in [2^14, 2^15), none for 0, inf, NaN
-          const int e = mx != 0 && ex < 255 ? min(126, max(-126, 141 - ex)) : 0;
-          const float up = __int_as_float((127 + e) << 23);
-          // (at least the smallest normal number: an unseen score of -inf must stay one)
-          x.sc = fmaxf(x.sc * a.k_scales[run.j] * __int_as_float((127 - e) << 23), 0x1p-126f);
+              for (int k = 0; k < 4; ++k) {
+                lo = max(lo, w[k] & 0x7fffu);
+                hi = max(hi, w[k] & 0x7fff0000u);
+              }
+            }
+            uint32_t mx = max(lo, hi >> 16);
+            mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+            mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+            const int ex = mx >> 7;  // biased exponent: mx 2^e in [2^14, 2^15), none for 0, inf, NaN
+            const int e = mx != 0 && ex < 255 ? min(126, max(-126, 141 - ex)) : 0;
+            const float up = __int_as_float((127 + e) << 23);
+            // (at least the smallest normal number: an unseen score of -inf must stay one)
+            const float of = fmaxf(sc * __int_as_float((127 - e) << 23), 0x1p-126f);
+            const float mine = __shfl_sync(0xffffffffu, of, 4 * (lane & 7));
+            if ((lane >> 3) == g) x.sc = mine;
+            if (wide || wg == 0) {
 #pragma unroll
-          for (int k = 0; k < D / 2; ++k) w[k] = pack_f16(bf16lo(w[k]) * up, bf16hi(w[k]) * up);
+              for (int d = 0; d < RND; ++d) {
+                uint32_t* w = &in[d][g].x;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) w[k] = pack_f16(bf16lo(w[k]) * up, bf16hi(w[k]) * up);
+              }
+            }
+          }
         }
         if (wide || wg == 0) {
+          const uint32_t stage = ring + S::OFF_Q + warp * 2048;
           const uint32_t q_col = kColQ + (wide ? 64 * wg : 0);
 #pragma unroll
-          for (int h = 0; h < D / 64; ++h)
-            tmem_st32(lane_t + q_col + 32 * h, *reinterpret_cast<const uint32_t(*)[32]>(&w[32 * h]));
+          for (int h = 0; h < RND / 2; ++h) {
+            uint32_t w[32];  // 128 bytes of this lane's row
+#pragma unroll
+            for (int d = 0; d < 2; ++d) {
+              __syncwarp();
+#pragma unroll
+              for (int g = 0; g < 4; ++g) {
+                const int row = 8 * g + (lane >> 2);
+                sts128(stage + row * 64 + (((lane & 3) ^ ((row >> 1) & 3)) << 4), in[2 * h + d][g]);
+              }
+              __syncwarp();
+#pragma unroll
+              for (int c = 0; c < 4; ++c) {
+                const uint4 v = lds128(stage + lane * 64 + ((c ^ ((lane >> 1) & 3)) << 4));
+                w[16 * d + 4 * c] = v.x;
+                w[16 * d + 4 * c + 1] = v.y;
+                w[16 * d + 4 * c + 2] = v.z;
+                w[16 * d + 4 * c + 3] = v.w;
+              }
+            }
+            tmem_st32(lane_t + q_col + 32 * h, w);
+          }
           tmem_wait_st();
         }
       }
@@ -641,39 +675,38 @@ __global__ void __launch_bounds__(TcShape<KV, D>::THREADS, 1) tree_tc_kernel(
         k_at.advance(wg);
       }
       int v_prev = 0;
-      Buf bf{wg, 0}, other{wg - 1, 0};  // S buffers of this step and of the step before it
-      int prev_buf = 0;         // this group's last step
-      uint32_t prev_par = 0;
       int p0 = (run.tile0 + (wide ? 0 : wg)) * kTok;
       const int seen_by_all = min(run.req.base, run.req.read) - kTok;
+      auto steps = [&](auto w_) {
+      constexpr bool wide = decltype(w_)::value;
       for (int u = wg; ok && u < n; u += 2) {
-        const uint32_t par = bf.parity(ph);
-        // V of the tile too: the MMA warp takes a P as the word that it is there. A narrow unit's
-        // buffers go round between the groups: a group waits for every S in order, the other's too,
-        // so that the phase it waits for is never the one after the next.
-        ok = mbar_wait(&full_v[at.st], at.par, a.err) &&
-             (wide || u == 0 || mbar_wait(&s_done[other.i], other.parity(ph), a.err)) &&
-             mbar_wait(&s_done[bf.i], par, a.err);
+        const int buf = buf_of(wide, u);
+        // V of the tile too: the MMA warps take a P as the word that it is there
+        ok = mbar_wait_both(&full_v[at.st], at.par, &s_done[buf], parity_of(ph, wide, u), a.err);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         if ((warp & 3) == 0 && lane == 0) {
-          // this tile's K is used up (a wide unit's once both groups say so), and the V of the
-          // group's tile before it too: its P V came before this S
+          // This tile's K is used up (a wide unit's once both groups say so). A stage of V is free
+          // after two arrivals: wide, one of each group for its last tile, whose P V came before this
+          // S; otherwise this one and the commit of the tile's P V.
           mbar_arrive_n(&free_k[k_at.st], wide ? 1 : 2);
-          if (u > 1) mbar_arrive_n(&free_v[v_prev], wide ? 1 : 2);
+          if (!wide)
+            mbar_arrive(&free_v[at.st]);
+          else if (u > 1)
+            mbar_arrive(&free_v[v_prev]);
         }
         v_prev = at.st;
         k_at.advance(wide ? 1 : 2);
         const int mask = page_mask[at.st];
         tc_fence_after();
         uint32_t sr[64];
-        const uint32_t scol = s_col(bf.i);
+        const uint32_t scol = s_col(buf);
         tmem_ld32(lane_t + scol, *reinterpret_cast<uint32_t(*)[32]>(&sr[0]));
         tmem_ld32(lane_t + scol + 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[32]));
         tmem_wait_ld();
         const bool masked = mask != (1 << kPages) - 1 || p0 > seen_by_all;
         if (masked) {
-          uint64_t seen = live ? tree_seen(a, run.req, b, t, p0) : 0ull;
+          uint64_t seen = live ? tree_seen(a, run.req, b, t, p0, me.seen0) : 0ull;
 #pragma unroll
           for (int p = 0; p < kPages; ++p)
             if (!((mask >> p) & 1)) seen &= ~(0xffffull << (16 * p));
@@ -734,27 +767,50 @@ __global__ void __launch_bounds__(TcShape<KV, D>::THREADS, 1) tree_tc_kernel(
         const float mx = sc * max3(max3(mx4[0], mx4[1], mx4[2]),
                                    max3(mx4[3], __uint_as_float(sr[60]), __uint_as_float(sr[61])),
                                    fmaxf(__uint_as_float(sr[62]), __uint_as_float(sr[63])));
-        if (u == wg) {
-          m_used = mx;
-        } else {
-          const bool need = mx > m_used + kLazyLog2;
-          // rescale this warp's rows of O (in TMEM): the group's last P V came before this S
-          if (__any_sync(0xffffffffu, need)) {
-            const float m_new = need ? mx : m_used;
-            const float alpha = m_new == -INFINITY ? 1.f : exp2f(m_used - m_new);
-#pragma unroll
-            for (int cb = 0; cb < D / 32; ++cb) {
-              uint32_t o[32];
-              tmem_ld32(lane_t + kColO + 128 * wg + 32 * cb, o);
-              tmem_wait_ld();
-#pragma unroll
-              for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
-              tmem_st32(lane_t + kColO + 128 * wg + 32 * cb, o);
-            }
-            tmem_wait_st();
-            l *= alpha;
-            m_used = m_new;
+        // The reference maximum m that P and O are scaled by: the first tile's maximum, then moved
+        // only past 2^8. In a wide unit it is the thread's own. Otherwise the two groups' tiles add
+        // into one O, so m goes from step to step: this group's step takes it from the other's
+        // last one, sets it and says so before anything else.
+        const bool first = wide ? u == wg : u == 0;
+        float m_before = m_used;
+        if (!wide && u > 0) {
+          ok = mbar_wait(&ref_set[1 - wg], ((ph_ref >> (1 - wg)) ^ (uint32_t)((u - 1) >> 1)) & 1u,
+                         a.err);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          m_before = ref[r];
+        }
+        const float m_new = first || mx > m_before + kLazyLog2 ? mx : m_before;
+        const bool moved = !first && m_new != m_before;
+        if (!wide) {
+          if (first || moved) ref[r] = m_new;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&ref_set[wg]);
+        }
+        if (__any_sync(0xffffffffu, moved)) {  // rescale this warp's rows of O (in TMEM)
+          // (every P V before this step is done: wide, it came before this S)
+          if (!wide) {
+            ok = mbar_wait(&pv_done[(u - 1) & 3], parity_of(ph, false, u - 1), a.err);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            tc_fence_after();
           }
+          const float alpha = moved ? exp2f(m_before - m_new) : 1.f;
+          const uint32_t ocol = kColO + (wide ? 128 * wg : 0);
+#pragma unroll
+          for (int cb = 0; cb < D / 32; ++cb) {
+            uint32_t o[32];
+            tmem_ld32(lane_t + ocol + 32 * cb, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
+            tmem_st32(lane_t + ocol + 32 * cb, o);
+          }
+          tmem_wait_st();
+        }
+        if (m_new != m_used) {  // the group's own sum, at the maximum of its last step
+          l *= exp2f(m_used - m_new);
+          m_used = m_new;
         }
         // P = 2^(s - m) over the first 32 columns of the tile's S buffer
         const float m_use = m_used == -INFINITY ? 0.f : m_used;
@@ -778,14 +834,15 @@ __global__ void __launch_bounds__(TcShape<KV, D>::THREADS, 1) tree_tc_kernel(
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();  // (one arrival per warp: arrivals on one barrier go one by one)
-        if (lane == 0) mbar_arrive(&p_ready[bf.i]);
-        prev_buf = bf.i;
-        prev_par = par;
-        bf.advance(wide, 2);
-        other.advance(wide, 2);
+        if (lane == 0) mbar_arrive(&p_ready[buf]);
         at.advance(wide ? 1 : 2);
         p0 += wide ? kTok : 2 * kTok;
       }
+      };
+      if (wide)
+        steps(BoolConst<true>{});
+      else
+        steps(BoolConst<false>{});
       // ---- the unit's rows ----
       uint4 in[RND][4];  // the next unit's queries, on their way during the waits
       next = get_run(unit + 1);
@@ -794,10 +851,12 @@ __global__ void __launch_bounds__(TcShape<KV, D>::THREADS, 1) tree_tc_kernel(
         then = find_row(*next);
         load_query(*next, then, in);
       }
-      if (ok && wg < n) ok = mbar_wait(&pv_done[prev_buf], prev_par, a.err);
+      // the unit's last P V (wide: the group's) is done; the other group hears of it below
+      const int last = wide ? n - 2 + wg : n - 1;
+      if (ok && (wide || (last & 1) == wg))
+        ok = mbar_wait(&pv_done[buf_of(wide, last)], parity_of(ph, wide, last), a.err);
       ok = __all_sync(0xffffffffu, ok);
-      if (ok && wg < n && (warp & 3) == 0 && lane == 0)
-        mbar_arrive_n(&free_v[v_prev], wide ? 1 : 2);
+      if (ok && wide && (warp & 3) == 0 && lane == 0) mbar_arrive(&free_v[v_prev]);
       tc_fence_after();
       if (!wide) ml[wg * kGroupThreads + r] = make_float2(m_used, l);
       tc_fence_before();
@@ -807,19 +866,16 @@ __global__ void __launch_bounds__(TcShape<KV, D>::THREADS, 1) tree_tc_kernel(
       ok = __all_sync(0xffffffffu, ok);
       tc_fence_after();
       if (threadIdx.x < 8) bad_nodes[8 * ((unit + 1) & 1) + threadIdx.x] = 0;
-      // wide: the group's own rows, all dims; else group wg takes dims wg D/2 .. of every row and
-      // merges the two groups' O
-      float M = m_used, L = l, w0 = 1.f, w1 = 0.f;
-      const bool two = !wide && n > 1;
+      // wide: the group's own rows, all dims; else group wg writes dims wg D/2 .. of every row, whose
+      // sum is the two groups', each at the maximum of its last step (O is at the larger, the last)
+      float M = m_used, L = l;
       if (!wide) {
         const float2 x = ml[r], y = ml[kGroupThreads + r];
         M = fmaxf(x.x, y.x);
         const float Mu = M == -INFINITY ? 0.f : M;
-        w0 = exp2f(x.x - Mu);
-        w1 = two ? exp2f(y.x - Mu) : 0.f;
-        L = w0 * x.y + (two ? w1 * y.y : 0.f);
+        L = exp2f(x.x - Mu) * x.y + exp2f(y.x - Mu) * y.y;
       }
-      const float vs = W8 ? a.v_scales[j] : 1.f;
+      const float vs = me.vs;
       const float f = run.whole ? (L != 0.f ? vs / L : 0.f) : vs;
       uint32_t any_bad = 0;
 #pragma unroll
@@ -850,7 +906,7 @@ __global__ void __launch_bounds__(TcShape<KV, D>::THREADS, 1) tree_tc_kernel(
           for (int nd = 0; nd < run.req.nodes; ++nd) {
             if (!((bad[nd >> 5] >> (nd & 31)) & 1)) continue;
             const int pos = run.req.base + nd;
-            if (!(tree_seen(a, run.req, b, t, pos) & 1)) continue;
+            if (!(tree_seen(a, run.req, b, t, pos, me.seen0) & 1)) continue;
             const int id = a.block_tables[(size_t)b * a.max_pages + pos / kPageSize];
             const int64_t at =
                 ((((int64_t)id * a.h_kv + j) * kPageSize + pos % kPageSize) * D + c) * KV::bytes;
@@ -894,20 +950,7 @@ __global__ void __launch_bounds__(TcShape<KV, D>::THREADS, 1) tree_tc_kernel(
         for (int c = c_lo; c < c_hi; c += 32) {
           uint32_t o[32];
           tmem_ld32(lane_t + kColO + (wide ? 128 * wg : 0) + c, o);
-          if (two) {
-            uint32_t o1[32];
-            tmem_ld32(lane_t + kColO + 128 + c, o1);
-            tmem_wait_ld();
-#pragma unroll
-            for (int k = 0; k < 32; ++k)
-              o[k] = __float_as_uint(w0 * __uint_as_float(o[k]) + w1 * __uint_as_float(o1[k]));
-          } else {
-            tmem_wait_ld();
-            if (!wide) {
-#pragma unroll
-              for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(w0 * __uint_as_float(o[k]));
-            }
-          }
+          tmem_wait_ld();
           emit(c, o);
         }
       }
@@ -915,6 +958,7 @@ __global__ void __launch_bounds__(TcShape<KV, D>::THREADS, 1) tree_tc_kernel(
       __syncwarp();
       if (lane == 0) mbar_arrive(o_read);
       ph = after_steps(ph, wide, n);
+      if (!wide) ph_ref ^= (uint32_t)(((n + 1) >> 1) & 1) | (uint32_t)((n >> 1) & 1) << 1;
       base.skip(run.n);
       k_base.skip(run.n);
       me = then;
