@@ -59,15 +59,13 @@ constexpr int kSBufs = 4;
 // the tiles of the rings at most, each a run of its own at worst, besides the run whose rows are
 // being written and the one it is about to copy.
 constexpr int kRuns = 32;
-// tensor memory columns: O, Q and S (then P) buffers. Units of up to 128 rows: one O, one Q and four
-// S buffers, two of them in the columns that larger units use for the second O; larger units: an O,
-// a Q and an S buffer for each group.
-constexpr uint32_t kColO = 0, kColQ = 256, kColS = 384;
+// tensor memory columns. WIDE: two O and four S (then P) buffers; otherwise an O, a Q and the same
+constexpr uint32_t kColO = 0, kColQ = 256;
 constexpr uint32_t kTmemCols = 512;
 constexpr float kLazyLog2 = 8.f;
 static_assert(2 * kGroupThreads == kTreeTcRows, "a unit is two groups' rows");
 
-template <typename KV, int D>
+template <typename KV, int D, bool WIDE>
 struct TcShape {
   static constexpr bool W8 = KV::bytes == 1;
   static constexpr int THREADS = 32 * (W8 ? kConvWarp + kConvThreads / 32 : kConvWarp);
@@ -76,14 +74,18 @@ struct TcShape {
   static constexpr int TILE = kTok * D * 2;       // K (or V) of a tile in MMA form
   static constexpr int RAW_TILE = kTok * D;       // 8-bit codes
   static constexpr int RAW_STAGE = 2 * RAW_TILE;
-  // 192 KB of rings: K tiles, needed until their S is done, and V tiles, needed until their P V
-  // is done, go round separately; 8-bit caches have 80 KB of raw codes before them
-  static constexpr int NK = (W8 ? 48 : 96) * 1024 / TILE, NV = (W8 ? 64 : 96) * 1024 / TILE;
-  static constexpr int NR = W8 ? 80 * 1024 / RAW_STAGE : 0;
+  // rings: K tiles, needed until their S is done, and V tiles, needed until their P V is done, go
+  // round separately; 8-bit caches have raw codes before them
+  static constexpr int NK = (WIDE ? W8 ? 32 : 64 : W8 ? 48 : 96) * 1024 / TILE;
+  static constexpr int NV = (WIDE ? W8 ? 48 : 80 : W8 ? 64 : 96) * 1024 / TILE;
+  static constexpr int NR = W8 ? (WIDE ? 64 : 80) * 1024 / RAW_STAGE : 0;
   static constexpr int OFF_V = NK * TILE;
   static constexpr int OFF_RAW = OFF_V + NV * TILE;
-  static constexpr int OFF_Q = OFF_RAW + NR * RAW_STAGE;    // 2 KB per softmax warp
-  static constexpr int OFF_ML = OFF_Q + kSoftThreads / 32 * 2048;  // [2][128] (max, sum)
+  static constexpr int OFF_Q = OFF_RAW + NR * RAW_STAGE;    // WIDE: 256 queries in MMA form
+  static constexpr int Q_GROUP = WIDE ? kGroupThreads * D * 2 : 0;
+  static constexpr int PIECE = WIDE ? 32 : 64;              // bytes of a row that change hands at once
+  static constexpr int OFF_STAGE = OFF_Q + 2 * Q_GROUP;     // 32 rows' pieces for each softmax warp
+  static constexpr int OFF_ML = OFF_STAGE + kSoftThreads * PIECE;  // [2][128] (max, sum)
   static constexpr int OFF_REF = OFF_ML + 2 * kGroupThreads * 8;   // [128] reference maxima
   static constexpr int OFF_BAR = OFF_REF + kGroupThreads * 4;
   static constexpr int BARS = 2 * NK + 2 * NV + 2 * NR + 3 * kSBufs + 6 + kRuns;
@@ -95,21 +97,20 @@ struct TcShape {
   static_assert(SMEM <= 227 * 1024 && SMEM > 114 * 1024, "one CTA per SM");
 };
 
+template <bool WIDE>
 __device__ __forceinline__ uint32_t s_col(int buf) {
-  return buf < 2 ? kColS + 64 * buf : kColO + 64 * buf;
+  return WIDE || buf >= 2 ? (WIDE ? 256 : 0) + 64 * buf : 384 + 64 * buf;
 }
 
 // A unit's steps in order: with up to 128 rows step u is tile u, otherwise ("wide") tile u / 2 for
-// rows 128 (u % 2) ... Group u % 2 takes it, in S buffer u % 4 (wide: u % 2). Every buffer's three
-// barriers complete once per step that uses it.
-__device__ __forceinline__ int buf_of(bool wide, int u) { return wide ? u & 1 : u & 3; }
+// rows 128 (u % 2) ... Group u % 2 takes it, in S buffer u % 4. Every buffer's three barriers
+// complete once per step that uses it.
 // parity of the buffer's barriers in step u; ph holds each buffer's at the unit's start
-__device__ __forceinline__ uint32_t parity_of(uint32_t ph, bool wide, int u) {
-  return ((ph >> buf_of(wide, u)) ^ (uint32_t)(u >> (wide ? 1 : 2))) & 1u;
+__device__ __forceinline__ uint32_t parity_of(uint32_t ph, int u) {
+  return ((ph >> (u & 3)) ^ (uint32_t)(u >> 2)) & 1u;
 }
 // the buffers' parities after a unit of n steps
-__device__ __forceinline__ uint32_t after_steps(uint32_t ph, bool wide, int n) {
-  if (wide) return ph ^ ((n >> 1) & 1 ? 3u : 0u);
+__device__ __forceinline__ uint32_t after_steps(uint32_t ph, int n) {
   if ((n >> 2) & 1) ph ^= 15u;
   return ph ^ ((1u << (n & 3)) - 1u);
 }
@@ -159,11 +160,12 @@ __device__ __forceinline__ bool not_finite(uint32_t h) {
   return (h & E) == E;
 }
 
-template <typename KV, int D>
-__global__ void __launch_bounds__(TcShape<KV, D>::THREADS, 1) tree_tc_kernel(
+// WIDE: units may have more than 128 rows.
+template <typename KV, int D, bool WIDE>
+__global__ void __launch_bounds__(TcShape<KV, D, WIDE>::THREADS, 1) tree_tc_kernel(
     const TreeArgs a, const __grid_constant__ CUtensorMap tm_k,
     const __grid_constant__ CUtensorMap tm_v) {
-  using S = TcShape<KV, D>;
+  using S = TcShape<KV, D, WIDE>;
   constexpr bool W8 = S::W8;
   constexpr int NK = S::NK, NV = S::NV, NR = S::NR;
   constexpr int PAGE_MMA = kPageSize * D * 2;  // V bytes of a page in MMA form
@@ -353,11 +355,11 @@ __global__ void __launch_bounds__(TcShape<KV, D>::THREADS, 1) tree_tc_kernel(
           mbar_wait(&there[t % stages], (uint32_t)(t / stages) & 1u, a.err);
     } else {
       // ===================== MMAs (one elected lane issues) =====================
-      // Two warps, since issuing a step's MMAs takes about as long as they run. Units of up to 128
-      // rows: one issues the S, up to four tiles ahead, the other the P V, all into one O. Larger
-      // ones: each issues the steps of one group, the next S as soon as the P V of its buffer is done.
+      // Two warps, since issuing a step's MMAs takes about as long as they run: one issues the S, up
+      // to four steps ahead, the other the P V.
       const int w = warp - kMmaWarp;
       const uint64_t k_desc = tc_desc(ring, 16, 1024), v_desc = tc_desc(ring + S::OFF_V, 2048, 1024);
+      const uint64_t q_desc = tc_desc(ring + S::OFF_Q, 16, 1024);
       bool ok = true;
       uint32_t ph = 0, unit = 0;
       Place<NK> k_base;  // the run's first tile
@@ -367,28 +369,34 @@ __global__ void __launch_bounds__(TcShape<KV, D>::THREADS, 1) tree_tc_kernel(
         tc_fence_after();
         return got;
       };
-      auto s_mma = [&](const Place<NK>& k, uint32_t q, int buf) {
+      auto s_mma = [&](const Place<NK>& k, int group, int buf) {
         const uint64_t kd = k_desc + (uint32_t)(k.st * (S::TILE >> 4));
-        const uint32_t d = tmem + s_col(buf);
+        const uint64_t qd = q_desc + (uint32_t)(group * (S::Q_GROUP >> 4));
+        const uint32_t d = tmem + s_col<WIDE>(buf);
         if (elect_one()) {
 #pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk)
-            tc_mma_ta(d, q + 8 * kk, kd + (((kk >> 2) * (kTok * 128) + (kk & 3) * 32) >> 4),
-                      S::IDESC_S, kk > 0 ? 1u : 0u);
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint64_t kb = kd + (((kk >> 2) * (kTok * 128) + (kk & 3) * 32) >> 4);
+            if constexpr (WIDE)
+              tc_mma_sa(d, qd + (((kk >> 2) * (kGroupThreads * 128) + (kk & 3) * 32) >> 4), kb,
+                        S::IDESC_S, kk > 0 ? 1u : 0u);
+            else
+              tc_mma_ta(d, tmem + kColQ + 8 * kk, kb, S::IDESC_S, kk > 0 ? 1u : 0u);
+          }
           tc_commit(&s_done[buf]);
         }
         __syncwarp();
       };
-      auto pv_mma = [&](const Place<NV>& v, uint32_t o, int buf, bool first, bool free) {
+      auto pv_mma = [&](const Place<NV>& v, uint32_t o, int buf, bool first) {
         const uint64_t vd = v_desc + (uint32_t)(v.st * (S::TILE >> 4));
-        const uint32_t pc = tmem + s_col(buf);
+        const uint32_t pc = tmem + s_col<WIDE>(buf);
         if (elect_one()) {
 #pragma unroll
           for (int kk = 0; kk < kPages; ++kk)
             tc_mma_ta(o, pc + 8 * kk, vd + ((kk * PAGE_MMA) >> 4), S::IDESC_PV,
                       first && kk == 0 ? 0u : 1u);
           tc_commit(&pv_done[buf]);
-          if (free) tc_commit(&free_v[v.st]);
+          tc_commit(&free_v[v.st]);
         }
         __syncwarp();
       };
@@ -398,49 +406,31 @@ __global__ void __launch_bounds__(TcShape<KV, D>::THREADS, 1) tree_tc_kernel(
         const TreeRun* run = get_run(unit);
         if (!run) break;
         const int tiles = uniform(run->n);
-        const bool wide = uniform(run->rows) > kGroupThreads;
+        const bool wide = WIDE && uniform(run->rows) > kGroupThreads;
         const int n = wide ? 2 * tiles : tiles;
         Place<NK> ks = k_base;  // K of the next S
         Place<NV> vs = v_base;  // V of the next P V
-        const uint32_t o_par = (unit - 1) & 1;  // the last unit's O is read (unit > 0)
         ok = wait(q_ready, unit & 1);
         if (elect_one()) mbar_arrive(q_ready);  // (the next unit's: this phase has been seen)
         __syncwarp();
-        if (wide) {
-          const uint32_t q = tmem + kColQ + 64 * w, o = tmem + kColO + 128 * w;
-          if (ok) ok = wait(&full_k[ks.st], ks.par);
-          if (ok) s_mma(ks, q, w);
-          ks.advance(1);
-          for (int u = w; ok && u < n; u += 2) {
-            const uint32_t par = parity_of(ph, true, u);
-            if (u + 2 < n) ok = wait(&full_k[ks.st], ks.par);  // K of the next S, before P is there
-            if (ok) ok = wait(&p_ready[w], par);
-            if (ok && u < 2 && unit > 0) ok = wait(o_read, o_par);
-            if (!ok) break;
-            pv_mma(vs, o, w, u < 2, false);
-            vs.advance(1);
-            if (u + 2 < n) {  // the next S overwrites the buffer of this P
-              ok = wait(&pv_done[w], par);
-              if (ok) s_mma(ks, q, w);
-              ks.advance(1);
-            }
-          }
-        } else if (w == 0) {
-          for (int u = 0; ok && u < n; ++u, ks.advance(1)) {
-            ok = wait(&full_k[ks.st], ks.par);
-            // the buffer's last P is used up; the first steps' buffers 2 and 3 may hold an O
-            if (ok && u >= 4) ok = wait(&pv_done[u & 3], parity_of(ph, false, u - 4));
-            if (ok && u == 2 && unit > 0) ok = wait(o_read, o_par);
-            if (ok) s_mma(ks, tmem + kColQ, u & 3);
+        if (w == 0) {
+          for (int u = 0; ok && u < n; ++u) {
+            const int group = wide ? u & 1 : 0;
+            if (group == 0) ok = wait(&full_k[ks.st], ks.par);
+            if (ok && u >= 4) ok = wait(&pv_done[u & 3], parity_of(ph, u - 4));  // P used up
+            if (ok) s_mma(ks, group, u & 3);
+            if (!wide || group) ks.advance(1);
           }
         } else {
-          for (int u = 0; ok && u < n; ++u, vs.advance(1)) {
-            ok = wait(&p_ready[u & 3], parity_of(ph, false, u));
-            if (ok && u == 0 && unit > 0) ok = wait(o_read, o_par);
-            if (ok) pv_mma(vs, tmem + kColO, u & 3, u == 0, true);
+          for (int u = 0; ok && u < n; ++u) {
+            const int group = wide ? u & 1 : 0;
+            ok = wait(&p_ready[u & 3], parity_of(ph, u));
+            if (ok && u == 0 && unit > 0) ok = wait(o_read, (unit - 1) & 1);  // the last unit's
+            if (ok) pv_mma(vs, tmem + kColO + 128 * group, u & 3, u == group);
+            if (!wide || group) vs.advance(1);
           }
         }
-        ph = after_steps(ph, wide, n);
+        ph = after_steps(ph, n);
         k_base.skip(tiles);
         v_base.skip(tiles);
       }
@@ -547,7 +537,7 @@ __global__ void __launch_bounds__(TcShape<KV, D>::THREADS, 1) tree_tc_kernel(
     };
     auto find_row = [&](const TreeRun& run) {
       Row x;
-      x.row = (run.rows > kGroupThreads ? wg * kGroupThreads : 0) + r;
+      x.row = (WIDE && run.rows > kGroupThreads ? wg * kGroupThreads : 0) + r;
       x.live = x.row < run.rows;
       const unsigned R = x.live ? run.row0 + x.row : 0;
       x.t = (int)(R / (unsigned)a.group);
@@ -566,7 +556,7 @@ __global__ void __launch_bounds__(TcShape<KV, D>::THREADS, 1) tree_tc_kernel(
     // through shared memory, and each lane puts its row into tensor memory.
     constexpr int RND = D / 32;  // rounds of 64 bytes
     auto needs_query = [&](const TreeRun& run) {  // (8-bit caches: both groups need a row's scale)
-      return ok && (W8 || run.rows > kGroupThreads || wg == 0);
+      return ok && (W8 || (WIDE && run.rows > kGroupThreads) || wg == 0);
     };
     auto load_query = [&](const TreeRun& run, const Row& x, uint4 (&in)[RND][4]) {
       if (!needs_query(run)) return;
@@ -583,7 +573,7 @@ __global__ void __launch_bounds__(TcShape<KV, D>::THREADS, 1) tree_tc_kernel(
       }
     };
     auto store_query = [&](const TreeRun& run, Row& x, uint4 (&in)[RND][4]) {
-      const bool wide = run.rows > kGroupThreads;
+      const bool wide = WIDE && run.rows > kGroupThreads;
       if (needs_query(run)) {
         if constexpr (W8) {  // f16, scaled by a row's 2^e (the four lanes that hold a row agree)
           const float sc = x.sc;
@@ -619,9 +609,21 @@ __global__ void __launch_bounds__(TcShape<KV, D>::THREADS, 1) tree_tc_kernel(
             }
           }
         }
-        if (wide || wg == 0) {
-          const uint32_t stage = ring + S::OFF_Q + warp * 2048;
-          const uint32_t q_col = kColQ + (wide ? 64 * wg : 0);
+        if constexpr (WIDE) {
+          if (wide || wg == 0) {
+            const int row0 = (warp & 3) * 32 + (lane >> 2);  // rows row0 + 8 g of the group
+            const uint32_t at = ring + S::OFF_Q + wg * S::Q_GROUP + row0 * 128;
+#pragma unroll
+            for (int d = 0; d < RND; ++d) {
+              const uint32_t ch = (((4 * d & 7) + (lane & 3)) ^ (row0 & 7)) << 4;
+#pragma unroll
+              for (int g = 0; g < 4; ++g)
+                sts128(at + (d >> 1) * (kGroupThreads * 128) + g * 1024 + ch, in[d][g]);
+            }
+            fence_proxy_async_smem();
+          }
+        } else if (wg == 0) {
+          const uint32_t stage = ring + S::OFF_STAGE + warp * 2048;
 #pragma unroll
           for (int h = 0; h < RND / 2; ++h) {
             uint32_t w[32];  // 128 bytes of this lane's row
@@ -643,7 +645,7 @@ __global__ void __launch_bounds__(TcShape<KV, D>::THREADS, 1) tree_tc_kernel(
                 w[16 * d + 4 * c + 3] = v.w;
               }
             }
-            tmem_st32(lane_t + q_col + 32 * h, w);
+            tmem_st32(lane_t + kColQ + 32 * h, w);
           }
           tmem_wait_st();
         }
@@ -662,7 +664,7 @@ __global__ void __launch_bounds__(TcShape<KV, D>::THREADS, 1) tree_tc_kernel(
     }
     for (; next; ++unit) {
       const TreeRun& run = *next;
-      const bool wide = run.rows > kGroupThreads, live = me.live;
+      const bool wide = WIDE && run.rows > kGroupThreads, live = me.live;
       const int n = wide ? 2 * run.n : run.n;  // steps; this group's: wg, wg + 2, ...
       const int b = run.b, j = run.j, t = me.t;
       const float sc = me.sc;
@@ -674,33 +676,27 @@ __global__ void __launch_bounds__(TcShape<KV, D>::THREADS, 1) tree_tc_kernel(
         at.advance(wg);
         k_at.advance(wg);
       }
-      int v_prev = 0;
       int p0 = (run.tile0 + (wide ? 0 : wg)) * kTok;
       const int seen_by_all = min(run.req.base, run.req.read) - kTok;
       auto steps = [&](auto w_) {
       constexpr bool wide = decltype(w_)::value;
       for (int u = wg; ok && u < n; u += 2) {
-        const int buf = buf_of(wide, u);
+        const int buf = u & 3;
         // V of the tile too: the MMA warps take a P as the word that it is there
-        ok = mbar_wait_both(&full_v[at.st], at.par, &s_done[buf], parity_of(ph, wide, u), a.err);
+        ok = mbar_wait_both(&full_v[at.st], at.par, &s_done[buf], parity_of(ph, u), a.err);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         if ((warp & 3) == 0 && lane == 0) {
           // This tile's K is used up (a wide unit's once both groups say so). A stage of V is free
-          // after two arrivals: wide, one of each group for its last tile, whose P V came before this
-          // S; otherwise this one and the commit of the tile's P V.
+          // after two arrivals, the commits of its P V; a small unit's tile has only one.
           mbar_arrive_n(&free_k[k_at.st], wide ? 1 : 2);
-          if (!wide)
-            mbar_arrive(&free_v[at.st]);
-          else if (u > 1)
-            mbar_arrive(&free_v[v_prev]);
+          if (!wide) mbar_arrive(&free_v[at.st]);
         }
-        v_prev = at.st;
         k_at.advance(wide ? 1 : 2);
         const int mask = page_mask[at.st];
         tc_fence_after();
         uint32_t sr[64];
-        const uint32_t scol = s_col(buf);
+        const uint32_t scol = s_col<WIDE>(buf);
         tmem_ld32(lane_t + scol, *reinterpret_cast<uint32_t(*)[32]>(&sr[0]));
         tmem_ld32(lane_t + scol + 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[32]));
         tmem_wait_ld();
@@ -788,13 +784,11 @@ __global__ void __launch_bounds__(TcShape<KV, D>::THREADS, 1) tree_tc_kernel(
           if (lane == 0) mbar_arrive(&ref_set[wg]);
         }
         if (__any_sync(0xffffffffu, moved)) {  // rescale this warp's rows of O (in TMEM)
-          // (every P V before this step is done: wide, it came before this S)
-          if (!wide) {
-            ok = mbar_wait(&pv_done[(u - 1) & 3], parity_of(ph, false, u - 1), a.err);
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok) break;
-            tc_fence_after();
-          }
+          constexpr int back = wide ? 2 : 1;  // to the last step that adds into this O
+          ok = mbar_wait(&pv_done[(u - back) & 3], parity_of(ph, u - back), a.err);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          tc_fence_after();
           const float alpha = moved ? exp2f(m_before - m_new) : 1.f;
           const uint32_t ocol = kColO + (wide ? 128 * wg : 0);
 #pragma unroll
@@ -839,10 +833,14 @@ __global__ void __launch_bounds__(TcShape<KV, D>::THREADS, 1) tree_tc_kernel(
         p0 += wide ? kTok : 2 * kTok;
       }
       };
-      if (wide)
-        steps(BoolConst<true>{});
-      else
+      if constexpr (WIDE) {
+        if (wide)
+          steps(BoolConst<true>{});
+        else
+          steps(BoolConst<false>{});
+      } else {
         steps(BoolConst<false>{});
+      }
       // ---- the unit's rows ----
       uint4 in[RND][4];  // the next unit's queries, on their way during the waits
       next = get_run(unit + 1);
@@ -854,9 +852,8 @@ __global__ void __launch_bounds__(TcShape<KV, D>::THREADS, 1) tree_tc_kernel(
       // the unit's last P V (wide: the group's) is done; the other group hears of it below
       const int last = wide ? n - 2 + wg : n - 1;
       if (ok && (wide || (last & 1) == wg))
-        ok = mbar_wait(&pv_done[buf_of(wide, last)], parity_of(ph, wide, last), a.err);
+        ok = mbar_wait(&pv_done[last & 3], parity_of(ph, last), a.err);
       ok = __all_sync(0xffffffffu, ok);
-      if (ok && wide && (warp & 3) == 0 && lane == 0) mbar_arrive(&free_v[v_prev]);
       tc_fence_after();
       if (!wide) ml[wg * kGroupThreads + r] = make_float2(m_used, l);
       tc_fence_before();
@@ -880,25 +877,33 @@ __global__ void __launch_bounds__(TcShape<KV, D>::THREADS, 1) tree_tc_kernel(
       uint32_t any_bad = 0;
 #pragma unroll
       for (int k = 0; k < 8; ++k) any_bad |= bad[k];
-      // 32 dims from c on of this thread's row: finished, or a partial. Rows leave as they came: 64
-      // bytes of each at a time through shared memory, four lanes writing a row's.
-      const uint32_t stage = ring + S::OFF_Q + warp * 2048;
+      // 32 dims from c on of this thread's row: finished, or a partial. Rows leave PIECE bytes of each
+      // at a time through shared memory, LPR lanes writing a row's.
+      constexpr int LPR = S::PIECE / 16;
+      const uint32_t stage = ring + S::OFF_STAGE + warp * (32 * S::PIECE);
+      auto place = [&](int row, int chunk) {  // (eight lanes touch eight different banks of 16 bytes)
+        return stage + row * S::PIECE + ((chunk ^ ((row / (8 / LPR)) & (LPR - 1))) << 4);
+      };
       const size_t out_off = row_at(run, me);
       const int part0 = ((int)blockIdx.x * 2 + run.slot) * kTreeTcRows + me.row - lane;
       auto leave = [&](const uint32_t (&v)[16], auto&& address) {
-        __syncwarp();
 #pragma unroll
-        for (int c4 = 0; c4 < 4; ++c4)
-          sts128(stage + lane * 64 + ((c4 ^ ((lane >> 1) & 3)) << 4),
-                 make_uint4(v[4 * c4], v[4 * c4 + 1], v[4 * c4 + 2], v[4 * c4 + 3]));
-        __syncwarp();
+        for (int h = 0; h < 64 / S::PIECE; ++h) {
+          __syncwarp();
 #pragma unroll
-        for (int g = 0; g < 4; ++g) {
-          const int row = 8 * g + (lane >> 2);
-          const uint4 x = lds128(stage + row * 64 + (((lane & 3) ^ ((row >> 1) & 3)) << 4));
-          const size_t at = __shfl_sync(0xffffffffu, (unsigned long long)out_off, row);
-          if (__shfl_sync(0xffffffffu, (int)live, row))
-            *reinterpret_cast<uint4*>(address(row, at) + 16 * (lane & 3)) = x;
+          for (int c4 = 0; c4 < LPR; ++c4) {
+            const uint32_t* x = v + 4 * (h * LPR + c4);
+            sts128(place(lane, c4), make_uint4(x[0], x[1], x[2], x[3]));
+          }
+          __syncwarp();
+#pragma unroll
+          for (int g = 0; g < LPR; ++g) {
+            const int row = (32 / LPR) * g + lane / LPR;
+            const uint4 x = lds128(place(row, lane % LPR));
+            const size_t at = __shfl_sync(0xffffffffu, (unsigned long long)out_off, row);
+            if (__shfl_sync(0xffffffffu, (int)live, row))
+              *reinterpret_cast<uint4*>(address(row, at) + h * S::PIECE + 16 * (lane % LPR)) = x;
+          }
         }
       };
       auto emit = [&](int c, uint32_t (&o)[32]) {
@@ -957,7 +962,7 @@ __global__ void __launch_bounds__(TcShape<KV, D>::THREADS, 1) tree_tc_kernel(
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(o_read);
-      ph = after_steps(ph, wide, n);
+      ph = after_steps(ph, n);
       if (!wide) ph_ref ^= (uint32_t)(((n + 1) >> 1) & 1) | (uint32_t)((n >> 1) & 1) << 1;
       base.skip(run.n);
       k_base.skip(run.n);
@@ -976,29 +981,36 @@ __global__ void __launch_bounds__(TcShape<KV, D>::THREADS, 1) tree_tc_kernel(
   }
 }
 
-template <typename KV, int D>
-cudaError_t launch_t(const TreeArgs& a, const CUtensorMap& tk, const CUtensorMap& tv,
+template <typename KV, int D, bool WIDE>
+cudaError_t launch_shape(const TreeArgs& a, const CUtensorMap& tk, const CUtensorMap& tv,
                      cudaStream_t s) {
-  using S = TcShape<KV, D>;
+  using S = TcShape<KV, D, WIDE>;
   static std::atomic<unsigned long long> attr_done{0};  // one bit per device
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev >= 64 || !((attr_done.load() >> dev) & 1ull)) {
-    e = cudaFuncSetAttribute(tree_tc_kernel<KV, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    e = cudaFuncSetAttribute(tree_tc_kernel<KV, D, WIDE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              S::SMEM);
     if (e != cudaSuccess) return e;
     // the softmax warps may take no more registers than the launch brings and the others give up
     cudaFuncAttributes fa{};
-    e = cudaFuncGetAttributes(&fa, tree_tc_kernel<KV, D>);
+    e = cudaFuncGetAttributes(&fa, tree_tc_kernel<KV, D, WIDE>);
     if (e != cudaSuccess) return e;
     if (kSoftThreads * S::SOFT_REGS + (S::THREADS - kSoftThreads) * S::REGS >
         S::THREADS * fa.numRegs)
       return cudaErrorLaunchOutOfResources;
     if (dev < 64) attr_done.fetch_or(1ull << dev);
   }
-  tree_tc_kernel<KV, D><<<a.ctas, S::THREADS, S::SMEM, s>>>(a, tk, tv);
+  tree_tc_kernel<KV, D, WIDE><<<a.ctas, S::THREADS, S::SMEM, s>>>(a, tk, tv);
   return cudaGetLastError();
+}
+
+template <typename KV, int D>
+cudaError_t launch_t(const TreeArgs& a, const CUtensorMap& tk, const CUtensorMap& tv,
+                     cudaStream_t s) {
+  return (long long)a.nodes * a.group > kGroupThreads ? launch_shape<KV, D, true>(a, tk, tv, s)
+                                                      : launch_shape<KV, D, false>(a, tk, tv, s);
 }
 
 }  // namespace
