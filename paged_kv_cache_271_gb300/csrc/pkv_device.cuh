@@ -128,15 +128,6 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, int* e
   }
 }
 
-// Waits for a phase of each of two barriers; both are asked before the first answer is needed.
-__device__ __forceinline__ bool mbar_wait_both(uint64_t* bar0, uint32_t parity0, uint64_t* bar1,
-                                               uint32_t parity1, int* err) {
-  const bool got0 = mbar_try_wait(smem_u32(bar0), parity0);
-  const bool got1 = mbar_try_wait(smem_u32(bar1), parity1);
-  if (got0 && got1) return true;
-  return mbar_wait(bar0, parity0, err) && mbar_wait(bar1, parity1, err);
-}
-
 // ---- bulk copies (TMA, untiled) -----------------------------------------------------------
 
 // Orders this thread's earlier generic-proxy shared-memory accesses before later async-proxy

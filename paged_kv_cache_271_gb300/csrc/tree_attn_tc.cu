@@ -293,7 +293,7 @@ __global__ void __launch_bounds__(TcShape<KV, D, WIDE>::THREADS, 1) tree_tc_kern
         const int pages = uniform((run->req.read + kPageSize - 1) / kPageSize);
         const int n = uniform(run->n), j = uniform(run->j);
         const int32_t* table = a.block_tables + (size_t)run->b * a.max_pages;
-        if (is_k) {  // the run's queries into L2, some tiles before their rows are read
+        if (WIDE && is_k) {  // the run's queries into L2, some tiles before their rows are read
           const int t0 = uniform(run->row0) / a.group;
           const int t1 = (uniform(run->row0 + run->rows) - 1) / a.group;
           const uint8_t* q = static_cast<const uint8_t*>(a.q) +
@@ -527,13 +527,12 @@ __global__ void __launch_bounds__(TcShape<KV, D, WIDE>::THREADS, 1) tree_tc_kern
     uint32_t ph = 0, ph_ref = 0, unit = 0;  // ph_ref: parities of ref_set at the unit's start
     Place<NV> base;  // V and K of the run's first tile
     Place<NK> k_base;
-    // The row of this thread in a run (row `row` of its unit, node t, query head `head`), its score
-    // factor, the factor of V, and the first 64 nodes it sees (loaded a unit ahead of their use).
+    // The row of this thread in a run (row `row` of its unit, node t, query head `head`) and its
+    // score factor; the factor of V.
     struct Row {
       int row, t, head;
       bool live;
       float sc, vs;
-      uint64_t seen0;
     };
     auto find_row = [&](const TreeRun& run) {
       Row x;
@@ -544,7 +543,6 @@ __global__ void __launch_bounds__(TcShape<KV, D, WIDE>::THREADS, 1) tree_tc_kern
       x.head = run.j * a.group + (int)(R - x.t * (unsigned)a.group);
       x.sc = W8 ? a.scale_log2 * a.k_scales[run.j] : a.scale_log2;
       x.vs = W8 ? a.v_scales[run.j] : 1.f;
-      x.seen0 = x.live && a.mask ? *tree_row(a, run.b, x.t) : 0ull;
       return x;
     };
     auto row_at = [&](const TreeRun& run, const Row& x) {  // its offset in q and out
@@ -683,7 +681,8 @@ __global__ void __launch_bounds__(TcShape<KV, D, WIDE>::THREADS, 1) tree_tc_kern
       for (int u = wg; ok && u < n; u += 2) {
         const int buf = u & 3;
         // V of the tile too: the MMA warps take a P as the word that it is there
-        ok = mbar_wait_both(&full_v[at.st], at.par, &s_done[buf], parity_of(ph, u), a.err);
+        ok = mbar_wait(&full_v[at.st], at.par, a.err) &&
+             mbar_wait(&s_done[buf], parity_of(ph, u), a.err);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         if ((warp & 3) == 0 && lane == 0) {
@@ -702,7 +701,7 @@ __global__ void __launch_bounds__(TcShape<KV, D, WIDE>::THREADS, 1) tree_tc_kern
         tmem_wait_ld();
         const bool masked = mask != (1 << kPages) - 1 || p0 > seen_by_all;
         if (masked) {
-          uint64_t seen = live ? tree_seen(a, run.req, b, t, p0, me.seen0) : 0ull;
+          uint64_t seen = live ? tree_seen(a, run.req, b, t, p0) : 0ull;
 #pragma unroll
           for (int p = 0; p < kPages; ++p)
             if (!((mask >> p) & 1)) seen &= ~(0xffffull << (16 * p));
@@ -911,7 +910,7 @@ __global__ void __launch_bounds__(TcShape<KV, D, WIDE>::THREADS, 1) tree_tc_kern
           for (int nd = 0; nd < run.req.nodes; ++nd) {
             if (!((bad[nd >> 5] >> (nd & 31)) & 1)) continue;
             const int pos = run.req.base + nd;
-            if (!(tree_seen(a, run.req, b, t, pos, me.seen0) & 1)) continue;
+            if (!(tree_seen(a, run.req, b, t, pos) & 1)) continue;
             const int id = a.block_tables[(size_t)b * a.max_pages + pos / kPageSize];
             const int64_t at =
                 ((((int64_t)id * a.h_kv + j) * kPageSize + pos % kPageSize) * D + c) * KV::bytes;

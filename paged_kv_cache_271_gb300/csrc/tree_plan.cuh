@@ -231,14 +231,8 @@ __device__ __forceinline__ uint64_t low_bits(int n) {  // the lowest n bits, n c
   return n <= 0 ? 0ull : n >= 64 ? ~0ull : (1ull << n) - 1;
 }
 
-// The first word of node t's row of the mask.
-__device__ __forceinline__ const uint64_t* tree_row(const TreeArgs& a, int b, int t) {
-  return a.mask + (size_t)b * a.mask_stride + (size_t)t * a.mask_words;
-}
-
-// w0: that word (if there is a mask).
 __device__ __forceinline__ uint64_t tree_seen(const TreeArgs& a, const TreeReq& r, int b, int t,
-                                              int p0, uint64_t w0) {
+                                              int p0) {
   uint64_t seen = low_bits(r.base - p0);
   const int n0 = p0 - r.base;  // node of bit 0 (negative: a cached position)
   if (n0 > -64) {
@@ -247,23 +241,18 @@ __device__ __forceinline__ uint64_t tree_seen(const TreeArgs& a, const TreeReq& 
       w = low_bits(t + 1 - max(n0, 0));
       if (n0 < 0) w <<= -n0;
     } else {
-      const uint64_t* row = tree_row(a, b, t);
+      const uint64_t* row = a.mask + (size_t)b * a.mask_stride + (size_t)t * a.mask_words;
       if (n0 < 0) {
-        w = w0 << -n0;
+        w = row[0] << -n0;
       } else {
         const int i = n0 >> 6, s = n0 & 63;
-        w = i == 0 ? w0 >> s : i < a.mask_words ? row[i] >> s : 0ull;
+        w = i < a.mask_words ? row[i] >> s : 0ull;
         if (s && i + 1 < a.mask_words) w |= row[i + 1] << (64 - s);
       }
     }
     seen |= w & ~low_bits(r.base - p0);
   }
   return seen & low_bits(r.read - p0);
-}
-
-__device__ __forceinline__ uint64_t tree_seen(const TreeArgs& a, const TreeReq& r, int b, int t,
-                                              int p0) {
-  return tree_seen(a, r, b, t, p0, a.mask && p0 > r.base - 64 ? *tree_row(a, b, t) : 0ull);
 }
 
 }  // namespace pkv
