@@ -702,9 +702,14 @@ def _opt_addr(t, name, dev: int):
     return None if t is None else _addr(t, name, dev)
 
 
+# the current stream's handle without a Stream object around it (a microsecond of a small call)
+_current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+
+
 def _raw_stream(stream, dev: int) -> int:
     if stream is None:
-        return torch.cuda.current_stream(dev).cuda_stream
+        return _current_raw_stream(dev)
     return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
 
 

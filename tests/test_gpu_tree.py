@@ -218,7 +218,8 @@ class Tree:
     """A batch of requests with drafts: pools with junk outside the cached rows, pages in random
     order, random trees."""
 
-    def __init__(self, ctx, tree, nodes, h_q, h_kv, d, io, cache, seed=0, spare=3, mask=None):
+    def __init__(self, ctx, tree, nodes, h_q, h_kv, d, io, cache, seed=0, spare=3, mask=None,
+                 level=None):
         g, r = gen(seed), np.random.default_rng(seed)
         self.ctx, self.tree, self.nodes = list(ctx), list(tree), nodes
         self.h_q, self.h_kv, self.d, self.io, self.cache = h_q, h_kv, d, io, cache
@@ -248,6 +249,8 @@ class Tree:
                     x = (x * 60).clamp(-448, 448)
                 elif cache == "int8":
                     x = (x * 40).round().clamp(-127, 127)
+                if level is not None and pool is self.k:
+                    x[:, :, 0] = level(b, pos)[:, None]
                 x = x.to(DT[cache])
                 if c:
                     raw_pool = pool.view(torch.uint8) if cache == "fp8" else pool
@@ -423,6 +426,23 @@ def test_tree_attention_over_many_requests(io, cache, d):
                                         ("f32", "f32", 64)])
 def test_tree_attention_of_long_contexts_is_split_and_joined(io, cache, d):
     Tree([20011, 3, 9000], [7, 3, 0], 7, 8, 2, d, io, cache, seed=11).check()
+
+
+@pytest.mark.parametrize("io,cache,d", KINDS)
+@pytest.mark.parametrize("nodes", [9, 40])  # rows of a KV head: up to 36, up to 160
+def test_tree_attention_maxima_that_move_at_every_tile(io, cache, d, nodes):
+    """Scores that jump by about 10 (2^14) from one 64 tokens to the next, up, down or in any order,
+    over one to seven of them; drafts of few and of many rows side by side."""
+    unit, q0 = {"f32": (1, 120), "bf16": (1, 120), "fp8": (40, 150), "int8": (18, 330)}[cache]
+    r = np.random.default_rng(21)
+    orders = [np.arange(1, 8), np.arange(7, 0, -1), *(r.permutation(7) + 1 for _ in range(6))]
+    ctx = r.integers(nodes, 449, 48).tolist()
+    tree = [int(n) for n in r.integers(1, nodes + 1, 48)]
+    steps = [torch.from_numpy(unit * orders[b % 8]).float().cuda() for b in range(48)]
+    t = Tree(ctx, tree, nodes, 8, 2, d, io, cache, seed=21,
+             level=lambda b, pos: steps[b][pos // 64])
+    t.q[..., 0] = q0 * (d / 128) ** 0.5
+    t.check()
 
 
 def test_tree_attention_matches_single_token_decode():

@@ -68,7 +68,8 @@ TREE = dict(q=P, dtype=BF16, batch=2, nodes=5, h_q=8, k_cache=P, v_cache=P, desc
     (dict(scale=0.0), EINVAL), (dict(scale=-1.0), EINVAL), (dict(scale=float("nan")), EINVAL),
     (dict(scale=float("inf")), EINVAL), (dict(mask_stride=4), ESHAPE), (dict(mask=ODD), EALIGN),
     (dict(out=ODD), EALIGN), (dict(ws=None), EINVAL), (dict(ws_bytes=16), EINVAL),
-    (dict(ws=ODD), EALIGN)])
+    (dict(ws=ODD), EALIGN), (dict(desc=desc(h_kv=1, pages=1 << 27)), ESHAPE),  # 2^31 rows
+    (dict(batch=60000, max_pages=1 << 20), ESHAPE)])  # 2^30 half tiles
 def test_tree_attention_refusals(changed, code):
     st, msg = call("pkv_tree_decode_attention", TREE, **changed)
     assert st == code and msg
