@@ -26,11 +26,12 @@ struct TreeSplit {
 // 24); bf16: 8 (64 requests, 64 rows: 122 us with 4, 118 with 8, 128 with 24). A wide tile costs as
 // much as one and a half narrow ones (the 192-row batch: 446 us when counted as one, 376 as one and
 // a half, 382 as two; bf16, ragged drafts of up to 256 rows: 163, 141, 138).
-TreeSplit tree_split(int dtype_q, int kv) {
+TreeSplit tree_split(int dtype_q, int kv, int head_dim) {
   if (dtype_q == PKV_BF16)
     return TreeSplit{kTreeTcRows,     kTreeTcTokens, 2, is_coded(kv) ? 12 : 8,
                      kTreeTcRows / 2, 3,             kTreeTcWave, true};
-  return TreeSplit{kTreeSimtRows, kTreeSimtTokens, 4, 1, kTreeSimtRows, 2, kTreeSimtWave, false};
+  return TreeSplit{kTreeSimtRows, kTreeSimtTokens, 1, 1,
+                   kTreeSimtRows, 2,               tree_simt_wave(head_dim), false};
 }
 
 size_t tree_acc_bytes(const TreeSplit& t, int ctas, int head_dim) {
@@ -166,7 +167,7 @@ size_t pkv_tree_decode_workspace_size(int32_t dtype_q, int32_t cache_dtype, int3
   if (batch <= 0 || tree_width <= 0 || num_q_heads <= 0 || num_kv_heads <= 0 || head_dim <= 0 ||
       max_pages_per_seq <= 0)
     return 0;
-  const TreeSplit t = tree_split(dtype_q, cache_dtype);
+  const TreeSplit t = tree_split(dtype_q, cache_dtype, head_dim);
   const int ctas = tree_ctas(t, batch, tree_width, num_q_heads, num_kv_heads, max_pages_per_seq);
   return tree_acc_bytes(t, ctas, head_dim) + tree_ml_bytes(t, ctas);
 }
@@ -206,7 +207,7 @@ int pkv_tree_decode_attention(const void* q, int32_t dtype_q, int32_t batch, int
   if (dtype_q == PKV_BF16 && kv == PKV_BF16 &&
       (long long)desc->num_pages * h_kv * desc->page_size >= (1ll << 31))
     return set_error(PKV_ESHAPE, "%s: a bf16 pool must have fewer than 2^31 rows", who);
-  const TreeSplit t = tree_split(dtype_q, kv);
+  const TreeSplit t = tree_split(dtype_q, kv, D);
   if (tree_most_work(t, batch, tree_width, num_q_heads, h_kv, max_pages_per_seq) >= (1ll << 30))
     return set_error(PKV_ESHAPE, "%s: the table can hold 2^30 half tiles of work or more", who);
   TreeArgs a{};

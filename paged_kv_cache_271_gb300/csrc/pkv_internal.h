@@ -179,8 +179,9 @@ struct CommitArgs {
 cudaError_t launch_qk_norm_rope_append(const NormRopeArgs& a, int io_dtype, int cache_dtype,
                                        cudaStream_t s);
 // Tree attention on CUDA cores (fp32 queries) and the combine of any split.
-constexpr int kTreeSimtRows = 32, kTreeSimtTokens = 32;
-constexpr int kTreeSimtWave = 152 * 4;  // four 55 KB CTAs fit an SM
+constexpr int kTreeSimtRows = 32, kTreeSimtTokens = 64;
+// CTAs resident at once, by their shared memory: of 52 KB four on an SM, of 92 KB two
+constexpr int tree_simt_wave(int head_dim) { return 152 * (head_dim == 64 ? 4 : 2); }
 cudaError_t launch_tree_simt(const TreeArgs& a, int kv_dtype, int head_dim, cudaStream_t s);
 // The same on tcgen05: bf16 queries; tk/tv: the 2-D K map and the V map of a bf16 pool (unused for
 // 8-bit caches).

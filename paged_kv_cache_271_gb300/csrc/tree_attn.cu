@@ -1,23 +1,32 @@
-// Tree attention on CUDA cores, for every cache and query type and both head dimensions, and the
-// combine of a split call.
+// Tree attention on CUDA cores, for fp32 queries over an fp32, FP8 or INT8 cache, and the combine of
+// a split call of any type.
 //
 // For node t of request b and query head h over KV head j:
 //   s_p = scale <q, K_p> for the positions p that node t sees, out = sum_p softmax(s)_p V_p,
 // the cached positions before the draft all seen, drafted node i seen when bit i of the mask row
 // is set; a row that sees nothing gives 0.
 //
-// A block takes units of 32 rows over tiles of 32 tokens (tree_plan.cuh): K and V of a tile are
-// widened to fp32 in shared memory and used by all 32 rows; a thread computes 4 rows x 2 tokens of
-// scores and 4 rows x D/16 dims of the weighted values, so each 16-byte shared-memory load feeds
-// five to six FMAs. The softmax is online: the running maximum and sum stay in the registers of
-// the 16 threads that share a row. It is bound by the FMA rate and by shared memory; the sums are
-// fp32 throughout, which the fp32 types need.
+// A block takes units of 32 rows over tiles of 64 tokens (tree_plan.cuh). K and V of a tile are fp32
+// in shared memory and used by all 32 rows; a thread computes 4 rows x 4 tokens of scores and 4 rows
+// x D / 16 dims of the weighted values, so that a 16-byte shared-memory load feeds eight to eleven
+// FMAs, issued as pairs. The next tile is on its way meanwhile, into the same buffers: its K comes
+// while this tile's softmax and values are worked on, its V during the next scores. The softmax is
+// online: the running maximum and sum stay in the registers of the 16 threads that share a row; sums
+// are fp32 throughout, as the fp32 types need, and a tile's weighted values are summed before they
+// join the whole's.
+//
+// Bound by FMAs and by the latency of the loads that feed them (two blocks of four warps on an SM):
+// 16 requests of 500 .. 4000 tokens, 96 rows a KV head, 128 dims, F32: 14.2 GFLOP in 423 us, 34
+// TFLOP/s, half of the fp32 rate (2 rows x 4 tokens a thread, 32-token tiles: 503 us); 32 rows, FP8:
+// 171 us (278). One request, 2000 tokens, 8 nodes: 32 us with its combine (64 threads and 32-token
+// tiles: 46).
 #include <math.h>
 
 #include <atomic>
 
 #include "pkv_device.cuh"
 #include "pkv_internal.h"
+#include "tcgen05.cuh"
 #include "tree_plan.cuh"
 
 namespace pkv {
@@ -26,36 +35,16 @@ namespace {
 
 constexpr int kThreads = 128;
 constexpr int kRows = kTreeSimtRows, kTok = kTreeSimtTokens;
+constexpr int kPages = kTok / kPageSize;
+static_assert(kRows == 32 && kTok == 64, "a thread has 4 rows and 4 tokens of a tile");
 
-template <typename KV, int D>
+template <int D>
 struct SimtShape {
   static constexpr int LD = D + 4;   // row pitch (floats): keeps float4 alignment, spreads banks
-  static constexpr int LP = kTok + 4;
-  // an fp32 cache's next tile is copied (cp.async) while this one is worked on: two K and V tiles
-  static constexpr bool AHEAD = KV::bytes == 4;
-  static constexpr int TILES = AHEAD ? 2 : 1;
-  static constexpr int SMEM = 4 * ((1 + 2 * TILES) * kRows * LD + kRows * LP);
+  static constexpr int LP = kTok + 8;
+  static constexpr int SMEM = 4 * ((kRows + 2 * kTok) * LD + kRows * LP);
+  static constexpr int CTAS = tree_simt_wave(D) / 152;  // resident on an SM
 };
-static_assert(kRows == kTok, "Q, K and V tiles have the same shape");
-
-// Four consecutive elements, widened.
-template <typename T>
-__device__ __forceinline__ float4 load4(const void* base, int64_t i) {
-  float o[4];
-  RowLoad<T, 4>::run(static_cast<const uint8_t*>(base) + i * T::bytes, o);
-  return make_float4(o[0], o[1], o[2], o[3]);
-}
-
-__device__ __forceinline__ void fma4(float4& acc, float p, const float4& v) {
-  acc.x = fmaf(p, v.x, acc.x);
-  acc.y = fmaf(p, v.y, acc.y);
-  acc.z = fmaf(p, v.z, acc.z);
-  acc.w = fmaf(p, v.w, acc.w);
-}
-
-__device__ __forceinline__ void store4(float* p, const float4& v) {
-  *reinterpret_cast<float4*>(p) = v;
-}
 
 // 16 bytes from global to shared memory, asynchronously; zeros when the source is not there.
 __device__ __forceinline__ void copy16(float* dst, const void* src, bool there) {
@@ -64,214 +53,312 @@ __device__ __forceinline__ void copy16(float* dst, const void* src, bool there) 
                : "memory");
 }
 
-template <typename KV, typename Q, int D>
-__global__ void __launch_bounds__(kThreads) tree_simt_kernel(const TreeArgs a) {
-  using S = SimtShape<KV, D>;
-  using TQ = typename Q::storage;
+template <bool B>
+struct Flag {
+  static constexpr bool value = B;
+};
+
+// Four fp32 values of shared memory as two pairs.
+__device__ __forceinline__ ulonglong2 pairs(const float* p) {
+  return *reinterpret_cast<const ulonglong2*>(p);
+}
+
+template <typename KV, int D>
+__global__ void __launch_bounds__(kThreads, SimtShape<D>::CTAS) tree_simt_kernel(const TreeArgs a) {
+  using S = SimtShape<D>;
+  constexpr bool WIDEN = KV::bytes == 1;
   constexpr int NQ = D / 64;  // float4 groups of dims a thread accumulates, 64 dims apart
   constexpr int LD = S::LD, LP = S::LP;
   extern __shared__ float4 smem4[];
   float* qs = reinterpret_cast<float*>(smem4);
-  float* tiles = qs + kRows * LD;  // K and V of a tile, of the next one behind them
-  float* ps = tiles + 2 * S::TILES * kTok * LD;
+  float* ks = qs + kRows * LD;
+  float* vs = ks + kTok * LD;
+  float* ps = vs + kTok * LD;
   __shared__ int scratch[64];
   __shared__ TreeShare share;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   tree_share<kThreads>(a, scratch, &share);
   TreeWalk walk(a, share);
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;  // tokens / dims, group of 4 rows
+  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;  // tokens tx + 16 m / dims, rows ty + 8 i
   TreeRun run;
   while (walk.next(a, run)) {
     const int b = run.b, j = run.j;
+    const int32_t* table = a.block_tables + (size_t)b * a.max_pages;
+    // the pages of a tile: their first rows in the pools, in elements, or -1
+    struct Pages {
+      int64_t row[kPages];
+      bool bad;  // one that should be there is not in the pool
+    };
+    auto pages_of = [&](int tile) {
+      Pages p;
+      p.bad = false;
+#pragma unroll
+      for (int h = 0; h < kPages; ++h) {
+        const int lp = kPages * tile + h;
+        const bool wanted = lp * kPageSize < run.req.read;
+        const int id = wanted ? table[lp] : -1;
+        const bool there = id >= 0 && id < a.num_pages;
+        p.row[h] = there ? ((int64_t)id * a.h_kv + j) * kPageSize * D : -1;
+        p.bad |= wanted && !there;
+      }
+      return p;
+    };
+    auto first_row = [](const Pages& p, int h) {  // (no indexing: the rows stay in registers)
+      return h < 2 ? (h == 0 ? p.row[0] : p.row[1]) : (h == 2 ? p.row[2] : p.row[3]);
+    };
+    // A tile of K or V comes into shared memory as fp32, zeros for a page that is not there: from an
+    // fp32 pool by asynchronous copies, from an 8-bit one through registers (get, then put).
+    auto copy = [&](float* dst, const void* pool, const Pages& p) {
+#pragma unroll
+      for (int i = 0; i < kTok * D / 4 / kThreads; ++i) {
+        const int e = i * kThreads + threadIdx.x, r = e / (D / 4), c = e % (D / 4);
+        const int64_t from = first_row(p, r / kPageSize);
+        copy16(dst + r * LD + 4 * c,
+               static_cast<const float*>(pool) + (from < 0 ? 0 : from + r % kPageSize * D + 4 * c),
+               from >= 0);
+      }
+    };
+    auto copied = [] { asm volatile("cp.async.commit_group;" ::: "memory"); };
+    constexpr int RAW = WIDEN ? kTok * D / 16 / kThreads : 1;  // 16-code chunks of a thread
+    auto get = [&](uint4 (&raw)[RAW], const void* pool, const Pages& p) {
+#pragma unroll
+      for (int i = 0; i < RAW; ++i) {
+        const int e = i * kThreads + threadIdx.x, r = e / (D / 16), c = e % (D / 16);
+        const int64_t from = first_row(p, r / kPageSize);
+        raw[i] = from < 0 ? make_uint4(0, 0, 0, 0)
+                          : *reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(pool) +
+                                                            from + r % kPageSize * D + 16 * c);
+      }
+    };
+    auto put = [&](float* dst, const uint4 (&raw)[RAW]) {
+#pragma unroll
+      for (int i = 0; i < RAW; ++i) {
+        const int e = i * kThreads + threadIdx.x, r = e / (D / 16), c = e % (D / 16);
+        const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          float o[4];
+          RowLoad<KV, 4>::run(reinterpret_cast<const uint8_t*>(&w[k]), o);
+          *reinterpret_cast<float4*>(dst + r * LD + 16 * c + 4 * k) =
+              make_float4(o[0], o[1], o[2], o[3]);
+        }
+      }
+    };
+    uint4 kraw[RAW], vraw[RAW];
     __syncthreads();  // the previous run is done with the shared tiles
+    Pages here = pages_of(run.tile0);
+    if constexpr (WIDEN) {
+      get(kraw, a.k_cache, here);
+      get(vraw, a.v_cache, here);
+    } else {
+      copy(ks, a.k_cache, here);
+      copied();
+      copy(vs, a.v_cache, here);
+      copied();
+    }
     for (int e = threadIdx.x; e < kRows * (D / 4); e += kThreads) {
       const int r = e / (D / 4), c = e % (D / 4);
       float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
       if (r < run.rows) {
         const int R = run.row0 + r, t = R / a.group, g = R % a.group;
-        v = load4<Q>(a.q, (((int64_t)b * a.nodes + t) * a.h_q + j * a.group + g) * D + 4 * c);
+        v = *reinterpret_cast<const float4*>(
+            static_cast<const float*>(a.q) +
+            (((int64_t)b * a.nodes + t) * a.h_q + j * a.group + g) * D + 4 * c);
       }
       *reinterpret_cast<float4*>(qs + r * LD + 4 * c) = v;
     }
+    if constexpr (WIDEN) {
+      put(ks, kraw);
+      put(vs, vraw);
+    }
     float m[4], l[4];
-    float4 acc[4][NQ];
+    uint64_t acc[4][2 * NQ];  // pairs of dims
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       m[i] = -INFINITY;
       l[i] = 0.f;
 #pragma unroll
-      for (int k = 0; k < NQ; ++k) acc[i][k] = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int k = 0; k < 2 * NQ; ++k) acc[i][k] = 0;
     }
-    const float sc = a.scale_log2 * (KV::bytes == 1 ? a.k_scales[j] : 1.f);
-    const int32_t* table = a.block_tables + (size_t)b * a.max_pages;
-    // a tile's K and V, widened, into buffer `at`; rows past the context or on a bad page are zero
-    auto fetch = [&](int tile, float* at) {
-      for (int e = threadIdx.x; e < kTok * (D / 4); e += kThreads) {
-        const int r = e / (D / 4), c = e % (D / 4), pos = tile * kTok + r;
-        const int id = pos < run.req.read ? table[pos / kPageSize] : -1;
-        const bool there = id >= 0 && id < a.num_pages;
-        const int64_t from =
-            there ? (((int64_t)id * a.h_kv + j) * kPageSize + pos % kPageSize) * D + 4 * c : 0;
-        float* k = at + r * LD + 4 * c;
-        float* v = k + kTok * LD;
-        if constexpr (S::AHEAD) {
-          copy16(k, static_cast<const float*>(a.k_cache) + from, there);
-          copy16(v, static_cast<const float*>(a.v_cache) + from, there);
-        } else {
-          const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
-          *reinterpret_cast<float4*>(k) = there ? load4<KV>(a.k_cache, from) : zero;
-          *reinterpret_cast<float4*>(v) = there ? load4<KV>(a.v_cache, from) : zero;
-        }
-      }
-      if constexpr (S::AHEAD) asm volatile("cp.async.commit_group;" ::: "memory");
-    };
-    if constexpr (S::AHEAD) fetch(run.tile0, tiles);
+    const float sc = a.scale_log2 * (WIDEN ? a.k_scales[j] : 1.f);
     for (int i0 = 0; i0 < run.n; ++i0) {
       const int tile = run.tile0 + i0, p0 = tile * kTok;
+      const bool more = i0 + 1 < run.n;
       const bool tail = p0 + kTok > min(run.req.base, run.req.read);  // not all positions seen
-      uint32_t page_ok = 0;  // one bit per token
+      uint64_t page_ok = 0;  // one bit per token
 #pragma unroll
-      for (int pg = 0; pg < kTok / kPageSize; ++pg) {
-        const int lp = p0 / kPageSize + pg;
-        const int id = lp * kPageSize < run.req.read ? table[lp] : -1;
-        if (id >= 0 && id < a.num_pages)
-          page_ok |= 0xffffu << (16 * pg);
-        else if (lp * kPageSize < run.req.read && threadIdx.x == 0)
-          atomicOr(a.err, PKV_DEVERR_BAD_PAGE);
-      }
-      float* ks = tiles;
-      if constexpr (S::AHEAD) {
-        ks = tiles + (i0 & 1) * 2 * kTok * LD;
-        if (i0 + 1 < run.n) {
-          fetch(tile + 1, tiles + (~i0 & 1) * 2 * kTok * LD);
-          asm volatile("cp.async.wait_group 1;" ::: "memory");
-        } else {
-          asm volatile("cp.async.wait_group 0;" ::: "memory");
+      for (int h = 0; h < kPages; ++h)
+        if (here.row[h] >= 0) page_ok |= 0xffffull << (16 * h);
+      if (here.bad && threadIdx.x == 0) atomicOr(a.err, PKV_DEVERR_BAD_PAGE);
+      if (more) here = pages_of(tile + 1);
+      if constexpr (WIDEN) {
+        if (more) {
+          get(kraw, a.k_cache, here);
+          get(vraw, a.v_cache, here);
         }
       } else {
-        __syncthreads();  // the previous tile is used up
-        fetch(tile, tiles);
+        asm volatile("cp.async.wait_group 1;" ::: "memory");  // K (V may still be on its way)
       }
-      const float* vs = ks + kTok * LD;
       __syncthreads();
-      // ---- scores of rows 4 ty + i, tokens tx and tx + 16 ----
-      float s[4][2];
+      // ---- scores of rows ty + 8 i, tokens tx + 16 m: sums of even and of odd dims ----
+      uint64_t s2[4][4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) s[i][0] = s[i][1] = 0.f;
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) s2[i][k] = 0;
 #pragma unroll 4
       for (int d = 0; d < D; d += 4) {
-        const float4 k0 = *reinterpret_cast<const float4*>(ks + tx * LD + d);
-        const float4 k1 = *reinterpret_cast<const float4*>(ks + (tx + 16) * LD + d);
+        ulonglong2 k[4];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) k[t] = pairs(ks + (tx + 16 * t) * LD + d);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const float4 q = *reinterpret_cast<const float4*>(qs + (4 * ty + i) * LD + d);
-          s[i][0] = fmaf(q.x, k0.x, fmaf(q.y, k0.y, fmaf(q.z, k0.z, fmaf(q.w, k0.w, s[i][0]))));
-          s[i][1] = fmaf(q.x, k1.x, fmaf(q.y, k1.y, fmaf(q.z, k1.z, fmaf(q.w, k1.w, s[i][1]))));
+          const ulonglong2 q = pairs(qs + (ty + 8 * i) * LD + d);
+#pragma unroll
+          for (int t = 0; t < 4; ++t) s2[i][t] = fma2(q.y, k[t].y, fma2(q.x, k[t].x, s2[i][t]));
         }
       }
+      __syncthreads();  // K is used up: the next tile's comes in its place
+      if constexpr (WIDEN) {
+        if (more) put(ks, kraw);
+      } else {
+        if (more) copy(ks, a.k_cache, here);
+        copied();
+      }
       // ---- online softmax; a row's 16 threads hold the same m and l ----
-      uint32_t seen[4];
+      uint64_t seen[4];
       float scale[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const int R = 4 * ty + i;
+        const int R = ty + 8 * i;
         seen[i] = page_ok;
         if (tail)
           seen[i] &= R < run.rows
-                         ? (uint32_t)tree_seen(a, run.req, b, (run.row0 + R) / a.group, p0)
-                         : 0u;
-        s[i][0] = (seen[i] >> tx) & 1 ? s[i][0] * sc : -INFINITY;
-        s[i][1] = (seen[i] >> (tx + 16)) & 1 ? s[i][1] * sc : -INFINITY;
-        float mx = fmaxf(s[i][0], s[i][1]);
+                         ? tree_seen(a, run.req, b, (run.row0 + R) / a.group, p0)
+                         : 0ull;
+        float s[4];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          float even, odd;
+          unpack2(s2[i][t], even, odd);
+          s[t] = (seen[i] >> (tx + 16 * t)) & 1 ? (even + odd) * sc : -INFINITY;
+        }
+        float mx = fmaxf(fmaxf(s[0], s[1]), fmaxf(s[2], s[3]));
 #pragma unroll
         for (int o = 8; o >= 1; o /= 2) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
         const float mn = fmaxf(m[i], mx);
         const float mu = mn == -INFINITY ? 0.f : mn;
         const float alpha = exp2f(m[i] - mu);
-        const float e0 = exp2f(s[i][0] - mu), e1 = exp2f(s[i][1] - mu);
-        float sum = e0 + e1;
+        float sum = 0.f;
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          const float e = exp2f(s[t] - mu);
+          ps[R * LP + tx + 16 * t] = e;
+          sum += e;
+        }
 #pragma unroll
         for (int o = 8; o >= 1; o /= 2) sum += __shfl_xor_sync(0xffffffffu, sum, o);
         l[i] = fmaf(l[i], alpha, sum);
         m[i] = mn;
         scale[i] = alpha;
-        ps[R * LP + tx] = e0;
-        ps[R * LP + tx + 16] = e1;
       }
-      __syncwarp();  // a row's P is written and read by the same half warp
-      // ---- weighted values of rows 4 ty + i, dims 4 tx + 64 k ..: the tile's own sums first, so that
+      if constexpr (WIDEN) {
+        __syncwarp();  // a row's P is written and read by the same half warp
+      } else {
+        asm volatile("cp.async.wait_group 1;" ::: "memory");  // V
+        __syncthreads();
+      }
+      // ---- weighted values of rows ty + 8 i, dims 4 tx + 64 k ..: the tile's own sums first, so that
       // a long context's sums do not round once per token against the whole ----
-      float4 own[4][NQ];
+      uint64_t own[4][2 * NQ];
 #pragma unroll
       for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int k = 0; k < NQ; ++k) own[i][k] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (!tail && page_ok == 0xffffffffu) {
-#pragma unroll 4
-        for (int t = 0; t < kTok; ++t) {
-          float p[4];
+        for (int k = 0; k < 2 * NQ; ++k) own[i][k] = 0;
+      // an unseen value may be infinite or NaN, which a weight of 0 does not remove: where some
+      // positions are not seen, a token whose values are not all finite takes part row by row
+      auto weigh = [&](auto careful_) {
+      constexpr bool careful = decltype(careful_)::value;
+#pragma unroll 2
+      for (int t = 0; t < kTok; t += 4) {
+        float4 p[4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) p[i] = ps[(4 * ty + i) * LP + t];
+        for (int i = 0; i < 4; ++i)
+          p[i] = *reinterpret_cast<const float4*>(ps + (ty + 8 * i) * LP + t);
 #pragma unroll
-          for (int k = 0; k < NQ; ++k) {
-            const float4 v = *reinterpret_cast<const float4*>(vs + t * LD + 4 * tx + 64 * k);
+        for (int u = 0; u < 4; ++u) {
+          ulonglong2 v[NQ];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) fma4(own[i][k], p[i], v);
+          for (int k = 0; k < NQ; ++k) v[k] = pairs(vs + (t + u) * LD + 4 * tx + 64 * k);
+          bool hot = false;
+          if constexpr (careful) {
+            uint64_t z = 0;  // sums of 0 v
+#pragma unroll
+            for (int k = 0; k < NQ; ++k) z = fma2(v[k].y, 0, fma2(v[k].x, 0, z));
+            float z0, z1;
+            unpack2(z, z0, z1);
+            hot = z0 + z1 != 0.f;
           }
-        }
-      } else {  // an unseen value may be infinite or NaN: it takes no part at all
-        for (int t = 0; t < kTok; ++t) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            if (!((seen[i] >> t) & 1)) continue;
-            const float p = ps[(4 * ty + i) * LP + t];
+            if (careful && hot && !((seen[i] >> (t + u)) & 1)) continue;
+            const float w = u == 0 ? p[i].x : u == 1 ? p[i].y : u == 2 ? p[i].z : p[i].w;
+            const uint64_t ww = pack2(w, w);
 #pragma unroll
-            for (int k = 0; k < NQ; ++k)
-              fma4(own[i][k], p, *reinterpret_cast<const float4*>(vs + t * LD + 4 * tx + 64 * k));
+            for (int k = 0; k < NQ; ++k) {
+              own[i][2 * k] = fma2(ww, v[k].x, own[i][2 * k]);
+              own[i][2 * k + 1] = fma2(ww, v[k].y, own[i][2 * k + 1]);
+            }
           }
         }
       }
+      };
+      if (tail || page_ok != ~0ull)
+        weigh(Flag<true>{});
+      else
+        weigh(Flag<false>{});
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+      for (int i = 0; i < 4; ++i) {
+        const uint64_t c = pack2(scale[i], scale[i]);
 #pragma unroll
-        for (int k = 0; k < NQ; ++k) {
-          acc[i][k].x = fmaf(acc[i][k].x, scale[i], own[i][k].x);
-          acc[i][k].y = fmaf(acc[i][k].y, scale[i], own[i][k].y);
-          acc[i][k].z = fmaf(acc[i][k].z, scale[i], own[i][k].z);
-          acc[i][k].w = fmaf(acc[i][k].w, scale[i], own[i][k].w);
-        }
-      if constexpr (S::AHEAD) __syncthreads();  // the tile after the next may overwrite this one
+        for (int k = 0; k < 2 * NQ; ++k) acc[i][k] = fma2(acc[i][k], c, own[i][k]);
+      }
+      __syncthreads();  // V is used up
+      if constexpr (WIDEN) {
+        if (more) put(vs, vraw);
+      } else {
+        if (more) copy(vs, a.v_cache, here);
+        copied();
+      }
     }
     // ---- the run's rows: finished, or a partial ----
-    const float vsc = KV::bytes == 1 ? a.v_scales[j] : 1.f;
+    const float vsc = WIDEN ? a.v_scales[j] : 1.f;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int r = 4 * ty + i;
+      const int r = ty + 8 * i;
       if (r >= run.rows) continue;
+      float* o;
       if (run.whole) {
         const int R = run.row0 + r, t = R / a.group, g = R % a.group;
-        TQ* o = static_cast<TQ*>(a.out) +
-                (((int64_t)b * a.nodes + t) * a.h_q + j * a.group + g) * D + 4 * tx;
-#pragma unroll
-        for (int k = 0; k < NQ; ++k) {
-          const float4 v = acc[i][k];
-          const bool any = l[i] != 0.f;  // (a NaN sum stays NaN)
-          store4(o + 64 * k, any ? make_float4(v.x / l[i] * vsc, v.y / l[i] * vsc,
-                                               v.z / l[i] * vsc, v.w / l[i] * vsc)
-                                 : make_float4(0.f, 0.f, 0.f, 0.f));
-        }
+        o = static_cast<float*>(a.out) +
+            (((int64_t)b * a.nodes + t) * a.h_q + j * a.group + g) * D + 4 * tx;
       } else {
         const size_t part = ((size_t)blockIdx.x * 2 + run.slot) * kRows + r;
+        o = a.ws_acc + part * D + 4 * tx;
+        if (tx == 0) *reinterpret_cast<float2*>(a.ws_ml + 2 * part) = make_float2(m[i], l[i]);
+      }
 #pragma unroll
-        for (int k = 0; k < NQ; ++k) {
-          const float4 v = acc[i][k];
-          store4(a.ws_acc + part * D + 4 * tx + 64 * k,
-                 make_float4(v.x * vsc, v.y * vsc, v.z * vsc, v.w * vsc));
-        }
-        if (tx == 0) {
-          a.ws_ml[2 * part] = m[i];
-          a.ws_ml[2 * part + 1] = l[i];
-        }
+      for (int k = 0; k < NQ; ++k) {
+        float4 v;
+        unpack2(acc[i][2 * k], v.x, v.y);
+        unpack2(acc[i][2 * k + 1], v.z, v.w);
+        if (!run.whole)
+          v = make_float4(v.x * vsc, v.y * vsc, v.z * vsc, v.w * vsc);
+        else if (l[i] != 0.f)  // (a NaN sum stays NaN)
+          v = make_float4(v.x / l[i] * vsc, v.y / l[i] * vsc, v.z / l[i] * vsc, v.w / l[i] * vsc);
+        else
+          v = make_float4(0.f, 0.f, 0.f, 0.f);
+        *reinterpret_cast<float4*>(o + 64 * k) = v;
       }
     }
   }
@@ -415,27 +502,27 @@ __global__ void __launch_bounds__(kCombineThreads) tree_combine_kernel(const Tre
   }
 }
 
-template <typename KV, typename Q, int D>
+template <typename KV, int D>
 cudaError_t simt_go(const TreeArgs& a, cudaStream_t s) {
   static std::atomic<unsigned long long> attr_done{0};  // one bit per device
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev >= 64 || !((attr_done.load() >> dev) & 1ull)) {
-    e = cudaFuncSetAttribute(tree_simt_kernel<KV, Q, D>,
-                             cudaFuncAttributeMaxDynamicSharedMemorySize, SimtShape<KV, D>::SMEM);
+    e = cudaFuncSetAttribute(tree_simt_kernel<KV, D>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, SimtShape<D>::SMEM);
     if (e != cudaSuccess) return e;
     if (dev < 64) attr_done.fetch_or(1ull << dev);
   }
-  tree_simt_kernel<KV, Q, D><<<a.ctas, kThreads, SimtShape<KV, D>::SMEM, s>>>(a);
+  tree_simt_kernel<KV, D><<<a.ctas, kThreads, SimtShape<D>::SMEM, s>>>(a);
   return cudaGetLastError();
 }
 
 template <int D>
 cudaError_t simt_types(const TreeArgs& a, int kv_dtype, cudaStream_t s) {
-  if (kv_dtype == PKV_F32) return simt_go<F32, F32, D>(a, s);
-  if (kv_dtype == PKV_FP8_E4M3) return simt_go<FP8, F32, D>(a, s);
-  return simt_go<INT8, F32, D>(a, s);
+  if (kv_dtype == PKV_F32) return simt_go<F32, D>(a, s);
+  if (kv_dtype == PKV_FP8_E4M3) return simt_go<FP8, D>(a, s);
+  return simt_go<INT8, D>(a, s);
 }
 
 template <typename TQ, int D, int RW, int CB>
