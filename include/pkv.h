@@ -760,9 +760,9 @@ size_t pkv_tree_decode_workspace_size(int32_t dtype_q, int32_t cache_dtype, int3
  * Requires num_q_heads % num_kv_heads == 0, at most PKV_MAX_TREE_GROUP query heads per KV head (any
  * number, not only powers of two) and tree_width <= PKV_MAX_TREE_NODES. PKV_ESHAPE also for a BF16
  * pool of 2^31 rows (num_pages * num_kv_heads * page_size) or more, a table row of 2^31 positions or
- * more, and a table that could hold about 2^29 tiles of 64 tokens over all
- * requests, KV heads and 256 rows (32) of drafted nodes and query heads. Equal inputs give equal
- * results; the split over the GPU, and so the rounding, depends on all requests' lengths.
+ * more, and a table that could hold about 2^28 tiles (of 64 tokens, counted for every request, KV
+ * head and 256 rows of drafted nodes and query heads; fp32 queries: 32 rows). Equal inputs give
+ * equal results; the split over the GPU, and so the rounding, depends on all requests' lengths.
  */
 int pkv_tree_decode_attention(const void* q, int32_t dtype_q, int32_t batch, int32_t tree_width,
                               int32_t num_q_heads, const void* k_cache, const void* v_cache,

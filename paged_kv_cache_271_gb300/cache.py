@@ -180,7 +180,8 @@ class PagedKVCache:
                     stream=None) -> list:
         """Keep the accepted path of each request's draft: move its rows together (tree_commit),
         read the new lengths back (this waits for the stream) and truncate the requests to them.
-        Returns the new lengths."""
+        Returns the new lengths. The drafted rows' pages must be the request's own, as ``reserve``
+        leaves them: fork a request before its draft or after this, not in between."""
         if stream is None:
             stream = torch.cuda.current_stream(self.k.device)
         elif not isinstance(stream, torch.cuda.Stream):  # a raw cudaStream_t handle

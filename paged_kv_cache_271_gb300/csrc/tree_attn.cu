@@ -370,8 +370,10 @@ __global__ void __launch_bounds__(kThreads, SimtShape<D>::CTAS) tree_simt_kernel
 // M = max m_c, out = sum 2^(m_c - M) acc_c / sum 2^(m_c - M) l_c. A warp merges RW rows, reading
 // the (m, l) pairs of up to 32 partials of each at once and the values of CB partials of each
 // together: a row is two reads that wait on one another, so what counts is how many are under way.
-// Few rows in all: one row per warp; many: four, in fewer blocks, each of which has to find its place
-// in the split first. Launched as a programmatic dependent: blocks that start early find it while
+// Few rows in all: one row per warp (with the attention, one request of 8 nodes: 20 us against 24 with
+// four rows a warp, over 8000 tokens 30 against 36); many: four, in fewer blocks, each of which has to
+// find its place in the split first (64 ragged drafts of up to 256 rows: 141 us against 162 with one;
+// 128 requests of 192 rows a head, FP8: 366 against 401). Launched as a programmatic dependent: blocks that start early find it while
 // the attention still runs.
 constexpr int kCombineThreads = 128;
 constexpr int kCombineWarps = kCombineThreads / 32;

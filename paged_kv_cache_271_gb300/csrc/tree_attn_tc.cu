@@ -7,19 +7,29 @@
 // rows it is bound by reading the cache once; the work here is arranged so that everything else
 // hides behind those reads:
 //
-//  * a copy warp streams tiles of K and V into a ring of shared-memory stages, running ahead across
-//    units; a bf16 tile arrives by TMA in the 128-byte-swizzled form the MMAs read. The codes of an
-//    8-bit tile arrive by bulk copies and four converter warps widen them to f16 (exactly) in that
-//    form; the K scale goes into the score factor and the V scale into the output;
-//  * an MMA warp (one lane) issues S = Q K^T (M = 128 rows, N = 64 tokens) and O += P V (N = D),
-//    with Q and P as A operands in tensor memory and all accumulators there;
-//  * two groups of four softmax warps, thread r of a group owning row r. Units of up to 128 rows:
-//    the groups take alternate tiles, each with a maximum, a sum and an O of its own, merged at the
-//    unit's end (three S buffers); larger units: group g takes rows 128 g .. of every tile (two S
-//    buffers), so the cache is still read once. Either way one group's softmax overlaps the other's
-//    MMAs;
+//  * two copy warps stream the share's tiles, one K and one V, through rings of shared memory,
+//    running ahead across units; a bf16 tile arrives by TMA in the 128-byte-swizzled form the MMAs
+//    read. The codes of an 8-bit tile arrive by bulk copies and four converter warps widen them to
+//    f16 (exactly) in that form; the K scale goes into the score factor and the V scale into the
+//    output. The K warp also walks the share and hands its runs to the others;
+//  * two MMA warps: one issues S = Q K^T (M = 128 rows, N = 64 tokens) up to four steps ahead, the
+//    other O += P V (N = D), with P as an A operand in the tensor memory that held S and all
+//    accumulators there (one warp issuing both was the limit of an 8-bit cache's small units);
+//  * two groups of four softmax warps, thread r of a group owning row r. Units of up to 128 rows: the
+//    groups take alternate tiles, which add into one O; a row's reference maximum goes from step to
+//    step through shared memory, set before anything else of a step is done, and each group keeps
+//    its own sum. Larger units: group g takes rows 128 g .. of every tile with an O of its own, so the
+//    cache is still read once;
 //  * O is rescaled only when a row's maximum grows by more than 2^8 (P <= 2^8 until then): the final
 //    (max, sum, O) is exact whatever maximum it was accumulated against.
+//
+// Two kernels: a call whose drafts have at most 128 rows a KV head keeps a unit's queries in tensor
+// memory beside an O and four S buffers and has the whole of shared memory for the rings; with more
+// rows the tensor memory holds two O and four S, and the queries are read from 64 KB of shared memory
+// (in tensor memory they left room for two S buffers: 425 us instead of 380 for 128 requests of 128
+// .. 8192 FP8 tokens and 192 rows a head; 169 instead of 142 for ragged bf16 drafts). The queries of
+// the larger kernel are prefetched into L2 when a run is handed out (wide FP8 208 us without, 204
+// with; in the smaller kernel the prefetch costs more than it gives: 64 dims 83 without, 92 with).
 //
 // P is rounded to the MMA's input type (bf16 for a bf16 cache, f16 otherwise), the only rounding
 // before the output's; scores, maxima and sums are fp32. For 8-bit caches a query row is scaled by
@@ -30,6 +40,13 @@
 // rows outside the context or on a bad page become 0, and a drafted row's infinite or NaN values,
 // which 0 P would still spread to rows that do not see the node, become 0 there and are added to
 // the rows that do see it at the unit's end.
+//
+// Measured with the combine, L2 flushed, against the bytes at the copy's 6.78 TB/s: 64 requests of 512
+// .. 4096 bf16 tokens, 64 rows a head: 118 us (5.84 TB/s; 102); ragged drafts of up to 256 rows: 142
+// (96); 4 requests of 8191 .. 65536 INT8 tokens, 96 rows: 60 (5.9 TB/s; 53); FP8, 64 rows: 108 (52).
+// Small units of an 8-bit or 64-dim cache and all large units are bound by the softmax steps, about
+// 1400 cycles of waits, tensor-memory loads and exponentials for 128 rows x 64 tokens, two at a time
+// on an SM, and by 4 to 8 thousand cycles from the last step of a unit to the first of the next.
 //
 // Every wait is bounded (PKV_DEVERR_TIMEOUT); the tensor memory is freed on every path.
 #include <atomic>
@@ -50,7 +67,7 @@ constexpr int kTok = kTreeTcTokens;        // tokens of a tile
 constexpr int kPages = kTok / kPageSize;   // pages of a tile
 constexpr int kGroupThreads = 128;         // a softmax group: one row per thread
 constexpr int kSoftThreads = 2 * kGroupThreads;
-constexpr int kMmaWarp = kSoftThreads / 32;  // two: MMAs of group 0's and of group 1's steps
+constexpr int kMmaWarp = kSoftThreads / 32;  // two: S and P V
 constexpr int kCopyWarp = kMmaWarp + 2;      // two: copies of K and of V
 constexpr int kConvWarp = kMmaWarp + 4;      // first of four (8-bit caches)
 constexpr int kConvThreads = 128;

@@ -6,7 +6,9 @@
 // row is written before it has been read. A thread owns 16 bytes of every row of one head of one
 // request and reads kAhead of its rows before it writes the first of them (a row written, i, is
 // below every node still to be read, path[k] >= k > i), so threads never wait for one another and
-// the moves' latency overlaps. Bound by latency: a step moves a few rows per request.
+// the moves' latency overlaps. Bound by latency: a step moves a few rows per request (64 requests of
+// up to 5 accepted nodes, bf16: 9 us, 256 of up to 12, FP8: 11 us, graph replay with about 5 us of its
+// own).
 #include <algorithm>
 
 #include "pkv_device.cuh"
