@@ -713,6 +713,18 @@ def _raw_stream(stream, dev: int) -> int:
     return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
 
 
+def _new(make, shape, dtype, device, stream):
+    """A tensor that a call makes for itself or its caller, on the stream that the call runs on: the
+    allocator then never hands its memory to another stream while the call still uses it, and a fill
+    comes before the call."""
+    if stream is None:
+        return make(shape, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):  # a raw cudaStream_t handle
+        stream = torch.cuda.ExternalStream(int(stream), device=device)
+    with torch.cuda.stream(stream):
+        return make(shape, dtype=dtype, device=device)
+
+
 @functools.lru_cache(maxsize=256)
 def _pool_desc(shape, dtype) -> _Desc:
     """cache_desc of pools of this shape and type (never changed: shared between calls)."""
@@ -781,7 +793,7 @@ def qk_norm_rope_append(q, k, v, positions, slot_mapping, k_cache, v_cache, cos_
             raise PkvError(-2, "%s must be [head_dim] of q's dtype" % name)
     _check_scales(desc, k_scales, v_scales)
     if q_out is None:
-        q_out = torch.empty((n, h_q, d), dtype=dtype, device=q.device)
+        q_out = _new(torch.empty, (n, h_q, d), dtype, q.device, stream)
         op, os_ = q_out.data_ptr(), h_q * d
     else:
         if q_out.dtype != dtype or q_out.shape != q.shape:
@@ -862,7 +874,8 @@ def tree_decode_attention(q, k_cache, v_cache, block_tables, context_lens, scale
         stride = 0 if tree_mask.shape[0] == 1 else T * words
     _check_scales(desc, k_scales, v_scales)
     if out is None:
-        out = (torch.empty_like if tree_lens is None else torch.zeros_like)(q)
+        out = _new(torch.empty if tree_lens is None else torch.zeros, q.shape, q.dtype, q.device,
+                   stream)
     elif out.shape != q.shape or out.dtype != q.dtype:
         raise PkvError(-2, "out must match q in shape and dtype")
     dev = torch.cuda.current_device()
@@ -870,7 +883,7 @@ def tree_decode_attention(q, k_cache, v_cache, block_tables, context_lens, scale
     if workspace is None:
         need = tree_decode_workspace_size(code, desc.cache_dtype, B, T, h_q, desc.num_kv_heads, d,
                                           maxp)
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        workspace = _new(torch.empty, need, torch.uint8, q.device, stream)
     _check(lib().pkv_tree_decode_attention(
         _addr(q, "q", dev), code, B, T, h_q, _addr(k_cache, "k_cache", dev),
         _addr(v_cache, "v_cache", dev), desc, _addr(block_tables, "block_tables", dev), maxp,
@@ -898,7 +911,7 @@ def tree_commit(k_cache, v_cache, block_tables, context_lens, tree_lens, path, p
         raise PkvError(-2, "block_tables and path must be [batch, n], the lengths [batch]")
     desc = _pools(k_cache, v_cache)
     if new_lens is None:
-        new_lens = torch.empty(B, dtype=torch.int32, device=k_cache.device)
+        new_lens = _new(torch.empty, B, torch.int32, k_cache.device, stream)
     elif new_lens.dtype != torch.int32 or new_lens.numel() != B:
         raise PkvError(-2, "new_lens must be int32 [batch]")
     dev = torch.cuda.current_device()

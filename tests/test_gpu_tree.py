@@ -584,6 +584,36 @@ def test_tree_attention_two_streams_two_workspaces():
         assert torch.equal(t.out, w)
 
 
+def test_calls_on_another_stream_make_their_tensors_there(monkeypatch):
+    """What a call allocates belongs to the stream it is given, and a new output's zeros come before
+    the attention: the current stream is kept busy so that a fill on it would come after."""
+    t = Tree([100, 30], [6, 3], 6, 4, 2, 128, "bf16", "bf16", seed=23)
+    want = t.check().clone()
+    x = t.q[0].contiguous()
+    nowhere = torch.full((6,), -1, device="cuda")
+    path = torch.zeros(2, 1, dtype=torch.int32, device="cuda")
+    none = path[:, 0].contiguous()
+    side, seen = torch.cuda.Stream(), []
+    for name in ("empty", "zeros"):
+        def spy(*a, _make=getattr(torch, name), **k):
+            seen.append(torch.cuda.current_stream().cuda_stream)
+            return _make(*a, **k)
+        monkeypatch.setattr(torch, name, spy)
+    for stream in (side, side.cuda_stream):
+        del seen[:]
+        torch.cuda.synchronize()
+        torch.cuda._sleep(20_000_000)
+        out = t.run(out=None, stream=stream)
+        qo = pkv.qk_norm_rope_append(x, x[:, :2], x[:, 2:], None, nowhere, t.k, t.v, None,
+                                     stream=stream)
+        lens = pkv.tree_commit(t.k, t.v, t.bt, t.cl, t.tl, path, none, stream=stream)
+        torch.cuda.synchronize()
+        assert seen == [side.cuda_stream] * 4  # zeros of out, workspace, q_out, new lengths
+        assert torch.equal(out[0], want[0]) and torch.equal(out[1, :3], want[1, :3])
+        assert (out[1, 3:] == 0).all() and torch.equal(qo, x) and lens.tolist() == [94, 27]
+    assert pkv.device_error() == 0
+
+
 def test_tree_attention_refuses_what_it_cannot_take():
     t = Tree([40], [4], 4, 4, 2, 128, "bf16", "bf16", seed=22)
     for change in (dict(tree_mask=t.mask.int()), dict(tree_mask=t.mask[:, :3].contiguous()),
