@@ -16,11 +16,11 @@
 // of squares is the only reduction. What does not change from token to token (a row's kind, its
 // addresses, its head's scale, the weights) is worked out once per block.
 //
-// Measured (graph replay, about 5 us of it the graph's own, L2 flushed): 12345 tokens of 48 heads of
-// 128 bf16 dims: 69 us, 4.9 TB/s (46 us at the copy's rate); 1536 tokens of 80 heads into an FP8 cache:
-// 25 us (9 at the copy's rate). Besides the bytes it is bound by instructions, about 450 a warp and
-// token, half of the issue slots. A block of three resident ones keeps two tokens in flight; one
-// token per loop cost 73 and 28 us.
+// Measured in graphs of calls over several states: 12345 tokens of 48 heads of 128 bf16 dims: 55 us,
+// 5.6 TB/s, 83 % of the copy (rows loaded into registers a token ahead instead of copied through
+// shared memory: 65; copied two tokens ahead 57, three 58, five 70: more reads under way get in the
+// way of the writes); 1536 tokens of 80 heads into an FP8 cache: 20 us (9 at the copy's rate), bound
+// by instructions, the exact quotients' above all.
 #include <algorithm>
 #include <math.h>
 
@@ -113,9 +113,19 @@ __device__ __forceinline__ void store_chunk(void* pool, int64_t at, const KnownD
 }
 
 // Row groups of a token a block takes at most; a token of more is shared by `parts` blocks (block
-// b always takes part b % parts). The next token's rows, position and slot are on their way while
-// this one's are worked on, its cos and sin right after.
+// b always takes part b % parts). The next token's rows, cos and sin are on their way while this one's
+// are worked on, the position and slot of the one after it too.
 constexpr int kGroups = 3;
+constexpr int kDepth = 2;  // tokens of the ring of rows
+
+__device__ __forceinline__ void copy8(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ uint2 lds64(uint32_t at) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(at) : "memory");
+  return v;
+}
 
 template <typename TIN, int CACHE, int D, bool INTER>
 __global__ void __launch_bounds__(kThreads, 3) qk_norm_rope_append_kernel(const NormRopeArgs a,
@@ -169,27 +179,41 @@ __global__ void __launch_bounds__(kThreads, 3) qk_norm_rope_append_kernel(const 
   }
   const int64_t out_step = step * a.q_out_stride;
 
-  struct Token {
+  struct Where {
     int pos;
     int64_t slot;
-    uint2 xa[kGroups], xb[kGroups];
+  };
+  struct Token {
+    Where at;
     float cs[CH], sn[CH];
   };
-  auto load_rows = [&](int64_t n, Token& t) {  // (called for n0, n0 + step, ... in turn)
+  // Rows come into a ring in shared memory, kDepth - 1 tokens ahead; a thread reads what it copied
+  // itself, so it waits for its own copies only and no barrier is needed.
+  __shared__ uint2 ring[kDepth * kGroups * 2 * kThreads];
+  const uint32_t ring0 = smem_u32(ring) + 8 * threadIdx.x;
+  constexpr uint32_t PART = 8 * kThreads, STAGE = 2 * kGroups * PART;
+  uint32_t put = 0, get = 0;  // byte offsets of the stages
+  auto copy_rows = [&](bool there) {  // (called for n0, n0 + step, ... in turn)
+    if (there) {
 #pragma unroll
-    for (int g = 0; g < kGroups; ++g) {
-      if (kind[g] != 3) {
-        t.xa[g] = __ldcs(reinterpret_cast<const uint2*>(src[g]));
-        t.xb[g] = __ldcs(reinterpret_cast<const uint2*>(src[g] + over));
+      for (int g = 0; g < kGroups; ++g) {
+        if (kind[g] != 3) {
+          copy8(ring0 + put + 2 * g * PART, src[g]);
+          copy8(ring0 + put + (2 * g + 1) * PART, src[g] + over);
+        }
+        src[g] += src_step[g];
       }
-      src[g] += src_step[g];
+      put = put == (kDepth - 1) * STAGE ? 0 : put + STAGE;
     }
-    t.pos = a.rot_dim > 0 ? a.positions[n] : 0;
-    t.slot = a.slots[n];
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  auto look_up = [&](int64_t n) {
+    if (n >= a.num_tokens) return Where{0, -1};
+    return Where{a.rot_dim > 0 ? a.positions[n] : 0, a.slots[n]};
   };
   auto load_turn = [&](Token& t) {
-    if (!turns || (unsigned)t.pos >= (unsigned)a.max_positions) return;
-    const float* row = a.cos_sin + (int64_t)t.pos * a.rot_dim;
+    if (!turns || (unsigned)t.at.pos >= (unsigned)a.max_positions) return;
+    const float* row = a.cos_sin + (int64_t)t.at.pos * a.rot_dim;
     if constexpr (INTER) {  // the pairs of chunk a, then of chunk b
 #pragma unroll
       for (int e = 0; e < CH / 2; ++e) {
@@ -204,23 +228,23 @@ __global__ void __launch_bounds__(kThreads, 3) qk_norm_rope_append_kernel(const 
     }
   };
   auto work = [&](Token& t) {  // (likewise)
-    const bool left_out = a.rot_dim > 0 && (unsigned)t.pos >= (unsigned)a.max_positions;
-    bool stored = t.slot >= 0;
+    const bool left_out = a.rot_dim > 0 && (unsigned)t.at.pos >= (unsigned)a.max_positions;
+    bool stored = t.at.slot >= 0;
     if (left_out) {  // the whole token
       if (threadIdx.x == 0 && part == 0) atomicOr(a.err, PKV_DEVERR_BAD_POSITION);
-    } else if (t.slot >= a.num_slots) {
+    } else if (t.at.slot >= a.num_slots) {
       if (threadIdx.x == 0 && part == 0) atomicOr(a.err, PKV_DEVERR_BAD_SLOT);
       stored = false;
     }
-    const uint64_t slot = (uint64_t)t.slot;
+    const uint64_t slot = (uint64_t)t.at.slot;
     const int64_t row0 = (int64_t)(((slot >> 4) * h_kv * kPageSize + (slot & 15)) * D);
     static_assert(kPageSize == 16, "slot arithmetic");
 #pragma unroll
     for (int g = 0; g < kGroups; ++g) {
       if (left_out || g >= groups) break;  // (uniform over the block)
       float xa[CH], xb[CH];
-      widen(t.xa[g], xa);
-      widen(t.xb[g], xb);
+      widen(lds64(ring0 + get + 2 * g * PART), xa);
+      widen(lds64(ring0 + get + (2 * g + 1) * PART), xb);
       const int64_t at = row0 + in_slot[g];
       if (kind[g] == 2 && stored) {
         store_chunk<TIN, CACHE, CH>(a.v_cache, at, scale[g], xa);
@@ -273,20 +297,33 @@ __global__ void __launch_bounds__(kThreads, 3) qk_norm_rope_append_kernel(const 
     }
 #pragma unroll
     for (int g = 0; g < kGroups; ++g) q_out[g] += out_step;
+    get = get == (kDepth - 1) * STAGE ? 0 : get + STAGE;
   };
 
   Token even{}, odd{};
-  load_rows(n0, even);
+  even.at = look_up(n0);
+  odd.at = look_up(n0 + step);
+  for (int i = 0; i < kDepth - 1; ++i) copy_rows(n0 + i * step < a.num_tokens);
   load_turn(even);
-  for (int64_t n = n0; n < a.num_tokens; n += 2 * step) {
-    const bool second = n + step < a.num_tokens, third = n + 2 * step < a.num_tokens;
-    if (second) load_rows(n + step, odd);
+  for (int64_t n = n0;;) {
+    copy_rows(n + (kDepth - 1) * step < a.num_tokens);
+    const bool second = n + step < a.num_tokens;
+    if (second) load_turn(odd);
+    asm volatile("cp.async.wait_group %0;" ::"n"(kDepth - 1) : "memory");
+    const Where w2 = look_up(n + 2 * step);
     work(even);
+    even.at = w2;
     if (!second) break;
-    load_turn(odd);
-    if (third) load_rows(n + 2 * step, even);
-    work(odd);
+    n += step;
+    copy_rows(n + (kDepth - 1) * step < a.num_tokens);
+    const bool third = n + step < a.num_tokens;
     if (third) load_turn(even);
+    asm volatile("cp.async.wait_group %0;" ::"n"(kDepth - 1) : "memory");
+    const Where w3 = look_up(n + 2 * step);
+    work(odd);
+    odd.at = w3;
+    if (!third) break;
+    n += step;
   }
 }
 

@@ -41,9 +41,11 @@
 // which 0 P would still spread to rows that do not see the node, become 0 there and are added to
 // the rows that do see it at the unit's end.
 //
-// Measured with the combine, L2 flushed, against the bytes at the copy's 6.78 TB/s: 64 requests of 512
-// .. 4096 bf16 tokens, 64 rows a head: 118 us (5.84 TB/s; 102); ragged drafts of up to 256 rows: 142
-// (96); 4 requests of 8191 .. 65536 INT8 tokens, 96 rows: 60 (5.9 TB/s; 53); FP8, 64 rows: 108 (52).
+// Measured with the combine in graphs of calls over several states, against the bytes at the copy's
+// 6.78 TB/s: 64 requests of 512 .. 4096 bf16 tokens, 64 rows a head: 106 us (6.5 TB/s; 102); ragged
+// drafts of up to 256 rows: 135 (96); 4 requests of 8191 .. 65536 INT8 tokens, 96 rows: 54 (6.6 TB/s;
+// 53); 128 requests of 128 .. 8192 FP8 tokens, 192 rows: 359 (161). (The figures above are of single
+// calls after a flush of the L2, some 10 us more.)
 // Small units of an 8-bit or 64-dim cache and all large units are bound by the softmax steps, about
 // 1400 cycles of waits, tensor-memory loads and exponentials for 128 rows x 64 tokens, two at a time
 // on an SM, and by 4 to 8 thousand cycles from the last step of a unit to the first of the next.
