@@ -151,6 +151,19 @@ class PagedKVCache:
             copy_pages(self.k, self.v, src, dst)
         return slots, bt, cl
 
+    def _device_slots(self, slots, stream) -> torch.Tensor:
+        """``slots`` on the device, for a call on ``stream``. Host slots are copied here, on the
+        current stream; the copy is complete on return, and its memory is not handed out again
+        before the work then queued on ``stream`` is done."""
+        if isinstance(slots, torch.Tensor):
+            return slots
+        slots = torch.from_numpy(np.asarray(slots, dtype=np.int64)).to(self.k.device)
+        if stream is not None:
+            if not isinstance(stream, torch.cuda.Stream):  # a raw cudaStream_t handle
+                stream = torch.cuda.ExternalStream(int(stream), device=self.k.device)
+            slots.record_stream(stream)
+        return slots
+
     def write(self, slots, k_new: torch.Tensor, v_new: torch.Tensor, stream=None):
         """Append rows k_new/v_new [N, h_kv, d] at the given slots (host array or CUDA int64)."""
         if not isinstance(slots, torch.Tensor):
@@ -161,8 +174,7 @@ class PagedKVCache:
                   **norm):
         """Norm, rotate and append in one pass (qk_norm_rope_append; ``norm``: q_weight, k_weight,
         eps, interleaved); returns the rotated queries."""
-        if not isinstance(slots, torch.Tensor):
-            slots = torch.from_numpy(np.asarray(slots, dtype=np.int64)).to(self.k.device)
+        slots = self._device_slots(slots, stream)
         return qk_norm_rope_append(q, k_new, v_new, positions, slots, self.k, self.v, cos_sin,
                                    q_out=q_out, k_scales=self.k_scales, v_scales=self.v_scales,
                                    stream=stream, **norm)

@@ -1,0 +1,62 @@
+"""The speculative-decoding operators in their less usual forms, on the GPU: calls on a stream of the
+caller's, drafts of a single tile each, scales and scores of any size, and the whole step against
+a 64-bit implementation.
+
+A rounding to type t is off by at most eps(t) / 2 relative to the value; tolerances are derived where
+they are computed.
+"""
+import numpy as np
+import pytest
+import torch
+
+import paged_kv_cache_271_gb300 as pkv
+from paged_kv_cache_271_gb300.cache import PagedKVCache
+from tests.test_gpu_tree import gen, randn, raw
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(autouse=True)
+def _clean_error_word():
+    assert torch.cuda.is_available()
+    pkv.device_error()
+    yield
+    pkv.device_error()
+
+
+# ---- host slots on a stream of the caller's ------------------------------------------------------
+
+
+def slots_on_a_busy_stream(call, n=600, h_kv=2, d=128):
+    """Runs call(cache, slots, k, v, stream) on a busy stream, then fills tensors of the slots' size
+    on the current one with the slots of the pool's other half. Every row has to be where its slot
+    says, and the other half as it was."""
+    g = gen(50)
+    k, v = (randn(g, n, h_kv, d, dtype=torch.bfloat16) for _ in range(2))
+    slots = np.random.default_rng(50).permutation(1024)[:n].astype(np.int64)
+    call(PagedKVCache(128, h_kv, d, torch.bfloat16), slots, k, v, None)  # (kernels are loaded here)
+    for raw_handle in (False, True):
+        cache = PagedKVCache(128, h_kv, d, torch.bfloat16)
+        cache.k.zero_()
+        cache.v.zero_()
+        side = torch.cuda.Stream()
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(100_000_000)
+        kept = call(cache, slots, k, v, side.cuda_stream if raw_handle else side)
+        assert not side.query()  # (else nothing is tested)
+        others = [torch.empty(n, dtype=torch.int64, device="cuda") for _ in range(8)]
+        for x in others:
+            x.copy_(torch.arange(1024, 1024 + n, device="cuda"))
+        torch.cuda.synchronize()
+        at = torch.from_numpy(slots).cuda()
+        for pool, rows in ((cache.k, k), (cache.v, v)):
+            assert torch.equal(pool[at // 16, :, at % 16], rows)
+            assert not raw(pool[64:]).any()
+        del kept, others
+    assert pkv.device_error() == 0
+
+
+def test_write_qkv_with_host_slots_on_a_busy_stream():
+    slots_on_a_busy_stream(lambda c, slots, k, v, stream: c.write_qkv(
+        slots, torch.cat([k, k], 1), k, v, None, None, stream=stream))

@@ -1,0 +1,58 @@
+"""Host side of the speculative-decoding calls in their less usual forms. No GPU."""
+import numpy as np
+import pytest
+import torch
+
+import paged_kv_cache_271_gb300 as pkv
+from paged_kv_cache_271_gb300 import cache as cache_module
+from paged_kv_cache_271_gb300.cache import PagedKVCache
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    from paged_kv_cache_271_gb300 import build
+    build.build()
+
+
+# ---- host slots on a stream of the caller's ------------------------------------------------------
+
+
+class FakeStream:
+    """Stands for torch.cuda.Stream where there is no GPU."""
+
+    def __init__(self, handle=77, device=None):
+        self.cuda_stream = handle
+
+
+@pytest.fixture
+def recorded(monkeypatch):
+    """[(address, stream handle)] of the tensors whose use on a stream was recorded, and the slots
+    that reached the operator, kept alive: (records, slots)."""
+    records, slots = [], []
+    monkeypatch.setattr(torch.cuda, "Stream", FakeStream)
+    monkeypatch.setattr(torch.cuda, "ExternalStream", FakeStream)
+    monkeypatch.setattr(torch.Tensor, "record_stream",
+                        lambda t, s: records.append((t.data_ptr(), s.cuda_stream)))
+    monkeypatch.setattr(cache_module, "qk_norm_rope_append",
+                        lambda q, k, v, positions, slot_mapping, *a, **kw: slots.append(slot_mapping))
+    return records, slots
+
+
+@pytest.mark.parametrize("stream", [FakeStream(), 77])
+def test_write_qkv_keeps_host_slots_until_the_stream_is_done(recorded, stream):
+    """The device copy of host slots is the call's own: it must outlive the work on the stream it
+    was given."""
+    records, slots = recorded
+    c = PagedKVCache(2, 1, 64, torch.float32, device="cpu")
+    c.write_qkv(np.array([3, 4]), None, None, None, None, None, stream=stream)
+    assert slots[0].tolist() == [3, 4] and slots[0].dtype == torch.int64
+    assert records == [(slots[0].data_ptr(), 77)]
+
+
+def test_write_qkv_leaves_the_callers_slots_alone(recorded):
+    records, slots = recorded
+    c = PagedKVCache(2, 1, 64, torch.float32, device="cpu")
+    mine = torch.tensor([3, 4])
+    c.write_qkv(mine, None, None, None, None, None, stream=77)
+    c.write_qkv([3, 4], None, None, None, None, None)  # the current stream: freed in its order
+    assert slots[0] is mine and slots[1].tolist() == [3, 4] and not records
