@@ -166,9 +166,8 @@ class PagedKVCache:
 
     def write(self, slots, k_new: torch.Tensor, v_new: torch.Tensor, stream=None):
         """Append rows k_new/v_new [N, h_kv, d] at the given slots (host array or CUDA int64)."""
-        if not isinstance(slots, torch.Tensor):
-            slots = torch.from_numpy(np.asarray(slots, dtype=np.int64)).to(self.k.device)
-        kv_append(k_new, v_new, slots, self.k, self.v, self.k_scales, self.v_scales, stream)
+        kv_append(k_new, v_new, self._device_slots(slots, stream), self.k, self.v, self.k_scales,
+                  self.v_scales, stream)
 
     def write_qkv(self, slots, q, k_new, v_new, positions, cos_sin, q_out=None, stream=None,
                   **norm):

@@ -60,3 +60,7 @@ def slots_on_a_busy_stream(call, n=600, h_kv=2, d=128):
 def test_write_qkv_with_host_slots_on_a_busy_stream():
     slots_on_a_busy_stream(lambda c, slots, k, v, stream: c.write_qkv(
         slots, torch.cat([k, k], 1), k, v, None, None, stream=stream))
+
+
+def test_write_with_host_slots_on_a_busy_stream():
+    slots_on_a_busy_stream(lambda c, slots, k, v, stream: c.write(slots, k, v, stream=stream))

@@ -35,6 +35,8 @@ def recorded(monkeypatch):
                         lambda t, s: records.append((t.data_ptr(), s.cuda_stream)))
     monkeypatch.setattr(cache_module, "qk_norm_rope_append",
                         lambda q, k, v, positions, slot_mapping, *a, **kw: slots.append(slot_mapping))
+    monkeypatch.setattr(cache_module, "kv_append",
+                        lambda k, v, slot_mapping, *a, **kw: slots.append(slot_mapping))
     return records, slots
 
 
@@ -56,3 +58,13 @@ def test_write_qkv_leaves_the_callers_slots_alone(recorded):
     c.write_qkv(mine, None, None, None, None, None, stream=77)
     c.write_qkv([3, 4], None, None, None, None, None)  # the current stream: freed in its order
     assert slots[0] is mine and slots[1].tolist() == [3, 4] and not records
+
+
+@pytest.mark.parametrize("stream", [FakeStream(), 77])
+def test_write_keeps_host_slots_until_the_stream_is_done(recorded, stream):
+    records, slots = recorded
+    c = PagedKVCache(2, 1, 64, torch.float32, device="cpu")
+    c.write([5], None, None, stream=stream)
+    assert slots[0].tolist() == [5] and records == [(slots[0].data_ptr(), 77)]
+    c.write([5], None, None)
+    assert len(records) == 1
