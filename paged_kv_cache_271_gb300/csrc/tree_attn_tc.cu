@@ -59,6 +59,7 @@
 #include "pkv_device.cuh"
 #include "pkv_internal.h"
 #include "tcgen05.cuh"
+#include "tree_exchange.h"
 #include "tree_plan.cuh"
 
 namespace pkv {
@@ -83,6 +84,7 @@ constexpr uint32_t kColO = 0, kColQ = 256;
 constexpr uint32_t kTmemCols = 512;
 constexpr float kLazyLog2 = 8.f;
 static_assert(2 * kGroupThreads == kTreeTcRows, "a unit is two groups' rows");
+static_assert(kExchangeRows == kGroupThreads, "a place for each row of a group");
 
 template <typename KV, int D, bool WIDE>
 struct TcShape {
@@ -104,8 +106,8 @@ struct TcShape {
   static constexpr int Q_GROUP = WIDE ? kGroupThreads * D * 2 : 0;
   static constexpr int PIECE = WIDE ? 32 : 64;              // bytes of a row that change hands at once
   static constexpr int OFF_STAGE = OFF_Q + 2 * Q_GROUP;     // 32 rows' pieces for each softmax warp
-  static constexpr int OFF_ML = OFF_STAGE + kSoftThreads * PIECE;  // [2][128] (max, sum)
-  static constexpr int OFF_REF = OFF_ML + 2 * kGroupThreads * 8;   // [128] reference maxima
+  static constexpr int OFF_ML = OFF_STAGE + kSoftThreads * PIECE;  // (max, sum) exchanged
+  static constexpr int OFF_REF = OFF_ML + kExchangeSlots * 8;      // [128] reference maxima
   static constexpr int OFF_BAR = OFF_REF + kGroupThreads * 4;
   static constexpr int BARS = 2 * NK + 2 * NV + 2 * NR + 3 * kSBufs + 6 + kRuns;
   static_assert(NK + NR + 3 <= kRuns, "runs in flight");
@@ -216,7 +218,7 @@ __global__ void __launch_bounds__(TcShape<KV, D, WIDE>::THREADS, 1) tree_tc_kern
   int* raw_mask = page_mask + NV;                                    // [NR]
   uint32_t* bad_nodes = reinterpret_cast<uint32_t*>(raw_mask + NR);  // [2][8] V row not finite
   uint32_t* s_taddr = bad_nodes + 16;
-  float2* ml = reinterpret_cast<float2*>(smem + S::OFF_ML);          // [2][128]
+  float2* ml = reinterpret_cast<float2*>(smem + S::OFF_ML);          // (tree_exchange.h)
   float* ref = reinterpret_cast<float*>(smem + S::OFF_REF);          // [128]
 
   __shared__ int scratch[64];
@@ -873,7 +875,7 @@ __global__ void __launch_bounds__(TcShape<KV, D, WIDE>::THREADS, 1) tree_tc_kern
         ok = mbar_wait(&pv_done[last & 3], parity_of(ph, last), a.err);
       ok = __all_sync(0xffffffffu, ok);
       tc_fence_after();
-      if (!wide) ml[wg * kGroupThreads + r] = make_float2(m_used, l);
+      if (!wide) ml[exchange_slot(unit, wg, r)] = make_float2(m_used, l);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(met);
@@ -885,7 +887,7 @@ __global__ void __launch_bounds__(TcShape<KV, D, WIDE>::THREADS, 1) tree_tc_kern
       // sum is the two groups', each at the maximum of its last step (O is at the larger, the last)
       float M = m_used, L = l;
       if (!wide) {
-        const float2 x = ml[r], y = ml[kGroupThreads + r];
+        const float2 x = ml[exchange_slot(unit, 0, r)], y = ml[exchange_slot(unit, 1, r)];
         M = fmaxf(x.x, y.x);
         const float Mu = M == -INFINITY ? 0.f : M;
         L = exp2f(x.x - Mu) * x.y + exp2f(y.x - Mu) * y.y;

@@ -11,7 +11,7 @@ import torch
 
 import paged_kv_cache_271_gb300 as pkv
 from paged_kv_cache_271_gb300.cache import PagedKVCache
-from tests.test_gpu_tree import gen, randn, raw
+from tests.test_gpu_tree import Tree, gen, randn, raw
 
 pytestmark = pytest.mark.gpu
 
@@ -64,3 +64,23 @@ def test_write_qkv_with_host_slots_on_a_busy_stream():
 
 def test_write_with_host_slots_on_a_busy_stream():
     slots_on_a_busy_stream(lambda c, slots, k, v, stream: c.write(slots, k, v, stream=stream))
+
+
+# ---- units of one tile -----------------------------------------------------------------------------
+
+
+@pytest.mark.parametrize("nodes", [3, 70])  # up to 6 rows a KV head; 140, mostly few
+@pytest.mark.parametrize("cache,d", [("bf16", 128), ("bf16", 64), ("fp8", 128), ("int8", 64)])
+def test_long_runs_of_single_tile_units(cache, d, nodes):
+    """Contexts of up to 64 tokens, sixteen units a block one behind the other: the second of a
+    unit's two groups of threads has no step of its own and runs ahead to the unit's end."""
+    r = np.random.default_rng(51)
+    ctx = r.integers(1, 65, 600)
+    tree = np.minimum(r.integers(1, 4, 600), ctx)
+    if nodes > 3:
+        tree[::97] = 63
+        ctx[::97] = 64
+    t = Tree(ctx.tolist(), tree.tolist(), nodes, 8, 4, d, "bf16", cache, seed=51)
+    first = t.check().clone()
+    for _ in range(20):
+        assert torch.equal(t.run(), first)
