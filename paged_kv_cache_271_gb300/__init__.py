@@ -874,8 +874,8 @@ def tree_decode_attention(q, k_cache, v_cache, block_tables, context_lens, scale
         stride = 0 if tree_mask.shape[0] == 1 else T * words
     _check_scales(desc, k_scales, v_scales)
     if out is None:
-        out = _new(torch.empty if tree_lens is None else torch.zeros, q.shape, q.dtype, q.device,
-                   stream)
+        # (without tree_lens too: requests without a context or left out have no rows to write)
+        out = _new(torch.zeros, q.shape, q.dtype, q.device, stream)
     elif out.shape != q.shape or out.dtype != q.dtype:
         raise PkvError(-2, "out must match q in shape and dtype")
     dev = torch.cuda.current_device()

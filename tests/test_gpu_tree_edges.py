@@ -84,3 +84,27 @@ def test_long_runs_of_single_tile_units(cache, d, nodes):
     first = t.check().clone()
     for _ in range(20):
         assert torch.equal(t.run(), first)
+
+
+# ---- outputs that the call makes --------------------------------------------------------------------
+
+
+@pytest.mark.parametrize("io,cache", [("bf16", "bf16"), ("bf16", "fp8"), ("f32", "f32")])
+@pytest.mark.parametrize("lens", [True, False])
+def test_a_new_output_is_zero_where_there_is_no_draft(io, cache, lens):
+    """With tree_lens and without: requests without a context, and ones that are left out because
+    their context is shorter than the draft."""
+    t = Tree([40, 0, 70, 4], [6, 0, 6, 4], 6, 4, 2, 128, io, cache, seed=52)
+    t.tl = torch.tensor([6, 0, 6, 5], dtype=torch.int32, device="cuda")  # (5 of 4: left out)
+    want = t.run().clone()
+    assert (want[1] == 3.25).all() and (want[3] == 3.25).all()
+    assert pkv.device_error() == pkv.DEVERR_BAD_TREE
+    want[1] = want[3] = 0
+    for _ in range(3):
+        poison = torch.full_like(want, float("nan"))
+        at = poison.data_ptr()
+        del poison  # (the next output of this size)
+        got = t.run(out=None, tree_lens=t.tl if lens else None)
+        assert got.data_ptr() == at and torch.equal(got, want)
+        assert pkv.device_error() == pkv.DEVERR_BAD_TREE
+        del got
