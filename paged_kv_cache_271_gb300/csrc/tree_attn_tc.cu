@@ -613,9 +613,11 @@ __global__ void __launch_bounds__(TcShape<KV, D, WIDE>::THREADS, 1) tree_tc_kern
             mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
             const int ex = mx >> 7;  // biased exponent: mx 2^e in [2^14, 2^15), none for 0, inf, NaN
             const int e = mx != 0 && ex < 255 ? min(126, max(-126, 141 - ex)) : 0;
-            const float up = __int_as_float((127 + e) << 23);
-            // (at least the smallest normal number: an unseen score of -inf must stay one)
-            const float of = fmaxf(sc * __int_as_float((127 - e) << 23), 0x1p-126f);
+            // the factor of the scores stays positive, and at least the smallest normal number (an
+            // unseen score of -inf must stay one): a K scale's sign, or a NaN one, is in the query
+            const float two_e = __int_as_float((127 + e) << 23);
+            const float up = sc < 0.f ? -two_e : sc == sc ? two_e : sc;
+            const float of = fmaxf(fabsf(sc) * __int_as_float((127 - e) << 23), 0x1p-126f);
             const float mine = __shfl_sync(0xffffffffu, of, 4 * (lane & 7));
             if ((lane >> 3) == g) x.sc = mine;
             if (wide || wg == 0) {

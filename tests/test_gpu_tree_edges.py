@@ -108,3 +108,23 @@ def test_a_new_output_is_zero_where_there_is_no_draft(io, cache, lens):
         assert got.data_ptr() == at and torch.equal(got, want)
         assert pkv.device_error() == pkv.DEVERR_BAD_TREE
         del got
+
+
+# ---- scales and scores of any size -------------------------------------------------------------------
+
+
+@pytest.mark.parametrize("io,cache,d", [("bf16", "fp8", 128), ("bf16", "int8", 64), ("f32", "fp8", 64),
+                                        ("f32", "int8", 128)])
+@pytest.mark.parametrize("nodes", [7, 70])  # up to 28 rows a KV head; 280
+def test_negative_zero_and_nan_scales_are_kept(io, cache, d, nodes):
+    t = Tree([nodes + 9, nodes + 300], [nodes, 5], nodes, 12, 3, d, io, cache, seed=53)
+    t.ks[0] *= -1
+    t.ks[1] = 0  # every seen position weighs the same
+    t.vs[2] *= -1
+    t.check()
+    want = t.out.clone()
+    t.ks[1] = float("nan")
+    got = t.run()
+    assert torch.equal(got[:, :, :4], want[:, :, :4]) and torch.equal(got[:, :, 8:], want[:, :, 8:])
+    for b, n in enumerate(t.tree):
+        assert torch.isnan(got[b, :n, 4:8]).all() and (got[b, n:] == 3.25).all()
