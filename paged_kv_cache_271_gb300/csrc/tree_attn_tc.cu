@@ -785,6 +785,11 @@ __global__ void __launch_bounds__(TcShape<KV, D, WIDE>::THREADS, 1) tree_tc_kern
         const float mx = sc * max3(max3(mx4[0], mx4[1], mx4[2]),
                                    max3(mx4[3], __uint_as_float(sr[60]), __uint_as_float(sr[61])),
                                    fmaxf(__uint_as_float(sr[62]), __uint_as_float(sr[63])));
+        // s sc - m is one FMA below: m is a rounded product, the product in the FMA is not, so that a row's
+        // weights are all off by one factor, which their sum shares: up to 2^0.5 for |m| <= 2^24. For
+        // larger m it would soon leave f16's range and then every range: there s sc is rounded as m is.
+        // (A tile that counts has its maximum near m.)
+        const bool huge = fabsf(mx) > 0x1p24f && mx != -INFINITY;
         // The reference maximum m that P and O are scaled by: the first tile's maximum, then moved
         // only past 2^8. In a wide unit it is the thread's own. Otherwise the two groups' tiles add
         // into one O, so m goes from step to step: this group's step takes it from the other's
@@ -798,31 +803,47 @@ __global__ void __launch_bounds__(TcShape<KV, D, WIDE>::THREADS, 1) tree_tc_kern
           if (!ok) break;
           m_before = ref[r];
         }
-        const float m_new = first || mx > m_before + kLazyLog2 ? mx : m_before;
+        // (the difference, not m_before + 2^3: past 2^26 that sum would round to several times as far)
+        const float m_new = first || mx - m_before > kLazyLog2 ? mx : m_before;
         const bool moved = !first && m_new != m_before;
         if (!wide) {
           if (first || moved) ref[r] = m_new;
           __syncwarp();
           if (lane == 0) mbar_arrive(&ref_set[wg]);
         }
-        if (__any_sync(0xffffffffu, moved)) {  // rescale this warp's rows of O (in TMEM)
-          constexpr int back = wide ? 2 : 1;  // to the last step that adds into this O
-          ok = mbar_wait(&pv_done[(u - back) & 3], parity_of(ph, u - back), a.err);
-          ok = __all_sync(0xffffffffu, ok);
-          if (!ok) break;
-          tc_fence_after();
-          const float alpha = moved ? exp2f(m_before - m_new) : 1.f;
-          const uint32_t ocol = kColO + (wide ? 128 * wg : 0);
+        float factor = sc;
+        if (__any_sync(0xffffffffu, moved || huge)) {  // (one vote for the two: most steps have neither)
+          if (__any_sync(0xffffffffu, moved)) {  // rescale this warp's rows of O (in TMEM)
+            constexpr int back = wide ? 2 : 1;  // to the last step that adds into this O
+            ok = mbar_wait(&pv_done[(u - back) & 3], parity_of(ph, u - back), a.err);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            tc_fence_after();
+            const float alpha = moved ? exp2f(m_before - m_new) : 1.f;
+            const uint32_t ocol = kColO + (wide ? 128 * wg : 0);
 #pragma unroll
-          for (int cb = 0; cb < D / 32; ++cb) {
-            uint32_t o[32];
-            tmem_ld32(lane_t + ocol + 32 * cb, o);
-            tmem_wait_ld();
+            for (int cb = 0; cb < D / 32; ++cb) {
+              uint32_t o[32];
+              tmem_ld32(lane_t + ocol + 32 * cb, o);
+              tmem_wait_ld();
 #pragma unroll
-            for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
-            tmem_st32(lane_t + ocol + 32 * cb, o);
+              for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
+              tmem_st32(lane_t + ocol + 32 * cb, o);
+            }
+            tmem_wait_st();
           }
-          tmem_wait_st();
+          if (__any_sync(0xffffffffu, huge)) {
+#pragma unroll
+            for (int k = 0; k < 32; ++k) {
+              float s0, s1;
+              unpack2(mul2(pack2(__uint_as_float(sr[2 * k]), __uint_as_float(sr[2 * k + 1])),
+                           pack2(sc, sc)),
+                      s0, s1);
+              sr[2 * k] = __float_as_uint(s0);
+              sr[2 * k + 1] = __float_as_uint(s1);
+            }
+            factor = 1.f;
+          }
         }
         if (m_new != m_used) {  // the group's own sum, at the maximum of its last step
           l *= exp2f(m_used - m_new);
@@ -832,7 +853,7 @@ __global__ void __launch_bounds__(TcShape<KV, D, WIDE>::THREADS, 1) tree_tc_kern
         const float m_use = m_used == -INFINITY ? 0.f : m_used;
         uint32_t pw[32];
         uint64_t sum[4] = {0, 0, 0, 0};  // (pairs of zeros)
-        const uint64_t sc2 = pack2(sc, sc), m2 = pack2(-m_use, -m_use);
+        const uint64_t sc2 = pack2(factor, factor), m2 = pack2(-m_use, -m_use);
 #pragma unroll
         for (int k = 0; k < 32; ++k) {
           float e0, e1;

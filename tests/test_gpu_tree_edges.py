@@ -11,7 +11,7 @@ import torch
 
 import paged_kv_cache_271_gb300 as pkv
 from paged_kv_cache_271_gb300.cache import PagedKVCache
-from tests.test_gpu_tree import Tree, gen, randn, raw
+from tests.test_gpu_tree import DT, H, KINDS, U32, Tree, gen, randn, raw
 
 pytestmark = pytest.mark.gpu
 
@@ -128,3 +128,41 @@ def test_negative_zero_and_nan_scales_are_kept(io, cache, d, nodes):
     assert torch.equal(got[:, :, :4], want[:, :, :4]) and torch.equal(got[:, :, 8:], want[:, :, 8:])
     for b, n in enumerate(t.tree):
         assert torch.isnan(got[b, :n, 4:8]).all() and (got[b, n:] == 3.25).all()
+
+
+@pytest.mark.parametrize("io,cache,d", KINDS)
+@pytest.mark.parametrize("power", [12, 22, 26, 28, 30, 32, 33, 60, 110])
+def test_scores_of_huge_size_pick_the_largest(io, cache, d, power):
+    """Queries 2^power times their usual size: where the largest score of a row leads the others by
+    30 more than fp32 can tell apart, the row's output is that position's value."""
+    checked = rows = 0
+    for nodes, ctx in ((7, 330), (60, 130)):  # up to 21 rows a KV head; 180
+        t = Tree([ctx], [nodes], nodes, 6, 2, d, io, cache, seed=54)
+        t.q *= 2.0 ** power
+        got = t.run()[0].double()
+        assert pkv.device_error() == 0
+        k, v = (x.double() for x in t.rows[0])
+        if t.ks is not None:
+            k, v = k * t.ks.double()[:, None], v * t.vs.double()[:, None]
+        k, v = (x.repeat_interleave(3, 1) for x in (k, v))
+        q = t.q[0].double()
+        see = torch.ones(nodes, ctx, dtype=torch.bool, device="cuda")
+        see[:, ctx - nodes:] = t.seen(0)
+        s = torch.einsum("thd,chd->thc", q, k) * t.scale
+        s = torch.where(see[:, None], s, torch.tensor(float("-inf"), dtype=s.dtype, device="cuda"))
+        sabs = torch.einsum("thd,chd->thc", q.abs(), k.abs()) * t.scale
+        # d products and sums, the scales and log2(e), and the score's own rounding, of both scores
+        fuzz = 2 * (d + 8) * U32 * torch.where(see[:, None], sabs, 0).amax(-1)
+        top = s.topk(2, -1)
+        clear = top.values[..., 0] - top.values[..., 1] > 30 + fuzz
+        want = torch.stack([v[top.indices[:, h, 0], h] for h in range(6)], 1)
+        # the others weigh less than ctx e^-30 < 2^-34 of the largest value; the weight's own
+        # rounding to the matrix type, the division, the scales and the output's
+        h = {"f32": 0, "bf16": 2.0 ** -8, "fp8": 2.0 ** -11, "int8": 2.0 ** -11}[cache]
+        tol = (h + 8 * U32) * want.abs() + 2.0 ** -33 * v.abs().max()
+        tol = tol + H[io] * (want.abs() + tol)
+        bad = ~((got - want).abs() <= tol) & clear[..., None]
+        assert not bad.any(), (nodes, bad.any(-1).sum().item(), clear.sum().item())
+        checked += int(clear.sum())
+        rows += clear.numel()
+    assert 2 * checked > rows
