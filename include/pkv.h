@@ -704,7 +704,8 @@ int pkv_cascade_set_prefix_kernel(int32_t which);
  *  slot_mapping   device int64 [num_tokens], distinct; a negative one skips the cache rows (q_out
  *                 is still written), one past the pool sets PKV_DEVERR_BAD_SLOT.
  *  q_out          device, laid out like q with q_out_stride; may be q itself (same stride).
- * dtype must equal cache_dtype for F32/BF16 caches, as for pkv_kv_append.
+ * dtype must equal cache_dtype for F32/BF16 caches, as for pkv_kv_append. PKV_ESHAPE also for a token's
+ * queries or a page of one pool of 2^31 elements or more.
  */
 int pkv_qk_norm_rope_append(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
                             const void* v, int64_t v_stride, int32_t dtype, int32_t num_tokens,

@@ -116,6 +116,8 @@ int pkv_qk_norm_rope_append(const void* q, int64_t q_stride, const void* k, int6
     return set_error(PKV_EINVAL, "%s: eps must be finite and >= 0", who);
   const int eb = dtype_bytes(dtype);
   const int64_t need_q = (int64_t)num_q_heads * D, need_kv = (int64_t)h_kv * D;
+  if (need_q >= (1ll << 31) || need_kv * desc->page_size >= (1ll << 31))
+    return set_error(PKV_ESHAPE, "%s: a token's queries or a page hold 2^31 elements or more", who);
   if (num_tokens > 1 && (q_stride < need_q || k_stride < need_kv || v_stride < need_kv ||
                          q_out_stride < need_q))
     return set_error(PKV_ESHAPE, "%s: a token stride is smaller than the token's row", who);

@@ -1,4 +1,6 @@
 """Host side of the speculative-decoding calls in their less usual forms. No GPU."""
+import ctypes
+
 import numpy as np
 import pytest
 import torch
@@ -6,6 +8,7 @@ import torch
 import paged_kv_cache_271_gb300 as pkv
 from paged_kv_cache_271_gb300 import cache as cache_module
 from paged_kv_cache_271_gb300.cache import PagedKVCache
+from tests.test_tree_ops_host import APPEND, BF16, ESHAPE, F32, INT8, TREE, call, desc
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -68,3 +71,25 @@ def test_write_keeps_host_slots_until_the_stream_is_done(recorded, stream):
     assert slots[0].tolist() == [5] and records == [(slots[0].data_ptr(), 77)]
     c.write([5], None, None)
     assert len(records) == 1
+
+
+# ---- sizes past what the kernels count with ----------------------------------------------------------
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_append_refuses_rows_and_pages_of_2_31_elements(d):
+    """Offsets within a token's row, and within a page, are 32 bits in the kernel."""
+    most_q, most_kv = (2 ** 31 - 1) // d, (2 ** 31 - 1) // (16 * d)
+    wide = dict(q_stride=1 << 40, k_stride=1 << 40, v_stride=1 << 40, q_out_stride=1 << 40)
+    big = dict(desc=desc(h_kv=2, d=d, pages=1), rot_dim=d, n=2, h_q=most_q, **wide)
+    st, msg = call("pkv_qk_norm_rope_append", APPEND, **dict(big, h_q=most_q + 1))
+    assert st == ESHAPE and "2^31" in msg
+    st, msg = call("pkv_qk_norm_rope_append", APPEND,
+                   **dict(big, h_q=8, desc=desc(h_kv=most_kv + 1, d=d, pages=1)))
+    assert st == ESHAPE and "2^31" in msg
+    # (one less is not refused for its size: the call gets to its next check)
+    st, msg = call("pkv_qk_norm_rope_append", APPEND, **dict(big, q=ctypes.c_void_p(4100)))
+    assert st == -4
+    st, msg = call("pkv_qk_norm_rope_append", APPEND, **dict(
+        big, h_q=8, desc=desc(h_kv=most_kv, d=d, pages=1), q=ctypes.c_void_p(4100)))
+    assert st == -4
