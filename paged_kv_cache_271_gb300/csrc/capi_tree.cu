@@ -49,12 +49,19 @@ int check_tree_types(const char* who, int dtype_q, int kv) {
   return PKV_OK;
 }
 
-// Half tiles of work (tree_plan.cuh) that the call's table could hold at most.
+// a b, or 2^60 where that is less (a, b in [0, 2^62]).
+long long capped_product(long long a, long long b) {
+  constexpr long long most = 1ll << 60;
+  return b != 0 && a > most / b ? most : a * b;
+}
+
+// Half tiles of work (tree_plan.cuh) that the call's table could hold at most (up to 2^60).
 long long tree_most_work(const TreeSplit& t, int batch, int nodes, int h_q, int h_kv,
                          int max_pages) {
   const long long units = ((long long)nodes * (h_q / h_kv) + t.rows - 1) / t.rows;
   const long long tiles = ((long long)max_pages * 16 + t.tokens - 1) / t.tokens;
-  return (long long)batch * h_kv * units * (tiles * t.wide_tile + 2 * t.pass_cost);
+  const long long passes = capped_product((long long)batch * h_kv, units);
+  return capped_product(passes, tiles * t.wide_tile + 2 * t.pass_cost);
 }
 
 // CTAs of a call: one wave, or fewer when the table cannot hold that many shares.

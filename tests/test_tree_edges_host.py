@@ -93,3 +93,21 @@ def test_append_refuses_rows_and_pages_of_2_31_elements(d):
     st, msg = call("pkv_qk_norm_rope_append", APPEND, **dict(
         big, h_q=8, desc=desc(h_kv=most_kv, d=d, pages=1), q=ctypes.c_void_p(4100)))
     assert st == -4
+
+
+@pytest.mark.parametrize("batch,h_kv,group,pages", [(65535, 65535, 128, (1 << 27) - 16),
+                                                    (32768, 32768, 128, (1 << 27) - 16),
+                                                    (65535, 32768, 64, 1 << 25)])
+def test_tree_attention_refuses_tables_whose_work_passes_64_bits(batch, h_kv, group, pages):
+    """The work that these tables could hold, counted in half tiles, is negative modulo 2^64."""
+    st, msg = call("pkv_tree_decode_attention", TREE, dtype=F32, batch=batch, nodes=256,
+                   h_q=h_kv * group, max_pages=pages, desc=desc(F32, h_kv=h_kv, d=64, pages=1),
+                   mask=None)
+    assert st == ESHAPE and "2^30" in msg
+
+
+def test_workspace_size_of_absurd_sizes_is_a_whole_wave():
+    whole = pkv.tree_decode_workspace_size(F32, F32, 64, 256, 8, 8, 64, 4096)
+    for sizes in ((65535, 256, 65535 * 128, 65535, 64, (1 << 27) - 16),
+                  (2 ** 31 - 1, 2 ** 31 - 1, 2 ** 31 - 1, 1, 64, 2 ** 31 - 1)):
+        assert pkv.tree_decode_workspace_size(F32, F32, *sizes) == whole
