@@ -16,8 +16,8 @@ from collections.abc import Mapping
 import numpy as np
 import torch
 
-from . import (PageAllocator, SeqTable, copy_pages, kv_append, qk_norm_rope_append, tree_commit,
-               tree_decode_attention)
+from . import (PageAllocator, PkvError, SeqTable, _ids, copy_pages, kv_append, qk_norm_rope_append,
+               tree_commit, tree_decode_attention)
 
 
 class _RowView(Mapping):
@@ -193,6 +193,10 @@ class PagedKVCache:
         read the new lengths back (this waits for the stream) and truncate the requests to them.
         Returns the new lengths. The drafted rows' pages must be the request's own, as ``reserve``
         leaves them: fork a request before its draft or after this, not in between."""
+        rids = _ids(rids)
+        self.table.lengths(rids)  # (refuses an unknown request)
+        if rids.size != context_lens.numel() or np.unique(rids).size != rids.size:
+            raise PkvError(-1, "rids must name each request of the batch once")
         if stream is None:
             stream = torch.cuda.current_stream(self.k.device)
         elif not isinstance(stream, torch.cuda.Stream):  # a raw cudaStream_t handle

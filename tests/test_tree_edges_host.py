@@ -1,4 +1,5 @@
 """Host side of the speculative-decoding calls in their less usual forms. No GPU."""
+import contextlib
 import ctypes
 
 import numpy as np
@@ -111,3 +112,28 @@ def test_workspace_size_of_absurd_sizes_is_a_whole_wave():
     for sizes in ((65535, 256, 65535 * 128, 65535, 64, (1 << 27) - 16),
                   (2 ** 31 - 1, 2 ** 31 - 1, 2 ** 31 - 1, 1, 64, 2 ** 31 - 1)):
         assert pkv.tree_decode_workspace_size(F32, F32, *sizes) == whole
+
+
+# ---- commit ------------------------------------------------------------------------------------------
+
+
+@pytest.mark.parametrize("rids", [[1], [1, 2, 2], [1, 2, 3], [1, 2, 4, 5], iter([1, 2])])
+def test_commit_tree_refuses_requests_before_it_moves_rows(monkeypatch, rids):
+    """One listed request for each row of the batch, all known, none twice: found before the rows in
+    the pools are moved, so that a refused call leaves cache and table as they were."""
+    moved = []
+    monkeypatch.setattr(cache_module, "tree_commit",
+                        lambda *a, **kw: moved.append(1) or torch.full((3,), 20))
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda *a: FakeStream())
+    monkeypatch.setattr(torch.cuda, "Stream", FakeStream)
+    monkeypatch.setattr(torch.cuda, "stream", lambda s: contextlib.nullcontext())
+    c = PagedKVCache(8, 1, 64, torch.float32, device="cpu")
+    for rid in (1, 2, 4):
+        c.add_request(rid)
+    c.reserve([1, 2, 4], [20, 20, 20])
+    ints = torch.zeros(3, dtype=torch.int32)
+    with pytest.raises(pkv.PkvError):
+        c.commit_tree(rids, ints[:, None], ints, ints, ints[:, None], ints)
+    assert not moved
+    assert c.commit_tree(iter([4, 1, 2]), ints[:, None], ints, ints, ints[:, None], ints) == [20] * 3
+    assert len(moved) == 1 and [c.lens[r] for r in (1, 2, 4)] == [20, 20, 20]
