@@ -11,6 +11,7 @@ import torch
 
 import paged_kv_cache_271_gb300 as pkv
 from paged_kv_cache_271_gb300.cache import PagedKVCache
+from tests import test_gpu_tree
 from tests.test_gpu_tree import DT, H, KINDS, U32, Tree, gen, randn, raw
 
 pytestmark = pytest.mark.gpu
@@ -166,3 +167,58 @@ def test_scores_of_huge_size_pick_the_largest(io, cache, d, power):
         checked += int(clear.sum())
         rows += clear.numel()
     assert 2 * checked > rows
+
+
+# ---- append: blocks with several row groups over many tokens -----------------------------------------
+
+# Rows (query, key and value heads) of a token, in groups of 16 (32 for 64 bf16 dims, 8 for 128 fp32
+# dims); calls of more than 456 groups in all give a block up to three groups of a token and several
+# tokens, an odd or an even number of them.
+LOOPS = [  # tokens, h_q, h_kv, d, io, cache, rot, interleaved, norm
+    (1401, 16, 8, 128, "bf16", "bf16", 128, False, True),   # two groups
+    (1000, 32, 8, 128, "bf16", "bf16", 128, False, True),   # three
+    (2300, 32, 8, 128, "bf16", "fp8", 128, False, True),    # three, six tokens at most
+    (777, 64, 8, 128, "bf16", "fp8", 128, False, True),     # three and two, in two parts
+    (643, 61, 9, 128, "bf16", "int8", 96, True, True),      # the same, the last one not full
+    (1500, 20, 5, 128, "bf16", "bf16", 48, True, False),    # heads of three kinds in one warp
+    (919, 70, 3, 64, "bf16", "int8", 64, False, True),
+    (1300, 12, 4, 128, "f32", "f32", 128, False, True),     # three groups
+    (1203, 9, 4, 128, "f32", "int8", 128, True, True),
+    (1100, 40, 4, 64, "f32", "fp8", 32, False, True),
+    (12345, 7, 1, 64, "f32", "f32", 64, True, True),        # one group, 28 tokens
+]
+
+
+@pytest.mark.parametrize("case", LOOPS, ids=lambda c: "-".join(map(str, c[:6])))
+def test_append_of_many_tokens_matches_the_formula(case):
+    test_gpu_tree.test_append_matches_the_formula(*case)
+
+
+@pytest.mark.parametrize("case", LOOPS[:10], ids=lambda c: "-".join(map(str, c[:6])))
+def test_append_of_many_tokens_is_that_of_each_alone(case):
+    """Bit for bit, in place as well, with padding, bad slots and bad positions among them."""
+    n, h_q, h_kv, d, io, cache, rot, inter, norm = case
+    q, k, v, w, pages, slots, table, pos, scales, kc, vc = test_gpu_tree.append_inputs(
+        n, h_q, h_kv, d, io, cache, rot, norm, seed=55)
+    slots, pos = slots.clone(), pos.clone()
+    slots[7::50], slots[9::50], pos[3::50], pos[4::50] = -1, pages * 16, -1, 500
+    ks, vs = scales or (None, None)
+
+    def one(i, j, kc, vc, out):
+        pkv.qk_norm_rope_append(q[i:j], k[i:j], v[i:j], pos[i:j], slots[i:j], kc, vc, table, w[0],
+                                w[1], 1e-5, inter, q_out=out[i:j], k_scales=ks, v_scales=vs)
+
+    pools = [(raw(kc).clone().view(kc.dtype), raw(vc).clone().view(vc.dtype)) for _ in range(3)]
+    want = q.clone()  # (rows of tokens left out stay)
+    for i in range(n):
+        one(i, i + 1, *pools[0], want)
+    assert pkv.device_error() == pkv.DEVERR_BAD_SLOT | pkv.DEVERR_BAD_POSITION
+    apart = q.clone()
+    one(0, n, *pools[1], apart)
+    k0, v0 = k.clone(), v.clone()
+    one(0, n, *pools[2], q)
+    assert pkv.device_error() == pkv.DEVERR_BAD_SLOT | pkv.DEVERR_BAD_POSITION
+    assert torch.equal(apart, want) and torch.equal(q, want)
+    assert torch.equal(k, k0) and torch.equal(v, v0)
+    for p in pools[1:]:
+        assert torch.equal(raw(p[0]), raw(pools[0][0])) and torch.equal(raw(p[1]), raw(pools[0][1]))
