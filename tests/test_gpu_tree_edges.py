@@ -5,6 +5,8 @@ a 64-bit implementation.
 A rounding to type t is off by at most eps(t) / 2 relative to the value; tolerances are derived where
 they are computed.
 """
+import math
+
 import numpy as np
 import pytest
 import torch
@@ -222,3 +224,113 @@ def test_append_of_many_tokens_is_that_of_each_alone(case):
     assert torch.equal(k, k0) and torch.equal(v, v0)
     for p in pools[1:]:
         assert torch.equal(raw(p[0]), raw(pools[0][0])) and torch.equal(raw(p[1]), raw(pools[0][1]))
+
+
+# ---- the step as it is used, node by node -------------------------------------------------------------
+
+
+def attention(q, k, v, see, scale, cache):
+    """(out, tolerance) [n, h_q, d] in fp64 on the CPU: queries [n, h_q, d] over rows k, v [c, h_kv, d],
+    of which node t sees those of see[t]."""
+    n, h_q, d = q.shape
+    c, h_kv, _ = k.shape
+    k, v = (x.repeat_interleave(h_q // h_kv, 1) for x in (k, v))
+    see = see[:, None, :]
+    s = (torch.einsum("thd,chd->thc", q, k) * scale).masked_fill(~see, -math.inf)
+    size = (torch.einsum("thd,chd->thc", q.abs(), k.abs()) * scale * see).amax(-1, keepdim=True)
+    p = torch.softmax(s, -1)
+    out, mag = (torch.einsum("thc,chd->thd", p, x) for x in (v, v.abs()))
+    # fp32 scores: d products and sums, the scales, twice (the score and the row's largest); the
+    # weights' exponents and the sums of c terms; the weights' rounding for the product with V
+    h = 2.0 ** -8 if cache == "bf16" else 2.0 ** -11
+    top = s.masked_fill(~see, 0).abs().amax(-1, keepdim=True)
+    tol = (h + (2 * (d + 4) * size + 4 * top + c + 80) * U32) * mag
+    if cache == "fp8":  # weights below f16's normals
+        tol = tol + 2.0 ** -24 * c * v.abs().amax(0)[None]
+    return out, tol + H["bf16"] * (out.abs() + tol)
+
+
+@pytest.mark.parametrize("cache", ["bf16", "fp8"])
+def test_every_node_of_every_step_attends_what_it_should(cache):
+    """Verification steps against a list of accepted rows kept on the CPU. The bounds tell a node that
+    sees one row too few: taking a node's own row out of the implementation breaks them."""
+    h_q, h_kv, d, B, T = 8, 2, 128, 3, 12
+    r, g = np.random.default_rng(60), gen(60)
+    ks = vs = None
+    if cache == "fp8":
+        ks, vs = (torch.tensor([0.02, 0.03], device="cuda") for _ in range(2))
+    c = PagedKVCache(64, h_kv, d, DT[cache], k_scales=ks, v_scales=vs)
+    table = pkv.rope_table(512, d)
+    norm = dict(q_weight=randn(g, d).add(1).bfloat16(), k_weight=randn(g, d).add(1).bfloat16())
+
+    def qkv(n):
+        x = randn(g, n, (h_q + 2 * h_kv) * d, dtype=torch.bfloat16)
+        return [y.view(n, -1, d) for y in x.split([h_q * d, h_kv * d, h_kv * d], dim=-1)]
+
+    def rows(slots):  # K and V rows of these slots on the CPU, in fp64
+        at = torch.from_numpy(np.asarray(slots)).cuda()
+        got = []
+        for pool, scale in ((c.k, ks), (c.v, vs)):
+            x = raw(pool)[at // 16, :, at % 16].view(DT[cache]).double()
+            got.append((x if scale is None else x * scale.double()[:, None]).cpu())
+        return got
+
+    lens = [45, 16, 3]
+    for b in range(B):
+        c.add_request(b)
+    slots = c.reserve(range(B), lens)
+    pos = torch.cat([torch.arange(n, dtype=torch.int32) for n in lens]).cuda()
+    c.write_qkv(slots, *qkv(sum(lens)), pos, table, **norm)
+    at = np.cumsum([0] + lens)
+    kept = [rows(slots[at[b]:at[b + 1]]) for b in range(B)]
+    for step in range(5):
+        parents = np.stack([[-1] + [int(r.integers(0, i)) for i in range(1, T)] for _ in range(B)])
+        masks, depths = pkv.tree_masks(parents)
+        n = [int(x) for x in r.integers(1, T + 1, B)]
+        n[step % B] = [T, 0, 1, T, 5][step]
+        pos = np.concatenate([lens[b] + depths[b, :n[b]] for b in range(B)]).astype(np.int32)
+        slots = c.reserve(range(B), n)
+        rot = c.write_qkv(slots, *qkv(sum(n)), torch.from_numpy(pos).cuda(), table, **norm)
+        at = np.cumsum([0] + n)
+        q = torch.zeros(B, T, h_q, d, dtype=torch.bfloat16, device="cuda")
+        for b in range(B):
+            q[b, :n[b]] = rot[at[b]:at[b + 1]]
+        bt = torch.from_numpy(c.block_table_array(range(B))).cuda()
+        cl = torch.from_numpy(c.context_lens_array(range(B))).cuda()
+        tl = torch.tensor(n, dtype=torch.int32, device="cuda")
+        out = c.attend_tree(q, bt, cl, d ** -0.5, torch.from_numpy(masks).cuda(), tl).double().cpu()
+        path = np.zeros((B, T), np.int32)
+        plen = np.zeros(B, np.int32)
+        for b in range(B):
+            assert not out[b, n[b]:].any()
+            if n[b] == 0:
+                continue
+            new = rows(slots[at[b]:at[b + 1]])
+            k, v = (torch.cat([x, y]) for x, y in zip(kept[b], new))
+            see = torch.zeros(n[b], lens[b] + n[b], dtype=torch.bool)
+            see[:, :lens[b]] = True
+            for i in range(n[b]):
+                j = i
+                while j >= 0:
+                    see[i, lens[b] + j] = True
+                    j = int(parents[b, j])
+            qb = q[b, :n[b]].double().cpu()
+            ref, tol = attention(qb, k, v, see, d ** -0.5, cache)
+            assert ((out[b, :n[b]] - ref).abs() <= tol).all(), (step, b)
+            for i in range(n[b]):
+                see[i, lens[b] + i] = False
+            ref, tol = attention(qb, k, v, see, d ** -0.5, cache)
+            assert ((out[b, :n[b]] - ref).abs() > tol).flatten(1).any(1).all(), (step, b)
+            walk = [0]
+            while True:
+                below = [i for i in range(n[b]) if parents[b, i] == walk[-1]]
+                if not below or r.random() < 0.2:
+                    break
+                walk.append(int(r.choice(below)))
+            path[b, :len(walk)], plen[b] = walk, len(walk)
+            kept[b] = [torch.cat([x, y[walk]]) for x, y in zip(kept[b], new)]
+        got = c.commit_tree(range(B), bt, cl, tl, torch.from_numpy(path).cuda(),
+                            torch.from_numpy(plen).cuda())
+        lens = [lens[b] + int(plen[b]) for b in range(B)]
+        assert got == lens == [len(kept[b][0]) for b in range(B)]
+    assert pkv.device_error() == 0
