@@ -89,6 +89,35 @@ def test_long_runs_of_single_tile_units(cache, d, nodes):
         assert torch.equal(t.run(), first)
 
 
+@pytest.mark.parametrize("io,cache", [("bf16", "bf16"), ("bf16", "fp8"), ("f32", "f32")])
+@pytest.mark.parametrize("nodes", [1, 3])
+def test_the_largest_batch(io, cache, nodes):
+    """65,535 requests of one page; a request's value rows are all alike, so every node that sees any
+    gives that row."""
+    B, h_kv, d = 65535, 1, 64
+    g = gen(56)
+    k = randn(g, B, h_kv, 16, d).to(DT[cache])
+    x = randn(g, B, h_kv, 1, d).to(DT[cache])
+    v = raw(x).view(B, h_kv, 1, -1).expand(-1, -1, 16, -1).contiguous().view(DT[cache])
+    q = randn(g, B, nodes, 2, d, dtype=DT[io])
+    bt = torch.randperm(B, generator=g, device="cuda").to(torch.int32)[:, None]
+    cl = torch.randint(0, 17, (B,), generator=g, device="cuda", dtype=torch.int32)
+    tl = torch.minimum(torch.randint(0, nodes + 1, (B,), generator=g, device="cuda",
+                                     dtype=torch.int32), cl)
+    ks = vs = torch.full((h_kv,), 0.5, device="cuda") if cache == "fp8" else None
+    out = pkv.tree_decode_attention(q, k, v, bt, cl, d ** -0.5, tree_lens=tl, k_scales=ks,
+                                    v_scales=vs)
+    assert pkv.device_error() == 0
+    want = x.double()[bt[:, 0].long()][:, :, 0, None] * (0.5 if cache == "fp8" else 1.0)
+    want = torch.where(torch.arange(nodes, device="cuda")[None, :, None, None] < tl[:, None, None, None],
+                       want, 0.0)
+    # the weights' rounding to the matrix type against their unrounded sum (16 terms), the division,
+    # the scales, the output's rounding; weights below f16's normals
+    h = {"f32": 0, "bf16": 2.0 ** -8, "fp8": 2.0 ** -11}[cache]
+    tol = (h + 40 * U32) * want.abs() + (2.0 ** -20 * want.abs().max() if cache == "fp8" else 0)
+    assert ((out.double() - want).abs() <= tol + H[io] * (want.abs() + tol)).all()
+
+
 # ---- outputs that the call makes --------------------------------------------------------------------
 
 
