@@ -200,6 +200,18 @@ def test_scores_of_huge_size_pick_the_largest(io, cache, d, power):
     assert 2 * checked > rows
 
 
+@pytest.mark.parametrize("io,cache,d", KINDS)
+def test_rows_of_huge_and_usual_scores_side_by_side(io, cache, d):
+    """Usual rows keep their bounds beside rows whose scores fp32 hardly tells apart (which only have
+    to be finite: their bound is as wide as the values)."""
+    for nodes, ctx in ((9, [40, 300, 64]), (60, [130, 700])):
+        t = Tree(ctx, [nodes] * len(ctx), nodes, 6, 2, d, io, cache, seed=57)
+        r = np.random.default_rng(57)
+        power = np.where(r.random((len(ctx), nodes, 6, 1)) < 0.3, r.integers(20, 60, (len(ctx), nodes, 6, 1)), 0)
+        t.q *= torch.from_numpy(2.0 ** power).to("cuda", t.q.dtype)
+        t.check()
+
+
 # ---- append: blocks with several row groups over many tokens -----------------------------------------
 
 # Rows (query, key and value heads) of a token, in groups of 16 (32 for 64 bf16 dims, 8 for 128 fp32
