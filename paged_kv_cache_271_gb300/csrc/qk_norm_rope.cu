@@ -243,12 +243,20 @@ __global__ void __launch_bounds__(kThreads, 3) qk_norm_rope_append_kernel(const 
     for (int g = 0; g < kGroups; ++g) {
       if (left_out || g >= groups) break;  // (uniform over the block)
       float xa[CH], xb[CH];
-      widen(lds64(ring0 + get + 2 * g * PART), xa);
-      widen(lds64(ring0 + get + (2 * g + 1) * PART), xb);
+      const uint2 ra = lds64(ring0 + get + 2 * g * PART);
+      const uint2 rb = lds64(ring0 + get + (2 * g + 1) * PART);
+      widen(ra, xa);
+      widen(rb, xb);
       const int64_t at = row0 + in_slot[g];
       if (kind[g] == 2 && stored) {
-        store_chunk<TIN, CACHE, CH>(a.v_cache, at, scale[g], xa);
-        store_chunk<TIN, CACHE, CH>(a.v_cache, at + over, scale[g], xb);
+        if constexpr (CACHE == PKV_F32 || CACHE == PKV_BF16) {  // the bits as they came (a NaN's too)
+          TIN* v = static_cast<TIN*>(a.v_cache) + at;
+          *reinterpret_cast<uint2*>(v) = ra;
+          *reinterpret_cast<uint2*>(v + over) = rb;
+        } else {
+          store_chunk<TIN, CACHE, CH>(a.v_cache, at, scale[g], xa);
+          store_chunk<TIN, CACHE, CH>(a.v_cache, at + over, scale[g], xb);
+        }
       }
       if (!rows_to_turn[g]) continue;
       float ss = 0.f;

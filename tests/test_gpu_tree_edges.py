@@ -267,6 +267,34 @@ def test_append_of_many_tokens_is_that_of_each_alone(case):
         assert torch.equal(raw(p[0]), raw(pools[0][0])) and torch.equal(raw(p[1]), raw(pools[0][1]))
 
 
+@pytest.mark.parametrize("cache", ["bf16", "fp8", "int8"])
+@pytest.mark.parametrize("scale", [0.02, 2.0 ** -100, 2.0 ** 100, 1e-38, -0.5, 0.0, float("nan")])
+def test_append_of_every_bf16_value_is_the_plain_appends(cache, scale):
+    """Value rows byte for byte, whatever they hold (infinities, NaN, subnormal numbers), and without
+    norm and rotation key rows too, but for which NaN a NaN becomes."""
+    x = torch.arange(65536, dtype=torch.int32, device="cuda").to(torch.int16).view(torch.bfloat16)
+    x = x[torch.randperm(65536, generator=gen(58), device="cuda")].view(256, 2, 128)
+    ks = vs = None if cache == "bf16" else torch.full((2,), scale, device="cuda")
+    slots = torch.randperm(320, generator=gen(59), device="cuda")[:256]
+    pools = [[test_gpu_tree.junk_pool(20, 2, 128, cache, 58) for _ in range(2)] for _ in range(3)]
+    q = torch.zeros(256, 4, 128, dtype=torch.bfloat16, device="cuda")
+    pkv.kv_append(x, x, slots, *pools[0], ks, vs)
+    pkv.qk_norm_rope_append(q, x, x, None, slots, *pools[1], None, k_scales=ks, v_scales=vs)
+    table = pkv.rope_table(4, 128)
+    pos = torch.zeros(256, dtype=torch.int32, device="cuda")  # (another path: the keys are rotated)
+    pkv.qk_norm_rope_append(q, x, x, pos, slots, *pools[2], table, k_scales=ks, v_scales=vs)
+    assert torch.equal(raw(pools[1][1]), raw(pools[0][1]))
+    assert torch.equal(raw(pools[2][1]), raw(pools[0][1]))
+    k0, k1 = pools[0][0], pools[1][0]
+    if cache == "int8":
+        assert torch.equal(k0, k1)
+    else:
+        nan = torch.isnan(k0.float())
+        assert torch.equal(torch.isnan(k1.float()), nan)
+        assert torch.equal(k0.view(raw(k0).dtype if cache == "fp8" else torch.int16)[~nan],
+                           k1.view(raw(k1).dtype if cache == "fp8" else torch.int16)[~nan])
+
+
 # ---- the step as it is used, node by node -------------------------------------------------------------
 
 
