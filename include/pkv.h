@@ -469,7 +469,8 @@ int pkv_seq_step_width(const pkv_seq_table* t, const int64_t* new_rids,
                        int32_t n_live, int32_t* width_out);
 /* Cuts the listed (distinct) requests back to new_lens[i] tokens, 0 .. their length: pages that
  * hold none of the kept tokens lose this request's reference and leave its row. PKV_EINVAL
- * (nothing changed) for an unknown or repeated id or a length outside that range. */
+ * (nothing changed) for an unknown or repeated id or a length outside that range. A window moves back
+ * with the length: pages released for it stay released, so release them after a draft is settled. */
 int pkv_seq_truncate(pkv_seq_table* t, const int64_t* rids, const int64_t* new_lens, int32_t n);
 /* Releases every page of the request whose positions all lie at or past sink_tokens, before
  * the last `window` positions and before the newest token (window 0: none); their row entries
@@ -741,7 +742,8 @@ size_t pkv_tree_decode_workspace_size(int32_t dtype_q, int32_t cache_dtype, int3
  *   out[b][t][h] = sum_p softmax(scale <q[b][t][h], K_p>)_p V_p
  * over the positions p < base and the nodes base + i whose bit i is set in node t's mask row.
  * A row that sees nothing gives 0. What is not seen takes no part, whatever it holds (NaN and
- * infinities too). Scores, maxima and sums are fp32; with BF16 queries the weights are rounded
+ * infinities too). There is no sliding window: every position before the draft is attended, and the
+ * entries of -1 that pkv_seq_release_outside_window leaves in a table row are bad page ids here. Scores, maxima and sums are fp32; with BF16 queries the weights are rounded
  * to the cache's matrix type (bf16 for a BF16 cache, f16 for FP8 and INT8) before they meet V.
  *  q, out       device [batch][tree_width][num_q_heads][head_dim] of dtype_q, 16-byte aligned;
  *               rows t >= tree_lens[b] of out are left as they were. F32 q takes an F32, FP8 or

@@ -16,10 +16,10 @@
 // join the whole's.
 //
 // Bound by FMAs and by the latency of the loads that feed them (two blocks of four warps on an SM):
-// 16 requests of 500 .. 4000 tokens, 96 rows a KV head, 128 dims, F32: 14.2 GFLOP in 423 us, 34
-// TFLOP/s, half of the fp32 rate (2 rows x 4 tokens a thread, 32-token tiles: 503 us); 32 rows, FP8:
-// 171 us (278). One request, 2000 tokens, 8 nodes: 32 us with its combine (64 threads and 32-token
-// tiles: 46).
+// 16 requests of 500 .. 4000 tokens, 96 rows a KV head, 128 dims, F32: 15.0 GFLOP in 462 us, 33
+// TFLOP/s, two fifths of the fp32 rate (on other lengths 423 us against 503 with 2 rows x 4 tokens a
+// thread and 32-token tiles); 32 rows, FP8: 182 us (171 against 278). One request, 2000 tokens, 8 nodes:
+// 25 us with its combine (single calls after a flush of the L2 32, 64 threads and 32-token tiles 46).
 #include <math.h>
 
 #include <atomic>

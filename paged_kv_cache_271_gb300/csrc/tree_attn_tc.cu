@@ -33,7 +33,8 @@
 //
 // P is rounded to the MMA's input type (bf16 for a bf16 cache, f16 otherwise), the only rounding
 // before the output's; scores, maxima and sums are fp32. For 8-bit caches a query row is scaled by
-// a power of two that puts its largest value in f16's top binade, undone in its score factor.
+// a power of two that puts its largest value in f16's top binade, undone in its score factor; the sign
+// of the K scale goes with it, so that score factors are positive.
 //
 // Tiles with unseen positions (the drafted nodes, the end of the context, bad pages) mask scores
 // by the row's 64 mask bits, and their V rows are mended in shared memory before the MMA reads them:
@@ -41,14 +42,17 @@
 // which 0 P would still spread to rows that do not see the node, become 0 there and are added to
 // the rows that do see it at the unit's end.
 //
-// Measured with the combine in graphs of calls over several states, against the bytes at the copy's
-// 6.78 TB/s: 64 requests of 512 .. 4096 bf16 tokens, 64 rows a head: 106 us (6.5 TB/s; 102); ragged
-// drafts of up to 256 rows: 135 (96); 4 requests of 8191 .. 65536 INT8 tokens, 96 rows: 54 (6.6 TB/s;
-// 53); 128 requests of 128 .. 8192 FP8 tokens, 192 rows: 359 (161). (The figures above are of single
-// calls after a flush of the L2, some 10 us more.)
-// Small units of an 8-bit or 64-dim cache and all large units are bound by the softmax steps, about
-// 1400 cycles of waits, tensor-memory loads and exponentials for 128 rows x 64 tokens, two at a time
-// on an SM, and by 4 to 8 thousand cycles from the last step of a unit to the first of the next.
+// Measured with the combine in graphs of calls over two states, in brackets the bytes of those states
+// and their time at the copy's 6.78 TB/s: 64 requests of 512 .. 4096 bf16 tokens, 64 rows a head: 111 us
+// (648 MB, 96); ragged drafts of up to 256 rows: 149 (651 MB, 96); 4 requests of 8191 .. 65536 INT8
+// tokens, 96 rows: 68 (210 MB, 31); 128 requests of 128 .. 8192 FP8 tokens, 192 rows: 388 (1108 MB, 163).
+// (The figures above, and beside the split's constants, are of single calls after a flush of the L2.)
+// Large units are bound by the softmax steps, about 1400 cycles of waits, tensor-memory loads and
+// exponentials for 128 rows x 64 tokens, two at a time on an SM, and by 4 to 8 thousand cycles from the
+// last step of a unit to the first of the next. Small units take, from whole calls, about 900 cycles a
+// tile of a 64-dim bf16 cache and 1200 to 1350 of an 8-bit one with 128 dims, for which the copy's rate
+// would allow 700: two steps at a time overlap in part only. Whether the hand-over of the maximum or the
+// converters, which widen one tile from end to end, set that pace has not been told apart.
 //
 // Every wait is bounded (PKV_DEVERR_TIMEOUT); the tensor memory is freed on every path.
 #include <atomic>

@@ -7,7 +7,7 @@
 // request and reads kAhead of its rows before it writes the first of them (a row written, i, is
 // below every node still to be read, path[k] >= k > i), so threads never wait for one another and
 // the moves' latency overlaps. Bound by latency: a step moves a few rows per request (64 requests of
-// up to 5 accepted nodes, bf16: 3.2 us a call in a graph, 256 of up to 12, FP8: 3.4).
+// up to 5 accepted nodes, bf16: 3.0 us a call in a graph, 256 of up to 12, FP8: 3.8).
 #include <algorithm>
 
 #include "pkv_device.cuh"
