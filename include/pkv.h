@@ -78,9 +78,12 @@ enum {
                               not extend past the shared prefix, a member index outside the
                               batch, more members or prefix pages than declared) */
   PKV_DEVERR_BAD_POSITION = 16, /* a position outside the rotation table: the token is left out */
-  PKV_DEVERR_BAD_TREE = 32 /* a draft longer than its request or than the tree width, or a path
+  PKV_DEVERR_BAD_TREE = 32, /* a draft longer than its request or than the tree width, or a path
                               that does not increase or leaves the draft: the request is left
                               out */
+  PKV_DEVERR_BAD_CHUNK = 64 /* a chunk whose rows are not in the batch's or that is longer than its
+                              request, a request longer than its row of sums, or a count of kept
+                              positions that its tables cannot hold: the request is left out */
 };
 
 /* Limits of the speculative-decoding entry points. */
@@ -88,6 +91,9 @@ enum {
   PKV_MAX_TREE_NODES = 256, /* drafted nodes of a request */
   PKV_MAX_TREE_GROUP = 128  /* query heads per KV head in the tree attention */
 };
+
+/* Limit of the chunk entry points: query heads per KV head. */
+enum { PKV_MAX_CHUNK_GROUP = 128 };
 
 /* Description of one layer's pair of pools. page_size must be 16; head_dim 64 or 128. */
 typedef struct {
@@ -795,6 +801,124 @@ int pkv_tree_commit(void* k_cache, void* v_cache, const pkv_cache_desc* desc,
                     const int32_t* path_lens, int32_t batch, int32_t max_path, int32_t* new_lens,
                     void* stream);
 
+/* ---- chunks of new tokens, and eviction ------------------------------------------------------ */
+
+/*
+ * The score of a query at position pq for a cached position p, and which positions it sees:
+ *   s = scale <q, K_p>;   softcap c > 0: s <- c tanh(s / c);   alibi_slopes: s <- s - slope_h (pq - p);
+ *   p <= pq;              window W > 0: and (p > pq - W or p < sink_tokens).
+ * scale positive and finite; softcap finite, >= 0 (0: none); alibi_slopes device fp32
+ * [num_q_heads] or NULL; window >= 0 (0: none), sink_tokens >= 0 (0 without a window). Positions
+ * are indices into the request's cache: after an eviction they are those of the kept tokens.
+ */
+typedef struct {
+  float scale;
+  float softcap;
+  const float* alibi_slopes;
+  int32_t window;
+  int32_t sink_tokens;
+} pkv_score_form;
+
+/* Bytes of device workspace pkv_chunk_attention needs for these sizes (0 for an empty call). Its
+ * contents do not matter, before or after; one workspace serves one stream at a time (two captured
+ * graphs that may run at the same time need one each). */
+size_t pkv_chunk_workspace_size(int32_t dtype_q, int32_t cache_dtype, int32_t num_rows,
+                                int32_t batch, int32_t num_q_heads, int32_t num_kv_heads,
+                                int32_t head_dim, int32_t max_pages_per_seq);
+
+/*
+ * Attention of a chunk of new tokens of each request over the paged cache (a prompt, a piece of
+ * one, or single tokens, beside one another). The chunk's K and V rows are already in the cache, as
+ * the request's last positions. Request b's queries are rows query_starts[b] .. query_starts[b+1]-1
+ * (n of them, n >= 0); row t is at position context_lens[b] - n + t. For query head h over KV head
+ * j = h / (num_q_heads / num_kv_heads):
+ *   out[row][h] = sum_p softmax(s)_p V_p,  lse[row][h] = ln sum_p e^{s_p}
+ * with scores and seen positions as `form` says. A row that sees nothing (its pages are bad) gives 0
+ * and -infinity. What is not seen takes no part, whatever it holds (NaN and infinities too). Scores,
+ * maxima and sums are fp32; with BF16 queries the weights are rounded to the cache's matrix type (bf16
+ * for a BF16 cache, f16 for FP8 and INT8) before they meet V.
+ *  q, out       device [num_rows][num_q_heads][head_dim] of dtype_q, 16-byte aligned. F32 q takes
+ *               an F32, FP8 or INT8 cache; BF16 q a BF16, FP8 or INT8 cache.
+ *  lse          device fp32 [num_rows][num_q_heads] or NULL.
+ *  block_tables, max_pages_per_seq, k_scales, v_scales   as pkv_paged_decode_attention. With a window,
+ *               pages that no row of the chunk sees are not read (their entries may be -1).
+ *  context_lens device int32 [batch], chunks included.
+ *  query_starts device int32 [batch + 1], not falling, within 0 .. num_rows. Rows of q that belong to
+ *               no request are not read, those of out and lse are left as they were.
+ * A request whose rows are not in 0 .. num_rows or that has fewer positions than rows is left out and
+ * flagged with PKV_DEVERR_BAD_CHUNK, one that is longer than its table row with PKV_DEVERR_BAD_PAGE;
+ * a page id outside the pool is skipped and flagged with PKV_DEVERR_BAD_PAGE.
+ *  workspace    device, >= pkv_chunk_workspace_size(...) bytes, 16-byte aligned.
+ * Requires num_q_heads % num_kv_heads == 0 and at most PKV_MAX_CHUNK_GROUP query heads per KV head.
+ * PKV_ESHAPE also for a BF16 pool of 2^31 rows (num_pages * num_kv_heads * page_size) or more,
+ * num_rows * num_q_heads of 2^31 or more, and a call whose table and rows could hold about 2^28 tiles
+ * (of 128 positions, counted for every KV head and 256 rows of tokens and query heads; fp32
+ * queries: 64 positions and 32 rows). Equal inputs give equal results; the split over the GPU, and so
+ * the rounding, depends on all requests' lengths.
+ */
+int pkv_chunk_attention(const void* q, int32_t dtype_q, int32_t num_rows, int32_t batch,
+                        int32_t num_q_heads, const void* k_cache, const void* v_cache,
+                        const pkv_cache_desc* desc, const int32_t* block_tables,
+                        int32_t max_pages_per_seq, const int32_t* context_lens,
+                        const int32_t* query_starts, const pkv_score_form* form,
+                        const float* k_scales, const float* v_scales, void* out, float* lse,
+                        void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Sums of the attention weights that the rows of a chunk give to each cached position:
+ *   weights_out[b][j][p] = add_to[b][j][p] + sum e^{s - lse[row][h]}
+ * over the counted rows and the query heads h of KV head j that see p, with s as in
+ * pkv_chunk_attention and the lse it left. Counted are a request's last last_rows rows (0: all).
+ * Rows whose lse is -infinity give nothing.
+ *  add_to       device fp32 [batch][num_kv_heads][width] or NULL (zeros).
+ *  weights_out  device fp32 [batch][num_kv_heads][width]; may be add_to. Columns p < context_lens[b]
+ *               are written, the others left as they were.
+ * A request longer than `width` is left out and flagged with PKV_DEVERR_BAD_CHUNK; the other
+ * arguments, refusals and flags are those of pkv_chunk_attention. Equal inputs give equal results.
+ */
+int pkv_chunk_weights(const void* q, int32_t dtype_q, int32_t num_rows, int32_t batch,
+                      int32_t num_q_heads, const void* k_cache, const pkv_cache_desc* desc,
+                      const int32_t* block_tables, int32_t max_pages_per_seq,
+                      const int32_t* context_lens, const int32_t* query_starts,
+                      const pkv_score_form* form, const float* k_scales, const float* lse,
+                      int32_t last_rows, const float* add_to, float* weights_out, int64_t width,
+                      void* stream);
+
+/*
+ * The positions that a request keeps when its cache is cut to `budget` tokens, for each KV head: its
+ * first sink_tokens, its last `recent`, and the ones with the largest sums between them, of equal sums
+ * the lower positions (-0 equals 0; NaN is above everything).
+ *  weights      device fp32 [batch][num_kv_heads][width].
+ *  context_lens device int32 [batch]; one outside 0 .. width keeps nothing and sets
+ *               PKV_DEVERR_BAD_CHUNK.
+ *  kept         device int32 [batch][num_kv_heads][budget]: the min(context_lens[b], budget) kept
+ *               positions in rising order, 0 behind them.
+ *  kept_lens    device int32 [batch]: min(context_lens[b], budget); not context_lens.
+ * budget > 0; recent, sink_tokens >= 0 and together at most budget.
+ */
+int pkv_evict_select(const float* weights, int64_t width, const int32_t* context_lens, int32_t batch,
+                     int32_t num_kv_heads, int32_t budget, int32_t recent, int32_t sink_tokens,
+                     int32_t* kept, int32_t* kept_lens, void* stream);
+
+/*
+ * Copies kept tokens together onto other pages: for KV head j of request b and i < kept_lens[b], the
+ * K and V rows of position kept[b][j][i] of table row block_tables[b] become position i of row
+ * new_tables[b] (codes as they are; scales stay the head's).
+ *  kept         device int32 [batch][num_kv_heads][budget], as pkv_evict_select leaves it.
+ *  new_tables   device int32 [batch][new_pages_per_seq]: pages that no table row of the call reads.
+ *               What they held is lost; rows behind kept_lens[b] are left as they were.
+ *  weights      device fp32 [batch][num_kv_heads][width] or NULL; new_weights [..][new_width] then
+ *               gets the kept positions' sums, 0 behind them, and is another array.
+ * A request whose kept_lens does not lie in 0 .. budget or is larger than its new table row or
+ * new_width is left out and flagged with PKV_DEVERR_BAD_CHUNK; a position outside its table row or a
+ * page id outside the pool is skipped and flagged with PKV_DEVERR_BAD_PAGE.
+ */
+int pkv_evict_move(void* k_cache, void* v_cache, const pkv_cache_desc* desc,
+                   const int32_t* block_tables, int32_t max_pages_per_seq, const int32_t* kept,
+                   const int32_t* kept_lens, int32_t batch, int32_t budget,
+                   const int32_t* new_tables, int32_t new_pages_per_seq, const float* weights,
+                   int64_t width, float* new_weights, int64_t new_width, void* stream);
+
 /* ---- prefix cache (host) ----------------------------------------------------------------- */
 
 /*
@@ -839,7 +963,8 @@ int32_t pkv_prefix_size(const pkv_prefix_cache* c);
  * bracketed by a pair of CUDA events on its stream. pkv_trace_read() synchronises those events
  * and reports, for the family named ("paged_decode", "decode_combine", "cascade_prefix",
  * "kv_append", "kv_absmax", "copy_pages", "qk_norm_rope_append", "tree_attention", "tree_combine",
- * "tree_commit", and the packed steps' "h2d_copy" and "d2h_copy"),
+ * "tree_commit", "chunk_attention", "chunk_combine", "chunk_weights", "evict_select", "evict_move",
+ * and the packed steps' "h2d_copy" and "d2h_copy"),
  * the number of launches and their summed device time in milliseconds since the last reset.
  * pkv_trace_reset() drops all records. */
 int pkv_trace_enable(int on);

@@ -11,7 +11,8 @@ Entry points (same names as the C ABI, without the ``pkv_`` prefix):
 ``pkv_incref``, ``pkv_decref``, ...), ``PrefixCache`` (``pkv_prefix_*``), ``cascade_groups``,
 ``cascade_decode_attention``, ``cascade_decode_step``, ``decode_set_chunk_pages``, ``trace_*``;
 for drafted tokens ``qk_norm_rope_append``, ``tree_masks``, ``tree_decode_attention`` and
-``tree_commit``.
+``tree_commit``; for prompts and caches of bounded size ``chunk_attention``, ``chunk_weights``,
+``evict_select`` and ``evict_move``.
 """
 from __future__ import annotations
 
@@ -29,12 +30,13 @@ __all__ = [
     "PageAllocator", "PrefixCache", "CascadeGroups", "cascade_groups", "cascade_decode_attention",
     "cascade_decode_step", "cascade_workspace_size", "HostStep", "trace_enable", "trace_reset",
     "trace_read", "rope_table", "qk_norm_rope_append", "tree_masks", "tree_decode_workspace_size",
-    "tree_decode_attention", "tree_commit",
+    "tree_decode_attention", "tree_commit", "chunk_workspace_size", "chunk_attention",
+    "chunk_weights", "evict_select", "evict_move",
 ]
 
 F32, BF16, FP8_E4M3, INT8 = 0, 1, 2, 3
 DEVERR_BAD_PAGE, DEVERR_BAD_SLOT, DEVERR_TIMEOUT, DEVERR_BAD_GROUP = 1, 2, 4, 8
-DEVERR_BAD_POSITION, DEVERR_BAD_TREE = 16, 32
+DEVERR_BAD_POSITION, DEVERR_BAD_TREE, DEVERR_BAD_CHUNK = 16, 32, 64
 _HERE = os.path.dirname(os.path.abspath(__file__))
 library_path = os.path.join(_HERE, "libpkv.so")
 _lib = None
@@ -50,6 +52,12 @@ class _Desc(ctypes.Structure):
     _fields_ = [("num_pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
                 ("num_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
                 ("cache_dtype", ctypes.c_int32)]
+
+
+class _ScoreForm(ctypes.Structure):
+    _fields_ = [("scale", ctypes.c_float), ("softcap", ctypes.c_float),
+                ("alibi_slopes", ctypes.c_void_p), ("window", ctypes.c_int32),
+                ("sink_tokens", ctypes.c_int32)]
 
 
 class _CascadeDesc(ctypes.Structure):
@@ -73,6 +81,7 @@ def lib():
                                   ctypes.c_float, ctypes.c_double, ctypes.c_size_t)
     D = ctypes.POINTER(_Desc)
     C = ctypes.POINTER(_CascadeDesc)
+    F = ctypes.POINTER(_ScoreForm)
     sig = {
         "pkv_last_error": (ctypes.c_char_p, []),
         "pkv_version": (ctypes.c_int, []),
@@ -139,6 +148,14 @@ def lib():
         "pkv_tree_decode_attention": (ctypes.c_int, [vp, i32, i32, i32, i32, vp, vp, D, vp, i32, vp,
                                                      vp, vp, i64, f32, vp, vp, vp, vp, sz, vp]),
         "pkv_tree_commit": (ctypes.c_int, [vp, vp, D, vp, i32, vp, vp, vp, vp, i32, i32, vp, vp]),
+        "pkv_chunk_workspace_size": (sz, [i32, i32, i32, i32, i32, i32, i32, i32]),
+        "pkv_chunk_attention": (ctypes.c_int, [vp, i32, i32, i32, i32, vp, vp, D, vp, i32, vp, vp,
+                                               F, vp, vp, vp, vp, vp, sz, vp]),
+        "pkv_chunk_weights": (ctypes.c_int, [vp, i32, i32, i32, i32, vp, D, vp, i32, vp, vp, F, vp,
+                                             vp, i32, vp, vp, i64, vp]),
+        "pkv_evict_select": (ctypes.c_int, [vp, i64, vp, i32, i32, i32, i32, i32, vp, vp, vp]),
+        "pkv_evict_move": (ctypes.c_int, [vp, vp, D, vp, i32, vp, vp, i32, i32, vp, i32, vp, i64,
+                                          vp, i64, vp]),
         "pkv_seq_release_outside_window": (ctypes.c_int, [vp, i64, i64, i64,
                                                           ctypes.POINTER(i32)]),
         "pkv_seq_len": (i64, [vp, i64]),
@@ -921,6 +938,176 @@ def tree_commit(k_cache, v_cache, block_tables, context_lens, tree_lens, path, p
         block_tables.shape[1], cl, tl, pa, pl, B, path.shape[1],
         _addr(new_lens, "new_lens", dev), _raw_stream(stream, dev)))
     return new_lens
+
+
+@functools.lru_cache(maxsize=256)
+def chunk_workspace_size(dtype_q, cache_dtype, num_rows, batch, num_q_heads, num_kv_heads,
+                         head_dim, max_pages_per_seq) -> int:
+    """Bytes of workspace of a chunk_attention call (dtypes as torch dtypes or codes)."""
+    code = lambda d: d if isinstance(d, int) else _dtype_code(torch.empty(0, dtype=d))
+    return int(lib().pkv_chunk_workspace_size(code(dtype_q), code(cache_dtype), num_rows, batch,
+                                              num_q_heads, num_kv_heads, head_dim,
+                                              max_pages_per_seq))
+
+
+def _chunk_args(q, desc, block_tables, context_lens, query_starts, alibi_slopes):
+    """Checks what the chunk calls share; returns (rows, batch, query heads)."""
+    if q.dim() != 3:
+        raise PkvError(-2, "q must be [rows, num_q_heads, head_dim]")
+    if (block_tables.dtype != torch.int32 or context_lens.dtype != torch.int32 or
+            query_starts.dtype != torch.int32):
+        raise PkvError(-3, "block_tables, context_lens and query_starts must be int32")
+    n, h_q, d = q.shape
+    B = context_lens.numel()
+    if block_tables.dim() != 2 or block_tables.shape[0] != B or query_starts.numel() != B + 1:
+        raise PkvError(-2, "block_tables must be [batch, max_pages], context_lens [batch], "
+                           "query_starts [batch + 1]")
+    if d != desc.head_dim:
+        raise PkvError(-2, "q head_dim does not match the pool")
+    if alibi_slopes is not None and (alibi_slopes.dtype != torch.float32 or
+                                     alibi_slopes.numel() != h_q):
+        raise PkvError(-2, "alibi_slopes must be float32 [num_q_heads]")
+    return n, B, h_q
+
+
+def chunk_attention(q, k_cache, v_cache, block_tables, context_lens, query_starts, scale,
+                    softcap=0.0, alibi_slopes=None, window=0, sink_tokens=0, out=None, lse=None,
+                    k_scales=None, v_scales=None, workspace=None, stream=None):
+    """Attention of a chunk of new tokens of each request over the paged pools, the chunk's own rows
+    included (they are the request's last cached rows already); returns out. q [N, h_q, d]: request
+    b's rows are query_starts[b] .. query_starts[b + 1] - 1 (int32 [batch + 1]). Every row sees the
+    positions up to its own. ``softcap`` c > 0: scores c tanh(s / c); ``alibi_slopes`` fp32 [h_q]: minus
+    slope times distance; ``window`` > 0: the last ``window`` positions and the first ``sink_tokens``.
+    ``lse`` fp32 [N, h_q] receives the logarithm of each row's sum, for ``chunk_weights``
+    (pkv_chunk_attention). Rows of no request are left as they were (zero in a new ``out``)."""
+    desc = _pools(k_cache, v_cache)
+    n, B, h_q = _chunk_args(q, desc, block_tables, context_lens, query_starts, alibi_slopes)
+    _check_scales(desc, k_scales, v_scales)
+    if lse is not None and (lse.dtype != torch.float32 or tuple(lse.shape) != (n, h_q)):
+        raise PkvError(-2, "lse must be float32 [rows, num_q_heads]")
+    if out is None:
+        out = _new(torch.zeros, q.shape, q.dtype, q.device, stream)
+    elif out.shape != q.shape or out.dtype != q.dtype:
+        raise PkvError(-2, "out must match q in shape and dtype")
+    dev = torch.cuda.current_device()
+    code, maxp = _dtype_code(q), block_tables.shape[1]
+    if workspace is None:
+        need = chunk_workspace_size(code, desc.cache_dtype, n, B, h_q, desc.num_kv_heads,
+                                    desc.head_dim, maxp)
+        workspace = _new(torch.empty, need, torch.uint8, q.device, stream)
+    form = _ScoreForm(scale, softcap, _opt_addr(alibi_slopes, "alibi_slopes", dev), window,
+                      sink_tokens)
+    _check(lib().pkv_chunk_attention(
+        _addr(q, "q", dev), code, n, B, h_q, _addr(k_cache, "k_cache", dev),
+        _addr(v_cache, "v_cache", dev), desc, _addr(block_tables, "block_tables", dev), maxp,
+        _addr(context_lens, "context_lens", dev), _addr(query_starts, "query_starts", dev), form,
+        _opt_addr(k_scales, "k_scales", dev), _opt_addr(v_scales, "v_scales", dev),
+        _addr(out, "out", dev), _opt_addr(lse, "lse", dev), _addr(workspace, "workspace", dev),
+        workspace.numel() * workspace.element_size(), _raw_stream(stream, dev)))
+    return out
+
+
+def chunk_weights(q, k_cache, block_tables, context_lens, query_starts, lse, scale, softcap=0.0,
+                  alibi_slopes=None, window=0, sink_tokens=0, last_rows=0, add_to=None, out=None,
+                  width=None, k_scales=None, stream=None):
+    """Sums fp32 [batch, num_kv_heads, width] of the attention weights e^(s - lse) that each request's
+    last ``last_rows`` new rows (0: all) give to its cached positions, over rows and the query heads of
+    a KV head, added to ``add_to`` (None: zeros); scores as in ``chunk_attention``, which left ``lse``
+    (pkv_chunk_weights). ``out`` may be ``add_to``; columns behind a request's context are left as they
+    were (in a new ``out`` as in ``add_to``, or zero). ``width`` of a new ``out`` without ``add_to``:
+    the table's positions unless given."""
+    desc = _pool_desc(k_cache.shape, k_cache.dtype)
+    n, B, h_q = _chunk_args(q, desc, block_tables, context_lens, query_starts, alibi_slopes)
+    if desc.cache_dtype in (FP8_E4M3, INT8):
+        _check_scales(desc, k_scales, k_scales)
+    if lse.dtype != torch.float32 or tuple(lse.shape) != (n, h_q):
+        raise PkvError(-2, "lse must be float32 [rows, num_q_heads]")
+    h_kv = desc.num_kv_heads
+    dev = torch.cuda.current_device()
+    for t, name in ((add_to, "add_to"), (out, "out")):
+        if t is not None and (t.dtype != torch.float32 or t.dim() != 3 or
+                              tuple(t.shape[:2]) != (B, h_kv)):
+            raise PkvError(-2, "%s must be float32 [batch, num_kv_heads, width]" % name)
+    if out is None:
+        if add_to is None:
+            width = block_tables.shape[1] * 16 if width is None else int(width)
+            out = _new(torch.zeros, (B, h_kv, width), torch.float32, q.device, stream)
+        else:
+            _addr(add_to, "add_to", dev)
+            out = _new(lambda *_, **__: add_to.clone(), None, None, q.device, stream)
+    elif add_to is not None and add_to.shape != out.shape:
+        raise PkvError(-2, "add_to and out must have one shape")
+    form = _ScoreForm(scale, softcap, _opt_addr(alibi_slopes, "alibi_slopes", dev), window,
+                      sink_tokens)
+    _check(lib().pkv_chunk_weights(
+        _addr(q, "q", dev), _dtype_code(q), n, B, h_q, _addr(k_cache, "k_cache", dev), desc,
+        _addr(block_tables, "block_tables", dev), block_tables.shape[1],
+        _addr(context_lens, "context_lens", dev), _addr(query_starts, "query_starts", dev), form,
+        _opt_addr(k_scales, "k_scales", dev), _addr(lse, "lse", dev), last_rows,
+        _opt_addr(add_to, "add_to", dev), _addr(out, "out", dev), out.shape[2],
+        _raw_stream(stream, dev)))
+    return out
+
+
+def evict_select(weights, context_lens, budget, recent=0, sink_tokens=0, kept=None, kept_lens=None,
+                 stream=None):
+    """The positions that each request keeps, for each KV head, when its cache is cut to ``budget``
+    tokens: the first ``sink_tokens``, the last ``recent`` and those with the largest ``weights``
+    (fp32 [batch, num_kv_heads, width]) between them, equal ones by position (pkv_evict_select).
+    Returns (kept int32 [batch, num_kv_heads, budget] in rising order, 0 behind them; kept_lens int32
+    [batch] = min(context, budget))."""
+    if weights.dtype != torch.float32 or weights.dim() != 3:
+        raise PkvError(-2, "weights must be float32 [batch, num_kv_heads, width]")
+    B, h_kv, width = weights.shape
+    if context_lens.dtype != torch.int32 or context_lens.numel() != B:
+        raise PkvError(-3, "context_lens must be int32 [batch]")
+    shape = (B, h_kv, max(int(budget), 0))
+    if kept is None:
+        kept = _new(torch.empty, shape, torch.int32, weights.device, stream)
+    elif kept.dtype != torch.int32 or tuple(kept.shape) != shape:
+        raise PkvError(-2, "kept must be int32 [batch, num_kv_heads, budget]")
+    if kept_lens is None:
+        kept_lens = _new(torch.empty, (B,), torch.int32, weights.device, stream)
+    elif kept_lens.dtype != torch.int32 or kept_lens.numel() != B:
+        raise PkvError(-2, "kept_lens must be int32 [batch]")
+    dev = torch.cuda.current_device()
+    _check(lib().pkv_evict_select(
+        _addr(weights, "weights", dev), width, _addr(context_lens, "context_lens", dev), B, h_kv,
+        int(budget), int(recent), int(sink_tokens), _addr(kept, "kept", dev),
+        _addr(kept_lens, "kept_lens", dev), _raw_stream(stream, dev)))
+    return kept, kept_lens
+
+
+def evict_move(k_cache, v_cache, block_tables, kept, kept_lens, new_tables, weights=None,
+               new_weights=None, stream=None):
+    """Copies each KV head's kept rows (``evict_select``) together onto the pages of ``new_tables``,
+    which no row of ``block_tables`` may hold; with ``weights`` [batch, num_kv_heads, width] their sums
+    into ``new_weights`` [batch, num_kv_heads, any width], zeros behind them (pkv_evict_move)."""
+    desc = _pools(k_cache, v_cache)
+    for t, name in ((block_tables, "block_tables"), (kept, "kept"), (kept_lens, "kept_lens"),
+                    (new_tables, "new_tables")):
+        if t.dtype != torch.int32:
+            raise PkvError(-3, "%s must be int32" % name)
+    B, h_kv = kept_lens.numel(), desc.num_kv_heads
+    if kept.dim() != 3 or tuple(kept.shape[:2]) != (B, h_kv):
+        raise PkvError(-2, "kept must be [batch, num_kv_heads, budget], kept_lens [batch]")
+    for t, name in ((block_tables, "block_tables"), (new_tables, "new_tables")):
+        if t.dim() != 2 or t.shape[0] != B:
+            raise PkvError(-2, "%s must be [batch, pages]" % name)
+    if (weights is None) != (new_weights is None):
+        raise PkvError(-1, "weights and new_weights go together")
+    for t, name in ((weights, "weights"), (new_weights, "new_weights")):
+        if t is not None and (t.dtype != torch.float32 or t.dim() != 3 or
+                              tuple(t.shape[:2]) != (B, h_kv)):
+            raise PkvError(-2, "%s must be float32 [batch, num_kv_heads, width]" % name)
+    dev = torch.cuda.current_device()
+    _check(lib().pkv_evict_move(
+        _addr(k_cache, "k_cache", dev), _addr(v_cache, "v_cache", dev), desc,
+        _addr(block_tables, "block_tables", dev), block_tables.shape[1], _addr(kept, "kept", dev),
+        _addr(kept_lens, "kept_lens", dev), B, kept.shape[2], _addr(new_tables, "new_tables", dev),
+        new_tables.shape[1], _opt_addr(weights, "weights", dev),
+        0 if weights is None else weights.shape[2], _opt_addr(new_weights, "new_weights", dev),
+        0 if new_weights is None else new_weights.shape[2], _raw_stream(stream, dev)))
 
 
 def kv_absmax_scales(x, scales_out=None, stream=None, int8=False):

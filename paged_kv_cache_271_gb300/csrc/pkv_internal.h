@@ -175,6 +175,76 @@ struct CommitArgs {
   int row_bytes;
 };
 
+// Attention of chunks of new tokens (chunk_plan.cuh has the work split), and the sums of its weights.
+struct ChunkArgs {
+  const void* q;  // [num_rows][h_q][D]
+  void* out;
+  float* lse;  // [num_rows][h_q]: written by the attention (or null), read by the weights
+  const void* k_cache;
+  const void* v_cache;
+  const int32_t* block_tables;
+  const int32_t* context_lens;  // chunks included
+  const int32_t* query_starts;  // [batch + 1]: request b's rows are query_starts[b] ..
+  const float* slopes;          // [h_q] or null: score -= slope * (row's position - position)
+  const float* k_scales;
+  const float* v_scales;
+  float* ws_acc;  // [ctas][2][unit_rows][D] partial weighted values
+  float* ws_ml;   // [ctas][2][unit_rows][2] partial (max, sum), log2 domain
+  void* ws_rec;   // [ctas] ChunkRecord
+  int* err;
+  int num_rows;
+  int batch;
+  int h_q;
+  int h_kv;
+  int group;  // h_q / h_kv
+  int num_pages;
+  int max_pages;
+  int tma_rank;
+  float scale;
+  float softcap;  // 0: none
+  int window;     // 0: none
+  int sink;
+  // the work split
+  int ctas;
+  int unit_rows;    // query rows of a unit
+  int unit_tokens;  // whole tokens of a unit
+  int subs;         // units of a token and KV head (1 unless group > unit_rows)
+  int tile_tokens;
+  int min_tiles;
+  int pass_cost;
+  int narrow_rows;
+  int wide_tile;
+  // the weights' sums: weights_out = add_to + sums over the last last_rows new tokens (0: all)
+  const float* add_to;  // [batch][h_kv][width] or null
+  float* weights_out;
+  int64_t width;
+  int last_rows;
+};
+
+// Eviction: kept[b][j][i], i < kept_lens[b], are the chosen positions of KV head j in rising order.
+struct EvictSelectArgs {
+  const float* weights;  // [batch][h_kv][width]
+  int64_t width;
+  const int32_t* context_lens;
+  int32_t* kept;  // [batch][h_kv][budget], 0 behind kept_lens
+  int32_t* kept_lens;
+  int* err;
+  int batch, h_kv, budget, recent, sink;
+};
+struct EvictMoveArgs {
+  void* k_cache;
+  void* v_cache;
+  const int32_t* block_tables;
+  const int32_t* new_tables;
+  const int32_t* kept;
+  const int32_t* kept_lens;
+  const float* weights;  // or null
+  float* new_weights;    // [batch][h_kv][new_width], 0 behind kept_lens
+  int64_t width, new_width;
+  int* err;
+  int batch, h_kv, budget, max_pages, new_pages, num_pages, row_bytes;
+};
+
 // Each returns the launch status. dtype codes are pkv_dtype values.
 cudaError_t launch_qk_norm_rope_append(const NormRopeArgs& a, int io_dtype, int cache_dtype,
                                        cudaStream_t s);
@@ -191,6 +261,17 @@ cudaError_t launch_tree_tc(const TreeArgs& a, int kv_dtype, int head_dim, const 
                            const void* tv, cudaStream_t s);
 cudaError_t launch_tree_combine(const TreeArgs& a, int q_dtype, int head_dim, cudaStream_t s);
 cudaError_t launch_tree_commit(const CommitArgs& a, cudaStream_t s);
+// Chunk attention on CUDA cores, and the combine of a split call of any type.
+constexpr int kChunkSimtRows = 32, kChunkSimtTokens = 64;
+constexpr int chunk_simt_wave(int head_dim) { return 152 * (head_dim == 64 ? 4 : 2); }
+cudaError_t launch_chunk_simt(const ChunkArgs& a, int q_dtype, int kv_dtype, int head_dim,
+                              cudaStream_t s);
+cudaError_t launch_chunk_combine(const ChunkArgs& a, int q_dtype, int head_dim, cudaStream_t s);
+// The weights' sums.
+cudaError_t launch_chunk_weights_simt(const ChunkArgs& a, int q_dtype, int kv_dtype, int head_dim,
+                                      cudaStream_t s);
+cudaError_t launch_evict_select(const EvictSelectArgs& a, cudaStream_t s);
+cudaError_t launch_evict_move(const EvictMoveArgs& a, cudaStream_t s);
 cudaError_t launch_decode_f32(const DecodeArgs& a, int q_dtype, int head_dim, int group,
                               cudaStream_t s);
 cudaError_t launch_decode_bf16(const DecodeArgs& a, int q_dtype, int head_dim, int group,
