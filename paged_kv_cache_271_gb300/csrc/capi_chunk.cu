@@ -17,11 +17,15 @@ namespace {
 // and wide tiles (chunk_plan.cuh) and the CTAs of one wave of the kernel that a call uses.
 struct ChunkSplit {
   int rows, tokens, min_tiles, pass_cost, narrow_rows, wide_tile, wave;
+  bool tc;
 };
 
+// bf16 queries run on the tensor cores, fp32 queries (whose weights keep 24 bits) on CUDA cores.
 ChunkSplit chunk_split(int dtype_q, int kv, int head_dim) {
+  if (dtype_q == PKV_BF16)
+    return ChunkSplit{kChunkTcRows, kChunkTcTokens, 2, 3, kChunkTcRows / 2, 3, kChunkTcWave, true};
   return ChunkSplit{kChunkSimtRows, kChunkSimtTokens, 1, 1, kChunkSimtRows, 2,
-                    chunk_simt_wave(head_dim)};
+                    chunk_simt_wave(head_dim), false};
 }
 
 // a b, or 2^60 where that is less (a, b in [0, 2^62]).
@@ -192,8 +196,16 @@ int pkv_chunk_attention(const void* q, int32_t dtype_q, int32_t num_rows, int32_
   a.ws_ml = reinterpret_cast<float*>(static_cast<char*>(workspace) + space.acc);
   a.ws_rec = static_cast<char*>(workspace) + space.ml;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  cudaError_t e =
-      traced("chunk_attention", s, [&] { return launch_chunk_simt(a, dtype_q, kv, D, s); });
+  CUtensorMap tk{}, tv{};
+  if (t.tc && kv == PKV_BF16) {
+    int rank = 2;
+    st = pool_tensor_map(k_cache, desc, &tk, &rank, true);
+    if (st == PKV_OK) st = pool_tensor_map(v_cache, desc, &tv, &a.tma_rank);
+    if (st != PKV_OK) return st;
+  }
+  cudaError_t e = traced("chunk_attention", s, [&] {
+    return t.tc ? launch_chunk_tc(a, kv, D, &tk, &tv, s) : launch_chunk_simt(a, kv, D, s);
+  });
   st = cuda_status(e, "chunk_attention launch");
   if (st != PKV_OK || a.ctas == 1) return st;  // (one CTA finishes every unit)
   e = traced("chunk_combine", s, [&] { return launch_chunk_combine(a, dtype_q, D, s); });

@@ -56,17 +56,11 @@ __device__ __forceinline__ ulonglong2 pairs(const float* p) {
 }
 
 __device__ __forceinline__ void store4(float* p, float4 v) { *reinterpret_cast<float4*>(p) = v; }
-__device__ __forceinline__ void store4(__nv_bfloat16* p, float4 v) {
-  store_from_float(p, 0, v.x);
-  store_from_float(p, 1, v.y);
-  store_from_float(p, 2, v.z);
-  store_from_float(p, 3, v.w);
-}
 
-template <typename TQ, typename KV, int D>
+template <typename KV, int D>
 __global__ void __launch_bounds__(kThreads, SimtShape<D>::CTAS) chunk_simt_kernel(const ChunkArgs a) {
   using S = SimtShape<D>;
-  constexpr bool WIDEN = KV::bytes < 4;
+  constexpr bool WIDEN = KV::bytes == 1;
   constexpr int NQ = D / 64;  // float4 groups of dims a thread accumulates, 64 dims apart
   constexpr int LD = S::LD, LP = S::LP;
   extern __shared__ float4 smem4[];
@@ -165,7 +159,7 @@ __global__ void __launch_bounds__(kThreads, SimtShape<D>::CTAS) chunk_simt_kerne
     for (int e = threadIdx.x; e < kRows * (D / 4); e += kThreads) {
       const int r = e / (D / 4), c = e % (D / 4);
       float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (r < run.rows) v = load4(static_cast<const TQ*>(a.q) + chunk_row(a, run, r) * D + 4 * c);
+      if (r < run.rows) v = load4(static_cast<const float*>(a.q) + chunk_row(a, run, r) * D + 4 * c);
       *reinterpret_cast<float4*>(qs + r * LD + 4 * c) = v;
     }
     if constexpr (WIDEN) {
@@ -366,7 +360,7 @@ __global__ void __launch_bounds__(kThreads, SimtShape<D>::CTAS) chunk_simt_kerne
           v = make_float4(v.x / l[i] * vsc, v.y / l[i] * vsc, v.z / l[i] * vsc, v.w / l[i] * vsc);
         else
           v = make_float4(0.f, 0.f, 0.f, 0.f);
-        store4(static_cast<TQ*>(a.out) + at * D + 4 * tx + 64 * k, v);
+        store4(static_cast<float*>(a.out) + at * D + 4 * tx + 64 * k, v);
       }
     }
     if (!run.whole && run.slot == 1)
@@ -448,28 +442,27 @@ __global__ void __launch_bounds__(kCombineThreads) chunk_combine_kernel(const Ch
   }
 }
 
-template <typename TQ, typename KV, int D>
+template <typename KV, int D>
 cudaError_t simt_go(const ChunkArgs& a, cudaStream_t s) {
   static std::atomic<unsigned long long> attr_done{0};  // one bit per device
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev >= 64 || !((attr_done.load() >> dev) & 1ull)) {
-    e = cudaFuncSetAttribute(chunk_simt_kernel<TQ, KV, D>,
+    e = cudaFuncSetAttribute(chunk_simt_kernel<KV, D>,
                              cudaFuncAttributeMaxDynamicSharedMemorySize, SimtShape<D>::SMEM);
     if (e != cudaSuccess) return e;
     if (dev < 64) attr_done.fetch_or(1ull << dev);
   }
-  chunk_simt_kernel<TQ, KV, D><<<a.ctas, kThreads, SimtShape<D>::SMEM, s>>>(a);
+  chunk_simt_kernel<KV, D><<<a.ctas, kThreads, SimtShape<D>::SMEM, s>>>(a);
   return cudaGetLastError();
 }
 
-template <typename TQ, int D>
+template <int D>
 cudaError_t simt_types(const ChunkArgs& a, int kv_dtype, cudaStream_t s) {
-  if (kv_dtype == PKV_F32) return simt_go<TQ, F32, D>(a, s);
-  if (kv_dtype == PKV_BF16) return simt_go<TQ, BF16, D>(a, s);
-  if (kv_dtype == PKV_FP8_E4M3) return simt_go<TQ, FP8, D>(a, s);
-  return simt_go<TQ, INT8, D>(a, s);
+  if (kv_dtype == PKV_F32) return simt_go<F32, D>(a, s);
+  if (kv_dtype == PKV_FP8_E4M3) return simt_go<FP8, D>(a, s);
+  return simt_go<INT8, D>(a, s);
 }
 
 template <typename TQ, int D>
@@ -489,13 +482,8 @@ cudaError_t launch_combine(const ChunkArgs& a, cudaStream_t s) {
 
 }  // namespace
 
-cudaError_t launch_chunk_simt(const ChunkArgs& a, int q_dtype, int kv_dtype, int head_dim,
-                              cudaStream_t s) {
-  if (q_dtype == PKV_BF16)
-    return head_dim == 64 ? simt_types<__nv_bfloat16, 64>(a, kv_dtype, s)
-                          : simt_types<__nv_bfloat16, 128>(a, kv_dtype, s);
-  return head_dim == 64 ? simt_types<float, 64>(a, kv_dtype, s)
-                        : simt_types<float, 128>(a, kv_dtype, s);
+cudaError_t launch_chunk_simt(const ChunkArgs& a, int kv_dtype, int head_dim, cudaStream_t s) {
+  return head_dim == 64 ? simt_types<64>(a, kv_dtype, s) : simt_types<128>(a, kv_dtype, s);
 }
 
 cudaError_t launch_chunk_combine(const ChunkArgs& a, int q_dtype, int head_dim, cudaStream_t s) {

@@ -1,0 +1,957 @@
+// Attention of chunks of new tokens on the fifth-generation tensor cores (tcgen05), bf16 queries over a
+// bf16, FP8 or INT8 cache.
+//
+// The mathematics is that of chunk_attn.cu; the work is cut as chunk_plan.cuh says, in units of up to
+// 256 (token, query head) rows of one KV head and tiles of 128 tokens, one persistent CTA per SM. A
+// tile of a full unit takes 4 x 256 x 128 x D operations, 2048 cycles of the tensor cores at D = 128, and
+// reads 64 KB of K and V from L2 or memory; everything else is arranged beside that:
+//
+//  * copy warps stream the share's tiles through rings of shared memory, running ahead across units;
+//    a bf16 tile arrives by TMA in the 128-byte-swizzled form the MMAs read, the codes of an 8-bit
+//    tile by bulk copies, which four converter warps widen to f16 (exactly) in that form;
+//  * one MMA warp issues S = Q K^T (128 rows x 128 tokens) and O += P V, with P as an A operand in the
+//    tensor memory that held S and all accumulators there;
+//  * two groups of four softmax warps, thread r of a group owning row r. In a unit of more than 128
+//    rows group g takes rows 128 g .. of every tile: while one group works on its scores, the tensor
+//    cores have the other's P V and next S. In a smaller unit both groups have the same rows and take
+//    alternate tiles, and the two sums are merged at the unit's end;
+//  * O is rescaled only when a row's maximum grows by more than 2^8 (P <= 2^8 until then): the final
+//    (max, sum, O) is exact whatever maximum it was accumulated against.
+//
+// P is rounded to the MMA's input type (bf16 for a bf16 cache, f16 otherwise), the only rounding
+// before the output's; scores, maxima and sums are fp32. For 8-bit caches a query row is scaled by
+// a power of two that puts its largest value in f16's top binade, undone in its score factor; the sign
+// of the K scale goes with it, so that score factors are positive.
+//
+// Tiles with unseen positions (the chunk's own, the window's edge, bad pages) mask scores by the row's
+// mask bits, and their V rows are mended in shared memory before the MMA reads them: rows outside the
+// context or on a page that is not there become 0, and infinite or NaN values, which a weight of 0
+// would still spread to rows that do not see them, become 0 there and are added to the rows that do
+// see them at the unit's end.
+//
+// Every wait is bounded (PKV_DEVERR_TIMEOUT); the tensor memory is freed on every path.
+#include <atomic>
+#include <cuda.h>
+#include <math.h>
+
+#include "chunk_plan.cuh"
+#include "chunk_score.cuh"
+#include "paged_decode_mma.cuh"
+#include "pkv_device.cuh"
+#include "pkv_internal.h"
+#include "tcgen05.cuh"
+
+namespace pkv {
+
+namespace {
+
+constexpr int kTok = kChunkTcTokens;       // tokens of a tile
+constexpr int kPages = kTok / kPageSize;   // pages of a tile
+constexpr int kGroupThreads = 128;         // a softmax group: one row per thread
+constexpr int kSoftThreads = 2 * kGroupThreads;
+constexpr int kMmaWarp = kSoftThreads / 32;
+constexpr int kCopyWarp = kMmaWarp + 1;    // K; the next one V (8-bit caches: one for both)
+constexpr int kConvWarp = kMmaWarp + 4;    // first of four (8-bit caches; one warp before is idle)
+constexpr int kConvThreads = 128;
+// Runs on their way from the first copy warp, which walks the share, to the other warps. It is ahead
+// of the slowest by the tiles in the rings at most, each a run of its own at worst, besides the run whose
+// rows are being written, the one after it and the one it is about to copy.
+constexpr int kRuns = 16;
+constexpr uint32_t kTmemCols = 512;        // O of group g at 128 g, S (then P) at 256 + 128 g
+constexpr float kLazyLog2 = 8.f;
+// tiles of a unit in which some rows see a position that others do not: those that cross the sinks'
+// end, and those of the at most 256 positions from the first to the last row's end or window
+constexpr int kEdgeTiles = 8;
+static_assert(2 * kGroupThreads == kChunkTcRows, "a unit is two groups' rows");
+
+template <typename KV, int D>
+struct TcShape {
+  static constexpr bool W8 = KV::bytes == 1;
+  static constexpr int THREADS = 32 * (W8 ? kConvWarp + kConvThreads / 32 : kConvWarp);
+  // registers of the softmax warps and of the others, out of what the launch gives every warp
+  static constexpr int SOFT_REGS = W8 ? 184 : 208, REGS = W8 ? 72 : 88;
+  static constexpr int TILE = kTok * D * 2;       // K (or V) of a tile in MMA form
+  static constexpr int NK = 64 * 1024 / TILE, NV = NK;
+  static constexpr int RAW = kTok / 2 * D;        // codes of half a tile's K or V
+  static constexpr int NR = W8 ? (D == 128 ? 3 : 8) : 0;
+  static constexpr int OFF_V = NK * TILE;
+  static constexpr int OFF_RAW = OFF_V + NV * TILE;
+  static constexpr int OFF_Q = OFF_RAW + NR * RAW;
+  static constexpr int Q_GROUP = kGroupThreads * D * 2;
+  static constexpr int OFF_ML = OFF_Q + 2 * Q_GROUP;               // [2][128] (max, sum)
+  static constexpr int OFF_BAR = OFF_ML + kSoftThreads * 8;
+  static constexpr int BARS = 2 * NK + 2 * NV + 2 * NR + 2 * 4 + 3 + kRuns;
+  static_assert(NK + (NR + 3) / 4 + 3 <= kRuns, "runs in flight");
+  static constexpr int OFF_MISC = OFF_BAR + 8 * BARS;              // masks, bad rows, TMEM address
+  static constexpr uint32_t IDESC_S = tc_idesc(128, kTok, false, W8);
+  static constexpr uint32_t IDESC_PV = tc_idesc(128, D, true, W8);
+  static constexpr int SMEM = 1024 + OFF_MISC + 4 * (NV + NR + 2 * kEdgeTiles * 4 + 1) + 16;
+  static_assert(SMEM <= 225 * 1024 && SMEM > 114 * 1024, "one CTA per SM");
+};
+
+// A place in a ring of N stages and the parity of its current use.
+template <int N>
+struct Place {
+  int st = 0;
+  uint32_t par = 0;
+  __device__ __forceinline__ void advance(int k) {  // k <= N
+    st += k;
+    if (st >= N) {
+      st -= N;
+      par ^= 1u;
+    }
+  }
+  __device__ __forceinline__ void skip(int k) {  // any k
+    const int t = st + k, w = t / N;
+    st = t - w * N;
+    par ^= (uint32_t)w & 1u;
+  }
+};
+
+template <int N>
+__device__ __forceinline__ void regs_up() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_down() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+template <bool F16>
+__device__ __forceinline__ uint32_t pack_p(float a, float b) {
+  return F16 ? pack_f16(a, b) : pack_bf16(a, b);
+}
+
+// Whether a 16-bit value (bits of the MMA input type) is infinite or NaN.
+template <bool F16>
+__device__ __forceinline__ bool not_finite(uint32_t h) {
+  constexpr uint32_t E = F16 ? 0x7c00u : 0x7f80u;
+  return (h & E) == E;
+}
+
+// z + 0 w for the two 16-bit values of a word: NaN from the first infinite or NaN one on.
+template <bool F16>
+__device__ __forceinline__ uint32_t add_zero_times(uint32_t w, uint32_t z) {
+  uint32_t r;
+  if constexpr (F16)
+    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(w), "r"(0u), "r"(z));
+  else
+    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(w), "r"(0u), "r"(z));
+  return r;
+}
+
+// tanh x = 1 - 2 / (1 + e^{2x}): off by at most some 2^-22, with the exact limits at infinities.
+__device__ __forceinline__ float tanh_of(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + ex2_approx(2.f * kLog2e * x)));
+  return fmaf(-2.f, r, 1.f);
+}
+
+// FORM: scores are capped or have a bias (otherwise they are the products, scaled).
+template <typename KV, int D, bool FORM>
+__global__ void __launch_bounds__(TcShape<KV, D>::THREADS, 1) chunk_tc_kernel(
+    const ChunkArgs a, const __grid_constant__ CUtensorMap tm_k,
+    const __grid_constant__ CUtensorMap tm_v) {
+  using S = TcShape<KV, D>;
+  constexpr bool W8 = S::W8;
+  constexpr int NK = S::NK, NV = S::NV, NR = S::NR;
+  constexpr int PAGE_MMA = kPageSize * D * 2;  // V bytes of a page in MMA form
+  constexpr int PAGE_RAW = kPageSize * D;
+  const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
+
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t ring = smem_u32(smem);
+  uint64_t* full_k = reinterpret_cast<uint64_t*>(smem + S::OFF_BAR);  // [NK] K of a tile is there
+  uint64_t* free_k = full_k + NK;                                    // [NK] its S done
+  uint64_t* full_v = free_k + NK;                                    // [NV] V of a tile is there
+  uint64_t* free_v = full_v + NV;                                    // [NV] its P V done
+  uint64_t* raw_full = free_v + NV;                                  // [NR] codes arrived
+  uint64_t* raw_freed = raw_full + NR;                               // [NR] codes in registers
+  uint64_t* s_done = raw_freed + NR;                                 // [2] S of a group's step
+  uint64_t* p_ready = s_done + 2;                                    // [2] its P
+  uint64_t* o_done = p_ready + 2;                                    // [2] a group's last P V of a run
+  uint64_t* q_ready = o_done + 2;                                    // [2] Q of a run stored
+  uint64_t* met = q_ready + 2;         // both groups ended a run
+  uint64_t* parted = met + 1;          // and are done with what the other reads or writes
+  uint64_t* mma_idle = parted + 1;
+  uint64_t* run_there = mma_idle + 1;  // [kRuns]
+  int* page_mask = reinterpret_cast<int*>(smem + S::OFF_MISC);       // [NV] good pages of the tile
+  int* raw_mask = page_mask + NV;                                    // [NR] of the half tile
+  uint32_t* bad_rows = reinterpret_cast<uint32_t*>(raw_mask + NR);   // [2][edge tile][4]: not finite
+  uint32_t* s_taddr = bad_rows + 2 * kEdgeTiles * 4;
+  float2* ml = reinterpret_cast<float2*>(smem + S::OFF_ML);
+
+  __shared__ int scratch[64];
+  __shared__ ChunkShare share;
+  __shared__ ChunkRun runs[kRuns];  // (n = 0: the share's end)
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (threadIdx.x == kCopyWarp * 32) {
+    for (int s = 0; s < NK; ++s) {
+      mbar_init(&full_k[s], W8 ? kConvThreads / 32 : 1);
+      mbar_init(&free_k[s], 1);
+    }
+    for (int s = 0; s < NV; ++s) {
+      mbar_init(&full_v[s], W8 ? kConvThreads / 32 : 1);
+      mbar_init(&free_v[s], 1);
+    }
+    for (int s = 0; s < NR; ++s) {
+      mbar_init(&raw_full[s], 1);
+      mbar_init(&raw_freed[s], kConvThreads / 32);
+    }
+    for (int g = 0; g < 2; ++g) {
+      mbar_init(&s_done[g], 1);
+      mbar_init(&p_ready[g], kGroupThreads / 32);
+      mbar_init(&o_done[g], 1);
+      mbar_init(&q_ready[g], kGroupThreads / 32);
+    }
+    mbar_init(met, kSoftThreads / 32);
+    mbar_init(parted, kSoftThreads / 32);
+    mbar_init(mma_idle, 1);
+    for (int i = 0; i < kRuns; ++i) mbar_init(&run_there[i], 1);
+    mbar_fence_init();
+    if constexpr (!W8) {
+      asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm_k)) : "memory");
+      asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm_v)) : "memory");
+    }
+  }
+  if (threadIdx.x < 2 * kEdgeTiles * 4) bad_rows[threadIdx.x] = 0;
+  chunk_share<S::THREADS>(a, scratch, &share);
+  if (share.count == 0) {  // (the whole CTA)
+    if (threadIdx.x == 0)
+      static_cast<ChunkRecord*>(a.ws_rec)[blockIdx.x] = ChunkRecord{0, 1, 0, 0};
+    return;
+  }
+  if (warp == kMmaWarp) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_u32(s_taddr)),
+                 "r"(kTmemCols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = (uint32_t)uniform((int)*s_taddr);
+  // run i of the share, or nullptr after the last (or a wait that gave up)
+  auto get_run = [&](uint32_t i) -> const ChunkRun* {
+    const bool got = mbar_wait(&run_there[i % kRuns], (i / kRuns) & 1u, a.err);
+    const ChunkRun* r = &runs[i % kRuns];
+    return __all_sync(0xffffffffu, got && r->n > 0) ? r : nullptr;
+  };
+  // Steps of a run: wide (more than 128 rows): step u is tile u / 2 for group u % 2, otherwise tile u
+  // for group u % 2. Every barrier of a group completes once per step of its own.
+  auto is_wide = [](const ChunkRun* run) { return uniform(run->rows) > kGroupThreads; };
+
+  if (warp >= kMmaWarp && warp < kConvWarp) {
+    regs_down<S::REGS>();
+    if (warp == kCopyWarp || (!W8 && warp == kCopyWarp + 1)) {
+      // ===================== copies: the share's tiles, in order =====================
+      const bool is_k = warp == kCopyWarp;
+      const uint64_t once = l2_evict_first_policy(), again = l2_evict_last_policy();
+      const int stages = W8 ? NR : is_k ? NK : NV;
+      uint64_t* const there = W8 ? raw_full : is_k ? full_k : full_v;
+      uint64_t* const gone = W8 ? raw_freed : is_k ? free_k : free_v;
+      const uint32_t ring0 = ring + (is_k ? 0 : S::OFF_V);
+      int st = 0, issued = 0;
+      uint32_t par = 0;
+      bool ok = true;
+      ChunkWalk walk(a, share);
+      ChunkRecord record{0, 1, 0, 0};
+      for (uint32_t unit = 0;; ++unit) {
+        const ChunkRun* run = nullptr;
+        if (is_k) {  // (a wait that gave up ends the share for every warp)
+          ChunkRun* r = &runs[unit % kRuns];
+          if (lane == 0) {
+            if (!ok || !walk.next(a, *r)) r->n = 0;
+            mbar_arrive(&run_there[unit % kRuns]);
+          }
+          __syncwarp();
+          if (r->n > 0) run = r;
+          if (run && !run->whole && run->slot == 1)
+            record = ChunkRecord{(int)chunk_row(a, *run, 0), run->heads, run->rows, run->shares};
+        } else if (ok) {
+          run = get_run(unit);
+        }
+        if (!run) break;
+        const int n = uniform(run->n), j = uniform(run->j), i0 = uniform(run->i0);
+        const ChunkTiles tiles{0, uniform(run->tiles.sinks), uniform(run->tiles.first)};
+        const int first = uniform(run->req.base + run->t0), ctx = uniform(run->req.base + run->req.n);
+        const int32_t* table = a.block_tables + (size_t)uniform(run->b) * a.max_pages;
+        // later units of the request read the same rows again
+        const uint64_t pol = uniform(run->req.n) > a.unit_tokens ? again : once;
+        // lane p: the id of page p of a tile; -1 where it is not read, -2 where it is but has no id
+        auto page_of = [&](int i) {
+          const int lp = tiles[i0 + i] * kPages + (lane & (kPages - 1)), p0 = lp * kPageSize;
+          // (a page outside every row's window may have been given back: it is not read)
+          if (i >= n || p0 >= ctx || (a.window > 0 && p0 >= a.sink &&
+                                      p0 + kPageSize <= first + 1 - a.window))
+            return -1;
+          const int id = table[lp];
+          return id >= 0 && id < a.num_pages ? id : -2;
+        };
+        int next = page_of(0);
+        for (int i = 0; i < n; ++i) {
+          const int mine = next;
+          next = page_of(i + 1);
+          int id[kPages];
+          const uint32_t mask = __ballot_sync(0xffffffffu, mine >= 0) & ((1u << kPages) - 1);
+          if (is_k && __any_sync(0xffffffffu, mine == -2) && lane == 0)
+            atomicOr(a.err, PKV_DEVERR_BAD_PAGE);
+#pragma unroll
+          for (int p = 0; p < kPages; ++p) id[p] = __shfl_sync(0xffffffffu, mine, p);
+          // a stage: a bf16 tile of K or V, or the codes of half of one (K, K, V, V)
+#pragma unroll 1
+          for (int part = 0; part < (W8 ? 4 : 1); ++part) {
+            if (issued >= stages) {
+              ok = __all_sync(0xffffffffu, mbar_wait(&gone[st], par ^ 1u, a.err));
+              if (!ok) break;
+            }
+            if (elect_one()) {
+              if constexpr (W8) {
+                constexpr int HALF = kPages / 2;
+                const uint32_t m = (mask >> ((part & 1) * HALF)) & ((1u << HALF) - 1);
+                raw_mask[st] = (int)m;
+                fence_proxy_async_smem();
+                mbar_arrive_expect_tx(&there[st], __popc(m) * PAGE_RAW);
+                const uint8_t* pool = static_cast<const uint8_t*>(part < 2 ? a.k_cache : a.v_cache);
+#pragma unroll
+                for (int p = 0; p < HALF; ++p) {
+                  const int page = part & 1 ? id[HALF + p] : id[p];
+                  if ((m >> p) & 1)
+                    bulk_g2s(smem + S::OFF_RAW + st * S::RAW + p * PAGE_RAW,
+                             pool + ((int64_t)page * a.h_kv + j) * PAGE_RAW, PAGE_RAW, &there[st],
+                             pol);
+                }
+              } else {
+                if (!is_k) page_mask[st] = (int)mask;
+                mbar_arrive_expect_tx(&there[st], __popc(mask) * PAGE_MMA);
+                const uint32_t dst = ring0 + st * S::TILE;
+#pragma unroll
+                for (int p = 0; p < kPages; ++p) {
+                  if (!((mask >> p) & 1)) continue;
+                  const int row = (id[p] * a.h_kv + j) * kPageSize;
+                  if (is_k) {  // 64-dim blocks of all 128 rows (one N = 128 operand)
+#pragma unroll
+                    for (int bx = 0; bx < D / 64; ++bx)
+                      tma_load_2d(dst + bx * (kTok * 128) + p * 2048, &tm_k, bx * 64, row,
+                                  &there[st], pol);
+                  } else {  // a block per page (K = 16)
+                    tma_tile<D / 64, 64>(dst + p * PAGE_MMA, &tm_v, a.tma_rank, row, &there[st],
+                                         pol);
+                  }
+                }
+              }
+            }
+            __syncwarp();
+            if (++st == stages) {
+              st = 0;
+              par ^= 1u;
+            }
+            ++issued;
+          }
+          if (!ok) break;
+        }
+      }
+      if (is_k && lane == 0) static_cast<ChunkRecord*>(a.ws_rec)[blockIdx.x] = record;
+      if (lane == 0)  // before leaving, every copy issued has landed
+        for (int t = max(0, issued - stages); t < issued; ++t)
+          mbar_wait(&there[t % stages], (uint32_t)(t / stages) & 1u, a.err);
+    } else if (warp == kMmaWarp) {
+      // ===================== MMAs (one elected lane issues) =====================
+      // They run in the order of their issue: an S overwrites a P after the P V before it.
+      const uint64_t k_desc = tc_desc(ring, 16, 1024), v_desc = tc_desc(ring + S::OFF_V, 2048, 1024);
+      const uint64_t q_desc = tc_desc(ring + S::OFF_Q, 16, 1024);
+      bool ok = true;
+      uint32_t ph_p = 0;  // parities of p_ready's next phase, bit g
+      Place<NK> ks;       // K of the next S
+      Place<NV> vs;       // V of the next P V
+      auto wait = [&](uint64_t* bar, uint32_t par) {
+        const bool got = __all_sync(0xffffffffu, mbar_wait(bar, par, a.err));
+        tc_fence_after();
+        return got;
+      };
+      auto s_mma = [&](int group, bool last_use) {
+        const uint64_t kd = k_desc + (uint32_t)(ks.st * (S::TILE >> 4));
+        const uint64_t qd = q_desc + (uint32_t)(group * (S::Q_GROUP >> 4));
+        const uint32_t d = tmem + 256 + 128 * group;
+        if (elect_one()) {
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t at = ((kk >> 2) * (kTok * 128) + (kk & 3) * 32) >> 4;
+            tc_mma_sa(d, qd + at, kd + at, S::IDESC_S, kk > 0 ? 1u : 0u);
+          }
+          tc_commit(&s_done[group]);
+          if (last_use) tc_commit(&free_k[ks.st]);
+        }
+        __syncwarp();
+        if (last_use) ks.advance(1);
+      };
+      static_assert(kTok == kGroupThreads, "Q and K tiles have one form");
+      auto pv_mma = [&](int group, bool first, bool last_use, bool last_step) {
+        const uint64_t vd = v_desc + (uint32_t)(vs.st * (S::TILE >> 4));
+        const uint32_t pc = tmem + 256 + 128 * group, o = tmem + 128 * group;
+        if (elect_one()) {
+#pragma unroll
+          for (int kk = 0; kk < kPages; ++kk)
+            tc_mma_ta(o, pc + 8 * kk, vd + ((kk * PAGE_MMA) >> 4), S::IDESC_PV,
+                      first && kk == 0 ? 0u : 1u);
+          if (last_use) tc_commit(&free_v[vs.st]);
+          if (last_step) tc_commit(&o_done[group]);
+        }
+        __syncwarp();
+        if (last_use) vs.advance(1);
+      };
+      for (uint32_t unit = 0; ok; ++unit) {
+        const ChunkRun* run = get_run(unit);
+        if (!run) break;
+        const bool wide = is_wide(run);
+        const int n = wide ? 2 * uniform(run->n) : uniform(run->n);
+        auto step_s = [&](int u) {  // S of step u; in a run's first two steps the queries are waited for
+          const int group = u & 1;
+          if (u < 2) ok = wait(&q_ready[group], unit & 1);
+          if (ok && (!wide || group == 0)) ok = wait(&full_k[ks.st], ks.par);
+          if (ok) s_mma(group, !wide || group == 1);
+        };
+        step_s(0);
+        if (ok && n > 1) step_s(1);
+        for (int u = 0; ok && u < n; ++u) {
+          const int group = u & 1;
+          ok = wait(&p_ready[group], (ph_p >> group) & 1u);
+          ph_p ^= 1u << group;
+          if (ok && (!wide || group == 0)) ok = wait(&full_v[vs.st], vs.par);
+          if (ok) pv_mma(group, u < 2, !wide || group == 1, u + 2 >= n);
+          if (ok && u + 2 < n) step_s(u + 2);
+        }
+      }
+      if (elect_one()) tc_commit(mma_idle);  // before leaving, every MMA issued is complete
+      __syncwarp();
+      wait(mma_idle, 0);
+    }
+  } else if (warp >= kConvWarp) {
+    // ===================== 8-bit codes to f16 in MMA form =====================
+    if constexpr (W8) {
+      regs_down<S::REGS>();
+      constexpr int CPR = D / 16;                          // 16-code chunks of a row
+      constexpr int PER = kTok / 2 * CPR / kConvThreads;   // chunks of a thread in half a tile
+      const int i0 = threadIdx.x - kConvWarp * 32;
+      // a thread's chunks are PER rows, ROWS rows apart. Eight threads read and write distinct banks:
+      // four chunks each of two rows.
+      constexpr int ROWS = kConvThreads / CPR;
+      int row0, c;
+      if constexpr (CPR == 8) {
+        row0 = 2 * (i0 >> 4) + ((i0 >> 2) & 1);
+        c = (i0 & 3) + 4 * (((i0 >> 2) ^ (i0 >> 3)) & 1);
+      } else {
+        row0 = i0 >> 2;
+        c = i0 & 3;
+      }
+      const int ch = 2 * c;  // 16-byte chunks ch and ch + 1 of the row's f16
+      const uint32_t x0 = ((ch & 7) ^ (row0 & 7)) << 4, x1 = (((ch & 7) + 1) ^ (row0 & 7)) << 4;
+      static_assert(ROWS % 8 == 0, "a thread's rows share their swizzle");
+      const uint32_t src0 = ring + S::OFF_RAW + row0 * D + c * 16;
+      const uint32_t k0 = ring + (ch >> 3) * (kTok * 128) + row0 * 128;
+      const uint32_t v0 = ring + S::OFF_V + (ch >> 3) * 2048;
+      Place<W8 ? NR : 1> raw;
+      Place<NK> pk;
+      Place<NV> pv;
+      bool ok = true;
+      int t = 0, end = 0;  // tiles done, tiles of the runs so far
+      uint32_t unit = 0;
+      for (;; ++t, pk.advance(1), pv.advance(1)) {
+        if (t == end) {
+          const ChunkRun* run = get_run(unit++);
+          if (!run) break;
+          end += run->n;
+        }
+        int mask = 0;
+#pragma unroll
+        for (int part = 0; part < 4; ++part) {  // K, K, V, V
+          ok = mbar_wait(&raw_full[raw.st], raw.par, a.err);
+          if (!ok) break;
+          const uint32_t src = src0 + raw.st * S::RAW;
+          if (part >= 2) mask |= raw_mask[raw.st] << ((part & 1) * (kPages / 2));
+          uint4 w[PER];
+#pragma unroll
+          for (int i = 0; i < PER; ++i) w[i] = lds128(src + i * ROWS * D);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&raw_freed[raw.st]);
+          raw.advance(1);
+          if (part == 0 && t >= NK) ok = mbar_wait(&free_k[pk.st], pk.par ^ 1u, a.err);
+          if (part == 2 && t >= NV) ok = mbar_wait(&free_v[pv.st], pv.par ^ 1u, a.err);
+          if (!ok) break;
+#pragma unroll
+          for (int i = 0; i < PER; ++i) {
+            const int r = (part & 1) * (kTok / 2) + i * ROWS;  // row of the tile, less row0
+            const int rv = r + row0;
+            const uint32_t at = part < 2 ? k0 + pk.st * S::TILE + r * 128
+                                         : v0 + pv.st * S::TILE + (rv >> 4) * PAGE_MMA +
+                                               (rv & 15) * 128;
+            uint4 lo, hi;
+            widen4<KV>(w[i].x, lo.x, lo.y);
+            widen4<KV>(w[i].y, lo.z, lo.w);
+            widen4<KV>(w[i].z, hi.x, hi.y);
+            widen4<KV>(w[i].w, hi.z, hi.w);
+            sts128(at + x0, lo);
+            sts128(at + x1, hi);
+          }
+          if (part & 1) {
+            if (part == 3 && i0 == 0) page_mask[pv.st] = mask;
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(part == 1 ? &full_k[pk.st] : &full_v[pv.st]);
+          }
+        }
+        if (!ok) break;
+      }
+    }
+  } else {
+    // ===================== softmax =====================
+    regs_up<S::SOFT_REGS>();
+    const int wg = warp >> 2;             // group
+    const int r = threadIdx.x & 127;      // row of the group
+    const uint32_t lane_t = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+    const uint32_t scol = lane_t + 256 + 128 * wg, ocol = lane_t + 128 * wg;
+    bool ok = true;
+    uint32_t unit = 0, ph_s = 0, ph_o = 0;  // parities of s_done's and o_done's next phases
+    Place<NV> base;                         // V of the run's first tile
+    // The row of this thread in a run (row `row` of its unit, at position pq), its offset in q and
+    // out in rows, and its score factor (log2 domain).
+    struct Row {
+      int row, pq;
+      size_t at;
+      bool live;
+      float sc, slope;
+    };
+    auto find_row = [&](const ChunkRun& run) {
+      Row x;
+      x.row = (run.rows > kGroupThreads ? wg * kGroupThreads : 0) + r;
+      x.live = x.row < run.rows;
+      const unsigned R = x.live ? x.row : 0, t = R / (unsigned)run.heads;
+      x.pq = run.req.base + run.t0 + (int)t;
+      x.at = chunk_row(a, run, (int)R);
+      x.sc = a.scale * kLog2e * (W8 ? a.k_scales[run.j] : 1.f);
+      x.slope = FORM && a.slopes ? a.slopes[run.j * a.group + run.g0 + R - t * run.heads] * kLog2e : 0.f;
+      return x;
+    };
+    // A run's queries: four lanes read 64 consecutive bytes of a row, eight rows an instruction, and
+    // put them into shared memory in MMA form once the S of the last run are done.
+    constexpr int RND = D / 32;  // rounds of 64 bytes
+    auto load_query = [&](const Row& x, uint4 (&in)[RND][4]) {
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const int from = 8 * g + (lane >> 2);
+        const size_t at = __shfl_sync(0xffffffffu, (unsigned long long)x.at, from);
+        const bool there = __shfl_sync(0xffffffffu, (int)x.live, from) != 0;
+        const uint4* src = reinterpret_cast<const uint4*>(
+                               static_cast<const __nv_bfloat16*>(a.q) + at * D) + (lane & 3);
+#pragma unroll
+        for (int d = 0; d < RND; ++d) in[d][g] = there ? src[4 * d] : make_uint4(0, 0, 0, 0);
+      }
+    };
+    auto store_query = [&](Row& x, uint4 (&in)[RND][4]) {
+      if constexpr (W8) {  // f16, scaled by a row's 2^e (the four lanes that hold a row agree)
+        const float sc = x.sc;
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          uint32_t lo = 0, hi = 0;  // largest |q| as bits (bf16 magnitudes order like integers)
+#pragma unroll
+          for (int d = 0; d < RND; ++d) {
+            const uint32_t* w = &in[d][g].x;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              lo = max(lo, w[k] & 0x7fffu);
+              hi = max(hi, w[k] & 0x7fff0000u);
+            }
+          }
+          uint32_t mx = max(lo, hi >> 16);
+          mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+          mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+          const int ex = mx >> 7;  // biased exponent: mx 2^e in [2^14, 2^15), none for 0, inf, NaN
+          const int e = mx != 0 && ex < 255 ? min(126, max(-126, 141 - ex)) : 0;
+          // the factor of the scores stays positive, and at least the smallest normal number (an
+          // unseen score of -inf must stay one): a K scale's sign, or a NaN one, is in the query
+          const float two_e = __int_as_float((127 + e) << 23);
+          const float up = sc < 0.f ? -two_e : sc == sc ? two_e : sc;
+          const float of = fmaxf(fabsf(sc) * __int_as_float((127 - e) << 23), 0x1p-126f);
+          const float mine = __shfl_sync(0xffffffffu, of, 4 * (lane & 7));
+          if ((lane >> 3) == g) x.sc = mine;
+#pragma unroll
+          for (int d = 0; d < RND; ++d) {
+            uint32_t* w = &in[d][g].x;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) w[k] = pack_f16(bf16lo(w[k]) * up, bf16hi(w[k]) * up);
+          }
+        }
+      }
+      const int row0 = (warp & 3) * 32 + (lane >> 2);  // rows row0 + 8 g of the group
+      const uint32_t at = ring + S::OFF_Q + wg * S::Q_GROUP + row0 * 128;
+#pragma unroll
+      for (int d = 0; d < RND; ++d) {
+        const uint32_t ch = (((4 * d & 7) + (lane & 3)) ^ (row0 & 7)) << 4;
+#pragma unroll
+        for (int g = 0; g < 4; ++g)
+          sts128(at + (d >> 1) * (kGroupThreads * 128) + g * 1024 + ch, in[d][g]);
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&q_ready[wg]);
+    };
+    Row me{};
+    const ChunkRun* next = get_run(0);
+    if (next) {
+      uint4 in[RND][4];
+      me = find_row(*next);
+      load_query(me, in);
+      store_query(me, in);
+    }
+    for (; next; ++unit) {
+      const ChunkRun& run = *next;
+      const bool wide = run.rows > kGroupThreads;
+      const bool live = me.live;
+      const float sc = me.sc;
+      const int ctx = run.req.base + run.req.n;
+      const int stride = wide ? 1 : 2;  // tiles between this group's steps
+      uint32_t* const bad = bad_rows + (unit & 1) * (kEdgeTiles * 4);
+      float m_used = -INFINITY, l = 0.f;
+      Place<NV> at = base;
+      if (!wide) at.advance(wg);
+      const int i_first = wide ? 0 : wg;
+      const bool any = i_first < run.n;  // the group has a step in the run
+      for (int i = i_first; ok && i < run.n; i += stride) {
+        const int p0 = run.tiles[run.i0 + i] * kTok;
+        // V of the tile too: what it says of its pages, and rows of it may have to be mended
+        ok = mbar_wait(&full_v[at.st], at.par, a.err) && mbar_wait(&s_done[wg], ph_s, a.err);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        ph_s ^= 1u;
+        const int mask = page_mask[at.st];
+        tc_fence_after();
+        uint32_t sr[kTok];
+#pragma unroll
+        for (int c = 0; c < kTok; c += 32)
+          tmem_ld32(scol + c, *reinterpret_cast<uint32_t(*)[32]>(&sr[c]));
+        tmem_wait_ld();
+        if constexpr (FORM) {  // the scores themselves, log2 domain
+          const bool cap = a.softcap > 0.f;
+          const float in = cap ? sc * (kLn2 / a.softcap) : sc, top = a.softcap * kLog2e;
+          // (distances of two positions side by side: pairs)
+          const float far0 = (float)(p0 - me.pq);
+#pragma unroll
+          for (int k = 0; k < kTok; ++k) {
+            float x = __uint_as_float(sr[k]) * in;
+            if (cap) x = top * tanh_of(x);
+            sr[k] = __float_as_uint(fmaf(me.slope, far0 + (float)k, x));
+          }
+        }
+        const bool edge = chunk_edge(a, run, p0, kTok);
+        if (edge || mask != (1 << kPages) - 1) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            uint64_t seen = live ? chunk_seen(a, me.pq, p0 + 64 * h) : 0ull;
+#pragma unroll
+            for (int p = 0; p < 4; ++p)
+              if (!((mask >> (4 * h + p)) & 1)) seen &= ~(0xffffull << (16 * p));
+#pragma unroll
+            for (int k = 0; k < 64; ++k)
+              if (!((seen >> k) & 1)) sr[64 * h + k] = __float_as_uint(-INFINITY);
+          }
+          // Mend V, a thread to a row. In a wide unit both groups do (and write every row they mend):
+          // each group's P V waits for its own group only.
+          constexpr int CH = D / 8;  // 16-byte chunks of a row
+          const uint32_t vrow =
+              ring + S::OFF_V + at.st * S::TILE + (r >> 4) * PAGE_MMA + (r & 15) * 128;
+          auto chunk_at = [&](int c) { return vrow + (c >> 3) * 2048 + (((c & 7) ^ (r & 7)) << 4); };
+          if (p0 + r >= ctx || !((mask >> (r >> 4)) & 1)) {
+#pragma unroll
+            for (int c = 0; c < CH; ++c) sts128(chunk_at(c), make_uint4(0, 0, 0, 0));
+          } else if (KV::code != PKV_INT8 && edge) {
+            uint32_t z = 0;
+#pragma unroll
+            for (int c = 0; c < CH; ++c) {
+              const uint4 x = lds128(chunk_at(c));
+              z = add_zero_times<W8>(x.x, z);
+              z = add_zero_times<W8>(x.y, z);
+              z = add_zero_times<W8>(x.z, z);
+              z = add_zero_times<W8>(x.w, z);
+            }
+            if (not_finite<W8>(z) || not_finite<W8>(z >> 16)) {
+#pragma unroll 1
+              for (int c = 0; c < CH; ++c) {
+                uint4 x = lds128(chunk_at(c));
+                uint32_t* w = &x.x;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                  if (not_finite<W8>(w[k])) w[k] &= 0xffff0000u;
+                  if (not_finite<W8>(w[k] >> 16)) w[k] &= 0xffffu;
+                }
+                sts128(chunk_at(c), x);
+              }
+              int e = 0;  // which of the run's edge tiles this is
+              for (int k = 0; k < i; ++k)
+                e += chunk_edge(a, run, run.tiles[run.i0 + k] * kTok, kTok) ? 1 : 0;
+              if (e < kEdgeTiles) atomicOr(&bad[4 * e + (r >> 5)], 1u << (r & 31));
+            }
+          }
+          fence_proxy_async_smem();
+        }
+        float mx4[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) mx4[k] = __uint_as_float(sr[k]);
+#pragma unroll
+        for (int k = 4; k < 124; k += 8) {
+#pragma unroll
+          for (int m = 0; m < 4; ++m)
+            mx4[m] = max3(mx4[m], __uint_as_float(sr[k + 2 * m]), __uint_as_float(sr[k + 2 * m + 1]));
+        }
+        float mx = max3(max3(mx4[0], mx4[1], mx4[2]),
+                        max3(mx4[3], __uint_as_float(sr[124]), __uint_as_float(sr[125])),
+                        fmaxf(__uint_as_float(sr[126]), __uint_as_float(sr[127])));
+        if constexpr (!FORM) mx *= sc;
+        // s sc - m is one FMA below: m is a rounded product, the product in the FMA is not, so that a row's
+        // weights are all off by one factor, which their sum shares: up to 2^0.5 for |m| <= 2^24. For
+        // larger m it would soon leave f16's range and then every range: there s sc is rounded as m is.
+        // (A tile that counts has its maximum near m.)
+        const bool huge = !FORM && fabsf(mx) > 0x1p24f && mx != -INFINITY;
+        // The reference maximum that P and O are scaled by: the first tile's maximum, then moved only
+        // past 2^8 (the difference, not a sum: past 2^26 that would round to several times as far).
+        const bool first = i == i_first;
+        const bool moved = !first && mx - m_used > kLazyLog2;
+        if (__any_sync(0xffffffffu, moved || huge)) {  // (one vote for the two: most steps have neither)
+          if (__any_sync(0xffffffffu, moved)) {
+            // rescale this warp's rows of O: this step's S was issued after the last P V, and is there
+            const float m_new = moved ? mx : m_used;
+            const float alpha = moved ? exp2f(m_used - m_new) : 1.f;
+#pragma unroll
+            for (int cb = 0; cb < D / 32; ++cb) {
+              uint32_t o[32];
+              tmem_ld32(ocol + 32 * cb, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
+              tmem_st32(ocol + 32 * cb, o);
+            }
+            l *= alpha;
+            m_used = m_new;
+          }
+          if (__any_sync(0xffffffffu, huge)) {
+#pragma unroll
+            for (int k = 0; k < kTok; ++k)
+              sr[k] = __float_as_uint(__fmul_rn(__uint_as_float(sr[k]), sc));
+          }
+        }
+        if (first) m_used = mx;
+        const float factor = FORM || __any_sync(0xffffffffu, huge) ? 1.f : sc;
+        // P = 2^(s - m) over the first 64 columns of S
+        const float m_use = m_used == -INFINITY ? 0.f : m_used;
+        uint64_t sum[4] = {0, 0, 0, 0};  // (pairs of zeros)
+        const uint64_t sc2 = pack2(factor, factor), m2 = pack2(-m_use, -m_use);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint32_t pw[32];
+#pragma unroll
+          for (int k = 0; k < 32; ++k) {
+            float e0, e1;
+            unpack2(fma2(pack2(__uint_as_float(sr[64 * h + 2 * k]),
+                               __uint_as_float(sr[64 * h + 2 * k + 1])), sc2, m2),
+                    e0, e1);
+            e0 = ex2_approx(e0);
+            e1 = ex2_approx(e1);
+            sum[k & 3] = add2(sum[k & 3], pack2(e0, e1));
+            pw[k] = pack_p<W8>(e0, e1);
+          }
+          tmem_st32(scol + 32 * h, pw);
+        }
+        float s0, s1;
+        unpack2(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), s0, s1);
+        l += s0 + s1;
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();  // (one arrival per warp: arrivals on one barrier go one by one)
+        if (lane == 0) mbar_arrive(&p_ready[wg]);
+        at.advance(stride);
+      }
+      // ---- the run's rows ----
+      // the next run's queries first, so that its first scores run while this one's rows are written
+      next = get_run(unit + 1);
+      Row then{};
+      if (next) {
+        uint4 in[RND][4];
+        then = find_row(*next);
+        load_query(then, in);
+        store_query(then, in);
+      }
+      if (ok && any) {
+        ok = mbar_wait(&o_done[wg], ph_o, a.err);
+        ok = __all_sync(0xffffffffu, ok);
+      }
+      if (any) ph_o ^= 1u;
+      if (!wide) ml[wg * kGroupThreads + r] = make_float2(m_used, l);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(met);
+      ok = mbar_wait(met, unit & 1, a.err) && ok;
+      ok = __all_sync(0xffffffffu, ok);
+      tc_fence_after();
+      if (threadIdx.x < kEdgeTiles * 4) bad_rows[((unit + 1) & 1) * (kEdgeTiles * 4) + threadIdx.x] = 0;
+      // wide: the group's own rows, all dims; else group wg writes dims wg D/2 .. of every row, from
+      // both groups' sums
+      float M = m_used, L = l, w0 = 1.f, w1 = 0.f;
+      if (!wide) {
+        const float2 x = ml[r], y = ml[kGroupThreads + r];
+        M = fmaxf(x.x, y.x);
+        const float Mu = M == -INFINITY ? 0.f : M;
+        w0 = exp2f(x.x - Mu);
+        w1 = exp2f(y.x - Mu);
+        L = w0 * x.y + w1 * y.y;
+      }
+      const float vs = W8 ? a.v_scales[run.j] : 1.f;
+      const float f = run.whole ? (L != 0.f ? vs / L : 0.f) : vs;
+      uint32_t any_bad = 0;
+#pragma unroll
+      for (int k = 0; k < kEdgeTiles * 4; ++k) any_bad |= bad[k];
+      const size_t part = ((size_t)blockIdx.x * 2 + run.slot) * kChunkTcRows + me.row;
+      auto emit = [&](int c, uint32_t (&o)[32]) {  // 32 dims from c on of this thread's row
+        if (any_bad && live) {  // the infinite and NaN values of the positions this row sees
+          int e = 0;
+          for (int k = 0; k < run.n && e < kEdgeTiles; ++k) {
+            const int q0 = run.tiles[run.i0 + k] * kTok;
+            if (!chunk_edge(a, run, q0, kTok)) continue;
+            for (int x = 0; x < kTok; ++x) {
+              const int pos = q0 + x;
+              if (!((bad[4 * e + (x >> 5)] >> (x & 31)) & 1) || !(chunk_seen(a, me.pq, pos) & 1))
+                continue;
+              const int id = a.block_tables[(size_t)run.b * a.max_pages + pos / kPageSize];
+              const uint8_t* v =
+                  static_cast<const uint8_t*>(a.v_cache) +
+                  ((((int64_t)id * a.h_kv + run.j) * kPageSize + pos % kPageSize) * D + c) * KV::bytes;
+#pragma unroll
+              for (int d = 0; d < 32; d += 4) {
+                float y[4];
+                RowLoad<KV, 4>::run(v + d * KV::bytes, y);
+#pragma unroll
+                for (int m = 0; m < 4; ++m)
+                  if (!(fabsf(y[m]) < INFINITY))
+                    o[d + m] = __float_as_uint(__uint_as_float(o[d + m]) + y[m]);
+              }
+            }
+            ++e;
+          }
+        }
+        if (!live) return;
+        if (run.whole) {
+          uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + me.at * D + c);
+#pragma unroll
+          for (int k = 0; k < 32; k += 8) {
+            uint32_t v[4];
+#pragma unroll
+            for (int m = 0; m < 4; ++m)
+              v[m] = L != 0.f ? pack_bf16(__uint_as_float(o[k + 2 * m]) * f,
+                                          __uint_as_float(o[k + 2 * m + 1]) * f)
+                              : 0u;
+            dst[k / 8] = make_uint4(v[0], v[1], v[2], v[3]);
+          }
+        } else {
+          float4* dst = reinterpret_cast<float4*>(a.ws_acc + part * D + c);
+#pragma unroll
+          for (int k = 0; k < 32; k += 4)
+            dst[k / 4] = make_float4(__uint_as_float(o[k]) * f, __uint_as_float(o[k + 1]) * f,
+                                     __uint_as_float(o[k + 2]) * f, __uint_as_float(o[k + 3]) * f);
+        }
+        if (c == 0) {
+          if (!run.whole)
+            *reinterpret_cast<float2*>(a.ws_ml + 2 * part) = make_float2(M, L);
+          else if (a.lse)
+            a.lse[me.at] = L != 0.f ? (M + log2f(L)) * kLn2 : -INFINITY;
+        }
+      };
+      if (ok) {
+        const int c_lo = wide ? 0 : wg * (D / 2), c_hi = wide ? D : c_lo + D / 2;
+        for (int c = c_lo; c < c_hi; c += 32) {
+          uint32_t o[32];
+          tmem_ld32((wide ? ocol : lane_t) + c, o);
+          tmem_wait_ld();
+          if (!wide) {
+            if (run.n > 1) {
+              uint32_t o1[32];
+              tmem_ld32(lane_t + 128 + c, o1);
+              tmem_wait_ld();
+#pragma unroll
+              for (int k = 0; k < 32; ++k)
+                o[k] = __float_as_uint(w0 * __uint_as_float(o[k]) + w1 * __uint_as_float(o1[k]));
+            }
+          }
+          emit(c, o);
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(parted);
+      ok = mbar_wait(parted, unit & 1, a.err) && ok;
+      ok = __all_sync(0xffffffffu, ok);
+      tc_fence_after();
+      base.skip(run.n);
+      me = then;
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    __syncwarp();
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
+                 "r"(kTmemCols)
+                 : "memory");
+  }
+}
+
+template <typename KV, int D, bool FORM>
+cudaError_t launch_shape(const ChunkArgs& a, const CUtensorMap& tk, const CUtensorMap& tv,
+                         cudaStream_t s) {
+  using S = TcShape<KV, D>;
+  static std::atomic<unsigned long long> attr_done{0};  // one bit per device
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= 64 || !((attr_done.load() >> dev) & 1ull)) {
+    e = cudaFuncSetAttribute(chunk_tc_kernel<KV, D, FORM>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             S::SMEM);
+    if (e != cudaSuccess) return e;
+    // the softmax warps may take no more registers than the launch brings and the others give up
+    cudaFuncAttributes fa{};
+    e = cudaFuncGetAttributes(&fa, chunk_tc_kernel<KV, D, FORM>);
+    if (e != cudaSuccess) return e;
+    if (kSoftThreads * S::SOFT_REGS + (S::THREADS - kSoftThreads) * S::REGS > S::THREADS * fa.numRegs)
+      return cudaErrorLaunchOutOfResources;
+    if (dev < 64) attr_done.fetch_or(1ull << dev);
+  }
+  chunk_tc_kernel<KV, D, FORM><<<a.ctas, S::THREADS, S::SMEM, s>>>(a, tk, tv);
+  return cudaGetLastError();
+}
+
+template <typename KV, int D>
+cudaError_t launch_t(const ChunkArgs& a, const CUtensorMap& tk, const CUtensorMap& tv,
+                     cudaStream_t s) {
+  return a.softcap > 0.f || a.slopes ? launch_shape<KV, D, true>(a, tk, tv, s)
+                                     : launch_shape<KV, D, false>(a, tk, tv, s);
+}
+
+}  // namespace
+
+cudaError_t launch_chunk_tc(const ChunkArgs& a, int kv_dtype, int head_dim, const void* tk,
+                            const void* tv, cudaStream_t s) {
+  const CUtensorMap& mk = *static_cast<const CUtensorMap*>(tk);
+  const CUtensorMap& mv = *static_cast<const CUtensorMap*>(tv);
+  if (head_dim == 64) {
+    if (kv_dtype == PKV_BF16) return launch_t<BF16, 64>(a, mk, mv, s);
+    if (kv_dtype == PKV_FP8_E4M3) return launch_t<FP8, 64>(a, mk, mv, s);
+    return launch_t<INT8, 64>(a, mk, mv, s);
+  }
+  if (kv_dtype == PKV_BF16) return launch_t<BF16, 128>(a, mk, mv, s);
+  if (kv_dtype == PKV_FP8_E4M3) return launch_t<FP8, 128>(a, mk, mv, s);
+  return launch_t<INT8, 128>(a, mk, mv, s);
+}
+
+}  // namespace pkv

@@ -264,8 +264,13 @@ cudaError_t launch_tree_commit(const CommitArgs& a, cudaStream_t s);
 // Chunk attention on CUDA cores, and the combine of a split call of any type.
 constexpr int kChunkSimtRows = 32, kChunkSimtTokens = 64;
 constexpr int chunk_simt_wave(int head_dim) { return 152 * (head_dim == 64 ? 4 : 2); }
-cudaError_t launch_chunk_simt(const ChunkArgs& a, int q_dtype, int kv_dtype, int head_dim,
-                              cudaStream_t s);
+cudaError_t launch_chunk_simt(const ChunkArgs& a, int kv_dtype, int head_dim, cudaStream_t s);
+// The same on tcgen05: bf16 queries; tk/tv: the 2-D K map and the V map of a bf16 pool (unused for
+// 8-bit caches).
+constexpr int kChunkTcRows = 256, kChunkTcTokens = 128;
+constexpr int kChunkTcWave = 152;  // one CTA per SM
+cudaError_t launch_chunk_tc(const ChunkArgs& a, int kv_dtype, int head_dim, const void* tk,
+                            const void* tv, cudaStream_t s);
 cudaError_t launch_chunk_combine(const ChunkArgs& a, int q_dtype, int head_dim, cudaStream_t s);
 // The weights' sums.
 cudaError_t launch_chunk_weights_simt(const ChunkArgs& a, int q_dtype, int kv_dtype, int head_dim,
