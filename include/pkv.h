@@ -864,6 +864,11 @@ int pkv_chunk_attention(const void* q, int32_t dtype_q, int32_t num_rows, int32_
                         const float* k_scales, const float* v_scales, void* out, float* lse,
                         void* workspace, size_t workspace_bytes, void* stream);
 
+/* Bytes of device workspace pkv_chunk_weights needs (0 for an empty call); as above. */
+size_t pkv_chunk_weights_workspace_size(int32_t dtype_q, int32_t num_rows, int32_t batch,
+                                        int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                                        int64_t width);
+
 /*
  * Sums of the attention weights that the rows of a chunk give to each cached position:
  *   weights_out[b][j][p] = add_to[b][j][p] + sum e^{s - lse[row][h]}
@@ -874,7 +879,9 @@ int pkv_chunk_attention(const void* q, int32_t dtype_q, int32_t num_rows, int32_
  *  weights_out  device fp32 [batch][num_kv_heads][width]; may be add_to. Columns p < context_lens[b]
  *               are written, the others left as they were.
  * A request longer than `width` is left out and flagged with PKV_DEVERR_BAD_CHUNK; the other
- * arguments, refusals and flags are those of pkv_chunk_attention. Equal inputs give equal results.
+ * arguments, refusals and flags are those of pkv_chunk_attention (of work: a call whose rows and width
+ * could hold 2^30 steps, of 128 rows and 256 positions, for fp32 queries 32 and 64). Equal inputs give
+ * equal results.
  */
 int pkv_chunk_weights(const void* q, int32_t dtype_q, int32_t num_rows, int32_t batch,
                       int32_t num_q_heads, const void* k_cache, const pkv_cache_desc* desc,
@@ -882,7 +889,7 @@ int pkv_chunk_weights(const void* q, int32_t dtype_q, int32_t num_rows, int32_t 
                       const int32_t* context_lens, const int32_t* query_starts,
                       const pkv_score_form* form, const float* k_scales, const float* lse,
                       int32_t last_rows, const float* add_to, float* weights_out, int64_t width,
-                      void* stream);
+                      void* workspace, size_t workspace_bytes, void* stream);
 
 /*
  * The positions that a request keeps when its cache is cut to `budget` tokens, for each KV head: its
@@ -963,7 +970,8 @@ int32_t pkv_prefix_size(const pkv_prefix_cache* c);
  * bracketed by a pair of CUDA events on its stream. pkv_trace_read() synchronises those events
  * and reports, for the family named ("paged_decode", "decode_combine", "cascade_prefix",
  * "kv_append", "kv_absmax", "copy_pages", "qk_norm_rope_append", "tree_attention", "tree_combine",
- * "tree_commit", "chunk_attention", "chunk_combine", "chunk_weights", "evict_select", "evict_move",
+ * "tree_commit", "chunk_attention", "chunk_combine", "chunk_weights",
+ * "chunk_weights_combine", "evict_select", "evict_move",
  * and the packed steps' "h2d_copy" and "d2h_copy"),
  * the number of launches and their summed device time in milliseconds since the last reset.
  * pkv_trace_reset() drops all records. */

@@ -31,7 +31,7 @@ __all__ = [
     "cascade_decode_step", "cascade_workspace_size", "HostStep", "trace_enable", "trace_reset",
     "trace_read", "rope_table", "qk_norm_rope_append", "tree_masks", "tree_decode_workspace_size",
     "tree_decode_attention", "tree_commit", "chunk_workspace_size", "chunk_attention",
-    "chunk_weights", "evict_select", "evict_move",
+    "chunk_weights_workspace_size", "chunk_weights", "evict_select", "evict_move",
 ]
 
 F32, BF16, FP8_E4M3, INT8 = 0, 1, 2, 3
@@ -152,7 +152,8 @@ def lib():
         "pkv_chunk_attention": (ctypes.c_int, [vp, i32, i32, i32, i32, vp, vp, D, vp, i32, vp, vp,
                                                F, vp, vp, vp, vp, vp, sz, vp]),
         "pkv_chunk_weights": (ctypes.c_int, [vp, i32, i32, i32, i32, vp, D, vp, i32, vp, vp, F, vp,
-                                             vp, i32, vp, vp, i64, vp]),
+                                             vp, i32, vp, vp, i64, vp, sz, vp]),
+        "pkv_chunk_weights_workspace_size": (sz, [i32, i32, i32, i32, i32, i32, i64]),
         "pkv_evict_select": (ctypes.c_int, [vp, i64, vp, i32, i32, i32, i32, i32, vp, vp, vp]),
         "pkv_evict_move": (ctypes.c_int, [vp, vp, D, vp, i32, vp, vp, i32, i32, vp, i32, vp, i64,
                                           vp, i64, vp]),
@@ -950,6 +951,15 @@ def chunk_workspace_size(dtype_q, cache_dtype, num_rows, batch, num_q_heads, num
                                               max_pages_per_seq))
 
 
+@functools.lru_cache(maxsize=256)
+def chunk_weights_workspace_size(dtype_q, num_rows, batch, num_q_heads, num_kv_heads, head_dim,
+                                 width) -> int:
+    """Bytes of workspace of a chunk_weights call (dtype_q as a torch dtype or code)."""
+    code = dtype_q if isinstance(dtype_q, int) else _dtype_code(torch.empty(0, dtype=dtype_q))
+    return int(lib().pkv_chunk_weights_workspace_size(code, num_rows, batch, num_q_heads,
+                                                      num_kv_heads, head_dim, width))
+
+
 def _chunk_args(q, desc, block_tables, context_lens, query_starts, alibi_slopes):
     """Checks what the chunk calls share; returns (rows, batch, query heads)."""
     if q.dim() != 3:
@@ -1009,7 +1019,7 @@ def chunk_attention(q, k_cache, v_cache, block_tables, context_lens, query_start
 
 def chunk_weights(q, k_cache, block_tables, context_lens, query_starts, lse, scale, softcap=0.0,
                   alibi_slopes=None, window=0, sink_tokens=0, last_rows=0, add_to=None, out=None,
-                  width=None, k_scales=None, stream=None):
+                  width=None, k_scales=None, workspace=None, stream=None):
     """Sums fp32 [batch, num_kv_heads, width] of the attention weights e^(s - lse) that each request's
     last ``last_rows`` new rows (0: all) give to its cached positions, over rows and the query heads of
     a KV head, added to ``add_to`` (None: zeros); scores as in ``chunk_attention``, which left ``lse``
@@ -1039,12 +1049,17 @@ def chunk_weights(q, k_cache, block_tables, context_lens, query_starts, lse, sca
         raise PkvError(-2, "add_to and out must have one shape")
     form = _ScoreForm(scale, softcap, _opt_addr(alibi_slopes, "alibi_slopes", dev), window,
                       sink_tokens)
+    code = _dtype_code(q)
+    if workspace is None:
+        need = chunk_weights_workspace_size(code, n, B, h_q, h_kv, desc.head_dim, out.shape[2])
+        workspace = _new(torch.empty, need, torch.uint8, q.device, stream)
     _check(lib().pkv_chunk_weights(
-        _addr(q, "q", dev), _dtype_code(q), n, B, h_q, _addr(k_cache, "k_cache", dev), desc,
+        _addr(q, "q", dev), code, n, B, h_q, _addr(k_cache, "k_cache", dev), desc,
         _addr(block_tables, "block_tables", dev), block_tables.shape[1],
         _addr(context_lens, "context_lens", dev), _addr(query_starts, "query_starts", dev), form,
         _opt_addr(k_scales, "k_scales", dev), _addr(lse, "lse", dev), last_rows,
         _opt_addr(add_to, "add_to", dev), _addr(out, "out", dev), out.shape[2],
+        _addr(workspace, "workspace", dev), workspace.numel() * workspace.element_size(),
         _raw_stream(stream, dev)))
     return out
 

@@ -8,6 +8,7 @@
 #include "chunk_plan.cuh"
 #include "pkv.h"
 #include "pkv_internal.h"
+#include "weigh_plan.cuh"
 
 using namespace pkv;
 
@@ -143,6 +144,38 @@ void set_split(ChunkArgs& a, const ChunkSplit& t) {
   a.wide_tile = t.wide_tile;
 }
 
+// The same for the weights' sums (weigh_plan.cuh): rows of a step, positions of an item, CTAs.
+struct WeighSplit {
+  int rows, tokens, wave;
+  bool tc;
+};
+
+WeighSplit weigh_split(int dtype_q, int head_dim) {
+  if (dtype_q == PKV_BF16) return WeighSplit{kWeighTcRows, kWeighTcTokens, kWeighTcWave, true};
+  return WeighSplit{kChunkSimtRows, kChunkSimtTokens, weigh_simt_wave(head_dim), false};
+}
+
+// Steps that the call's rows and sums could take at most (up to 2^60).
+long long weigh_most_work(const WeighSplit& t, int num_rows, int batch, int h_q, int h_kv,
+                          int64_t width) {
+  const long long items = capped_product((width + t.tokens - 1) / t.tokens, h_kv);
+  // (every request's items: two each, besides a step for every t.rows rows and a broken one)
+  const long long steps = (long long)num_rows * (h_q / h_kv) / t.rows + 3ll * batch;
+  return capped_product(items, steps);
+}
+
+int weigh_ctas(const WeighSplit& t, int num_rows, int batch, int h_q, int h_kv, int64_t width) {
+  const long long work = weigh_most_work(t, num_rows, batch, h_q, h_kv, width);
+  return (int)std::max(1ll, std::min<long long>(t.wave, work / 2 + 1));
+}
+
+ChunkSpace weigh_space(const WeighSplit& t, int ctas) {
+  ChunkSpace s;
+  s.acc = s.ml = align256((size_t)ctas * 2 * t.tokens * sizeof(float));
+  s.all = s.ml + align256((size_t)ctas * sizeof(WeighRecord));
+  return s;
+}
+
 }  // namespace
 
 extern "C" {
@@ -212,13 +245,23 @@ int pkv_chunk_attention(const void* q, int32_t dtype_q, int32_t num_rows, int32_
   return cuda_status(e, "chunk_combine launch");
 }
 
+size_t pkv_chunk_weights_workspace_size(int32_t dtype_q, int32_t num_rows, int32_t batch,
+                                        int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                                        int64_t width) {
+  if (num_rows < 0 || batch <= 0 || num_q_heads <= 0 || num_kv_heads <= 0 || head_dim <= 0 ||
+      width <= 0 || num_q_heads < num_kv_heads)
+    return 0;
+  const WeighSplit t = weigh_split(dtype_q, head_dim);
+  return weigh_space(t, weigh_ctas(t, num_rows, batch, num_q_heads, num_kv_heads, width)).all;
+}
+
 int pkv_chunk_weights(const void* q, int32_t dtype_q, int32_t num_rows, int32_t batch,
                       int32_t num_q_heads, const void* k_cache, const pkv_cache_desc* desc,
                       const int32_t* block_tables, int32_t max_pages_per_seq,
                       const int32_t* context_lens, const int32_t* query_starts,
                       const pkv_score_form* form, const float* k_scales, const float* lse,
                       int32_t last_rows, const float* add_to, float* weights_out, int64_t width,
-                      void* stream) {
+                      void* workspace, size_t workspace_bytes, void* stream) {
   const char* who = "pkv_chunk_weights";
   ChunkArgs a{};
   int st = check_chunk(who, q, dtype_q, num_rows, batch, num_q_heads, k_cache, desc, block_tables,
@@ -229,30 +272,40 @@ int pkv_chunk_weights(const void* q, int32_t dtype_q, int32_t num_rows, int32_t 
   if (batch == 0 || width == 0) return PKV_OK;
   const int kv = desc->cache_dtype, D = desc->head_dim;
   if (!weights_out || (num_rows > 0 && !lse)) return set_error(PKV_EINVAL, "%s: null pointer", who);
-  if (width >= (1ll << 31) - 128)
+  if (width >= (1ll << 31) - 256)
     return set_error(PKV_ESHAPE, "%s: a row of sums holds 2^31 positions or more", who);
-  const int rows = kChunkSimtRows, tokens = kChunkSimtTokens;
-  // (an item is as long as its request's blocks of rows, plus one)
-  const long long items =
-      capped_product((width + tokens - 1) / tokens, desc->num_kv_heads);
-  const long long blocks =
-      capped_product(num_rows, a.group) / rows + 2ll * batch;
-  if (capped_product(items, blocks) >= (1ll << 30))
-    return set_error(PKV_ESHAPE, "%s: rows and width can hold 2^30 blocks of work or more", who);
-  ChunkSplit t = chunk_split(dtype_q, kv, D);
-  t.rows = rows;
-  t.tokens = tokens;
-  set_split(a, t);
-  a.ctas = (int)std::max(1ll, std::min<long long>(152 * 4, capped_product(items, batch)));
+  const WeighSplit t = weigh_split(dtype_q, D);
+  if (weigh_most_work(t, num_rows, batch, a.h_q, a.h_kv, width) >= (1ll << 30))
+    return set_error(PKV_ESHAPE, "%s: rows and width can hold 2^30 steps of work or more", who);
+  a.unit_rows = t.rows;
+  a.tile_tokens = t.tokens;
+  a.ctas = weigh_ctas(t, num_rows, batch, a.h_q, a.h_kv, width);
+  const ChunkSpace space = weigh_space(t, a.ctas);
+  if (!workspace || workspace_bytes < space.all)
+    return set_error(PKV_EINVAL, "%s: workspace of %zu bytes needed, %zu given", who, space.all,
+                     workspace ? workspace_bytes : 0);
+  if (!aligned16(workspace)) return set_error(PKV_EALIGN, "%s: workspace alignment", who);
+  a.ws_acc = static_cast<float*>(workspace);
+  a.ws_rec = static_cast<char*>(workspace) + space.ml;
   a.lse = const_cast<float*>(lse);
   a.add_to = add_to;
   a.weights_out = weights_out;
   a.width = width;
   a.last_rows = last_rows;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  cudaError_t e = traced("chunk_weights", s,
-                         [&] { return launch_chunk_weights_simt(a, dtype_q, kv, D, s); });
-  return cuda_status(e, "chunk_weights launch");
+  CUtensorMap tk{};
+  if (t.tc && kv == PKV_BF16 && num_rows > 0) {
+    int rank = 2;
+    st = pool_tensor_map(k_cache, desc, &tk, &rank, true);
+    if (st != PKV_OK) return st;
+  }
+  cudaError_t e = traced("chunk_weights", s, [&] {
+    return t.tc ? launch_chunk_weights_tc(a, kv, D, &tk, s) : launch_chunk_weights_simt(a, kv, D, s);
+  });
+  st = cuda_status(e, "chunk_weights launch");
+  if (st != PKV_OK || a.ctas == 1) return st;  // (one CTA finishes every item)
+  e = traced("chunk_weights_combine", s, [&] { return launch_chunk_weights_combine(a, s); });
+  return cuda_status(e, "chunk_weights_combine launch");
 }
 
 int pkv_evict_select(const float* weights, int64_t width, const int32_t* context_lens, int32_t batch,

@@ -39,6 +39,7 @@
 #include "paged_decode_mma.cuh"
 #include "pkv_device.cuh"
 #include "pkv_internal.h"
+#include "tc_pipe.cuh"
 #include "tcgen05.cuh"
 
 namespace pkv {
@@ -89,34 +90,6 @@ struct TcShape {
   static_assert(SMEM <= 225 * 1024 && SMEM > 114 * 1024, "one CTA per SM");
 };
 
-// A place in a ring of N stages and the parity of its current use.
-template <int N>
-struct Place {
-  int st = 0;
-  uint32_t par = 0;
-  __device__ __forceinline__ void advance(int k) {  // k <= N
-    st += k;
-    if (st >= N) {
-      st -= N;
-      par ^= 1u;
-    }
-  }
-  __device__ __forceinline__ void skip(int k) {  // any k
-    const int t = st + k, w = t / N;
-    st = t - w * N;
-    par ^= (uint32_t)w & 1u;
-  }
-};
-
-template <int N>
-__device__ __forceinline__ void regs_up() {
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
-}
-template <int N>
-__device__ __forceinline__ void regs_down() {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
-}
-
 template <bool F16>
 __device__ __forceinline__ uint32_t pack_p(float a, float b) {
   return F16 ? pack_f16(a, b) : pack_bf16(a, b);
@@ -138,13 +111,6 @@ __device__ __forceinline__ uint32_t add_zero_times(uint32_t w, uint32_t z) {
   else
     asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(w), "r"(0u), "r"(z));
   return r;
-}
-
-// tanh x = 1 - 2 / (1 + e^{2x}): off by at most some 2^-22, with the exact limits at infinities.
-__device__ __forceinline__ float tanh_of(float x) {
-  float r;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + ex2_approx(2.f * kLog2e * x)));
-  return fmaf(-2.f, r, 1.f);
 }
 
 // FORM: scores are capped or have a bias (otherwise they are the products, scaled).
@@ -551,40 +517,7 @@ __global__ void __launch_bounds__(TcShape<KV, D>::THREADS, 1) chunk_tc_kernel(
       }
     };
     auto store_query = [&](Row& x, uint4 (&in)[RND][4]) {
-      if constexpr (W8) {  // f16, scaled by a row's 2^e (the four lanes that hold a row agree)
-        const float sc = x.sc;
-#pragma unroll
-        for (int g = 0; g < 4; ++g) {
-          uint32_t lo = 0, hi = 0;  // largest |q| as bits (bf16 magnitudes order like integers)
-#pragma unroll
-          for (int d = 0; d < RND; ++d) {
-            const uint32_t* w = &in[d][g].x;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              lo = max(lo, w[k] & 0x7fffu);
-              hi = max(hi, w[k] & 0x7fff0000u);
-            }
-          }
-          uint32_t mx = max(lo, hi >> 16);
-          mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-          mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-          const int ex = mx >> 7;  // biased exponent: mx 2^e in [2^14, 2^15), none for 0, inf, NaN
-          const int e = mx != 0 && ex < 255 ? min(126, max(-126, 141 - ex)) : 0;
-          // the factor of the scores stays positive, and at least the smallest normal number (an
-          // unseen score of -inf must stay one): a K scale's sign, or a NaN one, is in the query
-          const float two_e = __int_as_float((127 + e) << 23);
-          const float up = sc < 0.f ? -two_e : sc == sc ? two_e : sc;
-          const float of = fmaxf(fabsf(sc) * __int_as_float((127 - e) << 23), 0x1p-126f);
-          const float mine = __shfl_sync(0xffffffffu, of, 4 * (lane & 7));
-          if ((lane >> 3) == g) x.sc = mine;
-#pragma unroll
-          for (int d = 0; d < RND; ++d) {
-            uint32_t* w = &in[d][g].x;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) w[k] = pack_f16(bf16lo(w[k]) * up, bf16hi(w[k]) * up);
-          }
-        }
-      }
+      if constexpr (W8) query_to_f16<RND>(in, x.sc, x.sc);
       const int row0 = (warp & 3) * 32 + (lane >> 2);  // rows row0 + 8 g of the group
       const uint32_t at = ring + S::OFF_Q + wg * S::Q_GROUP + row0 * 128;
 #pragma unroll

@@ -308,107 +308,4 @@ struct ChunkRecord {
   int shares;
 };
 
-// ---- the weights' sums -----------------------------------------------------------------------
-
-// Request b's counted rows are its last last_rows new tokens (0: all); an item is a tile of
-// tile_tokens cached positions of one KV head, whose sums one CTA makes over all rows, in order: no
-// sum is made in parts by several CTAs, so equal inputs give equal results. The items of all
-// requests form one stream in which an item is as long as its request's blocks of unit_rows rows,
-// plus one, and a CTA takes the items that begin in its equal share of it. Early positions are seen by
-// more rows than late ones: a request's items alternate between its first tiles and its last.
-struct WeighReq {
-  ChunkReq r;
-  int from;   // first counted token
-  int tiles;
-  int cost;   // of an item
-};
-
-__device__ __forceinline__ WeighReq weigh_request(const ChunkArgs& a, int b) {
-  WeighReq w{chunk_request(a, b), 0, 0, 1};
-  const int ctx = w.r.base + w.r.n;
-  if (w.r.err == 0 && ctx > a.width) w.r = ChunkReq{0, 0, 0, PKV_DEVERR_BAD_CHUNK};
-  if (w.r.err != 0) return w;
-  const int count = a.last_rows > 0 ? min(a.last_rows, w.r.n) : w.r.n;
-  w.from = w.r.n - count;
-  w.tiles = (ctx + a.tile_tokens - 1) / a.tile_tokens;
-  w.cost = 1 + (count * a.group + a.unit_rows - 1) / a.unit_rows;
-  return w;
-}
-
-struct WeighShare {
-  int b, item, left;  // first request and item; length left in the share
-};
-
-template <int THREADS>
-__device__ __forceinline__ void weigh_share(const ChunkArgs& a, int* scratch, WeighShare* out) {
-  const int per = (a.batch + THREADS - 1) / THREADS;
-  const int b0 = min(a.batch, (int)threadIdx.x * per), b1 = min(a.batch, b0 + per);
-  int mine = 0, err = 0;
-  for (int b = b0; b < b1; ++b) {
-    const WeighReq w = weigh_request(a, b);
-    err |= w.r.err;
-    mine += w.tiles * w.cost * a.h_kv;
-  }
-  if (err && blockIdx.x == 0) atomicOr(a.err, err);
-  if (threadIdx.x == 0) out->left = 0;
-  int below, total;
-  block_scan<THREADS>(mine, scratch, below, total);
-  const int share = (int)(((unsigned)total + a.ctas - 1) / (unsigned)a.ctas);
-  const long long start = (long long)blockIdx.x * share;
-  if (start >= below && start < (long long)below + mine) {
-    int at = below, b = b0;
-    for (; b < b1 - 1; ++b) {
-      const WeighReq w = weigh_request(a, b);
-      if (start < at + w.tiles * w.cost * a.h_kv) break;
-      at += w.tiles * w.cost * a.h_kv;
-    }
-    const int cost = weigh_request(a, b).cost, item = ((int)start - at + cost - 1) / cost;
-    out->b = b;
-    out->item = item;
-    out->left = min(share, total - (int)start) - (at + item * cost - (int)start);
-  }
-  __syncthreads();
-}
-
-struct WeighItem {
-  WeighReq w;
-  int b, j, tile;
-  int t0, t1;  // counted tokens t0 .. t1 - 1 may see some of the tile's positions
-};
-
-// Walks a share item by item. Uniform over its callers.
-struct WeighWalk {
-  int b, item, left;
-  WeighReq w;
-  __device__ __forceinline__ WeighWalk(const ChunkArgs& a, const WeighShare& s)
-      : b(s.b), item(s.item), left(s.left) {
-    if (left > 0) w = weigh_request(a, b);
-  }
-  __device__ __forceinline__ bool next(const ChunkArgs& a, WeighItem& x) {
-    while (left > 0) {
-      if (item >= w.tiles * a.h_kv) {
-        if (++b >= a.batch) return false;
-        w = weigh_request(a, b);
-        item = 0;
-        continue;
-      }
-      x.w = w;
-      x.b = b;
-      x.j = item / w.tiles;
-      const int o = item - x.j * w.tiles;
-      x.tile = o & 1 ? w.tiles - 1 - (o >> 1) : o >> 1;
-      const int p0 = x.tile * a.tile_tokens;
-      x.t0 = max(w.from, p0 - w.r.base);
-      x.t1 = w.r.n;
-      if (a.window > 0 && p0 >= a.sink)
-        x.t1 = (int)min((long long)x.t1,
-                        (long long)p0 + a.tile_tokens - 1 + a.window - w.r.base);
-      ++item;
-      left -= w.cost;
-      return true;
-    }
-    return false;
-  }
-};
-
 }  // namespace pkv

@@ -3,9 +3,10 @@
 //                  e^{s_thp - lse_th},
 // with the scores s of the chunk attention and the lse it left.
 //
-// A block makes the sums of a tile of 64 positions of one KV head (chunk_plan.cuh): K of the tile stays
-// in shared memory as fp32, the rows come by 32, a thread computes 4 rows x 4 positions of scores. Sums
-// over thousands of rows are compensated (Kahan's summation), so that they are good to fp32.
+// For fp32 queries, on CUDA cores, and the combine of a split call of any type. A block takes tiles of 64
+// positions of one KV head (weigh_plan.cuh): K of the tile stays in shared memory as fp32, the rows come
+// by 32, a thread computes 4 rows x 4 positions of scores. Sums over thousands of rows are compensated
+// (Kahan's summation), so that they are good to fp32.
 #include <math.h>
 
 #include <atomic>
@@ -15,6 +16,7 @@
 #include "pkv_device.cuh"
 #include "pkv_internal.h"
 #include "tcgen05.cuh"
+#include "weigh_plan.cuh"
 
 namespace pkv {
 
@@ -29,7 +31,7 @@ struct WeighShape {
   static constexpr int SMEM = 4 * ((kRows + kTok) * LD + 8 * kTok + kRows);
 };
 
-template <typename TQ, typename KV, int D>
+template <typename KV, int D>
 __global__ void __launch_bounds__(kThreads) weights_simt_kernel(const ChunkArgs a) {
   constexpr int LD = WeighShape<D>::LD;
   extern __shared__ float4 smem4[];
@@ -39,15 +41,16 @@ __global__ void __launch_bounds__(kThreads) weights_simt_kernel(const ChunkArgs 
   float* lse2 = sums + 8 * kTok;       // [32] the rows' lse in the log2 domain
   __shared__ int scratch[32];
   __shared__ WeighShare share;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   weigh_share<kThreads>(a, scratch, &share);
   WeighWalk walk(a, share);
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;  // positions tx + 16 m, rows ty + 8 i
-  WeighItem it;
+  WeighRecord record{0, 0, 0, 0};
+  WeighRun it;
   while (walk.next(a, it)) {
-    const ChunkReq& req = it.w.r;
-    const int j = it.j, p0 = it.tile * kTok, ctx = req.base + req.n;
+    const ChunkReq& req = it.req;
+    const int j = it.j, p0 = it.item * kTok, ctx = req.base + req.n, rows = it.rows;
     const int32_t* table = a.block_tables + (size_t)it.b * a.max_pages;
-    const int rows = max(0, it.t1 - it.t0) * a.group;
     uint64_t page_ok = 0;
     __syncthreads();  // the last item's tile and sums are used up
     if (rows > 0) {
@@ -81,7 +84,7 @@ __global__ void __launch_bounds__(kThreads) weights_simt_kernel(const ChunkArgs 
     }
     const ScoreForm form(a, KV::bytes == 1 ? a.k_scales[j] : 1.f);
     float total[4] = {0.f, 0.f, 0.f, 0.f}, lost[4] = {0.f, 0.f, 0.f, 0.f};
-    for (int r0 = 0; r0 < rows; r0 += kRows) {
+    for (int r0 = it.s0 * kRows; r0 < min(rows, (it.s0 + it.n) * kRows); r0 += kRows) {
       __syncthreads();  // the last rows are used up
       for (int e = threadIdx.x; e < kRows * (D / 4); e += kThreads) {
         const int r = e / (D / 4), c = e % (D / 4);
@@ -89,7 +92,7 @@ __global__ void __launch_bounds__(kThreads) weights_simt_kernel(const ChunkArgs 
         if (r0 + r < rows) {
           const int t = (r0 + r) / a.group, g = (r0 + r) - t * a.group;
           const size_t at = (size_t)(req.q0 + it.t0 + t) * a.h_q + j * a.group + g;
-          v = load4(static_cast<const TQ*>(a.q) + at * D + 4 * c);
+          v = load4(static_cast<const float*>(a.q) + at * D + 4 * c);
           if (c == 0) lse2[r] = a.lse[at] * kLog2e;
         }
         *reinterpret_cast<float4*>(qs + r * LD + 4 * c) = v;
@@ -142,47 +145,75 @@ __global__ void __launch_bounds__(kThreads) weights_simt_kernel(const ChunkArgs 
     for (int k = 0; k < 4; ++k) sums[ty * kTok + tx + 16 * k] = total[k];
     __syncthreads();
     if (threadIdx.x < kTok && p0 + (int)threadIdx.x < ctx) {
-      const int64_t at = ((int64_t)it.b * a.h_kv + j) * a.width + p0 + threadIdx.x;
       float x = 0.f;
 #pragma unroll
       for (int i = 0; i < 8; ++i) x += sums[i * kTok + threadIdx.x];
-      a.weights_out[at] = (a.add_to ? a.add_to[at] : 0.f) + x;
+      const int64_t at = ((int64_t)it.b * a.h_kv + j) * a.width + p0 + threadIdx.x;
+      if (it.whole)
+        a.weights_out[at] = (a.add_to ? a.add_to[at] : 0.f) + x;
+      else
+        a.ws_acc[((size_t)blockIdx.x * 2 + it.slot) * kTok + threadIdx.x] = x;
     }
+    if (!it.whole && it.slot == 1)
+      record = WeighRecord{it.b * a.h_kv + j, p0, min(kTok, ctx - p0), it.shares};
   }
+  if (threadIdx.x == 0) static_cast<WeighRecord*>(a.ws_rec)[blockIdx.x] = record;
 }
 
-template <typename TQ, typename KV, int D>
+// Items that crossed shares: a block for each share adds the partials of the item that begins there.
+__global__ void weights_combine_kernel(const ChunkArgs a) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const WeighRecord rec = static_cast<const WeighRecord*>(a.ws_rec)[blockIdx.x];
+  if (rec.shares == 0 || (int)threadIdx.x >= rec.n) return;
+  const int T = a.tile_tokens;
+  float x = a.ws_acc[((size_t)blockIdx.x * 2 + 1) * T + threadIdx.x];
+  for (int c = 1; c <= rec.shares; ++c)
+    x += a.ws_acc[((size_t)(blockIdx.x + c) * 2) * T + threadIdx.x];
+  const int64_t at = (int64_t)rec.row * a.width + rec.p0 + threadIdx.x;
+  a.weights_out[at] = (a.add_to ? a.add_to[at] : 0.f) + x;
+}
+
+template <typename KV, int D>
 cudaError_t go(const ChunkArgs& a, cudaStream_t s) {
   static std::atomic<unsigned long long> attr_done{0};  // one bit per device
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev >= 64 || !((attr_done.load() >> dev) & 1ull)) {
-    e = cudaFuncSetAttribute(weights_simt_kernel<TQ, KV, D>,
+    e = cudaFuncSetAttribute(weights_simt_kernel<KV, D>,
                              cudaFuncAttributeMaxDynamicSharedMemorySize, WeighShape<D>::SMEM);
     if (e != cudaSuccess) return e;
     if (dev < 64) attr_done.fetch_or(1ull << dev);
   }
-  weights_simt_kernel<TQ, KV, D><<<a.ctas, kThreads, WeighShape<D>::SMEM, s>>>(a);
+  weights_simt_kernel<KV, D><<<a.ctas, kThreads, WeighShape<D>::SMEM, s>>>(a);
   return cudaGetLastError();
 }
 
-template <typename TQ, int D>
+template <int D>
 cudaError_t types(const ChunkArgs& a, int kv_dtype, cudaStream_t s) {
-  if (kv_dtype == PKV_F32) return go<TQ, F32, D>(a, s);
-  if (kv_dtype == PKV_BF16) return go<TQ, BF16, D>(a, s);
-  if (kv_dtype == PKV_FP8_E4M3) return go<TQ, FP8, D>(a, s);
-  return go<TQ, INT8, D>(a, s);
+  if (kv_dtype == PKV_F32) return go<F32, D>(a, s);
+  if (kv_dtype == PKV_FP8_E4M3) return go<FP8, D>(a, s);
+  return go<INT8, D>(a, s);
 }
 
 }  // namespace
 
-cudaError_t launch_chunk_weights_simt(const ChunkArgs& a, int q_dtype, int kv_dtype, int head_dim,
+cudaError_t launch_chunk_weights_simt(const ChunkArgs& a, int kv_dtype, int head_dim,
                                       cudaStream_t s) {
-  if (q_dtype == PKV_BF16)
-    return head_dim == 64 ? types<__nv_bfloat16, 64>(a, kv_dtype, s)
-                          : types<__nv_bfloat16, 128>(a, kv_dtype, s);
-  return head_dim == 64 ? types<float, 64>(a, kv_dtype, s) : types<float, 128>(a, kv_dtype, s);
+  return head_dim == 64 ? types<64>(a, kv_dtype, s) : types<128>(a, kv_dtype, s);
+}
+
+cudaError_t launch_chunk_weights_combine(const ChunkArgs& a, cudaStream_t s) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(a.ctas);
+  cfg.blockDim = dim3(a.tile_tokens);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, weights_combine_kernel, a);
 }
 
 }  // namespace pkv

@@ -272,9 +272,16 @@ constexpr int kChunkTcWave = 152;  // one CTA per SM
 cudaError_t launch_chunk_tc(const ChunkArgs& a, int kv_dtype, int head_dim, const void* tk,
                             const void* tv, cudaStream_t s);
 cudaError_t launch_chunk_combine(const ChunkArgs& a, int q_dtype, int head_dim, cudaStream_t s);
-// The weights' sums.
-cudaError_t launch_chunk_weights_simt(const ChunkArgs& a, int q_dtype, int kv_dtype, int head_dim,
+// The weights' sums (weigh_plan.cuh): on CUDA cores, on tcgen05, and the combine of a split call.
+constexpr int kWeighTcRows = 128, kWeighTcTokens = 256;
+constexpr int kWeighTcWave = 152;  // one CTA per SM
+// CTAs resident at once, by their shared memory: of 28 KB four on an SM (their registers), of 53 KB four
+constexpr int weigh_simt_wave(int) { return 152 * 4; }
+cudaError_t launch_chunk_weights_simt(const ChunkArgs& a, int kv_dtype, int head_dim,
                                       cudaStream_t s);
+cudaError_t launch_chunk_weights_tc(const ChunkArgs& a, int kv_dtype, int head_dim, const void* tk,
+                                    cudaStream_t s);
+cudaError_t launch_chunk_weights_combine(const ChunkArgs& a, cudaStream_t s);
 cudaError_t launch_evict_select(const EvictSelectArgs& a, cudaStream_t s);
 cudaError_t launch_evict_move(const EvictMoveArgs& a, cudaStream_t s);
 cudaError_t launch_decode_f32(const DecodeArgs& a, int q_dtype, int head_dim, int group,
