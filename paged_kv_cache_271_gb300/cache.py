@@ -16,8 +16,9 @@ from collections.abc import Mapping
 import numpy as np
 import torch
 
-from . import (PageAllocator, PkvError, SeqTable, _ids, copy_pages, kv_append, qk_norm_rope_append,
-               tree_commit, tree_decode_attention)
+from . import (PageAllocator, PkvError, SeqTable, _ids, chunk_attention, chunk_weights, copy_pages,
+               evict_move, evict_select, kv_append, qk_norm_rope_append, tree_commit,
+               tree_decode_attention)
 
 
 class _RowView(Mapping):
@@ -206,6 +207,82 @@ class PagedKVCache:
                               path_lens, stream=stream).tolist()
         self.table.truncate(rids, new)
         return new
+
+    # ---- chunks of new tokens, and a bounded cache -------------------------------------------
+
+    def attend_chunk(self, q, block_tables, context_lens, query_starts, scale, stream=None, **form):
+        """Attention of chunks of new tokens q [N, h_q, d], whose rows are in the cache already
+        (chunk_attention over these pools; ``form``: softcap, alibi_slopes, window, sink_tokens, out,
+        lse, workspace)."""
+        return chunk_attention(q, self.k, self.v, block_tables, context_lens, query_starts, scale,
+                               k_scales=self.k_scales, v_scales=self.v_scales, stream=stream, **form)
+
+    def chunk_weights(self, q, block_tables, context_lens, query_starts, lse, scale, stream=None,
+                      **form):
+        """Sums of the weights that the chunks' rows give to each cached position (chunk_weights;
+        ``form``: the attention's, last_rows, add_to, out, width, workspace)."""
+        return chunk_weights(q, self.k, block_tables, context_lens, query_starts, lse, scale,
+                             k_scales=self.k_scales, stream=stream, **form)
+
+    def evict(self, rids, weights, budget: int, recent: int = 0, sink_tokens: int = 0,
+              stream=None) -> torch.Tensor:
+        """Cut each request longer than ``budget`` tokens to its first ``sink_tokens``, its last
+        ``recent`` and the positions with the largest ``weights`` (fp32 [len(rids), h_kv, width], as
+        ``chunk_weights`` makes them) between them, ``budget`` in all, chosen for each KV head on its
+        own. The kept rows move together onto new pages, so that shared pages (a fork's, a cached
+        prefix's) stay as they are for their other holders, and the request gives its old pages back:
+        what is written into them later must be ordered after this call's work on ``stream``. Returns
+        the sums in the new order, zeros behind them. If the new pages are not there, PkvError is
+        raised and nothing changes."""
+        rids = _ids(rids)
+        lens = self.table.lengths(rids)  # (refuses an unknown request)
+        if np.unique(rids).size != rids.size:
+            raise PkvError(-1, "rids must name each request once")
+        if (weights.dtype != torch.float32 or weights.dim() != 3 or
+                tuple(weights.shape[:2]) != (rids.size, self.k.shape[1])):
+            raise PkvError(-2, "weights must be float32 [len(rids), num_kv_heads, width]")
+        budget = int(budget)
+        if budget <= 0 or recent < 0 or sink_tokens < 0 or recent + sink_tokens > budget:
+            raise PkvError(-1, "budget must be positive and hold recent and sink_tokens")
+        if rids.size and int(lens.max()) > weights.shape[2]:
+            raise PkvError(-2, "a request is longer than its row of weights")
+        cut = np.nonzero(lens > budget)[0]
+        if stream is None:
+            stream = torch.cuda.current_stream(self.k.device)
+        elif not isinstance(stream, torch.cuda.Stream):  # a raw cudaStream_t handle
+            stream = torch.cuda.ExternalStream(int(stream), device=self.k.device)
+        with torch.cuda.stream(stream):
+            if cut.size == 0:
+                return weights.clone()
+            old = self.table.tables(rids[cut])
+            if any((old[i, :-(-int(lens[c]) // self.page_size)] < 0).any()
+                   for i, c in enumerate(cut)):
+                raise PkvError(-1, "a request that gave pages back (release_outside_window) cannot "
+                                   "be cut")
+            per = -(-budget // self.page_size)
+            pages = np.asarray(self.allocator.alloc(per * cut.size), dtype=np.int32)
+            try:
+                dev = self.k.device
+                new = pages.reshape(cut.size, per)
+                rows = None if cut.size == rids.size else torch.from_numpy(cut).to(dev)
+                w = weights if rows is None else weights[rows]
+                bt, nt, cl = (torch.from_numpy(np.ascontiguousarray(x)).to(dev)
+                              for x in (old, new, lens[cut]))
+                kept, kept_lens = evict_select(w.contiguous(), cl, budget, recent, sink_tokens,
+                                               stream=stream)
+                moved = torch.empty_like(w, memory_format=torch.contiguous_format)
+                evict_move(self.k, self.v, bt, kept, kept_lens, nt, w.contiguous(), moved,
+                           stream=stream)
+                if rows is not None:
+                    moved = weights.clone().index_copy_(0, rows, moved)
+            except BaseException:
+                self.allocator.decref(pages)
+                raise
+            for i, rid in enumerate(rids[cut].tolist()):
+                self.table.free([rid])
+                self.table.add(rid, new[i].tolist(), per * self.page_size, adopt=True)
+            self.table.truncate(rids[cut], np.full(cut.size, budget))
+        return moved
 
     # ---- views for the decode ---------------------------------------------------------------
 

@@ -130,7 +130,7 @@ int check_chunk(const char* who, const void* q, int dtype_q, int num_rows, int b
   a.softcap = form->softcap;
   a.window = form->window;
   a.sink = form->sink_tokens;
-  return error_word(&a.err);
+  return PKV_OK;
 }
 
 void set_split(ChunkArgs& a, const ChunkSplit& t) {
@@ -228,6 +228,8 @@ int pkv_chunk_attention(const void* q, int32_t dtype_q, int32_t num_rows, int32_
   a.ws_acc = static_cast<float*>(workspace);
   a.ws_ml = reinterpret_cast<float*>(static_cast<char*>(workspace) + space.acc);
   a.ws_rec = static_cast<char*>(workspace) + space.ml;
+  st = error_word(&a.err);
+  if (st != PKV_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   CUtensorMap tk{}, tv{};
   if (t.tc && kv == PKV_BF16) {
@@ -287,6 +289,8 @@ int pkv_chunk_weights(const void* q, int32_t dtype_q, int32_t num_rows, int32_t 
   if (!aligned16(workspace)) return set_error(PKV_EALIGN, "%s: workspace alignment", who);
   a.ws_acc = static_cast<float*>(workspace);
   a.ws_rec = static_cast<char*>(workspace) + space.ml;
+  st = error_word(&a.err);
+  if (st != PKV_OK) return st;
   a.lse = const_cast<float*>(lse);
   a.add_to = add_to;
   a.weights_out = weights_out;
