@@ -11,10 +11,11 @@
 //    tile by bulk copies, which four converter warps widen to f16 (exactly) in that form;
 //  * one MMA warp issues S = Q K^T (128 rows x 128 tokens) and O += P V, with P as an A operand in the
 //    tensor memory that held S and all accumulators there;
-//  * two groups of four softmax warps, thread r of a group owning row r. In a unit of more than 128
-//    rows group g takes rows 128 g .. of every tile: while one group works on its scores, the tensor
-//    cores have the other's P V and next S. In a smaller unit both groups have the same rows and take
-//    alternate tiles, and the two sums are merged at the unit's end;
+//  * two groups of eight softmax warps, two threads to a row: thread (h, r) of a group has tokens 64 h ..
+//    of row r's scores, and the two agree on the row's maximum through shared memory. In a unit of more
+//    than 128 rows group g takes rows 128 g .. of every tile: while one group works on its scores, the
+//    tensor cores have the other's P V and next S. In a smaller unit both groups have the same rows and
+//    take alternate tiles, and the sums are merged at the unit's end;
 //  * O is rescaled only when a row's maximum grows by more than 2^8 (P <= 2^8 until then): the final
 //    (max, sum, O) is exact whatever maximum it was accumulated against.
 //
@@ -32,6 +33,7 @@
 // Every wait is bounded (PKV_DEVERR_TIMEOUT); the tensor memory is freed on every path.
 #include <atomic>
 #include <cuda.h>
+#include <limits.h>
 #include <math.h>
 
 #include "chunk_plan.cuh"
@@ -48,8 +50,9 @@ namespace {
 
 constexpr int kTok = kChunkTcTokens;       // tokens of a tile
 constexpr int kPages = kTok / kPageSize;   // pages of a tile
-constexpr int kGroupThreads = 128;         // a softmax group: one row per thread
-constexpr int kSoftThreads = 2 * kGroupThreads;
+constexpr int kGroupRows = 128;            // rows of a softmax group
+constexpr int kGroupWarps = 8;             // its warps: four for each half of a row's scores
+constexpr int kSoftThreads = 2 * kGroupWarps * 32;
 constexpr int kMmaWarp = kSoftThreads / 32;
 constexpr int kCopyWarp = kMmaWarp + 1;    // K; the next one V (8-bit caches: one for both)
 constexpr int kConvWarp = kMmaWarp + 4;    // first of four (8-bit caches; one warp before is idle)
@@ -63,14 +66,19 @@ constexpr float kLazyLog2 = 8.f;
 // tiles of a unit in which some rows see a position that others do not: those that cross the sinks'
 // end, and those of the at most 256 positions from the first to the last row's end or window
 constexpr int kEdgeTiles = 8;
-static_assert(2 * kGroupThreads == kChunkTcRows, "a unit is two groups' rows");
+static_assert(2 * kGroupRows == kChunkTcRows, "a unit is two groups' rows");
 
 template <typename KV, int D>
 struct TcShape {
   static constexpr bool W8 = KV::bytes == 1;
   static constexpr int THREADS = 32 * (W8 ? kConvWarp + kConvThreads / 32 : kConvWarp);
-  // registers of the softmax warps and of the others, out of what the launch gives every warp
-  static constexpr int SOFT_REGS = W8 ? 184 : 208, REGS = W8 ? 72 : 88;
+  // registers of the softmax warps, of MMA and copies, and of the converters, out of what the launch
+  // gives every warp
+  static constexpr int LAUNCH_REGS = W8 ? 80 : 96;
+  static constexpr int SOFT_REGS = W8 ? 88 : 104, REGS = W8 ? 48 : 64, CONV_REGS = 80;
+  static_assert(kSoftThreads * SOFT_REGS + 128 * REGS + (W8 ? 128 * CONV_REGS : 0) <=
+                    THREADS * LAUNCH_REGS,
+                "the split takes no more registers than the launch brings");
   static constexpr int TILE = kTok * D * 2;       // K (or V) of a tile in MMA form
   static constexpr int NK = 64 * 1024 / TILE, NV = NK;
   static constexpr int RAW = kTok / 2 * D;        // codes of half a tile's K or V
@@ -78,16 +86,18 @@ struct TcShape {
   static constexpr int OFF_V = NK * TILE;
   static constexpr int OFF_RAW = OFF_V + NV * TILE;
   static constexpr int OFF_Q = OFF_RAW + NR * RAW;
-  static constexpr int Q_GROUP = kGroupThreads * D * 2;
-  static constexpr int OFF_ML = OFF_Q + 2 * Q_GROUP;               // [2][128] (max, sum)
-  static constexpr int OFF_BAR = OFF_ML + kSoftThreads * 8;
-  static constexpr int BARS = 2 * NK + 2 * NV + 2 * NR + 2 * 4 + 3 + kRuns;
+  static constexpr int Q_GROUP = kGroupRows * D * 2;
+  static constexpr int OFF_HALF = OFF_Q + 2 * Q_GROUP;             // [2][2][128] of the half rows
+  static constexpr int OFF_REF = OFF_HALF + kSoftThreads * 4;      // [2][128] the rows' maxima
+  static constexpr int OFF_FAC = OFF_REF + 2 * kGroupRows * 4;     // [2][128] score factors (8-bit)
+  static constexpr int OFF_BAR = OFF_FAC + (W8 ? 2 * kGroupRows * 4 : 0);
+  static constexpr int BARS = 2 * NK + 2 * NV + 2 * NR + 2 * 4 + 8 + 3 + kRuns;
   static_assert(NK + (NR + 3) / 4 + 3 <= kRuns, "runs in flight");
-  static constexpr int OFF_MISC = OFF_BAR + 8 * BARS;              // masks, bad rows, TMEM address
+  static constexpr int OFF_MISC = OFF_BAR + 8 * BARS;              // masks, TMEM address
   static constexpr uint32_t IDESC_S = tc_idesc(128, kTok, false, W8);
   static constexpr uint32_t IDESC_PV = tc_idesc(128, D, true, W8);
-  static constexpr int SMEM = 1024 + OFF_MISC + 4 * (NV + NR + 2 * kEdgeTiles * 4 + 1) + 16;
-  static_assert(SMEM <= 225 * 1024 && SMEM > 114 * 1024, "one CTA per SM");
+  static constexpr int SMEM = 1024 + OFF_MISC + 4 * (NV + NR + 1) + 16;
+  static_assert(SMEM <= 223 * 1024 && SMEM > 114 * 1024, "one CTA per SM");
 };
 
 template <bool F16>
@@ -139,19 +149,22 @@ __global__ void __launch_bounds__(TcShape<KV, D>::THREADS, 1) chunk_tc_kernel(
   uint64_t* p_ready = s_done + 2;                                    // [2] its P
   uint64_t* o_done = p_ready + 2;                                    // [2] a group's last P V of a run
   uint64_t* q_ready = o_done + 2;                                    // [2] Q of a run stored
-  uint64_t* met = q_ready + 2;         // both groups ended a run
+  uint64_t* paired = q_ready + 2;      // [2][4] the two warps of 32 rows have left word of a half row
+  uint64_t* met = paired + 8;          // both groups ended a small run
   uint64_t* parted = met + 1;          // and are done with what the other reads or writes
   uint64_t* mma_idle = parted + 1;
   uint64_t* run_there = mma_idle + 1;  // [kRuns]
   int* page_mask = reinterpret_cast<int*>(smem + S::OFF_MISC);       // [NV] good pages of the tile
   int* raw_mask = page_mask + NV;                                    // [NR] of the half tile
-  uint32_t* bad_rows = reinterpret_cast<uint32_t*>(raw_mask + NR);   // [2][edge tile][4]: not finite
-  uint32_t* s_taddr = bad_rows + 2 * kEdgeTiles * 4;
-  float2* ml = reinterpret_cast<float2*>(smem + S::OFF_ML);
+  uint32_t* s_taddr = reinterpret_cast<uint32_t*>(raw_mask + NR);
+  float* half_row = reinterpret_cast<float*>(smem + S::OFF_HALF);
+  float* row_max = reinterpret_cast<float*>(smem + S::OFF_REF);
+  float* row_fac = reinterpret_cast<float*>(smem + S::OFF_FAC);
 
   __shared__ int scratch[64];
   __shared__ ChunkShare share;
   __shared__ ChunkRun runs[kRuns];  // (n = 0: the share's end)
+  __shared__ uint32_t bad_rows[kRuns][kEdgeTiles * 4];  // of a run's edge tiles: V row not finite
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (threadIdx.x == kCopyWarp * 32) {
     for (int s = 0; s < NK; ++s) {
@@ -168,9 +181,10 @@ __global__ void __launch_bounds__(TcShape<KV, D>::THREADS, 1) chunk_tc_kernel(
     }
     for (int g = 0; g < 2; ++g) {
       mbar_init(&s_done[g], 1);
-      mbar_init(&p_ready[g], kGroupThreads / 32);
+      mbar_init(&p_ready[g], kGroupWarps);
       mbar_init(&o_done[g], 1);
-      mbar_init(&q_ready[g], kGroupThreads / 32);
+      mbar_init(&q_ready[g], kGroupWarps);
+      for (int w = 0; w < 4; ++w) mbar_init(&paired[4 * g + w], 2);
     }
     mbar_init(met, kSoftThreads / 32);
     mbar_init(parted, kSoftThreads / 32);
@@ -182,7 +196,6 @@ __global__ void __launch_bounds__(TcShape<KV, D>::THREADS, 1) chunk_tc_kernel(
       asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm_v)) : "memory");
     }
   }
-  if (threadIdx.x < 2 * kEdgeTiles * 4) bad_rows[threadIdx.x] = 0;
   chunk_share<S::THREADS>(a, scratch, &share);
   if (share.count == 0) {  // (the whole CTA)
     if (threadIdx.x == 0)
@@ -208,7 +221,7 @@ __global__ void __launch_bounds__(TcShape<KV, D>::THREADS, 1) chunk_tc_kernel(
   };
   // Steps of a run: wide (more than 128 rows): step u is tile u / 2 for group u % 2, otherwise tile u
   // for group u % 2. Every barrier of a group completes once per step of its own.
-  auto is_wide = [](const ChunkRun* run) { return uniform(run->rows) > kGroupThreads; };
+  auto is_wide = [](const ChunkRun* run) { return uniform(run->rows) > kGroupRows; };
 
   if (warp >= kMmaWarp && warp < kConvWarp) {
     regs_down<S::REGS>();
@@ -229,6 +242,8 @@ __global__ void __launch_bounds__(TcShape<KV, D>::THREADS, 1) chunk_tc_kernel(
         const ChunkRun* run = nullptr;
         if (is_k) {  // (a wait that gave up ends the share for every warp)
           ChunkRun* r = &runs[unit % kRuns];
+          bad_rows[unit % kRuns][lane] = 0;
+          __syncwarp();
           if (lane == 0) {
             if (!ok || !walk.next(a, *r)) r->n = 0;
             mbar_arrive(&run_there[unit % kRuns]);
@@ -354,7 +369,7 @@ __global__ void __launch_bounds__(TcShape<KV, D>::THREADS, 1) chunk_tc_kernel(
         __syncwarp();
         if (last_use) ks.advance(1);
       };
-      static_assert(kTok == kGroupThreads, "Q and K tiles have one form");
+      static_assert(kTok == kGroupRows && kEdgeTiles * 4 == 32, "Q and K tiles have one form");
       auto pv_mma = [&](int group, bool first, bool last_use, bool last_step) {
         const uint64_t vd = v_desc + (uint32_t)(vs.st * (S::TILE >> 4));
         const uint32_t pc = tmem + 256 + 128 * group, o = tmem + 128 * group;
@@ -398,7 +413,7 @@ __global__ void __launch_bounds__(TcShape<KV, D>::THREADS, 1) chunk_tc_kernel(
   } else if (warp >= kConvWarp) {
     // ===================== 8-bit codes to f16 in MMA form =====================
     if constexpr (W8) {
-      regs_down<S::REGS>();
+      static_assert(S::CONV_REGS == S::LAUNCH_REGS, "no change");
       constexpr int CPR = D / 16;                          // 16-code chunks of a row
       constexpr int PER = kTok / 2 * CPR / kConvThreads;   // chunks of a thread in half a tile
       const int i0 = threadIdx.x - kConvWarp * 32;
@@ -475,57 +490,84 @@ __global__ void __launch_bounds__(TcShape<KV, D>::THREADS, 1) chunk_tc_kernel(
   } else {
     // ===================== softmax =====================
     regs_up<S::SOFT_REGS>();
-    const int wg = warp >> 2;             // group
-    const int r = threadIdx.x & 127;      // row of the group
-    const uint32_t lane_t = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-    const uint32_t scol = lane_t + 256 + 128 * wg, ocol = lane_t + 128 * wg;
+    const int wg = warp >> 3, h = (warp >> 2) & 1, quad = warp & 3;  // group, half of a row, rows / 32
+    const int r = quad * 32 + lane;                                  // row of the group
+    const uint32_t lane_t = tmem + ((uint32_t)(quad * 32) << 16);
+    const uint32_t s_all = lane_t + 256 + 128 * wg;
+    const uint32_t scol = s_all + 64 * h, pcol = s_all + 32 * h, ocol = lane_t + 128 * wg;
+    uint64_t* const pair = &paired[4 * wg + quad];
+    float* const mine = half_row + (2 * wg + h) * kGroupRows + r;
+    const float* const theirs = half_row + (2 * wg + 1 - h) * kGroupRows + r;
     bool ok = true;
-    uint32_t unit = 0, ph_s = 0, ph_o = 0;  // parities of s_done's and o_done's next phases
-    Place<NV> base;                         // V of the run's first tile
+    uint32_t unit = 0, ph_s = 0, ph_o = 0, ph_pair = 0, ph_met = 0;  // parities of the next phases
+    Place<NV> base;                                                  // V of the run's first tile
+    // What this warp says in shared memory and the other warp of its rows, exchanged.
+    auto exchange = [&](float x) {
+      *mine = x;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(pair);
+      ok = mbar_wait(pair, ph_pair, a.err);
+      ok = __all_sync(0xffffffffu, ok);
+      ph_pair ^= 1u;
+      return *theirs;
+    };
     // The row of this thread in a run (row `row` of its unit, at position pq), its offset in q and
-    // out in rows, and its score factor (log2 domain).
+    // out in rows.
     struct Row {
       int row, pq;
       size_t at;
       bool live;
-      float sc, slope;
+      float slope;
     };
     auto find_row = [&](const ChunkRun& run) {
       Row x;
-      x.row = (run.rows > kGroupThreads ? wg * kGroupThreads : 0) + r;
+      x.row = (run.rows > kGroupRows ? wg * kGroupRows : 0) + r;
       x.live = x.row < run.rows;
       const unsigned R = x.live ? x.row : 0, t = R / (unsigned)run.heads;
       x.pq = run.req.base + run.t0 + (int)t;
-      x.at = chunk_row(a, run, (int)R);
-      x.sc = a.scale * kLog2e * (W8 ? a.k_scales[run.j] : 1.f);
+      x.at = (size_t)(run.req.q0 + run.t0 + (int)t) * a.h_q + run.j * a.group + run.g0 +
+             (R - t * run.heads);
       x.slope = FORM && a.slopes ? a.slopes[run.j * a.group + run.g0 + R - t * run.heads] * kLog2e : 0.f;
       return x;
     };
-    // A run's queries: four lanes read 64 consecutive bytes of a row, eight rows an instruction, and
-    // put them into shared memory in MMA form once the S of the last run are done.
+    // A run's queries go straight into shared memory in MMA form while the last step of the run before
+    // is worked on, 16 rows a warp, four lanes copying 64 consecutive bytes of a row; for an 8-bit cache
+    // the lanes that copied a row then make f16 of it and leave its score factor.
     constexpr int RND = D / 32;  // rounds of 64 bytes
-    auto load_query = [&](const Row& x, uint4 (&in)[RND][4]) {
+    const int row0 = quad * 32 + 16 * h + (lane >> 2);  // rows row0 and row0 + 8 of the group
+    const uint32_t q_at = ring + S::OFF_Q + wg * S::Q_GROUP + row0 * 128;
+    auto q_chunk = [&](int d, int g) {
+      return q_at + (d >> 1) * (kGroupRows * 128) + g * 1024 +
+             ((((4 * d & 7) + (lane & 3)) ^ (row0 & 7)) << 4);
+    };
+    auto load_query = [&](const Row& x) {
 #pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        const int from = 8 * g + (lane >> 2);
+      for (int g = 0; g < 2; ++g) {
+        const int from = 16 * h + 8 * g + (lane >> 2);
         const size_t at = __shfl_sync(0xffffffffu, (unsigned long long)x.at, from);
         const bool there = __shfl_sync(0xffffffffu, (int)x.live, from) != 0;
-        const uint4* src = reinterpret_cast<const uint4*>(
-                               static_cast<const __nv_bfloat16*>(a.q) + at * D) + (lane & 3);
+        const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(a.q) + at * D + 8 * (lane & 3);
 #pragma unroll
-        for (int d = 0; d < RND; ++d) in[d][g] = there ? src[4 * d] : make_uint4(0, 0, 0, 0);
+        for (int d = 0; d < RND; ++d)
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(q_chunk(d, g)),
+                       "l"(src + 32 * d), "r"(there ? 16 : 0)
+                       : "memory");
       }
     };
-    auto store_query = [&](Row& x, uint4 (&in)[RND][4]) {
-      if constexpr (W8) query_to_f16<RND>(in, x.sc, x.sc);
-      const int row0 = (warp & 3) * 32 + (lane >> 2);  // rows row0 + 8 g of the group
-      const uint32_t at = ring + S::OFF_Q + wg * S::Q_GROUP + row0 * 128;
+    auto store_query = [&](const ChunkRun& run) {
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      if constexpr (W8) {
+        const float sc = a.scale * kLog2e * a.k_scales[run.j];
 #pragma unroll
-      for (int d = 0; d < RND; ++d) {
-        const uint32_t ch = (((4 * d & 7) + (lane & 3)) ^ (row0 & 7)) << 4;
+        for (int g = 0; g < 2; ++g) {
+          uint4 in[RND];
 #pragma unroll
-        for (int g = 0; g < 4; ++g)
-          sts128(at + (d >> 1) * (kGroupThreads * 128) + g * 1024 + ch, in[d][g]);
+          for (int d = 0; d < RND; ++d) in[d] = lds128(q_chunk(d, g));
+          const float factor = query_to_f16<RND>(in, sc);
+#pragma unroll
+          for (int d = 0; d < RND; ++d) sts128(q_chunk(d, g), in[d]);
+          if ((lane & 3) == 0) row_fac[wg * kGroupRows + row0 + 8 * g] = factor;
+        }
       }
       fence_proxy_async_smem();
       __syncwarp();
@@ -534,24 +576,29 @@ __global__ void __launch_bounds__(TcShape<KV, D>::THREADS, 1) chunk_tc_kernel(
     Row me{};
     const ChunkRun* next = get_run(0);
     if (next) {
-      uint4 in[RND][4];
       me = find_row(*next);
-      load_query(me, in);
-      store_query(me, in);
+      load_query(me);
+      store_query(*next);
     }
+    float sc = a.scale * kLog2e;  // of the row's scores (log2 domain)
     for (; next; ++unit) {
       const ChunkRun& run = *next;
-      const bool wide = run.rows > kGroupThreads;
+      const bool wide = run.rows > kGroupRows;
       const bool live = me.live;
-      const float sc = me.sc;
       const int ctx = run.req.base + run.req.n;
       const int stride = wide ? 1 : 2;  // tiles between this group's steps
-      uint32_t* const bad = bad_rows + (unit & 1) * (kEdgeTiles * 4);
+      uint32_t* const bad = bad_rows[unit % kRuns];
+      // tiles that begin behind edge_from, or before edge_win and not wholly among the sinks, have
+      // positions that some rows do not see (chunk_edge)
+      const int edge_from = run.req.base + run.t0 - kTok + 1;
+      const int edge_win = a.window > 0 ? run.req.base + run.t0 + run.tokens - a.window : INT_MIN;
       float m_used = -INFINITY, l = 0.f;
       Place<NV> at = base;
       if (!wide) at.advance(wg);
       const int i_first = wide ? 0 : wg;
       const bool any = i_first < run.n;  // the group has a step in the run
+      Row then{};
+      const ChunkRun* after = nullptr;
       for (int i = i_first; ok && i < run.n; i += stride) {
         const int p0 = run.tiles[run.i0 + i] * kTok;
         // V of the tile too: what it says of its pages, and rows of it may have to be mended
@@ -561,41 +608,49 @@ __global__ void __launch_bounds__(TcShape<KV, D>::THREADS, 1) chunk_tc_kernel(
         ph_s ^= 1u;
         const int mask = page_mask[at.st];
         tc_fence_after();
-        uint32_t sr[kTok];
-#pragma unroll
-        for (int c = 0; c < kTok; c += 32)
-          tmem_ld32(scol + c, *reinterpret_cast<uint32_t(*)[32]>(&sr[c]));
+        uint32_t sr[64];
+        tmem_ld32(scol, *reinterpret_cast<uint32_t(*)[32]>(&sr[0]));
+        tmem_ld32(scol + 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[32]));
+        if constexpr (W8) {
+          if (i == i_first) sc = row_fac[wg * kGroupRows + r];
+        }
+        if (i + stride >= run.n) {  // the group's last S of the run: its queries are used up
+          after = get_run(unit + 1);
+          if (after) {
+            then = find_row(*after);
+            load_query(then);
+          }
+        }
         tmem_wait_ld();
         if constexpr (FORM) {  // the scores themselves, log2 domain
           const bool cap = a.softcap > 0.f;
           const float in = cap ? sc * (kLn2 / a.softcap) : sc, top = a.softcap * kLog2e;
-          // (distances of two positions side by side: pairs)
-          const float far0 = (float)(p0 - me.pq);
+          const float far0 = (float)(p0 + 64 * h - me.pq);
 #pragma unroll
-          for (int k = 0; k < kTok; ++k) {
+          for (int k = 0; k < 64; ++k) {
             float x = __uint_as_float(sr[k]) * in;
             if (cap) x = top * tanh_of(x);
             sr[k] = __float_as_uint(fmaf(me.slope, far0 + (float)k, x));
           }
         }
-        const bool edge = chunk_edge(a, run, p0, kTok);
+        const bool edge = p0 > edge_from || (p0 < edge_win && p0 + kTok > a.sink);
         if (edge || mask != (1 << kPages) - 1) {
+          uint64_t seen = live ? chunk_seen(a, me.pq, p0 + 64 * h) : 0ull;
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            uint64_t seen = live ? chunk_seen(a, me.pq, p0 + 64 * h) : 0ull;
+          for (int p = 0; p < 4; ++p)
+            if (!((mask >> (4 * h + p)) & 1)) seen &= ~(0xffffull << (16 * p));
 #pragma unroll
-            for (int p = 0; p < 4; ++p)
-              if (!((mask >> (4 * h + p)) & 1)) seen &= ~(0xffffull << (16 * p));
-#pragma unroll
-            for (int k = 0; k < 64; ++k)
-              if (!((seen >> k) & 1)) sr[64 * h + k] = __float_as_uint(-INFINITY);
-          }
-          // Mend V, a thread to a row. In a wide unit both groups do (and write every row they mend):
-          // each group's P V waits for its own group only.
-          constexpr int CH = D / 8;  // 16-byte chunks of a row
-          const uint32_t vrow =
-              ring + S::OFF_V + at.st * S::TILE + (r >> 4) * PAGE_MMA + (r & 15) * 128;
-          auto chunk_at = [&](int c) { return vrow + (c >> 3) * 2048 + (((c & 7) ^ (r & 7)) << 4); };
+          for (int k = 0; k < 64; ++k)
+            if (!((seen >> k) & 1)) sr[k] = __float_as_uint(-INFINITY);
+          // Mend V, two threads to a row. In a wide unit both groups do (and write every row they
+          // mend): each group's P V waits for its own group only. A row is noted before it is mended:
+          // who finds it mended finds the note.
+          constexpr int CH = D / 16;  // 16-byte chunks of half a row
+          const uint32_t vrow = ring + S::OFF_V + at.st * S::TILE + (r >> 4) * PAGE_MMA + (r & 15) * 128;
+          auto chunk_at = [&](int c) {
+            const int k = CH * h + c;
+            return vrow + (k >> 3) * 2048 + (((k & 7) ^ (r & 7)) << 4);
+          };
           if (p0 + r >= ctx || !((mask >> (r >> 4)) & 1)) {
 #pragma unroll
             for (int c = 0; c < CH; ++c) sts128(chunk_at(c), make_uint4(0, 0, 0, 0));
@@ -610,6 +665,11 @@ __global__ void __launch_bounds__(TcShape<KV, D>::THREADS, 1) chunk_tc_kernel(
               z = add_zero_times<W8>(x.w, z);
             }
             if (not_finite<W8>(z) || not_finite<W8>(z >> 16)) {
+              int e = 0;  // which of the run's edge tiles this is
+              for (int k = 0; k < i; ++k)
+                e += chunk_edge(a, run, run.tiles[run.i0 + k] * kTok, kTok) ? 1 : 0;
+              if (e < kEdgeTiles) atomicOr(&bad[4 * e + (r >> 5)], 1u << (r & 31));
+              __threadfence_block();
 #pragma unroll 1
               for (int c = 0; c < CH; ++c) {
                 uint4 x = lds128(chunk_at(c));
@@ -621,10 +681,6 @@ __global__ void __launch_bounds__(TcShape<KV, D>::THREADS, 1) chunk_tc_kernel(
                 }
                 sts128(chunk_at(c), x);
               }
-              int e = 0;  // which of the run's edge tiles this is
-              for (int k = 0; k < i; ++k)
-                e += chunk_edge(a, run, run.tiles[run.i0 + k] * kTok, kTok) ? 1 : 0;
-              if (e < kEdgeTiles) atomicOr(&bad[4 * e + (r >> 5)], 1u << (r & 31));
             }
           }
           fence_proxy_async_smem();
@@ -633,15 +689,17 @@ __global__ void __launch_bounds__(TcShape<KV, D>::THREADS, 1) chunk_tc_kernel(
 #pragma unroll
         for (int k = 0; k < 4; ++k) mx4[k] = __uint_as_float(sr[k]);
 #pragma unroll
-        for (int k = 4; k < 124; k += 8) {
+        for (int k = 4; k < 60; k += 8) {
 #pragma unroll
           for (int m = 0; m < 4; ++m)
             mx4[m] = max3(mx4[m], __uint_as_float(sr[k + 2 * m]), __uint_as_float(sr[k + 2 * m + 1]));
         }
         float mx = max3(max3(mx4[0], mx4[1], mx4[2]),
-                        max3(mx4[3], __uint_as_float(sr[124]), __uint_as_float(sr[125])),
-                        fmaxf(__uint_as_float(sr[126]), __uint_as_float(sr[127])));
+                        max3(mx4[3], __uint_as_float(sr[60]), __uint_as_float(sr[61])),
+                        fmaxf(__uint_as_float(sr[62]), __uint_as_float(sr[63])));
         if constexpr (!FORM) mx *= sc;
+        mx = fmaxf(mx, exchange(mx));  // (both halves' scores have left S, where P goes)
+        if (!ok) break;
         // s sc - m is one FMA below: m is a rounded product, the product in the FMA is not, so that a row's
         // weights are all off by one factor, which their sum shares: up to 2^0.5 for |m| <= 2^24. For
         // larger m it would soon leave f16's range and then every range: there s sc is rounded as m is.
@@ -651,51 +709,49 @@ __global__ void __launch_bounds__(TcShape<KV, D>::THREADS, 1) chunk_tc_kernel(
         // past 2^8 (the difference, not a sum: past 2^26 that would round to several times as far).
         const bool first = i == i_first;
         const bool moved = !first && mx - m_used > kLazyLog2;
+        float factor = FORM ? 1.f : sc;
         if (__any_sync(0xffffffffu, moved || huge)) {  // (one vote for the two: most steps have neither)
           if (__any_sync(0xffffffffu, moved)) {
-            // rescale this warp's rows of O: this step's S was issued after the last P V, and is there
+            // rescale half the dims of this warp's rows of O: this step's S was issued after the last
+            // P V, and is there
             const float m_new = moved ? mx : m_used;
             const float alpha = moved ? exp2f(m_used - m_new) : 1.f;
-#pragma unroll
-            for (int cb = 0; cb < D / 32; ++cb) {
-              uint32_t o[32];
-              tmem_ld32(ocol + 32 * cb, o);
+#pragma unroll 1
+            for (int c = h * (D / 2); c < (h + 1) * (D / 2); c += 16) {
+              uint32_t o[16];
+              tmem_ld16(ocol + c, o);
               tmem_wait_ld();
 #pragma unroll
-              for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
-              tmem_st32(ocol + 32 * cb, o);
+              for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
+              tmem_st16(ocol + c, o);
             }
             l *= alpha;
             m_used = m_new;
           }
           if (__any_sync(0xffffffffu, huge)) {
 #pragma unroll
-            for (int k = 0; k < kTok; ++k)
+            for (int k = 0; k < 64; ++k)
               sr[k] = __float_as_uint(__fmul_rn(__uint_as_float(sr[k]), sc));
+            factor = 1.f;
           }
         }
         if (first) m_used = mx;
-        const float factor = FORM || __any_sync(0xffffffffu, huge) ? 1.f : sc;
-        // P = 2^(s - m) over the first 64 columns of S
+        // P = 2^(s - m), the two halves over the first 64 columns of S
         const float m_use = m_used == -INFINITY ? 0.f : m_used;
         uint64_t sum[4] = {0, 0, 0, 0};  // (pairs of zeros)
         const uint64_t sc2 = pack2(factor, factor), m2 = pack2(-m_use, -m_use);
+        uint32_t pw[32];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint32_t pw[32];
-#pragma unroll
-          for (int k = 0; k < 32; ++k) {
-            float e0, e1;
-            unpack2(fma2(pack2(__uint_as_float(sr[64 * h + 2 * k]),
-                               __uint_as_float(sr[64 * h + 2 * k + 1])), sc2, m2),
-                    e0, e1);
-            e0 = ex2_approx(e0);
-            e1 = ex2_approx(e1);
-            sum[k & 3] = add2(sum[k & 3], pack2(e0, e1));
-            pw[k] = pack_p<W8>(e0, e1);
-          }
-          tmem_st32(scol + 32 * h, pw);
+        for (int k = 0; k < 32; ++k) {
+          float e0, e1;
+          unpack2(fma2(pack2(__uint_as_float(sr[2 * k]), __uint_as_float(sr[2 * k + 1])), sc2, m2),
+                  e0, e1);
+          e0 = ex2_approx(e0);
+          e1 = ex2_approx(e1);
+          sum[k & 3] = add2(sum[k & 3], pack2(e0, e1));
+          pw[k] = pack_p<W8>(e0, e1);
         }
+        tmem_st32(pcol, pw);
         float s0, s1;
         unpack2(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), s0, s1);
         l += s0 + s1;
@@ -707,125 +763,160 @@ __global__ void __launch_bounds__(TcShape<KV, D>::THREADS, 1) chunk_tc_kernel(
       }
       // ---- the run's rows ----
       // the next run's queries first, so that its first scores run while this one's rows are written
-      next = get_run(unit + 1);
-      Row then{};
-      if (next) {
-        uint4 in[RND][4];
-        then = find_row(*next);
-        load_query(then, in);
-        store_query(then, in);
+      if (!any || !ok) {
+        after = get_run(unit + 1);
+        if (after) {
+          then = find_row(*after);
+          load_query(then);
+        }
       }
+      if (after) store_query(*after);
       if (ok && any) {
         ok = mbar_wait(&o_done[wg], ph_o, a.err);
         ok = __all_sync(0xffffffffu, ok);
       }
       if (any) ph_o ^= 1u;
-      if (!wide) ml[wg * kGroupThreads + r] = make_float2(m_used, l);
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(met);
-      ok = mbar_wait(met, unit & 1, a.err) && ok;
-      ok = __all_sync(0xffffffffu, ok);
       tc_fence_after();
-      if (threadIdx.x < kEdgeTiles * 4) bad_rows[((unit + 1) & 1) * (kEdgeTiles * 4) + threadIdx.x] = 0;
-      // wide: the group's own rows, all dims; else group wg writes dims wg D/2 .. of every row, from
-      // both groups' sums
-      float M = m_used, L = l, w0 = 1.f, w1 = 0.f;
-      if (!wide) {
-        const float2 x = ml[r], y = ml[kGroupThreads + r];
-        M = fmaxf(x.x, y.x);
+      // The row's maximum and sum; wide: over the group's two halves, and warp (group, h) writes dims
+      // h D/2 .. of its rows; else over both groups' halves, and it writes dims 32 (2 group + h) ...
+      float M = m_used, L, w0 = 1.f, w1 = 0.f;
+      if (wide) {
+        const float x = exchange(l);
+        L = h == 0 ? l + x : x + l;
+      } else {
+        *mine = l;
+        if (h == 0) row_max[wg * kGroupRows + r] = m_used;
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(met);
+        ok = mbar_wait(met, ph_met, a.err) && ok;
+        ok = __all_sync(0xffffffffu, ok);
+        tc_fence_after();
+        const float m0 = row_max[r], m1 = row_max[kGroupRows + r];
+        M = fmaxf(m0, m1);
         const float Mu = M == -INFINITY ? 0.f : M;
-        w0 = exp2f(x.x - Mu);
-        w1 = exp2f(y.x - Mu);
-        L = w0 * x.y + w1 * y.y;
+        w0 = exp2f(m0 - Mu);
+        w1 = exp2f(m1 - Mu);
+        L = w0 * (half_row[r] + half_row[kGroupRows + r]) +
+            w1 * (half_row[2 * kGroupRows + r] + half_row[3 * kGroupRows + r]);
       }
       const float vs = W8 ? a.v_scales[run.j] : 1.f;
       const float f = run.whole ? (L != 0.f ? vs / L : 0.f) : vs;
-      uint32_t any_bad = 0;
-#pragma unroll
-      for (int k = 0; k < kEdgeTiles * 4; ++k) any_bad |= bad[k];
-      const size_t part = ((size_t)blockIdx.x * 2 + run.slot) * kChunkTcRows + me.row;
-      auto emit = [&](int c, uint32_t (&o)[32]) {  // 32 dims from c on of this thread's row
-        if (any_bad && live) {  // the infinite and NaN values of the positions this row sees
-          int e = 0;
-          for (int k = 0; k < run.n && e < kEdgeTiles; ++k) {
-            const int q0 = run.tiles[run.i0 + k] * kTok;
-            if (!chunk_edge(a, run, q0, kTok)) continue;
-            for (int x = 0; x < kTok; ++x) {
-              const int pos = q0 + x;
-              if (!((bad[4 * e + (x >> 5)] >> (x & 31)) & 1) || !(chunk_seen(a, me.pq, pos) & 1))
-                continue;
-              const int id = a.block_tables[(size_t)run.b * a.max_pages + pos / kPageSize];
-              const uint8_t* v =
-                  static_cast<const uint8_t*>(a.v_cache) +
-                  ((((int64_t)id * a.h_kv + run.j) * kPageSize + pos % kPageSize) * D + c) * KV::bytes;
-#pragma unroll
-              for (int d = 0; d < 32; d += 4) {
-                float y[4];
-                RowLoad<KV, 4>::run(v + d * KV::bytes, y);
-#pragma unroll
-                for (int m = 0; m < 4; ++m)
-                  if (!(fabsf(y[m]) < INFINITY))
-                    o[d + m] = __float_as_uint(__uint_as_float(o[d + m]) + y[m]);
-              }
-            }
-            ++e;
-          }
-        }
-        if (!live) return;
-        if (run.whole) {
-          uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + me.at * D + c);
-#pragma unroll
-          for (int k = 0; k < 32; k += 8) {
-            uint32_t v[4];
-#pragma unroll
-            for (int m = 0; m < 4; ++m)
-              v[m] = L != 0.f ? pack_bf16(__uint_as_float(o[k + 2 * m]) * f,
-                                          __uint_as_float(o[k + 2 * m + 1]) * f)
-                              : 0u;
-            dst[k / 8] = make_uint4(v[0], v[1], v[2], v[3]);
-          }
-        } else {
-          float4* dst = reinterpret_cast<float4*>(a.ws_acc + part * D + c);
-#pragma unroll
-          for (int k = 0; k < 32; k += 4)
-            dst[k / 4] = make_float4(__uint_as_float(o[k]) * f, __uint_as_float(o[k + 1]) * f,
-                                     __uint_as_float(o[k + 2]) * f, __uint_as_float(o[k + 3]) * f);
-        }
-        if (c == 0) {
-          if (!run.whole)
-            *reinterpret_cast<float2*>(a.ws_ml + 2 * part) = make_float2(M, L);
-          else if (a.lse)
-            a.lse[me.at] = L != 0.f ? (M + log2f(L)) * kLn2 : -INFINITY;
-        }
-      };
-      if (ok) {
-        const int c_lo = wide ? 0 : wg * (D / 2), c_hi = wide ? D : c_lo + D / 2;
+      const bool none = run.whole && L == 0.f;
+      const bool any_bad = __any_sync(0xffffffffu, bad[lane] != 0);
+      const size_t part0 = ((size_t)blockIdx.x * 2 + run.slot) * kChunkTcRows;
+      if (ok && live && h == 0 && (wide || wg == 0)) {
+        if (!run.whole)
+          *reinterpret_cast<float2*>(a.ws_ml + 2 * (part0 + me.row)) = make_float2(M, L);
+        else if (a.lse)
+          a.lse[me.at] = L != 0.f ? (M + log2f(L)) * kLn2 : -INFINITY;
+      }
+      // O in blocks of 16 rows x 32 dims: a lane has dims 8 n + 2 (lane % 4) + {0, 1}, n < 4, of rows
+      // lane / 4 and lane / 4 + 8, so that four lanes write a row's 64 (bf16) or 32 (fp32) consecutive
+      // bytes
+      const int c_lo = wide ? h * (D / 2) : 32 * (2 * wg + h);
+      const int c_hi = min(D, c_lo + (wide ? D / 2 : 32));
+      const int q4 = lane & 3;
+      for (int b16 = 0; ok && c_lo < D && b16 < 2; ++b16) {
+        if (!__any_sync(0xffffffffu, live && (lane >> 4) == b16)) break;  // (rows are in order)
+        // (with the rows' factors, offsets, parts)
+        const int ra = 16 * b16 + (lane >> 2), rb = ra + 8;
+        const float fa = __shfl_sync(0xffffffffu, f, ra), fb = __shfl_sync(0xffffffffu, f, rb);
+        const float w0a = __shfl_sync(0xffffffffu, w0, ra), w0b = __shfl_sync(0xffffffffu, w0, rb);
+        const float w1a = __shfl_sync(0xffffffffu, w1, ra), w1b = __shfl_sync(0xffffffffu, w1, rb);
+        const size_t at_a = __shfl_sync(0xffffffffu, (unsigned long long)me.at, ra);
+        const size_t at_b = __shfl_sync(0xffffffffu, (unsigned long long)me.at, rb);
+        const uint32_t lives = __ballot_sync(0xffffffffu, live);
+        const uint32_t nones = __ballot_sync(0xffffffffu, none);
+        const bool live_a = (lives >> ra) & 1, live_b = (lives >> rb) & 1;
+        const bool none_a = (nones >> ra) & 1, none_b = (nones >> rb) & 1;
         for (int c = c_lo; c < c_hi; c += 32) {
-          uint32_t o[32];
-          tmem_ld32((wide ? ocol : lane_t) + c, o);
+          uint32_t o[16];
+          const uint32_t rows_t = ((uint32_t)(16 * b16) << 16) + c;
+          tmem_ld_16x256(( wide ? ocol : lane_t) + rows_t, o);
           tmem_wait_ld();
-          if (!wide) {
-            if (run.n > 1) {
-              uint32_t o1[32];
-              tmem_ld32(lane_t + 128 + c, o1);
-              tmem_wait_ld();
+          if (!wide && run.n > 1) {
+            uint32_t o1[16];
+            tmem_ld_16x256(lane_t + 128 + rows_t, o1);
+            tmem_wait_ld();
 #pragma unroll
-              for (int k = 0; k < 32; ++k)
-                o[k] = __float_as_uint(w0 * __uint_as_float(o[k]) + w1 * __uint_as_float(o1[k]));
+            for (int k = 0; k < 16; ++k) {
+              const float x0 = k & 2 ? w0b : w0a, x1 = k & 2 ? w1b : w1a;
+              o[k] = __float_as_uint(x0 * __uint_as_float(o[k]) + x1 * __uint_as_float(o1[k]));
             }
           }
-          emit(c, o);
+          if (any_bad) {  // the infinite and NaN values of the positions that a row sees
+            const int pq_a = __shfl_sync(0xffffffffu, me.pq, ra), pq_b = __shfl_sync(0xffffffffu, me.pq, rb);
+            int e = 0;
+            for (int k = 0; k < run.n && e < kEdgeTiles; ++k) {
+              const int q0 = run.tiles[run.i0 + k] * kTok;
+              if (!chunk_edge(a, run, q0, kTok)) continue;
+              for (int x = 0; x < kTok; ++x) {
+                if (!((bad[4 * e + (x >> 5)] >> (x & 31)) & 1)) continue;
+                const int pos = q0 + x;
+                const bool see_a = chunk_seen(a, pq_a, pos) & 1, see_b = chunk_seen(a, pq_b, pos) & 1;
+                const int id = a.block_tables[(size_t)run.b * a.max_pages + pos / kPageSize];
+                const uint8_t* v = static_cast<const uint8_t*>(a.v_cache) +
+                                   ((((int64_t)id * a.h_kv + run.j) * kPageSize + pos % kPageSize) * D +
+                                    c + 2 * q4) * KV::bytes;
+#pragma unroll
+                for (int n = 0; n < 4; ++n) {
+                  float y[2];
+                  RowLoad<KV, 2>::run(v + 8 * n * KV::bytes, y);
+#pragma unroll
+                  for (int m = 0; m < 2; ++m) {
+                    if (fabsf(y[m]) < INFINITY) continue;
+                    if (see_a) o[4 * n + m] = __float_as_uint(__uint_as_float(o[4 * n + m]) + y[m]);
+                    if (see_b) o[4 * n + 2 + m] = __float_as_uint(__uint_as_float(o[4 * n + 2 + m]) + y[m]);
+                  }
+                }
+              }
+              ++e;
+            }
+          }
+          if (run.whole) {
+            uint32_t va[4], vb[4];
+#pragma unroll
+            for (int n = 0; n < 4; ++n) {
+              va[n] = none_a ? 0u : pack_bf16(__uint_as_float(o[4 * n]) * fa,
+                                              __uint_as_float(o[4 * n + 1]) * fa);
+              vb[n] = none_b ? 0u : pack_bf16(__uint_as_float(o[4 * n + 2]) * fb,
+                                              __uint_as_float(o[4 * n + 3]) * fb);
+            }
+            quad_transpose(va, q4);
+            quad_transpose(vb, q4);
+            __nv_bfloat16* const out = static_cast<__nv_bfloat16*>(a.out) + c + 8 * q4;
+            if (live_a)
+              *reinterpret_cast<uint4*>(out + at_a * D) = make_uint4(va[0], va[1], va[2], va[3]);
+            if (live_b)
+              *reinterpret_cast<uint4*>(out + at_b * D) = make_uint4(vb[0], vb[1], vb[2], vb[3]);
+          } else {
+            const int first_row = me.row - lane;  // (of the warp)
+            float* const out = a.ws_acc + c + 2 * q4;
+#pragma unroll
+            for (int n = 0; n < 4; ++n) {
+              if (live_a)
+                *reinterpret_cast<float2*>(out + (part0 + first_row + ra) * D + 8 * n) = make_float2(
+                    __uint_as_float(o[4 * n]) * fa, __uint_as_float(o[4 * n + 1]) * fa);
+              if (live_b)
+                *reinterpret_cast<float2*>(out + (part0 + first_row + rb) * D + 8 * n) = make_float2(
+                    __uint_as_float(o[4 * n + 2]) * fb, __uint_as_float(o[4 * n + 3]) * fb);
+            }
+          }
         }
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(parted);
-      ok = mbar_wait(parted, unit & 1, a.err) && ok;
-      ok = __all_sync(0xffffffffu, ok);
-      tc_fence_after();
+      if (!wide) {  // the other group reads this one's O and sums
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(parted);
+        ok = mbar_wait(parted, ph_met, a.err) && ok;
+        ok = __all_sync(0xffffffffu, ok);
+        tc_fence_after();
+        ph_met ^= 1u;
+      }
       base.skip(run.n);
       me = then;
+      next = after;
     }
   }
 
@@ -856,8 +947,7 @@ cudaError_t launch_shape(const ChunkArgs& a, const CUtensorMap& tk, const CUtens
     cudaFuncAttributes fa{};
     e = cudaFuncGetAttributes(&fa, chunk_tc_kernel<KV, D, FORM>);
     if (e != cudaSuccess) return e;
-    if (kSoftThreads * S::SOFT_REGS + (S::THREADS - kSoftThreads) * S::REGS > S::THREADS * fa.numRegs)
-      return cudaErrorLaunchOutOfResources;
+    if (fa.numRegs < S::LAUNCH_REGS) return cudaErrorLaunchOutOfResources;
     if (dev < 64) attr_done.fetch_or(1ull << dev);
   }
   chunk_tc_kernel<KV, D, FORM><<<a.ctas, S::THREADS, S::SMEM, s>>>(a, tk, tv);

@@ -357,8 +357,7 @@ __global__ void __launch_bounds__(WeighTcShape<KV, D>::THREADS, 1) weights_tc_ke
         const size_t at = (size_t)(run->req.q0 + run->t0 + (int)t) * a.h_q + run->j * a.group + g;
         const float lse = live ? a.lse[at] : -INFINITY;
         const float slope = FORM && a.slopes ? a.slopes[run->j * a.group + g] * kLog2e : 0.f;
-        float factor = sc;
-        uint4 in[W8 ? D / 32 : 1][4];
+        uint4 in[4][W8 ? D / 32 : 1];
         if constexpr (W8) {  // four lanes read 64 consecutive bytes of a row, eight rows an instruction
 #pragma unroll
           for (int g4 = 0; g4 < 4; ++g4) {
@@ -368,9 +367,8 @@ __global__ void __launch_bounds__(WeighTcShape<KV, D>::THREADS, 1) weights_tc_ke
             const uint4* src = reinterpret_cast<const uint4*>(
                                    static_cast<const __nv_bfloat16*>(a.q) + src_at * D) + (lane & 3);
 #pragma unroll
-            for (int d = 0; d < D / 32; ++d) in[d][g4] = there ? src[4 * d] : make_uint4(0, 0, 0, 0);
+            for (int d = 0; d < D / 32; ++d) in[g4][d] = there ? src[4 * d] : make_uint4(0, 0, 0, 0);
           }
-          query_to_f16<D / 32>(in, sc, factor);
         }
         if (steps >= NQ) ok = mbar_wait(&free_q[qs.st], qs.par ^ 1u, a.err);
         if (ok && steps >= kCols) ok = mbar_wait(&free_c[cs.st], cs.par ^ 1u, a.err);
@@ -379,12 +377,16 @@ __global__ void __launch_bounds__(WeighTcShape<KV, D>::THREADS, 1) weights_tc_ke
         const uint32_t dst = ring + S::OFF_Q + qs.st * S::TILE;
         if constexpr (W8) {
           const int row0 = 32 * w + (lane >> 2);  // rows row0 + 8 g4
+          float* const factor = reinterpret_cast<float*>(col) + (cs.st * 4 + 1) * kStep;
 #pragma unroll
-          for (int d = 0; d < D / 32; ++d) {
-            const uint32_t ch = (((4 * d & 7) + (lane & 3)) ^ (row0 & 7)) << 4;
+          for (int g4 = 0; g4 < 4; ++g4) {
+            const float f = query_to_f16<D / 32>(in[g4], sc);
+            if ((lane & 3) == 0) factor[row0 + 8 * g4] = f;
 #pragma unroll
-            for (int g4 = 0; g4 < 4; ++g4)
-              sts128(dst + row0 * 128 + (d >> 1) * (kStep * 128) + g4 * 1024 + ch, in[d][g4]);
+            for (int d = 0; d < D / 32; ++d) {
+              const uint32_t ch = (((4 * d & 7) + (lane & 3)) ^ (row0 & 7)) << 4;
+              sts128(dst + row0 * 128 + (d >> 1) * (kStep * 128) + g4 * 1024 + ch, in[g4][d]);
+            }
           }
         } else {
           constexpr int CPR = D / 8;           // 16-byte chunks of a row: the lanes of one instruction
@@ -405,7 +407,6 @@ __global__ void __launch_bounds__(WeighTcShape<KV, D>::THREADS, 1) weights_tc_ke
         const int pos = run->req.base + run->t0 + (int)t;
         // a row that saw nothing gives nothing
         p[0] = lse == -INFINITY ? -INFINITY : -lse * kLog2e;
-        p[kStep] = factor;
         if constexpr (FORM) p[2 * kStep] = slope;
         reinterpret_cast<int*>(p)[3 * kStep] = pos;
         if constexpr (!W8) asm volatile("cp.async.wait_all;" ::: "memory");

@@ -39,45 +39,83 @@ __device__ __forceinline__ void regs_down() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
-// Queries of 32 rows for an 8-bit cache: bf16 to f16, scaled by a row's 2^e that puts its largest value
-// in f16's top binade. in[d][g]: chunk lane % 4 of 64-byte round d of row 8 g + lane / 4 (the four lanes
-// that hold a row agree). sc is the score factor of the KV head (log2 domain); mine receives that of this
-// lane's row with its 2^-e. It stays positive, and at least the smallest normal number (an unseen
-// score of -inf must stay one): a K scale's sign, or a NaN one, goes into the queries.
+// A row of queries for an 8-bit cache: bf16 to f16, scaled by 2^e that puts the row's largest value in
+// f16's top binade. Four lanes hold a row, chunk lane % 4 of each 64-byte round in in[d]. sc is the score
+// factor of the KV head (log2 domain); the row's own, with 2^-e, is returned. It stays positive, and at
+// least the smallest normal number (an unseen score of -inf must stay one): a K scale's sign, or a NaN
+// one, goes into the queries.
 template <int RND>
-__device__ __forceinline__ void query_to_f16(uint4 (&in)[RND][4], const float sc, float& mine) {
-  const int lane = threadIdx.x & 31;
-  float own = 0.f;
+__device__ __forceinline__ float query_to_f16(uint4 (&in)[RND], const float sc) {
+  uint32_t lo = 0, hi = 0;  // largest |q| as bits (bf16 magnitudes order like integers)
 #pragma unroll
-  for (int g = 0; g < 4; ++g) {
-    uint32_t lo = 0, hi = 0;  // largest |q| as bits (bf16 magnitudes order like integers)
+  for (int d = 0; d < RND; ++d) {
+    const uint32_t* w = &in[d].x;
 #pragma unroll
-    for (int d = 0; d < RND; ++d) {
-      const uint32_t* w = &in[d][g].x;
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        lo = max(lo, w[k] & 0x7fffu);
-        hi = max(hi, w[k] & 0x7fff0000u);
-      }
-    }
-    uint32_t mx = max(lo, hi >> 16);
-    mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-    mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-    const int ex = mx >> 7;  // biased exponent: mx 2^e in [2^14, 2^15), none for 0, inf, NaN
-    const int e = mx != 0 && ex < 255 ? min(126, max(-126, 141 - ex)) : 0;
-    const float two_e = __int_as_float((127 + e) << 23);
-    const float up = sc < 0.f ? -two_e : sc == sc ? two_e : sc;
-    const float of = fmaxf(fabsf(sc) * __int_as_float((127 - e) << 23), 0x1p-126f);
-    const float theirs = __shfl_sync(0xffffffffu, of, 4 * (lane & 7));
-    if ((lane >> 3) == g) own = theirs;
-#pragma unroll
-    for (int d = 0; d < RND; ++d) {
-      uint32_t* w = &in[d][g].x;
-#pragma unroll
-      for (int k = 0; k < 4; ++k) w[k] = pack_f16(bf16lo(w[k]) * up, bf16hi(w[k]) * up);
+    for (int k = 0; k < 4; ++k) {
+      lo = max(lo, w[k] & 0x7fffu);
+      hi = max(hi, w[k] & 0x7fff0000u);
     }
   }
-  mine = own;
+  uint32_t mx = max(lo, hi >> 16);
+  mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+  mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+  const int ex = mx >> 7;  // biased exponent: mx 2^e in [2^14, 2^15), none for 0, inf, NaN
+  const int e = mx != 0 && ex < 255 ? min(126, max(-126, 141 - ex)) : 0;
+  const float two_e = __int_as_float((127 + e) << 23);
+  const float up = sc < 0.f ? -two_e : sc == sc ? two_e : sc;
+#pragma unroll
+  for (int d = 0; d < RND; ++d) {
+    uint32_t* w = &in[d].x;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) w[k] = pack_f16(bf16lo(w[k]) * up, bf16hi(w[k]) * up);
+  }
+  return fmaxf(fabsf(sc) * __int_as_float((127 - e) << 23), 0x1p-126f);
+}
+
+// 16 consecutive columns of this thread's lane of tensor memory.
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, "
+      "[%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]),
+        "=r"(r[15])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+
+// 16 rows x 32 fp32 columns of tensor memory: r[4 n + 2 b + m] is column 8 n + 2 (lane % 4) + m of row
+// lane / 4 + 8 b.
+__device__ __forceinline__ void tmem_ld_16x256(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, "
+      "[%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]),
+        "=r"(r[15])
+      : "r"(taddr));
+}
+
+// Of four lanes with four words each: lane q4 gets word q4 of every lane, in lane order.
+__device__ __forceinline__ void quad_transpose(uint32_t (&x)[4], int q4) {
+  const bool odd = q4 & 1, high = q4 & 2;
+#pragma unroll
+  for (int k = 0; k < 4; k += 2) {
+    const uint32_t y = __shfl_xor_sync(0xffffffffu, odd ? x[k] : x[k + 1], 1);
+    (odd ? x[k] : x[k + 1]) = y;
+  }
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const uint32_t y = __shfl_xor_sync(0xffffffffu, high ? x[k] : x[k + 2], 2);
+    (high ? x[k] : x[k + 2]) = y;
+  }
 }
 
 // tanh x = 1 - 2 / (1 + e^{2x}): off by at most some 2^-22, with the exact limits at infinities.
