@@ -133,11 +133,23 @@ int check_chunk(const char* who, const void* q, int dtype_q, int num_rows, int b
   return PKV_OK;
 }
 
+int log2_of(int x) {
+  int n = 0;
+  while ((1 << n) < x) ++n;
+  return n;
+}
+
+void set_tile(ChunkArgs& a, int rows, int tokens) {
+  a.unit_rows = rows;
+  a.rows_shift = log2_of(rows);
+  a.tile_tokens = tokens;
+  a.tile_shift = log2_of(tokens);
+}
+
 void set_split(ChunkArgs& a, const ChunkSplit& t) {
-  a.unit_rows = t.rows;
+  set_tile(a, t.rows, t.tokens);
   a.unit_tokens = std::max(1, t.rows / a.group);
   a.subs = (a.group + t.rows - 1) / t.rows;
-  a.tile_tokens = t.tokens;
   a.min_tiles = t.min_tiles;
   a.pass_cost = t.pass_cost;
   a.narrow_rows = t.narrow_rows;
@@ -279,8 +291,7 @@ int pkv_chunk_weights(const void* q, int32_t dtype_q, int32_t num_rows, int32_t 
   const WeighSplit t = weigh_split(dtype_q, D);
   if (weigh_most_work(t, num_rows, batch, a.h_q, a.h_kv, width) >= (1ll << 30))
     return set_error(PKV_ESHAPE, "%s: rows and width can hold 2^30 steps of work or more", who);
-  a.unit_rows = t.rows;
-  a.tile_tokens = t.tokens;
+  set_tile(a, t.rows, t.tokens);
   a.ctas = weigh_ctas(t, num_rows, batch, a.h_q, a.h_kv, width);
   const ChunkSpace space = weigh_space(t, a.ctas);
   if (!workspace || workspace_bytes < space.all)

@@ -196,12 +196,6 @@ __global__ void __launch_bounds__(TcShape<KV, D>::THREADS, 1) chunk_tc_kernel(
       asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm_v)) : "memory");
     }
   }
-  chunk_share<S::THREADS>(a, scratch, &share);
-  if (share.count == 0) {  // (the whole CTA)
-    if (threadIdx.x == 0)
-      static_cast<ChunkRecord*>(a.ws_rec)[blockIdx.x] = ChunkRecord{0, 1, 0, 0};
-    return;
-  }
   if (warp == kMmaWarp) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                      smem_u32(s_taddr)),
@@ -209,10 +203,22 @@ __global__ void __launch_bounds__(TcShape<KV, D>::THREADS, 1) chunk_tc_kernel(
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
+  chunk_share<S::THREADS>(a, scratch, &share);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = (uint32_t)uniform((int)*s_taddr);
+  auto release = [&] {
+    __syncwarp();
+    if (warp == kMmaWarp)
+      asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols)
+                   : "memory");
+  };
+  if (share.count == 0) {  // (the whole CTA)
+    if (threadIdx.x == 0) static_cast<ChunkRecord*>(a.ws_rec)[blockIdx.x] = ChunkRecord{0, 1, 0, 0};
+    release();
+    return;
+  }
   // run i of the share, or nullptr after the last (or a wait that gave up)
   auto get_run = [&](uint32_t i) -> const ChunkRun* {
     const bool got = mbar_wait(&run_there[i % kRuns], (i / kRuns) & 1u, a.err);
@@ -623,14 +629,19 @@ __global__ void __launch_bounds__(TcShape<KV, D>::THREADS, 1) chunk_tc_kernel(
         }
         tmem_wait_ld();
         if constexpr (FORM) {  // the scores themselves, log2 domain
-          const bool cap = a.softcap > 0.f;
-          const float in = cap ? sc * (kLn2 / a.softcap) : sc, top = a.softcap * kLog2e;
-          const float far0 = (float)(p0 + 64 * h - me.pq);
+          if (a.softcap > 0.f) {
+            cap_scores<64>(sr, sc * (kLn2 / a.softcap), a.softcap * kLog2e);
+          } else {
+            const uint64_t sc2 = pack2(sc, sc);
 #pragma unroll
-          for (int k = 0; k < 64; ++k) {
-            float x = __uint_as_float(sr[k]) * in;
-            if (cap) x = top * tanh_of(x);
-            sr[k] = __float_as_uint(fmaf(me.slope, far0 + (float)k, x));
+            for (int k = 0; k < 64; k += 2) put2(&sr[k], mul2(get2(&sr[k]), sc2));
+          }
+          if (a.slopes) {
+            const float far0 = (float)(p0 + 64 * h - me.pq);
+            const uint64_t slope2 = pack2(me.slope, me.slope), far2 = pack2(far0, far0);
+#pragma unroll
+            for (int k = 0; k < 64; k += 2)
+              put2(&sr[k], fma2(slope2, add2(far2, pack2((float)k, (float)(k + 1))), get2(&sr[k])));
           }
         }
         const bool edge = p0 > edge_from || (p0 < edge_win && p0 + kTok > a.sink);
@@ -922,13 +933,8 @@ __global__ void __launch_bounds__(TcShape<KV, D>::THREADS, 1) chunk_tc_kernel(
 
   tc_fence_before();
   __syncthreads();
-  if (warp == kMmaWarp) {
-    __syncwarp();
-    tc_fence_after();
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
-                 "r"(kTmemCols)
-                 : "memory");
-  }
+  tc_fence_after();
+  release();
 }
 
 template <typename KV, int D, bool FORM>

@@ -49,6 +49,11 @@ __device__ __forceinline__ ChunkReq chunk_request(const ChunkArgs& a, int b) {
   return r;
 }
 
+// Tiles that hold the first n positions (their size is a power of two).
+__device__ __forceinline__ int tiles_for(const ChunkArgs& a, int n) {
+  return (int)((unsigned)n + a.tile_tokens - 1 >> a.tile_shift);
+}
+
 // The tiles of a unit: `sinks` from position 0 on, then those from tile `first` on, `n` in all.
 struct ChunkTiles {
   int n, sinks, first;
@@ -56,33 +61,36 @@ struct ChunkTiles {
 };
 
 __device__ __forceinline__ ChunkTiles chunk_tiles(const ChunkArgs& a, const ChunkReq& r, int block) {
-  const int T = a.tile_tokens, t0 = block * a.unit_tokens, t1 = min(r.n, t0 + a.unit_tokens);
-  const int end = (r.base + t1 + T - 1) / T;
+  const int t0 = block * a.unit_tokens, t1 = min(r.n, t0 + a.unit_tokens);
+  const int end = tiles_for(a, r.base + t1);
   ChunkTiles x{end, 0, 0};
   if (a.window > 0) {
-    const int first = max(0, r.base + t0 + 1 - a.window) / T, sinks = (a.sink + T - 1) / T;
+    const int first = max(0, r.base + t0 + 1 - a.window) >> a.tile_shift, sinks = tiles_for(a, a.sink);
     if (first > sinks) x = ChunkTiles{sinks + end - first, sinks, first};
   }
   return x;
 }
 
 // sum over 0 <= i < n of floor((a i + b) / m): whole multiples of m are taken out of a and b, the rest
-// counts lattice points below a line, which the same sum with the axes exchanged counts too.
+// counts lattice points below a line, which the same sum with the axes exchanged counts too. (Less than
+// m n + m must fit 32 bits: a tile's tokens by a request's blocks, at most 64 2^26 or 128 2^23 here.)
 __device__ __forceinline__ long long floor_sum(unsigned n, unsigned m, unsigned a, unsigned b) {
   unsigned long long sum = 0;
   while (n > 0) {
     if (a >= m) {
-      sum += (unsigned long long)(a / m) * n * (n - 1) / 2;
-      a %= m;
+      const unsigned q = a / m;
+      sum += (unsigned long long)n * (n - 1) / 2 * q;
+      a -= q * m;
     }
     if (b >= m) {
-      sum += (unsigned long long)(b / m) * n;
-      b %= m;
+      const unsigned q = b / m;
+      sum += (unsigned long long)q * n;
+      b -= q * m;
     }
-    const unsigned long long top = (unsigned long long)a * n + b;
+    const unsigned top = a * n + b;
     if (top < m) break;
-    n = (unsigned)(top / m);
-    b = (unsigned)(top % m);
+    n = top / m;
+    b = top - n * m;
     const unsigned t = m;
     m = a;
     a = t;
@@ -96,7 +104,7 @@ __device__ __forceinline__ long long tiles_below(const ChunkArgs& a, const Chunk
   const int T = a.tile_tokens, U = a.unit_tokens;
   long long n = floor_sum(k, T, U, r.base + U + T - 1);
   if (a.window > 0) {  // from block i1 on, the tiles between the sinks and the window are left out
-    const int sinks = (a.sink + T - 1) / T;
+    const int sinks = tiles_for(a, a.sink);
     const long long from = (long long)(sinks + 1) * T + a.window - 1 - r.base;
     const long long i1 = from <= 0 ? 0 : (from + U - 1) / U;
     if (i1 < k)
@@ -125,6 +133,43 @@ __device__ __forceinline__ int chunk_work(const ChunkArgs& a, const ChunkReq& r,
   return (int)tiles_below(a, r, k - 1) * a.wide_tile + chunk_tiles(a, r, k - 1).n * z.last_tile;
 }
 
+// block_scan of two values at once (scratch of 64 words).
+template <int THREADS>
+__device__ __forceinline__ void block_scan2(int v, int w, int* scratch, int& v_below, int& v_total,
+                                            int& w_below, int& w_total) {
+  constexpr int W = (THREADS + 31) / 32;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int x = v, y = w;
+#pragma unroll
+  for (int o = 1; o < 32; o *= 2) {
+    const int a = __shfl_up_sync(0xffffffffu, x, o), b = __shfl_up_sync(0xffffffffu, y, o);
+    if (lane >= o) {
+      x += a;
+      y += b;
+    }
+  }
+  if (lane == 31) {
+    scratch[warp] = x;
+    scratch[32 + warp] = y;
+  }
+  __syncthreads();
+  // (every warp adds up the warps' sums for itself)
+  int a = lane < W ? scratch[lane] : 0, b = lane < W ? scratch[32 + lane] : 0;
+  const int a0 = a, b0 = b;
+#pragma unroll
+  for (int o = 1; o < 32; o *= 2) {
+    const int c = __shfl_up_sync(0xffffffffu, a, o), d = __shfl_up_sync(0xffffffffu, b, o);
+    if (lane >= o) {
+      a += c;
+      b += d;
+    }
+  }
+  v_total = __shfl_sync(0xffffffffu, a, 31);
+  w_total = __shfl_sync(0xffffffffu, b, 31);
+  v_below = __shfl_sync(0xffffffffu, a - a0, warp) + x - v;
+  w_below = __shfl_sync(0xffffffffu, b - b0, warp) + y - w;
+}
+
 // A CTA's share: from (request, KV head, block, part) on, x half tiles into that unit, `count` long.
 struct ChunkShare {
   int b, j, block, sub, x, count, pass_cost, share;
@@ -148,8 +193,7 @@ __device__ __forceinline__ void chunk_share(const ChunkArgs& a, int* scratch, Ch
   if (err && blockIdx.x == 0) atomicOr(a.err, err);
   if (threadIdx.x == 0) out->count = 0;
   int work_below, work_all, passes_below, passes_all;
-  block_scan<THREADS>(work, scratch, work_below, work_all);
-  block_scan<THREADS>(passes, scratch + 32, passes_below, passes_all);
+  block_scan2<THREADS>(work, passes, scratch, work_below, work_all, passes_below, passes_all);
   const int cost = work_all >= 32 * a.ctas ? 2 * a.pass_cost : 0;
   const int total = work_all + cost * passes_all;
   const int share =

@@ -54,11 +54,6 @@ template <typename KV, int D>
 struct WeighTcShape {
   static constexpr bool W8 = KV::bytes == 1;
   static constexpr int THREADS = 32 * (W8 ? kConvWarp + 4 : kConvWarp);
-  // registers of the summing warps, of MMA and copies, of the loaders and of the converters, out of
-  // what the launch gives every warp
-  static constexpr int LAUNCH_REGS = W8 ? 72 : 80;
-  static constexpr int SUM_REGS = W8 ? 64 : 80, MMA_REGS = W8 ? 40 : 48, LOAD_REGS = 112;
-  static constexpr int CONV_REGS = 96;
   static constexpr int TILE = kHalf * D * 2;  // K of a half, or the queries of a step, in MMA form
   static constexpr int NK = D == 128 ? 3 : 6, NQ = D == 128 ? (W8 ? 2 : 3) : 4;
   static constexpr uint32_t IDESC = tc_idesc(128, 0, false, W8);  // (N: the step's columns)
@@ -74,9 +69,6 @@ struct WeighTcShape {
   static constexpr int OFF_MISC = OFF_BAR + 8 * BARS;       // masks, TMEM address
   static constexpr int SMEM = 1024 + OFF_MISC + 4 * (NK + NR + 1) + 16;
   static_assert(SMEM <= 224 * 1024 && SMEM > 114 * 1024, "one CTA per SM");
-  static_assert(kSumThreads * SUM_REGS + 128 * (MMA_REGS + LOAD_REGS) + (W8 ? 128 * CONV_REGS : 0) <=
-                    THREADS * LAUNCH_REGS,
-                "the split takes no more registers than the launch brings");
 };
 
 // A step's rows' numbers in shared memory.
@@ -160,12 +152,6 @@ __global__ void __launch_bounds__(WeighTcShape<KV, D>::THREADS, 1) weights_tc_ke
     if constexpr (!W8)
       asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm_k)) : "memory");
   }
-  weigh_share<S::THREADS>(a, scratch, &share);
-  if (share.count == 0) {  // (the whole CTA)
-    if (threadIdx.x == 0)
-      static_cast<WeighRecord*>(a.ws_rec)[blockIdx.x] = WeighRecord{0, 0, 0, 0};
-    return;
-  }
   if (warp == kMmaWarp) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                      smem_u32(s_taddr)),
@@ -173,10 +159,22 @@ __global__ void __launch_bounds__(WeighTcShape<KV, D>::THREADS, 1) weights_tc_ke
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
+  weigh_share<S::THREADS>(a, scratch, &share);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = (uint32_t)uniform((int)*s_taddr);
+  auto release = [&] {
+    __syncwarp();
+    if (warp == kMmaWarp)
+      asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols)
+                   : "memory");
+  };
+  if (share.count == 0) {  // (the whole CTA)
+    if (threadIdx.x == 0) static_cast<WeighRecord*>(a.ws_rec)[blockIdx.x] = WeighRecord{0, 0, 0, 0};
+    release();
+    return;
+  }
   // run i of the share, or nullptr after the last (or a wait that gave up)
   auto get_run = [&](uint32_t i) -> const WeighRun* {
     const bool got = mbar_wait(&run_there[i % kRuns], (i / kRuns) & 1u, a.err);
@@ -191,7 +189,6 @@ __global__ void __launch_bounds__(WeighTcShape<KV, D>::THREADS, 1) weights_tc_ke
   };
 
   if (warp >= kMmaWarp && warp < kLoadWarp) {
-    regs_down<S::MMA_REGS>();
     if (warp == kCopyWarp) {
       // ===================== copies of K, half by half =====================
       const uint64_t pol = l2_evict_first_policy();
@@ -339,89 +336,116 @@ __global__ void __launch_bounds__(WeighTcShape<KV, D>::THREADS, 1) weights_tc_ke
     }
   } else if (warp >= kLoadWarp && warp < kConvWarp) {
     // ===================== queries and the rows' numbers =====================
-    regs_up<S::LOAD_REGS>();
+    // A step's copies are issued before the step ahead of it is waited for, whatever runs they belong to.
+    // Four lanes copy 64 consecutive bytes of a row; for an 8-bit cache they then make f16 of the row in
+    // its place.
     const int w = warp - kLoadWarp, r = 32 * w + lane;  // this lane's row of a step
-    Place<NQ> qs;
-    Place<kCols> cs;
-    int steps = 0;
+    const int row0 = 32 * w + (lane >> 2);              // it copies pieces of rows row0 + 8 g
+    constexpr int RND = D / 32;
     bool ok = true;
-    for (uint32_t unit = 0; ok; ++unit) {
-      const WeighRun* run = get_run(unit);
-      if (!run) break;
-      const int n = steps_of(run);
-      const float sc = a.scale * kLog2e * (W8 ? a.k_scales[run->j] : 1.f);
-      for (int u = 0; u < n; ++u, ++steps, qs.advance(1), cs.advance(1)) {
-        const unsigned R = (unsigned)(run->s0 + u) * kStep + r;
-        const bool live = R < (unsigned)run->rows;
-        const unsigned t = live ? R / (unsigned)a.group : 0, g = live ? R - t * a.group : 0;
-        const size_t at = (size_t)(run->req.q0 + run->t0 + (int)t) * a.h_q + run->j * a.group + g;
-        const float lse = live ? a.lse[at] : -INFINITY;
-        const float slope = FORM && a.slopes ? a.slopes[run->j * a.group + g] * kLog2e : 0.f;
-        uint4 in[4][W8 ? D / 32 : 1];
-        if constexpr (W8) {  // four lanes read 64 consecutive bytes of a row, eight rows an instruction
+    struct Step {
+      const WeighRun* run;
+      int u, pos;  // step of the run; position of this lane's row
+      float neg_lse, slope;
+    };
+    uint32_t unit = 0;
+    auto advance = [&](Step& x) {  // to the next step, x.run = nullptr behind the last
+      if (x.run && ++x.u < steps_of(x.run)) return;
+      do {
+        x.run = get_run(unit++);
+      } while (x.run && steps_of(x.run) == 0);
+      x.u = 0;
+    };
+    auto q_chunk = [&](int st, int d, int g) {
+      return ring + S::OFF_Q + st * S::TILE + row0 * 128 + (d >> 1) * (kStep * 128) + g * 1024 +
+             ((((4 * d & 7) + (lane & 3)) ^ (row0 & 7)) << 4);
+    };
+    Place<NQ> q_in, q_out;
+    Place<kCols> cs;
+    int issued = 0, finished = 0;
+    auto issue = [&](Step& x) {
+      if (issued >= NQ) ok = __all_sync(0xffffffffu, mbar_wait(&free_q[q_in.st], q_in.par ^ 1u, a.err));
+      if (!ok) return;
+      const WeighRun& run = *x.run;
+      const unsigned first = (unsigned)(run.s0 + x.u) * kStep, R = first + r;
+      const bool live = R < (unsigned)run.rows;
+      const unsigned t = live ? R / (unsigned)a.group : 0, g = live ? R - t * a.group : 0;
+      const size_t at = (size_t)(run.req.q0 + run.t0 + (int)t) * a.h_q + run.j * a.group + g;
+      const float lse = live ? a.lse[at] : -INFINITY;
+      x.neg_lse = lse == -INFINITY ? -INFINITY : -lse * kLog2e;  // a row that saw nothing gives nothing
+      x.slope = FORM && a.slopes ? a.slopes[run.j * a.group + g] * kLog2e : 0.f;
+      x.pos = run.req.base + run.t0 + (int)t;
+      if (32 * w < run.rows - (int)first) {  // (columns beyond the last block of 32 are not used)
 #pragma unroll
-          for (int g4 = 0; g4 < 4; ++g4) {
-            const int from = 8 * g4 + (lane >> 2);
-            const size_t src_at = __shfl_sync(0xffffffffu, (unsigned long long)at, from);
-            const bool there = __shfl_sync(0xffffffffu, (int)live, from) != 0;
-            const uint4* src = reinterpret_cast<const uint4*>(
-                                   static_cast<const __nv_bfloat16*>(a.q) + src_at * D) + (lane & 3);
+        for (int g4 = 0; g4 < 4; ++g4) {
+          const int from = 8 * g4 + (lane >> 2);
+          const size_t src_at = __shfl_sync(0xffffffffu, (unsigned long long)at, from);
+          const bool there = __shfl_sync(0xffffffffu, (int)live, from) != 0;
+          const __nv_bfloat16* src =
+              static_cast<const __nv_bfloat16*>(a.q) + src_at * D + 8 * (lane & 3);
 #pragma unroll
-            for (int d = 0; d < D / 32; ++d) in[g4][d] = there ? src[4 * d] : make_uint4(0, 0, 0, 0);
-          }
-        }
-        if (steps >= NQ) ok = mbar_wait(&free_q[qs.st], qs.par ^ 1u, a.err);
-        if (ok && steps >= kCols) ok = mbar_wait(&free_c[cs.st], cs.par ^ 1u, a.err);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-        const uint32_t dst = ring + S::OFF_Q + qs.st * S::TILE;
-        if constexpr (W8) {
-          const int row0 = 32 * w + (lane >> 2);  // rows row0 + 8 g4
-          float* const factor = reinterpret_cast<float*>(col) + (cs.st * 4 + 1) * kStep;
-#pragma unroll
-          for (int g4 = 0; g4 < 4; ++g4) {
-            const float f = query_to_f16<D / 32>(in[g4], sc);
-            if ((lane & 3) == 0) factor[row0 + 8 * g4] = f;
-#pragma unroll
-            for (int d = 0; d < D / 32; ++d) {
-              const uint32_t ch = (((4 * d & 7) + (lane & 3)) ^ (row0 & 7)) << 4;
-              sts128(dst + row0 * 128 + (d >> 1) * (kStep * 128) + g4 * 1024 + ch, in[g4][d]);
-            }
-          }
-        } else {
-          constexpr int CPR = D / 8;           // 16-byte chunks of a row: the lanes of one instruction
-          constexpr int RPI = 32 / CPR;        // take RPI rows
-#pragma unroll 4
-          for (int i = 0; i < 32 / RPI; ++i) {
-            const int from = i * RPI + lane / CPR, c = lane % CPR, row = 32 * w + from;
-            const size_t src_at = __shfl_sync(0xffffffffu, (unsigned long long)at, from);
-            const bool there = __shfl_sync(0xffffffffu, (int)live, from) != 0;
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
-                             dst + (c >> 3) * (kStep * 128) + row * 128 + (((c & 7) ^ (row & 7)) << 4)),
-                         "l"(static_cast<const __nv_bfloat16*>(a.q) + src_at * D + 8 * c),
-                         "r"(there ? 16 : 0)
+          for (int d = 0; d < RND; ++d)
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(q_chunk(q_in.st, d, g4)),
+                         "l"(src + 32 * d), "r"(there ? 16 : 0)
                          : "memory");
-          }
-        }
-        float* p = reinterpret_cast<float*>(col) + cs.st * 4 * kStep + r;
-        const int pos = run->req.base + run->t0 + (int)t;
-        // a row that saw nothing gives nothing
-        p[0] = lse == -INFINITY ? -INFINITY : -lse * kLog2e;
-        if constexpr (FORM) p[2 * kStep] = slope;
-        reinterpret_cast<int*>(p)[3 * kStep] = pos;
-        if constexpr (!W8) asm volatile("cp.async.wait_all;" ::: "memory");
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(&full_q[qs.st]);
-          mbar_arrive(&full_c[cs.st]);
         }
       }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+      ++issued;
+      q_in.advance(1);
+    };
+    auto finish = [&](const Step& x) {
+      if (finished >= kCols) ok = __all_sync(0xffffffffu, mbar_wait(&free_c[cs.st], cs.par ^ 1u, a.err));
+      if (!ok) return;
+      const float sc = a.scale * kLog2e * (W8 ? a.k_scales[x.run->j] : 1.f);
+      float* const p = reinterpret_cast<float*>(col) + cs.st * 4 * kStep;
+      p[r] = x.neg_lse;
+      if constexpr (FORM) p[2 * kStep + r] = x.slope;
+      reinterpret_cast<int*>(p)[3 * kStep + r] = x.pos;
+      if constexpr (W8) {
+        if (32 * w < x.run->rows - (x.run->s0 + x.u) * kStep) {
+#pragma unroll
+          for (int g4 = 0; g4 < 4; ++g4) {
+            uint4 in[RND];
+#pragma unroll
+            for (int d = 0; d < RND; ++d) in[d] = lds128(q_chunk(q_out.st, d, g4));
+            const float f = query_to_f16<RND>(in, sc);
+#pragma unroll
+            for (int d = 0; d < RND; ++d) sts128(q_chunk(q_out.st, d, g4), in[d]);
+            if ((lane & 3) == 0) p[kStep + row0 + 8 * g4] = f;
+          }
+        }
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&full_q[q_out.st]);
+        mbar_arrive(&full_c[cs.st]);
+      }
+      ++finished;
+      q_out.advance(1);
+      cs.advance(1);
+    };
+    Step now{}, then{};
+    advance(now);
+    if (now.run) issue(now);
+    while (ok && now.run) {
+      then = now;
+      advance(then);
+      if (then.run) {
+        issue(then);
+        if (!ok) break;
+        asm volatile("cp.async.wait_group 1;" ::: "memory");
+      } else {
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+      }
+      finish(now);
+      now = then;
     }
+    asm volatile("cp.async.wait_all;" ::: "memory");
   } else if (warp >= kConvWarp) {
     // ===================== 8-bit codes to f16 in MMA form =====================
     if constexpr (W8) {
-      regs_up<S::CONV_REGS>();
       constexpr int CPR = D / 16;                       // 16-code chunks of a row
       constexpr int PER = kHalf / 2 * CPR / 128;        // chunks of a thread in half a tile
       constexpr int ROWS = 128 / CPR;
@@ -484,7 +508,6 @@ __global__ void __launch_bounds__(WeighTcShape<KV, D>::THREADS, 1) weights_tc_ke
     }
   } else {
     // ===================== sums =====================
-    if constexpr (S::SUM_REGS < S::LAUNCH_REGS) regs_down<S::SUM_REGS>();
     const int group = warp >> 2, h = group & 1, q = group >> 1;
     const int r = threadIdx.x & 127;  // position of the half
     const uint32_t scol = tmem + ((uint32_t)((warp & 3) * 32) << 16) + 128 * group;
@@ -494,12 +517,15 @@ __global__ void __launch_bounds__(WeighTcShape<KV, D>::THREADS, 1) weights_tc_ke
     Place<kCols> base;  // of the run's first step
     const float sc = a.scale * kLog2e;
     const bool cap = FORM && a.softcap > 0.f;
-    const float in = cap ? kLn2 / a.softcap : 1.f, top = a.softcap * kLog2e;
+    const float in = cap ? (W8 ? kLn2 : kLn2 * sc) / a.softcap : 0.f, top = a.softcap * kLog2e;
     for (uint32_t unit = 0;; ++unit) {
       const WeighRun* run = get_run(unit);
       if (!run) break;
       const int n = steps_of(run), halves = halves_of(run);
       const int p0 = run->item * kItem + h * kHalf, p = p0 + r, ctx = run->req.base + run->req.n;
+      const int64_t at = ((int64_t)run->b * a.h_kv + run->j) * a.width + p;
+      const bool writes = q == 0 && h < halves && p < ctx;
+      const float before = writes && run->whole && a.add_to ? a.add_to[at] : 0.f;  // (on its way meanwhile)
       float total = 0.f, lost = 0.f;
       bool good = false;
       if (h < halves && n > 0) {
@@ -539,13 +565,17 @@ __global__ void __launch_bounds__(WeighTcShape<KV, D>::THREADS, 1) weights_tc_ke
               if (lane == 0) mbar_arrive(&s_read[group]);
             }
             if constexpr (FORM) {
+              if (W8 || !cap) {
 #pragma unroll
-              for (int k = 0; k < 32; ++k) {
-                const float f = W8 ? cn.factor[c + k] : sc;
-                float x = __uint_as_float(s[k]) * (f * in);
-                if (cap) x = top * tanh_of(x);
-                if (a.slopes) x = fmaf(cn.slope[c + k], (float)(p - cn.pos[c + k]), x);
-                s[k] = __float_as_uint(x);
+                for (int k = 0; k < 32; ++k)
+                  s[k] = __float_as_uint(__uint_as_float(s[k]) * (W8 ? cn.factor[c + k] : sc));
+              }
+              if (cap) cap_scores<32>(s, in, top);
+              if (a.slopes) {
+#pragma unroll
+                for (int k = 0; k < 32; ++k)
+                  s[k] = __float_as_uint(fmaf(cn.slope[c + k], (float)(p - cn.pos[c + k]),
+                                              __uint_as_float(s[k])));
               }
             }
             if (edge) {
@@ -592,28 +622,27 @@ __global__ void __launch_bounds__(WeighTcShape<KV, D>::THREADS, 1) weights_tc_ke
       }
       // ---- the run's sums: the second steps' group hands its own to the first's, which writes ----
       if (n > 1 && h < halves) {
-        const int at = hands & 1;  // runs take turns between two places
-        float* const place = hand + at * kItem + h * kHalf + r;
+        const int spot = hands & 1;  // runs take turns between two places
+        float* const place = hand + spot * kItem + h * kHalf + r;
         if (q == 1) {
           if (hands >= 2)
-            ok = mbar_wait(&taken[2 * at + h], ((hands >> 1) - 1) & 1u, a.err) && ok;
+            ok = mbar_wait(&taken[2 * spot + h], ((hands >> 1) - 1) & 1u, a.err) && ok;
           *place = total;
           __syncwarp();
-          if (lane == 0) mbar_arrive(&handed[2 * at + h]);
+          if (lane == 0) mbar_arrive(&handed[2 * spot + h]);
         } else {
-          ok = mbar_wait(&handed[2 * at + h], (hands >> 1) & 1u, a.err) && ok;
+          ok = mbar_wait(&handed[2 * spot + h], (hands >> 1) & 1u, a.err) && ok;
           total += *place;
           __syncwarp();
-          if (lane == 0) mbar_arrive(&taken[2 * at + h]);
+          if (lane == 0) mbar_arrive(&taken[2 * spot + h]);
         }
         ++hands;
       }
       ok = __all_sync(0xffffffffu, ok);
-      if (q == 0 && h < halves && p < ctx && ok) {
+      if (writes && ok) {
         const float x = good ? total : 0.f;
-        const int64_t at = ((int64_t)run->b * a.h_kv + run->j) * a.width + p;
         if (run->whole)
-          a.weights_out[at] = (a.add_to ? a.add_to[at] : 0.f) + x;
+          a.weights_out[at] = before + x;
         else
           a.ws_acc[((size_t)blockIdx.x * 2 + run->slot) * kItem + h * kHalf + r] = x;
       }
@@ -626,13 +655,8 @@ __global__ void __launch_bounds__(WeighTcShape<KV, D>::THREADS, 1) weights_tc_ke
 
   tc_fence_before();
   __syncthreads();
-  if (warp == kMmaWarp) {
-    __syncwarp();
-    tc_fence_after();
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
-                 "r"(kTmemCols)
-                 : "memory");
-  }
+  tc_fence_after();
+  release();
 }
 
 template <typename KV, int D, bool FORM>
@@ -646,11 +670,6 @@ cudaError_t launch_shape(const ChunkArgs& a, const CUtensorMap& tk, cudaStream_t
     e = cudaFuncSetAttribute(weights_tc_kernel<KV, D, FORM>,
                              cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM);
     if (e != cudaSuccess) return e;
-    // the warps' split may take no more registers than the launch brings
-    cudaFuncAttributes fa{};
-    e = cudaFuncGetAttributes(&fa, weights_tc_kernel<KV, D, FORM>);
-    if (e != cudaSuccess) return e;
-    if (fa.numRegs < S::LAUNCH_REGS) return cudaErrorLaunchOutOfResources;
     if (dev < 64) attr_done.fetch_or(1ull << dev);
   }
   weights_tc_kernel<KV, D, FORM><<<a.ctas, S::THREADS, S::SMEM, s>>>(a, tk);

@@ -210,6 +210,8 @@ struct ChunkArgs {
   int unit_tokens;  // whole tokens of a unit
   int subs;         // units of a token and KV head (1 unless group > unit_rows)
   int tile_tokens;
+  int tile_shift;   // tile_tokens and unit_rows are powers of two
+  int rows_shift;
   int min_tiles;
   int pass_cost;
   int narrow_rows;

@@ -34,7 +34,7 @@ __device__ __forceinline__ WeighReq weigh_request(const ChunkArgs& a, int b) {
   if (w.r.err == 0 && ctx > a.width) w.r = ChunkReq{0, 0, 0, PKV_DEVERR_BAD_CHUNK};
   if (w.r.err != 0) return w;
   w.from = a.last_rows > 0 ? max(0, w.r.n - a.last_rows) : 0;
-  w.items = (ctx + a.tile_tokens - 1) / a.tile_tokens;
+  w.items = tiles_for(a, ctx);
   return w;
 }
 
@@ -44,7 +44,7 @@ struct WeighTokens {
 };
 
 __device__ __forceinline__ WeighTokens weigh_tokens(const ChunkArgs& a, const WeighReq& w, int i) {
-  const int p0 = i * a.tile_tokens;
+  const int p0 = i << a.tile_shift;
   WeighTokens x{max(w.from, p0 - w.r.base), w.r.n};
   if (a.window > 0 && p0 >= a.sink)
     x.t1 = (int)min((long long)x.t1, (long long)p0 + a.tile_tokens - 1 + a.window - w.r.base);
@@ -55,19 +55,19 @@ __device__ __forceinline__ WeighTokens weigh_tokens(const ChunkArgs& a, const We
 __device__ __forceinline__ long long weigh_steps(const ChunkArgs& a, const WeighReq& w, int i) {
   const WeighTokens x = weigh_tokens(a, w, i);
   const long long rows = ((long long)x.t1 - x.t0) * a.group;
-  return rows > 0 ? (rows + a.unit_rows - 1) / a.unit_rows : -(-rows / a.unit_rows);
+  return (rows + a.unit_rows - 1) >> a.rows_shift;  // (towards minus infinity: ceil(rows / unit_rows))
 }
 
 // Steps of the first k items, each at least one.
 __device__ __forceinline__ long long weigh_below(const ChunkArgs& a, const WeighReq& w, int k) {
-  const int step = a.tile_tokens * a.group / a.unit_rows;
+  const int step = a.tile_tokens * a.group >> a.rows_shift;
   // the places: from here the first row is the tile's own; the sinks end; the window's end is the chunk's
-  const int own = (w.from + w.r.base) / a.tile_tokens + 1;
+  const int own = (w.from + w.r.base >> a.tile_shift) + 1;
   int sinks = 0, last = 0;
   if (a.window > 0) {
     const long long x = (long long)w.r.base + w.r.n - a.window - a.tile_tokens + 1;
-    sinks = (a.sink + a.tile_tokens - 1) / a.tile_tokens;
-    last = max(sinks, x > 0 ? (int)((x + a.tile_tokens - 1) / a.tile_tokens) : 0);
+    sinks = tiles_for(a, a.sink);
+    last = max(sinks, x > 0 ? (int)(x + a.tile_tokens - 1 >> a.tile_shift) : 0);
   }
   long long sum = 0;
   for (int i = 0; i < k;) {
