@@ -336,7 +336,8 @@ __global__ void __launch_bounds__(WeighTcShape<KV, D>::THREADS, 1) weights_tc_ke
     }
   } else if (warp >= kLoadWarp && warp < kConvWarp) {
     // ===================== queries and the rows' numbers =====================
-    // A step's copies are issued before the step ahead of it is waited for, whatever runs they belong to.
+    // A step's loads are issued before the step ahead of it is waited for, if there is a place for them
+    // yet, whatever runs they belong to.
     // Four lanes copy 64 consecutive bytes of a row; for an 8-bit cache they then make f16 of the row in
     // its place.
     const int w = warp - kLoadWarp, r = 32 * w + lane;  // this lane's row of a step
@@ -345,8 +346,8 @@ __global__ void __launch_bounds__(WeighTcShape<KV, D>::THREADS, 1) weights_tc_ke
     bool ok = true;
     struct Step {
       const WeighRun* run;
-      int u, pos;  // step of the run; position of this lane's row
-      float neg_lse, slope;
+      int u, pos;                 // step of the run; position of this lane's row
+      float lse, slope, k_scale;  // (as they come: used when the step is finished)
     };
     uint32_t unit = 0;
     auto advance = [&](Step& x) {  // to the next step, x.run = nullptr behind the last
@@ -371,9 +372,9 @@ __global__ void __launch_bounds__(WeighTcShape<KV, D>::THREADS, 1) weights_tc_ke
       const bool live = R < (unsigned)run.rows;
       const unsigned t = live ? R / (unsigned)a.group : 0, g = live ? R - t * a.group : 0;
       const size_t at = (size_t)(run.req.q0 + run.t0 + (int)t) * a.h_q + run.j * a.group + g;
-      const float lse = live ? a.lse[at] : -INFINITY;
-      x.neg_lse = lse == -INFINITY ? -INFINITY : -lse * kLog2e;  // a row that saw nothing gives nothing
-      x.slope = FORM && a.slopes ? a.slopes[run.j * a.group + g] * kLog2e : 0.f;
+      x.lse = live ? a.lse[at] : -INFINITY;
+      x.slope = FORM && a.slopes ? a.slopes[run.j * a.group + g] : 0.f;
+      x.k_scale = W8 ? a.k_scales[run.j] : 1.f;
       x.pos = run.req.base + run.t0 + (int)t;
       if (32 * w < run.rows - (int)first) {  // (columns beyond the last block of 32 are not used)
 #pragma unroll
@@ -397,10 +398,10 @@ __global__ void __launch_bounds__(WeighTcShape<KV, D>::THREADS, 1) weights_tc_ke
     auto finish = [&](const Step& x) {
       if (finished >= kCols) ok = __all_sync(0xffffffffu, mbar_wait(&free_c[cs.st], cs.par ^ 1u, a.err));
       if (!ok) return;
-      const float sc = a.scale * kLog2e * (W8 ? a.k_scales[x.run->j] : 1.f);
+      const float sc = a.scale * kLog2e * x.k_scale;
       float* const p = reinterpret_cast<float*>(col) + cs.st * 4 * kStep;
-      p[r] = x.neg_lse;
-      if constexpr (FORM) p[2 * kStep + r] = x.slope;
+      p[r] = x.lse == -INFINITY ? -INFINITY : -x.lse * kLog2e;  // (a row that saw nothing gives nothing)
+      if constexpr (FORM) p[2 * kStep + r] = x.slope * kLog2e;
       reinterpret_cast<int*>(p)[3 * kStep + r] = x.pos;
       if constexpr (W8) {
         if (32 * w < x.run->rows - (x.run->s0 + x.u) * kStep) {
@@ -432,21 +433,24 @@ __global__ void __launch_bounds__(WeighTcShape<KV, D>::THREADS, 1) weights_tc_ke
     while (ok && now.run) {
       then = now;
       advance(then);
-      if (then.run) {
+      // (the place of two or three steps ago: not waited for while this step's work can be done)
+      const bool ahead =
+          then.run && (issued < NQ || __all_sync(0xffffffffu, mbar_test(&free_q[q_in.st], q_in.par ^ 1u)));
+      if (ahead) {
         issue(then);
-        if (!ok) break;
         asm volatile("cp.async.wait_group 1;" ::: "memory");
       } else {
         asm volatile("cp.async.wait_group 0;" ::: "memory");
       }
       finish(now);
+      if (ok && then.run && !ahead) issue(then);
       now = then;
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
   } else if (warp >= kConvWarp) {
     // ===================== 8-bit codes to f16 in MMA form =====================
     if constexpr (W8) {
-      constexpr int CPR = D / 16;                       // 16-code chunks of a row
+        constexpr int CPR = D / 16;                       // 16-code chunks of a row
       constexpr int PER = kHalf / 2 * CPR / 128;        // chunks of a thread in half a tile
       constexpr int ROWS = 128 / CPR;
       const int i0 = threadIdx.x - kConvWarp * 32;
@@ -548,13 +552,22 @@ __global__ void __launch_bounds__(WeighTcShape<KV, D>::THREADS, 1) weights_tc_ke
           tc_fence_after();
           const int left = run->rows - (run->s0 + u) * kStep;  // rows from this step on
           const int cols = min(kStep, left);
-          const int ta = (run->s0 + u) * kStep / a.group, tb = ((run->s0 + u) * kStep + cols - 1) / a.group;
-          const int pa = run->req.base + run->t0 + ta, pb = run->req.base + run->t0 + tb;
-          const bool edge = p0 + kHalf - 1 > pa || (a.window > 0 && p0 < pb + 1 - a.window &&
-                                                    p0 + kHalf > a.sink);
+          // Rows in order see positions in order: this position is seen from column `from` on and, with a
+          // window that it can leave, up to column `end`.
+          const long long back =
+              (long long)(run->req.base + run->t0 - p) * a.group + (run->s0 + u) * kStep;
+          const int from = (int)max(0ll, min((long long)kStep, -back));
+          const int end = a.window > 0 && p >= a.sink
+                              ? (int)max(0ll, min((long long)kStep, (long long)a.window * a.group - back))
+                              : kStep;
+          const int from_any = __reduce_min_sync(0xffffffffu, from);
+          const int from_all = __reduce_max_sync(0xffffffffu, from);
+          const int end_any = __reduce_max_sync(0xffffffffu, end);
+          const int end_all = __reduce_min_sync(0xffffffffu, end);
           const Columns cn = columns(col, cs.st);
           uint64_t sum[4] = {0, 0, 0, 0};
           const uint64_t sc2 = pack2(sc, sc);
+#pragma unroll 1
           for (int c = 0; c < cols; c += 32) {
             uint32_t s[32];
             tmem_ld32(scol + c, s);
@@ -564,6 +577,8 @@ __global__ void __launch_bounds__(WeighTcShape<KV, D>::THREADS, 1) weights_tc_ke
               __syncwarp();
               if (lane == 0) mbar_arrive(&s_read[group]);
             }
+            // (columns that see no position of the warp are left out)
+            if (c + 32 <= from_any || c >= end_any) continue;
             if constexpr (FORM) {
               if (W8 || !cap) {
 #pragma unroll
@@ -578,30 +593,26 @@ __global__ void __launch_bounds__(WeighTcShape<KV, D>::THREADS, 1) weights_tc_ke
                                               __uint_as_float(s[k])));
               }
             }
-            if (edge) {
+            if (c < from_all || c + 32 > end_all) {
+              const int f0 = from - c, e0 = end - c;
 #pragma unroll
-              for (int k = 0; k < 32; ++k) {
-                const int d = cn.pos[c + k] - p;  // how far the position lies behind the row
-                if (d < 0 || (a.window > 0 && d >= a.window && p >= a.sink))
-                  s[k] = __float_as_uint(-INFINITY);
-              }
+              for (int k = 0; k < 32; ++k)
+                if (k < f0 || k >= e0) s[k] = __float_as_uint(-INFINITY);
             }
 #pragma unroll
             for (int k = 0; k < 32; k += 4) {
-              const float4 nl = *reinterpret_cast<const float4*>(cn.neg_lse + c + k);
-              const uint64_t s01 = pack2(__uint_as_float(s[k]), __uint_as_float(s[k + 1]));
-              const uint64_t s23 = pack2(__uint_as_float(s[k + 2]), __uint_as_float(s[k + 3]));
-              uint64_t x01, x23;
+              const ulonglong2 nl = *reinterpret_cast<const ulonglong2*>(cn.neg_lse + c + k);
+              uint64_t x01 = get2(&s[k]), x23 = get2(&s[k + 2]);
               if constexpr (FORM) {
-                x01 = add2(s01, pack2(nl.x, nl.y));
-                x23 = add2(s23, pack2(nl.z, nl.w));
+                x01 = add2(x01, nl.x);
+                x23 = add2(x23, nl.y);
               } else if constexpr (W8) {
-                const float4 f = *reinterpret_cast<const float4*>(cn.factor + c + k);
-                x01 = fma2(s01, pack2(f.x, f.y), pack2(nl.x, nl.y));
-                x23 = fma2(s23, pack2(f.z, f.w), pack2(nl.z, nl.w));
+                const ulonglong2 f = *reinterpret_cast<const ulonglong2*>(cn.factor + c + k);
+                x01 = fma2(x01, f.x, nl.x);
+                x23 = fma2(x23, f.y, nl.y);
               } else {
-                x01 = fma2(s01, sc2, pack2(nl.x, nl.y));
-                x23 = fma2(s23, sc2, pack2(nl.z, nl.w));
+                x01 = fma2(x01, sc2, nl.x);
+                x23 = fma2(x23, sc2, nl.y);
               }
               float e0, e1, e2, e3;
               unpack2(x01, e0, e1);

@@ -283,6 +283,11 @@ cudaError_t launch_chunk_weights_simt(const ChunkArgs& a, int kv_dtype, int head
                                       cudaStream_t s);
 cudaError_t launch_chunk_weights_tc(const ChunkArgs& a, int kv_dtype, int head_dim, const void* tk,
                                     cudaStream_t s);
+// Few rows a request (bf16 queries): a warp a page at a time, `blocks` (1 or 4) blocks of 8 rows a pass.
+constexpr int kWeighFewRows = 32;
+constexpr int weigh_few_wave(int blocks) { return 152 * (blocks == 1 ? 4 : 3); }
+cudaError_t launch_chunk_weights_few(const ChunkArgs& a, int kv_dtype, int head_dim, int blocks,
+                                     cudaStream_t s);
 cudaError_t launch_chunk_weights_combine(const ChunkArgs& a, cudaStream_t s);
 cudaError_t launch_evict_select(const EvictSelectArgs& a, cudaStream_t s);
 cudaError_t launch_evict_move(const EvictMoveArgs& a, cudaStream_t s);
