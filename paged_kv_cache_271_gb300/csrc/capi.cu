@@ -172,7 +172,39 @@ std::mutex g_map_mu;
 std::vector<MapEntry> g_maps;
 EncodeTiledFn g_encode = nullptr;
 
+// The driver's encoder, looked up once (g_map_mu held).
+int find_encoder() {
+  if (!g_encode) {
+    void* fn = nullptr;
+    cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
+    const cudaError_t ce = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000,
+                                                            cudaEnableDefault, &q);
+    if (ce != cudaSuccess || q != cudaDriverEntryPointSuccess || !fn)
+      return set_error(PKV_ECUDA, "cuTensorMapEncodeTiled is not available");
+    g_encode = reinterpret_cast<EncodeTiledFn>(fn);
+  }
+  // (the encoder needs a current context; a new host thread may not have one yet)
+  return bind_context("tensor map");
+}
+
 }  // namespace
+
+int query_tensor_map(const void* q, int num_rows, int h_q, int head_dim, int heads, int tokens,
+                     CUtensorMap* out) {
+  std::lock_guard<std::mutex> lk(g_map_mu);
+  const int st = find_encoder();
+  if (st != PKV_OK) return st;
+  const cuuint64_t dims[3] = {(cuuint64_t)head_dim, (cuuint64_t)h_q, (cuuint64_t)num_rows};
+  const cuuint64_t strides[2] = {(cuuint64_t)head_dim * 2, (cuuint64_t)h_q * head_dim * 2};
+  const cuuint32_t box[3] = {64, (cuuint32_t)heads, (cuuint32_t)tokens};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  const CUresult r = g_encode(out, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(q), dims,
+                              strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return set_error(PKV_ECUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
+  return PKV_OK;
+}
 
 int pool_tensor_map(const void* base, const pkv_cache_desc* d, CUtensorMap* out, int* rank,
                     bool force_2d) {
@@ -190,18 +222,8 @@ int pool_tensor_map(const void* base, const pkv_cache_desc* d, CUtensorMap* out,
       *rank = e.rank;
       return PKV_OK;
     }
-  if (!g_encode) {
-    void* fn = nullptr;
-    cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
-    ce = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault,
-                                          &q);
-    if (ce != cudaSuccess || q != cudaDriverEntryPointSuccess || !fn)
-      return set_error(PKV_ECUDA, "cuTensorMapEncodeTiled is not available");
-    g_encode = reinterpret_cast<EncodeTiledFn>(fn);
-  }
-  // (the encoder needs a current context; a new host thread may not have one yet)
-  const int bst = bind_context("pool tensor map");
-  if (bst != PKV_OK) return bst;
+  const int est = find_encoder();
+  if (est != PKV_OK) return est;
   MapEntry e{};
   e.dev = dev;
   e.base = base;

@@ -334,14 +334,19 @@ int pkv_chunk_weights(const void* q, int32_t dtype_q, int32_t num_rows, int32_t 
   a.width = width;
   a.last_rows = last_rows;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  CUtensorMap tk{};
+  CUtensorMap tk{}, tq{};
   if (t.tc && kv == PKV_BF16 && num_rows > 0) {
     int rank = 2;
     st = pool_tensor_map(k_cache, desc, &tk, &rank, true);
+    // a step's rows are whole tokens where the heads divide them: a box
+    if (st == PKV_OK && kWeighTcRows % a.group == 0) {
+      a.step_tokens = kWeighTcRows / a.group;
+      st = query_tensor_map(q, num_rows, a.h_q, D, a.group, a.step_tokens, &tq);
+    }
     if (st != PKV_OK) return st;
   }
   cudaError_t e = traced("chunk_weights", s, [&] {
-    return t.tc ? launch_chunk_weights_tc(a, kv, D, &tk, s) : launch_chunk_weights_simt(a, kv, D, s);
+    return t.tc ? launch_chunk_weights_tc(a, kv, D, &tk, &tq, s) : launch_chunk_weights_simt(a, kv, D, s);
   });
   st = cuda_status(e, "chunk_weights launch");
   if (st != PKV_OK || a.ctas == 1) return st;  // (one CTA finishes every item)

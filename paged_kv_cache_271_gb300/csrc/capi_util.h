@@ -35,6 +35,11 @@ inline bool is_coded(int dtype) { return dtype == PKV_FP8_E4M3 || dtype == PKV_I
 int pool_tensor_map(const void* base, const pkv_cache_desc* d, CUtensorMap* out, int* rank,
                     bool force_2d = false);
 
+// Queries [num_rows][h_q][head_dim] in bf16 as boxes of `heads` heads of `tokens` rows, 64 dims each, 128-byte
+// swizzled: heads x tokens rows of 128 bytes. Encoded for the call.
+int query_tensor_map(const void* q, int num_rows, int h_q, int head_dim, int heads, int tokens,
+                     CUtensorMap* out);
+
 // Launch tracing: while it is on, a launch is bracketed by two events recorded under `name`.
 extern std::atomic<bool> g_trace_on;
 cudaError_t trace_begin(cudaEvent_t (&ev)[2], cudaStream_t s);

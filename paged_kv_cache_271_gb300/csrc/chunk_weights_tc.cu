@@ -10,18 +10,24 @@
 // clock and SM), and 2 x 512 cycles of exponentials:
 //
 //  * a copy warp streams the tiles' K by TMA (bf16) or as codes that four converter warps widen to f16;
-//  * four loader warps bring the rows' queries into shared memory in MMA form (for 8-bit caches as f16,
-//    scaled by a row's power of two) and each row's numbers: minus its lse, its score factor, slope and
-//    position;
+//  * four loader warps bring the rows' queries into shared memory in MMA form and each row's numbers: minus
+//    its lse, its score factor, slope and position. The queries come by TMA where a step's rows are whole
+//    tokens (a bf16 cache, a group that divides 128: 92 us instead of 97 for 4095 rows over themselves),
+//    else by copies of 16 bytes; for 8-bit caches they are then made f16, scaled by a row's power of two;
 //  * one MMA warp; four groups of four warps that add up weights: group 2 q + h takes half h of the item
 //    in every second step, reading S^T from its own 128 columns of tensor memory, 32 at a time.
+//
+// 4095 prompt rows over themselves, 32 query heads on 8, bf16: 75 us, 69 GFLOP and half as many exponentials
+// as score columns: 0.92 PFLOP/s. The rings and MMAs alone, without the sums, take 62.
 //
 // A step's weights are summed in eight chains of 16 and join the position's sum by a compensated addition
 // (Kahan's), so that sums over thousands of rows are good to fp32. Every wait is bounded
 // (PKV_DEVERR_TIMEOUT); the tensor memory is freed on every path.
 #include <atomic>
+#include <climits>
 #include <cuda.h>
 #include <math.h>
+#include <type_traits>
 
 #include "chunk_score.cuh"
 #include "paged_decode_mma.cuh"
@@ -54,6 +60,10 @@ template <typename KV, int D>
 struct WeighTcShape {
   static constexpr bool W8 = KV::bytes == 1;
   static constexpr int THREADS = 32 * (W8 ? kConvWarp + 4 : kConvWarp);
+  // Registers: the block's at launch, and the warps' own: those of the sums take what the others leave.
+  static constexpr int LAUNCH_REGS = W8 ? 72 : 80, SUM_REGS = W8 ? 88 : 96, REGS = 48;
+  static_assert(kSumThreads * SUM_REGS + (THREADS - kSumThreads) * REGS <= THREADS * LAUNCH_REGS,
+                "the block's own registers");
   static constexpr int TILE = kHalf * D * 2;  // K of a half, or the queries of a step, in MMA form
   static constexpr int NK = D == 128 ? 3 : 6, NQ = D == 128 ? (W8 ? 2 : 3) : 4;
   static constexpr uint32_t IDESC = tc_idesc(128, 0, false, W8);  // (N: the step's columns)
@@ -86,7 +96,8 @@ __device__ __forceinline__ Columns columns(T* base, int st) {
 
 template <typename KV, int D, bool FORM>
 __global__ void __launch_bounds__(WeighTcShape<KV, D>::THREADS, 1) weights_tc_kernel(
-    const ChunkArgs a, const __grid_constant__ CUtensorMap tm_k) {
+    const ChunkArgs a, const __grid_constant__ CUtensorMap tm_k,
+    const __grid_constant__ CUtensorMap tm_q) {
   using S = WeighTcShape<KV, D>;
   constexpr bool W8 = S::W8;
   constexpr int NK = S::NK, NQ = S::NQ, NR = S::NR;
@@ -189,6 +200,7 @@ __global__ void __launch_bounds__(WeighTcShape<KV, D>::THREADS, 1) weights_tc_ke
   };
 
   if (warp >= kMmaWarp && warp < kLoadWarp) {
+    regs_down<S::REGS>();
     if (warp == kCopyWarp) {
       // ===================== copies of K, half by half =====================
       const uint64_t pol = l2_evict_first_policy();
@@ -336,6 +348,7 @@ __global__ void __launch_bounds__(WeighTcShape<KV, D>::THREADS, 1) weights_tc_ke
     }
   } else if (warp >= kLoadWarp && warp < kConvWarp) {
     // ===================== queries and the rows' numbers =====================
+    regs_down<S::REGS>();
     // A step's loads are issued before the step ahead of it is waited for, if there is a place for them
     // yet, whatever runs they belong to.
     // Four lanes copy 64 consecutive bytes of a row; for an 8-bit cache they then make f16 of the row in
@@ -376,7 +389,17 @@ __global__ void __launch_bounds__(WeighTcShape<KV, D>::THREADS, 1) weights_tc_ke
       x.slope = FORM && a.slopes ? a.slopes[run.j * a.group + g] : 0.f;
       x.k_scale = W8 ? a.k_scales[run.j] : 1.f;
       x.pos = run.req.base + run.t0 + (int)t;
-      if (32 * w < run.rows - (int)first) {  // (columns beyond the last block of 32 are not used)
+      if (!W8 && a.step_tokens > 0) {  // the step's tokens in a box for each 64 dims, by the first warp
+        if (w == 0 && elect_one()) {
+          mbar_arrive_expect_tx(&full_q[q_in.st], kStep * D * 2);
+          const int token = run.req.q0 + run.t0 + (run.s0 + x.u) * a.step_tokens;
+#pragma unroll
+          for (int bx = 0; bx < D / 64; ++bx)
+            tma_load_box(ring + S::OFF_Q + q_in.st * S::TILE + bx * (kStep * 128), &tm_q, bx * 64,
+                         run.j * a.group, token, &full_q[q_in.st]);
+        }
+        __syncwarp();
+      } else if (32 * w < run.rows - (int)first) {  // (columns beyond the last block of 32 are not used)
 #pragma unroll
         for (int g4 = 0; g4 < 4; ++g4) {
           const int from = 8 * g4 + (lane >> 2);
@@ -420,7 +443,7 @@ __global__ void __launch_bounds__(WeighTcShape<KV, D>::THREADS, 1) weights_tc_ke
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) {
-        mbar_arrive(&full_q[q_out.st]);
+        if (W8 || a.step_tokens == 0 || w > 0) mbar_arrive(&full_q[q_out.st]);  // (else: its copy's word)
         mbar_arrive(&full_c[cs.st]);
       }
       ++finished;
@@ -447,8 +470,12 @@ __global__ void __launch_bounds__(WeighTcShape<KV, D>::THREADS, 1) weights_tc_ke
       now = then;
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
+    if (!ok && !W8 && a.step_tokens > 0 && w == 0)  // (else the MMAs have waited for every box)
+      for (int t = max(0, issued - NQ); t < issued; ++t)
+        mbar_wait(&full_q[t % NQ], (uint32_t)(t / NQ) & 1u, a.err);
   } else if (warp >= kConvWarp) {
     // ===================== 8-bit codes to f16 in MMA form =====================
+    regs_down<S::REGS>();
     if constexpr (W8) {
         constexpr int CPR = D / 16;                       // 16-code chunks of a row
       constexpr int PER = kHalf / 2 * CPR / 128;        // chunks of a thread in half a tile
@@ -512,6 +539,7 @@ __global__ void __launch_bounds__(WeighTcShape<KV, D>::THREADS, 1) weights_tc_ke
     }
   } else {
     // ===================== sums =====================
+    regs_up<S::SUM_REGS>();
     const int group = warp >> 2, h = group & 1, q = group >> 1;
     const int r = threadIdx.x & 127;  // position of the half
     const uint32_t scol = tmem + ((uint32_t)((warp & 3) * 32) << 16) + 128 * group;
@@ -540,6 +568,19 @@ __global__ void __launch_bounds__(WeighTcShape<KV, D>::THREADS, 1) weights_tc_ke
         __syncwarp();
         if (lane == 0) mbar_arrive(&free_k[k.st]);
       }
+      // Rows in order see positions in order: of the run's rows, this position is seen from `from` on and up
+      // to the last or, with a window that it can leave, up to `end`. (Rows that are not there hold what
+      // lies behind the request's, or zeros.)
+      const unsigned rows = (unsigned)(run->rows - run->s0 * kStep);
+      const long long first = (long long)(p - run->req.base - run->t0) * a.group - (long long)run->s0 * kStep;
+      const unsigned from = (unsigned)max(0ll, min((long long)INT_MAX, first));
+      const unsigned end = a.window > 0 && p >= a.sink
+                               ? (unsigned)max(0ll, min((long long)rows, first + (long long)a.window * a.group))
+                               : rows;
+      const unsigned from_any = __reduce_min_sync(0xffffffffu, from);
+      const unsigned from_all = __reduce_max_sync(0xffffffffu, from);
+      const unsigned end_any = __reduce_max_sync(0xffffffffu, end);
+      const unsigned end_all = __reduce_min_sync(0xffffffffu, end);
       Place<kCols> cs = base;
       cs.advance(q);
       for (int u = q; ok && u < n; u += 2, cs.advance(2)) {
@@ -550,78 +591,75 @@ __global__ void __launch_bounds__(WeighTcShape<KV, D>::THREADS, 1) weights_tc_ke
         if (h < halves) {
           ph_s ^= 1u;
           tc_fence_after();
-          const int left = run->rows - (run->s0 + u) * kStep;  // rows from this step on
-          const int cols = min(kStep, left);
-          // Rows in order see positions in order: this position is seen from column `from` on and, with a
-          // window that it can leave, up to column `end`.
-          const long long back =
-              (long long)(run->req.base + run->t0 - p) * a.group + (run->s0 + u) * kStep;
-          const int from = (int)max(0ll, min((long long)kStep, -back));
-          const int end = a.window > 0 && p >= a.sink
-                              ? (int)max(0ll, min((long long)kStep, (long long)a.window * a.group - back))
-                              : kStep;
-          const int from_any = __reduce_min_sync(0xffffffffu, from);
-          const int from_all = __reduce_max_sync(0xffffffffu, from);
-          const int end_any = __reduce_max_sync(0xffffffffu, end);
-          const int end_all = __reduce_min_sync(0xffffffffu, end);
+          const unsigned u0 = (unsigned)u * kStep;
+          const int cols = (int)min((unsigned)kStep, rows - u0);
           const Columns cn = columns(col, cs.st);
           uint64_t sum[4] = {0, 0, 0, 0};
           const uint64_t sc2 = pack2(sc, sc);
+          // With the tests of what its positions see, or, where every row sees them all, without: in one
+          // body the tests cost more than the few steps that need them (4095 rows over themselves: 85 us
+          // instead of 75).
+          auto step = [&](auto edge) {
 #pragma unroll 1
-          for (int c = 0; c < cols; c += 32) {
-            uint32_t s[32];
-            tmem_ld32(scol + c, s);
-            tmem_wait_ld();
-            if (c + 32 >= cols) {
-              tc_fence_before();
-              __syncwarp();
-              if (lane == 0) mbar_arrive(&s_read[group]);
-            }
-            // (columns that see no position of the warp are left out)
-            if (c + 32 <= from_any || c >= end_any) continue;
-            if constexpr (FORM) {
-              if (W8 || !cap) {
-#pragma unroll
-                for (int k = 0; k < 32; ++k)
-                  s[k] = __float_as_uint(__uint_as_float(s[k]) * (W8 ? cn.factor[c + k] : sc));
+            for (int c = 0; c < cols; c += 32) {
+              uint32_t s[32];
+              tmem_ld32(scol + c, s);
+              tmem_wait_ld();
+              if (c + 32 >= cols) {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&s_read[group]);
               }
-              if (cap) cap_scores<32>(s, in, top);
-              if (a.slopes) {
-#pragma unroll
-                for (int k = 0; k < 32; ++k)
-                  s[k] = __float_as_uint(fmaf(cn.slope[c + k], (float)(p - cn.pos[c + k]),
-                                              __uint_as_float(s[k])));
-              }
-            }
-            if (c < from_all || c + 32 > end_all) {
-              const int f0 = from - c, e0 = end - c;
-#pragma unroll
-              for (int k = 0; k < 32; ++k)
-                if (k < f0 || k >= e0) s[k] = __float_as_uint(-INFINITY);
-            }
-#pragma unroll
-            for (int k = 0; k < 32; k += 4) {
-              const ulonglong2 nl = *reinterpret_cast<const ulonglong2*>(cn.neg_lse + c + k);
-              uint64_t x01 = get2(&s[k]), x23 = get2(&s[k + 2]);
+              // (columns that see no position of the warp are left out)
+              if (decltype(edge)::value && (u0 + c + 32 <= from_any || u0 + c >= end_any)) continue;
               if constexpr (FORM) {
-                x01 = add2(x01, nl.x);
-                x23 = add2(x23, nl.y);
-              } else if constexpr (W8) {
-                const ulonglong2 f = *reinterpret_cast<const ulonglong2*>(cn.factor + c + k);
-                x01 = fma2(x01, f.x, nl.x);
-                x23 = fma2(x23, f.y, nl.y);
-              } else {
-                x01 = fma2(x01, sc2, nl.x);
-                x23 = fma2(x23, sc2, nl.y);
+                if (W8 || !cap) {
+#pragma unroll
+                  for (int k = 0; k < 32; ++k)
+                    s[k] = __float_as_uint(__uint_as_float(s[k]) * (W8 ? cn.factor[c + k] : sc));
+                }
+                if (cap) cap_scores<32>(s, in, top);
+                if (a.slopes) {
+#pragma unroll
+                  for (int k = 0; k < 32; ++k)
+                    s[k] = __float_as_uint(fmaf(cn.slope[c + k], (float)(p - cn.pos[c + k]),
+                                                __uint_as_float(s[k])));
+                }
               }
-              float e0, e1, e2, e3;
-              unpack2(x01, e0, e1);
-              unpack2(x23, e2, e3);
-              sum[(k >> 1) & 3] = add2(sum[(k >> 1) & 3], pack2(ex2_approx(e0), ex2_approx(e1)));
-              sum[((k >> 1) & 3) + 1] =
-                  add2(sum[((k >> 1) & 3) + 1], pack2(ex2_approx(e2), ex2_approx(e3)));
+              if constexpr (decltype(edge)::value) {
+                const int f0 = (int)(from - (u0 + c)), e0 = (int)(end - (u0 + c));
+#pragma unroll
+                for (int k = 0; k < 32; ++k)
+                  if (k < f0 || k >= e0) s[k] = __float_as_uint(-INFINITY);
+              }
+#pragma unroll
+              for (int k = 0; k < 32; k += 4) {
+                const ulonglong2 nl = *reinterpret_cast<const ulonglong2*>(cn.neg_lse + c + k);
+                uint64_t x01 = get2(&s[k]), x23 = get2(&s[k + 2]);
+                if constexpr (FORM) {
+                  x01 = add2(x01, nl.x);
+                  x23 = add2(x23, nl.y);
+                } else if constexpr (W8) {
+                  const ulonglong2 f = *reinterpret_cast<const ulonglong2*>(cn.factor + c + k);
+                  x01 = fma2(x01, f.x, nl.x);
+                  x23 = fma2(x23, f.y, nl.y);
+                } else {
+                  x01 = fma2(x01, sc2, nl.x);
+                  x23 = fma2(x23, sc2, nl.y);
+                }
+                float e0, e1, e2, e3;
+                unpack2(x01, e0, e1);
+                unpack2(x23, e2, e3);
+                sum[(k >> 1) & 3] = add2(sum[(k >> 1) & 3], pack2(ex2_approx(e0), ex2_approx(e1)));
+                sum[((k >> 1) & 3) + 1] =
+                    add2(sum[((k >> 1) & 3) + 1], pack2(ex2_approx(e2), ex2_approx(e3)));
+              }
             }
-          }
+          };
+          if (u0 < from_all || u0 + ((cols + 31) & ~31) > end_all)
+            step(std::true_type{});
+          else
+            step(std::false_type{});
           float x, y;
           unpack2(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), x, y);
           const float add = (x + y) - lost, z = total + add;
@@ -671,41 +709,48 @@ __global__ void __launch_bounds__(WeighTcShape<KV, D>::THREADS, 1) weights_tc_ke
 }
 
 template <typename KV, int D, bool FORM>
-cudaError_t launch_shape(const ChunkArgs& a, const CUtensorMap& tk, cudaStream_t s) {
+cudaError_t launch_shape(const ChunkArgs& a, const CUtensorMap& tk, const CUtensorMap& tq,
+                         cudaStream_t s) {
   using S = WeighTcShape<KV, D>;
   static std::atomic<unsigned long long> attr_done{0};  // one bit per device
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev >= 64 || !((attr_done.load() >> dev) & 1ull)) {
+    cudaFuncAttributes fa{};  // (a launch with fewer could not give the sums theirs: they would wait)
+    e = cudaFuncGetAttributes(&fa, weights_tc_kernel<KV, D, FORM>);
+    if (e != cudaSuccess) return e;
+    if (fa.numRegs < S::LAUNCH_REGS) return cudaErrorLaunchOutOfResources;
     e = cudaFuncSetAttribute(weights_tc_kernel<KV, D, FORM>,
                              cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM);
     if (e != cudaSuccess) return e;
     if (dev < 64) attr_done.fetch_or(1ull << dev);
   }
-  weights_tc_kernel<KV, D, FORM><<<a.ctas, S::THREADS, S::SMEM, s>>>(a, tk);
+  weights_tc_kernel<KV, D, FORM><<<a.ctas, S::THREADS, S::SMEM, s>>>(a, tk, tq);
   return cudaGetLastError();
 }
 
 template <typename KV, int D>
-cudaError_t launch_t(const ChunkArgs& a, const CUtensorMap& tk, cudaStream_t s) {
-  return a.softcap > 0.f || a.slopes ? launch_shape<KV, D, true>(a, tk, s)
-                                     : launch_shape<KV, D, false>(a, tk, s);
+cudaError_t launch_t(const ChunkArgs& a, const CUtensorMap& tk, const CUtensorMap& tq,
+                     cudaStream_t s) {
+  return a.softcap > 0.f || a.slopes ? launch_shape<KV, D, true>(a, tk, tq, s)
+                                     : launch_shape<KV, D, false>(a, tk, tq, s);
 }
 
 }  // namespace
 
 cudaError_t launch_chunk_weights_tc(const ChunkArgs& a, int kv_dtype, int head_dim, const void* tk,
-                                    cudaStream_t s) {
+                                    const void* tq, cudaStream_t s) {
   const CUtensorMap& mk = *static_cast<const CUtensorMap*>(tk);
+  const CUtensorMap& mq = *static_cast<const CUtensorMap*>(tq);
   if (head_dim == 64) {
-    if (kv_dtype == PKV_BF16) return launch_t<BF16, 64>(a, mk, s);
-    if (kv_dtype == PKV_FP8_E4M3) return launch_t<FP8, 64>(a, mk, s);
-    return launch_t<INT8, 64>(a, mk, s);
+    if (kv_dtype == PKV_BF16) return launch_t<BF16, 64>(a, mk, mq, s);
+    if (kv_dtype == PKV_FP8_E4M3) return launch_t<FP8, 64>(a, mk, mq, s);
+    return launch_t<INT8, 64>(a, mk, mq, s);
   }
-  if (kv_dtype == PKV_BF16) return launch_t<BF16, 128>(a, mk, s);
-  if (kv_dtype == PKV_FP8_E4M3) return launch_t<FP8, 128>(a, mk, s);
-  return launch_t<INT8, 128>(a, mk, s);
+  if (kv_dtype == PKV_BF16) return launch_t<BF16, 128>(a, mk, mq, s);
+  if (kv_dtype == PKV_FP8_E4M3) return launch_t<FP8, 128>(a, mk, mq, s);
+  return launch_t<INT8, 128>(a, mk, mq, s);
 }
 
 }  // namespace pkv

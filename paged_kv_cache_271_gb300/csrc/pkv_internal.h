@@ -221,6 +221,7 @@ struct ChunkArgs {
   float* weights_out;
   int64_t width;
   int last_rows;
+  int step_tokens;  // tcgen05, bf16 cache: whole tokens of a step, by TMA (0: rows by copies)
 };
 
 // Eviction: kept[b][j][i], i < kept_lens[b], are the chosen positions of KV head j in rising order.
@@ -282,7 +283,7 @@ constexpr int weigh_simt_wave(int) { return 152 * 4; }
 cudaError_t launch_chunk_weights_simt(const ChunkArgs& a, int kv_dtype, int head_dim,
                                       cudaStream_t s);
 cudaError_t launch_chunk_weights_tc(const ChunkArgs& a, int kv_dtype, int head_dim, const void* tk,
-                                    cudaStream_t s);
+                                    const void* tq, cudaStream_t s);
 // Few rows a request (bf16 queries): a warp a page at a time, `blocks` (1 or 4) blocks of 8 rows a pass.
 constexpr int kWeighFewRows = 32;
 constexpr int weigh_few_wave(int blocks) { return 152 * (blocks == 1 ? 4 : 3); }

@@ -84,6 +84,16 @@ __device__ __forceinline__ float query_to_f16(uint4 (&in)[RND], const float sc) 
   return fmaxf(fabsf(sc) * __int_as_float((127 - e) << 23), 0x1p-126f);
 }
 
+// 3-D tiled TMA load of one box into shared memory, completing on `bar` (x a multiple of 8 elements).
+__device__ __forceinline__ void tma_load_box(uint32_t smem_dst, const CUtensorMap* map, int x, int y,
+                                             int z, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+      : "memory");
+}
+
 // 16 consecutive columns of this thread's lane of tensor memory.
 __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
   asm volatile(
