@@ -51,7 +51,7 @@ constexpr int kMmaWarp = kSumThreads / 32;
 constexpr int kCopyWarp = kMmaWarp + 1;
 constexpr int kLoadWarp = kMmaWarp + 4;    // first of four (two warps before are idle)
 constexpr int kConvWarp = kLoadWarp + 4;   // first of four (8-bit caches)
-constexpr int kCols = 4;                   // steps whose rows' numbers are kept
+constexpr int kCols = 4;                   // steps whose rows' numbers are kept: two even, two odd
 constexpr int kRuns = 16;
 constexpr uint32_t kTmemCols = 512;        // S^T of group g at 128 g
 static_assert(kItem == 2 * kHalf && kStep == 128, "two halves, M = 128, N = 128");
@@ -74,8 +74,8 @@ struct WeighTcShape {
   static constexpr int OFF_COL = OFF_RAW + NR * RAW;        // [kCols][4][128] a step's rows' numbers
   static constexpr int OFF_SUM = OFF_COL + kCols * 4 * kStep * 4;  // [2][256] the second steps' sums
   static constexpr int OFF_BAR = OFF_SUM + 2 * kItem * 4;
-  static constexpr int BARS = 2 * NK + 2 * NQ + 2 * NR + 2 * 4 + 2 * kCols + 8 + 1 + kRuns;
-  static_assert(NK + (NR + 1) / 2 + 4 <= kRuns, "runs in flight");
+  static constexpr int BARS = 2 * NK + 2 * NQ + 2 * NR + 2 * 4 + 2 * kCols + 8 + 1 + 2 * kRuns;
+  static constexpr int READERS = kSumThreads / 32 + 1 + 4 + (W8 ? 4 : 0);  // warps that follow the runs
   static constexpr int OFF_MISC = OFF_BAR + 8 * BARS;       // masks, TMEM address
   static constexpr int SMEM = 1024 + OFF_MISC + 4 * (NK + NR + 1) + 16;
   static_assert(SMEM <= 224 * 1024 && SMEM > 114 * 1024, "one CTA per SM");
@@ -122,6 +122,7 @@ __global__ void __launch_bounds__(WeighTcShape<KV, D>::THREADS, 1) weights_tc_ke
   uint64_t* taken = handed + 4;                                      // [2][half] read
   uint64_t* mma_idle = taken + 4;
   uint64_t* run_there = mma_idle + 1;                                // [kRuns]
+  uint64_t* run_gone = run_there + kRuns;                            // [kRuns] its place is free again
   int* page_mask = reinterpret_cast<int*>(smem + S::OFF_MISC);       // [NK] good pages of the half
   int* raw_mask = page_mask + NK;                                    // [NR]
   uint32_t* s_taddr = reinterpret_cast<uint32_t*>(raw_mask + NR);
@@ -135,7 +136,7 @@ __global__ void __launch_bounds__(WeighTcShape<KV, D>::THREADS, 1) weights_tc_ke
   if (threadIdx.x == kCopyWarp * 32) {
     for (int s = 0; s < NK; ++s) {
       mbar_init(&full_k[s], W8 ? 4 : 1);
-      mbar_init(&free_k[s], 1 + 8);  // the MMAs and the two groups of the half (for its mask)
+      mbar_init(&free_k[s], 1 + kSumThreads / 32);  // the MMAs and every warp of the sums
     }
     for (int s = 0; s < NQ; ++s) {
       mbar_init(&full_q[s], 4);
@@ -158,7 +159,10 @@ __global__ void __launch_bounds__(WeighTcShape<KV, D>::THREADS, 1) weights_tc_ke
       mbar_init(&taken[i], 4);
     }
     mbar_init(mma_idle, 1);
-    for (int i = 0; i < kRuns; ++i) mbar_init(&run_there[i], 1);
+    for (int i = 0; i < kRuns; ++i) {
+      mbar_init(&run_there[i], 1);
+      mbar_init(&run_gone[i], S::READERS);
+    }
     mbar_fence_init();
     if constexpr (!W8)
       asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm_k)) : "memory");
@@ -186,10 +190,11 @@ __global__ void __launch_bounds__(WeighTcShape<KV, D>::THREADS, 1) weights_tc_ke
     release();
     return;
   }
-  // run i of the share, or nullptr after the last (or a wait that gave up)
+  // run i of the share, or nullptr after the last (or a wait that gave up); run i - 2 is done with
   auto get_run = [&](uint32_t i) -> const WeighRun* {
     const bool got = mbar_wait(&run_there[i % kRuns], (i / kRuns) & 1u, a.err);
     const WeighRun* r = &runs[i % kRuns];
+    if (i >= 2 && lane == 0) mbar_arrive(&run_gone[(i - 2) % kRuns]);
     return __all_sync(0xffffffffu, got && r->n > 0) ? r : nullptr;
   };
   // Step u of a run (from its first on) belongs to the groups 2 (u % 2) + h; a run without rows has no
@@ -215,6 +220,9 @@ __global__ void __launch_bounds__(WeighTcShape<KV, D>::THREADS, 1) weights_tc_ke
       for (uint32_t unit = 0;; ++unit) {
         WeighRun* run = &runs[unit % kRuns];
         if (lane == 0) {  // (a wait that gave up ends the share for every warp)
+          // (items without rows take no place in the rings: nothing else holds this warp back there)
+          if (unit >= kRuns)
+            ok = mbar_wait(&run_gone[unit % kRuns], (unit / kRuns - 1) & 1u, a.err) && ok;
           if (!ok || !walk.next(a, *run)) run->n = 0;
           mbar_arrive(&run_there[unit % kRuns]);
         }
@@ -363,8 +371,7 @@ __global__ void __launch_bounds__(WeighTcShape<KV, D>::THREADS, 1) weights_tc_ke
       float lse, slope, k_scale;  // (as they come: used when the step is finished)
     };
     uint32_t unit = 0;
-    auto advance = [&](Step& x) {  // to the next step, x.run = nullptr behind the last
-      if (x.run && ++x.u < steps_of(x.run)) return;
+    auto next_run = [&](Step& x) {  // to the first step of the next run that has any, or nullptr
       do {
         x.run = get_run(unit++);
       } while (x.run && steps_of(x.run) == 0);
@@ -375,8 +382,8 @@ __global__ void __launch_bounds__(WeighTcShape<KV, D>::THREADS, 1) weights_tc_ke
              ((((4 * d & 7) + (lane & 3)) ^ (row0 & 7)) << 4);
     };
     Place<NQ> q_in, q_out;
-    Place<kCols> cs;
-    int issued = 0, finished = 0;
+    uint32_t used[2] = {0, 0};  // places taken for even and odd steps of runs
+    int issued = 0;
     auto issue = [&](Step& x) {
       if (issued >= NQ) ok = __all_sync(0xffffffffu, mbar_wait(&free_q[q_in.st], q_in.par ^ 1u, a.err));
       if (!ok) return;
@@ -419,10 +426,15 @@ __global__ void __launch_bounds__(WeighTcShape<KV, D>::THREADS, 1) weights_tc_ke
       q_in.advance(1);
     };
     auto finish = [&](const Step& x) {
-      if (finished >= kCols) ok = __all_sync(0xffffffffu, mbar_wait(&free_c[cs.st], cs.par ^ 1u, a.err));
+      // (a ring for each pair of groups, so that a group sees every phase of its barriers)
+      const int q = x.u & 1;
+      const uint32_t use = q ? used[1] : used[0];
+      const int cs = 2 * q + (int)(use & 1u);
+      if (use >= 2)
+        ok = __all_sync(0xffffffffu, mbar_wait(&free_c[cs], ((use >> 1) & 1u) ^ 1u, a.err));
       if (!ok) return;
       const float sc = a.scale * kLog2e * x.k_scale;
-      float* const p = reinterpret_cast<float*>(col) + cs.st * 4 * kStep;
+      float* const p = reinterpret_cast<float*>(col) + cs * 4 * kStep;
       p[r] = x.lse == -INFINITY ? -INFINITY : -x.lse * kLog2e;  // (a row that saw nothing gives nothing)
       if constexpr (FORM) p[2 * kStep + r] = x.slope * kLog2e;
       reinterpret_cast<int*>(p)[3 * kStep + r] = x.pos;
@@ -444,21 +456,32 @@ __global__ void __launch_bounds__(WeighTcShape<KV, D>::THREADS, 1) weights_tc_ke
       __syncwarp();
       if (lane == 0) {
         if (W8 || a.step_tokens == 0 || w > 0) mbar_arrive(&full_q[q_out.st]);  // (else: its copy's word)
-        mbar_arrive(&full_c[cs.st]);
+        mbar_arrive(&full_c[cs]);
       }
-      ++finished;
+      if (q)
+        ++used[1];
+      else
+        ++used[0];
       q_out.advance(1);
-      cs.advance(1);
     };
     Step now{}, then{};
-    advance(now);
+    next_run(now);
     if (now.run) issue(now);
     while (ok && now.run) {
       then = now;
-      advance(then);
+      // The step behind this one, if it is known already: a run that is still to come may wait for this step,
+      // and this step's run is held until then (a warp gives run i back when it takes run i + 2).
+      bool known = ++then.u < steps_of(now.run), last = false;
+      if (!known &&
+          __all_sync(0xffffffffu, mbar_test(&run_there[unit % kRuns], (unit / kRuns) & 1u))) {
+        then.run = get_run(unit++);
+        then.u = 0;
+        last = !then.run;
+        known = then.run && steps_of(then.run) > 0;
+      }
       // (the place of two or three steps ago: not waited for while this step's work can be done)
       const bool ahead =
-          then.run && (issued < NQ || __all_sync(0xffffffffu, mbar_test(&free_q[q_in.st], q_in.par ^ 1u)));
+          known && (issued < NQ || __all_sync(0xffffffffu, mbar_test(&free_q[q_in.st], q_in.par ^ 1u)));
       if (ahead) {
         issue(then);
         asm volatile("cp.async.wait_group 1;" ::: "memory");
@@ -466,6 +489,7 @@ __global__ void __launch_bounds__(WeighTcShape<KV, D>::THREADS, 1) weights_tc_ke
         asm volatile("cp.async.wait_group 0;" ::: "memory");
       }
       finish(now);
+      if (ok && !known && !last) next_run(then);
       if (ok && then.run && !ahead) issue(then);
       now = then;
     }
@@ -546,7 +570,7 @@ __global__ void __launch_bounds__(WeighTcShape<KV, D>::THREADS, 1) weights_tc_ke
     bool ok = true;
     uint32_t ph_s = 0, hands = 0;  // parity of s_done's next phase; runs that handed sums over
     Place<NK> ks;
-    Place<kCols> base;  // of the run's first step
+    Place<2> cs;  // of the group's steps
     const float sc = a.scale * kLog2e;
     const bool cap = FORM && a.softcap > 0.f;
     const float in = cap ? (W8 ? kLn2 : kLn2 * sc) / a.softcap : 0.f, top = a.softcap * kLog2e;
@@ -560,11 +584,13 @@ __global__ void __launch_bounds__(WeighTcShape<KV, D>::THREADS, 1) weights_tc_ke
       const float before = writes && run->whole && a.add_to ? a.add_to[at] : 0.f;  // (on its way meanwhile)
       float total = 0.f, lost = 0.f;
       bool good = false;
-      if (h < halves && n > 0) {
+      // (Every warp waits for the other half's K too: a phase that a warp does not see could still be to
+      // come when it asks for the one behind it, whose parity then looks as if it were over.)
+      for (int i = 0; i < halves && n > 0; ++i) {
         Place<NK> k = ks;
-        k.advance(h);
+        k.advance(i);
         ok = ok && mbar_wait(&full_k[k.st], k.par, a.err);
-        good = ok && ((page_mask[k.st] >> (r >> 4)) & 1);
+        if (i == h) good = ok && ((page_mask[k.st] >> (r >> 4)) & 1);
         __syncwarp();
         if (lane == 0) mbar_arrive(&free_k[k.st]);
       }
@@ -581,10 +607,9 @@ __global__ void __launch_bounds__(WeighTcShape<KV, D>::THREADS, 1) weights_tc_ke
       const unsigned from_all = __reduce_max_sync(0xffffffffu, from);
       const unsigned end_any = __reduce_max_sync(0xffffffffu, end);
       const unsigned end_all = __reduce_min_sync(0xffffffffu, end);
-      Place<kCols> cs = base;
-      cs.advance(q);
-      for (int u = q; ok && u < n; u += 2, cs.advance(2)) {
-        ok = mbar_wait(&full_c[cs.st], cs.par, a.err);
+      for (int u = q; ok && u < n; u += 2, cs.advance(1)) {
+        const int at_c = 2 * q + cs.st;
+        ok = mbar_wait(&full_c[at_c], cs.par, a.err);
         if (ok && h < halves) ok = mbar_wait(&s_done[group], ph_s, a.err);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
@@ -593,7 +618,7 @@ __global__ void __launch_bounds__(WeighTcShape<KV, D>::THREADS, 1) weights_tc_ke
           tc_fence_after();
           const unsigned u0 = (unsigned)u * kStep;
           const int cols = (int)min((unsigned)kStep, rows - u0);
-          const Columns cn = columns(col, cs.st);
+          const Columns cn = columns(col, at_c);
           uint64_t sum[4] = {0, 0, 0, 0};
           const uint64_t sc2 = pack2(sc, sc);
           // With the tests of what its positions see, or, where every row sees them all, without: in one
@@ -667,7 +692,7 @@ __global__ void __launch_bounds__(WeighTcShape<KV, D>::THREADS, 1) weights_tc_ke
           total = z;
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(&free_c[cs.st]);
+        if (lane == 0) mbar_arrive(&free_c[at_c]);
       }
       // ---- the run's sums: the second steps' group hands its own to the first's, which writes ----
       if (n > 1 && h < halves) {
@@ -695,10 +720,7 @@ __global__ void __launch_bounds__(WeighTcShape<KV, D>::THREADS, 1) weights_tc_ke
         else
           a.ws_acc[((size_t)blockIdx.x * 2 + run->slot) * kItem + h * kHalf + r] = x;
       }
-      if (n > 0) {
-        ks.skip(halves);
-        base.skip(n);
-      }
+      if (n > 0) ks.skip(halves);
     }
   }
 

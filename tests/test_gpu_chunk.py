@@ -250,6 +250,43 @@ def test_one_long_context_and_many_requests(io, cache):
     assert pkv.device_error() == 0
 
 
+@pytest.mark.parametrize("cache,d", [("bf16", 128), ("bf16", 64), ("fp8", 128)])
+@pytest.mark.parametrize("new,group", [(32, 4), (9, 4), (13, 3)])
+def test_sums_of_many_short_runs(cache, d, new, group):
+    """A CTA's share is tens of items of one step each, some of one half and some of two, whose rings
+    begin before the first copies land; every call gives the same bits."""
+    r = np.random.default_rng(8)
+    c = Chunk(r.integers(0, 1700, 96), [new] * 96, 6 * group, 6, d, "bf16", cache, seed=8)
+    lse = torch.empty(c.q.shape[:2], device="cuda")
+    c.check(c.attend(lse=lse), lse)
+    ref, tol = c.sums(lse)
+    first = c.weigh(lse)
+    assert ((first.double() - ref).abs() <= tol).all()
+    spoil = torch.empty(1 << 26, device="cuda")
+    for i in range(30):
+        if i % 3 == 0:
+            spoil.fill_(i)  # (K comes from memory again, in another order)
+        assert torch.equal(c.weigh(lse), first)
+    assert pkv.device_error() == 0
+
+
+@pytest.mark.parametrize("cache,d,new", [("bf16", 64, 20), ("fp8", 64, 20), ("fp8", 64, 2)])
+def test_sums_of_long_contexts_behind_a_window(cache, d, new):
+    """Most items have no rows: more of them in a share than the kernel keeps at a time."""
+    c = Chunk([20000] * 6, [new] * 6, 16, 8, d, "bf16", cache, seed=9, window=40, sinks=3)
+    lse = torch.empty(c.q.shape[:2], device="cuda")
+    c.check(c.attend(lse=lse), lse)
+    ref, tol = c.sums(lse)
+    for _ in range(5):
+        out = torch.full((6, 8, c.bt.shape[1] * 16), 5.0, device="cuda")
+        c.weigh(lse, out=out, add_to=None)
+        for b in range(6):
+            n = c.ctx[b]
+            assert ((out[b, :, :n].double() - ref[b, :, :n]).abs() <= tol[b, :, :n]).all()
+            assert (out[b, :, n:] == 5).all()
+    assert pkv.device_error() == 0
+
+
 @pytest.mark.parametrize("io,cache,d", [KINDS[i] for i in (0, 1, 2, 5, 6, 8)])
 @pytest.mark.parametrize("window,sinks", [(0, 0), (70, 5)])
 def test_values_and_keys_that_are_not_finite_reach_only_rows_that_see_them(io, cache, d, window, sinks):
