@@ -351,7 +351,7 @@ __global__ void __launch_bounds__(TcShape<KV, D>::THREADS, 1) chunk_tc_kernel(
       const uint64_t k_desc = tc_desc(ring, 16, 1024), v_desc = tc_desc(ring + S::OFF_V, 2048, 1024);
       const uint64_t q_desc = tc_desc(ring + S::OFF_Q, 16, 1024);
       bool ok = true;
-      uint32_t ph_p = 0;  // parities of p_ready's next phase, bit g
+      uint32_t ph_p = 0, ph_q = 0;  // parities of the next phases of p_ready and q_ready, bit g
       Place<NK> ks;       // K of the next S
       Place<NV> vs;       // V of the next P V
       auto wait = [&](uint64_t* bar, uint32_t par) {
@@ -397,7 +397,10 @@ __global__ void __launch_bounds__(TcShape<KV, D>::THREADS, 1) chunk_tc_kernel(
         const int n = wide ? 2 * uniform(run->n) : uniform(run->n);
         auto step_s = [&](int u) {  // S of step u; in a run's first two steps the queries are waited for
           const int group = u & 1;
-          if (u < 2) ok = wait(&q_ready[group], unit & 1);
+          if (u < 2) {
+            ok = wait(&q_ready[group], (ph_q >> group) & 1u);
+            ph_q ^= 1u << group;
+          }
           if (ok && (!wide || group == 0)) ok = wait(&full_k[ks.st], ks.par);
           if (ok) s_mma(group, !wide || group == 1);
         };
@@ -546,7 +549,10 @@ __global__ void __launch_bounds__(TcShape<KV, D>::THREADS, 1) chunk_tc_kernel(
       return q_at + (d >> 1) * (kGroupRows * 128) + g * 1024 +
              ((((4 * d & 7) + (lane & 3)) ^ (row0 & 7)) << 4);
     };
-    auto load_query = [&](const Row& x) {
+    // Queries are brought for runs in which the group has a step: the MMAs wait for each of them.
+    auto has_step = [&](const ChunkRun& run) { return run.rows > kGroupRows || wg < run.n; };
+    auto load_query = [&](const ChunkRun& run, const Row& x) {
+      if (!has_step(run)) return;
 #pragma unroll
       for (int g = 0; g < 2; ++g) {
         const int from = 16 * h + 8 * g + (lane >> 2);
@@ -561,6 +567,7 @@ __global__ void __launch_bounds__(TcShape<KV, D>::THREADS, 1) chunk_tc_kernel(
       }
     };
     auto store_query = [&](const ChunkRun& run) {
+      if (!has_step(run)) return;
       asm volatile("cp.async.wait_all;" ::: "memory");
       if constexpr (W8) {
         const float sc = a.scale * kLog2e * a.k_scales[run.j];
@@ -583,7 +590,7 @@ __global__ void __launch_bounds__(TcShape<KV, D>::THREADS, 1) chunk_tc_kernel(
     const ChunkRun* next = get_run(0);
     if (next) {
       me = find_row(*next);
-      load_query(me);
+      load_query(*next, me);
       store_query(*next);
     }
     float sc = a.scale * kLog2e;  // of the row's scores (log2 domain)
@@ -607,8 +614,11 @@ __global__ void __launch_bounds__(TcShape<KV, D>::THREADS, 1) chunk_tc_kernel(
       const ChunkRun* after = nullptr;
       for (int i = i_first; ok && i < run.n; i += stride) {
         const int p0 = run.tiles[run.i0 + i] * kTok;
-        // V of the tile too: what it says of its pages, and rows of it may have to be mended
-        ok = mbar_wait(&full_v[at.st], at.par, a.err) && mbar_wait(&s_done[wg], ph_s, a.err);
+        // V of the tile too: what it says of its pages, and rows of it may have to be mended. S first: it
+        // is issued behind P V of two steps before, so that V's stage is past its last use, which may have
+        // been the other group's (before, a phase could look over that has not begun).
+        static_assert(NV >= 2, "P V of two steps before");
+        ok = mbar_wait(&s_done[wg], ph_s, a.err) && mbar_wait(&full_v[at.st], at.par, a.err);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         ph_s ^= 1u;
@@ -624,7 +634,7 @@ __global__ void __launch_bounds__(TcShape<KV, D>::THREADS, 1) chunk_tc_kernel(
           after = get_run(unit + 1);
           if (after) {
             then = find_row(*after);
-            load_query(then);
+            load_query(*after, then);
           }
         }
         tmem_wait_ld();
@@ -778,7 +788,7 @@ __global__ void __launch_bounds__(TcShape<KV, D>::THREADS, 1) chunk_tc_kernel(
         after = get_run(unit + 1);
         if (after) {
           then = find_row(*after);
-          load_query(then);
+          load_query(*after, then);
         }
       }
       if (after) store_query(*after);
