@@ -874,7 +874,8 @@ size_t pkv_chunk_weights_workspace_size(int32_t dtype_q, int32_t num_rows, int32
  *   weights_out[b][j][p] = add_to[b][j][p] + sum e^{s - lse[row][h]}
  * over the counted rows and the query heads h of KV head j that see p, with s as in
  * pkv_chunk_attention and the lse it left. Counted are a request's last last_rows rows (0: all).
- * Rows whose lse is -infinity give nothing.
+ * Rows whose lse is -infinity give nothing. (Rows of q that belong to another request or to none may
+ * be read here; what they hold takes no part.)
  *  add_to       device fp32 [batch][num_kv_heads][width] or NULL (zeros).
  *  weights_out  device fp32 [batch][num_kv_heads][width]; may be add_to. Columns p < context_lens[b]
  *               are written, the others left as they were.

@@ -21,6 +21,10 @@ struct ChunkSplit {
   bool tc;
 };
 
+// The tensor cores' constants were measured in graphs (64 biased decode steps; an 8191-token prompt; a
+// window): 132, 431 and 244 us; with a unit's cost of 1 tile 134, 472, 254, of 6 138, 439, 245; with wide
+// tiles (more than 128 rows) of weight 2 against a narrow one's 2 132, 435, 246, of 4 132, 440, 251; least
+// tiles of 1 or 4 make no difference there.
 // bf16 queries run on the tensor cores, fp32 queries (whose weights keep 24 bits) on CUDA cores.
 ChunkSplit chunk_split(int dtype_q, int kv, int head_dim) {
   if (dtype_q == PKV_BF16)
@@ -288,18 +292,21 @@ int pkv_chunk_weights(const void* q, int32_t dtype_q, int32_t num_rows, int32_t 
   if (!weights_out || (num_rows > 0 && !lse)) return set_error(PKV_EINVAL, "%s: null pointer", who);
   if (width >= (1ll << 31) - 256)
     return set_error(PKV_ESHAPE, "%s: a row of sums holds 2^31 positions or more", who);
-  // few rows a request on the mean: K is read once, straight into registers (the choice is made on what
-  // the host knows; both kernels take any rows). Measured, 64 requests of 512 .. 4096 FP8 tokens, 4 rows a
-  // KV head: XXX us against YYY; 8 prompts' last 128 rows: ZZZ against WWW.
+  // Few rows a request on the mean: K is read once, straight into registers (the choice is made on what
+  // the host knows; both kernels take any rows), by passes of 8 rows or 32. Measured, us, 64 requests of
+  // 512 .. 4096 tokens, 8 KV heads, at 4 / 8 / 16 / 32 / 64 rows of each:
+  //   FP8,  passes of 8: 37 / 37 / 67 / 128 / 247, of 32: 91 / 92 / 92 / 95 / 191, tcgen05: 135 (64: 139)
+  //   bf16, passes of 8: 52 / 53 / 97 / 183 / 357, of 32: 103 / 104 / 105 / 107 / 209, tcgen05: 72
+  // and for 8 requests at 16 / 32 rows: FP8 15 / 24, 24 / 25, 22 / 22; bf16 15 / 26, 24 / 26, 16 / 15.
   const long long counted = last_rows > 0 ? std::min<long long>((long long)last_rows * batch, num_rows)
                                           : num_rows;
   const long long mean = (counted * a.group + batch - 1) / batch;
-  if (dtype_q == PKV_BF16 && mean <= kWeighFewRows) {
-    const int blocks = mean <= 8 ? 1 : 4;
-    const WeighSplit few{8 * blocks, kPageSize, weigh_few_wave(blocks), false};
-    const long long work = weigh_most_work(few, num_rows, batch, a.h_q, a.h_kv, width);
-    if (work >= (1ll << 30))
-      return set_error(PKV_ESHAPE, "%s: rows and width can hold 2^30 steps of work or more", who);
+  const bool codes = kv == PKV_FP8_E4M3 || kv == PKV_INT8;
+  const int blocks = mean <= 16 ? 1 : 4;
+  const WeighSplit few{8 * blocks, kPageSize, weigh_few_wave(blocks), false};
+  const long long work = weigh_most_work(few, num_rows, batch, a.h_q, a.h_kv, width);
+  if (dtype_q == PKV_BF16 && mean <= (codes ? kWeighFewRowsCodes : kWeighFewRows) &&
+      work < (1ll << 30)) {
     set_tile(a, few.rows, few.tokens);
     a.ctas = (int)std::max(1ll, std::min<long long>(few.wave, work / 4 + 1));
     a.lse = const_cast<float*>(lse);

@@ -7,8 +7,8 @@
 // (m16n8k16: 16 positions x 8 rows) would have it take 2 and 2 of distant ones, and the queries are
 // taken in the same order. A warp has a page (16 positions) and the next one in registers, no shared
 // memory, no barriers, and 12 to 16 warps on an SM keep 50 to 100 KB of reads under way (through the
-// rings of the tcgen05 kernel the same call took 141 us instead of XXX: a step of 4 rows there costs as
-// much as one of 128).
+// rings of the tcgen05 kernel the same call, 64 requests of 512 .. 4096 FP8 tokens and 8 KV heads, takes
+// 135 us instead of 37, or 4.8 TB/s: a step of 4 rows there costs as much as one of 128).
 //
 // The pages of all requests and KV heads, in order, form one stream, and each warp takes an equal
 // contiguous share of it, whole pages: no sum is made in parts, so equal inputs give equal results.
@@ -283,7 +283,8 @@ cudaError_t go(const ChunkArgs& a, cudaStream_t s) {
 
 template <int D, int NB>
 cudaError_t types(const ChunkArgs& a, int kv_dtype, cudaStream_t s) {
-  if (kv_dtype == PKV_BF16) return go<BF16, D, NB>(a, s);
+  if constexpr (NB == 1)
+    if (kv_dtype == PKV_BF16) return go<BF16, D, NB>(a, s);
   if (kv_dtype == PKV_FP8_E4M3) return go<FP8, D, NB>(a, s);
   return go<INT8, D, NB>(a, s);
 }
@@ -292,7 +293,7 @@ cudaError_t types(const ChunkArgs& a, int kv_dtype, cudaStream_t s) {
 
 cudaError_t launch_chunk_weights_few(const ChunkArgs& a, int kv_dtype, int head_dim, int blocks,
                                      cudaStream_t s) {
-  if (blocks == 1)
+  if (blocks == 1 || kv_dtype == PKV_BF16)
     return head_dim == 64 ? types<64, 1>(a, kv_dtype, s) : types<128, 1>(a, kv_dtype, s);
   return head_dim == 64 ? types<64, 4>(a, kv_dtype, s) : types<128, 4>(a, kv_dtype, s);
 }

@@ -17,8 +17,13 @@
 //  * one MMA warp; four groups of four warps that add up weights: group 2 q + h takes half h of the item
 //    in every second step, reading S^T from its own 128 columns of tensor memory, 32 at a time.
 //
-// 4095 prompt rows over themselves, 32 query heads on 8, bf16: 75 us, 69 GFLOP and half as many exponentials
-// as score columns: 0.92 PFLOP/s. The rings and MMAs alone, without the sums, take 62.
+// 4095 prompt rows over themselves, 32 query heads on 8, bf16: 78 us for 69 GFLOP, 0.88 PFLOP/s (the rings
+// and MMAs alone, without the sums, took 62).
+//
+// A wait for a phase by its parity means something only to a warp that has seen the phase before end. So
+// every warp of the sums waits for both halves' K, though it needs one; the rows' numbers have a ring for even
+// and one for odd steps; and each warp gives a run's place back (items without rows take no place in any
+// ring, so nothing else would keep the copy warp from lapping a slow reader).
 //
 // A step's weights are summed in eight chains of 16 and join the position's sum by a compensated addition
 // (Kahan's), so that sums over thousands of rows are good to fp32. Every wait is bounded

@@ -9,7 +9,8 @@
 // order. A row of sums belongs to a cluster of up to 8 blocks, each with a contiguous slice that it reads
 // from memory once and keeps in shared memory as integers (slices too long for that are read again);
 // the blocks' counts are added up, and their places found, through distributed shared memory. (One
-// block a row that read it five times: 168 us with the copy for 8 rows of 65536, now XXX.)
+// block a row that read it five times: 168 us with the copy for 8 rows of 65536, now 33, of which the
+// choice is 20.)
 #include <cooperative_groups.h>
 
 #include <atomic>

@@ -284,8 +284,9 @@ cudaError_t launch_chunk_weights_simt(const ChunkArgs& a, int kv_dtype, int head
                                       cudaStream_t s);
 cudaError_t launch_chunk_weights_tc(const ChunkArgs& a, int kv_dtype, int head_dim, const void* tk,
                                     const void* tq, cudaStream_t s);
-// Few rows a request (bf16 queries): a warp a page at a time, `blocks` (1 or 4) blocks of 8 rows a pass.
-constexpr int kWeighFewRows = 32;
+// Few rows a request (bf16 queries): a warp a page at a time, `blocks` blocks of 8 rows a pass (1, for 8-bit
+// caches also 4). The rows of a KV head up to which a call takes it, on the mean: bf16 and 8-bit caches.
+constexpr int kWeighFewRows = 8, kWeighFewRowsCodes = 32;
 constexpr int weigh_few_wave(int blocks) { return 152 * (blocks == 1 ? 4 : 3); }
 cudaError_t launch_chunk_weights_few(const ChunkArgs& a, int kv_dtype, int head_dim, int blocks,
                                      cudaStream_t s);

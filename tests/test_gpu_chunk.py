@@ -438,6 +438,59 @@ def test_equal_calls_give_equal_bits_on_any_stream_and_in_a_graph():
         assert torch.equal(static, out) and torch.equal(sums, w)
 
 
+@pytest.mark.parametrize("cache,d", [("bf16", 128), ("bf16", 64), ("fp8", 128)])
+@pytest.mark.parametrize("value", [math.nan, math.inf])
+def test_query_rows_of_others_take_no_part(cache, d, value):
+    """Rows behind the last request, and a request's own, that are not finite: the others' results do not
+    change by a bit (steps of sums read whole boxes of rows)."""
+    c = Chunk([40, 300, 0, 1000], [20, 5, 33, 70], 8, 2, d, "bf16", cache, seed=4)
+    lse = torch.empty(c.q.shape[:2], device="cuda")
+    out = c.attend(lse=lse)
+    w = c.weigh(lse)
+    c.q[c.rows:] = value
+    c.q[20:25] = value  # request 1
+    lse2 = torch.empty_like(lse)
+    out2 = c.attend(lse=lse2)
+    keep = [i for i in range(c.rows) if not 20 <= i < 25]
+    assert torch.equal(out2[keep], out[keep]) and torch.equal(lse2[keep], lse[keep])
+    w2 = c.weigh(lse2)
+    assert torch.equal(w2[[0, 2, 3]], w[[0, 2, 3]])
+    assert pkv.device_error() == 0
+
+
+def test_two_calls_at_once_on_two_streams():
+    calls = []
+    for seed, cache, d in ((1, "bf16", 128), (2, "fp8", 64)):
+        c = Chunk([100, 900, 0, 33], [300, 1, 200, 40], 8, 2, d, "bf16", cache, seed=seed)
+        B, P = len(c.new), c.bt.shape[1]
+        ws = [torch.empty(1 << 26, dtype=torch.uint8, device="cuda") for _ in range(2)]
+        lse = torch.empty(c.q.shape[:2], device="cuda")
+        out = torch.zeros_like(c.q)
+        w = torch.zeros(B, 2, P * 16, device="cuda")
+
+        def call(c=c, ws=ws, lse=lse, out=out, w=w):
+            c.attend(out=out, lse=lse, workspace=ws[0])
+            c.weigh(lse, out=w, workspace=ws[1])
+        call()
+        calls.append((call, out, lse, w, out.clone(), lse.clone(), w.clone()))
+    streams = [torch.cuda.Stream() for _ in calls]
+    torch.cuda.synchronize()
+    for call, out, lse, w, *_ in calls:
+        for x in (out, lse, w):
+            x.zero_()
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for st, (call, *_) in zip(streams, calls):
+            with torch.cuda.stream(st):
+                call()
+    torch.cuda.synchronize()
+    for _, out, lse, w, *want in calls:
+        n = sum((300, 1, 200, 40))
+        assert torch.equal(out[:n], want[0][:n]) and torch.equal(lse[:n], want[1][:n])
+        assert torch.equal(w, want[2])
+    assert pkv.device_error() == 0
+
+
 def test_empty_calls():
     q = torch.empty(0, 4, 64, dtype=torch.bfloat16, device="cuda")
     pool = torch.zeros(2, 2, 16, 64, dtype=torch.bfloat16, device="cuda")
