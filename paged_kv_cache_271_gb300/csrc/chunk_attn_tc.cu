@@ -644,8 +644,24 @@ __global__ void __launch_bounds__(TcShape<KV, D>::THREADS, 1) chunk_tc_kernel(
           }
         }
         tmem_wait_ld();
+        const bool edge = p0 > edge_from || (p0 < edge_win && p0 + kTok > a.sink);
+        // which of its positions this thread's row sees, in tiles where that need not be all
+        const bool part = edge || mask != (1 << kPages) - 1;
+        uint64_t seen = ~0ull;
+        if (part) {
+          seen = live ? chunk_seen(a, me.pq, p0 + 64 * h) : 0ull;
+#pragma unroll
+          for (int p = 0; p < 4; ++p)
+            if (!((mask >> (4 * h + p)) & 1)) seen &= ~(0xffffull << (16 * p));
+        }
         if constexpr (FORM) {  // the scores themselves, log2 domain
           if (a.softcap > 0.f) {
+            // (what is not seen may be whatever memory held, and has no say in how the cap is taken)
+            if (part) {
+#pragma unroll
+              for (int k = 0; k < 64; ++k)
+                if (!((seen >> k) & 1)) sr[k] = 0u;
+            }
             cap_scores<64>(sr, sc * (kLn2 / a.softcap), a.softcap * kLog2e);
           } else {
             const uint64_t sc2 = pack2(sc, sc);
@@ -660,12 +676,7 @@ __global__ void __launch_bounds__(TcShape<KV, D>::THREADS, 1) chunk_tc_kernel(
               put2(&sr[k], fma2(slope2, add2(far2, pack2((float)k, (float)(k + 1))), get2(&sr[k])));
           }
         }
-        const bool edge = p0 > edge_from || (p0 < edge_win && p0 + kTok > a.sink);
-        if (edge || mask != (1 << kPages) - 1) {
-          uint64_t seen = live ? chunk_seen(a, me.pq, p0 + 64 * h) : 0ull;
-#pragma unroll
-          for (int p = 0; p < 4; ++p)
-            if (!((mask >> (4 * h + p)) & 1)) seen &= ~(0xffffull << (16 * p));
+        if (part) {
 #pragma unroll
           for (int k = 0; k < 64; ++k)
             if (!((seen >> k) & 1)) sr[k] = __float_as_uint(-INFINITY);

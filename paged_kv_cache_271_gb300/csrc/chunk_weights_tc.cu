@@ -604,7 +604,8 @@ __global__ void __launch_bounds__(WeighTcShape<KV, D>::THREADS, 1) weights_tc_ke
       // lies behind the request's, or zeros.)
       const unsigned rows = (unsigned)(run->rows - run->s0 * kStep);
       const long long first = (long long)(p - run->req.base - run->t0) * a.group - (long long)run->s0 * kStep;
-      const unsigned from = (unsigned)max(0ll, min((long long)INT_MAX, first));
+      // (a page that is not there is seen by none)
+      const unsigned from = good ? (unsigned)max(0ll, min((long long)INT_MAX, first)) : INT_MAX;
       const unsigned end = a.window > 0 && p >= a.sink
                                ? (unsigned)max(0ll, min((long long)rows, first + (long long)a.window * a.group))
                                : rows;
@@ -642,6 +643,15 @@ __global__ void __launch_bounds__(WeighTcShape<KV, D>::THREADS, 1) weights_tc_ke
               }
               // (columns that see no position of the warp are left out)
               if (decltype(edge)::value && (u0 + c + 32 <= from_any || u0 + c >= end_any)) continue;
+              const int f0 = (int)(from - (u0 + c)), e0 = (int)(end - (u0 + c));
+              if constexpr (FORM && decltype(edge)::value) {
+                // (what is not seen may be whatever memory held, and has no say in how the cap is taken)
+                if (cap) {
+#pragma unroll
+                  for (int k = 0; k < 32; ++k)
+                    if (k < f0 || k >= e0) s[k] = 0u;
+                }
+              }
               if constexpr (FORM) {
                 if (W8 || !cap) {
 #pragma unroll
@@ -657,7 +667,6 @@ __global__ void __launch_bounds__(WeighTcShape<KV, D>::THREADS, 1) weights_tc_ke
                 }
               }
               if constexpr (decltype(edge)::value) {
-                const int f0 = (int)(from - (u0 + c)), e0 = (int)(end - (u0 + c));
 #pragma unroll
                 for (int k = 0; k < 32; ++k)
                   if (k < f0 || k >= e0) s[k] = __float_as_uint(-INFINITY);

@@ -438,6 +438,26 @@ def test_equal_calls_give_equal_bits_on_any_stream_and_in_a_graph():
         assert torch.equal(static, out) and torch.equal(sums, w)
 
 
+@pytest.mark.parametrize("cache,d", [("bf16", 128), ("bf16", 64), ("int8", 128)])
+@pytest.mark.parametrize("form", [dict(window=1, sinks=4), dict(window=300, sinks=20), dict()])
+def test_capped_scores_do_not_depend_on_what_is_not_seen(cache, d, form):
+    """Pages that no row sees are not read: what memory held before has no say in the cap's rounding."""
+    c = Chunk([4220, 1100, 2700], [130, 170, 5], 16, 1, d, "bf16", cache, seed=6, softcap=20.0, **form)
+    lse = torch.empty(c.q.shape[:2], device="cuda")
+    out = c.attend(lse=lse)
+    c.check(out, lse)
+    w = c.weigh(lse)
+    other = Chunk([3000, 900, 2000], [130, 170, 40], 16, 1, d, "bf16", cache, seed=7)
+    for i in range(12):
+        other.q.mul_(3.0 if i % 2 else 1 / 3.0)
+        other.attend()  # (leaves other rows in shared memory)
+        lse2 = torch.empty_like(lse)
+        out2 = c.attend(lse=lse2)
+        assert torch.equal(out2[:c.rows], out[:c.rows]) and torch.equal(lse2[:c.rows], lse[:c.rows])
+        assert torch.equal(c.weigh(lse2), w)
+    assert pkv.device_error() == 0
+
+
 @pytest.mark.parametrize("cache,d", [("bf16", 128), ("bf16", 64), ("fp8", 128)])
 @pytest.mark.parametrize("value", [math.nan, math.inf])
 def test_query_rows_of_others_take_no_part(cache, d, value):
