@@ -647,20 +647,24 @@ __global__ void __launch_bounds__(TcShape<KV, D>::THREADS, 1) chunk_tc_kernel(
         const bool edge = p0 > edge_from || (p0 < edge_win && p0 + kTok > a.sink);
         // which of its positions this thread's row sees, in tiles where that need not be all
         const bool part = edge || mask != (1 << kPages) - 1;
-        uint64_t seen = ~0ull;
-        if (part) {
-          seen = live ? chunk_seen(a, me.pq, p0 + 64 * h) : 0ull;
+        auto seen_now = [&] {
+          uint64_t seen = live ? chunk_seen(a, me.pq, p0 + 64 * h) : 0ull;
 #pragma unroll
           for (int p = 0; p < 4; ++p)
             if (!((mask >> (4 * h + p)) & 1)) seen &= ~(0xffffull << (16 * p));
-        }
+          return seen;
+        };
         if constexpr (FORM) {  // the scores themselves, log2 domain
           if (a.softcap > 0.f) {
             // (what is not seen may be whatever memory held, and has no say in how the cap is taken)
-            if (part) {
+            if (part) {  // (bits made twice, kept they cost registers in every tile: INT8 mix 930 us, not 866)
+              const uint64_t seen = seen_now();
+              const uint32_t lo = (uint32_t)seen, hi = (uint32_t)(seen >> 32);
 #pragma unroll
-              for (int k = 0; k < 64; ++k)
-                if (!((seen >> k) & 1)) sr[k] = 0u;
+              for (int k = 0; k < 32; ++k) {
+                sr[k] &= 0u - ((lo >> k) & 1u);
+                sr[32 + k] &= 0u - ((hi >> k) & 1u);
+              }
             }
             cap_scores<64>(sr, sc * (kLn2 / a.softcap), a.softcap * kLog2e);
           } else {
@@ -677,6 +681,7 @@ __global__ void __launch_bounds__(TcShape<KV, D>::THREADS, 1) chunk_tc_kernel(
           }
         }
         if (part) {
+          const uint64_t seen = seen_now();
 #pragma unroll
           for (int k = 0; k < 64; ++k)
             if (!((seen >> k) & 1)) sr[k] = __float_as_uint(-INFINITY);
