@@ -521,7 +521,7 @@ __global__ void __launch_bounds__(TcShape<KV, D>::THREADS, 1) chunk_tc_kernel(
       *mine = x;
       __syncwarp();
       if (lane == 0) mbar_arrive(pair);
-      ok = mbar_wait(pair, ph_pair, a.err);
+      ok = mbar_wait(pair, ph_pair, a.err) && ok;
       ok = __all_sync(0xffffffffu, ok);
       ph_pair ^= 1u;
       return *theirs;
@@ -826,6 +826,8 @@ __global__ void __launch_bounds__(TcShape<KV, D>::THREADS, 1) chunk_tc_kernel(
       if (wide) {
         const float x = exchange(l);
         L = h == 0 ? l + x : x + l;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(pair);  // (read: waited for below)
       } else {
         *mine = l;
         if (h == 0) row_max[wg * kGroupRows + r] = m_used;
@@ -948,7 +950,11 @@ __global__ void __launch_bounds__(TcShape<KV, D>::THREADS, 1) chunk_tc_kernel(
           }
         }
       }
-      if (!wide) {  // the other group reads this one's O and sums
+      if (wide) {  // the other warp has read this one's sums
+        ok = mbar_wait(pair, ph_pair, a.err) && ok;
+        ok = __all_sync(0xffffffffu, ok);
+        ph_pair ^= 1u;
+      } else {  // the other group reads this one's O and sums
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(parted);
