@@ -82,7 +82,8 @@ __global__ void __launch_bounds__(kThreads) weights_simt_kernel(const ChunkArgs 
       }
       if (bad && threadIdx.x == 0) atomicOr(a.err, PKV_DEVERR_BAD_PAGE);
     }
-    const ScoreForm form(a, KV::bytes == 1 ? a.k_scales[j] : 1.f);
+    // (a call without rows, which carries the sums over, may come without scales)
+    const ScoreForm form(a, KV::bytes == 1 && rows > 0 ? a.k_scales[j] : 1.f);
     float total[4] = {0.f, 0.f, 0.f, 0.f}, lost[4] = {0.f, 0.f, 0.f, 0.f};
     for (int r0 = it.s0 * kRows; r0 < min(rows, (it.s0 + it.n) * kRows); r0 += kRows) {
       __syncthreads();  // the last rows are used up

@@ -530,6 +530,30 @@ def test_empty_calls():
     assert torch.equal(new, add) and new.data_ptr() != add.data_ptr()
 
 
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("cache", ["fp8", "int8"])
+def test_sums_without_rows_are_carried_over_without_scales(io, cache):
+    """num_rows = 0: neither queries nor lse nor scales are needed, in the C call (the contexts are there)."""
+    d, h_kv, width = 64, 2, 300
+    pool = torch.zeros(3, h_kv, 16, d, dtype=torch.uint8, device="cuda")
+    desc = pkv._Desc(3, 16, h_kv, d, pkv.FP8_E4M3 if cache == "fp8" else pkv.INT8)
+    cl = torch.tensor([300, 0, 70], dtype=torch.int32, device="cuda")
+    qs = torch.zeros(4, dtype=torch.int32, device="cuda")
+    add = torch.rand(3, h_kv, width, device="cuda")
+    out = torch.full_like(add, 7.0)
+    code = pkv.F32 if io == "f32" else pkv.BF16
+    need = pkv.chunk_weights_workspace_size(code, 0, 3, 4, h_kv, d, width)
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+    form = pkv._ScoreForm(0.1, 0.0, None, 0, 0)
+    st = pkv.lib().pkv_chunk_weights(
+        None, code, 0, 3, 4, pool.data_ptr(), desc, None, 1, cl.data_ptr(), qs.data_ptr(), form, None,
+        None, 0, add.data_ptr(), out.data_ptr(), width, ws.data_ptr(), need,
+        torch.cuda.current_stream().cuda_stream)
+    assert st == 0 and pkv.device_error() == 0
+    for b, n in enumerate((300, 0, 70)):
+        assert torch.equal(out[b, :, :n], add[b, :, :n]) and (out[b, :, n:] == 7).all()
+
+
 # ---- eviction ----------------------------------------------------------------------------------
 
 
