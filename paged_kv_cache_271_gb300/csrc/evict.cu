@@ -47,7 +47,7 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const Evic
       __syncthreads();
   };
   const int j = blockIdx.y, b = blockIdx.z, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  __shared__ int count[kDigits];                 // this block's candidates by digit
+  __shared__ __align__(16) int count[kDigits];   // this block's candidates by digit
   __shared__ int above[kSelectWarps], same[kSelectWarps];
   __shared__ int block_above, block_same, found_digit, found_above, found_count;
   __shared__ uint32_t keys[kSliceKeys];
@@ -94,8 +94,7 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const Evic
 #pragma unroll
         for (int r = 0; r < kMostParts; ++r) {  // (unrolled: the reads are under way together)
           if (r >= parts) break;
-          const int* theirs = cluster.map_shared_rank(count, r);
-          const int4 v = *reinterpret_cast<const int4*>(theirs + top - 3);
+          const int4 v = *reinterpret_cast<const int4*>(cluster.map_shared_rank(count, r) + top - 3);
           c[0] += v.w; c[1] += v.z; c[2] += v.y; c[3] += v.x;
         }
         mine = c[0] + c[1] + c[2] + c[3];

@@ -121,3 +121,23 @@ def test_workspace_sizes():
     w = pkv.chunk_weights_workspace_size
     assert w(BF16, 5, 0, 8, 2, 128, 100) == 0
     assert 0 < w(BF16, 0, 1, 8, 2, 128, 100) <= w(BF16, 4096, 4, 8, 2, 128, 8192)
+
+
+def test_shared_arrays_read_in_wider_words_say_their_alignment():
+    """A shared array of scalars is aligned to its element; where a kernel reads it in words of 16 bytes, its
+    declaration has to ask for them (the order of a block's variables is the compiler's)."""
+    import glob
+    import os
+    import re
+    wide = r"reinterpret_cast<(?:const )?(?:u?int4|float4|ulonglong2)\s*\*>\(([^;]*?)\)"
+    looked = 0
+    for path in glob.glob(os.path.join(os.path.dirname(pkv.__file__), "csrc", "*.cu*")):
+        text = open(path).read()
+        for line in re.findall(r"^\s*(?:static )?__shared__ [^;]*;", text, re.M):
+            kind = re.match(r"\s*__shared__\s+(__align__\(16\)|alignas\(16\))?\s*(\w+)\s+(\w+)\[", line)
+            if not kind or kind[2] not in ("int", "float", "uint32_t", "uint8_t", "int32_t"):
+                continue
+            reads = [r for r in re.findall(wide, text) if re.search(r"\b%s\b" % kind[3], r)]
+            looked += len(reads)
+            assert kind[1] or not reads, (os.path.basename(path), line.strip(), reads)
+    assert looked >= 1
