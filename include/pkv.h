@@ -846,7 +846,8 @@ size_t pkv_chunk_workspace_size(int32_t dtype_q, int32_t cache_dtype, int32_t nu
  *  query_starts device int32 [batch + 1], not falling, within 0 .. num_rows. Rows of q that belong to
  *               no request are not read, those of out and lse are left as they were.
  * A request whose rows are not in 0 .. num_rows or that has fewer positions than rows is left out and
- * flagged with PKV_DEVERR_BAD_CHUNK, one that is longer than its table row with PKV_DEVERR_BAD_PAGE;
+ * flagged with PKV_DEVERR_BAD_CHUNK (where starts fall so that requests have more than num_rows rows in
+ * all, every request is left out), one that is longer than its table row with PKV_DEVERR_BAD_PAGE;
  * a page id outside the pool is skipped and flagged with PKV_DEVERR_BAD_PAGE.
  *  workspace    device, >= pkv_chunk_workspace_size(...) bytes, 16-byte aligned.
  * Requires num_q_heads % num_kv_heads == 0 and at most PKV_MAX_CHUNK_GROUP query heads per KV head.

@@ -49,6 +49,17 @@ __device__ __forceinline__ ChunkReq chunk_request(const ChunkArgs& a, int b) {
   return r;
 }
 
+// Whether the accepted requests have more rows in all than the call: starts that fall somewhere can give a
+// row to several of them. The plan's sums are bounded (by the host) for num_rows rows, so such a call's
+// requests are all left out. Every thread of the block calls it, `falls` if a start that it looked at may
+// fall (that request is flagged); a barrier.
+__device__ __forceinline__ bool chunk_rows_overlap(const ChunkArgs& a, bool falls) {
+  if (!__syncthreads_or(falls)) return false;
+  long long rows = 0;
+  for (int b = 0; b < a.batch; ++b) rows += chunk_request(a, b).n;
+  return rows > a.num_rows;
+}
+
 // Tiles that hold the first n positions (their size is a power of two).
 __device__ __forceinline__ int tiles_for(const ChunkArgs& a, int n) {
   return (int)((unsigned)n + a.tile_tokens - 1 >> a.tile_shift);
@@ -192,6 +203,7 @@ __device__ __forceinline__ void chunk_share(const ChunkArgs& a, int* scratch, Ch
   }
   if (err && blockIdx.x == 0) atomicOr(a.err, err);
   if (threadIdx.x == 0) out->count = 0;
+  if (chunk_rows_overlap(a, err & PKV_DEVERR_BAD_CHUNK)) return;  // (behind a barrier)
   int work_below, work_all, passes_below, passes_all;
   block_scan2<THREADS>(work, passes, scratch, work_below, work_all, passes_below, passes_all);
   const int cost = work_all >= 32 * a.ctas ? 2 * a.pass_cost : 0;

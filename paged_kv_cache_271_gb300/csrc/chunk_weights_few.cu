@@ -84,6 +84,7 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? 4 : 3) weights_few_kernel(
     }
     if (err && blockIdx.x == 0) atomicOr(a.err, err);
     if (threadIdx.x < kWarps) shares[threadIdx.x].left = 0;
+    if (chunk_rows_overlap(a, err & PKV_DEVERR_BAD_CHUNK)) return;
     int below, total;
     block_scan<kThreads>(mine, scratch, below, total);
     const int warps = a.ctas * kWarps;

@@ -112,6 +112,7 @@ __device__ __forceinline__ void weigh_share(const ChunkArgs& a, int* scratch, We
   }
   if (err && blockIdx.x == 0) atomicOr(a.err, err);
   if (threadIdx.x == 0) out->count = 0;
+  if (chunk_rows_overlap(a, err & PKV_DEVERR_BAD_CHUNK)) return;  // (behind a barrier)
   int below, total;
   block_scan<THREADS>(mine, scratch, below, total);
   const int share = max(2, (int)(((unsigned)total + a.ctas - 1) / (unsigned)a.ctas));

@@ -374,6 +374,28 @@ def test_bad_requests_are_left_out_and_flagged():
                     assert (w[b, :, c.ctx[b]:] == 2).all()
 
 
+@pytest.mark.parametrize("io,cache,new", [("bf16", "bf16", 20), ("bf16", "fp8", 20), ("bf16", "fp8", 2),
+                                          ("f32", "f32", 20)])
+def test_rows_given_to_several_requests_leave_every_request_out(io, cache, new):
+    """Starts that rise and fall: the work that the plan counts is bounded for rows that belong to one request
+    each. A fall that gives no row twice leaves out its own request alone."""
+    n = 40
+    c = Chunk([900] * n, [new] * n, 4, 2, 64, io, cache)  # (a request could hold all rows)
+    lse = torch.empty(c.q.shape[:2], device="cuda")
+    c.attend(lse=lse)
+    sums = c.weigh(lse)
+    for last, every in ((c.rows, True), (new, False)):
+        c.qs = torch.tensor([0, last] * (n // 2) + [0], dtype=torch.int32, device="cuda")
+        assert (last * (n // 2) > c.q.shape[0]) == every
+        out, w = torch.full_like(c.q, 2.0), torch.full_like(sums, 2.0)
+        c.attend(out=out)
+        assert pkv.device_error() == pkv.DEVERR_BAD_CHUNK
+        c.weigh(lse, out=w)
+        assert pkv.device_error() == pkv.DEVERR_BAD_CHUNK
+        assert (out[new:] == 2).all() and (w[1::2] == 2).all()
+        assert (out[:new] == 2).all() == every and (w[::2, :, :900] == 2).all() == every
+
+
 def test_released_pages_outside_the_window_are_not_read():
     for io, cache in (("bf16", "bf16"), ("bf16", "fp8"), ("f32", "f32")):
         c = Chunk([700], [50], 4, 2, 128, io, cache, window=100, sinks=20)
