@@ -86,9 +86,11 @@ struct WeighTcShape {
   static_assert(SMEM <= 224 * 1024 && SMEM > 114 * 1024, "one CTA per SM");
 };
 
+constexpr float kNanLse = 0x1p127f;  // stands for minus a NaN lse: an infinite weight wherever seen
+
 // A step's rows' numbers in shared memory.
 struct Columns {
-  const float* neg_lse;  // log2 domain; -inf where there is no row, or its lse is -inf
+  const float* neg_lse;  // log2 domain; -inf where there is no row, or its lse is -inf; kNanLse
   const float* factor;   // scores (log2 domain) are factor times the product (8-bit caches: a row's own)
   const float* slope;    // log2 domain
   const int* pos;        // the row's position
@@ -137,6 +139,9 @@ __global__ void __launch_bounds__(WeighTcShape<KV, D>::THREADS, 1) weights_tc_ke
   __shared__ int scratch[32];
   __shared__ WeighShare share;
   __shared__ WeighRun runs[kRuns];  // (n = 0: the share's end)
+  __shared__ uint32_t no_lse[kCols][4];  // of a step's rows, bits: its lse is -inf
+  // whether there is one among 32 rows; one whose lse is NaN
+  __shared__ __align__(4) uint8_t some_none[kCols][4], some_nan[kCols][4];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (threadIdx.x == kCopyWarp * 32) {
     for (int s = 0; s < NK; ++s) {
@@ -398,7 +403,7 @@ __global__ void __launch_bounds__(WeighTcShape<KV, D>::THREADS, 1) weights_tc_ke
       const bool live = R < (unsigned)run.rows;
       const unsigned t = live ? R / (unsigned)a.group : 0, g = live ? R - t * a.group : 0;
       const size_t at = (size_t)(run.req.q0 + run.t0 + (int)t) * a.h_q + run.j * a.group + g;
-      x.lse = live ? a.lse[at] : -INFINITY;
+      x.lse = live ? a.lse[at] : INFINITY;  // (gives nothing)
       x.slope = FORM && a.slopes ? a.slopes[run.j * a.group + g] : 0.f;
       x.k_scale = W8 ? a.k_scales[run.j] : 1.f;
       x.pos = run.req.base + run.t0 + (int)t;
@@ -441,7 +446,17 @@ __global__ void __launch_bounds__(WeighTcShape<KV, D>::THREADS, 1) weights_tc_ke
       if (!ok) return;
       const float sc = a.scale * kLog2e * x.k_scale;
       float* const p = reinterpret_cast<float*>(col) + cs * 4 * kStep;
-      p[r] = x.lse == -INFINITY ? -INFINITY : -x.lse * kLog2e;  // (a row that saw nothing gives nothing)
+      // A row that saw nothing gives nothing: -inf. One whose lse is NaN gives an infinite weight to what
+      // it sees, which the sums then call NaN (NaN itself would also reach what it does not see: those
+      // scores are -inf).
+      p[r] = x.lse != x.lse ? kNanLse : x.lse == -INFINITY ? -INFINITY : -x.lse * kLog2e;
+      const uint32_t none = __ballot_sync(0xffffffffu, x.lse == -INFINITY);
+      const bool nan = __any_sync(0xffffffffu, x.lse != x.lse);
+      if (lane == 0) {
+        no_lse[cs][w] = none;
+        some_none[cs][w] = none != 0;
+        some_nan[cs][w] = nan;
+      }
       if constexpr (FORM) p[2 * kStep + r] = x.slope * kLog2e;
       reinterpret_cast<int*>(p)[3 * kStep + r] = x.pos;
       if constexpr (W8) {
@@ -617,6 +632,7 @@ __global__ void __launch_bounds__(WeighTcShape<KV, D>::THREADS, 1) weights_tc_ke
       for (int u = q; ok && u < n; u += 2, cs.advance(1)) {
         const int at_c = 2 * q + cs.st;
         ok = mbar_wait(&full_c[at_c], cs.par, a.err);
+        const bool none = *reinterpret_cast<const uint32_t*>(some_none[at_c]) != 0;
         if (ok && h < halves) ok = mbar_wait(&s_done[group], ph_s, a.err);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
@@ -628,9 +644,10 @@ __global__ void __launch_bounds__(WeighTcShape<KV, D>::THREADS, 1) weights_tc_ke
           const Columns cn = columns(col, at_c);
           uint64_t sum[4] = {0, 0, 0, 0};
           const uint64_t sc2 = pack2(sc, sc);
-          // With the tests of what its positions see, or, where every row sees them all, without: in one
-          // body the tests cost more than the few steps that need them (4095 rows over themselves: 85 us
-          // instead of 75).
+          // With the tests of what its positions see, or, where every row sees them all and has an lse,
+          // without: in one body the tests cost more than the few steps that need them (4095 rows over
+          // themselves: 85 us instead of 75). What gives a position nothing has a score of -inf there,
+          // whatever its product is.
           auto step = [&](auto edge) {
 #pragma unroll 1
             for (int c = 0; c < cols; c += 32) {
@@ -644,13 +661,16 @@ __global__ void __launch_bounds__(WeighTcShape<KV, D>::THREADS, 1) weights_tc_ke
               }
               // (columns that see no position of the warp are left out)
               if (decltype(edge)::value && (u0 + c + 32 <= from_any || u0 + c >= end_any)) continue;
-              const int f0 = (int)(from - (u0 + c)), e0 = (int)(end - (u0 + c));
+              uint32_t gives = ~0u;  // the columns that give this position something
+              if constexpr (decltype(edge)::value)
+                gives = (uint32_t)(low_bits((int)(end - (u0 + c))) & ~low_bits((int)(from - (u0 + c)))) &
+                        ~no_lse[at_c][c >> 5];
               if constexpr (FORM && decltype(edge)::value) {
                 // (what is not seen may be whatever memory held, and has no say in how the cap is taken)
                 if (cap) {
 #pragma unroll
                   for (int k = 0; k < 32; ++k)
-                    if (k < f0 || k >= e0) s[k] = 0u;
+                    if (!((gives >> k) & 1)) s[k] = 0u;
                 }
               }
               if constexpr (FORM) {
@@ -670,7 +690,7 @@ __global__ void __launch_bounds__(WeighTcShape<KV, D>::THREADS, 1) weights_tc_ke
               if constexpr (decltype(edge)::value) {
 #pragma unroll
                 for (int k = 0; k < 32; ++k)
-                  if (k < f0 || k >= e0) s[k] = __float_as_uint(-INFINITY);
+                  if (!((gives >> k) & 1)) s[k] = __float_as_uint(-INFINITY);
               }
 #pragma unroll
               for (int k = 0; k < 32; k += 4) {
@@ -696,7 +716,7 @@ __global__ void __launch_bounds__(WeighTcShape<KV, D>::THREADS, 1) weights_tc_ke
               }
             }
           };
-          if (u0 < from_all || u0 + ((cols + 31) & ~31) > end_all)
+          if (none || u0 < from_all || u0 + ((cols + 31) & ~31) > end_all)
             step(std::true_type{});
           else
             step(std::false_type{});
@@ -705,6 +725,7 @@ __global__ void __launch_bounds__(WeighTcShape<KV, D>::THREADS, 1) weights_tc_ke
           const float add = (x + y) - lost, z = total + add;
           lost = (z - total) - add;
           total = z;
+          if (*reinterpret_cast<const uint32_t*>(some_nan[at_c]) != 0 && !(total < INFINITY)) total = NAN;
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&free_c[at_c]);

@@ -500,6 +500,42 @@ def test_query_rows_of_others_take_no_part(cache, d, value):
     assert pkv.device_error() == 0
 
 
+@pytest.mark.parametrize("io,cache,d", [("bf16", "bf16", 128), ("bf16", "bf16", 64), ("bf16", "fp8", 128),
+                                        ("bf16", "int8", 64), ("f32", "f32", 64), ("f32", "int8", 128)])
+@pytest.mark.parametrize("new", [[200, 90, 3], [1, 2, 2]], ids=["many", "few"])
+@pytest.mark.parametrize("form", [dict(), dict(softcap=10.0), dict(window=33, sinks=4, alibi=True)], ids=str)
+def test_sums_take_nothing_from_rows_that_saw_nothing_nor_for_what_is_not_seen(io, cache, d, new, form):
+    """A row whose lse is -infinity gives nothing, whatever its queries hold; one whose lse is NaN gives NaN
+    to the positions that it sees, and to no other."""
+    c = Chunk([40, 300, 700], new, 8, 2, d, io, cache, seed=12, **form)
+    lse = torch.empty(c.q.shape[:2], device="cuda")
+    c.attend(lse=lse)
+    none, nan = int(c.starts[1]) - 1, int(c.starts[2]) - 2  # the last row of request 0, one of request 1
+    dropped = lse.clone()
+    dropped[none], dropped[nan, 5] = -math.inf, -math.inf
+    ref, tol = c.sums(dropped)
+    assert ((c.weigh(dropped).double() - ref).abs() <= tol).all()
+    clean = c.q.clone()
+    for value in (math.nan, math.inf, -math.inf):
+        c.q.copy_(clean)
+        c.q[none] = value
+        assert ((c.weigh(dropped).double() - ref).abs() <= tol).all(), value
+    c.q[nan, 5] = math.nan
+    poison = dropped.clone()
+    poison[nan, 5] = math.nan
+    w = c.weigh(poison)
+    pos = torch.arange(w.shape[2], device="cuda")
+    at = c.ctx[1] - 2
+    seen = (pos <= at) & (pos < c.ctx[1])
+    if c.window:
+        seen &= (pos > at - c.window) | (pos < c.sinks)
+    assert torch.isnan(w[1, 1, seen]).all()
+    keep = torch.ones_like(w, dtype=torch.bool)
+    keep[1, 1, seen] = False
+    assert ((w.double() - ref).abs() <= tol)[keep].all()
+    assert pkv.device_error() == 0
+
+
 def test_two_calls_at_once_on_two_streams():
     calls = []
     for seed, cache, d in ((1, "bf16", 128), (2, "fp8", 64)):
