@@ -836,7 +836,8 @@ size_t pkv_chunk_workspace_size(int32_t dtype_q, int32_t cache_dtype, int32_t nu
  * with scores and seen positions as `form` says. A row that sees nothing (its pages are bad) gives 0
  * and -infinity. What is not seen takes no part, whatever it holds (NaN and infinities too). Scores,
  * maxima and sums are fp32; with BF16 queries the weights are rounded to the cache's matrix type (bf16
- * for a BF16 cache, f16 for FP8 and INT8) before they meet V.
+ * for a BF16 cache, f16 for FP8 and INT8: all its bits from 2^-21 of a row's largest on, none below
+ * 2^-31) before they meet V.
  *  q, out       device [num_rows][num_q_heads][head_dim] of dtype_q, 16-byte aligned. F32 q takes
  *               an F32, FP8 or INT8 cache; BF16 q a BF16, FP8 or INT8 cache.
  *  lse          device fp32 [num_rows][num_q_heads] or NULL.

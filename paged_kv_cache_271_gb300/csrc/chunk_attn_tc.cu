@@ -16,11 +16,13 @@
 //    than 128 rows group g takes rows 128 g .. of every tile: while one group works on its scores, the
 //    tensor cores have the other's P V and next S. In a smaller unit both groups have the same rows and
 //    take alternate tiles, and the sums are merged at the unit's end;
-//  * O is rescaled only when a row's maximum grows by more than 2^8 (P <= 2^8 until then): the final
-//    (max, sum, O) is exact whatever maximum it was accumulated against.
+//  * O is rescaled only when a row's maximum grows by more than 2^8 (8-bit caches: 2^7): the final
+//    (max, sum, O) is exact whatever reference it was accumulated against.
 //
 // P is rounded to the MMA's input type (bf16 for a bf16 cache, f16 otherwise), the only rounding
-// before the output's; scores, maxima and sums are fp32. For 8-bit caches a query row is scaled by
+// before the output's; scores, maxima and sums are fp32. (Outputs' relative error against 64 bits, over a
+// bf16 cache: 0.0019 to 0.0022, where weights in 32 bits give 0.0017, the output's own rounding; over 8-bit
+// caches no more than that. The rest of P as a second operand would cost a fourth of a tile's MMAs.) For 8-bit caches a query row is scaled by
 // a power of two that puts its largest value in f16's top binade, undone in its score factor; the sign
 // of the K scale goes with it, so that score factors are positive.
 //
@@ -68,7 +70,16 @@ constexpr int kConvThreads = 128;
 // rows are being written, the one after it and the one it is about to copy.
 constexpr int kRuns = 16;
 constexpr uint32_t kTmemCols = 512;        // O of group g at 128 g, S (then P) at 256 + 128 g
-constexpr float kLazyLog2 = 8.f;
+// A row's weights are 2^(s - m) with m below the maximum that it was taken from by `lift`, and O is
+// rescaled when a later maximum passes m + lift by more than `lazy`. f16, the weights' type over an 8-bit
+// cache, ends at 2^16 and steps by 2^-24 below 2^-14: lifted by 2^7, weights of 2^-21 of the largest keep
+// all bits and ones of 2^-31 are not lost, while a long context's many small ones next to a sink still
+// add up (131,072 of 2^-24.6 gave 0.0078 in place of 0.0051 without). lift + lazy leaves room for what
+// rounding m adds (at most 2^1; where m is above 2^26, lift may round up to 8).
+template <bool F16>
+constexpr float kLiftLog2 = F16 ? 7.f : 0.f;
+template <bool F16>
+constexpr float kLazyLog2 = F16 ? 7.f : 8.f;
 // tiles of a unit in which some rows see a position that others do not: those that cross the sinks'
 // end, and those of the at most 256 positions from the first to the last row's end or window
 constexpr int kEdgeTiles = 8;
@@ -748,16 +759,16 @@ __global__ void __launch_bounds__(TcShape<KV, D>::THREADS, 1) chunk_tc_kernel(
         // larger m it would soon leave f16's range and then every range: there s sc is rounded as m is.
         // (A tile that counts has its maximum near m.)
         const bool huge = !FORM && fabsf(mx) > 0x1p24f && mx != -INFINITY;
-        // The reference maximum that P and O are scaled by: the first tile's maximum, then moved only
-        // past 2^8 (the difference, not a sum: past 2^26 that would round to several times as far).
+        // The reference that P and O are scaled by: from the first tile's maximum, then moved only when
+        // passed by far (the difference, not a sum: past 2^26 that would round to several times as far).
         const bool first = i == i_first;
-        const bool moved = !first && mx - m_used > kLazyLog2;
+        const bool moved = !first && mx - m_used > kLazyLog2<W8> + kLiftLog2<W8>;
         float factor = FORM ? 1.f : sc;
         if (__any_sync(0xffffffffu, moved || huge)) {  // (one vote for the two: most steps have neither)
           if (__any_sync(0xffffffffu, moved)) {
             // rescale half the dims of this warp's rows of O: this step's S was issued after the last
             // P V, and is there
-            const float m_new = moved ? mx : m_used;
+            const float m_new = moved ? mx - kLiftLog2<W8> : m_used;
             const float alpha = moved ? exp2f(m_used - m_new) : 1.f;
 #pragma unroll 1
             for (int c = h * (D / 2); c < (h + 1) * (D / 2); c += 16) {
@@ -778,7 +789,7 @@ __global__ void __launch_bounds__(TcShape<KV, D>::THREADS, 1) chunk_tc_kernel(
             factor = 1.f;
           }
         }
-        if (first) m_used = mx;
+        if (first) m_used = mx - kLiftLog2<W8>;
         // P = 2^(s - m), the two halves over the first 64 columns of S
         const float m_use = m_used == -INFINITY ? 0.f : m_used;
         uint64_t sum[4] = {0, 0, 0, 0};  // (pairs of zeros)

@@ -287,6 +287,48 @@ def test_sums_of_long_contexts_behind_a_window(cache, d, new):
     assert pkv.device_error() == 0
 
 
+@pytest.mark.parametrize("cache", ["bf16", "fp8", "int8"])
+@pytest.mark.parametrize("below", [10.0, 15.0, 24.6, 30.0])
+@pytest.mark.parametrize("new,h_q", [(400, 128), (3, 8)])
+def test_many_small_weights_beside_a_large_one(cache, below, new, h_q):
+    """One position with 2^below times the weight of each of 131,072 others, whose values alone are not 0:
+    together the small ones count, though each is near the end of the matrix type's range."""
+    d, past = 64, 1 << 17
+    ctx = past + new
+    pages = -(-ctx // 16)
+    one = {"bf16": 1.0, "fp8": 0x38, "int8": 1}[cache]  # (0x38: the code of 1)
+    dtype = {"bf16": torch.bfloat16, "fp8": torch.uint8, "int8": torch.int8}[cache]
+    k, v = (torch.zeros(pages, 1, 16, d, dtype=dtype, device="cuda") for _ in range(2))
+    k[0, 0, 0, 0] = one
+    v.fill_(one)
+    v[0, 0, 0] = 0
+    scales = dict(k_scales=torch.ones(1, device="cuda"), v_scales=torch.ones(1, device="cuda"))
+    q = torch.zeros(new, h_q, d, dtype=torch.bfloat16, device="cuda")
+    q[:, :, 0] = 16.0
+    q[:, :, 1] = torch.arange(new, device="cuda")[:, None]  # (meets zeros)
+    scale = below * math.log(2.0) / 16.0
+    lse = torch.empty(new, h_q, device="cuda")
+    out = pkv.chunk_attention(q, k, v, torch.arange(pages, dtype=torch.int32, device="cuda")[None],
+                              torch.tensor([ctx], dtype=torch.int32, device="cuda"),
+                              torch.tensor([0, new], dtype=torch.int32, device="cuda"), scale, lse=lse,
+                              **(scales if cache != "bf16" else {}))
+    scale = torch.tensor(scale).item()  # (as the call took it: fp32)
+    top = math.exp(torch.tensor(scale, dtype=torch.float32).double().item() * 16.0)
+    n = torch.arange(past, past + new, dtype=torch.float64, device="cuda")[:, None, None]  # small ones
+    ref = n / (n + top)
+    # the large weight's score: its product with the scale and log2(e) and the exponential (4 U32 of the
+    # score, 2^-21); a small weight: 2^-21; sums over tiles, one rounding or truncation (2 U32) each, and
+    # 64 within them and over shares; a small weight's rounding to the matrix type: in f16 half a step,
+    # 2^-25, of a value kept 2^7 times as large or more; the output's
+    e = 4 * U32 * below + 2.0 ** -20 + 2 * (past // 128 + 64) * U32
+    p = H["bf16"] if cache == "bf16" else H["f16"] + 2.0 ** (below - 32)
+    tol = (2 * e + p) * ref + H["bf16"] * ref * (1 + p) + 1e-30
+    assert ((out.double() - ref).abs() <= tol).all(), ((out.double() - ref).abs() / tol).max()
+    want = torch.log(n + top).expand(new, h_q, 1)[..., 0]
+    assert ((lse.double() - want).abs() <= 2 * e + 4 * U32 * want).all()
+    assert pkv.device_error() == 0
+
+
 @pytest.mark.parametrize("io,cache,d", [KINDS[i] for i in (0, 1, 2, 5, 6, 8)])
 @pytest.mark.parametrize("window,sinks", [(0, 0), (70, 5)])
 def test_values_and_keys_that_are_not_finite_reach_only_rows_that_see_them(io, cache, d, window, sinks):
