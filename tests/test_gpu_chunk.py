@@ -270,6 +270,47 @@ def test_sums_of_many_short_runs(cache, d, new, group):
     assert pkv.device_error() == 0
 
 
+FEW = [  # new tokens of each request, h_q, h_kv: on the mean few rows to a KV head
+    ([4] * 20, 8, 2), ([3] * 20, 8, 2), ([6, 7, 8, 5], 8, 2), ([8] * 9, 4, 1),
+    ([1] * 64 + [300], 3, 1), ([1] * 64 + [40], 2, 2), ([1] * 30 + [300] + [1] * 34, 3, 3),
+    ([0, 1, 2] * 20 + [77, 0], 4, 2),
+]
+
+
+@pytest.mark.parametrize("new,h_q,h_kv", FEW, ids=lambda x: str(x)[:30])
+@pytest.mark.parametrize("cache,d", [("bf16", 128), ("bf16", 64), ("fp8", 128), ("fp8", 64), ("int8", 128),
+                                     ("int8", 64)])
+@pytest.mark.parametrize("form", [dict(), dict(window=37, sinks=5), dict(alibi=True, softcap=20.0)], ids=str)
+def test_sums_of_few_rows_in_several_passes(cache, d, new, h_q, h_kv, form):
+    """Calls of few rows on the mean, whose requests have one to many times the rows that are taken at
+    once; with earlier sums, in place too, and the same bits every time."""
+    past = np.random.default_rng(3).integers(0, 700, len(new))
+    c = Chunk(past, new, h_q, h_kv, d, "bf16", cache, seed=13, pad=0, **form)
+    lse = torch.empty(c.q.shape[:2], device="cuda")
+    c.attend(lse=lse)
+    for last in (0, 40):
+        add = torch.rand(len(new), h_kv, c.bt.shape[1] * 16, generator=gen(14), device="cuda") * 3
+        ref, tol = c.sums(lse, last, add)
+        w = c.weigh(lse, last_rows=last, add_to=add)
+        assert ((w.double() - ref).abs() <= tol).all()
+        assert torch.equal(c.weigh(lse, last_rows=last, add_to=add), w)
+        assert c.weigh(lse, last_rows=last, add_to=add, out=add) is add
+        assert torch.equal(add, w)
+    assert pkv.device_error() == 0
+
+
+@pytest.mark.parametrize("cache", ["bf16", "fp8"])
+def test_small_sums_join_large_earlier_ones_once(cache):
+    """900 rows of one request beside 200 decode steps add some 0.001 each to sums of 1000 before: every
+    addition by itself would be half a step or less."""
+    c = Chunk([700] + [20] * 200, [300] + [1] * 200, 3, 1, 64, "bf16", cache, seed=15, pad=0)
+    lse = torch.empty(c.q.shape[:2], device="cuda")
+    c.attend(lse=lse)
+    add = torch.full((201, 1, c.bt.shape[1] * 16), 1000.0, device="cuda")
+    ref, tol = c.sums(lse, 0, add)
+    assert ((c.weigh(lse, add_to=add).double() - ref).abs() <= tol).all()
+
+
 @pytest.mark.parametrize("cache,d,new", [("bf16", 64, 20), ("fp8", 64, 20), ("fp8", 64, 2)])
 def test_sums_of_long_contexts_behind_a_window(cache, d, new):
     """Most items have no rows: more of them in a share than the kernel keeps at a time."""
