@@ -276,7 +276,8 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? 4 : 3) weights_few_kernel(
               float add = tig == 0 ? total[0] : total[1];
               if (pass > 0) add -= *gone;
               const float sum = base + add;
-              *gone = (sum - base) - add;
+              const float left_out = (sum - base) - add;
+              *gone = fabsf(left_out) < INFINITY ? left_out : 0.f;  // (infinite sums stay that)
               out[at] = sum;
             }
           } else {

@@ -311,6 +311,22 @@ def test_small_sums_join_large_earlier_ones_once(cache):
     assert ((c.weigh(lse, add_to=add).double() - ref).abs() <= tol).all()
 
 
+@pytest.mark.parametrize("io,cache", [("bf16", "bf16"), ("bf16", "fp8"), ("f32", "f32")])
+@pytest.mark.parametrize("new", [[300] + [1] * 64, [200, 100, 3]], ids=["few", "many"])
+def test_infinite_earlier_sums_stay_that(io, cache, new):
+    """Positions that a program pins, or gives up, by sums of either infinity."""
+    c = Chunk([100] * len(new), new, 3, 1, 64, io, cache, seed=16, pad=0)
+    lse = torch.empty(c.q.shape[:2], device="cuda")
+    c.attend(lse=lse)
+    add = torch.zeros(len(new), 1, c.bt.shape[1] * 16, device="cuda")
+    plain = c.weigh(lse, add_to=add)
+    add[:, :, 3::7] = math.inf
+    add[:, :, 5::11] = -math.inf
+    w = c.weigh(lse, add_to=add)
+    pinned = torch.isinf(add)
+    assert torch.equal(w[pinned], add[pinned]) and torch.equal(w[~pinned], plain[~pinned])
+
+
 @pytest.mark.parametrize("cache,d,new", [("bf16", 64, 20), ("fp8", 64, 20), ("fp8", 64, 2)])
 def test_sums_of_long_contexts_behind_a_window(cache, d, new):
     """Most items have no rows: more of them in a share than the kernel keeps at a time."""
