@@ -960,8 +960,16 @@ def chunk_weights_workspace_size(dtype_q, num_rows, batch, num_q_heads, num_kv_h
                                                       num_kv_heads, head_dim, width))
 
 
-def _chunk_args(q, desc, block_tables, context_lens, query_starts, alibi_slopes):
+def _int32(**values):
+    """Refuses numbers that the C call's 32-bit arguments would cut to others."""
+    for name, v in values.items():
+        if not -2 ** 31 <= v < 2 ** 31:
+            raise PkvError(-1, "%s does not fit 32 bits" % name)
+
+
+def _chunk_args(q, desc, block_tables, context_lens, query_starts, alibi_slopes, **numbers):
     """Checks what the chunk calls share; returns (rows, batch, query heads)."""
+    _int32(**numbers)
     if q.dim() != 3:
         raise PkvError(-2, "q must be [rows, num_q_heads, head_dim]")
     if (block_tables.dtype != torch.int32 or context_lens.dtype != torch.int32 or
@@ -991,7 +999,8 @@ def chunk_attention(q, k_cache, v_cache, block_tables, context_lens, query_start
     ``lse`` fp32 [N, h_q] receives the logarithm of each row's sum, for ``chunk_weights``
     (pkv_chunk_attention). Rows of no request are left as they were (zero in a new ``out``)."""
     desc = _pools(k_cache, v_cache)
-    n, B, h_q = _chunk_args(q, desc, block_tables, context_lens, query_starts, alibi_slopes)
+    n, B, h_q = _chunk_args(q, desc, block_tables, context_lens, query_starts, alibi_slopes,
+                            window=window, sink_tokens=sink_tokens)
     _check_scales(desc, k_scales, v_scales)
     if lse is not None and (lse.dtype != torch.float32 or tuple(lse.shape) != (n, h_q)):
         raise PkvError(-2, "lse must be float32 [rows, num_q_heads]")
@@ -1027,7 +1036,8 @@ def chunk_weights(q, k_cache, block_tables, context_lens, query_starts, lse, sca
     were (in a new ``out`` as in ``add_to``, or zero). ``width`` of a new ``out`` without ``add_to``:
     the table's positions unless given."""
     desc = _pool_desc(k_cache.shape, k_cache.dtype)
-    n, B, h_q = _chunk_args(q, desc, block_tables, context_lens, query_starts, alibi_slopes)
+    n, B, h_q = _chunk_args(q, desc, block_tables, context_lens, query_starts, alibi_slopes,
+                            window=window, sink_tokens=sink_tokens, last_rows=last_rows)
     if desc.cache_dtype in (FP8_E4M3, INT8):
         _check_scales(desc, k_scales, k_scales)
     if lse.dtype != torch.float32 or tuple(lse.shape) != (n, h_q):
@@ -1073,6 +1083,7 @@ def evict_select(weights, context_lens, budget, recent=0, sink_tokens=0, kept=No
     [batch] = min(context, budget))."""
     if weights.dtype != torch.float32 or weights.dim() != 3:
         raise PkvError(-2, "weights must be float32 [batch, num_kv_heads, width]")
+    _int32(budget=budget, recent=recent, sink_tokens=sink_tokens)
     B, h_kv, width = weights.shape
     if context_lens.dtype != torch.int32 or context_lens.numel() != B:
         raise PkvError(-3, "context_lens must be int32 [batch]")

@@ -141,3 +141,24 @@ def test_shared_arrays_read_in_wider_words_say_their_alignment():
             looked += len(reads)
             assert kind[1] or not reads, (os.path.basename(path), line.strip(), reads)
     assert looked >= 1
+
+
+def test_numbers_beyond_32_bits_are_refused():
+    """ctypes would cut them to others without a word: a window of 2^32 + 5 to one of 5."""
+    import torch
+    q = torch.zeros(2, 2, 64, dtype=torch.bfloat16)
+    pool = torch.zeros(2, 1, 16, 64, dtype=torch.bfloat16)
+    ints = lambda *x: torch.tensor(x, dtype=torch.int32)
+    args = (ints(0)[None], ints(5), ints(0, 2))
+    big = 2 ** 32 + 5
+    for kw in (dict(window=big), dict(window=8, sink_tokens=big), dict(window=-big)):
+        with pytest.raises(pkv.PkvError, match="32 bits"):
+            pkv.chunk_attention(q, pool, pool, *args, 0.1, **kw)
+        with pytest.raises(pkv.PkvError, match="32 bits"):
+            pkv.chunk_weights(q, pool, *args, torch.zeros(2, 2), 0.1, **kw)
+    with pytest.raises(pkv.PkvError, match="32 bits"):
+        pkv.chunk_weights(q, pool, *args, torch.zeros(2, 2), 0.1, last_rows=big)
+    w = torch.zeros(1, 1, 16)
+    for kw in (dict(budget=big), dict(budget=8, recent=big), dict(budget=8, sink_tokens=big)):
+        with pytest.raises(pkv.PkvError, match="32 bits"):
+            pkv.evict_select(w, ints(5), **kw)
