@@ -102,6 +102,12 @@ int check_chunk(const char* who, const void* q, int dtype_q, int num_rows, int b
     return set_error(PKV_EINVAL, "%s: scale must be positive and finite", who);
   if (!(form->softcap >= 0.f) || std::isinf(form->softcap))
     return set_error(PKV_EINVAL, "%s: softcap must be finite and >= 0", who);
+  // The kernels take scale log2(e), 1 / softcap and scale / softcap as fp32, beyond which 0 times infinity
+  // would be a score. Caps are moved to where they are in range: below 2^-100 all of them leave weights that
+  // are equal, above 2^100 the scores (up to 2^88) as they are, to the last bit.
+  const float cap = form->softcap > 0.f ? std::min(std::max(form->softcap, 0x1p-100f), 0x1p100f) : 0.f;
+  if (!(form->scale <= 0x1p126f) || (cap > 0.f && !(form->scale / cap <= 0x1p120f)))
+    return set_error(PKV_EINVAL, "%s: scale beyond 2^126, or 2^120 times softcap", who);
   if (form->window < 0 || form->sink_tokens < 0 || (form->window == 0 && form->sink_tokens != 0))
     return set_error(PKV_EINVAL, "%s: window and sink_tokens must be >= 0; sinks need a window",
                      who);
@@ -131,7 +137,7 @@ int check_chunk(const char* who, const void* q, int dtype_q, int num_rows, int b
   a.num_pages = desc->num_pages;
   a.max_pages = max_pages;
   a.scale = form->scale;
-  a.softcap = form->softcap;
+  a.softcap = cap;
   a.window = form->window;
   a.sink = form->sink_tokens;
   return PKV_OK;

@@ -36,6 +36,7 @@ SHARED = [  # what both chunk calls refuse
     (dict(form=form(scale=0.0)), EINVAL), (dict(form=form(scale=INF)), EINVAL),
     (dict(form=form(scale=NAN)), EINVAL), (dict(form=form(softcap=-1.0)), EINVAL),
     (dict(form=form(softcap=NAN)), EINVAL), (dict(form=form(softcap=INF)), EINVAL),
+    (dict(form=form(scale=1e38)), EINVAL), (dict(form=form(scale=1e37, softcap=1.0)), EINVAL),
     (dict(form=form(window=-1)), EINVAL), (dict(form=form(window=5, sinks=-1)), EINVAL),
     (dict(form=form(sinks=1)), EINVAL), (dict(q=None), EINVAL), (dict(k_cache=None), EINVAL),
     (dict(tables=None), EINVAL), (dict(ctx=None), EINVAL), (dict(starts=None), EINVAL),

@@ -233,6 +233,26 @@ def test_forms_match_the_formula(io, cache, d, form):
     assert pkv.device_error() == 0
 
 
+@pytest.mark.parametrize("io,cache", [("bf16", "bf16"), ("bf16", "int8"), ("f32", "f32")])
+@pytest.mark.parametrize("softcap", [1e-42, 1e-35, 1e-6, 1e6, 1e29, 1e36, 3e38])
+def test_caps_far_from_the_scores(io, cache, softcap):
+    """A cap far below the scores leaves every position seen the same weight, one far above them the scores;
+    a query of zeros has scores of 0 under any."""
+    c = Chunk([100, 0], [70, 200], 8, 2, 64, io, cache, seed=17, softcap=softcap)
+    c.q[7] = 0
+    lse = torch.empty(c.q.shape[:2], device="cuda")
+    out = c.attend(lse=lse)
+    # (the cap's own error is relative to it, or to the score: 2^-21 of the smaller)
+    c.softcap = 0.0 if softcap >= 1e6 else softcap
+    if softcap < 1:
+        c.check(out, lse)
+    else:
+        c.score_error = lambda q, k, e=c.score_error: e(q, k) + 2.0 ** -19 * c.scale * (
+            q.abs() @ k.abs().T).amax(-1)
+        c.check(out, lse)
+    assert pkv.device_error() == 0
+
+
 @pytest.mark.parametrize("io,cache", [("bf16", "bf16"), ("bf16", "fp8"), ("f32", "f32")])
 def test_one_long_context_and_many_requests(io, cache):
     c = Chunk([9000], [3], 16, 2, 128, io, cache)
