@@ -843,6 +843,69 @@ def test_move_skips_and_flags_what_is_not_there():
         assert torch.equal(raw(c.k_cache).view(len(other), -1)[other], before.view(len(other), -1)[other])
 
 
+def test_eviction_and_decode_sums_in_a_graph_and_on_two_streams():
+    """Sums of a decode step, the choice and the move, captured once and replayed over other sums and over
+    other lengths; and two such calls at the same time."""
+    calls = []
+    for seed, cache in ((21, "bf16"), (22, "fp8")):
+        c = Chunk([300, 1000, 40], [1, 1, 1], 4, 2, 64, "bf16", cache, seed=seed, spare=12)
+        lse = torch.empty(c.q.shape[:2], device="cuda")
+        c.attend(lse=lse)
+        w = torch.rand(3, 2, c.bt.shape[1] * 16, device="cuda")
+        nt = torch.from_numpy(c.spare_pages[:12].reshape(3, 4).astype(np.int32)).cuda()
+        kept = torch.zeros(3, 2, 64, dtype=torch.int32, device="cuda")
+        lens = torch.zeros(3, dtype=torch.int32, device="cuda")
+        sums, moved = torch.zeros_like(w), torch.zeros(3, 2, 70, device="cuda")
+
+        def call(c=c, lse=lse, w=w, nt=nt, kept=kept, lens=lens, sums=sums, moved=moved):
+            c.weigh(lse, add_to=w, out=sums)
+            pkv.evict_select(sums, c.cl, 64, 8, 2, kept=kept, kept_lens=lens)
+            pkv.evict_move(c.k_cache, c.v_cache, c.bt, kept, lens, nt, sums, moved)
+
+        def wrong(c=c, nt=nt, kept=kept, lens=lens, sums=sums, moved=moved):
+            for b, n in enumerate(c.cl.tolist()):
+                m = min(n, 64)
+                assert int(lens[b]) == m
+                for j in range(2):
+                    at = kept_positions(sums[b, j, :n].cpu().numpy(), n, 64, 8, 2)
+                    if not np.array_equal(kept[b, j, :m].cpu().numpy(), at):
+                        return "kept"
+                    at = torch.from_numpy(at).cuda()
+                    if not torch.equal(moved[b, j, :m], sums[b, j, at]) or moved[b, j, m:].any():
+                        return "sums"
+                    for pool in (c.k_cache, c.v_cache):
+                        x = pool.view(torch.uint8) if pool.element_size() == 1 else pool
+                        new = x[nt[b].long(), j].reshape(-1, 64)[:m]
+                        if not torch.equal(raw(new), raw(x[c.bt[b].long()[at // 16], j, at % 16])):
+                            return "rows"
+            return None
+        calls.append((c, w, call, wrong, kept, lens, moved))
+    for c, w, call, wrong, kept, lens, moved in calls:
+        call()
+        assert wrong() is None
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            call()
+        for i in range(3):
+            w.copy_(torch.rand_like(w))
+            if i == 2:
+                c.cl.copy_(torch.tensor([200, 3, 30], dtype=torch.int32))
+            for x in (kept, lens, moved):
+                x.fill_(-1)
+            graph.replay()
+            torch.cuda.synchronize()
+            assert wrong() is None
+    streams = [torch.cuda.Stream() for _ in calls]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for st, (_, _, call, *_) in zip(streams, calls):
+            with torch.cuda.stream(st):
+                call()
+    torch.cuda.synchronize()
+    assert [wrong() for _, _, _, wrong, *_ in calls] == [None, None]
+    assert pkv.device_error() == 0
+
+
 # ---- as they are used together -------------------------------------------------------------------
 
 
