@@ -56,6 +56,7 @@ __device__ __forceinline__ ChunkReq chunk_request(const ChunkArgs& a, int b) {
 __device__ __forceinline__ bool chunk_rows_overlap(const ChunkArgs& a, bool falls) {
   if (!__syncthreads_or(falls)) return false;
   long long rows = 0;
+#pragma unroll 1
   for (int b = 0; b < a.batch; ++b) rows += chunk_request(a, b).n;
   return rows > a.num_rows;
 }
@@ -203,7 +204,7 @@ __device__ __forceinline__ void chunk_share(const ChunkArgs& a, int* scratch, Ch
   }
   if (err && blockIdx.x == 0) atomicOr(a.err, err);
   if (threadIdx.x == 0) out->count = 0;
-  if (chunk_rows_overlap(a, err & PKV_DEVERR_BAD_CHUNK)) return;  // (behind a barrier)
+  const bool overlap = chunk_rows_overlap(a, err & PKV_DEVERR_BAD_CHUNK);
   int work_below, work_all, passes_below, passes_all;
   block_scan2<THREADS>(work, passes, scratch, work_below, work_all, passes_below, passes_all);
   const int cost = work_all >= 32 * a.ctas ? 2 * a.pass_cost : 0;
@@ -212,7 +213,7 @@ __device__ __forceinline__ void chunk_share(const ChunkArgs& a, int* scratch, Ch
       max(2 * a.min_tiles, (int)(((unsigned)total + a.ctas - 1) / (unsigned)a.ctas));
   const int mine = work + cost * passes, below = work_below + cost * passes_below;
   const long long start = (long long)blockIdx.x * share;
-  if (start >= below && start < (long long)below + mine) {
+  if (!overlap && start >= below && start < (long long)below + mine) {
     int at = below, b = b0;
     for (; b < b1 - 1; ++b) {
       const ChunkReq r = chunk_request(a, b);

@@ -112,12 +112,12 @@ __device__ __forceinline__ void weigh_share(const ChunkArgs& a, int* scratch, We
   }
   if (err && blockIdx.x == 0) atomicOr(a.err, err);
   if (threadIdx.x == 0) out->count = 0;
-  if (chunk_rows_overlap(a, err & PKV_DEVERR_BAD_CHUNK)) return;  // (behind a barrier)
+  const bool overlap = chunk_rows_overlap(a, err & PKV_DEVERR_BAD_CHUNK);
   int below, total;
   block_scan<THREADS>(mine, scratch, below, total);
   const int share = max(2, (int)(((unsigned)total + a.ctas - 1) / (unsigned)a.ctas));
   const long long start = (long long)blockIdx.x * share;
-  if (start >= below && start < (long long)below + mine) {
+  if (!overlap && start >= below && start < (long long)below + mine) {
     int at = below, b = b0;
     for (; b < b1 - 1; ++b) {
       const WeighReq w = weigh_request(a, b);
