@@ -725,7 +725,7 @@ __global__ void __launch_bounds__(WeighTcShape<KV, D>::THREADS, 1) weights_tc_ke
           const float add = (x + y) - lost, z = total + add;
           lost = (z - total) - add;
           total = z;
-          if (*reinterpret_cast<const uint32_t*>(some_nan[at_c]) != 0 && !(total < INFINITY)) total = NAN;
+          if (!(total < INFINITY) && *reinterpret_cast<const uint32_t*>(some_nan[at_c]) != 0) total = NAN;
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&free_c[at_c]);
