@@ -749,8 +749,10 @@ size_t pkv_tree_decode_workspace_size(int32_t dtype_q, int32_t cache_dtype, int3
  * over the positions p < base and the nodes base + i whose bit i is set in node t's mask row.
  * A row that sees nothing gives 0. What is not seen takes no part, whatever it holds (NaN and
  * infinities too). There is no sliding window: every position before the draft is attended, and the
- * entries of -1 that pkv_seq_release_outside_window leaves in a table row are bad page ids here. Scores, maxima and sums are fp32; with BF16 queries the weights are rounded
- * to the cache's matrix type (bf16 for a BF16 cache, f16 for FP8 and INT8) before they meet V.
+ * entries of -1 that pkv_seq_release_outside_window leaves in a table row are bad page ids here. Scores,
+ * maxima and sums are fp32; with BF16 queries the weights are rounded to the cache's matrix type (bf16 for
+ * a BF16 cache, f16 for FP8 and INT8: all its bits from 2^-21 of a row's largest on, none below 2^-31)
+ * before they meet V.
  *  q, out       device [batch][tree_width][num_q_heads][head_dim] of dtype_q, 16-byte aligned;
  *               rows t >= tree_lens[b] of out are left as they were. F32 q takes an F32, FP8 or
  *               INT8 cache; BF16 q a BF16, FP8 or INT8 cache.

@@ -20,8 +20,8 @@
 //    step through shared memory, set before anything else of a step is done, and each group keeps
 //    its own sum. Larger units: group g takes rows 128 g .. of every tile with an O of its own, so the
 //    cache is still read once;
-//  * O is rescaled only when a row's maximum grows by more than 2^8 (P <= 2^8 until then): the final
-//    (max, sum, O) is exact whatever maximum it was accumulated against.
+//  * O is rescaled only when a row's maximum grows by more than 2^8 (8-bit caches: 2^7): the final
+//    (max, sum, O) is exact whatever reference it was accumulated against.
 //
 // Two kernels: a call whose drafts have at most 128 rows a KV head keeps a unit's queries in tensor
 // memory beside an O and four S buffers and has the whole of shared memory for the rings; with more
@@ -86,7 +86,6 @@ constexpr int kRuns = 32;
 // tensor memory columns. WIDE: two O and four S (then P) buffers; otherwise an O, a Q and the same
 constexpr uint32_t kColO = 0, kColQ = 256;
 constexpr uint32_t kTmemCols = 512;
-constexpr float kLazyLog2 = 8.f;
 static_assert(2 * kGroupThreads == kTreeTcRows, "a unit is two groups' rows");
 static_assert(kExchangeRows == kGroupThreads, "a place for each row of a group");
 
@@ -794,8 +793,8 @@ __global__ void __launch_bounds__(TcShape<KV, D, WIDE>::THREADS, 1) tree_tc_kern
         // larger m it would soon leave f16's range and then every range: there s sc is rounded as m is.
         // (A tile that counts has its maximum near m.)
         const bool huge = fabsf(mx) > 0x1p24f && mx != -INFINITY;
-        // The reference maximum m that P and O are scaled by: the first tile's maximum, then moved
-        // only past 2^8. In a wide unit it is the thread's own. Otherwise the two groups' tiles add
+        // The reference m that P and O are scaled by: from the first tile's maximum, then moved only when
+        // passed by far. In a wide unit it is the thread's own. Otherwise the two groups' tiles add
         // into one O, so m goes from step to step: this group's step takes it from the other's
         // last one, sets it and says so before anything else.
         const bool first = wide ? u == wg : u == 0;
@@ -807,8 +806,8 @@ __global__ void __launch_bounds__(TcShape<KV, D, WIDE>::THREADS, 1) tree_tc_kern
           if (!ok) break;
           m_before = ref[r];
         }
-        // (the difference, not m_before + 2^3: past 2^26 that sum would round to several times as far)
-        const float m_new = first || mx - m_before > kLazyLog2 ? mx : m_before;
+        // (the difference, not m_before + lazy: past 2^26 that sum would round to several times as far)
+        const float m_new = first || mx - m_before > kLazyLog2<W8> + kLiftLog2<W8> ? mx - kLiftLog2<W8> : m_before;
         const bool moved = !first && m_new != m_before;
         if (!wide) {
           if (first || moved) ref[r] = m_new;

@@ -403,3 +403,38 @@ def test_every_node_of_every_step_attends_what_it_should(cache):
         lens = [lens[b] + int(plen[b]) for b in range(B)]
         assert got == lens == [len(kept[b][0]) for b in range(B)]
     assert pkv.device_error() == 0
+
+
+@pytest.mark.parametrize("cache", ["bf16", "fp8", "int8"])
+@pytest.mark.parametrize("below", [10.0, 24.6, 30.0])
+@pytest.mark.parametrize("batch,nodes,h_q", [(40, 64, 16), (200, 4, 8), (2, 4, 8)])
+def test_many_small_weights_beside_a_large_one(cache, below, batch, nodes, h_q):
+    """One position with 2^below times the weight of each of 131,072 others, whose values alone are not 0:
+    together the small ones count, though each is near the end of the matrix type's range. (All requests
+    share one context.)"""
+    d, past = 64, 1 << 17
+    pages = -(-(past + nodes) // 16)
+    one = {"bf16": 1.0, "fp8": 0x38, "int8": 1}[cache]  # (0x38: the code of 1)
+    dtype = {"bf16": torch.bfloat16, "fp8": torch.uint8, "int8": torch.int8}[cache]
+    k, v = (torch.zeros(pages, 1, 16, d, dtype=dtype, device="cuda") for _ in range(2))
+    k[0, 0, 0, 0] = one
+    v.fill_(one)
+    v[0, 0, 0] = 0
+    scales = {} if cache == "bf16" else dict(k_scales=torch.ones(1, device="cuda"),
+                                             v_scales=torch.ones(1, device="cuda"))
+    q = torch.zeros(batch, nodes, h_q, d, dtype=torch.bfloat16, device="cuda")
+    q[..., 0] = 16.0
+    scale = torch.tensor(below * math.log(2.0) / 16.0).item()  # (as the call takes it: fp32)
+    out = pkv.tree_decode_attention(
+        q, k, v, torch.arange(pages, dtype=torch.int32, device="cuda")[None].repeat(batch, 1),
+        torch.full((batch,), past + nodes, dtype=torch.int32, device="cuda"), scale, **scales)
+    n = torch.arange(past, past + nodes, dtype=torch.float64, device="cuda")[None, :, None, None]
+    ref = n / (n + math.exp(scale * 16.0))
+    # the large weight's score (4 U32 of it) and exponential (2^-21); a small weight's; sums over tiles of 64,
+    # one rounding or truncation (2 U32) each, and 64 within them and over shares; a small weight's rounding
+    # to the matrix type: in f16 half a step, 2^-25, of a value kept 2^7 times as large or more; the output's
+    e = 4 * U32 * below + 2.0 ** -20 + 2 * (past // 64 + 64) * U32
+    p = H["bf16"] if cache == "bf16" else 2.0 ** -11 + 2.0 ** (below - 32)
+    tol = (2 * e + p) * ref + H["bf16"] * ref * (1 + p)
+    assert ((out.double() - ref).abs() <= tol).all(), ((out.double() - ref).abs() / tol).max()
+    assert pkv.device_error() == 0
