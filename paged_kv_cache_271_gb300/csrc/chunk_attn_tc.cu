@@ -21,10 +21,10 @@
 //
 // P is rounded to the MMA's input type (bf16 for a bf16 cache, f16 otherwise), the only rounding
 // before the output's; scores, maxima and sums are fp32. (Outputs' relative error against 64 bits, over a
-// bf16 cache: 0.0019 to 0.0022, where weights in 32 bits give 0.0017, the output's own rounding; over 8-bit
-// caches no more than that. The rest of P as a second operand would cost a fourth of a tile's MMAs.) For 8-bit caches a query row is scaled by
-// a power of two that puts its largest value in f16's top binade, undone in its score factor; the sign
-// of the K scale goes with it, so that score factors are positive.
+// bf16 cache: 0.0019 to 0.0023, where weights in 32 bits give 0.0017, the output's own rounding; over 8-bit
+// caches no more than that. What bf16 leaves out, as a second operand, would be half as many MMAs again.)
+// For 8-bit caches a query row is scaled by a power of two that puts its largest value in f16's top binade,
+// undone in its score factor; the sign of the K scale goes with it, so that score factors are positive.
 //
 // Tiles with unseen positions (the chunk's own, the window's edge, bad pages) mask scores by the row's
 // mask bits, and their V rows are mended in shared memory before the MMA reads them: rows outside the
@@ -32,11 +32,11 @@
 // would still spread to rows that do not see them, become 0 there and are added to the rows that do
 // see them at the unit's end.
 //
-// Measured: an 8191-token prompt, 32 heads on 8 of 128 dims, bf16, 431 us (1.28 PFLOP/s of the 1.91 that a
-// library product reaches); 2048 tokens over 32768 cached ones, 64 heads, FP8, 2.03 ms (1.12); 64 decode steps
-// with biases 132 us (5.1 TB/s). A tile of a full unit takes about 3300 cycles: S is issued in 640 a group
-// (both its operands come from shared memory, 128 bytes a clock), and of a group's chain of S, maximum,
-// exchange, exponentials, P and P V two are under way at a time.
+// Measured: an 8191-token prompt, 32 heads on 8 of 128 dims, bf16, 436 us (1.26 PFLOP/s of the 1.91 that a
+// library product reaches); 2048 tokens over 32768 cached ones, 64 heads, FP8, 2.04 ms (1.11); 64 decode steps
+// with biases 133 us (4.5 TB/s), without 114 (5.2), over FP8 152 (2.0). A tile of a full unit takes about 3300
+// cycles: S is issued in 640 a group (both its operands come from shared memory, 128 bytes a clock), and of a
+// group's chain of S, maximum, exchange, exponentials, P and P V two are under way at a time.
 //
 // Every wait is bounded (PKV_DEVERR_TIMEOUT); the tensor memory is freed on every path.
 #include <atomic>

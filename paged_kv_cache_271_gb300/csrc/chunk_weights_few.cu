@@ -1,14 +1,14 @@
 // Sums of attention weights for calls of few rows a request (decode steps), bf16 queries over a bf16, FP8 or
 // INT8 cache; the mathematics is that of chunk_weights.cu.
 //
-// Such a call is bound by reading K once: 64 requests' rows are 90 MB for some thousand operations a
+// Such a call is bound by reading K once: 64 requests' rows are 149 MB of FP8 for some thousand operations a
 // row. So K goes from memory straight into registers, in the form the MMA wants: a dot product does not
 // mind the order of its terms, so each lane takes 16 consecutive bytes of a row where the MMA
 // (m16n8k16: 16 positions x 8 rows) would have it take 2 and 2 of distant ones, and the queries are
 // taken in the same order. A warp has a page (16 positions) and the next one in registers, no shared
 // memory, no barriers, and 12 to 16 warps on an SM keep 50 to 100 KB of reads under way (through the
 // rings of the tcgen05 kernel the same call, 64 requests of 512 .. 4096 FP8 tokens and 8 KV heads, takes
-// 135 us instead of 37, or 4.8 TB/s: a step of 4 rows there costs as much as one of 128).
+// 142 us instead of 39, or 4.1 TB/s: a step of 4 rows there costs as much as one of 128).
 //
 // The pages of all requests and KV heads, in order, form one stream, and each warp takes an equal
 // contiguous share of it, whole pages: no sum is made in parts, so equal inputs give equal results.

@@ -17,7 +17,7 @@
 //  * one MMA warp; four groups of four warps that add up weights: group 2 q + h takes half h of the item
 //    in every second step, reading S^T from its own 128 columns of tensor memory, 32 at a time.
 //
-// 4095 prompt rows over themselves, 32 query heads on 8, bf16: 78 us for 69 GFLOP, 0.88 PFLOP/s (the rings
+// 4095 prompt rows over themselves, 32 query heads on 8, bf16: 81 us for 69 GFLOP, 0.85 PFLOP/s (the rings
 // and MMAs alone, without the sums, took 62).
 //
 // A wait for a phase by its parity means something only to a warp that has seen the phase before end. So
