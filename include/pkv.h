@@ -809,8 +809,9 @@ int pkv_tree_commit(void* k_cache, void* v_cache, const pkv_cache_desc* desc,
  * The score of a query at position pq for a cached position p, and which positions it sees:
  *   s = scale <q, K_p>;   softcap c > 0: s <- c tanh(s / c);   alibi_slopes: s <- s - slope_h (pq - p);
  *   p <= pq;              window W > 0: and (p > pq - W or p < sink_tokens).
- * scale positive, at most 2^126; softcap finite, 0 (none) or at least 2^-120 scale (caps below 2^-100
- * and above 2^100 are taken as these); alibi_slopes device fp32 [num_q_heads] or NULL; window >= 0 (0: none), sink_tokens >= 0 (0 without a window). Positions
+ * scale positive, at most 2^126; softcap finite, >= 0 (0: none; others are taken as 2^-100 .. 2^100, and a
+ * scale above 2^120 times that is refused); alibi_slopes device fp32 [num_q_heads] or NULL; window >= 0
+ * (0: none), sink_tokens >= 0 (0 without a window). Positions
  * are indices into the request's cache: after an eviction they are those of the kept tokens.
  */
 typedef struct {

@@ -103,12 +103,13 @@ __device__ __forceinline__ float ex2_approx(float x) {
   return y;
 }
 
-// Of the tree and the chunk attention. A row's weights are 2^(s - m) with m below the maximum that it was taken from by `lift`, and O is
-// rescaled when a later maximum passes m + lift by more than `lazy`. f16, the weights' type over an 8-bit
-// cache, ends at 2^16 and steps by 2^-24 below 2^-14: lifted by 2^7, weights of 2^-21 of the largest keep
-// all bits and ones of 2^-31 are not lost, while a long context's many small ones next to a sink still
-// add up (131,072 of 2^-24.6 gave 0.0078 in place of 0.0051 without). lift + lazy leaves room for what
-// rounding m adds (at most 2^1; where m is above 2^26, lift may round up to 8).
+// The softmax of the tree and the chunk attention. A row's weights are 2^(s - m), with m below the maximum
+// that it was taken from by `lift`, and O is rescaled when a later maximum passes m + lift by more than
+// `lazy`. f16, the weights' type over an 8-bit cache, ends at 2^16 and steps by 2^-24 below 2^-14: lifted by
+// 2^7, weights of 2^-21 of the largest keep all bits and ones of 2^-31 are not lost, while a long context's
+// many small ones next to a sink still add up (131,072 of 2^-24.6 gave 0.0078 in place of 0.0051 without).
+// lift + lazy leaves room for what rounding m adds (at most 2^1; where m is above 2^26, lift may round up
+// to 8).
 template <bool F16>
 constexpr float kLiftLog2 = F16 ? 7.f : 0.f;
 template <bool F16>
